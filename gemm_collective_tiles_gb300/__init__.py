@@ -15,6 +15,13 @@ Ops (iris docs "Fused Communication and Compute Operations"; ROCm/iris PR #544
 * ``concurrent_gemm_collective``  independent GEMM beside an all-gather /
   all-reduce / reduce-scatter, with an explicit GEMM/comm CTA split.
 
+Block-scaled 8-bit floats (``fp8.py``), on plain device tensors:
+
+* ``quantize_fp8``     codes and one scale per 1 x 128 or 128 x 128 block
+* ``matmul_fp8``       out = (A * scales) @ (B * scales) + bias
+* ``weight_grad_fp8``  out = (X * scales)^T @ dY from an 8-bit checkpoint of X
+* ``fp8_linear``       the three as one differentiable linear layer
+
 The W ranks live in W regions of one device allocation (``SymmetricHeap``);
 a ``HeapTensor`` names the same byte offset in every region.
 """
@@ -47,6 +54,7 @@ __all__ = [
     "SymmetricHeap", "HeapTensor", "Workspace", "make_config", "workspace_size",
     "all_gather_matmul", "matmul_reduce_scatter", "matmul_all_gather", "matmul_all_reduce",
     "concurrent_gemm_collective", "concurrent_two_stream", "query_status", "num_sms", "IrisError",
+    "empty_fp8", "quantize_fp8", "matmul_fp8", "weight_grad_fp8", "fp8_linear",
 ]
 
 _DT = {torch.float16: _native.IRIS_F16, torch.bfloat16: _native.IRIS_BF16,
@@ -338,3 +346,6 @@ def num_sms() -> int:
     n = ctypes.c_int(0)
     _native.check("iris_b200_num_sms", _native.load().iris_b200_num_sms(ctypes.byref(n)))
     return n.value
+
+
+from .fp8 import empty_fp8, fp8_linear, matmul_fp8, quantize_fp8, weight_grad_fp8  # noqa: E402

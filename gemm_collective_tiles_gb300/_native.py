@@ -25,6 +25,7 @@ IRIS_NOALLOC_MAX_FLAGS = 16384
 IRIS_NOALLOC_SCRATCH_BYTES = 256 + 8 * IRIS_NOALLOC_MAX_FLAGS
 
 IRIS_F16, IRIS_BF16, IRIS_F32 = 0, 1, 2
+IRIS_E4M3, IRIS_E5M2 = 0, 1
 IRIS_COLL_ALL_GATHER, IRIS_COLL_ALL_REDUCE, IRIS_COLL_REDUCE_SCATTER = 0, 1, 2
 IRIS_COLL_ALL_TO_ALL, IRIS_COLL_BROADCAST = 3, 4
 (IRIS_OP_ALL_GATHER_MATMUL, IRIS_OP_MATMUL_REDUCE_SCATTER, IRIS_OP_MATMUL_ALL_GATHER,
@@ -42,6 +43,11 @@ EXPORTS = (
     "iris_b200_concurrent_two_stream",
     "iris_b200_sm_partition_streams",
     "iris_b200_sm_partition_release",
+    "iris_b200_quantize_fp8",
+    "iris_b200_matmul_fp8_workspace_size",
+    "iris_b200_matmul_fp8",
+    "iris_b200_weight_grad_fp8_workspace_size",
+    "iris_b200_weight_grad_fp8",
     "iris_b200_query_status",
     "iris_b200_strerror",
     "iris_b200_num_sms",
@@ -88,13 +94,21 @@ class iris_b200_heap(ctypes.Structure):
     ]
 
 
+class iris_b200_mat(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("col_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
 def _declare(lib):
     P = ctypes.POINTER
     i64, sz, vp, ci = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int
-    cfgp, heapp = P(iris_b200_config), P(iris_b200_heap)
+    cfgp, heapp, matp = P(iris_b200_config), P(iris_b200_heap), P(iris_b200_mat)
     sig = {
         "iris_b200_workspace_size": (ci, [ci, i64, i64, i64, ci, ci, cfgp, P(sz)]),
         "iris_b200_all_gather_matmul": (ci, [heapp, sz, sz, sz, sz, sz, i64, i64, i64, ci, cfgp, vp, sz, vp]),
@@ -108,6 +122,14 @@ def _declare(lib):
             ci, [vp, vp, vp, i64, i64, i64, ci, ci, heapp, sz, sz, i64, ci, cfgp, vp, sz, vp, sz, vp, vp]),
         "iris_b200_sm_partition_streams": (ci, [ci, P(vp), P(vp), P(ci), P(ci)]),
         "iris_b200_sm_partition_release": (ci, []),
+        "iris_b200_quantize_fp8": (ci, [matp, ci, matp, ci, matp, i64, i64, ci, ci, vp]),
+        "iris_b200_matmul_fp8_workspace_size": (ci, [matp, matp, matp, ci, i64, i64, i64, cfgp, P(sz)]),
+        "iris_b200_matmul_fp8": (
+            ci, [matp, ci, matp, matp, ci, matp, vp, ci, matp, ci, i64, i64, i64, cfgp, vp, sz, vp]),
+        "iris_b200_weight_grad_fp8_workspace_size": (
+            ci, [matp, matp, ci, matp, ci, i64, i64, i64, cfgp, P(sz)]),
+        "iris_b200_weight_grad_fp8": (
+            ci, [matp, ci, matp, matp, ci, matp, ci, i64, i64, i64, cfgp, vp, sz, vp]),
         "iris_b200_query_status": (ci, [vp, vp, P(ci), P(ci), P(ci)]),
         "iris_b200_strerror": (ctypes.c_char_p, [ci]),
         "iris_b200_num_sms": (ci, [P(ci)]),

@@ -1,5 +1,6 @@
 """Build the in-tree shared library ``_lib/libgemm_collective_tiles.so`` with
-nvcc for sm_103a (one translation unit; no PyTorch headers involved).
+nvcc for sm_103a (two translation units, compiled side by side; no PyTorch
+headers involved).
 
 Usage: ``python -m gemm_collective_tiles_gb300.build`` or ``build()``.
 """
@@ -13,10 +14,12 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_FP8 = os.path.join(PKG, "csrc_fp8")
 LIBDIR = os.path.join(PKG, "_lib")
 LIBNAME = "libgemm_collective_tiles.so"
-SOURCES = ["iris_api.cu"]
-HEADERS = ["fused_kernel.cuh", "ptx.cuh"]
+SOURCES = [os.path.join(CSRC, "iris_api.cu"), os.path.join(CSRC_FP8, "fp8_api.cu")]
+HEADERS = [os.path.join(CSRC, f) for f in ("fused_kernel.cuh", "ptx.cuh")]
+HEADERS += [os.path.join(CSRC_FP8, f) for f in ("fp8_ptx.cuh", "fp8_quant.cuh", "fp8_gemm.cuh")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,7 +38,7 @@ def _stale(target: str) -> bool:
     if not os.path.exists(target):
         return True
     t = os.path.getmtime(target)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    deps = SOURCES + HEADERS
     deps.append(os.path.join(ROOT, "include", "gemm_collective_tiles.h"))
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
@@ -51,10 +54,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     cmd = [nvcc_path(), "-O3", "-std=c++17", "-lineinfo", *ARCH,
            "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
            "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           "-DGCT_BUILD", "-o", tmp]
+           "-DGCT_BUILD", "--threads", str(len(SOURCES)), "-o", tmp]
     if extra_flags:
         cmd += list(extra_flags)
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
+    cmd += SOURCES
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, capture_output=True, text=True)

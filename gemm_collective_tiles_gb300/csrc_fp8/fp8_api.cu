@@ -1,0 +1,521 @@
+// Host side of the block-scaled 8-bit float entry points declared in
+// include/gemm_collective_tiles.h: argument checks, operand layouts, the
+// choice of tile and split, tensor maps and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+
+#include "gemm_collective_tiles.h"
+#include "fp8_gemm.cuh"
+
+using namespace gct;
+using namespace gct::fp8;
+
+namespace {
+
+constexpr size_t WS_HEADER = 256;
+constexpr size_t WS_FIXED = WS_HEADER + MAX_SPLIT_SLOTS * 8;
+constexpr unsigned long long DEFAULT_WAIT_NS = 2000000000ull;
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+std::mutex g_mu;
+EncodeTiledFn g_encode = nullptr;
+
+int cuda_fail(const char* what, int code) {
+    static const bool on = [] {
+        const char* e = std::getenv("IRIS_B200_DEBUG");
+        return e && e[0] && e[0] != '0';
+    }();
+    if (on) std::fprintf(stderr, "[iris_b200] %s failed: %d\n", what, code);
+    return IRIS_ECUDA;
+}
+
+// per device: SMs, co-resident CTA pairs of each pair kernel (0 = not set up)
+struct DeviceInfo {
+    int sms, pairs_mm, pairs_wg;
+    bool done;
+};
+DeviceInfo g_dev[64];
+
+template <int KIND, int CG>
+int setup_kernel(int sms, int* pairs) {
+    using G = Geo<KIND, CG>;
+    cudaError_t e = cudaFuncSetAttribute(block_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(G::BYTES));
+    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (8-bit products)", static_cast<int>(e));
+    // the warpgroups' register shares must fit in what the launch allots, or
+    // a warpgroup would wait for registers that never come
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, block_gemm_kernel<KIND, CG>);
+    if (e != cudaSuccess) return cuda_fail("cudaFuncGetAttributes", static_cast<int>(e));
+    const int need = 128 * G::REGS_CTL + 256 * G::REGS_PROMOTE + (KIND == KIND_WG ? 128 * G::REGS_CONV : 0);
+    if (fa.numRegs * G::THREADS < need) return cuda_fail("register shares of the 8-bit products", fa.numRegs);
+    if (pairs) {
+        cudaLaunchAttribute attr;
+        cudaLaunchConfig_t lc;
+        std::memset(&lc, 0, sizeof(lc));
+        lc.gridDim = dim3(sms - (sms & 1));
+        lc.blockDim = dim3(G::THREADS);
+        lc.dynamicSmemBytes = G::BYTES;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        lc.attrs = &attr;
+        lc.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(pairs, block_gemm_kernel<KIND, CG>, &lc);
+        if (e != cudaSuccess || *pairs < 1) return cuda_fail("cudaOccupancyMaxActiveClusters", static_cast<int>(e));
+    }
+    return IRIS_OK;
+}
+
+int device_info(DeviceInfo* out) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IRIS_ECUDA;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceInfo& d = g_dev[dev];
+    if (!d.done) {
+        if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return IRIS_ECUDA;
+        int rc;
+        if ((rc = setup_kernel<KIND_MM, 1>(d.sms, nullptr))) return rc;
+        if ((rc = setup_kernel<KIND_MM, 2>(d.sms, &d.pairs_mm))) return rc;
+        if ((rc = setup_kernel<KIND_WG, 1>(d.sms, nullptr))) return rc;
+        if ((rc = setup_kernel<KIND_WG, 2>(d.sms, &d.pairs_wg))) return rc;
+        if (!g_encode) {
+            void* fn = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+                    cudaSuccess ||
+                q != cudaDriverEntryPointSuccess || !fn)
+                return cuda_fail("cuTensorMapEncodeTiled entry point", -1);
+            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+        }
+        d.done = true;
+    }
+    *out = d;
+    return IRIS_OK;
+}
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+int dtype_size(iris_dtype t) { return t == IRIS_F32 ? 4 : 2; }
+
+bool dims_ok(int64_t M, int64_t N, int64_t K) {
+    // 128-rounded sizes stay below 2^31
+    const int64_t lim = (int64_t(1) << 31) - 512;
+    return M >= 0 && N >= 0 && K >= 0 && M <= lim && N <= lim && K <= lim;
+}
+bool dtype16(iris_dtype t) { return t == IRIS_F16 || t == IRIS_BF16; }
+bool dtype_ok(iris_dtype t) { return dtype16(t) || t == IRIS_F32; }
+bool fp8_ok(iris_fp8 t) { return t == IRIS_E4M3 || t == IRIS_E5M2; }
+
+// a matrix that is read: pointer (unless empty), no negative stride, element alignment
+int check_in(const iris_b200_mat* m, int64_t rows, int64_t cols, int elem) {
+    if (!m || m->row_stride < 0 || m->col_stride < 0) return IRIS_EINVAL;
+    if (rows == 0 || cols == 0) return IRIS_OK;
+    if (!m->data) return IRIS_EINVAL;
+    return reinterpret_cast<uintptr_t>(m->data) % elem ? IRIS_EALIGN : IRIS_OK;
+}
+// a matrix that is written: also no two elements at one address
+int check_out(const iris_b200_mat* m, int64_t rows, int64_t cols, int elem) {
+    const int rc = check_in(m, rows, cols, elem);
+    if (rc) return rc;
+    const int64_t r = m->row_stride, c = m->col_stride;
+    if (rows > 1 && r < 1) return IRIS_EINVAL;
+    if (cols > 1 && c < 1) return IRIS_EINVAL;
+    if (rows > 1 && cols > 1 && r <= c * (cols - 1) && c <= r * (rows - 1)) return IRIS_EINVAL;
+    return IRIS_OK;
+}
+
+// How the tensor memory accelerator can read a matrix in place: rows of unit
+// stride on a 16-byte base and pitch.
+bool tma_rows(const void* data, int64_t row_stride, int64_t col_stride, int64_t rows, int64_t cols, int elem) {
+    return aligned16(data) && (col_stride == 1 || cols == 1) &&
+           (rows == 1 || (row_stride >= cols && row_stride * elem % 16 == 0 && row_stride * elem < (int64_t(1) << 40)));
+}
+int64_t packed_pitch(int64_t cols, int elem) { return static_cast<int64_t>(round_up(cols * elem, 16)) / elem; }
+
+// Operand as it will be read: in place, or copied into rows of whole 16 bytes.
+struct Operand {
+    const void* data;
+    int64_t rows, cols, pitch;  // rows of unit-stride elements
+    bool transposed;            // its rows are the matrix's columns
+    bool copy;
+    size_t copy_bytes;
+};
+Operand resolve_operand(const iris_b200_mat* m, int64_t rows, int64_t cols, int elem, bool may_transpose) {
+    Operand o{m->data, rows, cols, m->row_stride, false, false, 0};
+    if (tma_rows(m->data, m->row_stride, m->col_stride, rows, cols, elem)) {
+        if (rows == 1) o.pitch = packed_pitch(cols, elem);
+        return o;
+    }
+    if (may_transpose && tma_rows(m->data, m->col_stride, m->row_stride, cols, rows, elem)) {
+        o = Operand{m->data, cols, rows, m->col_stride, true, false, 0};
+        if (cols == 1) o.pitch = packed_pitch(rows, elem);
+        return o;
+    }
+    o.copy = true;
+    o.pitch = packed_pitch(cols, elem);
+    o.copy_bytes = round_up(static_cast<size_t>(rows) * o.pitch * elem, 256);
+    return o;
+}
+template <typename E>
+int launch_repack(const iris_b200_mat* m, Operand& o, void* dst, int sms, cudaStream_t stream) {
+    const int64_t tiles = cdiv(o.rows, 32) * cdiv(o.cols, 32);
+    repack_kernel<E><<<static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(sms) * 8)), 256, 0, stream>>>(
+        static_cast<const E*>(m->data), m->row_stride, m->col_stride, static_cast<E*>(dst), o.pitch, o.rows, o.cols);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail("repack launch", static_cast<int>(e));
+    o.data = dst;
+    return IRIS_OK;
+}
+
+int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand& o, uint32_t b0, uint32_t b1, bool swizzle) {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.pitch) * elem};
+    cuuint32_t box[2] = {b0, b1}, es[2] = {1, 1};
+    const CUresult r = g_encode(m, dt, 2, const_cast<void*>(o.data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit operand)", static_cast<int>(r));
+}
+// {n, row, part} with a box of 128 bytes x 32 rows
+int make_store_map(CUtensorMap* m, iris_dtype t, const void* data, int64_t N, int64_t M, int64_t parts, int64_t pitch,
+                   int64_t part_stride) {
+    const int elem = dtype_size(t);
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(parts)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * elem, static_cast<cuuint64_t>(part_stride) * elem};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem), 32, 1}, es[3] = {1, 1, 1};
+    const CUtensorMapDataType dt = t == IRIS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : t == IRIS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = g_encode(m, dt, 3, const_cast<void*>(data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit output)", static_cast<int>(r));
+}
+
+// Tile, split and workspace of one product (rows x cols over depth).
+struct Plan {
+    int cg, split, part_stages, stages, m_blocks, n_blocks, group_m, grid;
+    bool staged;
+    int64_t part_pitch;
+    size_t copy_a, copy_b, partial, total;  // workspace offsets
+};
+
+// Estimated time in us of a variant.  Constants measured on GB300: a
+// launch, a stage of each tile kind with every SM running, an epilogue, and
+// the hand-over of split parts (their fp32 sums make one trip through L2).
+double estimate(bool wg, int cg, int slots, int64_t tiles, int64_t stages, int64_t split, double out_elems) {
+    const double stage = wg ? (cg == 2 ? 0.30 : 0.20) : (cg == 2 ? 0.33 : 0.22);
+    const int64_t part = cdiv(stages, split);
+    const int64_t waves = cdiv(tiles * split, slots);
+    double t = 4.0 + waves * (part * stage + (cg == 2 ? 1.0 : 0.7));
+    if (split > 1) t += 2.0 + out_elems * split * 8.0 / 4.0e6;
+    return t;
+}
+
+int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& d, const Operand& a, const Operand& b,
+              bool direct_out, int64_t rows, int64_t cols, int64_t depth) {
+    iris_b200_config z;
+    std::memset(&z, 0, sizeof(z));
+    if (!cfg) cfg = &z;
+    if (cfg->tile_m != 0 && cfg->tile_m != 128 && cfg->tile_m != 256) return IRIS_EINVAL;
+    if (cfg->k_split < 0 || cfg->k_split > 4096 || cfg->group_m < 0) return IRIS_EINVAL;
+    if (cfg->grid < 0 || cfg->grid > d.sms) return IRIS_EINVAL;
+    if (cfg->debug_skip_flag < 0) return IRIS_EINVAL;
+    if (cfg->tile_m == 256 && cfg->grid == 1) return IRIS_EINVAL;
+    const int64_t stages = cdiv(depth, wg ? 64 : 128);
+    const int grid = cfg->grid ? cfg->grid : d.sms;
+    const int pairs = std::min(wg ? d.pairs_wg : d.pairs_mm, grid / 2);
+    double best = 0;
+    pl.cg = 0;
+    for (int cg = 1; cg <= 2; ++cg) {
+        if (cfg->tile_m && cfg->tile_m != 128 * cg) continue;
+        const int slots = cg == 2 ? pairs : grid;
+        if (slots < 1) continue;
+        const int64_t mb = cdiv(rows, 128 * cg), nb = cdiv(cols, 128 * cg), tiles = mb * nb;
+        // arrival counters are one per tile and CTA; parts beyond a few
+        // hundred MB would cost more than an idle SM
+        const int64_t most = tiles * cg > MAX_SPLIT_SLOTS ? 1
+                             : cfg->k_split ? std::min<int64_t>(cfg->k_split, stages)
+                                            : std::min<int64_t>({stages, 64, std::max<int64_t>(1, (64 << 20) / std::max<int64_t>(1, rows * cols))});
+        for (int64_t want = cfg->k_split ? most : 1; want <= most; ++want) {
+            const int64_t part = cdiv(stages, want), split = cdiv(stages, part);
+            if (!cfg->k_split && split != want) continue;
+            const double t = estimate(wg, cg, slots, tiles, stages, split, double(rows) * cols);
+            if (pl.cg == 0 || t < best) {
+                best = t;
+                pl.cg = cg;
+                pl.split = static_cast<int>(split);
+                pl.part_stages = static_cast<int>(part);
+                if (mb * nb * split > 0x7FFFFFFF) return IRIS_EINVAL;
+                pl.m_blocks = static_cast<int>(mb);
+                pl.n_blocks = static_cast<int>(nb);
+            }
+        }
+    }
+    if (pl.cg == 0) return IRIS_EINVAL;
+    pl.stages = static_cast<int>(stages);
+    pl.group_m = cfg->group_m ? std::max(1, cfg->group_m / pl.cg) : 16 / pl.cg;
+    const int64_t units = int64_t(pl.m_blocks) * pl.n_blocks * pl.split;
+    pl.grid = static_cast<int>(std::min<int64_t>(units, pl.cg == 2 ? pairs : grid)) * pl.cg;
+    pl.staged = pl.split > 1 || !direct_out;
+    pl.part_pitch = packed_pitch(cols, 4);
+    pl.copy_a = WS_FIXED;
+    pl.copy_b = pl.copy_a + a.copy_bytes;
+    pl.partial = pl.copy_b + b.copy_bytes;
+    pl.total = pl.partial + (pl.staged ? round_up(size_t(pl.split) * rows * pl.part_pitch * 4, 256) : 0);
+    return IRIS_OK;
+}
+
+template <int KIND, int CG>
+int launch_gemm(const GemmParams& p, int grid, cudaStream_t stream) {
+    using G = Geo<KIND, CG>;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t lc;
+    std::memset(&lc, 0, sizeof(lc));
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(G::THREADS);
+    lc.dynamicSmemBytes = G::BYTES;
+    lc.stream = stream;
+    if (CG == 2) {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        lc.attrs = &attr;
+        lc.numAttrs = 1;
+    }
+    const cudaError_t e = cudaLaunchKernelEx(&lc, block_gemm_kernel<KIND, CG>, p);
+    return e == cudaSuccess ? IRIS_OK : cuda_fail("kernel launch (8-bit product)", static_cast<int>(e));
+}
+
+// out (rows x cols) of one product: everything that both kinds share.
+// `wg`: operand a is X (depth x rows codes), b is dY (depth x cols, 16-bit);
+// else a is A (rows x depth codes), b is B (depth x cols codes).
+int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b200_mat* sa, const iris_b200_mat* mb,
+                int b_type /* fp8 type or 16-bit dtype */, const iris_b200_mat* sb, const void* bias, iris_dtype bias_dtype,
+                const iris_b200_mat* out, iris_dtype out_dtype, int64_t rows, int64_t cols, int64_t depth,
+                const iris_b200_config* cfg, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
+    int rc;
+    if (rows == 0 || cols == 0) {
+        if (need) *need = WS_FIXED;
+        return IRIS_OK;
+    }
+    const int b_elem = wg ? 2 : 1;
+    const Operand none{nullptr, 0, 0, 0, false, false, 0};
+    Operand a = depth == 0 ? none : wg ? resolve_operand(ma, depth, rows, 1, false) : resolve_operand(ma, rows, depth, 1, false);
+    Operand b = depth == 0 ? none : resolve_operand(mb, depth, cols, b_elem, !wg);
+    const bool direct = tma_rows(out->data, out->row_stride, out->col_stride, rows, cols, dtype_size(out_dtype));
+    DeviceInfo d;
+    if ((rc = device_info(&d))) return rc;
+    Plan pl;
+    if ((rc = make_plan(pl, wg, cfg, d, a, b, direct, rows, cols, std::max<int64_t>(depth, 1)))) return rc;
+    if (need) {
+        *need = pl.total;
+        return IRIS_OK;
+    }
+    if (!ws || ws_bytes < pl.total) return IRIS_ENOWS;
+    if (!aligned16(ws)) return IRIS_EALIGN;
+
+    GemmParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = static_cast<int>(rows);
+    p.N = static_cast<int>(cols);
+    p.D = static_cast<int>(depth);
+    p.bias = bias;
+    p.bias_type = bias_dtype;
+    p.out = out->data;
+    p.out_type = out_dtype;
+    p.out_rs = out->row_stride;
+    p.out_cs = out->col_stride;
+    if (depth == 0) {
+        const int64_t n = cdiv(rows * cols, 256);
+        fill_kernel<<<static_cast<unsigned>(std::min<int64_t>(n, int64_t(d.sms) * 8)), 256, 0, stream>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? IRIS_OK : cuda_fail("fill launch", static_cast<int>(e));
+    }
+    char* w = static_cast<char*>(ws);
+    if (a.copy && (rc = launch_repack<uint8_t>(ma, a, w + pl.copy_a, d.sms, stream))) return rc;
+    if (b.copy) {
+        rc = wg ? launch_repack<uint16_t>(mb, b, w + pl.copy_b, d.sms, stream)
+                : launch_repack<uint8_t>(mb, b, w + pl.copy_b, d.sms, stream);
+        if (rc) return rc;
+    }
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (wg) {
+        const CUtensorMapDataType t16 = b_type == IRIS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, 64, false))) return rc;
+        if ((rc = make_map_2d(&p.tmB, t16, 2, b, 64, 64, true))) return rc;
+        const int t = b_type == IRIS_BF16;
+        p.idesc = idesc_of(t, t, 1, 1, 128 * pl.cg, 128 * pl.cg);
+        p.x_bf16 = t;
+        p.codes_e5m2 = a_type == IRIS_E5M2;
+    } else {
+        p.b_mn = !b.transposed;
+        // few rows: the box holds just them (whole groups of 8), the rest of
+        // the stage keeps what it held and feeds rows that are never read
+        p.a_box = rows < 128 ? static_cast<int>(round_up(rows, 8)) : 128;
+        if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, p.a_box, true))) return rc;
+        if ((rc = make_map_2d(&p.tmB, u8, 1, b, 128, 128, true))) return rc;
+        p.idesc = idesc_of(a_type, b_type, 0, p.b_mn, 128 * pl.cg, 128 * pl.cg);
+        p.sb = static_cast<const float*>(sb->data);
+        p.sb_rs = sb->row_stride;
+        p.sb_cs = sb->col_stride;
+    }
+    p.sa = static_cast<const float*>(sa->data);
+    p.sa_rs = sa->row_stride;
+    p.sa_cs = sa->col_stride;
+    p.stages_total = pl.stages;
+    p.part_stages = pl.part_stages;
+    p.split = pl.split;
+    p.m_blocks = pl.m_blocks;
+    p.n_blocks = pl.n_blocks;
+    p.group_m = pl.group_m;
+    p.n_units = pl.m_blocks * pl.n_blocks * pl.split;
+    p.ws = reinterpret_cast<WsHeader*>(w);
+    p.arrived = reinterpret_cast<unsigned long long*>(w + WS_HEADER);
+    p.partial = reinterpret_cast<float*>(w + pl.partial);
+    p.part_rs = pl.part_pitch;
+    p.part_stride = rows * pl.part_pitch;
+    p.staged = pl.staged;
+    p.wait_ns = cfg && cfg->wait_ns ? cfg->wait_ns : DEFAULT_WAIT_NS;
+    p.debug_skip = cfg ? static_cast<uint32_t>(cfg->debug_skip_flag) : 0u;
+    if (pl.staged)
+        rc = make_store_map(&p.tmC, IRIS_F32, p.partial, cols, rows, pl.split, pl.part_pitch, p.part_stride);
+    else
+        rc = make_store_map(&p.tmC, out_dtype, out->data, cols, rows, 1,
+                            rows == 1 ? packed_pitch(cols, dtype_size(out_dtype)) : out->row_stride,
+                            int64_t(packed_pitch(cols, dtype_size(out_dtype))));
+    if (rc) return rc;
+    if (wg) return pl.cg == 2 ? launch_gemm<KIND_WG, 2>(p, pl.grid, stream) : launch_gemm<KIND_WG, 1>(p, pl.grid, stream);
+    return pl.cg == 2 ? launch_gemm<KIND_MM, 2>(p, pl.grid, stream) : launch_gemm<KIND_MM, 1>(p, pl.grid, stream);
+}
+
+int check_matmul(const iris_b200_mat* A, const iris_b200_mat* B, const iris_b200_mat* out, iris_dtype out_dtype,
+                 int64_t M, int64_t N, int64_t K) {
+    int rc;
+    if (!dims_ok(M, N, K) || !dtype_ok(out_dtype)) return IRIS_EINVAL;
+    if ((rc = check_in(A, M, K, 1)) || (rc = check_in(B, K, N, 1))) return rc;
+    return check_out(out, M, N, dtype_size(out_dtype));
+}
+int check_wgrad(const iris_b200_mat* X, const iris_b200_mat* dY, iris_dtype dtype, const iris_b200_mat* out,
+                iris_dtype out_dtype, int64_t M, int64_t N, int64_t K) {
+    int rc;
+    if (!dims_ok(M, N, K) || !dtype16(dtype) || !dtype_ok(out_dtype)) return IRIS_EINVAL;
+    if ((rc = check_in(X, M, K, 1)) || (rc = check_in(dY, M, N, 2))) return rc;
+    return check_out(out, K, N, dtype_size(out_dtype));
+}
+
+template <int T>
+void launch_quant(const QuantParams& q, bool vec, bool tile, unsigned grid, cudaStream_t stream) {
+    if (vec && tile) quantize_vec_kernel<T, true><<<grid, Q_THREADS, 0, stream>>>(q);
+    else if (vec) quantize_vec_kernel<T, false><<<grid, Q_THREADS, 0, stream>>>(q);
+    else if (tile) quantize_any_kernel<T, true><<<grid, Q_THREADS, 0, stream>>>(q);
+    else quantize_any_kernel<T, false><<<grid, Q_THREADS, 0, stream>>>(q);
+}
+
+}  // namespace
+
+extern "C" {
+
+int iris_b200_quantize_fp8(const iris_b200_mat* x, iris_dtype x_dtype, const iris_b200_mat* codes, iris_fp8 type,
+                           const iris_b200_mat* scales, int64_t M, int64_t K, int block_rows, int pow2,
+                           cudaStream_t stream) {
+    int rc;
+    if (!dims_ok(M, 0, K) || !dtype_ok(x_dtype) || !fp8_ok(type) || (block_rows != 1 && block_rows != 128)) return IRIS_EINVAL;
+    const int64_t kb = cdiv(K, 128), sr = block_rows == 1 ? M : cdiv(M, 128);
+    if ((rc = check_in(x, M, K, dtype_size(x_dtype))) || (rc = check_out(codes, M, K, 1)) || (rc = check_out(scales, sr, kb, 4)))
+        return rc;
+    if (M == 0 || K == 0) return IRIS_OK;
+    const int64_t blocks = kb * cdiv(M, Q_ROWS);
+    if (blocks > 0x7FFFFFFF) return IRIS_EINVAL;
+    QuantParams q;
+    q.x = x->data;
+    q.codes = static_cast<uint8_t*>(codes->data);
+    q.scales = static_cast<float*>(scales->data);
+    q.x_rs = x->row_stride;
+    q.x_cs = x->col_stride;
+    q.c_rs = codes->row_stride;
+    q.c_cs = codes->col_stride;
+    q.s_rs = scales->row_stride;
+    q.s_cs = scales->col_stride;
+    q.M = M;
+    q.K = K;
+    q.kblocks = static_cast<unsigned>(kb);
+    q.e5m2 = type == IRIS_E5M2;
+    q.pow2 = pow2 != 0;
+    q.fmax = q.e5m2 ? 57344.f : 448.f;
+    // f16 input: with scales of at least 2^-15 (e5m2: 2^-8) the codes' finest
+    // step is f16's own, 2^-24, so scaled codes are f16 values again and
+    // nothing that f16 can hold is lost to the bound
+    q.pmin = x_dtype == IRIS_F16 ? (q.e5m2 ? -8 : -15) : -100;
+    const int e = dtype_size(x_dtype);
+    // 16-byte reads and 8-byte writes where every row starts on them
+    const bool vec = (x->col_stride == 1 || K == 1) && (codes->col_stride == 1 || K == 1) && aligned16(x->data) &&
+                     (M == 1 || x->row_stride * e % 16 == 0) && reinterpret_cast<uintptr_t>(codes->data) % 8 == 0 &&
+                     (M == 1 || codes->row_stride % 8 == 0);
+    const bool tile = block_rows == 128;
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (x_dtype == IRIS_F32) launch_quant<T_F32>(q, vec, tile, grid, stream);
+    else if (x_dtype == IRIS_F16) launch_quant<T_F16>(q, vec, tile, grid, stream);
+    else launch_quant<T_BF16>(q, vec, tile, grid, stream);
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? IRIS_OK : cuda_fail("quantize launch", static_cast<int>(err));
+}
+
+int iris_b200_matmul_fp8_workspace_size(const iris_b200_mat* A, const iris_b200_mat* B, const iris_b200_mat* out,
+                                        iris_dtype out_dtype, int64_t M, int64_t N, int64_t K,
+                                        const iris_b200_config* cfg, size_t* bytes) {
+    if (!bytes) return IRIS_EINVAL;
+    const int rc = check_matmul(A, B, out, out_dtype, M, N, K);
+    if (rc) return rc;
+    return run_product(false, A, IRIS_E4M3, nullptr, B, 0, nullptr, nullptr, IRIS_F32, out, out_dtype, M, N, K, cfg, nullptr,
+                       0, nullptr, bytes);
+}
+
+int iris_b200_matmul_fp8(const iris_b200_mat* A, iris_fp8 a_type, const iris_b200_mat* a_scales, const iris_b200_mat* B,
+                         iris_fp8 b_type, const iris_b200_mat* b_scales, const void* bias, iris_dtype bias_dtype,
+                         const iris_b200_mat* out, iris_dtype out_dtype, int64_t M, int64_t N, int64_t K,
+                         const iris_b200_config* cfg, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    int rc = check_matmul(A, B, out, out_dtype, M, N, K);
+    if (rc) return rc;
+    if (!fp8_ok(a_type) || !fp8_ok(b_type) || (bias && !dtype_ok(bias_dtype))) return IRIS_EINVAL;
+    const int64_t kb = cdiv(K, 128);
+    if ((rc = check_in(a_scales, M, kb, 4)) || (rc = check_in(b_scales, kb, cdiv(N, 128), 4))) return rc;
+    if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_size(bias_dtype)) return IRIS_EALIGN;
+    return run_product(false, A, a_type, a_scales, B, b_type, b_scales, bias, bias_dtype, out, out_dtype, M, N, K, cfg,
+                       workspace, workspace_bytes, stream, nullptr);
+}
+
+int iris_b200_weight_grad_fp8_workspace_size(const iris_b200_mat* X, const iris_b200_mat* dY, iris_dtype dtype,
+                                             const iris_b200_mat* out, iris_dtype out_dtype, int64_t M, int64_t N,
+                                             int64_t K, const iris_b200_config* cfg, size_t* bytes) {
+    if (!bytes) return IRIS_EINVAL;
+    const int rc = check_wgrad(X, dY, dtype, out, out_dtype, M, N, K);
+    if (rc) return rc;
+    return run_product(true, X, IRIS_E4M3, nullptr, dY, dtype, nullptr, nullptr, IRIS_F32, out, out_dtype, K, N, M, cfg,
+                       nullptr, 0, nullptr, bytes);
+}
+
+int iris_b200_weight_grad_fp8(const iris_b200_mat* X, iris_fp8 x_type, const iris_b200_mat* x_scales,
+                              const iris_b200_mat* dY, iris_dtype dtype, const iris_b200_mat* out, iris_dtype out_dtype,
+                              int64_t M, int64_t N, int64_t K, const iris_b200_config* cfg, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+    int rc = check_wgrad(X, dY, dtype, out, out_dtype, M, N, K);
+    if (rc) return rc;
+    if (!fp8_ok(x_type)) return IRIS_EINVAL;
+    if ((rc = check_in(x_scales, M, cdiv(K, 128), 4))) return rc;
+    return run_product(true, X, x_type, x_scales, dY, dtype, nullptr, nullptr, IRIS_F32, out, out_dtype, K, N, M, cfg,
+                       workspace, workspace_bytes, stream, nullptr);
+}
+
+}  // extern "C"

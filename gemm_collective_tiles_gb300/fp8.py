@@ -1,0 +1,230 @@
+"""Block-scaled 8-bit floats: quantisation, matrix product, weight gradient.
+
+A matrix is held as codes (``torch.float8_e4m3fn`` or ``torch.float8_e5m2``)
+and one fp32 scale for each block of 128 columns, per row ("rows": activations
+and gradients) or per 128 rows ("tiles": weights); a value is code * scale.
+The codes and scales of a layer's input serve twice: as the operand of the
+forward product and as the 8-bit checkpoint that the backward pass reads.
+
+Like the library's other ops, every op here writes into tensors that the
+caller owns, enqueues its kernels on one stream and returns (the products:
+the workspace, to be passed to the next call on that stream).  Tensors may
+have any non-negative strides.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _native
+from ._native import iris_b200_mat
+
+_FP8 = {torch.float8_e4m3fn: _native.IRIS_E4M3, torch.float8_e5m2: _native.IRIS_E5M2}
+_DT = {torch.float16: _native.IRIS_F16, torch.bfloat16: _native.IRIS_BF16, torch.float32: _native.IRIS_F32}
+_BLOCK = 128
+_ROWS = {"rows": 1, "tiles": _BLOCK}
+
+
+def _blocks(n: int) -> int:
+    return (n + _BLOCK - 1) // _BLOCK
+
+
+def _mat(t: torch.Tensor) -> iris_b200_mat:
+    return iris_b200_mat(t.data_ptr(), *t.stride())
+
+
+def _check(name: str, t: torch.Tensor, shape, dtypes, device=None) -> None:
+    """A 2-D (or, for a bias, 1-D) device tensor of this shape and one of these types."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} is not a tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has type {t.dtype}")
+    if shape is None:
+        if t.dim() != 2:
+            raise ValueError(f"{name} has {t.dim()} dimensions, not 2")
+    elif tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not on a CUDA device")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _cfgp(config):
+    if config is None:
+        return None
+    from . import make_config
+    return ctypes.byref(make_config(**config) if isinstance(config, dict) else config)
+
+
+def _stream(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.cuda_stream
+    return int(stream)
+
+
+_F32 = (torch.float32,)
+
+
+def empty_fp8(M: int, K: int, block: str = "rows", dtype: torch.dtype = torch.float8_e4m3fn, device="cuda"):
+    """Uninitialised (codes, scales) for an M x K matrix: code rows on 16
+    bytes, so that products read them in place, and "rows" scales with the
+    rows next to each other in memory."""
+    if block not in _ROWS:
+        raise ValueError(f"unknown block {block!r}")
+    if dtype not in _FP8:
+        raise TypeError(f"{dtype} is not an 8-bit float type")
+    codes = torch.empty(M, (K + 15) // 16 * 16, dtype=dtype, device=device)[:, :K]
+    if block == "rows":
+        return codes, torch.empty(_blocks(K), M, dtype=torch.float32, device=device).t()
+    return codes, torch.empty(_blocks(M), _blocks(K), dtype=torch.float32, device=device)
+
+
+def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block: str = "rows",
+                 pow2: bool = True, stream=None) -> None:
+    """Quantise x (M, K) (f16, bf16 or f32) into codes (M, K) and scales:
+    (M, ceil(K/128)) for "rows", (ceil(M/128), ceil(K/128)) for "tiles".
+
+    With ``pow2`` a block's scale is the smallest power of two that takes its
+    largest finite magnitude into the codes' range, and scaled codes are exact
+    16-bit floats; without it the scale maps that magnitude to the largest
+    code.  NaN and infinities become the NaN code and leave the scale to the
+    block's other elements; zero blocks get the smallest scale."""
+    if block not in _ROWS:
+        raise ValueError(f"unknown block {block!r}")
+    _check("x", x, None, _DT)
+    M, K = x.shape
+    _check("codes", codes, (M, K), _FP8, x.device)
+    _check("scales", scales, (M if block == "rows" else _blocks(M), _blocks(K)), _F32, x.device)
+    with torch.cuda.device(x.device):
+        _native.check("iris_b200_quantize_fp8", _native.load().iris_b200_quantize_fp8(
+            _mat(x), _DT[x.dtype], _mat(codes), _FP8[codes.dtype], _mat(scales), M, K, _ROWS[block], int(pow2),
+            _stream(stream, x.device)))
+
+
+def _run(name: str, ws, device, size_args, call):
+    """One product: the given workspace, or a new one where it is missing or too small."""
+    with torch.cuda.device(device):
+        rc = _native.IRIS_ENOWS if ws is None else call(ws)
+        if rc == _native.IRIS_ENOWS:
+            from . import Workspace
+            need = ctypes.c_size_t(0)
+            size = "iris_b200_" + name + "_workspace_size"
+            _native.check(size, getattr(_native.load(), size)(*size_args, ctypes.byref(need)))
+            ws = Workspace(int(need.value), device)
+            rc = call(ws)
+        _native.check("iris_b200_" + name, rc)
+    return ws
+
+
+def matmul_fp8(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale: torch.Tensor, out: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, config=None, workspace=None, stream=None):
+    """out = (A * A_scale) @ (B * B_scale) + bias.
+
+    A (M, K) codes with "rows" scales (M, ceil(K/128)); B (K, N) codes with
+    "tiles" scales (ceil(K/128), ceil(N/128)), in either order: the transpose
+    of a quantised matrix is ``codes.t(), scales.t()``.  bias (N,) and out
+    (M, N) are f16, bf16 or f32.  The 128-deep blocks are summed in fp32 and
+    rounded once.  Returns the workspace."""
+    _check("A", A, None, _FP8)
+    M, K = A.shape
+    dev = A.device
+    _check("B", B, None, _FP8, dev)
+    N = B.shape[1]
+    if B.shape[0] != K:
+        raise ValueError(f"A has {K} columns and B has {B.shape[0]} rows")
+    _check("A_scale", A_scale, (M, _blocks(K)), _F32, dev)
+    _check("B_scale", B_scale, (_blocks(K), _blocks(N)), _F32, dev)
+    _check("out", out, (M, N), _DT, dev)
+    bias_ptr, bias_dt = None, _native.IRIS_F32
+    if bias is not None:
+        _check("bias", bias, (N,), _DT, dev)
+        if N > 1 and bias.stride(0) != 1:
+            raise ValueError("bias is not contiguous")
+        bias_ptr, bias_dt = bias.data_ptr(), _DT[bias.dtype]
+    a, b, o, cfg, st = _mat(A), _mat(B), _mat(out), _cfgp(config), _stream(stream, dev)
+    sa, sb = _mat(A_scale), _mat(B_scale)
+    lib = _native.load()
+    return _run("matmul_fp8", workspace, dev, (a, b, o, _DT[out.dtype], M, N, K, cfg), lambda ws: lib.iris_b200_matmul_fp8(
+        a, _FP8[A.dtype], sa, b, _FP8[B.dtype], sb, bias_ptr, bias_dt, o, _DT[out.dtype], M, N, K, cfg,
+        ws.ptr, ws.nbytes, st))
+
+
+def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, out: torch.Tensor, config=None,
+                    workspace=None, stream=None):
+    """out = (X * X_scale)^T @ dY: the weight gradient (K, N) of a linear layer
+    from the 8-bit checkpoint of its input.
+
+    X (M, K) codes with "rows" scales (M, ceil(K/128)); dY (M, N) f16 or bf16;
+    out f16, bf16 or f32.  X's values enter in dY's type, exactly where the
+    scales are powers of two.  Returns the workspace."""
+    _check("X", X, None, _FP8)
+    M, K = X.shape
+    dev = X.device
+    _check("dY", dY, None, (torch.float16, torch.bfloat16), dev)
+    if dY.shape[0] != M:
+        raise ValueError(f"X has {M} rows and dY has {dY.shape[0]}")
+    N = dY.shape[1]
+    _check("X_scale", X_scale, (M, _blocks(K)), _F32, dev)
+    _check("out", out, (K, N), _DT, dev)
+    x, d, o, cfg, st, sx = _mat(X), _mat(dY), _mat(out), _cfgp(config), _stream(stream, dev), _mat(X_scale)
+    lib = _native.load()
+    dt, odt = _DT[dY.dtype], _DT[out.dtype]
+    return _run("weight_grad_fp8", workspace, dev, (x, d, dt, o, odt, M, N, K, cfg), lambda ws: lib.iris_b200_weight_grad_fp8(
+        x, _FP8[X.dtype], sx, d, dt, o, odt, M, N, K, cfg, ws.ptr, ws.nbytes, st))
+
+
+class _Fp8Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, W_scale, weight, bias, grad_dtype, workspace):
+        x2 = x.reshape(-1, x.shape[-1])
+        M, K = x2.shape
+        codes, scales = empty_fp8(M, K, "rows", device=x.device)
+        quantize_fp8(x2, codes, scales)
+        y = torch.empty(M, W.shape[1], dtype=x.dtype, device=x.device)
+        ctx.ws = matmul_fp8(codes, scales, W, W_scale, y, bias=bias, workspace=workspace)
+        # the 8-bit checkpoint is all that is kept of x
+        ctx.save_for_backward(codes, scales, W, W_scale)
+        ctx.x_shape, ctx.grad_dtype, ctx.has_bias = x.shape, grad_dtype, bias is not None
+        return y.reshape(*x.shape[:-1], W.shape[1])
+
+    @staticmethod
+    def backward(ctx, dy):
+        codes, scales, W, W_scale = ctx.saved_tensors
+        M, K = codes.shape
+        N = W.shape[1]
+        dy2 = dy.reshape(M, N)
+        dx = dw = db = None
+        ws = ctx.ws
+        if ctx.needs_input_grad[0]:
+            dcodes, dscales = empty_fp8(M, N, "rows", ctx.grad_dtype, dy.device)
+            quantize_fp8(dy2, dcodes, dscales)
+            dx = torch.empty(M, K, dtype=dy.dtype, device=dy.device)
+            ws = matmul_fp8(dcodes, dscales, W.t(), W_scale.t(), dx, workspace=ws)
+            dx = dx.reshape(ctx.x_shape)
+        if ctx.needs_input_grad[3]:
+            dw = torch.empty(K, N, dtype=torch.float32, device=dy.device)
+            weight_grad_fp8(codes, scales, dy2, dw, workspace=ws)
+        if ctx.has_bias and ctx.needs_input_grad[4]:
+            db = dy2.float().sum(0).to(dy.dtype)
+        return dx, None, None, dw, db, None, None
+
+
+def fp8_linear(x: torch.Tensor, W: torch.Tensor, W_scale: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, grad_dtype: torch.dtype = torch.float8_e5m2, workspace=None):
+    """Differentiable y = x @ (W * W_scale) + bias, x (..., K) f16 or bf16.
+
+    W (K, N) codes with "tiles" scales; ``weight`` is the fp32 master weight
+    (K, N) that W was quantised from and that receives the gradient (None: no
+    weight gradient).  The forward pass quantises x once; codes and scales are
+    the product's operand and, in place of x, what is kept for the backward
+    pass: dx = quantised(dy) @ W^T, dweight = checkpoint^T @ dy."""
+    if x.dim() < 1 or x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("x is a f16 or bf16 tensor (..., K)")
+    if weight is not None and (weight.dtype != torch.float32 or weight.shape != W.shape):
+        raise ValueError(f"weight is a float32 tensor of shape {tuple(W.shape)}")
+    return _Fp8Linear.apply(x, W, W_scale, weight, bias, grad_dtype, workspace)
