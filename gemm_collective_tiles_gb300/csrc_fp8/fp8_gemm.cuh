@@ -122,12 +122,11 @@ __device__ __forceinline__ void raise_timeout(const Ctl& c, int where, int index
     __threadfence();
     atomicExch(&c.ws->abort_epoch, c.epoch);
 }
-template <bool CLUSTER>
 __device__ __forceinline__ bool wait_bar(const Ctl& c, uint64_t* bar, uint32_t parity, int where) {
-    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
-        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if ((i & 15) == 0) {
             if (launch_aborted(c)) return false;
             if (global_timer_ns() - t0 > c.limit) {
@@ -242,7 +241,7 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         const int row = (x.mb * CG + ctl.half) * BM;
         const int col = x.nb * G::BN + ctl.half * (G::BN / CG);
         for (int s = x.lo; s < x.hi; ++s) {
-            if (!wait_bar<false>(ctl, &sm.empty[stage], phase ^ 1, WAIT_EMPTY)) {
+            if (!wait_bar(ctl, &sm.empty[stage], phase ^ 1, WAIT_EMPTY)) {
                 ok = false;
                 break;
             }
@@ -307,7 +306,7 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         const Unit x = unit_of(p, u);
         for (int s0 = x.lo; s0 < x.hi && ok; s0 += CH, ++chunk) {
             const uint32_t buf = chunk & 1, use = chunk >> 1;
-            if (!wait_bar<CG == 2>(ctl, &sm.acc_empty[buf], (use & 1) ^ 1, WAIT_ACC_EMPTY)) {
+            if (!wait_bar(ctl, &sm.acc_empty[buf], (use & 1) ^ 1, WAIT_ACC_EMPTY)) {
                 ok = false;
                 break;
             }
@@ -315,8 +314,8 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
             const uint32_t d = tmem + buf * G::BN;
             const int end = min(x.hi, s0 + CH);
             for (int s = s0; s < end; ++s) {
-                if (!wait_bar<false>(ctl, &sm.full[stage], phase, WAIT_FULL) ||
-                    (KIND == KIND_WG && !wait_bar<CG == 2>(ctl, &sm.conv[stage], phase, WAIT_CONVERTED))) {
+                if (!wait_bar(ctl, &sm.full[stage], phase, WAIT_FULL) ||
+                    (KIND == KIND_WG && !wait_bar(ctl, &sm.conv[stage], phase, WAIT_CONVERTED))) {
                     ok = false;
                     break;
                 }
@@ -356,17 +355,42 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
     drain_bar(ctl, sm.final_bar, 0, WAIT_DRAIN_MMA);
 }
 
+__device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// bytes that are infinity or NaN, as a nonzero word (add: 4 or 1 in each byte)
+__device__ __forceinline__ uint32_t special_codes(uint32_t w, uint32_t add) {
+    return ((w & 0x7F7F7F7Fu) + add) & 0x80808080u;
+}
+// a power of two small enough for 2^120 times it to be a bf16 number, or zero
+__device__ __forceinline__ bool simple_scale(float s) {
+    return (__float_as_uint(s) & 0x7FFFFFu) == 0u && s <= 128.f;
+}
 // Converters: 64 x 128 codes of a stage -> 16-bit values times their row's
 // scale, in the MN-major swizzled layout (two columns of 64 k, rows of 128
 // bytes, 16-byte units XORed with the row).  A thread takes 16 codes of four
 // rows; threads of the second column write their two units in the other
 // order, so eight threads of a row touch all banks once.  The product is
 // rounded once to the 16-bit type; a power-of-two scale makes it exact.
+// bf16 with power-of-two scales, the usual case, needs no conversion
+// instructions: a code's exponent and mantissa bits set into a bf16 number
+// give its value times 2^-120 (e5m2: 2^-112), subnormal codes included, and
+// one packed multiplication by scale * 2^120 is exact.  NaN and infinity do
+// not follow that rule; a thread that meets one converts its codes one by one.
 template <int CG>
 __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, int t, int first, int step) {
     using G = Geo<KIND_WG, CG>;
     uint32_t stage = 0, phase = 0;
     const int seg = t & 7, row0 = t >> 3, col = seg >> 2;
+    const int e5m2 = p.codes_e5m2;
+    const uint32_t add = e5m2 ? 0x04040404u : 0x01010101u, mask = e5m2 ? 0x0FE00FE0u : 0x07F007F0u;
+    const int shift = e5m2 ? 3 : 4;
+    const float widen = __int_as_float((127 + (e5m2 ? 112 : 120)) << 23);
     for (int u = first; u < p.n_units; u += step) {
         const Unit x = unit_of(p, u);
         // this CTA's 128 output rows are one block of scales
@@ -384,29 +408,45 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
         fetch(x.lo);
         for (int s = x.lo; s < x.hi; ++s) {
             float sc[4];
+            bool simple = true;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[i] = next[i];
+            for (int i = 0; i < 4; ++i) {
+                sc[i] = next[i];
+                simple = simple && simple_scale(sc[i]);
+            }
             if (s + 1 < x.hi) fetch(s + 1);
-            if (!wait_bar<false>(ctl, &sm.raw[stage], phase, WAIT_RAW)) return;
+            if (!wait_bar(ctl, &sm.raw[stage], phase, WAIT_RAW)) return;
             const uint8_t* src = sm.raw_tile(stage);
             uint8_t* dst = sm.a(stage) + col * 8192;
+            uint4 c4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c4[i] = *reinterpret_cast<const uint4*>(src + (row0 + 16 * i) * 128 + seg * 16);
+            uint32_t special = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                special |= special_codes(c4[i].x, add) | special_codes(c4[i].y, add) | special_codes(c4[i].z, add) |
+                           special_codes(c4[i].w, add);
+            const bool fast = p.x_bf16 && simple && !special;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = row0 + 16 * i;
-                const uint4 c4 = *reinterpret_cast<const uint4*>(src + r * 128 + seg * 16);
-                const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
+                const uint32_t w[4] = {c4[i].x, c4[i].y, c4[i].z, c4[i].w};
                 uint32_t o[8];
+                if (fast) {
+                    const __nv_bfloat162 f = __float2bfloat162_rn(sc[i] * widen);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t h = cvt_f8x2_f16x2(w[j / 2] >> (16 * (j & 1)), p.codes_e5m2);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                    const float a = f.x * sc[i], b = f.y * sc[i];
-                    if (p.x_bf16) {
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&v);
-                    } else {
-                        const __half2 v = __floats2half2_rn(a, b);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&v);
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t v = __byte_perm(w[j / 2], 0u, (j & 1) ? 0x3424u : 0x1404u);  // codes in bytes 1 and 3
+                        const uint32_t b = (v & 0x80008000u) | ((v >> shift) & mask);
+                        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
+                        o[j] = *reinterpret_cast<const uint32_t*>(&y);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t h = cvt_f8x2_f16x2(w[j / 2] >> (16 * (j & 1)), p.codes_e5m2);
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                        o[j] = pack16(f.x * sc[i], f.y * sc[i], p.x_bf16);
                     }
                 }
                 const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
@@ -426,7 +466,7 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
             __syncwarp();
             if ((t & 31) == 0) {
                 if (CG == 2)
-                    mbar_arrive_cluster(mapa_shared(&sm.conv[stage], 0));
+                    mbar_arrive_remote(mapa_shared(&sm.conv[stage], 0));
                 else
                     mbar_arrive(&sm.conv[stage]);
             }
@@ -438,14 +478,6 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
     }
 }
 
-__device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
-    if (bf16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ float load_bias(const GemmParams& p, int col) {
     if (!p.bias || col >= p.N) return 0.f;
     if (p.bias_type == T_F32) return load_elem<T_F32>(p.bias, col);
@@ -483,17 +515,27 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
 
         const float* sa = p.sa + static_cast<long long>(row) * p.sa_rs;
         const float* sb = p.sb + (col0 / 128) * p.sb_cs;
-        auto scale_of = [&](int s) {
-            return (KIND == KIND_MM && live && row < p.M && s < x.hi) ? __ldg(sa + s * p.sa_cs) * __ldg(sb + s * p.sb_rs) : 0.f;
+        // the two scales of a stage are fetched two stages ahead and
+        // multiplied where they are used, so that no load is waited for
+        struct Scales {
+            float a, b;
         };
-        float s_cur = scale_of(x.lo), s_next = scale_of(x.lo + 1);
+        auto scales_of = [&](int s) {
+            Scales v{0.f, 0.f};
+            if (KIND == KIND_MM && live && s < x.hi) {
+                if (row < p.M) v.a = __ldg(sa + s * p.sa_cs);
+                v.b = __ldg(sb + s * p.sb_rs);
+            }
+            return v;
+        };
+        Scales s_cur = scales_of(x.lo), s_next = scales_of(x.lo + 1);
         for (int s0 = x.lo; s0 < x.hi; s0 += CH, ++chunk) {
             const uint32_t buf = chunk & 1;
-            const float s_after = scale_of(s0 + 2);
-            if (!wait_bar<false>(ctl, &sm.acc_full[buf], (chunk >> 1) & 1, WAIT_ACC_FULL)) return false;
+            const Scales s_after = scales_of(s0 + 2);
+            if (!wait_bar(ctl, &sm.acc_full[buf], (chunk >> 1) & 1, WAIT_ACC_FULL)) return false;
             tc_fence_after();
             if (live) {
-                const float sc = KIND == KIND_MM ? s_cur : 1.f;
+                const float sc = KIND == KIND_MM ? s_cur.a * s_cur.b : 1.f;
                 const unsigned long long sc2 = pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
                 const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::BN + h * COLS;
                 // KIND_MM promotes every stage: its next load runs under the
@@ -516,7 +558,7 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
             __syncwarp();
             if (lane == 0) {
                 if (CG == 2)
-                    mbar_arrive_cluster(mapa_shared(&sm.acc_empty[buf], 0));
+                    mbar_arrive_remote(mapa_shared(&sm.acc_empty[buf], 0));
                 else
                     mbar_arrive(&sm.acc_empty[buf]);
             }
@@ -581,7 +623,7 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
             auto sync = [&]() {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sm.sync);
-                const bool ok = wait_bar<false>(ctl, sm.sync, syncs & 1, WAIT_SYNC);
+                const bool ok = wait_bar(ctl, sm.sync, syncs & 1, WAIT_SYNC);
                 ++syncs;
                 return ok;
             };
