@@ -57,8 +57,7 @@ int setup_kernel(int sms, int* pairs) {
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, block_gemm_kernel<KIND, CG>);
     if (e != cudaSuccess) return cuda_fail("cudaFuncGetAttributes", static_cast<int>(e));
-    const int need = 128 * G::REGS_CTL + 256 * G::REGS_PROMOTE + (KIND == KIND_WG ? 128 * G::REGS_CONV : 0);
-    if (fa.numRegs * G::THREADS < need) return cuda_fail("register shares of the 8-bit products", fa.numRegs);
+    if (fa.numRegs * G::THREADS < G::REGS_TOTAL) return cuda_fail("register shares of the 8-bit products", fa.numRegs);
     if (pairs) {
         cudaLaunchAttribute attr;
         cudaLaunchConfig_t lc;
@@ -187,6 +186,17 @@ int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand&
                                 swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit operand)", static_cast<int>(r));
+}
+// 16-bit rows as groups of 64 columns, {64, row, column / 64}: a box of 64 rows
+// of `groups` groups, 8192 bytes each
+int make_map_groups(CUtensorMap* m, CUtensorMapDataType dt, const Operand& o, uint32_t groups) {
+    cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(o.rows), static_cast<cuuint64_t>(o.cols / 64)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.pitch) * 2, 128};
+    cuuint32_t box[3] = {64, 64, groups}, es[3] = {1, 1, 1};
+    const CUresult r = g_encode(m, dt, 3, const_cast<void*>(o.data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (groups of columns)", static_cast<int>(r));
 }
 // {n, row, part} with a box of 128 bytes x 32 rows
 int make_store_map(CUtensorMap* m, iris_dtype t, const void* data, int64_t N, int64_t M, int64_t parts, int64_t pitch,
@@ -354,7 +364,12 @@ int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b2
     if (wg) {
         const CUtensorMapDataType t16 = b_type == IRIS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
         if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, 64, false))) return rc;
-        if ((rc = make_map_2d(&p.tmB, t16, 2, b, 64, 64, true))) return rc;
+        // one box of all of a CTA's columns where no 64-column group runs past
+        // the end of a row, else a box per group
+        p.b_chunked = cols % 64 == 0;
+        if ((rc = p.b_chunked ? make_map_groups(&p.tmB, t16, b, 2)
+                              : make_map_2d(&p.tmB, t16, 2, b, 64, 64, true)))
+            return rc;
         const int t = b_type == IRIS_BF16;
         p.idesc = idesc_of(t, t, 1, 1, 128 * pl.cg, 128 * pl.cg);
         p.x_bf16 = t;

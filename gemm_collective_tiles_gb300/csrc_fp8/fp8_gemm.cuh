@@ -9,20 +9,21 @@
 // tensor cores leave in tensor memory; eight promotion warps add each chunk,
 // times its scale, into fp32 registers.  In KIND_MM a chunk is one K block of
 // 128, because its two scales hold for that block alone.  In KIND_WG the scale
-// varies along the contraction, so four converter warps turn codes into
-// scaled 16-bit operands on their way from shared memory to the MMA (exact
-// for power-of-two scales: a code has at most 4 significant bits), and a chunk
-// is WG_CHUNK stages long, which bounds the length of the sums that the tensor
+// varies along the contraction, so eight more warps turn codes into scaled
+// 16-bit operands on their way from shared memory to the MMA (exact for
+// power-of-two scales: a code has at most 4 significant bits), and a chunk is
+// WG_CHUNK stages long, which bounds the length of the sums that the tensor
 // cores keep by themselves.
 //
 // CTA layout, one CTA per SM:
-//   warp 0       TMA producer (lane 0)
+//   warp 0       TMA producer (lane 0); KIND_WG: of the codes
 //   warp 1       MMA issuer (lane 0); owns tensor memory
-//   warps 2, 3   none: they make the first warpgroup whole, which gives its
+//   warp 2       KIND_WG: TMA producer of dY (lane 0)
+//   warp 3       none: it makes the first warpgroup whole, which gives its
 //                registers to the promotion warps
 //   warps 4-11   promotion and epilogue: quadrant warp % 4 of the accumulator's
 //                rows, column half (warp - 4) / 4
-//   warps 12-15  KIND_WG: converters
+//   warps 12-19  KIND_WG: converters
 // CG = 2: a cluster of two CTAs computes a 256 x 256 tile with
 // tcgen05.mma.cta_group::2, each staging its 128 rows of A and 128 columns of
 // B; the even CTA issues the MMAs.  CG = 1: 128 x 128 tiles, for few rows.
@@ -52,13 +53,14 @@ constexpr int DEV_TIMEOUT = 1;
 enum : int {
     WAIT_EMPTY = 101,
     WAIT_FULL = 102,
-    WAIT_CONVERTED = 103,
+    WAIT_FULL_B = 103,
     WAIT_ACC_EMPTY = 104,
     WAIT_ACC_FULL = 105,
     WAIT_RAW = 106,
     WAIT_SYNC = 107,
     WAIT_DRAIN_TMA = 108,
     WAIT_DRAIN_MMA = 109,
+    WAIT_A_EMPTY = 110,
 };
 
 // The library's workspace header (same layout for every op).
@@ -83,6 +85,7 @@ struct GemmParams {
     int stages_total, part_stages, split;  // contraction in stages; stages per part; parts
     int m_blocks, n_blocks, group_m, n_units;
     int b_mn;         // MM: B has its columns contiguous
+    int b_chunked;    // WG: tmB is {64, m, n / 64}, one box per stage
     int a_box;        // MM: rows of A that a stage loads
     uint32_t idesc;
     const float* sa;  // MM: scales of A (row, K block); WG: scales of X (m, K block)
@@ -169,36 +172,48 @@ struct Geo {
     static constexpr uint32_t A_BYTES = BM * 128;      // 128 rows x 128 bytes of contraction
     static constexpr uint32_t B_BYTES = (BN / CG) * 128;
     static constexpr uint32_t RAW_BYTES = KIND == KIND_WG ? 64 * 128 : 0;
-    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + RAW_BYTES;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + (KIND == KIND_MM ? B_BYTES : 0);
+    // KIND_MM: a stage is one A and one B box.  KIND_WG: codes, converted A
+    // and B have rings of their own (RAWS, STAGES, BS slots), because each is
+    // held over another part of the way: load to conversion, conversion to
+    // MMA, load to MMA.
     static constexpr int STAGES = KIND == KIND_MM ? 6 : 4;
-    static constexpr int THREADS = KIND == KIND_MM ? 384 : 512;
+    static constexpr int RAWS = KIND == KIND_MM ? 0 : 6;
+    static constexpr int BS = KIND == KIND_MM ? 0 : 5;
+    static constexpr int THREADS = KIND == KIND_MM ? 384 : 640;
     static constexpr uint32_t OUT_BYTES = 32 * 128;    // staging per promotion warp
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int NUM_BARS = 4 * STAGES + 4 + 2;
-    static constexpr uint32_t BYTES = 1024 + STAGES * STAGE_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
-    // registers: the launch's total (168 or 128 a thread) is shared out anew
-    static constexpr int REGS_CTL = KIND == KIND_MM ? 56 : 40;
-    static constexpr int REGS_CONV = 96;
-    static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 224 : 184;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * RAWS + 2 * BS + 4 + 2;
+    static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES + BS * B_BYTES + RAWS * RAW_BYTES;
+    static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
+    // registers: the launch's total (168 or 96 a thread) is shared out anew
+    static constexpr int REGS_CTL = KIND == KIND_MM ? 56 : 48;
+    static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 224 : 160;
+    static constexpr int REGS_CONVERT = KIND == KIND_MM ? 0 : 56;
+    static constexpr int REGS_TOTAL = 128 * REGS_CTL + 256 * (REGS_PROMOTE + REGS_CONVERT);
 };
-static_assert(128 * Geo<KIND_MM, 2>::REGS_CTL + 256 * Geo<KIND_MM, 2>::REGS_PROMOTE <= 384 * 168, "register split");
-static_assert(128 * (Geo<KIND_WG, 2>::REGS_CTL + Geo<KIND_WG, 2>::REGS_CONV) + 256 * Geo<KIND_WG, 2>::REGS_PROMOTE <= 512 * 128,
-              "register split");
+static_assert(Geo<KIND_MM, 2>::REGS_TOTAL <= 384 * 168 && Geo<KIND_WG, 2>::REGS_TOTAL <= 640 * 96, "register split");
 
 template <int KIND, int CG>
 struct Smem {
     using G = Geo<KIND, CG>;
-    uint8_t *tiles, *out;
-    uint64_t *full, *empty, *raw, *conv, *acc_full, *acc_empty, *sync, *final_bar;
+    uint8_t *tiles, *b_tiles, *raw_tiles, *out;
+    // KIND_MM: full / empty per stage.  KIND_WG: full / empty of the converted
+    // A (converters -> MMA), raw_full / raw_empty, b_full / b_empty
+    uint64_t *full, *empty, *raw_full, *raw_empty, *b_full, *b_empty, *acc_full, *acc_empty, *sync, *final_bar;
     uint32_t *tmem_slot, *epoch_slot, *last;
     __device__ void carve(uint8_t* p) {
         tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
-        out = tiles + G::STAGES * G::STAGE_BYTES;
+        b_tiles = tiles + G::STAGES * G::STAGE_BYTES;
+        raw_tiles = b_tiles + G::BS * G::B_BYTES;
+        out = tiles + G::TILES_BYTES;
         full = reinterpret_cast<uint64_t*>(out + 8 * G::OUT_BYTES);
         empty = full + G::STAGES;
-        raw = empty + G::STAGES;
-        conv = raw + G::STAGES;
-        acc_full = conv + G::STAGES;
+        raw_full = empty + G::STAGES;
+        raw_empty = raw_full + G::RAWS;
+        b_full = raw_empty + G::RAWS;
+        b_empty = b_full + G::BS;
+        acc_full = b_empty + G::BS;
         acc_empty = acc_full + 2;
         sync = acc_empty + 2;
         final_bar = sync + 1;
@@ -207,8 +222,36 @@ struct Smem {
         last = tmem_slot + 2;
     }
     __device__ uint8_t* a(uint32_t s) const { return tiles + s * G::STAGE_BYTES; }
-    __device__ uint8_t* b(uint32_t s) const { return tiles + s * G::STAGE_BYTES + G::A_BYTES; }
-    __device__ uint8_t* raw_tile(uint32_t s) const { return tiles + s * G::STAGE_BYTES + G::A_BYTES + G::B_BYTES; }
+    __device__ uint8_t* b(uint32_t s) const {
+        return KIND == KIND_MM ? tiles + s * G::STAGE_BYTES + G::A_BYTES : b_tiles + s * G::B_BYTES;
+    }
+    __device__ uint8_t* raw(uint32_t s) const { return raw_tiles + s * G::RAW_BYTES; }
+};
+
+// Position in a ring of N slots.
+template <int N>
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+// A producer's record of its fills: bit s of `filled` is the phase of slot s's
+// last one.
+struct Fills {
+    uint32_t used = 0, filled = 0;
+    __device__ __forceinline__ void add(uint32_t slot, uint32_t phase) {
+        filled = (filled & ~(1u << slot)) | phase << slot;
+        used |= 1u << slot;
+    }
+    // every load has landed before the CTA leaves
+    __device__ __forceinline__ void drain(const Ctl& ctl, uint64_t* bars, int n) const {
+        for (int s = 0; s < n; ++s)
+            if ((used & (1u << s)) && !drain_bar(ctl, &bars[s], filled >> s & 1u, WAIT_DRAIN_TMA)) return;
+    }
 };
 
 struct Unit {
@@ -230,102 +273,141 @@ __device__ __forceinline__ Unit unit_of(const GemmParams& p, int u) {
     return x;
 }
 
+// Loads.  KIND_MM: `which` 0 streams A and B.  KIND_WG: 0 streams the codes, 1
+// streams dY.  The odd CTA's pair loads count on the even CTA's barrier, so to
+// know that they have landed it waits until the MMA has read its last fill.
 template <int KIND, int CG>
-__device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, int first, int step) {
+__device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, int which, int first, int step) {
     using G = Geo<KIND, CG>;
-    // bit s of `filled`: the phase of stage s's last fill
-    uint32_t stage = 0, phase = 0, used = 0, filled = 0;
-    bool ok = true;
-    for (int u = first; u < p.n_units && ok; u += step) {
-        const Unit x = unit_of(p, u);
-        const int row = (x.mb * CG + ctl.half) * BM;
-        const int col = x.nb * G::BN + ctl.half * (G::BN / CG);
-        for (int s = x.lo; s < x.hi; ++s) {
-            if (!wait_bar(ctl, &sm.empty[stage], phase ^ 1, WAIT_EMPTY)) {
-                ok = false;
-                break;
-            }
-            const int d = s * G::DEPTH;
-            if constexpr (KIND == KIND_MM) {
-                const uint32_t bytes = p.a_box * 128 + G::B_BYTES;
+    if constexpr (KIND == KIND_MM) {
+        Ring<G::STAGES> st;
+        Fills fills;
+        const uint32_t bytes = p.a_box * 128 + G::B_BYTES;
+        bool ok = true;
+        for (int u = first; u < p.n_units && ok; u += step) {
+            const Unit x = unit_of(p, u);
+            const int row = (x.mb * CG + ctl.half) * BM;
+            const int col = x.nb * G::BN + ctl.half * (G::BN / CG);
+            for (int s = x.lo; s < x.hi; ++s) {
+                if (!wait_bar(ctl, &sm.empty[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                const int d = s * G::DEPTH;
                 const int bc0 = p.b_mn ? col : d, bc1 = p.b_mn ? d : col;
                 if (CG == 1) {
-                    mbar_arrive_expect_tx(&sm.full[stage], bytes);
-                    tma_load_2d(sm.a(stage), &p.tmA, d, row, &sm.full[stage]);
-                    tma_load_2d(sm.b(stage), &p.tmB, bc0, bc1, &sm.full[stage]);
+                    mbar_arrive_expect_tx(&sm.full[st.slot], bytes);
+                    tma_load_2d(sm.a(st.slot), &p.tmA, d, row, &sm.full[st.slot]);
+                    tma_load_2d(sm.b(st.slot), &p.tmB, bc0, bc1, &sm.full[st.slot]);
                 } else {
-                    if (ctl.half == 0) mbar_arrive_expect_tx(&sm.full[stage], CG * bytes);
-                    const uint32_t fb = mapa_shared(&sm.full[stage], 0);
-                    tma_load_2d_pair(sm.a(stage), &p.tmA, d, row, fb);
-                    tma_load_2d_pair(sm.b(stage), &p.tmB, bc0, bc1, fb);
+                    if (ctl.half == 0) mbar_arrive_expect_tx(&sm.full[st.slot], CG * bytes);
+                    const uint32_t fb = mapa_shared(&sm.full[st.slot], 0);
+                    tma_load_2d_pair(sm.a(st.slot), &p.tmA, d, row, fb);
+                    tma_load_2d_pair(sm.b(st.slot), &p.tmB, bc0, bc1, fb);
                 }
-            } else {
-                mbar_arrive_expect_tx(&sm.raw[stage], G::RAW_BYTES);
-                tma_load_2d(sm.raw_tile(stage), &p.tmA, row, d, &sm.raw[stage]);
-                if (CG == 1) {
-                    mbar_arrive_expect_tx(&sm.full[stage], G::B_BYTES);
-                    for (int c = 0; c < G::BN / CG / 64; ++c)
-                        tma_load_2d(sm.b(stage) + c * 8192, &p.tmB, col + c * 64, d, &sm.full[stage]);
-                } else {
-                    if (ctl.half == 0) mbar_arrive_expect_tx(&sm.full[stage], CG * G::B_BYTES);
-                    const uint32_t fb = mapa_shared(&sm.full[stage], 0);
-                    for (int c = 0; c < G::BN / CG / 64; ++c)
-                        tma_load_2d_pair(sm.b(stage) + c * 8192, &p.tmB, col + c * 64, d, fb);
-                }
-            }
-            filled = (filled & ~(1u << stage)) | phase << stage;
-            used |= 1u << stage;
-            if (++stage == G::STAGES) {
-                stage = 0;
-                phase ^= 1;
+                fills.add(st.slot, st.phase);
+                st.next();
             }
         }
+        fills.drain(ctl, ctl.half ? sm.empty : sm.full, G::STAGES);
+    } else if (which == 0) {
+        Ring<G::RAWS> st;
+        Fills fills;
+        bool ok = true;
+        for (int u = first; u < p.n_units && ok; u += step) {
+            const Unit x = unit_of(p, u);
+            const int row = (x.mb * CG + ctl.half) * BM;
+            for (int s = x.lo; s < x.hi; ++s) {
+                if (!wait_bar(ctl, &sm.raw_empty[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(&sm.raw_full[st.slot], G::RAW_BYTES);
+                tma_load_2d(sm.raw(st.slot), &p.tmA, row, s * G::DEPTH, &sm.raw_full[st.slot]);
+                fills.add(st.slot, st.phase);
+                st.next();
+            }
+        }
+        fills.drain(ctl, sm.raw_full, G::RAWS);
+    } else {
+        Ring<G::BS> st;
+        Fills fills;
+        bool ok = true;
+        for (int u = first; u < p.n_units && ok; u += step) {
+            const Unit x = unit_of(p, u);
+            const int col = x.nb * G::BN + ctl.half * (G::BN / CG);
+            for (int s = x.lo; s < x.hi; ++s) {
+                if (!wait_bar(ctl, &sm.b_empty[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                const int d = s * G::DEPTH;
+                if (ctl.half == 0) mbar_arrive_expect_tx(&sm.b_full[st.slot], CG * G::B_BYTES);
+                const uint32_t fb = CG == 2 ? mapa_shared(&sm.b_full[st.slot], 0) : 0u;
+                if (p.b_chunked) {
+                    if (CG == 1)
+                        tma_load_3d(sm.b(st.slot), &p.tmB, 0, d, col / 64, &sm.b_full[st.slot]);
+                    else
+                        tma_load_3d_pair(sm.b(st.slot), &p.tmB, 0, d, col / 64, fb);
+                } else
+                for (int c = 0; c < G::BN / CG / 64; ++c) {
+                    if (CG == 1)
+                        tma_load_2d(sm.b(st.slot) + c * 8192, &p.tmB, col + c * 64, d, &sm.b_full[st.slot]);
+                    else
+                        tma_load_2d_pair(sm.b(st.slot) + c * 8192, &p.tmB, col + c * 64, d, fb);
+                }
+                fills.add(st.slot, st.phase);
+                st.next();
+            }
+        }
+        fills.drain(ctl, ctl.half ? sm.b_empty : sm.b_full, G::BS);
     }
-    // every load has landed before the CTA leaves.  The odd CTA's loads count
-    // on the even CTA's barrier: it waits until the MMA has read its last fill.
-    bool left = true;
-    for (int s = 0; s < G::STAGES; ++s)
-        if ((used & (1u << s)) && left) {
-            const uint32_t ph = filled >> s & 1u;
-            left = drain_bar(ctl, ctl.half ? &sm.empty[s] : &sm.full[s], ph, WAIT_DRAIN_TMA);
-            if (KIND == KIND_WG) left = left && drain_bar(ctl, &sm.raw[s], ph, WAIT_DRAIN_TMA);
-        }
+}
+
+// arrive on this barrier (of both CTAs of a pair) when the MMAs so far are done
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if (CG == 2)
+        umma_commit_pair_both(bar);
+    else
+        umma_commit<1>(bar);
 }
 
 template <int KIND, int CG>
 __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, uint32_t tmem, int first, int step) {
     using G = Geo<KIND, CG>;
     constexpr int CH = KIND == KIND_MM ? 1 : WG_CHUNK;
-    // per MMA step of K = 32 codes or 16 elements, in descriptor units of 16
-    // bytes: 32 bytes along a K-major swizzled row, else 32 or 16 rows of 128
+    // Descriptors.  K-major (A and B^T of KIND_MM): 8-row groups 1024 bytes
+    // apart (stride offset), K steps of 32 codes 32 bytes further along the
+    // swizzled rows.  MN-major: rows of 128 bytes per contraction index, 8-deep
+    // groups 1024 bytes apart (stride offset), K steps of 32 or 16 rows;
+    // KIND_WG's two 64-element columns are 8192 bytes apart (leading offset).
     const uint64_t a_adv = KIND == KIND_MM ? 2 : 128;
     const uint64_t b_adv = KIND == KIND_MM ? (p.b_mn ? 256 : 2) : 128;
-    uint32_t stage = 0, phase = 0, chunk = 0;
+    const uint32_t lead = KIND == KIND_MM ? 16 : 8192;
+    Ring<G::STAGES> st;
+    Ring<KIND == KIND_WG ? G::BS : 1> bst;
+    uint32_t chunk = 0;
     bool ok = true;
     for (int u = first; u < p.n_units && ok; u += step) {
         const Unit x = unit_of(p, u);
         for (int s0 = x.lo; s0 < x.hi && ok; s0 += CH, ++chunk) {
             const uint32_t buf = chunk & 1, use = chunk >> 1;
-            if (!wait_bar(ctl, &sm.acc_empty[buf], (use & 1) ^ 1, WAIT_ACC_EMPTY)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem + buf * G::BN;
             const int end = min(x.hi, s0 + CH);
-            for (int s = s0; s < end; ++s) {
-                if (!wait_bar(ctl, &sm.full[stage], phase, WAIT_FULL) ||
-                    (KIND == KIND_WG && !wait_bar(ctl, &sm.conv[stage], phase, WAIT_CONVERTED))) {
+            for (int s = s0; s < end && ok; ++s) {
+                if (!wait_bar(ctl, &sm.full[st.slot], st.phase, WAIT_FULL) ||
+                    (KIND == KIND_WG && !wait_bar(ctl, &sm.b_full[bst.slot], bst.phase, WAIT_FULL_B))) {
+                    ok = false;
+                    break;
+                }
+                const uint64_t ad = smem_desc(smem_u32(sm.a(st.slot)), lead, 1024);
+                const uint64_t bd = smem_desc(smem_u32(sm.b(KIND == KIND_MM ? st.slot : bst.slot)), lead, 1024);
+                if (s == s0 && !wait_bar(ctl, &sm.acc_empty[buf], (use & 1) ^ 1, WAIT_ACC_EMPTY)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                // K-major: 8-row groups 1024 bytes apart (stride offset).
-                // MN-major: 128-byte columns of 8-deep groups 1024 bytes
-                // apart (stride offset); KIND_WG's two 64-element columns
-                // 8192 bytes apart (leading offset).
-                const uint64_t ad = smem_desc(smem_u32(sm.a(stage)), KIND == KIND_MM ? 16 : 8192, 1024);
-                const uint64_t bd = smem_desc(smem_u32(sm.b(stage)), KIND == KIND_MM ? 16 : 8192, 1024);
+                const uint32_t d = tmem + buf * G::BN;
 #pragma unroll
                 for (int k = 0; k < G::UMMA_STEPS; ++k) {
                     const uint32_t acc = (s > s0 || k > 0) ? 1u : 0u;
@@ -334,21 +416,14 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
                     else
                         umma_f16<CG>(d, ad + k * a_adv, bd + k * b_adv, p.idesc, acc);
                 }
-                if (CG == 2)
-                    umma_commit_pair_both(&sm.empty[stage]);
-                else
-                    umma_commit<1>(&sm.empty[stage]);
-                if (++stage == G::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                if (s == end - 1 && p.debug_skip != static_cast<uint32_t>(u) + 1) commit<CG>(&sm.acc_full[buf]);
+                commit<CG>(&sm.empty[st.slot]);
+                st.next();
+                if (KIND == KIND_WG) {
+                    commit<CG>(&sm.b_empty[bst.slot]);
+                    bst.next();
                 }
             }
-            if (!ok) break;
-            if (p.debug_skip == static_cast<uint32_t>(u) + 1) continue;
-            if (CG == 2)
-                umma_commit_pair_both(&sm.acc_full[buf]);
-            else
-                umma_commit<1>(&sm.acc_full[buf]);
         }
     }
     umma_commit<CG>(sm.final_bar);
@@ -363,118 +438,18 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// bytes that are infinity or NaN, as a nonzero word (add: 4 or 1 in each byte)
-__device__ __forceinline__ uint32_t special_codes(uint32_t w, uint32_t add) {
-    return ((w & 0x7F7F7F7Fu) + add) & 0x80808080u;
-}
-// a power of two small enough for 2^120 times it to be a bf16 number, or zero
-__device__ __forceinline__ bool simple_scale(float s) {
-    return (__float_as_uint(s) & 0x7FFFFFu) == 0u && s <= 128.f;
-}
-// Converters: 64 x 128 codes of a stage -> 16-bit values times their row's
-// scale, in the MN-major swizzled layout (two columns of 64 k, rows of 128
-// bytes, 16-byte units XORed with the row).  A thread takes 16 codes of four
-// rows; threads of the second column write their two units in the other
-// order, so eight threads of a row touch all banks once.  The product is
-// rounded once to the 16-bit type; a power-of-two scale makes it exact.
-// bf16 with power-of-two scales, the usual case, needs no conversion
-// instructions: a code's exponent and mantissa bits set into a bf16 number
-// give its value times 2^-120 (e5m2: 2^-112), subnormal codes included, and
-// one packed multiplication by scale * 2^120 is exact.  NaN and infinity do
-// not follow that rule; a thread that meets one converts its codes one by one.
-template <int CG>
-__device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, int t, int first, int step) {
-    using G = Geo<KIND_WG, CG>;
-    uint32_t stage = 0, phase = 0;
-    const int seg = t & 7, row0 = t >> 3, col = seg >> 2;
-    const int e5m2 = p.codes_e5m2;
-    const uint32_t add = e5m2 ? 0x04040404u : 0x01010101u, mask = e5m2 ? 0x0FE00FE0u : 0x07F007F0u;
-    const int shift = e5m2 ? 3 : 4;
-    const float widen = __int_as_float((127 + (e5m2 ? 112 : 120)) << 23);
-    for (int u = first; u < p.n_units; u += step) {
-        const Unit x = unit_of(p, u);
-        // this CTA's 128 output rows are one block of scales
-        const int kblk = x.mb * CG + ctl.half;
-        const bool live = kblk * BM < p.M;
-        const float* sx = p.sa + kblk * p.sa_cs;
-        float next[4];
-        auto fetch = [&](int s) {
+// 16 codes -> 16 scaled 16-bit values.  Codes go to f16 pairs (exact) and
+// through fp32, times the scale, to the 16-bit type: one rounding, none for a
+// power-of-two scale.  (Setting a code's bits into a bf16 number and scaling
+// pairs of those takes as many instructions, all of them half rate.)
+template <bool BF16, bool E5M2>
+__device__ __forceinline__ void convert16(const uint4& c, float scale, uint32_t (&o)[8]) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int m = s * G::DEPTH + row0 + 16 * i;
-                next[i] = (live && m < p.D) ? __ldg(sx + m * p.sa_rs) : 0.f;
-            }
-        };
-        fetch(x.lo);
-        for (int s = x.lo; s < x.hi; ++s) {
-            float sc[4];
-            bool simple = true;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[i] = next[i];
-                simple = simple && simple_scale(sc[i]);
-            }
-            if (s + 1 < x.hi) fetch(s + 1);
-            if (!wait_bar(ctl, &sm.raw[stage], phase, WAIT_RAW)) return;
-            const uint8_t* src = sm.raw_tile(stage);
-            uint8_t* dst = sm.a(stage) + col * 8192;
-            uint4 c4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c4[i] = *reinterpret_cast<const uint4*>(src + (row0 + 16 * i) * 128 + seg * 16);
-            uint32_t special = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                special |= special_codes(c4[i].x, add) | special_codes(c4[i].y, add) | special_codes(c4[i].z, add) |
-                           special_codes(c4[i].w, add);
-            const bool fast = p.x_bf16 && simple && !special;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = row0 + 16 * i;
-                const uint32_t w[4] = {c4[i].x, c4[i].y, c4[i].z, c4[i].w};
-                uint32_t o[8];
-                if (fast) {
-                    const __nv_bfloat162 f = __float2bfloat162_rn(sc[i] * widen);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t v = __byte_perm(w[j / 2], 0u, (j & 1) ? 0x3424u : 0x1404u);  // codes in bytes 1 and 3
-                        const uint32_t b = (v & 0x80008000u) | ((v >> shift) & mask);
-                        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&y);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t h = cvt_f8x2_f16x2(w[j / 2] >> (16 * (j & 1)), p.codes_e5m2);
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                        o[j] = pack16(f.x * sc[i], f.y * sc[i], p.x_bf16);
-                    }
-                }
-                const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
-                const int j0 = (seg & 3) * 2;
-                uint8_t* line = dst + r * 128;
-                uint4* u0 = reinterpret_cast<uint4*>(line + ((j0 ^ (r & 7)) << 4));
-                uint4* u1 = reinterpret_cast<uint4*>(line + (((j0 + 1) ^ (r & 7)) << 4));
-                if (col) {
-                    *u1 = v1;
-                    *u0 = v0;
-                } else {
-                    *u0 = v0;
-                    *u1 = v1;
-                }
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if ((t & 31) == 0) {
-                if (CG == 2)
-                    mbar_arrive_remote(mapa_shared(&sm.conv[stage], 0));
-                else
-                    mbar_arrive(&sm.conv[stage]);
-            }
-            if (++stage == G::STAGES) {
-                stage = 0;
-                phase ^= 1;
-            }
-        }
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t h = cvt_f8x2_f16x2(w[j / 2] >> (16 * (j & 1)), E5M2);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        o[j] = pack16(f.x * scale, f.y * scale, BF16);
     }
 }
 
@@ -493,67 +468,61 @@ __device__ __forceinline__ void store_out(const GemmParams& p, long long row, lo
         static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(v);
 }
 
-// Promotion and epilogue of every unit; false = a wait gave up.
+// A promotion warp: sums and epilogue of its 32 rows x COLS columns of each
+// tile, kept in fp32 registers.
 template <int KIND, int CG>
-__device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, uint32_t tmem, int w, int lane,
-                            int first, int step) {
+struct Worker {
     using G = Geo<KIND, CG>;
-    constexpr int COLS = G::COLS, CH = KIND == KIND_MM ? 1 : WG_CHUNK;
-    const int q = w & 3, h = w >> 2;
+    static constexpr int COLS = G::COLS;
+    const GemmParams& p;
+    const Ctl& ctl;
+    Smem<KIND, CG>& sm;
+    const uint32_t tmem;
+    const int w, lane, q, h;
+    uint8_t* const stg;
     uint32_t chunk = 0, syncs = 0;
-    uint8_t* stg = sm.out + w * G::OUT_BYTES;
-    for (int u = first; u < p.n_units; u += step) {
-        const Unit x = unit_of(p, u);
-        const int blk = x.mb * CG + ctl.half;
-        const int row0 = blk * BM + q * 32, row = row0 + lane;
-        const int col0 = x.nb * G::BN + h * COLS;
-        // rows or columns outside the matrix: nothing to add up, in step with the others
-        const bool live = row0 < p.M && col0 < p.N;
-        unsigned long long acc[COLS / 2];
+    unsigned long long acc[COLS / 2];  // pairs of fp32 sums
+
+    __device__ __forceinline__ Worker(const GemmParams& p_, const Ctl& c_, Smem<KIND, CG>& s_, uint32_t t_, int w_, int lane_)
+        : p(p_), ctl(c_), sm(s_), tmem(t_), w(w_), lane(lane_), q(w_ & 3), h(w_ >> 2), stg(s_.out + w_ * G::OUT_BYTES) {
+        clear();
+    }
+    __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+    }
 
-        const float* sa = p.sa + static_cast<long long>(row) * p.sa_rs;
-        const float* sb = p.sb + (col0 / 128) * p.sb_cs;
-        // the two scales of a stage are fetched two stages ahead and
-        // multiplied where they are used, so that no load is waited for
-        struct Scales {
-            float a, b;
-        };
-        auto scales_of = [&](int s) {
-            Scales v{0.f, 0.f};
-            if (KIND == KIND_MM && live && s < x.hi) {
-                if (row < p.M) v.a = __ldg(sa + s * p.sa_cs);
-                v.b = __ldg(sb + s * p.sb_rs);
-            }
-            return v;
-        };
-        Scales s_cur = scales_of(x.lo), s_next = scales_of(x.lo + 1);
-        for (int s0 = x.lo; s0 < x.hi; s0 += CH, ++chunk) {
-            const uint32_t buf = chunk & 1;
-            const Scales s_after = scales_of(s0 + 2);
-            if (!wait_bar(ctl, &sm.acc_full[buf], (chunk >> 1) & 1, WAIT_ACC_FULL)) return false;
-            tc_fence_after();
-            if (live) {
-                const float sc = KIND == KIND_MM ? s_cur.a * s_cur.b : 1.f;
-                const unsigned long long sc2 = pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
-                const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::BN + h * COLS;
-                // KIND_MM promotes every stage: its next load runs under the
-                // sums.  KIND_WG promotes every WG_CHUNK stages and has fewer
-                // registers.
-                constexpr int NB = KIND == KIND_MM ? 2 : 1;
-                uint32_t r[NB][32];
-                tmem_ld_32x32b_x32(base, r[0]);
-#pragma unroll
-                for (int c = 0; c < COLS / 32; ++c) {
-                    tmem_wait_regs(r[c % NB]);
-                    if (NB == 2 && c + 1 < COLS / 32) tmem_ld_32x32b_x32(base + (c + 1) * 32, r[(c + 1) % NB]);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[c * 16 + i] = fma_f32x2(pack_f32x2(r[c % NB][2 * i], r[c % NB][2 * i + 1]), sc2, acc[c * 16 + i]);
-                    if (NB == 1 && c + 1 < COLS / 32) tmem_ld_32x32b_x32(base + (c + 1) * 32, r[0]);
-                }
-            }
+    // where this warp's part of a unit lies
+    struct Place {
+        int u;
+        Unit x;
+        int blk, row0;
+        bool live;  // some of its rows and columns exist; otherwise it only keeps step
+    };
+    __device__ __forceinline__ Place place(int u) const {
+        Place pl;
+        pl.u = u;
+        pl.x = unit_of(p, u);
+        pl.blk = pl.x.mb * CG + ctl.half;
+        pl.row0 = pl.blk * BM + q * 32;
+        pl.live = pl.row0 < p.M && col_of(pl, 0) < p.N;
+        return pl;
+    }
+    // first matrix column of the warp's c-th 32 columns
+    __device__ __forceinline__ int col_of(const Place& pl, int c) const {
+        return pl.x.nb * G::BN + h * COLS + c * 32;
+    }
+
+    // acc += the next chunk's product * scale.  Wide loads make few round
+    // trips to tensor memory; the buffer is handed back as soon as the last
+    // one has arrived.
+    template <int LD>
+    __device__ __forceinline__ bool promote(bool live, float scale) {
+        const uint32_t buf = chunk & 1;
+        if (!wait_bar(ctl, &sm.acc_full[buf], (chunk >> 1) & 1, WAIT_ACC_FULL)) return false;
+        ++chunk;
+        tc_fence_after();
+        auto release = [&]() {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -562,14 +531,32 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
                 else
                     mbar_arrive(&sm.acc_empty[buf]);
             }
-            s_cur = s_next;
-            s_next = s_after;
+        };
+        if (live) {
+            const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::BN + h * COLS;
+            const uint32_t f = __float_as_uint(scale);
+            const unsigned long long f2 = pack_f32x2(f, f);
+            uint32_t r[LD];
+#pragma unroll
+            for (int c = 0; c < COLS / LD; ++c) {
+                tmem_ld_cols(base + c * LD, r);
+                tmem_wait_regs(r);
+                if (c == COLS / LD - 1) release();
+#pragma unroll
+                for (int i = 0; i < LD / 2; ++i)
+                    acc[c * (LD / 2) + i] = fma_f32x2(pack_f32x2(r[2 * i], r[2 * i + 1]), f2, acc[c * (LD / 2) + i]);
+            }
+        } else {
+            release();
         }
+        return true;
+    }
 
+    __device__ __forceinline__ bool epilogue(const Place& pl) {
         // epilogue: 32 rows x 128 bytes at a time through swizzled staging and
         // a tensor store, which clips the ragged edges.  Whole sums are
         // rounded here, once; parts stay fp32.
-        if (live) {
+        if (pl.live) {
             const bool wide = p.staged || p.out_type == T_F32;
             const bool add_bias = KIND == KIND_MM && p.bias != nullptr && !p.staged;
 #pragma unroll
@@ -578,7 +565,7 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
 #pragma unroll
                 for (int i = 0; i < 16; ++i) unpack_f32x2(acc[c * 16 + i], v[2 * i], v[2 * i + 1]);
                 if (add_bias) {
-                    const float b = load_bias(p, col0 + c * 32 + lane);
+                    const float b = load_bias(p, col_of(pl, c) + lane);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
                 }
@@ -603,8 +590,8 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        const int cc = col0 + (wide ? c : c - 1) * 32;
-                        if (cc < p.N) tma_store_3d(&p.tmC, stg, cc, row0, p.staged ? x.part : 0);
+                        const int cc = col_of(pl, wide ? c : c - 1);
+                        if (cc < p.N) tma_store_3d(&p.tmC, stg, cc, pl.row0, p.staged ? pl.x.part : 0);
                         bulk_commit();
                     }
                 }
@@ -632,17 +619,17 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
                 bool last = true;
                 __threadfence();
                 if (p.split > 1)
-                    last = arrive_count(p.arrived + (u / p.split) * CG + ctl.half, ctl.epoch) == static_cast<uint32_t>(p.split);
+                    last = arrive_count(p.arrived + (pl.u / p.split) * CG + ctl.half, ctl.epoch) == static_cast<uint32_t>(p.split);
                 __threadfence();
                 *reinterpret_cast<volatile uint32_t*>(sm.last) = last ? 1u : 0u;
             }
             if (!sync()) return false;
             if (*reinterpret_cast<volatile uint32_t*>(sm.last)) {
                 __threadfence();
-                const int rows = min(BM, p.M - blk * BM), tile_c = x.nb * G::BN;
+                const int rows = min(BM, p.M - pl.blk * BM), tile_c = pl.x.nb * G::BN;
                 const int quads = (min(G::BN, p.N - tile_c) + 3) / 4;
                 for (int i = w * 32 + lane; i < rows * quads; i += 256) {
-                    const int r = blk * BM + i / quads, c = tile_c + (i % quads) * 4;
+                    const int r = pl.blk * BM + i / quads, c = tile_c + (i % quads) * 4;
                     const float* src = p.partial + static_cast<long long>(r) * p.part_rs + c;
                     float4 sum = __ldcg(reinterpret_cast<const float4*>(src));
                     for (int k = 1; k < p.split; ++k) {
@@ -661,8 +648,125 @@ __device__ bool run_promote(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>&
             // the flag is read by all before the next unit may set it anew
             if (!sync()) return false;
         }
+        clear();
+        return true;
+    }
+};
+
+// Promotion warps; false = a wait gave up.
+template <int CG>
+__device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM, CG>& sm, uint32_t tmem, int w, int lane,
+                            int first, int step) {
+    Worker<KIND_MM, CG> wk(p, ctl, sm, tmem, w, lane);
+    for (int u = first; u < p.n_units; u += step) {
+        const auto pl = wk.place(u);
+        const int row = pl.row0 + lane;
+        const float* sa = p.sa + static_cast<long long>(row) * p.sa_rs;
+        const float* sb = p.sb + (wk.col_of(pl, 0) / 128) * p.sb_cs;
+        // a stage's scales are fetched two stages ahead and multiplied where
+        // they are used, so that no load is waited for
+        struct Scales {
+            float a, b;
+        };
+        auto scales_of = [&](int s) {
+            Scales v{0.f, 0.f};
+            if (pl.live && s < pl.x.hi) {
+                if (row < p.M) v.a = __ldg(sa + s * p.sa_cs);
+                v.b = __ldg(sb + s * p.sb_rs);
+            }
+            return v;
+        };
+        Scales cur = scales_of(pl.x.lo), next = scales_of(pl.x.lo + 1);
+        for (int s = pl.x.lo; s < pl.x.hi; ++s) {
+            const Scales after = scales_of(s + 2);
+            if (!wk.template promote<64>(pl.live, cur.a * cur.b)) return false;
+            cur = next;
+            next = after;
+        }
+        if (!wk.epilogue(pl)) return false;
     }
     return true;
+}
+
+template <int CG>
+__device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, uint32_t tmem, int w, int lane,
+                               int first, int step) {
+    Worker<KIND_WG, CG> wk(p, ctl, sm, tmem, w, lane);
+    for (int u = first; u < p.n_units; u += step) {
+        const auto pl = wk.place(u);
+        for (int s = pl.x.lo; s < pl.x.hi; s += WG_CHUNK)
+            if (!wk.template promote<16>(pl.live, 1.f)) return false;
+        if (!wk.epilogue(pl)) return false;
+    }
+    return true;
+}
+
+// Conversion: 64 x 128 codes -> 16-bit values times their row's scale, in the
+// MN-major swizzled layout (two columns of 64 k, rows of 128 bytes, 16-byte
+// units XORed with the row).  Two groups of four warps take the stages in
+// turn, so one stage's latencies (barrier, shared memory, fence) pass under the
+// other's arithmetic.  A thread takes 16 codes of four rows; threads of the
+// second column write their two units in the other order, so eight threads of
+// a row touch all banks once.
+template <int CG, bool BF16, bool E5M2>
+__device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, int t, int first, int step) {
+    using G = Geo<KIND_WG, CG>;
+    Ring<G::RAWS> rs;
+    Ring<G::STAGES> st;
+    const int group = t >> 7, tt = t & 127;
+    const int seg = tt & 7, r0 = tt >> 3, col = seg >> 2, j0 = (seg & 3) * 2;
+    // offsets of the two units of row r0 in a slot; rows r0 + 16 i have the same XOR
+    const uint32_t u0 = col * 8192 + r0 * 128 + ((j0 ^ (r0 & 7)) << 4);
+    const uint32_t u1 = col * 8192 + r0 * 128 + (((j0 + 1) ^ (r0 & 7)) << 4);
+    int turn = 0;  // stages so far, over all units
+    for (int u = first; u < p.n_units; u += step) {
+        const Unit x = unit_of(p, u);
+        // this CTA's 128 output rows are one block of scales
+        const int kblk = x.mb * CG + ctl.half;
+        const bool live = kblk * BM < p.M;
+        const float* sx = p.sa + kblk * p.sa_cs;
+        // a stage's scales are fetched one turn (two stages) ahead
+        float next[4];
+        auto fetch = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = s * G::DEPTH + r0 + 16 * i;
+                next[i] = (live && s < x.hi && m < p.D) ? __ldg(sx + m * p.sa_rs) : 0.f;
+            }
+        };
+        fetch(x.lo + ((turn & 1) != group));
+        for (int s = x.lo; s < x.hi; ++s, ++turn, rs.next(), st.next()) {
+            if ((turn & 1) != group) continue;
+            float sc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[i] = next[i];
+            fetch(s + 2);
+            if (!wait_bar(ctl, &sm.raw_full[rs.slot], rs.phase, WAIT_RAW)) return;
+            if (!wait_bar(ctl, &sm.empty[st.slot], st.phase ^ 1, WAIT_A_EMPTY)) return;
+            const uint8_t* src = sm.raw(rs.slot) + r0 * 128 + seg * 16;
+            uint8_t* dst = sm.a(st.slot);
+            uint4 c4 = *reinterpret_cast<const uint4*>(src);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 c = c4;
+                if (i < 3) c4 = *reinterpret_cast<const uint4*>(src + (i + 1) * 2048);
+                uint32_t o[8];
+                convert16<BF16, E5M2>(c, sc[i], o);
+                const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4*>(dst + (col ? u1 : u0) + i * 2048) = col ? v1 : v0;
+                *reinterpret_cast<uint4*>(dst + (col ? u0 : u1) + i * 2048) = col ? v0 : v1;
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if ((t & 31) == 0) {
+                mbar_arrive(&sm.raw_empty[rs.slot]);
+                if (CG == 2)
+                    mbar_arrive_remote(mapa_shared(&sm.full[st.slot], 0));
+                else
+                    mbar_arrive(&sm.full[st.slot]);
+            }
+        }
+    }
 }
 
 template <int KIND, int CG>
@@ -675,10 +779,16 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
     const int half = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::STAGES; ++s) {
-            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.full[s], KIND == KIND_MM ? 1 : CG * 4);
             mbar_init(&sm.empty[s], 1);
-            mbar_init(&sm.raw[s], 1);
-            mbar_init(&sm.conv[s], CG * 4);
+        }
+        for (int s = 0; s < G::RAWS; ++s) {
+            mbar_init(&sm.raw_full[s], 1);
+            mbar_init(&sm.raw_empty[s], 4);
+        }
+        for (int s = 0; s < G::BS; ++s) {
+            mbar_init(&sm.b_full[s], 1);
+            mbar_init(&sm.b_empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.acc_full[b], 1);
@@ -705,19 +815,30 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
     if (warp < 4) {
         reg_dec<G::REGS_CTL>();
         if (warp == 0) {
-            if (lane == 0) run_tma<KIND, CG>(p, ctl, sm, first, step);
+            if (lane == 0) run_tma<KIND, CG>(p, ctl, sm, 0, first, step);
+        } else if (KIND == KIND_WG && warp == 2) {
+            if (lane == 0) run_tma<KIND, CG>(p, ctl, sm, 1, first, step);
         } else if (warp == 1) {
             if (lane == 0 && half == 0) run_mma<KIND, CG>(p, ctl, sm, tmem, first, step);
         }
         __syncwarp();
     } else if (warp < 12) {
         reg_inc<G::REGS_PROMOTE>();
-        run_promote<KIND, CG>(p, ctl, sm, tmem, warp - 4, lane, first, step);
+        if constexpr (KIND == KIND_MM)
+            run_promote_mm<CG>(p, ctl, sm, tmem, warp - 4, lane, first, step);
+        else
+            run_promote_wg<CG>(p, ctl, sm, tmem, warp - 4, lane, first, step);
         if (lane == 0) bulk_wait_all();  // its stores have left shared memory, stopped or not
         __syncwarp();
     } else if constexpr (KIND == KIND_WG) {
-        reg_dec<G::REGS_CONV>();
-        run_convert<CG>(p, ctl, sm, threadIdx.x - 384, first, step);
+        reg_dec<G::REGS_CONVERT>();
+        const int t = threadIdx.x - 384;
+        if (p.x_bf16)
+            p.codes_e5m2 ? run_convert<CG, true, true>(p, ctl, sm, t, first, step)
+                         : run_convert<CG, true, false>(p, ctl, sm, t, first, step);
+        else
+            p.codes_e5m2 ? run_convert<CG, false, true>(p, ctl, sm, t, first, step)
+                         : run_convert<CG, false, false>(p, ctl, sm, t, first, step);
         __syncwarp();
     }
 
