@@ -20,7 +20,6 @@ using namespace gct::fp8;
 namespace {
 
 constexpr size_t WS_HEADER = 256;
-constexpr size_t WS_FIXED = WS_HEADER + MAX_SPLIT_SLOTS * 8;
 constexpr unsigned long long DEFAULT_WAIT_NS = 2000000000ull;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -39,15 +38,35 @@ int cuda_fail(const char* what, int code) {
     return IRIS_ECUDA;
 }
 
-// per device: SMs, co-resident CTA pairs of each pair kernel (0 = not set up)
+// per device: SMs and how many clusters of a kernel run at once, by kind and
+// log2 of the cluster's CTAs (a pair for CG 2, the parts of a split for CG 1)
 struct DeviceInfo {
-    int sms, pairs_mm, pairs_wg;
+    int sms;
+    int pairs[2], clusters[2][4];
     bool done;
 };
 DeviceInfo g_dev[64];
 
+cudaLaunchConfig_t launch_config(int grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                                 cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t lc;
+    std::memset(&lc, 0, sizeof(lc));
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    if (cluster > 1) {
+        attr->id = cudaLaunchAttributeClusterDimension;
+        attr->val.clusterDim.x = cluster;
+        attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+    }
+    return lc;
+}
+
 template <int KIND, int CG>
-int setup_kernel(int sms, int* pairs) {
+int setup_kernel(DeviceInfo& d) {
     using G = Geo<KIND, CG>;
     cudaError_t e = cudaFuncSetAttribute(block_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(G::BYTES));
@@ -58,20 +77,17 @@ int setup_kernel(int sms, int* pairs) {
     e = cudaFuncGetAttributes(&fa, block_gemm_kernel<KIND, CG>);
     if (e != cudaSuccess) return cuda_fail("cudaFuncGetAttributes", static_cast<int>(e));
     if (fa.numRegs * G::THREADS < G::REGS_TOTAL) return cuda_fail("register shares of the 8-bit products", fa.numRegs);
-    if (pairs) {
+    for (int lg = 0; lg < 4; ++lg) {
+        if (CG == 2 && lg != 1) continue;
+        int* n = CG == 2 ? &d.pairs[KIND] : &d.clusters[KIND][lg];
+        if (lg == 0) {
+            *n = d.sms;
+            continue;
+        }
         cudaLaunchAttribute attr;
-        cudaLaunchConfig_t lc;
-        std::memset(&lc, 0, sizeof(lc));
-        lc.gridDim = dim3(sms - (sms & 1));
-        lc.blockDim = dim3(G::THREADS);
-        lc.dynamicSmemBytes = G::BYTES;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        lc.attrs = &attr;
-        lc.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(pairs, block_gemm_kernel<KIND, CG>, &lc);
-        if (e != cudaSuccess || *pairs < 1) return cuda_fail("cudaOccupancyMaxActiveClusters", static_cast<int>(e));
+        const cudaLaunchConfig_t lc = launch_config(d.sms >> lg << lg, G::THREADS, G::BYTES, 1 << lg, nullptr, &attr);
+        e = cudaOccupancyMaxActiveClusters(n, block_gemm_kernel<KIND, CG>, &lc);
+        if (e != cudaSuccess || *n < 1) return cuda_fail("cudaOccupancyMaxActiveClusters", static_cast<int>(e));
     }
     return IRIS_OK;
 }
@@ -84,10 +100,9 @@ int device_info(DeviceInfo* out) {
     if (!d.done) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return IRIS_ECUDA;
         int rc;
-        if ((rc = setup_kernel<KIND_MM, 1>(d.sms, nullptr))) return rc;
-        if ((rc = setup_kernel<KIND_MM, 2>(d.sms, &d.pairs_mm))) return rc;
-        if ((rc = setup_kernel<KIND_WG, 1>(d.sms, nullptr))) return rc;
-        if ((rc = setup_kernel<KIND_WG, 2>(d.sms, &d.pairs_wg))) return rc;
+        if ((rc = setup_kernel<KIND_MM, 1>(d)) || (rc = setup_kernel<KIND_MM, 2>(d)) || (rc = setup_kernel<KIND_WG, 1>(d)) ||
+            (rc = setup_kernel<KIND_WG, 2>(d)))
+            return rc;
         if (!g_encode) {
             void* fn = nullptr;
             cudaDriverEntryPointQueryResult q;
@@ -198,17 +213,16 @@ int make_map_groups(CUtensorMap* m, CUtensorMapDataType dt, const Operand& o, ui
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (groups of columns)", static_cast<int>(r));
 }
-// {n, row, part} with a box of 128 bytes x 32 rows
-int make_store_map(CUtensorMap* m, iris_dtype t, const void* data, int64_t N, int64_t M, int64_t parts, int64_t pitch,
-                   int64_t part_stride) {
+// out {n, row} with a box of 128 bytes x 32 rows
+int make_store_map(CUtensorMap* m, iris_dtype t, const void* data, int64_t N, int64_t M, int64_t pitch) {
     const int elem = dtype_size(t);
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(parts)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * elem, static_cast<cuuint64_t>(part_stride) * elem};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem), 32, 1}, es[3] = {1, 1, 1};
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * elem};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), 32}, es[2] = {1, 1};
     const CUtensorMapDataType dt = t == IRIS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : t == IRIS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const CUresult r = g_encode(m, dt, 3, const_cast<void*>(data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const CUresult r = g_encode(m, dt, 2, const_cast<void*>(data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit output)", static_cast<int>(r));
 }
@@ -216,74 +230,60 @@ int make_store_map(CUtensorMap* m, iris_dtype t, const void* data, int64_t N, in
 // Tile, split and workspace of one product (rows x cols over depth).
 struct Plan {
     int cg, split, part_stages, stages, m_blocks, n_blocks, group_m, grid;
-    bool staged;
-    int64_t part_pitch;
-    size_t copy_a, copy_b, partial, total;  // workspace offsets
+    size_t copy_a, copy_b, total;  // workspace offsets
 };
 
-// Estimated time in us of a variant.  Constants measured on GB300: a
-// launch, a stage of each tile kind with every SM running, an epilogue, and
-// the hand-over of split parts (their fp32 sums make one trip through L2).
-double estimate(bool wg, int cg, int slots, int64_t tiles, int64_t stages, int64_t split, double out_elems) {
-    const double stage = wg ? (cg == 2 ? 0.30 : 0.20) : (cg == 2 ? 0.33 : 0.22);
-    const int64_t part = cdiv(stages, split);
-    const int64_t waves = cdiv(tiles * split, slots);
-    double t = 4.0 + waves * (part * stage + (cg == 2 ? 1.0 : 0.7));
-    if (split > 1) t += 2.0 + out_elems * split * 8.0 / 4.0e6;
-    return t;
+// Estimated time in us of a variant: `slots` clusters run at once, each tile
+// takes `part` stages and an epilogue.  Constants measured on GB300.
+double estimate(bool wg, int cg, int slots, int64_t tiles, int64_t part, int split) {
+    const double stage = wg ? (cg == 2 ? 0.50 : 0.35) : (cg == 2 ? 0.52 : 0.35);
+    const double per_tile = part * stage + (cg == 2 ? 1.5 : 1.0) + (split > 1 ? 1.5 : 0.0);
+    return 4.0 + cdiv(tiles, slots) * per_tile;
 }
 
 int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& d, const Operand& a, const Operand& b,
-              bool direct_out, int64_t rows, int64_t cols, int64_t depth) {
+              int64_t rows, int64_t cols, int64_t depth) {
     iris_b200_config z;
     std::memset(&z, 0, sizeof(z));
     if (!cfg) cfg = &z;
     if (cfg->tile_m != 0 && cfg->tile_m != 128 && cfg->tile_m != 256) return IRIS_EINVAL;
-    if (cfg->k_split < 0 || cfg->k_split > 4096 || cfg->group_m < 0) return IRIS_EINVAL;
-    if (cfg->grid < 0 || cfg->grid > d.sms) return IRIS_EINVAL;
-    if (cfg->debug_skip_flag < 0) return IRIS_EINVAL;
-    if (cfg->tile_m == 256 && cfg->grid == 1) return IRIS_EINVAL;
+    if (cfg->k_split != 0 && cfg->k_split != 1 && cfg->k_split != 2 && cfg->k_split != 4 && cfg->k_split != 8) return IRIS_EINVAL;
+    if (cfg->tile_m == 256 && (cfg->k_split > 1 || cfg->grid == 1)) return IRIS_EINVAL;
+    if (cfg->group_m < 0 || cfg->debug_skip_flag < 0 || cfg->grid < 0 || cfg->grid > d.sms) return IRIS_EINVAL;
+    if (cfg->grid && cfg->k_split > cfg->grid) return IRIS_EINVAL;
     const int64_t stages = cdiv(depth, wg ? 64 : 128);
     const int grid = cfg->grid ? cfg->grid : d.sms;
-    const int pairs = std::min(wg ? d.pairs_wg : d.pairs_mm, grid / 2);
     double best = 0;
     pl.cg = 0;
     for (int cg = 1; cg <= 2; ++cg) {
         if (cfg->tile_m && cfg->tile_m != 128 * cg) continue;
-        const int slots = cg == 2 ? pairs : grid;
-        if (slots < 1) continue;
         const int64_t mb = cdiv(rows, 128 * cg), nb = cdiv(cols, 128 * cg), tiles = mb * nb;
-        // arrival counters are one per tile and CTA; parts beyond a few
-        // hundred MB would cost more than an idle SM
-        const int64_t most = tiles * cg > MAX_SPLIT_SLOTS ? 1
-                             : cfg->k_split ? std::min<int64_t>(cfg->k_split, stages)
-                                            : std::min<int64_t>({stages, 64, std::max<int64_t>(1, (64 << 20) / std::max<int64_t>(1, rows * cols))});
-        for (int64_t want = cfg->k_split ? most : 1; want <= most; ++want) {
-            const int64_t part = cdiv(stages, want), split = cdiv(stages, part);
-            if (!cfg->k_split && split != want) continue;
-            const double t = estimate(wg, cg, slots, tiles, stages, split, double(rows) * cols);
+        if (tiles > 0x7FFFFFFF) continue;
+        for (int lg = 0; lg < (cg == 2 ? 1 : 4); ++lg) {
+            const int split = 1 << lg;
+            const int64_t part = cdiv(stages, split);
+            const int slots = std::min(cg == 2 ? d.pairs[wg] : d.clusters[wg][lg], grid / (cg * split));
+            if (slots < 1) continue;
+            // every part has stages (an empty one, where the config asks for it, adds zeros)
+            if (cfg->k_split ? split != cfg->k_split : part * (split - 1) >= stages) continue;
+            const double t = estimate(wg, cg, slots, tiles, part, split);
             if (pl.cg == 0 || t < best) {
                 best = t;
                 pl.cg = cg;
-                pl.split = static_cast<int>(split);
+                pl.split = split;
                 pl.part_stages = static_cast<int>(part);
-                if (mb * nb * split > 0x7FFFFFFF) return IRIS_EINVAL;
                 pl.m_blocks = static_cast<int>(mb);
                 pl.n_blocks = static_cast<int>(nb);
+                pl.grid = static_cast<int>(std::min<int64_t>(tiles, slots)) * cg * split;
             }
         }
     }
     if (pl.cg == 0) return IRIS_EINVAL;
     pl.stages = static_cast<int>(stages);
     pl.group_m = cfg->group_m ? std::max(1, cfg->group_m / pl.cg) : 16 / pl.cg;
-    const int64_t units = int64_t(pl.m_blocks) * pl.n_blocks * pl.split;
-    pl.grid = static_cast<int>(std::min<int64_t>(units, pl.cg == 2 ? pairs : grid)) * pl.cg;
-    pl.staged = pl.split > 1 || !direct_out;
-    pl.part_pitch = packed_pitch(cols, 4);
-    pl.copy_a = WS_FIXED;
+    pl.copy_a = WS_HEADER;
     pl.copy_b = pl.copy_a + a.copy_bytes;
-    pl.partial = pl.copy_b + b.copy_bytes;
-    pl.total = pl.partial + (pl.staged ? round_up(size_t(pl.split) * rows * pl.part_pitch * 4, 256) : 0);
+    pl.total = pl.copy_b + b.copy_bytes;
     return IRIS_OK;
 }
 
@@ -291,19 +291,7 @@ template <int KIND, int CG>
 int launch_gemm(const GemmParams& p, int grid, cudaStream_t stream) {
     using G = Geo<KIND, CG>;
     cudaLaunchAttribute attr;
-    cudaLaunchConfig_t lc;
-    std::memset(&lc, 0, sizeof(lc));
-    lc.gridDim = dim3(grid);
-    lc.blockDim = dim3(G::THREADS);
-    lc.dynamicSmemBytes = G::BYTES;
-    lc.stream = stream;
-    if (CG == 2) {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        lc.attrs = &attr;
-        lc.numAttrs = 1;
-    }
+    const cudaLaunchConfig_t lc = launch_config(grid, G::THREADS, G::BYTES, CG * p.split, stream, &attr);
     const cudaError_t e = cudaLaunchKernelEx(&lc, block_gemm_kernel<KIND, CG>, p);
     return e == cudaSuccess ? IRIS_OK : cuda_fail("kernel launch (8-bit product)", static_cast<int>(e));
 }
@@ -317,7 +305,7 @@ int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b2
                 const iris_b200_config* cfg, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
     int rc;
     if (rows == 0 || cols == 0) {
-        if (need) *need = WS_FIXED;
+        if (need) *need = WS_HEADER;
         return IRIS_OK;
     }
     const int b_elem = wg ? 2 : 1;
@@ -328,7 +316,7 @@ int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b2
     DeviceInfo d;
     if ((rc = device_info(&d))) return rc;
     Plan pl;
-    if ((rc = make_plan(pl, wg, cfg, d, a, b, direct, rows, cols, std::max<int64_t>(depth, 1)))) return rc;
+    if ((rc = make_plan(pl, wg, cfg, d, a, b, rows, cols, std::max<int64_t>(depth, 1)))) return rc;
     if (need) {
         *need = pl.total;
         return IRIS_OK;
@@ -395,22 +383,14 @@ int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b2
     p.m_blocks = pl.m_blocks;
     p.n_blocks = pl.n_blocks;
     p.group_m = pl.group_m;
-    p.n_units = pl.m_blocks * pl.n_blocks * pl.split;
+    p.n_tiles = pl.m_blocks * pl.n_blocks;
     p.ws = reinterpret_cast<WsHeader*>(w);
-    p.arrived = reinterpret_cast<unsigned long long*>(w + WS_HEADER);
-    p.partial = reinterpret_cast<float*>(w + pl.partial);
-    p.part_rs = pl.part_pitch;
-    p.part_stride = rows * pl.part_pitch;
-    p.staged = pl.staged;
+    p.tma_out = direct;
     p.wait_ns = cfg && cfg->wait_ns ? cfg->wait_ns : DEFAULT_WAIT_NS;
     p.debug_skip = cfg ? static_cast<uint32_t>(cfg->debug_skip_flag) : 0u;
-    if (pl.staged)
-        rc = make_store_map(&p.tmC, IRIS_F32, p.partial, cols, rows, pl.split, pl.part_pitch, p.part_stride);
-    else
-        rc = make_store_map(&p.tmC, out_dtype, out->data, cols, rows, 1,
-                            rows == 1 ? packed_pitch(cols, dtype_size(out_dtype)) : out->row_stride,
-                            int64_t(packed_pitch(cols, dtype_size(out_dtype))));
-    if (rc) return rc;
+    if (direct && (rc = make_store_map(&p.tmC, out_dtype, out->data, cols, rows,
+                                       rows == 1 ? packed_pitch(cols, dtype_size(out_dtype)) : out->row_stride)))
+        return rc;
     if (wg) return pl.cg == 2 ? launch_gemm<KIND_WG, 2>(p, pl.grid, stream) : launch_gemm<KIND_WG, 1>(p, pl.grid, stream);
     return pl.cg == 2 ? launch_gemm<KIND_MM, 2>(p, pl.grid, stream) : launch_gemm<KIND_MM, 1>(p, pl.grid, stream);
 }

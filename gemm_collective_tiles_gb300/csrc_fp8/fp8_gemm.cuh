@@ -17,7 +17,7 @@
 //
 // CTA layout, one CTA per SM:
 //   warp 0       TMA producer (lane 0); KIND_WG: of the codes
-//   warp 1       MMA issuer (lane 0); owns tensor memory
+//   warp 1       MMA issuer; owns tensor memory
 //   warp 2       KIND_WG: TMA producer of dY (lane 0)
 //   warp 3       none: it makes the first warpgroup whole, which gives its
 //                registers to the promotion warps
@@ -28,11 +28,14 @@
 // tcgen05.mma.cta_group::2, each staging its 128 rows of A and 128 columns of
 // B; the even CTA issues the MMAs.  CG = 1: 128 x 128 tiles, for few rows.
 //
-// Work units (tile, part of the contraction) are dealt out in a fixed order;
-// with more than one part, the parts' fp32 sums go to the workspace and the
-// last CTA to arrive adds them in part order, so results do not depend on
-// timing.  Every wait is bounded: one that gives up records where in the
-// workspace header, stops the launch, and the roles drain and leave.
+// CG = 1 can split the contraction: a cluster of 2, 4 or 8 CTAs takes a tile,
+// each a part of its stages; the fp32 sums meet in shared memory, where each
+// CTA adds a slice of every warp's columns over all parts in part order, so
+// results do not depend on timing and nothing goes through global memory.
+//
+// Tiles are dealt out in a fixed order.  Every wait is bounded: one that gives
+// up records where in the workspace header, stops the launch, and the roles
+// drain and leave.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,7 +49,7 @@ namespace fp8 {
 enum : int { KIND_MM = 0, KIND_WG = 1 };
 constexpr int BM = 128;         // rows per CTA (tensor-memory lanes)
 constexpr int WG_CHUNK = 8;     // KIND_WG: 64-deep stages per chunk
-constexpr int MAX_SPLIT_SLOTS = 1024;  // (tile, CTA half) arrival counters in the workspace
+constexpr int MAX_SPLIT = 8;    // CTAs of a cluster that share a tile
 constexpr int DEV_TIMEOUT = 1;
 
 // where-codes recorded when a bounded wait gives up
@@ -57,7 +60,7 @@ enum : int {
     WAIT_ACC_EMPTY = 104,
     WAIT_ACC_FULL = 105,
     WAIT_RAW = 106,
-    WAIT_SYNC = 107,
+    WAIT_PARTS = 107,
     WAIT_DRAIN_TMA = 108,
     WAIT_DRAIN_MMA = 109,
     WAIT_A_EMPTY = 110,
@@ -79,11 +82,11 @@ static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 struct GemmParams {
     CUtensorMap tmA;  // MM: codes {k, row}, box {128, a_box}; WG: codes {k, m}, box {128, 64}, no swizzle
     CUtensorMap tmB;  // MM: codes {k, n} or {n, k}, box {128, 128}; WG: dY {n, m}, box {64, 64}
-    CUtensorMap tmC;  // out or the parts' sums: {n, row, part}, box {128 bytes, 32, 1}
+    CUtensorMap tmC;  // out {n, row}, box {128 bytes, 32}
     int M, N;         // output rows and columns
     int D;            // contraction length
     int stages_total, part_stages, split;  // contraction in stages; stages per part; parts
-    int m_blocks, n_blocks, group_m, n_units;
+    int m_blocks, n_blocks, group_m, n_tiles;
     int b_mn;         // MM: B has its columns contiguous
     int b_chunked;    // WG: tmB is {64, m, n / 64}, one box per stage
     int a_box;        // MM: rows of A that a stage loads
@@ -99,19 +102,16 @@ struct GemmParams {
     int out_type;
     long long out_rs, out_cs;
     WsHeader* ws;
-    unsigned long long* arrived;  // MAX_SPLIT_SLOTS epoch-tagged counters
-    float* partial;               // split parts: [part][row][pitch]
-    long long part_rs, part_stride;
-    int staged;                   // the epilogue stores parts (or one fp32 copy) to `partial`
+    int tma_out;                  // tensor stores can write the output
     unsigned long long wait_ns;
-    uint32_t debug_skip;          // test hook: k > 0: unit k - 1 never reports its accumulator
+    uint32_t debug_skip;          // test hook: k > 0: tile k - 1 never reports its accumulator
 };
 
 struct Ctl {
     WsHeader* ws;
     uint32_t epoch;
     unsigned long long limit;
-    int half;
+    int rank;  // in the cluster: the half of a pair's tile, or the part of the contraction
 };
 
 __device__ __forceinline__ bool launch_aborted(const Ctl& c) {
@@ -125,7 +125,8 @@ __device__ __forceinline__ void raise_timeout(const Ctl& c, int where, int index
     __threadfence();
     atomicExch(&c.ws->abort_epoch, c.epoch);
 }
-__device__ __forceinline__ bool wait_bar(const Ctl& c, uint64_t* bar, uint32_t parity, int where) {
+template <typename Bar>  // a barrier by pointer or by shared-memory address
+__device__ __forceinline__ bool wait_bar(const Ctl& c, Bar bar, uint32_t parity, int where) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
@@ -139,6 +140,12 @@ __device__ __forceinline__ bool wait_bar(const Ctl& c, uint64_t* bar, uint32_t p
         }
     }
 }
+// for barriers that other CTAs' promotion warps arrive on after writing shared
+// memory that this one reads
+__device__ __forceinline__ bool wait_bar_cluster(const Ctl& c, uint64_t* bar, uint32_t parity, int where) {
+    if (!wait_bar(c, bar, parity, where)) return false;
+    return mbar_try_wait_cluster(bar, parity);  // the phase is over: this only acquires at cluster scope
+}
 // teardown: waits for asynchronous work already issued, also while stopping
 __device__ __forceinline__ bool drain_bar(const Ctl& c, uint64_t* bar, uint32_t parity, int where) {
     const uint64_t t0 = global_timer_ns();
@@ -150,19 +157,6 @@ __device__ __forceinline__ bool drain_bar(const Ctl& c, uint64_t* bar, uint32_t 
     }
     return true;
 }
-// arrival count within this launch; a counter left by another launch restarts
-__device__ __forceinline__ uint32_t arrive_count(unsigned long long* ctr, uint32_t epoch) {
-    unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(ctr);
-    while (true) {
-        const unsigned long long want = (static_cast<uint32_t>(cur >> 32) == epoch)
-                                            ? cur + 1
-                                            : ((static_cast<unsigned long long>(epoch) << 32) | 1ull);
-        const unsigned long long prev = atomicCAS(ctr, cur, want);
-        if (prev == cur) return static_cast<uint32_t>(want);
-        cur = prev;
-    }
-}
-
 template <int KIND, int CG>
 struct Geo {
     static constexpr int BN = CG == 2 ? 256 : 128;     // tile columns (of the pair)
@@ -172,19 +166,17 @@ struct Geo {
     static constexpr uint32_t A_BYTES = BM * 128;      // 128 rows x 128 bytes of contraction
     static constexpr uint32_t B_BYTES = (BN / CG) * 128;
     static constexpr uint32_t RAW_BYTES = KIND == KIND_WG ? 64 * 128 : 0;
-    static constexpr uint32_t STAGE_BYTES = A_BYTES + (KIND == KIND_MM ? B_BYTES : 0);
-    // KIND_MM: a stage is one A and one B box.  KIND_WG: codes, converted A
-    // and B have rings of their own (RAWS, STAGES, BS slots), because each is
-    // held over another part of the way: load to conversion, conversion to
-    // MMA, load to MMA.
-    static constexpr int STAGES = KIND == KIND_MM ? 6 : 4;
-    static constexpr int RAWS = KIND == KIND_MM ? 0 : 6;
-    static constexpr int BS = KIND == KIND_MM ? 0 : 5;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+    // a stage holds one A and one B box; KIND_WG: the converted A and B, and
+    // the codes have a ring of their own (RAWS slots)
+    static constexpr int STAGES = KIND == KIND_MM ? 5 : 4;
+    static constexpr int RAWS = KIND == KIND_MM ? 0 : 4;
     static constexpr int THREADS = KIND == KIND_MM ? 384 : 640;
-    static constexpr uint32_t OUT_BYTES = 32 * 128;    // staging per promotion warp
-    static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * RAWS + 2 * BS + 4 + 2;
-    static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES + BS * B_BYTES + RAWS * RAW_BYTES;
+    static constexpr uint32_t OUT_BYTES = 2 * 32 * 128;  // staging per promotion warp: two boxes
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int ACCS = TMEM_COLS / BN;        // accumulators under way
+    static constexpr int NUM_BARS = 3 * STAGES + 2 * RAWS + 2 * ACCS + 2 * 8 + 1;
+    static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES + RAWS * RAW_BYTES;
     static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
     // registers: the launch's total (168 or 96 a thread) is shared out anew
     static constexpr int REGS_CTL = KIND == KIND_MM ? 56 : 48;
@@ -197,34 +189,33 @@ static_assert(Geo<KIND_MM, 2>::REGS_TOTAL <= 384 * 168 && Geo<KIND_WG, 2>::REGS_
 template <int KIND, int CG>
 struct Smem {
     using G = Geo<KIND, CG>;
-    uint8_t *tiles, *b_tiles, *raw_tiles, *out;
-    // KIND_MM: full / empty per stage.  KIND_WG: full / empty of the converted
-    // A (converters -> MMA), raw_full / raw_empty, b_full / b_empty
-    uint64_t *full, *empty, *raw_full, *raw_empty, *b_full, *b_empty, *acc_full, *acc_empty, *sync, *final_bar;
-    uint32_t *tmem_slot, *epoch_slot, *last;
+    uint8_t *tiles, *raw_tiles, *out;
+    // per stage: full (KIND_MM: A and B have landed; KIND_WG: A is converted),
+    // b_full (KIND_WG: B has landed), done (its MMAs have run: the stage may be
+    // filled again); per slot of codes: raw_full, raw_empty; per accumulator:
+    // acc_full, acc_empty; per promotion warp: parts_in (every part's sums lie
+    // in shared memory), parts_out (every part has read this CTA's)
+    uint64_t *full, *done, *raw_full, *raw_empty, *b_full, *acc_full, *acc_empty, *parts_in, *parts_out, *final_bar;
+    uint32_t *tmem_slot, *epoch_slot;
     __device__ void carve(uint8_t* p) {
         tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
-        b_tiles = tiles + G::STAGES * G::STAGE_BYTES;
-        raw_tiles = b_tiles + G::BS * G::B_BYTES;
+        raw_tiles = tiles + G::STAGES * G::STAGE_BYTES;
         out = tiles + G::TILES_BYTES;
         full = reinterpret_cast<uint64_t*>(out + 8 * G::OUT_BYTES);
-        empty = full + G::STAGES;
-        raw_full = empty + G::STAGES;
+        done = full + G::STAGES;
+        b_full = done + G::STAGES;
+        raw_full = b_full + G::STAGES;
         raw_empty = raw_full + G::RAWS;
-        b_full = raw_empty + G::RAWS;
-        b_empty = b_full + G::BS;
-        acc_full = b_empty + G::BS;
-        acc_empty = acc_full + 2;
-        sync = acc_empty + 2;
-        final_bar = sync + 1;
+        acc_full = raw_empty + G::RAWS;
+        acc_empty = acc_full + G::ACCS;
+        parts_in = acc_empty + G::ACCS;
+        parts_out = parts_in + 8;
+        final_bar = parts_out + 8;
         tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
         epoch_slot = tmem_slot + 1;
-        last = tmem_slot + 2;
     }
     __device__ uint8_t* a(uint32_t s) const { return tiles + s * G::STAGE_BYTES; }
-    __device__ uint8_t* b(uint32_t s) const {
-        return KIND == KIND_MM ? tiles + s * G::STAGE_BYTES + G::A_BYTES : b_tiles + s * G::B_BYTES;
-    }
+    __device__ uint8_t* b(uint32_t s) const { return tiles + s * G::STAGE_BYTES + G::A_BYTES; }
     __device__ uint8_t* raw(uint32_t s) const { return raw_tiles + s * G::RAW_BYTES; }
 };
 
@@ -254,21 +245,26 @@ struct Fills {
     }
 };
 
+// which half of a pair's tile this CTA works on
+template <int CG>
+__device__ __forceinline__ int half(const Ctl& ctl) {
+    return CG == 2 ? ctl.rank : 0;
+}
+
 struct Unit {
-    int mb, nb, part, lo, hi;  // tile, part, its stages
+    int mb, nb, lo, hi;  // tile and this CTA's stages of it
 };
 // Tiles in groups of group_m rows of tiles, so the tiles running at once share
-// their operands in L2; a tile's parts follow one another.
-__device__ __forceinline__ Unit unit_of(const GemmParams& p, int u) {
+// their operands in L2.
+template <int CG>
+__device__ __forceinline__ Unit unit_of(const GemmParams& p, const Ctl& ctl, int t) {
     Unit x;
-    const int t = u / p.split;
-    x.part = u - t * p.split;
     const int per = p.group_m * p.n_blocks;
     const int g = t / per, first = g * p.group_m;
     const int rows = min(p.group_m, p.m_blocks - first), in = t - g * per;
     x.mb = first + in % rows;
     x.nb = in / rows;
-    x.lo = x.part * p.part_stages;
+    x.lo = CG == 1 ? ctl.rank * p.part_stages : 0;
     x.hi = min(p.stages_total, x.lo + p.part_stages);
     return x;
 }
@@ -284,12 +280,12 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         Fills fills;
         const uint32_t bytes = p.a_box * 128 + G::B_BYTES;
         bool ok = true;
-        for (int u = first; u < p.n_units && ok; u += step) {
-            const Unit x = unit_of(p, u);
-            const int row = (x.mb * CG + ctl.half) * BM;
-            const int col = x.nb * G::BN + ctl.half * (G::BN / CG);
+        for (int u = first; u < p.n_tiles && ok; u += step) {
+            const Unit x = unit_of<CG>(p, ctl, u);
+            const int row = (x.mb * CG + half<CG>(ctl)) * BM;
+            const int col = x.nb * G::BN + half<CG>(ctl) * (G::BN / CG);
             for (int s = x.lo; s < x.hi; ++s) {
-                if (!wait_bar(ctl, &sm.empty[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                if (!wait_bar(ctl, &sm.done[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
                     ok = false;
                     break;
                 }
@@ -300,7 +296,7 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
                     tma_load_2d(sm.a(st.slot), &p.tmA, d, row, &sm.full[st.slot]);
                     tma_load_2d(sm.b(st.slot), &p.tmB, bc0, bc1, &sm.full[st.slot]);
                 } else {
-                    if (ctl.half == 0) mbar_arrive_expect_tx(&sm.full[st.slot], CG * bytes);
+                    if (half<CG>(ctl) == 0) mbar_arrive_expect_tx(&sm.full[st.slot], CG * bytes);
                     const uint32_t fb = mapa_shared(&sm.full[st.slot], 0);
                     tma_load_2d_pair(sm.a(st.slot), &p.tmA, d, row, fb);
                     tma_load_2d_pair(sm.b(st.slot), &p.tmB, bc0, bc1, fb);
@@ -309,14 +305,14 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
                 st.next();
             }
         }
-        fills.drain(ctl, ctl.half ? sm.empty : sm.full, G::STAGES);
+        fills.drain(ctl, half<CG>(ctl) ? sm.done : sm.full, G::STAGES);
     } else if (which == 0) {
         Ring<G::RAWS> st;
         Fills fills;
         bool ok = true;
-        for (int u = first; u < p.n_units && ok; u += step) {
-            const Unit x = unit_of(p, u);
-            const int row = (x.mb * CG + ctl.half) * BM;
+        for (int u = first; u < p.n_tiles && ok; u += step) {
+            const Unit x = unit_of<CG>(p, ctl, u);
+            const int row = (x.mb * CG + half<CG>(ctl)) * BM;
             for (int s = x.lo; s < x.hi; ++s) {
                 if (!wait_bar(ctl, &sm.raw_empty[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
                     ok = false;
@@ -330,19 +326,19 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         }
         fills.drain(ctl, sm.raw_full, G::RAWS);
     } else {
-        Ring<G::BS> st;
+        Ring<G::STAGES> st;
         Fills fills;
         bool ok = true;
-        for (int u = first; u < p.n_units && ok; u += step) {
-            const Unit x = unit_of(p, u);
-            const int col = x.nb * G::BN + ctl.half * (G::BN / CG);
+        for (int u = first; u < p.n_tiles && ok; u += step) {
+            const Unit x = unit_of<CG>(p, ctl, u);
+            const int col = x.nb * G::BN + half<CG>(ctl) * (G::BN / CG);
             for (int s = x.lo; s < x.hi; ++s) {
-                if (!wait_bar(ctl, &sm.b_empty[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                if (!wait_bar(ctl, &sm.done[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
                     ok = false;
                     break;
                 }
                 const int d = s * G::DEPTH;
-                if (ctl.half == 0) mbar_arrive_expect_tx(&sm.b_full[st.slot], CG * G::B_BYTES);
+                if (half<CG>(ctl) == 0) mbar_arrive_expect_tx(&sm.b_full[st.slot], CG * G::B_BYTES);
                 const uint32_t fb = CG == 2 ? mapa_shared(&sm.b_full[st.slot], 0) : 0u;
                 if (p.b_chunked) {
                     if (CG == 1)
@@ -360,19 +356,14 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
                 st.next();
             }
         }
-        fills.drain(ctl, ctl.half ? sm.b_empty : sm.b_full, G::BS);
+        fills.drain(ctl, half<CG>(ctl) ? sm.done : sm.b_full, G::STAGES);
     }
 }
 
-// arrive on this barrier (of both CTAs of a pair) when the MMAs so far are done
-template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    if (CG == 2)
-        umma_commit_pair_both(bar);
-    else
-        umma_commit<1>(bar);
-}
-
+// MMAs.  The whole warp runs the loop, so that addresses and descriptors stay
+// in uniform registers, where the tensor-core instructions take them from; one
+// elected lane issues.  A stage has few MMAs (four), so whatever else the loop
+// does per stage shows.
 template <int KIND, int CG>
 __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, uint32_t tmem, int first, int step) {
     using G = Geo<KIND, CG>;
@@ -382,51 +373,52 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
     // swizzled rows.  MN-major: rows of 128 bytes per contraction index, 8-deep
     // groups 1024 bytes apart (stride offset), K steps of 32 or 16 rows;
     // KIND_WG's two 64-element columns are 8192 bytes apart (leading offset).
-    const uint64_t a_adv = KIND == KIND_MM ? 2 : 128;
-    const uint64_t b_adv = KIND == KIND_MM ? (p.b_mn ? 256 : 2) : 128;
+    const uint32_t a_adv = KIND == KIND_MM ? 2 : 128;
+    const uint32_t b_adv = KIND == KIND_MM ? (p.b_mn ? 256 : 2) : 128;
     const uint32_t lead = KIND == KIND_MM ? 16 : 8192;
+    const uint64_t a_desc = smem_desc(smem_u32(sm.a(0)), lead, 1024), b_desc = smem_desc(smem_u32(sm.b(0)), lead, 1024);
+    const uint32_t full = smem_u32(sm.full), done = smem_u32(sm.done), b_full = smem_u32(sm.b_full);
+    const uint32_t acc_full = smem_u32(sm.acc_full), acc_empty = smem_u32(sm.acc_empty);
+    const uint32_t idesc = p.idesc;
     Ring<G::STAGES> st;
-    Ring<KIND == KIND_WG ? G::BS : 1> bst;
-    uint32_t chunk = 0;
+    Ring<G::ACCS> acc;
     bool ok = true;
-    for (int u = first; u < p.n_units && ok; u += step) {
-        const Unit x = unit_of(p, u);
-        for (int s0 = x.lo; s0 < x.hi && ok; s0 += CH, ++chunk) {
-            const uint32_t buf = chunk & 1, use = chunk >> 1;
+    for (int u = first; u < p.n_tiles && ok; u += step) {
+        const Unit x = unit_of<CG>(p, ctl, u);
+        const bool report = p.debug_skip != static_cast<uint32_t>(u) + 1;
+        for (int s0 = x.lo; s0 < x.hi && ok; s0 += CH, acc.next()) {
+            if (!wait_bar(ctl, acc_empty + 8 * acc.slot, acc.phase ^ 1, WAIT_ACC_EMPTY)) {
+                ok = false;
+                break;
+            }
             const int end = min(x.hi, s0 + CH);
-            for (int s = s0; s < end && ok; ++s) {
-                if (!wait_bar(ctl, &sm.full[st.slot], st.phase, WAIT_FULL) ||
-                    (KIND == KIND_WG && !wait_bar(ctl, &sm.b_full[bst.slot], bst.phase, WAIT_FULL_B))) {
-                    ok = false;
-                    break;
-                }
-                const uint64_t ad = smem_desc(smem_u32(sm.a(st.slot)), lead, 1024);
-                const uint64_t bd = smem_desc(smem_u32(sm.b(KIND == KIND_MM ? st.slot : bst.slot)), lead, 1024);
-                if (s == s0 && !wait_bar(ctl, &sm.acc_empty[buf], (use & 1) ^ 1, WAIT_ACC_EMPTY)) {
+            const uint32_t d = tmem + acc.slot * G::BN;
+            for (int s = s0; s < end; ++s, st.next()) {
+                if (!wait_bar(ctl, full + 8 * st.slot, st.phase, WAIT_FULL) ||
+                    (KIND == KIND_WG && !wait_bar(ctl, b_full + 8 * st.slot, st.phase, WAIT_FULL_B))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem + buf * G::BN;
+                const uint64_t ad = a_desc + st.slot * (G::STAGE_BYTES / 16), bd = b_desc + st.slot * (G::STAGE_BYTES / 16);
+                const uint32_t more = s > s0 ? 1u : 0u;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < G::UMMA_STEPS; ++k) {
-                    const uint32_t acc = (s > s0 || k > 0) ? 1u : 0u;
-                    if (KIND == KIND_MM)
-                        umma_f8<CG>(d, ad + k * a_adv, bd + k * b_adv, p.idesc, acc);
-                    else
-                        umma_f16<CG>(d, ad + k * a_adv, bd + k * b_adv, p.idesc, acc);
+                    for (int k = 0; k < G::UMMA_STEPS; ++k) {
+                        if (KIND == KIND_MM)
+                            umma_f8<CG>(d, ad + k * a_adv, bd + k * b_adv, idesc, k > 0 ? 1u : more);
+                        else
+                            umma_f16<CG>(d, ad + k * a_adv, bd + k * b_adv, idesc, k > 0 ? 1u : more);
+                    }
+                    umma_commit_all<CG>(done + 8 * st.slot);
+                    if (s == end - 1 && report) umma_commit_all<CG>(acc_full + 8 * acc.slot);
                 }
-                if (s == end - 1 && p.debug_skip != static_cast<uint32_t>(u) + 1) commit<CG>(&sm.acc_full[buf]);
-                commit<CG>(&sm.empty[st.slot]);
-                st.next();
-                if (KIND == KIND_WG) {
-                    commit<CG>(&sm.b_empty[bst.slot]);
-                    bst.next();
-                }
+                __syncwarp();
             }
         }
     }
-    umma_commit<CG>(sm.final_bar);
+    if (elect_one()) umma_commit<CG>(sm.final_bar);
+    __syncwarp();
     drain_bar(ctl, sm.final_bar, 0, WAIT_DRAIN_MMA);
 }
 
@@ -480,7 +472,8 @@ struct Worker {
     const uint32_t tmem;
     const int w, lane, q, h;
     uint8_t* const stg;
-    uint32_t chunk = 0, syncs = 0;
+    Ring<G::ACCS> from;  // the accumulator that the next chunk will be in
+    uint32_t tiles_done = 0, stores = 0;
     unsigned long long acc[COLS / 2];  // pairs of fp32 sums
 
     __device__ __forceinline__ Worker(const GemmParams& p_, const Ctl& c_, Smem<KIND, CG>& s_, uint32_t t_, int w_, int lane_)
@@ -502,8 +495,8 @@ struct Worker {
     __device__ __forceinline__ Place place(int u) const {
         Place pl;
         pl.u = u;
-        pl.x = unit_of(p, u);
-        pl.blk = pl.x.mb * CG + ctl.half;
+        pl.x = unit_of<CG>(p, ctl, u);
+        pl.blk = pl.x.mb * CG + half<CG>(ctl);
         pl.row0 = pl.blk * BM + q * 32;
         pl.live = pl.row0 < p.M && col_of(pl, 0) < p.N;
         return pl;
@@ -518,9 +511,9 @@ struct Worker {
     // one has arrived.
     template <int LD>
     __device__ __forceinline__ bool promote(bool live, float scale) {
-        const uint32_t buf = chunk & 1;
-        if (!wait_bar(ctl, &sm.acc_full[buf], (chunk >> 1) & 1, WAIT_ACC_FULL)) return false;
-        ++chunk;
+        const uint32_t buf = from.slot;
+        if (!wait_bar(ctl, &sm.acc_full[buf], from.phase, WAIT_ACC_FULL)) return false;
+        from.next();
         tc_fence_after();
         auto release = [&]() {
             tc_fence_before();
@@ -552,13 +545,103 @@ struct Worker {
         return true;
     }
 
+    // a staged box to an output that no tensor store can reach: rows of
+    // elements, a lane per column
+    __device__ __forceinline__ void store_box(const uint8_t* box, int row0, int c0, bool wide) const {
+        const int rows = min(32, p.M - row0);
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r) {
+            if (wide) {
+                const uint8_t* at = box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+                if (c0 + lane < p.N) store_out(p, row0 + r, c0 + lane, *reinterpret_cast<const float*>(at));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = lane + e * 32;
+                    const uint8_t* at = box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
+                    if (c0 + c < p.N)
+                        static_cast<uint16_t*>(p.out)[(row0 + r) * p.out_rs + (c0 + c) * p.out_cs] =
+                            *reinterpret_cast<const uint16_t*>(at);
+                }
+            }
+        }
+    }
+
+    // Split contraction: each warp lays its 32 x 64 sums into shared memory
+    // (rows of 16 units of 16 bytes, XORed with the row), tells the same warp
+    // of every part, and adds its part's share of the columns (units
+    // rank * 16 / S ...) over all parts in order.
+    __device__ __forceinline__ bool join(const Place& pl) {
+        const int S = p.split;
+        // the other parts have read what lay here before
+        if (tiles_done > 0 && !wait_bar_cluster(ctl, &sm.parts_out[w], (tiles_done - 1) & 1, WAIT_PARTS)) return false;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float v[4];
+            unpack_f32x2(acc[2 * j], v[0], v[1]);
+            unpack_f32x2(acc[2 * j + 1], v[2], v[3]);
+            *reinterpret_cast<float4*>(stg + lane * 256 + ((j ^ (lane & 15)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        __syncwarp();
+        if (lane < S) mbar_arrive_cluster(mapa_shared(&sm.parts_in[w], lane));
+        if (!wait_bar_cluster(ctl, &sm.parts_in[w], tiles_done & 1, WAIT_PARTS)) return false;
+        ++tiles_done;
+        const int units = 16 / S, row = pl.row0 + lane;
+#pragma unroll 1
+        for (int i = 0; i < units; ++i) {
+            const int j = ctl.rank * units + i;
+            const uint32_t at = (j ^ (lane & 15)) << 4;
+            float4 t[MAX_SPLIT];
+#pragma unroll
+            for (int k = 0; k < MAX_SPLIT; ++k)
+                if (k < S) t[k] = ld_shared_cluster_f4(mapa_shared(stg + lane * 256, k) + at);
+            float4 sum = t[0];
+#pragma unroll
+            for (int k = 1; k < MAX_SPLIT; ++k)
+                if (k < S) {
+                    sum.x += t[k].x;
+                    sum.y += t[k].y;
+                    sum.z += t[k].z;
+                    sum.w += t[k].w;
+                }
+            const int c = col_of(pl, 0) + j * 4;
+            float v[4] = {sum.x, sum.y, sum.z, sum.w};
+            if (KIND == KIND_MM && p.bias) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += load_bias(p, c + e);
+            }
+            if (row < p.M) {
+                if (p.tma_out && c + 4 <= p.N) {  // unit stride, rows on 16 bytes
+                    const long long o = row * p.out_rs + c;
+                    if (p.out_type == T_F32)
+                        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+                    else
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
+                            make_uint2(pack16(v[0], v[1], p.out_type == T_BF16), pack16(v[2], v[3], p.out_type == T_BF16));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < p.N) store_out(p, row, c + e, v[e]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane < S) mbar_arrive_cluster(mapa_shared(&sm.parts_out[w], lane));
+        return true;
+    }
+
     __device__ __forceinline__ bool epilogue(const Place& pl) {
-        // epilogue: 32 rows x 128 bytes at a time through swizzled staging and
-        // a tensor store, which clips the ragged edges.  Whole sums are
-        // rounded here, once; parts stay fp32.
+        if (CG == 1 && p.split > 1) {
+            // not live in one part: not live in any
+            if (pl.live && !join(pl)) return false;
+            clear();
+            return true;
+        }
+        // 32 rows x 128 bytes at a time through swizzled staging, two boxes in
+        // turn; the sums are rounded here, once
         if (pl.live) {
-            const bool wide = p.staged || p.out_type == T_F32;
-            const bool add_bias = KIND == KIND_MM && p.bias != nullptr && !p.staged;
+            const bool wide = p.out_type == T_F32;
+            const bool add_bias = KIND == KIND_MM && p.bias != nullptr;
 #pragma unroll
             for (int c = 0; c < COLS / 32; ++c) {
                 float v[32];
@@ -569,84 +652,41 @@ struct Worker {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
                 }
-                if (wide || (c & 1) == 0) {  // the staging buffer is used anew
-                    if (lane == 0) bulk_wait_read_all();
+                if (wide || (c & 1) == 0) {  // a staging box is used anew
+                    if (lane == 0) bulk_wait_read<1>();
                     __syncwarp();
                 }
+                uint8_t* box = stg + (stores & 1) * 4096;
                 if (wide) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<float4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                        *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else {
                     const int bf = p.out_type == T_BF16;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4*>(stg + lane * 128 + (((j + (c & 1) * 4) ^ (lane & 7)) << 4)) =
+                        *reinterpret_cast<uint4*>(box + lane * 128 + (((j + (c & 1) * 4) ^ (lane & 7)) << 4)) =
                             make_uint4(pack16(v[8 * j], v[8 * j + 1], bf), pack16(v[8 * j + 2], v[8 * j + 3], bf),
                                        pack16(v[8 * j + 4], v[8 * j + 5], bf), pack16(v[8 * j + 6], v[8 * j + 7], bf));
                 }
                 if (wide || (c & 1) == 1) {
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        const int cc = col_of(pl, wide ? c : c - 1);
-                        if (cc < p.N) tma_store_3d(&p.tmC, stg, cc, pl.row0, p.staged ? pl.x.part : 0);
-                        bulk_commit();
+                    const int cc = col_of(pl, wide ? c : c - 1);
+                    if (p.tma_out) {  // a tensor store, which clips the ragged edges
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (cc < p.N) tma_store_2d(&p.tmC, box, cc, pl.row0);
+                            bulk_commit();
+                        }
+                        ++stores;
+                    } else {
+                        __syncwarp();
+                        store_box(box, pl.row0, cc, wide);
+                        __syncwarp();
                     }
                 }
             }
-        }
-
-        if (p.staged) {
-            // publish this part, then the last one of the tile adds them up in
-            // part order and writes the output
-            if (lane == 0) {
-                bulk_wait_all();
-                fence_proxy_async_global();
-            }
-            __syncwarp();
-            __threadfence();
-            auto sync = [&]() {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sm.sync);
-                const bool ok = wait_bar(ctl, sm.sync, syncs & 1, WAIT_SYNC);
-                ++syncs;
-                return ok;
-            };
-            if (!sync()) return false;
-            if (w == 0 && lane == 0) {
-                bool last = true;
-                __threadfence();
-                if (p.split > 1)
-                    last = arrive_count(p.arrived + (pl.u / p.split) * CG + ctl.half, ctl.epoch) == static_cast<uint32_t>(p.split);
-                __threadfence();
-                *reinterpret_cast<volatile uint32_t*>(sm.last) = last ? 1u : 0u;
-            }
-            if (!sync()) return false;
-            if (*reinterpret_cast<volatile uint32_t*>(sm.last)) {
-                __threadfence();
-                const int rows = min(BM, p.M - pl.blk * BM), tile_c = pl.x.nb * G::BN;
-                const int quads = (min(G::BN, p.N - tile_c) + 3) / 4;
-                for (int i = w * 32 + lane; i < rows * quads; i += 256) {
-                    const int r = pl.blk * BM + i / quads, c = tile_c + (i % quads) * 4;
-                    const float* src = p.partial + static_cast<long long>(r) * p.part_rs + c;
-                    float4 sum = __ldcg(reinterpret_cast<const float4*>(src));
-                    for (int k = 1; k < p.split; ++k) {
-                        const float4 t = __ldcg(reinterpret_cast<const float4*>(src + k * p.part_stride));
-                        sum.x += t.x;
-                        sum.y += t.y;
-                        sum.z += t.z;
-                        sum.w += t.w;
-                    }
-                    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < p.N) store_out(p, r, c + e, v[e] + (KIND == KIND_MM ? load_bias(p, c + e) : 0.f));
-                }
-            }
-            // the flag is read by all before the next unit may set it anew
-            if (!sync()) return false;
         }
         clear();
         return true;
@@ -658,7 +698,7 @@ template <int CG>
 __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM, CG>& sm, uint32_t tmem, int w, int lane,
                             int first, int step) {
     Worker<KIND_MM, CG> wk(p, ctl, sm, tmem, w, lane);
-    for (int u = first; u < p.n_units; u += step) {
+    for (int u = first; u < p.n_tiles; u += step) {
         const auto pl = wk.place(u);
         const int row = pl.row0 + lane;
         const float* sa = p.sa + static_cast<long long>(row) * p.sa_rs;
@@ -692,7 +732,7 @@ template <int CG>
 __device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, uint32_t tmem, int w, int lane,
                                int first, int step) {
     Worker<KIND_WG, CG> wk(p, ctl, sm, tmem, w, lane);
-    for (int u = first; u < p.n_units; u += step) {
+    for (int u = first; u < p.n_tiles; u += step) {
         const auto pl = wk.place(u);
         for (int s = pl.x.lo; s < pl.x.hi; s += WG_CHUNK)
             if (!wk.template promote<16>(pl.live, 1.f)) return false;
@@ -719,10 +759,10 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
     const uint32_t u0 = col * 8192 + r0 * 128 + ((j0 ^ (r0 & 7)) << 4);
     const uint32_t u1 = col * 8192 + r0 * 128 + (((j0 + 1) ^ (r0 & 7)) << 4);
     int turn = 0;  // stages so far, over all units
-    for (int u = first; u < p.n_units; u += step) {
-        const Unit x = unit_of(p, u);
+    for (int u = first; u < p.n_tiles; u += step) {
+        const Unit x = unit_of<CG>(p, ctl, u);
         // this CTA's 128 output rows are one block of scales
-        const int kblk = x.mb * CG + ctl.half;
+        const int kblk = x.mb * CG + half<CG>(ctl);
         const bool live = kblk * BM < p.M;
         const float* sx = p.sa + kblk * p.sa_cs;
         // a stage's scales are fetched one turn (two stages) ahead
@@ -742,7 +782,7 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
             for (int i = 0; i < 4; ++i) sc[i] = next[i];
             fetch(s + 2);
             if (!wait_bar(ctl, &sm.raw_full[rs.slot], rs.phase, WAIT_RAW)) return;
-            if (!wait_bar(ctl, &sm.empty[st.slot], st.phase ^ 1, WAIT_A_EMPTY)) return;
+            if (!wait_bar(ctl, &sm.done[st.slot], st.phase ^ 1, WAIT_A_EMPTY)) return;
             const uint8_t* src = sm.raw(rs.slot) + r0 * 128 + seg * 16;
             uint8_t* dst = sm.a(st.slot);
             uint4 c4 = *reinterpret_cast<const uint4*>(src);
@@ -776,41 +816,43 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
     Smem<KIND, CG> sm;
     sm.carve(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int half = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    // CTAs per cluster: the pair, or the parts of the contraction
+    const int csize = CG == 2 ? 2 : p.split;
+    const int rank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::STAGES; ++s) {
             mbar_init(&sm.full[s], KIND == KIND_MM ? 1 : CG * 4);
-            mbar_init(&sm.empty[s], 1);
+            mbar_init(&sm.done[s], 1);
+            mbar_init(&sm.b_full[s], 1);
         }
         for (int s = 0; s < G::RAWS; ++s) {
             mbar_init(&sm.raw_full[s], 1);
             mbar_init(&sm.raw_empty[s], 4);
         }
-        for (int s = 0; s < G::BS; ++s) {
-            mbar_init(&sm.b_full[s], 1);
-            mbar_init(&sm.b_empty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < G::ACCS; ++b) {
             mbar_init(&sm.acc_full[b], 1);
             mbar_init(&sm.acc_empty[b], CG * 8);
         }
-        mbar_init(sm.sync, 8);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&sm.parts_in[i], csize);
+            mbar_init(&sm.parts_out[i], csize);
+        }
         mbar_init(sm.final_bar, 1);
         fence_mbar_init();
         uint32_t e = *reinterpret_cast<volatile uint32_t*>(&p.ws->epoch) + 1u;
         *sm.epoch_slot = e == 0u ? 1u : e;
         tma_prefetch_desc(&p.tmA);
         tma_prefetch_desc(&p.tmB);
-        tma_prefetch_desc(&p.tmC);
+        if (p.split == 1 && p.tma_out) tma_prefetch_desc(&p.tmC);
     }
     if (warp == 1) tmem_alloc<G::TMEM_COLS, CG>(sm.tmem_slot);
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync();
+    if (csize > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot;
-    const Ctl ctl{p.ws, *sm.epoch_slot, p.wait_ns, half};
-    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+    const Ctl ctl{p.ws, *sm.epoch_slot, p.wait_ns, rank};
+    const int first = blockIdx.x / csize, step = gridDim.x / csize;
 
     if (warp < 4) {
         reg_dec<G::REGS_CTL>();
@@ -819,7 +861,7 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
         } else if (KIND == KIND_WG && warp == 2) {
             if (lane == 0) run_tma<KIND, CG>(p, ctl, sm, 1, first, step);
         } else if (warp == 1) {
-            if (lane == 0 && half == 0) run_mma<KIND, CG>(p, ctl, sm, tmem, first, step);
+            if (CG == 1 || rank == 0) run_mma<KIND, CG>(p, ctl, sm, tmem, first, step);
         }
         __syncwarp();
     } else if (warp < 12) {
@@ -844,9 +886,9 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
 
     tc_fence_before();
     __syncthreads();
-    // neither CTA of a pair leaves (or frees tensor memory) while the other
-    // may still signal its barriers
-    if (CG == 2) cluster_sync();
+    // no CTA of a cluster leaves (or frees tensor memory) while another may
+    // still signal its barriers or read its shared memory
+    if (csize > 1) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc<G::TMEM_COLS, CG>(tmem);
