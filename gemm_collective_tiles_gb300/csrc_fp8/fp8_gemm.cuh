@@ -19,8 +19,7 @@
 //   warp 0       TMA producer (lane 0); KIND_WG: of the codes
 //   warp 1       MMA issuer; owns tensor memory
 //   warp 2       KIND_WG: TMA producer of dY (lane 0)
-//   warp 3       none: it makes the first warpgroup whole, which gives its
-//                registers to the promotion warps
+//   warp 3       KIND_MM, CG = 1: second MMA issuer
 //   warps 4-11   promotion and epilogue: quadrant warp % 4 of the accumulator's
 //                rows, column half (warp - 4) / 4
 //   warps 12-19  KIND_WG: converters
@@ -60,10 +59,10 @@ enum : int {
     WAIT_ACC_EMPTY = 104,
     WAIT_ACC_FULL = 105,
     WAIT_RAW = 106,
-    WAIT_PARTS = 107,
-    WAIT_DRAIN_TMA = 108,
-    WAIT_DRAIN_MMA = 109,
-    WAIT_A_EMPTY = 110,
+    WAIT_A_EMPTY = 107,
+    WAIT_PARTS = 108,
+    WAIT_DRAIN_TMA = 120,  // from here on: teardown
+    WAIT_DRAIN_MMA = 121,
 };
 
 // The library's workspace header (same layout for every op).
@@ -125,14 +124,15 @@ __device__ __forceinline__ void raise_timeout(const Ctl& c, int where, int index
     __threadfence();
     atomicExch(&c.ws->abort_epoch, c.epoch);
 }
-template <typename Bar>  // a barrier by pointer or by shared-memory address
-__device__ __forceinline__ bool wait_bar(const Ctl& c, Bar bar, uint32_t parity, int where) {
-    if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait for a phase of a barrier; false = gave up, here or elsewhere.
+__device__ __forceinline__ bool wait_bar(const Ctl& c, uint32_t bar, uint32_t parity, int where) {
+    if (bar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (bar_try_wait(bar, parity)) return true;
         if ((i & 15) == 0) {
-            if (launch_aborted(c)) return false;
+            // teardown waits are for work already issued: they go on while the launch stops
+            if (where < WAIT_DRAIN_TMA && launch_aborted(c)) return false;
             if (global_timer_ns() - t0 > c.limit) {
                 raise_timeout(c, where, -1);
                 return false;
@@ -142,21 +142,11 @@ __device__ __forceinline__ bool wait_bar(const Ctl& c, Bar bar, uint32_t parity,
 }
 // for barriers that other CTAs' promotion warps arrive on after writing shared
 // memory that this one reads
-__device__ __forceinline__ bool wait_bar_cluster(const Ctl& c, uint64_t* bar, uint32_t parity, int where) {
+__device__ __forceinline__ bool wait_bar_cluster(const Ctl& c, uint32_t bar, uint32_t parity, int where) {
     if (!wait_bar(c, bar, parity, where)) return false;
-    return mbar_try_wait_cluster(bar, parity);  // the phase is over: this only acquires at cluster scope
+    return bar_try_wait_cluster(bar, parity);  // the phase is over: this only acquires at cluster scope
 }
-// teardown: waits for asynchronous work already issued, also while stopping
-__device__ __forceinline__ bool drain_bar(const Ctl& c, uint64_t* bar, uint32_t parity, int where) {
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (global_timer_ns() - t0 > c.limit) {
-            raise_timeout(c, where, -1);
-            return false;
-        }
-    }
-    return true;
-}
+
 template <int KIND, int CG>
 struct Geo {
     static constexpr int BN = CG == 2 ? 256 : 128;     // tile columns (of the pair)
@@ -171,11 +161,12 @@ struct Geo {
     // the codes have a ring of their own (RAWS slots)
     static constexpr int STAGES = KIND == KIND_MM ? 5 : 4;
     static constexpr int RAWS = KIND == KIND_MM ? 0 : 4;
+    static constexpr int ISSUERS = KIND == KIND_MM && CG == 1 ? 2 : 1;  // warps that issue MMAs
     static constexpr int THREADS = KIND == KIND_MM ? 384 : 640;
     static constexpr uint32_t OUT_BYTES = 2 * 32 * 128;  // staging per promotion warp: two boxes
     static constexpr int TMEM_COLS = 512;
     static constexpr int ACCS = TMEM_COLS / BN;        // accumulators under way
-    static constexpr int NUM_BARS = 3 * STAGES + 2 * RAWS + 2 * ACCS + 2 * 8 + 1;
+    static constexpr int NUM_BARS = 3 * STAGES + 2 * RAWS + 2 * ACCS + 2 * 8 + 2;
     static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES + RAWS * RAW_BYTES;
     static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
     // registers: the launch's total (168 or 96 a thread) is shared out anew
@@ -189,34 +180,37 @@ static_assert(Geo<KIND_MM, 2>::REGS_TOTAL <= 384 * 168 && Geo<KIND_WG, 2>::REGS_
 template <int KIND, int CG>
 struct Smem {
     using G = Geo<KIND, CG>;
-    uint8_t *tiles, *raw_tiles, *out;
-    // per stage: full (KIND_MM: A and B have landed; KIND_WG: A is converted),
-    // b_full (KIND_WG: B has landed), done (its MMAs have run: the stage may be
-    // filled again); per slot of codes: raw_full, raw_empty; per accumulator:
-    // acc_full, acc_empty; per promotion warp: parts_in (every part's sums lie
-    // in shared memory), parts_out (every part has read this CTA's)
-    uint64_t *full, *done, *raw_full, *raw_empty, *b_full, *acc_full, *acc_empty, *parts_in, *parts_out, *final_bar;
+    uint8_t* base;  // tiles, codes, staging
+    // shared-memory addresses.  Barriers per stage: full (KIND_MM: A and B have
+    // landed; KIND_WG: A is converted), b_full (KIND_WG: B has landed), done
+    // (its MMAs have run: the stage may be filled again); per slot of codes:
+    // raw_full, raw_empty; per accumulator: acc_full, acc_empty; per promotion
+    // warp: parts_in (every part's sums lie in shared memory), parts_out (every
+    // part has read this CTA's)
+    uint32_t tiles, raw_tiles, full, done, raw_full, raw_empty, b_full, acc_full, acc_empty, parts_in, parts_out, final_bar;
     uint32_t *tmem_slot, *epoch_slot;
     __device__ void carve(uint8_t* p) {
-        tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
+        base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
+        tiles = smem_u32(base);
         raw_tiles = tiles + G::STAGES * G::STAGE_BYTES;
-        out = tiles + G::TILES_BYTES;
-        full = reinterpret_cast<uint64_t*>(out + 8 * G::OUT_BYTES);
-        done = full + G::STAGES;
-        b_full = done + G::STAGES;
-        raw_full = b_full + G::STAGES;
-        raw_empty = raw_full + G::RAWS;
-        acc_full = raw_empty + G::RAWS;
-        acc_empty = acc_full + G::ACCS;
-        parts_in = acc_empty + G::ACCS;
-        parts_out = parts_in + 8;
-        final_bar = parts_out + 8;
-        tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
+        full = tiles + G::TILES_BYTES + 8 * G::OUT_BYTES;
+        done = full + 8 * G::STAGES;
+        b_full = done + 8 * G::STAGES;
+        raw_full = b_full + 8 * G::STAGES;
+        raw_empty = raw_full + 8 * G::RAWS;
+        acc_full = raw_empty + 8 * G::RAWS;
+        acc_empty = acc_full + 8 * G::ACCS;
+        parts_in = acc_empty + 8 * G::ACCS;
+        parts_out = parts_in + 64;
+        final_bar = parts_out + 64;
+        tmem_slot = reinterpret_cast<uint32_t*>(base + (final_bar + 16 - tiles));
         epoch_slot = tmem_slot + 1;
     }
-    __device__ uint8_t* a(uint32_t s) const { return tiles + s * G::STAGE_BYTES; }
-    __device__ uint8_t* b(uint32_t s) const { return tiles + s * G::STAGE_BYTES + G::A_BYTES; }
-    __device__ uint8_t* raw(uint32_t s) const { return raw_tiles + s * G::RAW_BYTES; }
+    __device__ __forceinline__ uint32_t a(uint32_t s) const { return tiles + s * G::STAGE_BYTES; }
+    __device__ __forceinline__ uint32_t b(uint32_t s) const { return tiles + s * G::STAGE_BYTES + G::A_BYTES; }
+    __device__ __forceinline__ uint32_t raw(uint32_t s) const { return raw_tiles + s * G::RAW_BYTES; }
+    __device__ __forceinline__ uint8_t* at(uint32_t addr) const { return base + (addr - tiles); }
+    __device__ __forceinline__ uint8_t* out(int w) const { return base + G::TILES_BYTES + w * G::OUT_BYTES; }
 };
 
 // Position in a ring of N slots.
@@ -239,9 +233,9 @@ struct Fills {
         used |= 1u << slot;
     }
     // every load has landed before the CTA leaves
-    __device__ __forceinline__ void drain(const Ctl& ctl, uint64_t* bars, int n) const {
+    __device__ __forceinline__ void drain(const Ctl& ctl, uint32_t bars, int n) const {
         for (int s = 0; s < n; ++s)
-            if ((used & (1u << s)) && !drain_bar(ctl, &bars[s], filled >> s & 1u, WAIT_DRAIN_TMA)) return;
+            if ((used & (1u << s)) && !wait_bar(ctl, bars + 8 * s, filled >> s & 1u, WAIT_DRAIN_TMA)) return;
     }
 };
 
@@ -285,19 +279,19 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
             const int row = (x.mb * CG + half<CG>(ctl)) * BM;
             const int col = x.nb * G::BN + half<CG>(ctl) * (G::BN / CG);
             for (int s = x.lo; s < x.hi; ++s) {
-                if (!wait_bar(ctl, &sm.done[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                if (!wait_bar(ctl, sm.done + 8 * st.slot, st.phase ^ 1, WAIT_EMPTY)) {
                     ok = false;
                     break;
                 }
                 const int d = s * G::DEPTH;
                 const int bc0 = p.b_mn ? col : d, bc1 = p.b_mn ? d : col;
                 if (CG == 1) {
-                    mbar_arrive_expect_tx(&sm.full[st.slot], bytes);
-                    tma_load_2d(sm.a(st.slot), &p.tmA, d, row, &sm.full[st.slot]);
-                    tma_load_2d(sm.b(st.slot), &p.tmB, bc0, bc1, &sm.full[st.slot]);
+                    bar_expect_tx(sm.full + 8 * st.slot, bytes);
+                    tma_load_2d(sm.a(st.slot), &p.tmA, d, row, sm.full + 8 * st.slot);
+                    tma_load_2d(sm.b(st.slot), &p.tmB, bc0, bc1, sm.full + 8 * st.slot);
                 } else {
-                    if (half<CG>(ctl) == 0) mbar_arrive_expect_tx(&sm.full[st.slot], CG * bytes);
-                    const uint32_t fb = mapa_shared(&sm.full[st.slot], 0);
+                    if (half<CG>(ctl) == 0) bar_expect_tx(sm.full + 8 * st.slot, CG * bytes);
+                    const uint32_t fb = map_to(sm.full + 8 * st.slot, 0);
                     tma_load_2d_pair(sm.a(st.slot), &p.tmA, d, row, fb);
                     tma_load_2d_pair(sm.b(st.slot), &p.tmB, bc0, bc1, fb);
                 }
@@ -314,12 +308,12 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
             const Unit x = unit_of<CG>(p, ctl, u);
             const int row = (x.mb * CG + half<CG>(ctl)) * BM;
             for (int s = x.lo; s < x.hi; ++s) {
-                if (!wait_bar(ctl, &sm.raw_empty[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                if (!wait_bar(ctl, sm.raw_empty + 8 * st.slot, st.phase ^ 1, WAIT_EMPTY)) {
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(&sm.raw_full[st.slot], G::RAW_BYTES);
-                tma_load_2d(sm.raw(st.slot), &p.tmA, row, s * G::DEPTH, &sm.raw_full[st.slot]);
+                bar_expect_tx(sm.raw_full + 8 * st.slot, G::RAW_BYTES);
+                tma_load_2d(sm.raw(st.slot), &p.tmA, row, s * G::DEPTH, sm.raw_full + 8 * st.slot);
                 fills.add(st.slot, st.phase);
                 st.next();
             }
@@ -333,22 +327,22 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
             const Unit x = unit_of<CG>(p, ctl, u);
             const int col = x.nb * G::BN + half<CG>(ctl) * (G::BN / CG);
             for (int s = x.lo; s < x.hi; ++s) {
-                if (!wait_bar(ctl, &sm.done[st.slot], st.phase ^ 1, WAIT_EMPTY)) {
+                if (!wait_bar(ctl, sm.done + 8 * st.slot, st.phase ^ 1, WAIT_EMPTY)) {
                     ok = false;
                     break;
                 }
                 const int d = s * G::DEPTH;
-                if (half<CG>(ctl) == 0) mbar_arrive_expect_tx(&sm.b_full[st.slot], CG * G::B_BYTES);
-                const uint32_t fb = CG == 2 ? mapa_shared(&sm.b_full[st.slot], 0) : 0u;
+                if (half<CG>(ctl) == 0) bar_expect_tx(sm.b_full + 8 * st.slot, CG * G::B_BYTES);
+                const uint32_t fb = CG == 2 ? map_to(sm.b_full + 8 * st.slot, 0) : 0u;
                 if (p.b_chunked) {
                     if (CG == 1)
-                        tma_load_3d(sm.b(st.slot), &p.tmB, 0, d, col / 64, &sm.b_full[st.slot]);
+                        tma_load_3d(sm.b(st.slot), &p.tmB, 0, d, col / 64, sm.b_full + 8 * st.slot);
                     else
                         tma_load_3d_pair(sm.b(st.slot), &p.tmB, 0, d, col / 64, fb);
                 } else
                 for (int c = 0; c < G::BN / CG / 64; ++c) {
                     if (CG == 1)
-                        tma_load_2d(sm.b(st.slot) + c * 8192, &p.tmB, col + c * 64, d, &sm.b_full[st.slot]);
+                        tma_load_2d(sm.b(st.slot) + c * 8192, &p.tmB, col + c * 64, d, sm.b_full + 8 * st.slot);
                     else
                         tma_load_2d_pair(sm.b(st.slot) + c * 8192, &p.tmB, col + c * 64, d, fb);
                 }
@@ -363,9 +357,11 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
 // MMAs.  The whole warp runs the loop, so that addresses and descriptors stay
 // in uniform registers, where the tensor-core instructions take them from; one
 // elected lane issues.  A stage has few MMAs (four), so whatever else the loop
-// does per stage shows.
+// does per stage shows: with 128 x 128 tiles it takes longer than the MMAs, and
+// two issuers take the chunks in turn (each chunk has its own accumulator).
 template <int KIND, int CG>
-__device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, uint32_t tmem, int first, int step) {
+__device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, uint32_t tmem, int issuer, int first,
+                        int step) {
     using G = Geo<KIND, CG>;
     constexpr int CH = KIND == KIND_MM ? 1 : WG_CHUNK;
     // Descriptors.  K-major (A and B^T of KIND_MM): 8-row groups 1024 bytes
@@ -376,9 +372,7 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
     const uint32_t a_adv = KIND == KIND_MM ? 2 : 128;
     const uint32_t b_adv = KIND == KIND_MM ? (p.b_mn ? 256 : 2) : 128;
     const uint32_t lead = KIND == KIND_MM ? 16 : 8192;
-    const uint64_t a_desc = smem_desc(smem_u32(sm.a(0)), lead, 1024), b_desc = smem_desc(smem_u32(sm.b(0)), lead, 1024);
-    const uint32_t full = smem_u32(sm.full), done = smem_u32(sm.done), b_full = smem_u32(sm.b_full);
-    const uint32_t acc_full = smem_u32(sm.acc_full), acc_empty = smem_u32(sm.acc_empty);
+    const uint64_t a_desc = smem_desc(sm.a(0), lead, 1024), b_desc = smem_desc(sm.b(0), lead, 1024);
     const uint32_t idesc = p.idesc;
     Ring<G::STAGES> st;
     Ring<G::ACCS> acc;
@@ -387,15 +381,19 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         const Unit x = unit_of<CG>(p, ctl, u);
         const bool report = p.debug_skip != static_cast<uint32_t>(u) + 1;
         for (int s0 = x.lo; s0 < x.hi && ok; s0 += CH, acc.next()) {
-            if (!wait_bar(ctl, acc_empty + 8 * acc.slot, acc.phase ^ 1, WAIT_ACC_EMPTY)) {
+            if (G::ISSUERS == 2 && (acc.slot & 1) != issuer) {
+                st.next();
+                continue;
+            }
+            if (!wait_bar(ctl, sm.acc_empty + 8 * acc.slot, acc.phase ^ 1, WAIT_ACC_EMPTY)) {
                 ok = false;
                 break;
             }
             const int end = min(x.hi, s0 + CH);
             const uint32_t d = tmem + acc.slot * G::BN;
             for (int s = s0; s < end; ++s, st.next()) {
-                if (!wait_bar(ctl, full + 8 * st.slot, st.phase, WAIT_FULL) ||
-                    (KIND == KIND_WG && !wait_bar(ctl, b_full + 8 * st.slot, st.phase, WAIT_FULL_B))) {
+                if (!wait_bar(ctl, sm.full + 8 * st.slot, st.phase, WAIT_FULL) ||
+                    (KIND == KIND_WG && !wait_bar(ctl, sm.b_full + 8 * st.slot, st.phase, WAIT_FULL_B))) {
                     ok = false;
                     break;
                 }
@@ -410,16 +408,16 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
                         else
                             umma_f16<CG>(d, ad + k * a_adv, bd + k * b_adv, idesc, k > 0 ? 1u : more);
                     }
-                    umma_commit_all<CG>(done + 8 * st.slot);
-                    if (s == end - 1 && report) umma_commit_all<CG>(acc_full + 8 * acc.slot);
+                    umma_commit_all<CG>(sm.done + 8 * st.slot);
+                    if (s == end - 1 && report) umma_commit_all<CG>(sm.acc_full + 8 * acc.slot);
                 }
                 __syncwarp();
             }
         }
     }
-    if (elect_one()) umma_commit<CG>(sm.final_bar);
+    if (elect_one()) umma_commit_one<CG>(sm.final_bar + 8 * issuer);
     __syncwarp();
-    drain_bar(ctl, sm.final_bar, 0, WAIT_DRAIN_MMA);
+    wait_bar(ctl, sm.final_bar + 8 * issuer, 0, WAIT_DRAIN_MMA);
 }
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
@@ -477,7 +475,7 @@ struct Worker {
     unsigned long long acc[COLS / 2];  // pairs of fp32 sums
 
     __device__ __forceinline__ Worker(const GemmParams& p_, const Ctl& c_, Smem<KIND, CG>& s_, uint32_t t_, int w_, int lane_)
-        : p(p_), ctl(c_), sm(s_), tmem(t_), w(w_), lane(lane_), q(w_ & 3), h(w_ >> 2), stg(s_.out + w_ * G::OUT_BYTES) {
+        : p(p_), ctl(c_), sm(s_), tmem(t_), w(w_), lane(lane_), q(w_ & 3), h(w_ >> 2), stg(s_.out(w_)) {
         clear();
     }
     __device__ __forceinline__ void clear() {
@@ -512,7 +510,7 @@ struct Worker {
     template <int LD>
     __device__ __forceinline__ bool promote(bool live, float scale) {
         const uint32_t buf = from.slot;
-        if (!wait_bar(ctl, &sm.acc_full[buf], from.phase, WAIT_ACC_FULL)) return false;
+        if (!wait_bar(ctl, sm.acc_full + 8 * buf, from.phase, WAIT_ACC_FULL)) return false;
         from.next();
         tc_fence_after();
         auto release = [&]() {
@@ -520,9 +518,9 @@ struct Worker {
             __syncwarp();
             if (lane == 0) {
                 if (CG == 2)
-                    mbar_arrive_remote(mapa_shared(&sm.acc_empty[buf], 0));
+                    mbar_arrive_remote(map_to(sm.acc_empty + 8 * buf, 0));
                 else
-                    mbar_arrive(&sm.acc_empty[buf]);
+                    bar_arrive(sm.acc_empty + 8 * buf);
             }
         };
         if (live) {
@@ -574,7 +572,7 @@ struct Worker {
     __device__ __forceinline__ bool join(const Place& pl) {
         const int S = p.split;
         // the other parts have read what lay here before
-        if (tiles_done > 0 && !wait_bar_cluster(ctl, &sm.parts_out[w], (tiles_done - 1) & 1, WAIT_PARTS)) return false;
+        if (tiles_done > 0 && !wait_bar_cluster(ctl, sm.parts_out + 8 * w, (tiles_done - 1) & 1, WAIT_PARTS)) return false;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             float v[4];
@@ -583,18 +581,18 @@ struct Worker {
             *reinterpret_cast<float4*>(stg + lane * 256 + ((j ^ (lane & 15)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
         }
         __syncwarp();
-        if (lane < S) mbar_arrive_cluster(mapa_shared(&sm.parts_in[w], lane));
-        if (!wait_bar_cluster(ctl, &sm.parts_in[w], tiles_done & 1, WAIT_PARTS)) return false;
+        if (lane < S) mbar_arrive_cluster(map_to(sm.parts_in + 8 * w, lane));
+        if (!wait_bar_cluster(ctl, sm.parts_in + 8 * w, tiles_done & 1, WAIT_PARTS)) return false;
         ++tiles_done;
         const int units = 16 / S, row = pl.row0 + lane;
 #pragma unroll 1
         for (int i = 0; i < units; ++i) {
             const int j = ctl.rank * units + i;
-            const uint32_t at = (j ^ (lane & 15)) << 4;
+            const uint32_t stg_addr = smem_u32(stg), at = (j ^ (lane & 15)) << 4;
             float4 t[MAX_SPLIT];
 #pragma unroll
             for (int k = 0; k < MAX_SPLIT; ++k)
-                if (k < S) t[k] = ld_shared_cluster_f4(mapa_shared(stg + lane * 256, k) + at);
+                if (k < S) t[k] = ld_shared_cluster_f4(map_to(stg_addr + lane * 256, k) + at);
             float4 sum = t[0];
 #pragma unroll
             for (int k = 1; k < MAX_SPLIT; ++k)
@@ -626,7 +624,7 @@ struct Worker {
             }
         }
         __syncwarp();
-        if (lane < S) mbar_arrive_cluster(mapa_shared(&sm.parts_out[w], lane));
+        if (lane < S) mbar_arrive_cluster(map_to(sm.parts_out + 8 * w, lane));
         return true;
     }
 
@@ -700,28 +698,34 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
     Worker<KIND_MM, CG> wk(p, ctl, sm, tmem, w, lane);
     for (int u = first; u < p.n_tiles; u += step) {
         const auto pl = wk.place(u);
-        const int row = pl.row0 + lane;
-        const float* sa = p.sa + static_cast<long long>(row) * p.sa_rs;
-        const float* sb = p.sb + (wk.col_of(pl, 0) / 128) * p.sb_cs;
-        // a stage's scales are fetched two stages ahead and multiplied where
-        // they are used, so that no load is waited for
-        struct Scales {
-            float a, b;
-        };
-        auto scales_of = [&](int s) {
-            Scales v{0.f, 0.f};
-            if (pl.live && s < pl.x.hi) {
-                if (row < p.M) v.a = __ldg(sa + s * p.sa_cs);
-                v.b = __ldg(sb + s * p.sb_rs);
+        // A stage's two scales are fetched two stages ahead and multiplied
+        // where they are used, so that no load is waited for.  Rows below the
+        // last read its scales; past the last stage the last one's are read.
+        const float* pa = p.sa + min(pl.row0 + lane, p.M - 1) * p.sa_rs + pl.x.lo * p.sa_cs;
+        const float* pb = p.sb + min(wk.col_of(pl, 0), p.N - 1) / 128 * p.sb_cs + pl.x.lo * p.sb_rs;
+        int left = pl.x.hi - pl.x.lo;
+        float a0 = 0.f, b0 = 0.f, a1 = 0.f, b1 = 0.f;
+        auto advance = [&]() {
+            if (--left > 0) {
+                pa += p.sa_cs;
+                pb += p.sb_rs;
             }
-            return v;
         };
-        Scales cur = scales_of(pl.x.lo), next = scales_of(pl.x.lo + 1);
+        if (left > 0) {
+            a0 = __ldg(pa);
+            b0 = __ldg(pb);
+            advance();
+            a1 = __ldg(pa);
+            b1 = __ldg(pb);
+        }
         for (int s = pl.x.lo; s < pl.x.hi; ++s) {
-            const Scales after = scales_of(s + 2);
-            if (!wk.template promote<64>(pl.live, cur.a * cur.b)) return false;
-            cur = next;
-            next = after;
+            advance();
+            const float a2 = __ldg(pa), b2 = __ldg(pb);
+            if (!wk.template promote<64>(pl.live, a0 * b0)) return false;
+            a0 = a1;
+            b0 = b1;
+            a1 = a2;
+            b1 = b2;
         }
         if (!wk.epilogue(pl)) return false;
     }
@@ -781,10 +785,10 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[i] = next[i];
             fetch(s + 2);
-            if (!wait_bar(ctl, &sm.raw_full[rs.slot], rs.phase, WAIT_RAW)) return;
-            if (!wait_bar(ctl, &sm.done[st.slot], st.phase ^ 1, WAIT_A_EMPTY)) return;
-            const uint8_t* src = sm.raw(rs.slot) + r0 * 128 + seg * 16;
-            uint8_t* dst = sm.a(st.slot);
+            if (!wait_bar(ctl, sm.raw_full + 8 * rs.slot, rs.phase, WAIT_RAW)) return;
+            if (!wait_bar(ctl, sm.done + 8 * st.slot, st.phase ^ 1, WAIT_A_EMPTY)) return;
+            const uint8_t* src = sm.at(sm.raw(rs.slot)) + r0 * 128 + seg * 16;
+            uint8_t* dst = sm.at(sm.a(st.slot));
             uint4 c4 = *reinterpret_cast<const uint4*>(src);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -799,11 +803,11 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
             fence_proxy_async_shared();
             __syncwarp();
             if ((t & 31) == 0) {
-                mbar_arrive(&sm.raw_empty[rs.slot]);
+                bar_arrive(sm.raw_empty + 8 * rs.slot);
                 if (CG == 2)
-                    mbar_arrive_remote(mapa_shared(&sm.full[st.slot], 0));
+                    mbar_arrive_remote(map_to(sm.full + 8 * st.slot, 0));
                 else
-                    mbar_arrive(&sm.full[st.slot]);
+                    bar_arrive(sm.full + 8 * st.slot);
             }
         }
     }
@@ -821,23 +825,24 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
     const int rank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::STAGES; ++s) {
-            mbar_init(&sm.full[s], KIND == KIND_MM ? 1 : CG * 4);
-            mbar_init(&sm.done[s], 1);
-            mbar_init(&sm.b_full[s], 1);
+            bar_init(sm.full + 8 * s, KIND == KIND_MM ? 1 : CG * 4);
+            bar_init(sm.done + 8 * s, 1);
+            bar_init(sm.b_full + 8 * s, 1);
         }
         for (int s = 0; s < G::RAWS; ++s) {
-            mbar_init(&sm.raw_full[s], 1);
-            mbar_init(&sm.raw_empty[s], 4);
+            bar_init(sm.raw_full + 8 * s, 1);
+            bar_init(sm.raw_empty + 8 * s, 4);
         }
         for (int b = 0; b < G::ACCS; ++b) {
-            mbar_init(&sm.acc_full[b], 1);
-            mbar_init(&sm.acc_empty[b], CG * 8);
+            bar_init(sm.acc_full + 8 * b, 1);
+            bar_init(sm.acc_empty + 8 * b, CG * 8);
         }
         for (int i = 0; i < 8; ++i) {
-            mbar_init(&sm.parts_in[i], csize);
-            mbar_init(&sm.parts_out[i], csize);
+            bar_init(sm.parts_in + 8 * i, csize);
+            bar_init(sm.parts_out + 8 * i, csize);
         }
-        mbar_init(sm.final_bar, 1);
+        bar_init(sm.final_bar, 1);
+        bar_init(sm.final_bar + 8, 1);
         fence_mbar_init();
         uint32_t e = *reinterpret_cast<volatile uint32_t*>(&p.ws->epoch) + 1u;
         *sm.epoch_slot = e == 0u ? 1u : e;
@@ -861,8 +866,9 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
         } else if (KIND == KIND_WG && warp == 2) {
             if (lane == 0) run_tma<KIND, CG>(p, ctl, sm, 1, first, step);
         } else if (warp == 1) {
-            if (CG == 1 || rank == 0) run_mma<KIND, CG>(p, ctl, sm, tmem, first, step);
+            if (CG == 1 || rank == 0) run_mma<KIND, CG>(p, ctl, sm, tmem, 0, first, step);
         }
+        if (G::ISSUERS == 2 && warp == 3) run_mma<KIND, CG>(p, ctl, sm, tmem, 1, first, step);
         __syncwarp();
     } else if (warp < 12) {
         reg_inc<G::REGS_PROMOTE>();
