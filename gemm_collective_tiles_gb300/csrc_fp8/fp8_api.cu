@@ -38,11 +38,14 @@ int cuda_fail(const char* what, int code) {
     return IRIS_ECUDA;
 }
 
-// per device: SMs and how many clusters of a kernel run at once, by kind and
-// log2 of the cluster's CTAs (a pair for CG 2, the parts of a split for CG 1)
+// The kernels: a pair's tile, a CTA's, and a CTA's with few rows.
+enum Variant { PAIR = 0, CTA = 1, FEW = 2 };
+
+// per device: SMs and how many clusters of a kernel run at once, by kind,
+// variant and log2 of the cluster's CTAs (a pair, or the parts of a split)
 struct DeviceInfo {
     int sms;
-    int pairs[2], clusters[2][4];
+    int clusters[2][3][4];
     bool done;
 };
 DeviceInfo g_dev[64];
@@ -65,28 +68,28 @@ cudaLaunchConfig_t launch_config(int grid, int threads, size_t smem, int cluster
     return lc;
 }
 
-template <int KIND, int CG>
+template <int KIND, int CG, int ROWS>
 int setup_kernel(DeviceInfo& d) {
-    using G = Geo<KIND, CG>;
-    cudaError_t e = cudaFuncSetAttribute(block_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    using G = Geo<KIND, CG, ROWS>;
+    cudaError_t e = cudaFuncSetAttribute(block_gemm_kernel<KIND, CG, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(G::BYTES));
     if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (8-bit products)", static_cast<int>(e));
     // the warpgroups' register shares must fit in what the launch allots, or
     // a warpgroup would wait for registers that never come
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, block_gemm_kernel<KIND, CG>);
+    e = cudaFuncGetAttributes(&fa, block_gemm_kernel<KIND, CG, ROWS>);
     if (e != cudaSuccess) return cuda_fail("cudaFuncGetAttributes", static_cast<int>(e));
     if (fa.numRegs * G::THREADS < G::REGS_TOTAL) return cuda_fail("register shares of the 8-bit products", fa.numRegs);
     for (int lg = 0; lg < 4; ++lg) {
         if (CG == 2 && lg != 1) continue;
-        int* n = CG == 2 ? &d.pairs[KIND] : &d.clusters[KIND][lg];
+        int* n = &d.clusters[KIND][CG == 2 ? PAIR : ROWS == 64 ? FEW : CTA][lg];
         if (lg == 0) {
             *n = d.sms;
             continue;
         }
         cudaLaunchAttribute attr;
         const cudaLaunchConfig_t lc = launch_config(d.sms >> lg << lg, G::THREADS, G::BYTES, 1 << lg, nullptr, &attr);
-        e = cudaOccupancyMaxActiveClusters(n, block_gemm_kernel<KIND, CG>, &lc);
+        e = cudaOccupancyMaxActiveClusters(n, block_gemm_kernel<KIND, CG, ROWS>, &lc);
         if (e != cudaSuccess || *n < 1) return cuda_fail("cudaOccupancyMaxActiveClusters", static_cast<int>(e));
     }
     return IRIS_OK;
@@ -100,8 +103,9 @@ int device_info(DeviceInfo* out) {
     if (!d.done) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return IRIS_ECUDA;
         int rc;
-        if ((rc = setup_kernel<KIND_MM, 1>(d)) || (rc = setup_kernel<KIND_MM, 2>(d)) || (rc = setup_kernel<KIND_WG, 1>(d)) ||
-            (rc = setup_kernel<KIND_WG, 2>(d)))
+        if ((rc = setup_kernel<KIND_MM, 1, 128>(d)) || (rc = setup_kernel<KIND_MM, 2, 128>(d)) ||
+            (rc = setup_kernel<KIND_MM, 1, 64>(d)) || (rc = setup_kernel<KIND_WG, 1, 128>(d)) ||
+            (rc = setup_kernel<KIND_WG, 2, 128>(d)))
             return rc;
         if (!g_encode) {
             void* fn = nullptr;
@@ -229,15 +233,16 @@ int make_store_map(CUtensorMap* m, iris_dtype t, const void* data, int64_t N, in
 
 // Tile, split and workspace of one product (rows x cols over depth).
 struct Plan {
+    Variant variant;
     int cg, split, part_stages, stages, m_blocks, n_blocks, group_m, grid;
     size_t copy_a, copy_b, total;  // workspace offsets
 };
 
 // Estimated time in us of a variant: `slots` clusters run at once, each tile
 // takes `part` stages and an epilogue.  Constants measured on GB300.
-double estimate(bool wg, int cg, int slots, int64_t tiles, int64_t part, int split) {
-    const double stage = wg ? (cg == 2 ? 0.50 : 0.35) : (cg == 2 ? 0.52 : 0.35);
-    const double per_tile = part * stage + (cg == 2 ? 1.5 : 1.0) + (split > 1 ? 1.5 : 0.0);
+double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split) {
+    const double stage = wg ? (v == PAIR ? 0.50 : 0.35) : (v == PAIR ? 0.47 : v == CTA ? 0.35 : 0.22);
+    const double per_tile = part * stage + (v == PAIR ? 1.5 : 1.0) + (split > 1 ? 2.0 : 0.0);
     return 4.0 + cdiv(tiles, slots) * per_tile;
 }
 
@@ -262,14 +267,16 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
         for (int lg = 0; lg < (cg == 2 ? 1 : 4); ++lg) {
             const int split = 1 << lg;
             const int64_t part = cdiv(stages, split);
-            const int slots = std::min(cg == 2 ? d.pairs[wg] : d.clusters[wg][lg], grid / (cg * split));
+            const Variant v = cg == 2 ? PAIR : !wg && rows <= 64 ? FEW : CTA;
+            const int slots = std::min(d.clusters[wg][v][cg == 2 ? 1 : lg], grid / (cg * split));
             if (slots < 1) continue;
             // every part has stages (an empty one, where the config asks for it, adds zeros)
             if (cfg->k_split ? split != cfg->k_split : part * (split - 1) >= stages) continue;
-            const double t = estimate(wg, cg, slots, tiles, part, split);
+            const double t = estimate(wg, v, slots, tiles, part, split);
             if (pl.cg == 0 || t < best) {
                 best = t;
                 pl.cg = cg;
+                pl.variant = v;
                 pl.split = split;
                 pl.part_stages = static_cast<int>(part);
                 pl.m_blocks = static_cast<int>(mb);
@@ -287,12 +294,12 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
     return IRIS_OK;
 }
 
-template <int KIND, int CG>
+template <int KIND, int CG, int ROWS>
 int launch_gemm(const GemmParams& p, int grid, cudaStream_t stream) {
-    using G = Geo<KIND, CG>;
+    using G = Geo<KIND, CG, ROWS>;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t lc = launch_config(grid, G::THREADS, G::BYTES, CG * p.split, stream, &attr);
-    const cudaError_t e = cudaLaunchKernelEx(&lc, block_gemm_kernel<KIND, CG>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&lc, block_gemm_kernel<KIND, CG, ROWS>, p);
     return e == cudaSuccess ? IRIS_OK : cuda_fail("kernel launch (8-bit product)", static_cast<int>(e));
 }
 
@@ -391,8 +398,10 @@ int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b2
     if (direct && (rc = make_store_map(&p.tmC, out_dtype, out->data, cols, rows,
                                        rows == 1 ? packed_pitch(cols, dtype_size(out_dtype)) : out->row_stride)))
         return rc;
-    if (wg) return pl.cg == 2 ? launch_gemm<KIND_WG, 2>(p, pl.grid, stream) : launch_gemm<KIND_WG, 1>(p, pl.grid, stream);
-    return pl.cg == 2 ? launch_gemm<KIND_MM, 2>(p, pl.grid, stream) : launch_gemm<KIND_MM, 1>(p, pl.grid, stream);
+    if (wg) return pl.cg == 2 ? launch_gemm<KIND_WG, 2, 128>(p, pl.grid, stream) : launch_gemm<KIND_WG, 1, 128>(p, pl.grid, stream);
+    return pl.variant == PAIR  ? launch_gemm<KIND_MM, 2, 128>(p, pl.grid, stream)
+           : pl.variant == CTA ? launch_gemm<KIND_MM, 1, 128>(p, pl.grid, stream)
+                               : launch_gemm<KIND_MM, 1, 64>(p, pl.grid, stream);
 }
 
 int check_matmul(const iris_b200_mat* A, const iris_b200_mat* B, const iris_b200_mat* out, iris_dtype out_dtype,
@@ -431,7 +440,7 @@ int iris_b200_quantize_fp8(const iris_b200_mat* x, iris_dtype x_dtype, const iri
     if ((rc = check_in(x, M, K, dtype_size(x_dtype))) || (rc = check_out(codes, M, K, 1)) || (rc = check_out(scales, sr, kb, 4)))
         return rc;
     if (M == 0 || K == 0) return IRIS_OK;
-    const int64_t blocks = kb * cdiv(M, Q_ROWS);
+    const int64_t blocks = kb * cdiv(M, block_rows == 1 ? Q_ROWS : Q_TILE);
     if (blocks > 0x7FFFFFFF) return IRIS_EINVAL;
     QuantParams q;
     q.x = x->data;
@@ -454,10 +463,11 @@ int iris_b200_quantize_fp8(const iris_b200_mat* x, iris_dtype x_dtype, const iri
     // nothing that f16 can hold is lost to the bound
     q.pmin = x_dtype == IRIS_F16 ? (q.e5m2 ? -8 : -15) : -100;
     const int e = dtype_size(x_dtype);
-    // 16-byte reads and 8-byte writes where every row starts on them
+    // 16-byte reads and writes where every row starts on them (16384 x 4096
+    // bf16: 31 us; the same rows one element off: 60 us)
     const bool vec = (x->col_stride == 1 || K == 1) && (codes->col_stride == 1 || K == 1) && aligned16(x->data) &&
-                     (M == 1 || x->row_stride * e % 16 == 0) && reinterpret_cast<uintptr_t>(codes->data) % 8 == 0 &&
-                     (M == 1 || codes->row_stride % 8 == 0);
+                     (M == 1 || x->row_stride * e % 16 == 0) && aligned16(codes->data) &&
+                     (M == 1 || codes->row_stride % 16 == 0);
     const bool tile = block_rows == 128;
     const unsigned grid = static_cast<unsigned>(blocks);
     if (x_dtype == IRIS_F32) launch_quant<T_F32>(q, vec, tile, grid, stream);

@@ -239,6 +239,12 @@ __device__ __forceinline__ unsigned long long fma_f32x2(unsigned long long a, un
     return d;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // ---------------------------------------------------------------- conversions
 // two fp32 -> two 8-bit codes (lo in the low byte), to nearest even; NaN gives
 // the type's NaN, finite values beyond the largest code give that code

@@ -43,14 +43,14 @@ __device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi) {
     }
 }
 
-// largest finite magnitude so far and |v|
+constexpr float INF = __builtin_huge_valf();
+// the larger of m and |v|, over finite v
 __device__ __forceinline__ float amax_finite(float m, float v) {
-    const float a = fabsf(v);
-    return a < __int_as_float(0x7F800000) ? fmaxf(m, a) : m;
+    return fabsf(v) < INF ? fmaxf(m, fabsf(v)) : m;
 }
 // an infinity has no code of its own: it becomes NaN, like a NaN
 __device__ __forceinline__ float finite_or_nan(float v) {
-    return fabsf(v) < __int_as_float(0x7F800000) ? v : __int_as_float(0x7FFFFFFF);
+    return fabsf(v) < INF ? v : __int_as_float(0x7FFFFFFF);
 }
 
 // Scale and reciprocal of a block.  Power of two: FMAX is 1.75 * 2^n, so the
@@ -72,14 +72,15 @@ __device__ __forceinline__ void block_scale(const QuantParams& p, float amax, fl
 }
 
 constexpr int Q_THREADS = 256;
-constexpr int Q_ROWS = 128;  // rows per CTA
-constexpr int Q_PER = Q_ROWS / (Q_THREADS / 16);  // rows per thread
+constexpr int Q_TILE = 128;  // rows of a tile of scales
+constexpr int Q_ROWS = 64;   // rows per CTA with a scale per row
 
 // largest value over the CTA (every thread gets it)
 __device__ __forceinline__ float cta_max(float v) {
     __shared__ float part[Q_THREADS / 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    __syncthreads();  // the last round's values have been read
     if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
     v = part[0];
@@ -88,157 +89,223 @@ __device__ __forceinline__ float cta_max(float v) {
     return v;
 }
 
-// One CTA quantises 128 rows x one 128-column block; 16 lanes share a row,
-// 8 consecutive elements each, and a thread holds its 8 rows in registers, so
-// x is read once and every load is in flight before the first reduction.
+// One CTA quantises R rows x one 128-column block; 8 lanes share a row, 16
+// consecutive elements each, and a thread holds its rows in registers, so x is
+// read once and every load is in flight before the first reduction.  Bound by
+// memory, with instructions close behind: 16-bit maxima are taken on pairs, as
+// integers (magnitudes order like their bits), which keeps them to about six
+// per element.
 // TILE: one scale for the whole 128 x 128 block, else one per row.
-// Needs x rows on 16 bytes and code rows on 8 bytes, both with unit stride.
+// Needs rows of x and codes on 16 bytes, both with unit stride.
 template <int T, bool TILE>
-__global__ void __launch_bounds__(Q_THREADS) quantize_vec_kernel(const QuantParams p) {
-    const int lane16 = threadIdx.x & 15, grp = threadIdx.x >> 4;
-    const long long kb = blockIdx.x % p.kblocks, rb = blockIdx.x / p.kblocks;
-    const long long col = kb * 128 + lane16 * 8, row0 = rb * Q_ROWS;
-    const int left = static_cast<int>(max(0ll, min(8ll, p.K - col)));  // elements of this lane that exist
-    constexpr int W = T == T_F32 ? 2 : 1;                               // 16-byte words per 8 elements
-    uint4 raw[Q_PER][W];
-    float m[Q_PER];
+__global__ void __launch_bounds__(Q_THREADS, TILE ? 3 : 4) quantize_vec_kernel(const __grid_constant__ QuantParams p) {
+    constexpr int GROUPS = Q_THREADS / 8, R = TILE ? Q_TILE : Q_ROWS, PER = R / GROUPS;
+    constexpr int E = T == T_F32 ? 4 : 2, W = E;  // bytes per element; 16-byte words per 16 elements
+    const int lane8 = threadIdx.x & 7, grp = threadIdx.x >> 3;
+    const unsigned kb = blockIdx.x % p.kblocks, rb = blockIdx.x / p.kblocks;
+    const long long col = static_cast<long long>(kb) * 128 + lane8 * 16;
+    const long long row = static_cast<long long>(rb) * R + grp;         // this thread's first row
+    const int left = static_cast<int>(max(0ll, min(16ll, p.K - col)));  // elements of this lane that exist
+    const int rows = static_cast<int>(max(0ll, min(static_cast<long long>(PER), (p.M - row + GROUPS - 1) / GROUPS)));
+    const char* src = static_cast<const char*>(p.x) + (row * p.x_rs + col) * E;
+    const long long step = GROUPS * p.x_rs * E;
+    uint32_t raw[PER][4 * W];
 #pragma unroll
-    for (int i = 0; i < Q_PER; ++i) {
-        const long long r = row0 + grp + i * (Q_THREADS / 16);
+    for (int i = 0; i < PER; ++i) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) raw[i][w] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.M && left > 0) {
-            const char* src = static_cast<const char*>(p.x) + (r * p.x_rs + col) * (T == T_F32 ? 4 : 2);
-            if (left == 8) {
+        for (int w = 0; w < 4 * W; ++w) raw[i][w] = 0u;
+        if (i < rows && left > 0) {
+            const char* at = src + i * step;
+            if (left == 16) {
 #pragma unroll
-                for (int w = 0; w < W; ++w) raw[i][w] = __ldg(reinterpret_cast<const uint4*>(src) + w);
+                for (int w = 0; w < W; ++w) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4*>(at) + w);
+                    raw[i][4 * w] = q.x;
+                    raw[i][4 * w + 1] = q.y;
+                    raw[i][4 * w + 2] = q.z;
+                    raw[i][4 * w + 3] = q.w;
+                }
             } else {  // ragged last block: element by element
-                uint32_t tmp[4 * W];
 #pragma unroll
-                for (int w = 0; w < 4 * W; ++w) tmp[w] = 0u;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 16; ++e)
                     if (e < left) {
-                        if (T == T_F32)
-                            tmp[e] = reinterpret_cast<const uint32_t*>(src)[e];
+                        if constexpr (T == T_F32)
+                            raw[i][e] = reinterpret_cast<const uint32_t*>(at)[e];
                         else
-                            tmp[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[e]) << (16 * (e & 1));
+                            raw[i][e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[e]) << (16 * (e & 1));
                     }
-#pragma unroll
-                for (int w = 0; w < W; ++w) raw[i][w] = make_uint4(tmp[4 * w], tmp[4 * w + 1], tmp[4 * w + 2], tmp[4 * w + 3]);
             }
         }
     }
-    auto values = [&](int i, float (&v)[8]) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const uint32_t q[4] = {raw[i][w].x, raw[i][w].y, raw[i][w].z, raw[i][w].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (T == T_F32)
-                    v[4 * w + e] = __uint_as_float(q[e]);
-                else
-                    unpack16<T>(q[e], v[2 * e], v[2 * e + 1]);
-            }
+    auto value = [&](int i, int e) {
+        if constexpr (T == T_F32) {
+            return __uint_as_float(raw[i][e]);
+        } else {
+            float lo, hi;
+            unpack16<T>(raw[i][e / 2], lo, hi);
+            return (e & 1) ? hi : lo;
         }
     };
+    // largest magnitudes.  f32: the hardware maximum passes over NaN.  16-bit:
+    // as integers, infinity and NaN are the largest; either way a block that
+    // is not all finite shows as one at least INF or NaN, and is done again.
+    float m[PER];
 #pragma unroll
-    for (int i = 0; i < Q_PER; ++i) {
-        float v[8];
-        values(i, v);
-        m[i] = 0.f;
+    for (int i = 0; i < PER; ++i) {
+        if constexpr (T == T_F32) {
+            m[i] = fabsf(value(i, 0));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m[i] = amax_finite(m[i], v[e]);
+            for (int e = 1; e < 16; ++e) m[i] = fmaxf(m[i], fabsf(value(i, e)));
+        } else {
+            uint32_t two = raw[i][0] & 0x7FFF7FFFu;
+#pragma unroll
+            for (int w = 1; w < 8; ++w) two = max_u16x2(two, raw[i][w] & 0x7FFF7FFFu);
+            two = max(two & 0xFFFFu, two >> 16);
+            m[i] = T == T_F16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(two))) : __uint_as_float(two << 16);
+        }
     }
-    if (TILE) {
+    auto reduce = [&]() {
+        if (TILE) {
 #pragma unroll
-        for (int i = 1; i < Q_PER; ++i) m[0] = fmaxf(m[0], m[i]);
-        m[0] = cta_max(m[0]);
+            for (int i = 1; i < PER; ++i) m[0] = fmaxf(m[0], m[i]);
+            m[0] = cta_max(m[0]);
+        } else {
 #pragma unroll
-        for (int i = 1; i < Q_PER; ++i) m[i] = m[0];
-    } else {
+            for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
+                for (int i = 0; i < PER; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+        }
+    };
+    bool odd = false;  // something is not finite
 #pragma unroll
-            for (int i = 0; i < Q_PER; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], o));
+    for (int i = 0; i < PER; ++i) odd = odd || !(m[i] < INF);
+    odd = TILE ? __syncthreads_or(odd) : __any_sync(0xFFFFFFFFu, odd);
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            m[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m[i] = amax_finite(m[i], value(i, e));
+        }
     }
+    reduce();
     float scale, inv;
     if (TILE) {
         block_scale(p, m[0], scale, inv);
         if (threadIdx.x == 0) p.scales[rb * p.s_rs + kb * p.s_cs] = scale;
     }
+    uint8_t* dst = p.codes + row * p.c_rs + col;
 #pragma unroll
-    for (int i = 0; i < Q_PER; ++i) {
-        const long long r = row0 + grp + i * (Q_THREADS / 16);
-        if (r >= p.M) continue;
+    for (int i = 0; i < PER; ++i) {
+        if (i >= rows) break;
         if (!TILE) {
             block_scale(p, m[i], scale, inv);
-            if (lane16 == 0) p.scales[r * p.s_rs + kb * p.s_cs] = scale;
+            if (lane8 == 0) p.scales[(row + GROUPS * i) * p.s_rs + kb * p.s_cs] = scale;
         }
         if (left <= 0) continue;
-        float v[8];
-        values(i, v);
+        uint32_t out[4];
+        auto encode = [&](auto fix, int e5m2) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = finite_or_nan(v[e]) * inv;
-        const uint32_t lo = cvt_f8x2(v[0], v[1], p.e5m2) | cvt_f8x2(v[2], v[3], p.e5m2) << 16;
-        const uint32_t hi = cvt_f8x2(v[4], v[5], p.e5m2) | cvt_f8x2(v[6], v[7], p.e5m2) << 16;
-        uint8_t* dst = p.codes + r * p.c_rs + col;
-        if (left == 8) {
-            *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+            for (int w = 0; w < 4; ++w)
+                out[w] = cvt_f8x2(fix(value(i, 4 * w)) * inv, fix(value(i, 4 * w + 1)) * inv, e5m2) |
+                         cvt_f8x2(fix(value(i, 4 * w + 2)) * inv, fix(value(i, 4 * w + 3)) * inv, e5m2) << 16;
+        };
+        if (odd)
+            encode([](float v) { return finite_or_nan(v); }, p.e5m2);
+        else if (p.e5m2)
+            encode([](float v) { return v; }, 1);
+        else
+            encode([](float v) { return v; }, 0);
+        uint8_t* to = dst + GROUPS * i * p.c_rs;
+        if (left == 16) {
+            *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < left) dst[e] = static_cast<uint8_t>((e < 4 ? lo : hi) >> (8 * (e & 3)));
+            for (int e = 0; e < 16; ++e)
+                if (e < left) to[e] = static_cast<uint8_t>(out[e / 4] >> (8 * (e & 3)));
         }
     }
 }
 
-// Any strides and alignment: a warp takes a row's 128 columns, four elements
-// 32 apart per lane, so unit-stride rows are still read and written in whole
-// sectors.  TILE: the CTA's 8 warps walk the tile's 128 rows twice (largest
-// value, then codes; the second read comes from the caches).
+// Any strides and alignment: a warp takes rows of 128 columns, four elements 32
+// apart per lane, so unit-stride rows are still read and written in whole
+// sectors; four rows at a time, so that 16 loads per lane are in flight.
+// TILE: the CTA's warps walk the tile's rows twice (largest value, then codes;
+// the second read comes from the caches).
 template <int T, bool TILE>
-__global__ void __launch_bounds__(Q_THREADS) quantize_any_kernel(const QuantParams p) {
-    constexpr int WARPS = Q_THREADS / 32;
+__global__ void __launch_bounds__(Q_THREADS) quantize_any_kernel(const __grid_constant__ QuantParams p) {
+    constexpr int R = TILE ? Q_TILE : Q_ROWS, WARPS = Q_THREADS / 32, PER = R / WARPS, U = 4;
+    constexpr int E = T == T_F32 ? 4 : 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const long long kb = blockIdx.x % p.kblocks, rb = blockIdx.x / p.kblocks;
-    const long long col0 = kb * 128 + lane, row0 = rb * Q_ROWS;
+    const unsigned kb = blockIdx.x % p.kblocks, rb = blockIdx.x / p.kblocks;
+    const long long col = static_cast<long long>(kb) * 128 + lane, row = static_cast<long long>(rb) * R + warp;
+    const char* const x0 = static_cast<const char*>(p.x) + (row * p.x_rs + col * p.x_cs) * E;
+    uint8_t* const c0 = p.codes + row * p.c_rs + col * p.c_cs;
+    const long long x_row = p.x_rs * WARPS * E, x_col = p.x_cs * 32 * E, c_row = p.c_rs * WARPS, c_col = p.c_cs * 32;
+    const int rows = static_cast<int>(max(0ll, min(static_cast<long long>(PER), (p.M - row + WARPS - 1) / WARPS)));
+    bool there[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) there[e] = col + 32 * e < p.K;
+    auto load = [&](int i, float (&v)[U][4]) {  // rows i .. i + U - 1 of this warp
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const char* at = x0 + (i + j) * x_row;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[j][e] = i + j < rows && there[e] ? load_elem<T>(at, 0) : 0.f;
+                at += x_col;
+            }
+        }
+    };
     float scale = 0.f, inv = 0.f;
     if (TILE) {
         float m = 0.f;
-        for (int i = warp; i < Q_ROWS; i += WARPS) {
-            const long long r = row0 + i;
-            if (r >= p.M) break;
+#pragma unroll 1
+        for (int i = 0; i < PER; i += U) {
+            float v[U][4];
+            load(i, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (col0 + 32 * e < p.K) m = amax_finite(m, load_elem<T>(p.x, r * p.x_rs + (col0 + 32 * e) * p.x_cs));
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m = amax_finite(m, v[j][e]);
         }
         m = cta_max(m);
         block_scale(p, m, scale, inv);
         if (threadIdx.x == 0) p.scales[rb * p.s_rs + kb * p.s_cs] = scale;
     }
-#pragma unroll 4
-    for (int i = warp; i < Q_ROWS; i += WARPS) {
-        const long long r = row0 + i;
-        if (r >= p.M) break;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = col0 + 32 * e < p.K ? load_elem<T>(p.x, r * p.x_rs + (col0 + 32 * e) * p.x_cs) : 0.f;
+#pragma unroll 1
+    for (int i = 0; i < rows; i += U) {
+        float v[U][4];
+        load(i, v);
+        float m[U];
         if (!TILE) {
-            float m = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m = amax_finite(m, v[e]);
+            for (int j = 0; j < U; ++j) {
+                m[j] = 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            block_scale(p, m, scale, inv);
-            if (lane == 0) p.scales[r * p.s_rs + kb * p.s_cs] = scale;
+                for (int e = 0; e < 4; ++e) m[j] = amax_finite(m[j], v[j][e]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < U; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], o));
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (col0 + 32 * e < p.K)
-                p.codes[r * p.c_rs + (col0 + 32 * e) * p.c_cs] =
-                    static_cast<uint8_t>(cvt_f8x2(finite_or_nan(v[e]) * inv, 0.f, p.e5m2));
+        for (int j = 0; j < U; ++j) {
+            if (i + j >= rows) break;
+            if (!TILE) {
+                block_scale(p, m[j], scale, inv);
+                if (lane == 0) p.scales[(row + (i + j) * WARPS) * p.s_rs + kb * p.s_cs] = scale;
+            }
+            uint8_t* to = c0 + (i + j) * c_row;
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const uint32_t two = cvt_f8x2(finite_or_nan(v[j][e]) * inv, finite_or_nan(v[j][e + 1]) * inv, p.e5m2);
+                if (there[e]) to[0] = static_cast<uint8_t>(two);
+                if (there[e + 1]) to[c_col] = static_cast<uint8_t>(two >> 8);
+                to += 2 * c_col;
+            }
+        }
     }
 }
 
