@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import build as _build
 
@@ -94,12 +95,12 @@ class iris_b200_heap(ctypes.Structure):
     ]
 
 
-class iris_b200_mat(ctypes.Structure):
-    _fields_ = [
-        ("data", ctypes.c_void_p),
-        ("row_stride", ctypes.c_int64),
-        ("col_stride", ctypes.c_int64),
-    ]
+# The argument structs of the 8-bit float ops, packed by one call each (a
+# ctypes.Structure per matrix would cost more than the launch): every matrix is
+# (data, row_stride, col_stride).
+pack_quantize_fp8 = struct.Struct("@11q4i").pack     # x, codes, scales; M, K; x_dtype, type, block_rows, pow2
+pack_matmul_fp8 = struct.Struct("@19q4i").pack       # A, a_scales, B, b_scales, out; bias; M, N, K; 4 types
+pack_weight_grad_fp8 = struct.Struct("@15q4i").pack  # X, x_scales, dY, out; M, N, K; 3 types, 0
 
 
 _lib = None
@@ -108,7 +109,7 @@ _lib = None
 def _declare(lib):
     P = ctypes.POINTER
     i64, sz, vp, ci = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int
-    cfgp, heapp, matp = P(iris_b200_config), P(iris_b200_heap), P(iris_b200_mat)
+    cfgp, heapp, args = P(iris_b200_config), P(iris_b200_heap), ctypes.c_char_p
     sig = {
         "iris_b200_workspace_size": (ci, [ci, i64, i64, i64, ci, ci, cfgp, P(sz)]),
         "iris_b200_all_gather_matmul": (ci, [heapp, sz, sz, sz, sz, sz, i64, i64, i64, ci, cfgp, vp, sz, vp]),
@@ -122,14 +123,11 @@ def _declare(lib):
             ci, [vp, vp, vp, i64, i64, i64, ci, ci, heapp, sz, sz, i64, ci, cfgp, vp, sz, vp, sz, vp, vp]),
         "iris_b200_sm_partition_streams": (ci, [ci, P(vp), P(vp), P(ci), P(ci)]),
         "iris_b200_sm_partition_release": (ci, []),
-        "iris_b200_quantize_fp8": (ci, [matp, ci, matp, ci, matp, i64, i64, ci, ci, vp]),
-        "iris_b200_matmul_fp8_workspace_size": (ci, [matp, matp, matp, ci, i64, i64, i64, cfgp, P(sz)]),
-        "iris_b200_matmul_fp8": (
-            ci, [matp, ci, matp, matp, ci, matp, vp, ci, matp, ci, i64, i64, i64, cfgp, vp, sz, vp]),
-        "iris_b200_weight_grad_fp8_workspace_size": (
-            ci, [matp, matp, ci, matp, ci, i64, i64, i64, cfgp, P(sz)]),
-        "iris_b200_weight_grad_fp8": (
-            ci, [matp, ci, matp, matp, ci, matp, ci, i64, i64, i64, cfgp, vp, sz, vp]),
+        "iris_b200_quantize_fp8": (ci, [args, vp]),
+        "iris_b200_matmul_fp8_workspace_size": (ci, [args, cfgp, P(sz)]),
+        "iris_b200_matmul_fp8": (ci, [args, cfgp, vp, sz, vp]),
+        "iris_b200_weight_grad_fp8_workspace_size": (ci, [args, cfgp, P(sz)]),
+        "iris_b200_weight_grad_fp8": (ci, [args, cfgp, vp, sz, vp]),
         "iris_b200_query_status": (ci, [vp, vp, P(ci), P(ci), P(ci)]),
         "iris_b200_strerror": (ctypes.c_char_p, [ci]),
         "iris_b200_num_sms": (ci, [P(ci)]),

@@ -125,16 +125,16 @@ int device_info(DeviceInfo* out) {
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-int dtype_size(iris_dtype t) { return t == IRIS_F32 ? 4 : 2; }
+int dtype_size(int t) { return t == IRIS_F32 ? 4 : 2; }
 
 bool dims_ok(int64_t M, int64_t N, int64_t K) {
     // 128-rounded sizes stay below 2^31
     const int64_t lim = (int64_t(1) << 31) - 512;
     return M >= 0 && N >= 0 && K >= 0 && M <= lim && N <= lim && K <= lim;
 }
-bool dtype16(iris_dtype t) { return t == IRIS_F16 || t == IRIS_BF16; }
-bool dtype_ok(iris_dtype t) { return dtype16(t) || t == IRIS_F32; }
-bool fp8_ok(iris_fp8 t) { return t == IRIS_E4M3 || t == IRIS_E5M2; }
+bool dtype16(int t) { return t == IRIS_F16 || t == IRIS_BF16; }
+bool dtype_ok(int t) { return dtype16(t) || t == IRIS_F32; }
+bool fp8_ok(int t) { return t == IRIS_E4M3 || t == IRIS_E5M2; }
 
 // a matrix that is read: pointer (unless empty), no negative stride, element alignment
 int check_in(const iris_b200_mat* m, int64_t rows, int64_t cols, int elem) {
@@ -218,7 +218,7 @@ int make_map_groups(CUtensorMap* m, CUtensorMapDataType dt, const Operand& o, ui
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (groups of columns)", static_cast<int>(r));
 }
 // out {n, row} with a box of 128 bytes x 32 rows
-int make_store_map(CUtensorMap* m, iris_dtype t, const void* data, int64_t N, int64_t M, int64_t pitch) {
+int make_store_map(CUtensorMap* m, int t, const void* data, int64_t N, int64_t M, int64_t pitch) {
     const int elem = dtype_size(t);
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * elem};
@@ -306,9 +306,9 @@ int launch_gemm(const GemmParams& p, int grid, cudaStream_t stream) {
 // out (rows x cols) of one product: everything that both kinds share.
 // `wg`: operand a is X (depth x rows codes), b is dY (depth x cols, 16-bit);
 // else a is A (rows x depth codes), b is B (depth x cols codes).
-int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b200_mat* sa, const iris_b200_mat* mb,
-                int b_type /* fp8 type or 16-bit dtype */, const iris_b200_mat* sb, const void* bias, iris_dtype bias_dtype,
-                const iris_b200_mat* out, iris_dtype out_dtype, int64_t rows, int64_t cols, int64_t depth,
+int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_mat* sa, const iris_b200_mat* mb,
+                int b_type /* fp8 type or 16-bit dtype */, const iris_b200_mat* sb, const void* bias, int bias_dtype,
+                const iris_b200_mat* out, int out_dtype, int64_t rows, int64_t cols, int64_t depth,
                 const iris_b200_config* cfg, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
     int rc;
     if (rows == 0 || cols == 0) {
@@ -404,19 +404,39 @@ int run_product(bool wg, const iris_b200_mat* ma, iris_fp8 a_type, const iris_b2
                                : launch_gemm<KIND_MM, 1, 64>(p, pl.grid, stream);
 }
 
-int check_matmul(const iris_b200_mat* A, const iris_b200_mat* B, const iris_b200_mat* out, iris_dtype out_dtype,
-                 int64_t M, int64_t N, int64_t K) {
+int check_matmul(const iris_b200_matmul_fp8_args* g) {
     int rc;
-    if (!dims_ok(M, N, K) || !dtype_ok(out_dtype)) return IRIS_EINVAL;
-    if ((rc = check_in(A, M, K, 1)) || (rc = check_in(B, K, N, 1))) return rc;
-    return check_out(out, M, N, dtype_size(out_dtype));
+    if (!g || !dims_ok(g->M, g->N, g->K) || !dtype_ok(g->out_dtype) || !fp8_ok(g->a_type) || !fp8_ok(g->b_type)) return IRIS_EINVAL;
+    if (g->bias && !dtype_ok(g->bias_dtype)) return IRIS_EINVAL;
+    const int64_t kb = cdiv(g->K, 128);
+    if ((rc = check_in(&g->A, g->M, g->K, 1)) || (rc = check_in(&g->B, g->K, g->N, 1)) ||
+        (rc = check_in(&g->a_scales, g->M, kb, 4)) || (rc = check_in(&g->b_scales, kb, cdiv(g->N, 128), 4)))
+        return rc;
+    if (g->bias && reinterpret_cast<uintptr_t>(g->bias) % dtype_size(g->bias_dtype)) return IRIS_EALIGN;
+    return check_out(&g->out, g->M, g->N, dtype_size(g->out_dtype));
 }
-int check_wgrad(const iris_b200_mat* X, const iris_b200_mat* dY, iris_dtype dtype, const iris_b200_mat* out,
-                iris_dtype out_dtype, int64_t M, int64_t N, int64_t K) {
+int check_wgrad(const iris_b200_weight_grad_fp8_args* g) {
     int rc;
-    if (!dims_ok(M, N, K) || !dtype16(dtype) || !dtype_ok(out_dtype)) return IRIS_EINVAL;
-    if ((rc = check_in(X, M, K, 1)) || (rc = check_in(dY, M, N, 2))) return rc;
-    return check_out(out, K, N, dtype_size(out_dtype));
+    if (!g || !dims_ok(g->M, g->N, g->K) || !dtype16(g->dy_dtype) || !dtype_ok(g->out_dtype) || !fp8_ok(g->x_type) || g->reserved)
+        return IRIS_EINVAL;
+    if ((rc = check_in(&g->X, g->M, g->K, 1)) || (rc = check_in(&g->dY, g->M, g->N, 2)) ||
+        (rc = check_in(&g->x_scales, g->M, cdiv(g->K, 128), 4)))
+        return rc;
+    return check_out(&g->out, g->K, g->N, dtype_size(g->out_dtype));
+}
+int product(const iris_b200_matmul_fp8_args* g, const iris_b200_config* cfg, void* ws, size_t ws_bytes, cudaStream_t stream,
+            size_t* need) {
+    const int rc = check_matmul(g);
+    if (rc) return rc;
+    return run_product(false, &g->A, g->a_type, &g->a_scales, &g->B, g->b_type, &g->b_scales, g->bias, g->bias_dtype, &g->out,
+                       g->out_dtype, g->M, g->N, g->K, cfg, ws, ws_bytes, stream, need);
+}
+int product(const iris_b200_weight_grad_fp8_args* g, const iris_b200_config* cfg, void* ws, size_t ws_bytes,
+            cudaStream_t stream, size_t* need) {
+    const int rc = check_wgrad(g);
+    if (rc) return rc;
+    return run_product(true, &g->X, g->x_type, &g->x_scales, &g->dY, g->dy_dtype, nullptr, nullptr, IRIS_F32, &g->out,
+                       g->out_dtype, g->K, g->N, g->M, cfg, ws, ws_bytes, stream, need);
 }
 
 template <int T>
@@ -431,16 +451,18 @@ void launch_quant(const QuantParams& q, bool vec, bool tile, unsigned grid, cuda
 
 extern "C" {
 
-int iris_b200_quantize_fp8(const iris_b200_mat* x, iris_dtype x_dtype, const iris_b200_mat* codes, iris_fp8 type,
-                           const iris_b200_mat* scales, int64_t M, int64_t K, int block_rows, int pow2,
-                           cudaStream_t stream) {
+int iris_b200_quantize_fp8(const iris_b200_quantize_fp8_args* g, cudaStream_t stream) {
     int rc;
-    if (!dims_ok(M, 0, K) || !dtype_ok(x_dtype) || !fp8_ok(type) || (block_rows != 1 && block_rows != 128)) return IRIS_EINVAL;
-    const int64_t kb = cdiv(K, 128), sr = block_rows == 1 ? M : cdiv(M, 128);
-    if ((rc = check_in(x, M, K, dtype_size(x_dtype))) || (rc = check_out(codes, M, K, 1)) || (rc = check_out(scales, sr, kb, 4)))
+    if (!g || !dims_ok(g->M, 0, g->K) || !dtype_ok(g->x_dtype) || !fp8_ok(g->type) || (g->block_rows != 1 && g->block_rows != 128))
+        return IRIS_EINVAL;
+    const iris_b200_mat *x = &g->x, *codes = &g->codes, *scales = &g->scales;
+    const int64_t M = g->M, K = g->K, kb = cdiv(K, 128), sr = g->block_rows == 1 ? M : cdiv(M, 128);
+    if ((rc = check_in(x, M, K, dtype_size(g->x_dtype))) || (rc = check_out(codes, M, K, 1)) ||
+        (rc = check_out(scales, sr, kb, 4)))
         return rc;
     if (M == 0 || K == 0) return IRIS_OK;
-    const int64_t blocks = kb * cdiv(M, block_rows == 1 ? Q_ROWS : Q_TILE);
+    const bool tile = g->block_rows == 128;
+    const int64_t blocks = kb * cdiv(M, tile ? Q_TILE : Q_ROWS);
     if (blocks > 0x7FFFFFFF) return IRIS_EINVAL;
     QuantParams q;
     q.x = x->data;
@@ -455,72 +477,42 @@ int iris_b200_quantize_fp8(const iris_b200_mat* x, iris_dtype x_dtype, const iri
     q.M = M;
     q.K = K;
     q.kblocks = static_cast<unsigned>(kb);
-    q.e5m2 = type == IRIS_E5M2;
-    q.pow2 = pow2 != 0;
+    q.e5m2 = g->type == IRIS_E5M2;
+    q.pow2 = g->pow2 != 0;
     q.fmax = q.e5m2 ? 57344.f : 448.f;
+    q.rfmax = 1.f / q.fmax;
     // f16 input: with scales of at least 2^-15 (e5m2: 2^-8) the codes' finest
     // step is f16's own, 2^-24, so scaled codes are f16 values again and
     // nothing that f16 can hold is lost to the bound
-    q.pmin = x_dtype == IRIS_F16 ? (q.e5m2 ? -8 : -15) : -100;
-    const int e = dtype_size(x_dtype);
+    q.pmin = g->x_dtype == IRIS_F16 ? (q.e5m2 ? -8 : -15) : -100;
+    const int e = dtype_size(g->x_dtype);
     // 16-byte reads and writes where every row starts on them (16384 x 4096
     // bf16: 31 us; the same rows one element off: 60 us)
     const bool vec = (x->col_stride == 1 || K == 1) && (codes->col_stride == 1 || K == 1) && aligned16(x->data) &&
                      (M == 1 || x->row_stride * e % 16 == 0) && aligned16(codes->data) &&
                      (M == 1 || codes->row_stride % 16 == 0);
-    const bool tile = block_rows == 128;
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (x_dtype == IRIS_F32) launch_quant<T_F32>(q, vec, tile, grid, stream);
-    else if (x_dtype == IRIS_F16) launch_quant<T_F16>(q, vec, tile, grid, stream);
+    if (g->x_dtype == IRIS_F32) launch_quant<T_F32>(q, vec, tile, grid, stream);
+    else if (g->x_dtype == IRIS_F16) launch_quant<T_F16>(q, vec, tile, grid, stream);
     else launch_quant<T_BF16>(q, vec, tile, grid, stream);
     const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? IRIS_OK : cuda_fail("quantize launch", static_cast<int>(err));
 }
 
-int iris_b200_matmul_fp8_workspace_size(const iris_b200_mat* A, const iris_b200_mat* B, const iris_b200_mat* out,
-                                        iris_dtype out_dtype, int64_t M, int64_t N, int64_t K,
-                                        const iris_b200_config* cfg, size_t* bytes) {
-    if (!bytes) return IRIS_EINVAL;
-    const int rc = check_matmul(A, B, out, out_dtype, M, N, K);
-    if (rc) return rc;
-    return run_product(false, A, IRIS_E4M3, nullptr, B, 0, nullptr, nullptr, IRIS_F32, out, out_dtype, M, N, K, cfg, nullptr,
-                       0, nullptr, bytes);
+int iris_b200_matmul_fp8_workspace_size(const iris_b200_matmul_fp8_args* args, const iris_b200_config* cfg, size_t* bytes) {
+    return bytes ? product(args, cfg, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;
 }
-
-int iris_b200_matmul_fp8(const iris_b200_mat* A, iris_fp8 a_type, const iris_b200_mat* a_scales, const iris_b200_mat* B,
-                         iris_fp8 b_type, const iris_b200_mat* b_scales, const void* bias, iris_dtype bias_dtype,
-                         const iris_b200_mat* out, iris_dtype out_dtype, int64_t M, int64_t N, int64_t K,
-                         const iris_b200_config* cfg, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    int rc = check_matmul(A, B, out, out_dtype, M, N, K);
-    if (rc) return rc;
-    if (!fp8_ok(a_type) || !fp8_ok(b_type) || (bias && !dtype_ok(bias_dtype))) return IRIS_EINVAL;
-    const int64_t kb = cdiv(K, 128);
-    if ((rc = check_in(a_scales, M, kb, 4)) || (rc = check_in(b_scales, kb, cdiv(N, 128), 4))) return rc;
-    if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_size(bias_dtype)) return IRIS_EALIGN;
-    return run_product(false, A, a_type, a_scales, B, b_type, b_scales, bias, bias_dtype, out, out_dtype, M, N, K, cfg,
-                       workspace, workspace_bytes, stream, nullptr);
+int iris_b200_matmul_fp8(const iris_b200_matmul_fp8_args* args, const iris_b200_config* cfg, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream) {
+    return product(args, cfg, workspace, workspace_bytes, stream, nullptr);
 }
-
-int iris_b200_weight_grad_fp8_workspace_size(const iris_b200_mat* X, const iris_b200_mat* dY, iris_dtype dtype,
-                                             const iris_b200_mat* out, iris_dtype out_dtype, int64_t M, int64_t N,
-                                             int64_t K, const iris_b200_config* cfg, size_t* bytes) {
-    if (!bytes) return IRIS_EINVAL;
-    const int rc = check_wgrad(X, dY, dtype, out, out_dtype, M, N, K);
-    if (rc) return rc;
-    return run_product(true, X, IRIS_E4M3, nullptr, dY, dtype, nullptr, nullptr, IRIS_F32, out, out_dtype, K, N, M, cfg,
-                       nullptr, 0, nullptr, bytes);
+int iris_b200_weight_grad_fp8_workspace_size(const iris_b200_weight_grad_fp8_args* args, const iris_b200_config* cfg,
+                                             size_t* bytes) {
+    return bytes ? product(args, cfg, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;
 }
-
-int iris_b200_weight_grad_fp8(const iris_b200_mat* X, iris_fp8 x_type, const iris_b200_mat* x_scales,
-                              const iris_b200_mat* dY, iris_dtype dtype, const iris_b200_mat* out, iris_dtype out_dtype,
-                              int64_t M, int64_t N, int64_t K, const iris_b200_config* cfg, void* workspace,
+int iris_b200_weight_grad_fp8(const iris_b200_weight_grad_fp8_args* args, const iris_b200_config* cfg, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
-    int rc = check_wgrad(X, dY, dtype, out, out_dtype, M, N, K);
-    if (rc) return rc;
-    if (!fp8_ok(x_type)) return IRIS_EINVAL;
-    if ((rc = check_in(x_scales, M, cdiv(K, 128), 4))) return rc;
-    return run_product(true, X, x_type, x_scales, dY, dtype, nullptr, nullptr, IRIS_F32, out, out_dtype, K, N, M, cfg,
-                       workspace, workspace_bytes, stream, nullptr);
+    return product(args, cfg, workspace, workspace_bytes, stream, nullptr);
 }
 
 }  // extern "C"

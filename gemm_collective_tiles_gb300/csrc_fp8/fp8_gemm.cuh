@@ -573,12 +573,13 @@ struct Worker {
         }
     }
 
-    // Split contraction: each warp lays its 32 x 64 sums into shared memory
-    // (rows of 16 units of 16 bytes, XORed with the row), tells the same warp
-    // of every part, and adds its part's share of the columns (units
-    // rank * 16 / S ...) over all parts in order.
+    // Split contraction over S CTAs: each warp lays its 32 x 64 sums into shared
+    // memory (rows of 16 units of 16 bytes, XORed with the row), tells the same
+    // warp of every part, and adds its part's share of the columns (units
+    // rank * 16 / S ...) over all parts in order.  Every S makes 16 loads from
+    // the other CTAs, all under way at once.
+    template <int S>
     __device__ __forceinline__ bool join(const Place& pl) {
-        const int S = p.split;
         // the other parts have read what lay here before
         if (tiles_done > 0 && !wait_bar_cluster(ctl, sm.parts_out + 8 * w, (tiles_done - 1) & 1, WAIT_PARTS)) return false;
 #pragma unroll
@@ -592,25 +593,28 @@ struct Worker {
         if (lane < S) mbar_arrive_cluster(map_to(sm.parts_in + 8 * w, lane));
         if (!wait_bar_cluster(ctl, sm.parts_in + 8 * w, tiles_done & 1, WAIT_PARTS)) return false;
         ++tiles_done;
-        const int units = 16 / S, row = pl.row0 + lane;
-#pragma unroll 1
-        for (int i = 0; i < units; ++i) {
-            const int j = ctl.rank * units + i;
-            const uint32_t stg_addr = smem_u32(stg), at = (j ^ (lane & 15)) << 4;
-            float4 t[MAX_SPLIT];
+        constexpr int UNITS = 16 / S;
+        const uint32_t mine = smem_u32(stg) + lane * 256;
+        float4 t[UNITS][S];
 #pragma unroll
-            for (int k = 0; k < MAX_SPLIT; ++k)
-                if (k < S) t[k] = ld_shared_cluster_f4(map_to(stg_addr + lane * 256, k) + at);
-            float4 sum = t[0];
+        for (int k = 0; k < S; ++k) {
+            const uint32_t from_k = map_to(mine, k);
 #pragma unroll
-            for (int k = 1; k < MAX_SPLIT; ++k)
-                if (k < S) {
-                    sum.x += t[k].x;
-                    sum.y += t[k].y;
-                    sum.z += t[k].z;
-                    sum.w += t[k].w;
-                }
-            const int c = col_of(pl, 0) + j * 4;
+            for (int i = 0; i < UNITS; ++i)
+                t[i][k] = ld_shared_cluster_f4(from_k + (((ctl.rank * UNITS + i) ^ (lane & 15)) << 4));
+        }
+        const int row = pl.row0 + lane;
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            float4 sum = t[i][0];
+#pragma unroll
+            for (int k = 1; k < S; ++k) {
+                sum.x += t[i][k].x;
+                sum.y += t[i][k].y;
+                sum.z += t[i][k].z;
+                sum.w += t[i][k].w;
+            }
+            const int c = col_of(pl, 0) + (ctl.rank * UNITS + i) * 4;
             float v[4] = {sum.x, sum.y, sum.z, sum.w};
             if (KIND == KIND_MM && p.bias) {
 #pragma unroll
@@ -631,15 +635,16 @@ struct Worker {
                 }
             }
         }
+        // the values above are in registers: the parts may lay their next sums
         __syncwarp();
-        if (lane < S) mbar_arrive_cluster(map_to(sm.parts_out + 8 * w, lane));
+        if (lane < S) mbar_arrive_remote(map_to(sm.parts_out + 8 * w, lane));
         return true;
     }
 
     __device__ __forceinline__ bool epilogue(const Place& pl) {
         if (CG == 1 && p.split > 1) {
             // not live in one part: not live in any
-            if (pl.live && !join(pl)) return false;
+            if (pl.live && !(p.split == 2 ? join<2>(pl) : p.split == 4 ? join<4>(pl) : join<8>(pl))) return false;
             clear();
             return true;
         }

@@ -21,7 +21,7 @@ struct QuantParams {
     long long M, K;
     unsigned kblocks;          // blocks along K
     int e5m2, pow2;
-    float fmax;                // largest code: 448 or 57344
+    float fmax, rfmax;         // largest code (448 or 57344) and its reciprocal in fp32
     int pmin;                  // exponent of the smallest scale
 };
 
@@ -56,8 +56,8 @@ __device__ __forceinline__ float finite_or_nan(float v) {
 // Scale and reciprocal of a block.  Power of two: FMAX is 1.75 * 2^n, so the
 // smallest 2^p with amax <= 2^p * FMAX follows from amax's exponent and from
 // whether its mantissa is above 1.75; both factors are exact.  Otherwise
-// scale = amax / FMAX and the codes are x * (FMAX / amax), both rounded to
-// nearest (true divisions, not approximations).
+// scale = amax * (1 / FMAX) and the codes are x * (FMAX * (1 / amax)), every
+// operation in fp32, rounded to nearest.
 __device__ __forceinline__ void block_scale(const QuantParams& p, float amax, float& scale, float& inv) {
     amax = fmaxf(amax, p.fmax * __int_as_float((p.pmin + 127) << 23));
     if (p.pow2) {
@@ -66,8 +66,8 @@ __device__ __forceinline__ void block_scale(const QuantParams& p, float amax, fl
         scale = __int_as_float((e + 127) << 23);
         inv = __int_as_float((127 - e) << 23);
     } else {
-        scale = __fdiv_rn(amax, p.fmax);
-        inv = __fdiv_rn(p.fmax, amax);
+        scale = amax * p.rfmax;
+        inv = __frcp_rn(amax) * p.fmax;
     }
 }
 

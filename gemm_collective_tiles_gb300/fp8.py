@@ -19,10 +19,10 @@ from typing import Optional
 import torch
 
 from . import _native
-from ._native import iris_b200_mat
 
 _FP8 = {torch.float8_e4m3fn: _native.IRIS_E4M3, torch.float8_e5m2: _native.IRIS_E5M2}
 _DT = {torch.float16: _native.IRIS_F16, torch.bfloat16: _native.IRIS_BF16, torch.float32: _native.IRIS_F32}
+_DT16 = {torch.float16: _native.IRIS_F16, torch.bfloat16: _native.IRIS_BF16}
 _BLOCK = 128
 _ROWS = {"rows": 1, "tiles": _BLOCK}
 
@@ -31,25 +31,28 @@ def _blocks(n: int) -> int:
     return (n + _BLOCK - 1) // _BLOCK
 
 
-def _mat(t: torch.Tensor) -> iris_b200_mat:
-    return iris_b200_mat(t.data_ptr(), *t.stride())
-
-
-def _check(name: str, t: torch.Tensor, shape, dtypes, device=None) -> None:
-    """A 2-D (or, for a bias, 1-D) device tensor of this shape and one of these types."""
+def _refuse(name: str, t, shape, dtypes, device) -> None:
+    """Say what is wrong with an argument that _mat did not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} is not a tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has type {t.dtype}")
-    if shape is None:
-        if t.dim() != 2:
-            raise ValueError(f"{name} has {t.dim()} dimensions, not 2")
-    elif tuple(t.shape) != shape:
+    if t.dim() != 2:
+        raise ValueError(f"{name} has {t.dim()} dimensions, not 2")
+    if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     if not t.is_cuda:
         raise ValueError(f"{name} is not on a CUDA device")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
+    raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _mat(name: str, t: torch.Tensor, shape, dtypes, device):
+    """(data, row stride, column stride) of a 2-D device tensor of this shape and one of these types."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2 and (shape is None or t.shape == shape)
+            and t.is_cuda and (device is None or t.device == device)):
+        _refuse(name, t, shape, dtypes, device)
+    r, c = t.stride()
+    return t.data_ptr(), r, c
 
 
 def _cfgp(config):
@@ -61,7 +64,7 @@ def _cfgp(config):
 
 def _stream(stream, device) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -96,27 +99,36 @@ def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
     block's other elements; zero blocks get the smallest scale."""
     if block not in _ROWS:
         raise ValueError(f"unknown block {block!r}")
-    _check("x", x, None, _DT)
+    mx = _mat("x", x, None, _DT, None)
     M, K = x.shape
-    _check("codes", codes, (M, K), _FP8, x.device)
-    _check("scales", scales, (M if block == "rows" else _blocks(M), _blocks(K)), _F32, x.device)
-    with torch.cuda.device(x.device):
-        _native.check("iris_b200_quantize_fp8", _native.load().iris_b200_quantize_fp8(
-            _mat(x), _DT[x.dtype], _mat(codes), _FP8[codes.dtype], _mat(scales), M, K, _ROWS[block], int(pow2),
-            _stream(stream, x.device)))
+    dev = x.device
+    mc = _mat("codes", codes, (M, K), _FP8, dev)
+    ms = _mat("scales", scales, (M if block == "rows" else _blocks(M), _blocks(K)), _F32, dev)
+    args = _native.pack_quantize_fp8(*mx, *mc, *ms, M, K, _DT[x.dtype], _FP8[codes.dtype], _ROWS[block], bool(pow2))
+    lib, st = _native.load(), _stream(stream, dev)
+    if dev.index == torch.cuda.current_device():
+        rc = lib.iris_b200_quantize_fp8(args, st)
+    else:
+        with torch.cuda.device(dev):
+            rc = lib.iris_b200_quantize_fp8(args, st)
+    if rc:
+        _native.check("iris_b200_quantize_fp8", rc)
 
 
-def _run(name: str, ws, device, size_args, call):
-    """One product: the given workspace, or a new one where it is missing or too small."""
-    with torch.cuda.device(device):
-        rc = _native.IRIS_ENOWS if ws is None else call(ws)
-        if rc == _native.IRIS_ENOWS:
-            from . import Workspace
-            need = ctypes.c_size_t(0)
-            size = "iris_b200_" + name + "_workspace_size"
-            _native.check(size, getattr(_native.load(), size)(*size_args, ctypes.byref(need)))
-            ws = Workspace(int(need.value), device)
-            rc = call(ws)
+def _product(name: str, fn, args, config, ws, dev, stream):
+    """One product with the given workspace, or a new one where it is missing or too small."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _product(name, fn, args, config, ws, dev, stream)
+    cfg, st = _cfgp(config), _stream(stream, dev)
+    rc = _native.IRIS_ENOWS if ws is None else fn(args, cfg, ws.ptr, ws.nbytes, st)
+    if rc == _native.IRIS_ENOWS:
+        from . import Workspace
+        need, size = ctypes.c_size_t(0), "iris_b200_" + name + "_workspace_size"
+        _native.check(size, getattr(_native.load(), size)(args, cfg, ctypes.byref(need)))
+        ws = Workspace(int(need.value), dev)
+        rc = fn(args, cfg, ws.ptr, ws.nbytes, st)
+    if rc:
         _native.check("iris_b200_" + name, rc)
     return ws
 
@@ -130,28 +142,26 @@ def matmul_fp8(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale:
     of a quantised matrix is ``codes.t(), scales.t()``.  bias (N,) and out
     (M, N) are f16, bf16 or f32.  The 128-deep blocks are summed in fp32 and
     rounded once.  Returns the workspace."""
-    _check("A", A, None, _FP8)
+    ma = _mat("A", A, None, _FP8, None)
     M, K = A.shape
     dev = A.device
-    _check("B", B, None, _FP8, dev)
+    mb = _mat("B", B, None, _FP8, dev)
     N = B.shape[1]
     if B.shape[0] != K:
         raise ValueError(f"A has {K} columns and B has {B.shape[0]} rows")
-    _check("A_scale", A_scale, (M, _blocks(K)), _F32, dev)
-    _check("B_scale", B_scale, (_blocks(K), _blocks(N)), _F32, dev)
-    _check("out", out, (M, N), _DT, dev)
-    bias_ptr, bias_dt = None, _native.IRIS_F32
+    kb = _blocks(K)
+    msa = _mat("A_scale", A_scale, (M, kb), _F32, dev)
+    msb = _mat("B_scale", B_scale, (kb, _blocks(N)), _F32, dev)
+    mo = _mat("out", out, (M, N), _DT, dev)
+    bias_ptr, bias_dt = 0, _native.IRIS_F32
     if bias is not None:
-        _check("bias", bias, (N,), _DT, dev)
-        if N > 1 and bias.stride(0) != 1:
-            raise ValueError("bias is not contiguous")
+        if bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias is not a contiguous tensor of shape ({N},)")
+        _mat("bias", bias.unsqueeze(0), None, _DT, dev)
         bias_ptr, bias_dt = bias.data_ptr(), _DT[bias.dtype]
-    a, b, o, cfg, st = _mat(A), _mat(B), _mat(out), _cfgp(config), _stream(stream, dev)
-    sa, sb = _mat(A_scale), _mat(B_scale)
-    lib = _native.load()
-    return _run("matmul_fp8", workspace, dev, (a, b, o, _DT[out.dtype], M, N, K, cfg), lambda ws: lib.iris_b200_matmul_fp8(
-        a, _FP8[A.dtype], sa, b, _FP8[B.dtype], sb, bias_ptr, bias_dt, o, _DT[out.dtype], M, N, K, cfg,
-        ws.ptr, ws.nbytes, st))
+    args = _native.pack_matmul_fp8(*ma, *msa, *mb, *msb, *mo, bias_ptr, M, N, K, _FP8[A.dtype], _FP8[B.dtype], bias_dt,
+                                   _DT[out.dtype])
+    return _product("matmul_fp8", _native.load().iris_b200_matmul_fp8, args, config, workspace, dev, stream)
 
 
 def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, out: torch.Tensor, config=None,
@@ -162,20 +172,17 @@ def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, ou
     X (M, K) codes with "rows" scales (M, ceil(K/128)); dY (M, N) f16 or bf16;
     out f16, bf16 or f32.  X's values enter in dY's type, exactly where the
     scales are powers of two.  Returns the workspace."""
-    _check("X", X, None, _FP8)
+    mx = _mat("X", X, None, _FP8, None)
     M, K = X.shape
     dev = X.device
-    _check("dY", dY, None, (torch.float16, torch.bfloat16), dev)
+    md = _mat("dY", dY, None, _DT16, dev)
     if dY.shape[0] != M:
         raise ValueError(f"X has {M} rows and dY has {dY.shape[0]}")
     N = dY.shape[1]
-    _check("X_scale", X_scale, (M, _blocks(K)), _F32, dev)
-    _check("out", out, (K, N), _DT, dev)
-    x, d, o, cfg, st, sx = _mat(X), _mat(dY), _mat(out), _cfgp(config), _stream(stream, dev), _mat(X_scale)
-    lib = _native.load()
-    dt, odt = _DT[dY.dtype], _DT[out.dtype]
-    return _run("weight_grad_fp8", workspace, dev, (x, d, dt, o, odt, M, N, K, cfg), lambda ws: lib.iris_b200_weight_grad_fp8(
-        x, _FP8[X.dtype], sx, d, dt, o, odt, M, N, K, cfg, ws.ptr, ws.nbytes, st))
+    ms = _mat("X_scale", X_scale, (M, _blocks(K)), _F32, dev)
+    mo = _mat("out", out, (K, N), _DT, dev)
+    args = _native.pack_weight_grad_fp8(*mx, *ms, *md, *mo, M, N, K, _FP8[X.dtype], _DT[dY.dtype], _DT[out.dtype], 0)
+    return _product("weight_grad_fp8", _native.load().iris_b200_weight_grad_fp8, args, config, workspace, dev, stream)
 
 
 class _Fp8Linear(torch.autograd.Function):

@@ -466,13 +466,13 @@ IRIS_API int iris_b200_num_sms(int* n);
  * once, at least the size that the op's size query returns for the same
  * arguments, one call at a time.  An operand that the tensor memory
  * accelerator cannot read in place (a base or row pitch that is not a
- * multiple of 16 bytes, or no unit stride) is first copied into the
- * workspace on the same stream, and an output that it cannot write goes
- * through an fp32 copy there; both are counted by the size query.
+ * multiple of 16 bytes, or no unit stride) is first copied into the workspace
+ * on the same stream, which the size query counts.
  * Of the config, tile_m (128 = one CTA per 128 x 128 tile, 256 = CTA pairs on
- * 256 x 256), k_split (parts of the contraction per tile), group_m (in
- * 128-row blocks), grid, wait_ns and debug_skip_flag (work unit whose
- * accumulator is never handed over) apply.
+ * 256 x 256), k_split (1, 2, 4 or 8 CTAs of a cluster share a tile's
+ * contraction; 128 x 128 tiles only), group_m (in 128-row blocks), grid,
+ * wait_ns and debug_skip_flag (k > 0: tile k - 1's accumulator is never handed
+ * over) apply; 0 = chosen by the sizes.
  * Zero sizes: no rows or columns of output is a no-op; an empty contraction
  * gives bias or zero.  Sizes are below 2^31 - 512.
  */
@@ -492,17 +492,25 @@ typedef struct {
  * amax = the block's largest finite |x|, at least FMAX * 2^PMIN.
  *   pow2 != 0:  scale = the smallest power of two with amax <= scale * FMAX,
  *               codes = RNE8(x / scale) (the division is exact);
- *   pow2 == 0:  scale = amax / FMAX, codes = RNE8(x * (FMAX / amax)).
+ *   pow2 == 0:  scale = amax * (1 / FMAX), codes = RNE8(x * (FMAX * (1 / amax))),
+ *               every operation in fp32, rounded to nearest.
  * PMIN is -100; for f16 input -15 (e5m2: -8), where the codes' finest step is
  * f16's own.  NaN and infinities become the NaN code and leave the scale to
  * the block's other elements.
  */
-IRIS_API int iris_b200_quantize_fp8(const iris_b200_mat* x, iris_dtype x_dtype, const iris_b200_mat* codes,
-                                    iris_fp8 type, const iris_b200_mat* scales, int64_t M, int64_t K,
-                                    int block_rows, int pow2, cudaStream_t stream);
+typedef struct {
+    iris_b200_mat x, codes, scales;
+    int64_t M, K;
+    int32_t x_dtype;       /* iris_dtype */
+    int32_t type;          /* iris_fp8 */
+    int32_t block_rows;    /* 1 or 128 */
+    int32_t pow2;
+} iris_b200_quantize_fp8_args;
+
+IRIS_API int iris_b200_quantize_fp8(const iris_b200_quantize_fp8_args* args, cudaStream_t stream);
 
 /*
- * matmul_fp8 -- out (M x N) = (A * scales) @ (B * scales) + bias.
+ * matmul_fp8 -- out (M x N) = (A * a_scales) @ (B * b_scales) + bias.
  *
  *   A, a_scales  M x K codes, M x ceil(K/128) scales (1 x 128 blocks).
  *   B, b_scales  K x N codes in either order (a transposed view has its
@@ -513,35 +521,41 @@ IRIS_API int iris_b200_quantize_fp8(const iris_b200_mat* x, iris_dtype x_dtype, 
  * blocks are scaled and summed in fp32 (the product of a pair of scales has
  * to be a finite fp32 number) and rounded once.
  */
-IRIS_API int iris_b200_matmul_fp8_workspace_size(const iris_b200_mat* A, const iris_b200_mat* B,
-                                                 const iris_b200_mat* out, iris_dtype out_dtype, int64_t M,
-                                                 int64_t N, int64_t K, const iris_b200_config* cfg, size_t* bytes);
-IRIS_API int iris_b200_matmul_fp8(const iris_b200_mat* A, iris_fp8 a_type, const iris_b200_mat* a_scales,
-                                  const iris_b200_mat* B, iris_fp8 b_type, const iris_b200_mat* b_scales,
-                                  const void* bias, iris_dtype bias_dtype, const iris_b200_mat* out,
-                                  iris_dtype out_dtype, int64_t M, int64_t N, int64_t K,
-                                  const iris_b200_config* cfg, void* workspace, size_t workspace_bytes,
-                                  cudaStream_t stream);
+typedef struct {
+    iris_b200_mat A, a_scales, B, b_scales, out;
+    const void* bias;
+    int64_t M, N, K;
+    int32_t a_type, b_type;            /* iris_fp8 */
+    int32_t bias_dtype, out_dtype;     /* iris_dtype */
+} iris_b200_matmul_fp8_args;
+
+IRIS_API int iris_b200_matmul_fp8_workspace_size(const iris_b200_matmul_fp8_args* args, const iris_b200_config* cfg,
+                                                 size_t* bytes);
+IRIS_API int iris_b200_matmul_fp8(const iris_b200_matmul_fp8_args* args, const iris_b200_config* cfg,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
- * weight_grad_fp8 -- out (K x N) = (X * scales)^T @ dY: the weight gradient
+ * weight_grad_fp8 -- out (K x N) = (X * x_scales)^T @ dY: the weight gradient
  * of a linear layer whose input X was kept as an 8-bit checkpoint.
  *
  *   X, x_scales  M x K codes, M x ceil(K/128) scales (1 x 128 blocks).
- *   dY           M x N, f16 or bf16 (`dtype`).
+ *   dY           M x N, f16 or bf16.
  *   out          f16, bf16 or f32.
  * X's values enter the product in dY's type: exact for power-of-two scales
  * (in f16's range), rounded once to 16 bits otherwise.  Sums are fp32.
  */
-IRIS_API int iris_b200_weight_grad_fp8_workspace_size(const iris_b200_mat* X, const iris_b200_mat* dY,
-                                                      iris_dtype dtype, const iris_b200_mat* out,
-                                                      iris_dtype out_dtype, int64_t M, int64_t N, int64_t K,
+typedef struct {
+    iris_b200_mat X, x_scales, dY, out;
+    int64_t M, N, K;
+    int32_t x_type;                    /* iris_fp8 */
+    int32_t dy_dtype, out_dtype;       /* iris_dtype */
+    int32_t reserved;                  /* 0 */
+} iris_b200_weight_grad_fp8_args;
+
+IRIS_API int iris_b200_weight_grad_fp8_workspace_size(const iris_b200_weight_grad_fp8_args* args,
                                                       const iris_b200_config* cfg, size_t* bytes);
-IRIS_API int iris_b200_weight_grad_fp8(const iris_b200_mat* X, iris_fp8 x_type, const iris_b200_mat* x_scales,
-                                       const iris_b200_mat* dY, iris_dtype dtype, const iris_b200_mat* out,
-                                       iris_dtype out_dtype, int64_t M, int64_t N, int64_t K,
-                                       const iris_b200_config* cfg, void* workspace, size_t workspace_bytes,
-                                       cudaStream_t stream);
+IRIS_API int iris_b200_weight_grad_fp8(const iris_b200_weight_grad_fp8_args* args, const iris_b200_config* cfg,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
