@@ -238,16 +238,25 @@ struct Plan {
     size_t copy_a, copy_b, total;  // workspace offsets
 };
 
-// Estimated time in us of a variant: `slots` clusters run at once, each tile
-// takes `part` stages and an epilogue.  Constants measured on GB300.
-double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split) {
-    const double stage = wg ? (v == PAIR ? 0.50 : 0.35) : (v == PAIR ? 0.47 : v == CTA ? 0.35 : 0.22);
-    const double per_tile = part * stage + (v == PAIR ? 1.5 : 1.0) + (split > 1 ? 2.0 : 0.0);
-    return 4.0 + cdiv(tiles, slots) * per_tile;
+// Estimated time in us of a variant: `slots` clusters run at once and take the
+// tiles in turn; a tile costs `part` stages, its epilogue and, where its
+// contraction is split, the meeting of the parts.  Constants measured on GB300
+// (launch 4.5; e.g. 1 x 4096 x 1024: 12.3 us as 8 CTAs of 32 stages, 9.1 split
+// over 8; 100 x 1000 x 3000: 7.8 us whole, 11.4 split over 2; 8192 x 512 x 512
+// weight gradient: 57 us whole, 26 split over 4).  Element stores, for outputs
+// that no tensor store can reach, cost a tile about 2 us and a meeting 6.
+double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, int64_t rows, bool direct) {
+    const double stage = wg ? (v == PAIR ? 0.47 : 0.40) : (v == PAIR ? 0.45 : 0.30);
+    double tile = part * stage + (v == PAIR ? 2.0 : 1.0);
+    if (split > 1)
+        tile += (rows <= 32 ? 2.0 : 4.5) + (direct ? 0.0 : 6.0);
+    else if (!direct)
+        tile += 2.0;
+    return 4.5 + cdiv(tiles, slots) * tile;
 }
 
 int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& d, const Operand& a, const Operand& b,
-              int64_t rows, int64_t cols, int64_t depth) {
+              bool direct, int64_t rows, int64_t cols, int64_t depth) {
     iris_b200_config z;
     std::memset(&z, 0, sizeof(z));
     if (!cfg) cfg = &z;
@@ -272,7 +281,7 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
             if (slots < 1) continue;
             // every part has stages (an empty one, where the config asks for it, adds zeros)
             if (cfg->k_split ? split != cfg->k_split : part * (split - 1) >= stages) continue;
-            const double t = estimate(wg, v, slots, tiles, part, split);
+            const double t = estimate(wg, v, slots, tiles, part, split, rows, direct);
             if (pl.cg == 0 || t < best) {
                 best = t;
                 pl.cg = cg;
@@ -323,7 +332,7 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
     DeviceInfo d;
     if ((rc = device_info(&d))) return rc;
     Plan pl;
-    if ((rc = make_plan(pl, wg, cfg, d, a, b, rows, cols, std::max<int64_t>(depth, 1)))) return rc;
+    if ((rc = make_plan(pl, wg, cfg, d, a, b, direct, rows, cols, std::max<int64_t>(depth, 1)))) return rc;
     if (need) {
         *need = pl.total;
         return IRIS_OK;
