@@ -19,7 +19,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIBNAME = "libgemm_collective_tiles.so"
 SOURCES = [os.path.join(CSRC, "iris_api.cu"), os.path.join(CSRC_FP8, "fp8_api.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("fused_kernel.cuh", "ptx.cuh")]
-HEADERS += [os.path.join(CSRC_FP8, f) for f in ("fp8_ptx.cuh", "fp8_quant.cuh", "fp8_gemm.cuh")]
+HEADERS += [os.path.join(CSRC_FP8, f) for f in ("fp8_ptx.cuh", "fp8_quant.cuh", "fp8_gemm.cuh", "fp8_few.cuh")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "gemm_collective_tiles.h"
+#include "fp8_few.cuh"
 #include "fp8_gemm.cuh"
 
 using namespace gct;
@@ -38,14 +39,15 @@ int cuda_fail(const char* what, int code) {
     return IRIS_ECUDA;
 }
 
-// The kernels: a pair's tile, a CTA's, and a CTA's with few rows.
-enum Variant { PAIR = 0, CTA = 1, FEW = 2 };
+// The kernels: a pair's 256 x 256 tile, a CTA's 128 x 128, and the ones for at
+// most 16 or 32 rows.
+enum Variant { PAIR = 0, CTA = 1, FEW16 = 2, FEW32 = 3 };
 
 // per device: SMs and how many clusters of a kernel run at once, by kind,
 // variant and log2 of the cluster's CTAs (a pair, or the parts of a split)
 struct DeviceInfo {
     int sms;
-    int clusters[2][3][4];
+    int clusters[2][4][4];
     bool done;
 };
 DeviceInfo g_dev[64];
@@ -68,31 +70,36 @@ cudaLaunchConfig_t launch_config(int grid, int threads, size_t smem, int cluster
     return lc;
 }
 
-template <int KIND, int CG, int ROWS>
-int setup_kernel(DeviceInfo& d) {
-    using G = Geo<KIND, CG, ROWS>;
-    cudaError_t e = cudaFuncSetAttribute(block_gemm_kernel<KIND, CG, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(G::BYTES));
+template <typename Kernel>
+int setup_kernel(Kernel kernel, int* clusters, int lg_lo, int lg_hi, int threads, size_t smem, int regs, int sms) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (8-bit products)", static_cast<int>(e));
     // the warpgroups' register shares must fit in what the launch allots, or
     // a warpgroup would wait for registers that never come
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, block_gemm_kernel<KIND, CG, ROWS>);
+    e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return cuda_fail("cudaFuncGetAttributes", static_cast<int>(e));
-    if (fa.numRegs * G::THREADS < G::REGS_TOTAL) return cuda_fail("register shares of the 8-bit products", fa.numRegs);
-    for (int lg = 0; lg < 4; ++lg) {
-        if (CG == 2 && lg != 1) continue;
-        int* n = &d.clusters[KIND][CG == 2 ? PAIR : ROWS == 64 ? FEW : CTA][lg];
-        if (lg == 0) {
-            *n = d.sms;
-            continue;
-        }
+    if (fa.numRegs * threads < regs) return cuda_fail("register shares of the 8-bit products", fa.numRegs);
+    for (int lg = lg_lo; lg <= lg_hi; ++lg) {
+        clusters[lg] = sms;
+        if (lg == 0) continue;
         cudaLaunchAttribute attr;
-        const cudaLaunchConfig_t lc = launch_config(d.sms >> lg << lg, G::THREADS, G::BYTES, 1 << lg, nullptr, &attr);
-        e = cudaOccupancyMaxActiveClusters(n, block_gemm_kernel<KIND, CG, ROWS>, &lc);
-        if (e != cudaSuccess || *n < 1) return cuda_fail("cudaOccupancyMaxActiveClusters", static_cast<int>(e));
+        const cudaLaunchConfig_t lc = launch_config(sms >> lg << lg, threads, smem, 1 << lg, nullptr, &attr);
+        e = cudaOccupancyMaxActiveClusters(&clusters[lg], kernel, &lc);
+        if (e != cudaSuccess || clusters[lg] < 1) return cuda_fail("cudaOccupancyMaxActiveClusters", static_cast<int>(e));
     }
     return IRIS_OK;
+}
+template <int KIND, int CG>
+int setup_tiles(DeviceInfo& d) {
+    using G = Geo<KIND, CG>;
+    return setup_kernel(block_gemm_kernel<KIND, CG>, d.clusters[KIND][CG == 2 ? PAIR : CTA], CG == 2, CG == 2 ? 1 : 3,
+                        G::THREADS, G::BYTES, G::REGS_TOTAL, d.sms);
+}
+template <int NT>
+int setup_few(DeviceInfo& d) {
+    return setup_kernel(few_rows_kernel<NT>, d.clusters[KIND_MM][NT == 16 ? FEW16 : FEW32], 0, 3, FewGeo<NT>::THREADS,
+                        FewGeo<NT>::BYTES, 0, d.sms);
 }
 
 int device_info(DeviceInfo* out) {
@@ -103,9 +110,8 @@ int device_info(DeviceInfo* out) {
     if (!d.done) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return IRIS_ECUDA;
         int rc;
-        if ((rc = setup_kernel<KIND_MM, 1, 128>(d)) || (rc = setup_kernel<KIND_MM, 2, 128>(d)) ||
-            (rc = setup_kernel<KIND_MM, 1, 64>(d)) || (rc = setup_kernel<KIND_WG, 1, 128>(d)) ||
-            (rc = setup_kernel<KIND_WG, 2, 128>(d)))
+        if ((rc = setup_tiles<KIND_MM, 1>(d)) || (rc = setup_tiles<KIND_MM, 2>(d)) || (rc = setup_tiles<KIND_WG, 1>(d)) ||
+            (rc = setup_tiles<KIND_WG, 2>(d)) || (rc = setup_few<16>(d)) || (rc = setup_few<32>(d)))
             return rc;
         if (!g_encode) {
             void* fn = nullptr;
@@ -245,12 +251,12 @@ struct Plan {
 // over 8; 100 x 1000 x 3000: 7.8 us whole, 11.4 split over 2; 8192 x 512 x 512
 // weight gradient: 57 us whole, 26 split over 4).  Element stores, for outputs
 // that no tensor store can reach, cost a tile about 2 us and a meeting 6.
-double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, int64_t rows, bool direct) {
+double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, bool direct) {
     const double stage = wg ? (v == PAIR ? 0.47 : 0.40) : (v == PAIR ? 0.45 : 0.30);
     double tile = part * stage + (v == PAIR ? 2.0 : 1.0);
     if (split > 1)
-        tile += (rows <= 32 ? 2.0 : 4.5) + (direct ? 0.0 : 6.0);
-    else if (!direct)
+        tile += v >= FEW16 ? 2.0 : 4.5 + (direct ? 0.0 : 6.0);
+    else if (!direct && v <= CTA)
         tile += 2.0;
     return 4.5 + cdiv(tiles, slots) * tile;
 }
@@ -276,12 +282,12 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
         for (int lg = 0; lg < (cg == 2 ? 1 : 4); ++lg) {
             const int split = 1 << lg;
             const int64_t part = cdiv(stages, split);
-            const Variant v = cg == 2 ? PAIR : !wg && rows <= 64 ? FEW : CTA;
+            const Variant v = cg == 2 ? PAIR : wg || rows > 32 ? CTA : rows <= 16 ? FEW16 : FEW32;
             const int slots = std::min(d.clusters[wg][v][cg == 2 ? 1 : lg], grid / (cg * split));
             if (slots < 1) continue;
             // every part has stages (an empty one, where the config asks for it, adds zeros)
             if (cfg->k_split ? split != cfg->k_split : part * (split - 1) >= stages) continue;
-            const double t = estimate(wg, v, slots, tiles, part, split, rows, direct);
+            const double t = estimate(wg, v, slots, tiles, part, split, direct);
             if (pl.cg == 0 || t < best) {
                 best = t;
                 pl.cg = cg;
@@ -303,13 +309,21 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
     return IRIS_OK;
 }
 
-template <int KIND, int CG, int ROWS>
-int launch_gemm(const GemmParams& p, int grid, cudaStream_t stream) {
-    using G = Geo<KIND, CG, ROWS>;
+template <typename Kernel>
+int launch_kernel(Kernel kernel, const GemmParams& p, int grid, int threads, size_t smem, int cluster, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t lc = launch_config(grid, G::THREADS, G::BYTES, CG * p.split, stream, &attr);
-    const cudaError_t e = cudaLaunchKernelEx(&lc, block_gemm_kernel<KIND, CG, ROWS>, p);
+    const cudaLaunchConfig_t lc = launch_config(grid, threads, smem, cluster, stream, &attr);
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p);
     return e == cudaSuccess ? IRIS_OK : cuda_fail("kernel launch (8-bit product)", static_cast<int>(e));
+}
+template <int KIND, int CG>
+int launch_tiles(const GemmParams& p, int grid, cudaStream_t stream) {
+    using G = Geo<KIND, CG>;
+    return launch_kernel(block_gemm_kernel<KIND, CG>, p, grid, G::THREADS, G::BYTES, CG * p.split, stream);
+}
+template <int NT>
+int launch_few(const GemmParams& p, int grid, cudaStream_t stream) {
+    return launch_kernel(few_rows_kernel<NT>, p, grid, FewGeo<NT>::THREADS, FewGeo<NT>::BYTES, p.split, stream);
 }
 
 // out (rows x cols) of one product: everything that both kinds share.
@@ -380,12 +394,13 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
         p.codes_e5m2 = a_type == IRIS_E5M2;
     } else {
         p.b_mn = !b.transposed;
-        // few rows: the box holds just them (whole groups of 8), the rest of
-        // the stage keeps what it held and feeds rows that are never read
-        p.a_box = rows < 128 ? static_cast<int>(round_up(rows, 8)) : 128;
+        const bool few = pl.variant == FEW16 || pl.variant == FEW32;
+        p.a_box = pl.variant == FEW16 ? 16 : pl.variant == FEW32 ? 32 : 128;
         if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, p.a_box, true))) return rc;
         if ((rc = make_map_2d(&p.tmB, u8, 1, b, 128, 128, true))) return rc;
-        p.idesc = idesc_of(a_type, b_type, 0, p.b_mn, 128 * pl.cg, 128 * pl.cg);
+        // few rows: the weights are the MMA's first operand
+        p.idesc = few ? idesc_of(b_type, a_type, p.b_mn, 0, 128, p.a_box)
+                      : idesc_of(a_type, b_type, 0, p.b_mn, 128 * pl.cg, 128 * pl.cg);
         p.sb = static_cast<const float*>(sb->data);
         p.sb_rs = sb->row_stride;
         p.sb_cs = sb->col_stride;
@@ -404,13 +419,16 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
     p.tma_out = direct;
     p.wait_ns = cfg && cfg->wait_ns ? cfg->wait_ns : DEFAULT_WAIT_NS;
     p.debug_skip = cfg ? static_cast<uint32_t>(cfg->debug_skip_flag) : 0u;
-    if (direct && (rc = make_store_map(&p.tmC, out_dtype, out->data, cols, rows,
+    if (direct && pl.variant <= CTA && (rc = make_store_map(&p.tmC, out_dtype, out->data, cols, rows,
                                        rows == 1 ? packed_pitch(cols, dtype_size(out_dtype)) : out->row_stride)))
         return rc;
-    if (wg) return pl.cg == 2 ? launch_gemm<KIND_WG, 2, 128>(p, pl.grid, stream) : launch_gemm<KIND_WG, 1, 128>(p, pl.grid, stream);
-    return pl.variant == PAIR  ? launch_gemm<KIND_MM, 2, 128>(p, pl.grid, stream)
-           : pl.variant == CTA ? launch_gemm<KIND_MM, 1, 128>(p, pl.grid, stream)
-                               : launch_gemm<KIND_MM, 1, 64>(p, pl.grid, stream);
+    if (wg) return pl.variant == PAIR ? launch_tiles<KIND_WG, 2>(p, pl.grid, stream) : launch_tiles<KIND_WG, 1>(p, pl.grid, stream);
+    switch (pl.variant) {
+        case PAIR: return launch_tiles<KIND_MM, 2>(p, pl.grid, stream);
+        case CTA: return launch_tiles<KIND_MM, 1>(p, pl.grid, stream);
+        case FEW16: return launch_few<16>(p, pl.grid, stream);
+        default: return launch_few<32>(p, pl.grid, stream);
+    }
 }
 
 int check_matmul(const iris_b200_matmul_fp8_args* g) {

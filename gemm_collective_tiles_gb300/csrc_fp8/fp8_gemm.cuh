@@ -25,9 +25,7 @@
 //   warps 12-19  KIND_WG: converters
 // CG = 2: a cluster of two CTAs computes a 256 x 256 tile with
 // tcgen05.mma.cta_group::2, each staging its 128 rows of A and 128 columns of
-// B; the even CTA issues the MMAs.  CG = 1: 128 x 128 tiles; ROWS = 64 is that
-// with stages that hold 64 rows of A (the MMA's other rows read what lies behind
-// them and are never looked at), so that more of B is on its way.
+// B; the even CTA issues the MMAs.  CG = 1: 128 x 128 tiles, for fewer rows.
 //
 // CG = 1 can split the contraction: a cluster of 2, 4 or 8 CTAs takes a tile,
 // each a part of its stages; the fp32 sums meet in shared memory, where each
@@ -149,42 +147,44 @@ __device__ __forceinline__ bool wait_bar_cluster(const Ctl& c, uint32_t bar, uin
     return bar_try_wait_cluster(bar, parity);  // the phase is over: this only acquires at cluster scope
 }
 
-template <int KIND, int CG, int ROWS>
+template <int KIND, int CG>
 struct Geo {
-    static_assert(ROWS == 128 || (ROWS == 64 && KIND == KIND_MM && CG == 1), "tile kinds");
     static constexpr int BN = CG == 2 ? 256 : 128;     // tile columns (of the pair)
     static constexpr int COLS = BN / 2;                // accumulator columns of a promotion warp
     static constexpr int DEPTH = KIND == KIND_MM ? 128 : 64;  // contraction per stage
     static constexpr int UMMA_STEPS = 4;               // 128 / 32 or 64 / 16
-    static constexpr uint32_t A_BYTES = ROWS * 128;    // rows x 128 bytes of contraction
+    static constexpr uint32_t A_BYTES = BM * 128;      // rows x 128 bytes of contraction
     static constexpr uint32_t B_BYTES = (BN / CG) * 128;
     static constexpr uint32_t RAW_BYTES = KIND == KIND_WG ? 64 * 128 : 0;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     // a stage holds one A and one B box; KIND_WG: the converted A and B, and
     // the codes have a ring of their own (RAWS slots)
-    static constexpr int STAGES = ROWS == 64 ? 8 : KIND == KIND_MM ? 5 : 4;
+    static constexpr int STAGES = KIND == KIND_MM && CG == 2 ? 5 : 4;
     static constexpr int RAWS = KIND == KIND_MM ? 0 : 4;
     static constexpr int ISSUERS = KIND == KIND_MM && CG == 1 ? 2 : 1;  // warps that issue MMAs
     static constexpr int THREADS = KIND == KIND_MM ? 384 : 640;
     static constexpr uint32_t OUT_BYTES = 2 * 32 * 128;  // staging per promotion warp: two boxes
     static constexpr int TMEM_COLS = 512;
     static constexpr int ACCS = TMEM_COLS / BN;        // accumulators under way
+    // Two warps that take turns at a ring (issuers, converter groups) each own
+    // every other slot: a wait by parity is only valid for one who sees every
+    // phase of the barrier, and with an odd ring each would see every other.
+    static_assert(ISSUERS == 1 || (STAGES % 2 == 0 && ACCS % 2 == 0), "issuers by parity of the slot");
+    static_assert(KIND == KIND_MM || (STAGES % 2 == 0 && RAWS % 2 == 0), "converter groups by parity of the slot");
     static constexpr int NUM_BARS = 3 * STAGES + 2 * RAWS + 2 * ACCS + 2 * 8 + 2;
     static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES + RAWS * RAW_BYTES;
-    // 64 rows: only the warps of the first two row quadrants have staging
-    static constexpr uint32_t OUTS_BYTES = (ROWS == 64 ? 4 : 8) * OUT_BYTES;
-    static constexpr uint32_t BYTES = 1024 + TILES_BYTES + OUTS_BYTES + NUM_BARS * 8 + 32;
+    static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
     // registers: the launch's total (168 or 96 a thread) is shared out anew
     static constexpr int REGS_CTL = KIND == KIND_MM ? 56 : 48;
     static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 224 : 160;
     static constexpr int REGS_CONVERT = KIND == KIND_MM ? 0 : 56;
     static constexpr int REGS_TOTAL = 128 * REGS_CTL + 256 * (REGS_PROMOTE + REGS_CONVERT);
 };
-static_assert(Geo<KIND_MM, 2, 128>::REGS_TOTAL <= 384 * 168 && Geo<KIND_WG, 2, 128>::REGS_TOTAL <= 640 * 96, "register split");
+static_assert(Geo<KIND_MM, 2>::REGS_TOTAL <= 384 * 168 && Geo<KIND_WG, 2>::REGS_TOTAL <= 640 * 96, "register split");
 
-template <int KIND, int CG, int ROWS>
+template <int KIND, int CG>
 struct Smem {
-    using G = Geo<KIND, CG, ROWS>;
+    using G = Geo<KIND, CG>;
     uint8_t* base;  // tiles, codes, staging
     // shared-memory addresses.  Barriers per stage: full (KIND_MM: A and B have
     // landed; KIND_WG: A is converted), b_full (KIND_WG: B has landed), done
@@ -198,7 +198,7 @@ struct Smem {
         base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
         tiles = smem_u32(base);
         raw_tiles = tiles + G::STAGES * G::STAGE_BYTES;
-        full = tiles + G::TILES_BYTES + G::OUTS_BYTES;
+        full = tiles + G::TILES_BYTES + 8 * G::OUT_BYTES;
         done = full + 8 * G::STAGES;
         b_full = done + 8 * G::STAGES;
         raw_full = b_full + 8 * G::STAGES;
@@ -215,10 +215,7 @@ struct Smem {
     __device__ __forceinline__ uint32_t b(uint32_t s) const { return tiles + s * G::STAGE_BYTES + G::A_BYTES; }
     __device__ __forceinline__ uint32_t raw(uint32_t s) const { return raw_tiles + s * G::RAW_BYTES; }
     __device__ __forceinline__ uint8_t* at(uint32_t addr) const { return base + (addr - tiles); }
-    __device__ __forceinline__ uint8_t* out(int w) const {
-        if (ROWS == 64) w = (w >> 2) * 2 + (w & 1);
-        return base + G::TILES_BYTES + w * G::OUT_BYTES;
-    }
+    __device__ __forceinline__ uint8_t* out(int w) const { return base + G::TILES_BYTES + w * G::OUT_BYTES; }
 };
 
 // Position in a ring of N slots.
@@ -274,9 +271,9 @@ __device__ __forceinline__ Unit unit_of(const GemmParams& p, const Ctl& ctl, int
 // Loads.  KIND_MM: `which` 0 streams A and B.  KIND_WG: 0 streams the codes, 1
 // streams dY.  The odd CTA's pair loads count on the even CTA's barrier, so to
 // know that they have landed it waits until the MMA has read its last fill.
-template <int KIND, int CG, int ROWS>
-__device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG, ROWS>& sm, int which, int first, int step) {
-    using G = Geo<KIND, CG, ROWS>;
+template <int KIND, int CG>
+__device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, int which, int first, int step) {
+    using G = Geo<KIND, CG>;
     if constexpr (KIND == KIND_MM) {
         Ring<G::STAGES> st;
         Fills fills;
@@ -367,10 +364,10 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG, ROWS
 // elected lane issues.  A stage has few MMAs (four), so whatever else the loop
 // does per stage shows: with 128 x 128 tiles it takes longer than the MMAs, and
 // two issuers take the chunks in turn (each chunk has its own accumulator).
-template <int KIND, int CG, int ROWS>
-__device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG, ROWS>& sm, uint32_t tmem, int issuer, int first,
+template <int KIND, int CG>
+__device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm, uint32_t tmem, int issuer, int first,
                         int step) {
-    using G = Geo<KIND, CG, ROWS>;
+    using G = Geo<KIND, CG>;
     constexpr int CH = KIND == KIND_MM ? 1 : WG_CHUNK;
     // Descriptors.  K-major (A and B^T of KIND_MM): 8-row groups 1024 bytes
     // apart (stride offset), K steps of 32 codes 32 bytes further along the
@@ -468,13 +465,13 @@ __device__ __forceinline__ void store_out(const GemmParams& p, long long row, lo
 
 // A promotion warp: sums and epilogue of its 32 rows x COLS columns of each
 // tile, kept in fp32 registers.
-template <int KIND, int CG, int ROWS>
+template <int KIND, int CG>
 struct Worker {
-    using G = Geo<KIND, CG, ROWS>;
+    using G = Geo<KIND, CG>;
     static constexpr int COLS = G::COLS;
     const GemmParams& p;
     const Ctl& ctl;
-    Smem<KIND, CG, ROWS>& sm;
+    Smem<KIND, CG>& sm;
     const uint32_t tmem;
     const int w, lane, q, h;
     uint8_t* const stg;
@@ -482,7 +479,7 @@ struct Worker {
     uint32_t tiles_done = 0, stores = 0;
     unsigned long long acc[COLS / 2];  // pairs of fp32 sums
 
-    __device__ __forceinline__ Worker(const GemmParams& p_, const Ctl& c_, Smem<KIND, CG, ROWS>& s_, uint32_t t_, int w_, int lane_)
+    __device__ __forceinline__ Worker(const GemmParams& p_, const Ctl& c_, Smem<KIND, CG>& s_, uint32_t t_, int w_, int lane_)
         : p(p_), ctl(c_), sm(s_), tmem(t_), w(w_), lane(lane_), q(w_ & 3), h(w_ >> 2), stg(s_.out(w_)) {
         clear();
     }
@@ -520,6 +517,7 @@ struct Worker {
         const uint32_t buf = from.slot;
         if (!wait_bar(ctl, sm.acc_full + 8 * buf, from.phase, WAIT_ACC_FULL)) return false;
         from.next();
+        __syncwarp();  // tensor-memory loads are for the converged warp
         tc_fence_after();
         auto release = [&]() {
             tc_fence_before();
@@ -582,7 +580,7 @@ struct Worker {
     // rank * 16 / S ...) over all parts in order.  Every S makes 16 loads from
     // the other CTAs, all under way at once.
     template <int S>
-    __device__ __forceinline__ bool join(const Place& pl) {
+    __device__ __forceinline__ bool join(const Place& pl, bool more) {
         // the other parts have read what lay here before
         if (tiles_done > 0 && !wait_bar_cluster(ctl, sm.parts_out + 8 * w, (tiles_done - 1) & 1, WAIT_PARTS)) return false;
 #pragma unroll
@@ -638,16 +636,17 @@ struct Worker {
                 }
             }
         }
-        // the values above are in registers: the parts may lay their next sums
+        // the values above are in registers: the parts may lay their next sums,
+        // if there are any: a CTA on its way out gets no more arrivals
         __syncwarp();
-        if (lane < S) mbar_arrive_remote(map_to(sm.parts_out + 8 * w, lane));
+        if (more && lane < S) mbar_arrive_cluster(map_to(sm.parts_out + 8 * w, lane));
         return true;
     }
 
-    __device__ __forceinline__ bool epilogue(const Place& pl) {
+    __device__ __forceinline__ bool epilogue(const Place& pl, bool more) {
         if (CG == 1 && p.split > 1) {
             // not live in one part: not live in any
-            if (pl.live && !(p.split == 2 ? join<2>(pl) : p.split == 4 ? join<4>(pl) : join<8>(pl))) return false;
+            if (pl.live && !(p.split == 2 ? join<2>(pl, more) : p.split == 4 ? join<4>(pl, more) : join<8>(pl, more))) return false;
             clear();
             return true;
         }
@@ -711,10 +710,10 @@ struct Worker {
 };
 
 // Promotion warps; false = a wait gave up.
-template <int CG, int ROWS>
-__device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM, CG, ROWS>& sm, uint32_t tmem, int w, int lane,
+template <int CG>
+__device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM, CG>& sm, uint32_t tmem, int w, int lane,
                             int first, int step) {
-    Worker<KIND_MM, CG, ROWS> wk(p, ctl, sm, tmem, w, lane);
+    Worker<KIND_MM, CG> wk(p, ctl, sm, tmem, w, lane);
     for (int u = first; u < p.n_tiles; u += step) {
         const auto pl = wk.place(u);
         // A stage's two scales are fetched AHEAD stages ahead, into registers
@@ -722,8 +721,7 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
         // waited for: passing them from register to register would wait for
         // each within its stage.  Pairs unroll by two only, because three
         // copies of their longer loop no longer run from the instruction
-        // cache (8192^3: 411 us passed on, 394 with two, 444 with three; one
-        // token, 4096 x 14336: 18.7 passed on, 16.5 with two, 15.4 with four).
+        // cache (8192^3: 411 us passed on, 394 with two, 444 with three).
         // Rows below the last read its scales; past the last stage the last
         // one's are read.
         constexpr int AHEAD = CG == 2 ? 2 : 4;
@@ -752,20 +750,20 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
                 if (!wk.template promote<64>(pl.live, scale)) return false;
             }
         }
-        if (!wk.epilogue(pl)) return false;
+        if (!wk.epilogue(pl, u + step < p.n_tiles)) return false;
     }
     return true;
 }
 
 template <int CG>
-__device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG, 128>& sm, uint32_t tmem, int w, int lane,
+__device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, uint32_t tmem, int w, int lane,
                                int first, int step) {
-    Worker<KIND_WG, CG, 128> wk(p, ctl, sm, tmem, w, lane);
+    Worker<KIND_WG, CG> wk(p, ctl, sm, tmem, w, lane);
     for (int u = first; u < p.n_tiles; u += step) {
         const auto pl = wk.place(u);
         for (int s = pl.x.lo; s < pl.x.hi; s += WG_CHUNK)
             if (!wk.template promote<16>(pl.live, 1.f)) return false;
-        if (!wk.epilogue(pl)) return false;
+        if (!wk.epilogue(pl, u + step < p.n_tiles)) return false;
     }
     return true;
 }
@@ -778,8 +776,8 @@ __device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG
 // second column write their two units in the other order, so eight threads of
 // a row touch all banks once.
 template <int CG, bool BF16, bool E5M2>
-__device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG, 128>& sm, int t, int first, int step) {
-    using G = Geo<KIND_WG, CG, 128>;
+__device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, int t, int first, int step) {
+    using G = Geo<KIND_WG, CG>;
     Ring<G::RAWS> rs;
     Ring<G::STAGES> st;
     const int group = t >> 7, tt = t & 127;
@@ -838,11 +836,11 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
     }
 }
 
-template <int KIND, int CG, int ROWS>
-__global__ void __launch_bounds__(Geo<KIND, CG, ROWS>::THREADS, 1) block_gemm_kernel(const __grid_constant__ GemmParams p) {
-    using G = Geo<KIND, CG, ROWS>;
+template <int KIND, int CG>
+__global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(const __grid_constant__ GemmParams p) {
+    using G = Geo<KIND, CG>;
     extern __shared__ uint8_t smem_raw[];
-    Smem<KIND, CG, ROWS> sm;
+    Smem<KIND, CG> sm;
     sm.carve(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // CTAs per cluster: the pair, or the parts of the contraction
@@ -887,18 +885,18 @@ __global__ void __launch_bounds__(Geo<KIND, CG, ROWS>::THREADS, 1) block_gemm_ke
     if (warp < 4) {
         reg_dec<G::REGS_CTL>();
         if (warp == 0) {
-            if (lane == 0) run_tma<KIND, CG, ROWS>(p, ctl, sm, 0, first, step);
+            if (lane == 0) run_tma<KIND, CG>(p, ctl, sm, 0, first, step);
         } else if (KIND == KIND_WG && warp == 2) {
-            if (lane == 0) run_tma<KIND, CG, ROWS>(p, ctl, sm, 1, first, step);
+            if (lane == 0) run_tma<KIND, CG>(p, ctl, sm, 1, first, step);
         } else if (warp == 1) {
-            if (CG == 1 || rank == 0) run_mma<KIND, CG, ROWS>(p, ctl, sm, tmem, 0, first, step);
+            if (CG == 1 || rank == 0) run_mma<KIND, CG>(p, ctl, sm, tmem, 0, first, step);
         }
-        if (G::ISSUERS == 2 && warp == 3) run_mma<KIND, CG, ROWS>(p, ctl, sm, tmem, 1, first, step);
+        if (G::ISSUERS == 2 && warp == 3) run_mma<KIND, CG>(p, ctl, sm, tmem, 1, first, step);
         __syncwarp();
     } else if (warp < 12) {
         reg_inc<G::REGS_PROMOTE>();
         if constexpr (KIND == KIND_MM)
-            run_promote_mm<CG, ROWS>(p, ctl, sm, tmem, warp - 4, lane, first, step);
+            run_promote_mm<CG>(p, ctl, sm, tmem, warp - 4, lane, first, step);
         else
             run_promote_wg<CG>(p, ctl, sm, tmem, warp - 4, lane, first, step);
         if (lane == 0) bulk_wait_all();  // its stores have left shared memory, stopped or not
