@@ -252,7 +252,7 @@ struct Plan {
 // weight gradient: 57 us whole, 26 split over 4).  Element stores, for outputs
 // that no tensor store can reach, cost a tile about 2 us and a meeting 6.
 double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, bool direct) {
-    const double stage = wg ? (v == PAIR ? 0.47 : 0.40) : (v == PAIR ? 0.45 : 0.30);
+    const double stage = wg ? (v == PAIR ? 0.47 : 0.40) : (v == PAIR ? 0.45 : v == CTA ? 0.32 : v == FEW16 ? 0.27 : 0.42);
     double tile = part * stage + (v == PAIR ? 2.0 : 1.0);
     if (split > 1)
         tile += v >= FEW16 ? 2.0 : 4.5 + (direct ? 0.0 : 6.0);
@@ -275,14 +275,16 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
     const int grid = cfg->grid ? cfg->grid : d.sms;
     double best = 0;
     pl.cg = 0;
-    for (int cg = 1; cg <= 2; ++cg) {
+    for (int i = PAIR; i <= FEW32; ++i) {
+        const Variant v = static_cast<Variant>(i);
+        const int cg = v == PAIR ? 2 : 1;
         if (cfg->tile_m && cfg->tile_m != 128 * cg) continue;
+        if (v >= FEW16 && (wg || rows > (v == FEW16 ? 16 : 32))) continue;
         const int64_t mb = cdiv(rows, 128 * cg), nb = cdiv(cols, 128 * cg), tiles = mb * nb;
         if (tiles > 0x7FFFFFFF) continue;
         for (int lg = 0; lg < (cg == 2 ? 1 : 4); ++lg) {
             const int split = 1 << lg;
             const int64_t part = cdiv(stages, split);
-            const Variant v = cg == 2 ? PAIR : wg || rows > 32 ? CTA : rows <= 16 ? FEW16 : FEW32;
             const int slots = std::min(d.clusters[wg][v][cg == 2 ? 1 : lg], grid / (cg * split));
             if (slots < 1) continue;
             // every part has stages (an empty one, where the config asks for it, adds zeros)
@@ -394,7 +396,7 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
         p.codes_e5m2 = a_type == IRIS_E5M2;
     } else {
         p.b_mn = !b.transposed;
-        const bool few = pl.variant == FEW16 || pl.variant == FEW32;
+        const bool few = pl.variant >= FEW16;
         p.a_box = pl.variant == FEW16 ? 16 : pl.variant == FEW32 ? 32 : 128;
         if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, p.a_box, true))) return rc;
         if ((rc = make_map_2d(&p.tmB, u8, 1, b, 128, 128, true))) return rc;

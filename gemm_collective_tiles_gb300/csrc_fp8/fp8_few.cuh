@@ -35,9 +35,9 @@ struct FewGeo {
     static constexpr uint32_t SUMS = NT * 128;  // fp32 sums of one group
     static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES;
     static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 4;
-    static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 2 * SUMS * 4 + NUM_BARS * 8 + 32;
+    static constexpr uint32_t SCALE_BYTES = 8 * 2 * NT * 4;  // per promotion warp: the tokens' scales of two stages
+    static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 2 * SUMS * 4 + SCALE_BYTES + NUM_BARS * 8 + 32;
     static constexpr int THREADS = 384;
-    static_assert(NT == 16 || NT == 32, "a lane holds the scale of one token");
 };
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
     uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t tiles = smem_u32(base);
     float* const sums = reinterpret_cast<float*>(base + G::TILES_BYTES);
-    const uint32_t full = tiles + G::TILES_BYTES + 2 * G::SUMS * 4, done = full + 8 * G::STAGES;
+    float* const scales = sums + 2 * G::SUMS;
+    const uint32_t full = tiles + G::TILES_BYTES + 2 * G::SUMS * 4 + G::SCALE_BYTES, done = full + 8 * G::STAGES;
     const uint32_t acc_full = done + 8 * G::STAGES, acc_empty = acc_full + 8 * G::ACCS;
     const uint32_t parts_in = acc_empty + 8 * G::ACCS, parts_out = parts_in + 8, final_bar = parts_out + 8;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base + (final_bar + 16 - tiles));
@@ -149,7 +150,8 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
         const int w = warp - 4, q = w & 3, group = w >> 2;
         Ring<G::ACCS> acc;
         uint32_t tiles_done = 0;
-        constexpr int AHEAD = 4;
+        constexpr int AHEAD = NT == 16 ? 4 : 2;
+        float* const my_scales = scales + w * 2 * NT;
         bool ok = true;
         for (int u = first; u < p.n_tiles && ok; u += step) {
             const int col0 = u * 128;
@@ -157,8 +159,10 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
             unsigned long long sum[NT / 2];
 #pragma unroll
             for (int i = 0; i < NT / 2; ++i) sum[i] = 0ull;
-            // this group's stages; lane l holds the scales of token l, AHEAD of
-            // its stages ahead, in registers of their own
+            // this group's stages; lane l fetches the scales of token l, AHEAD
+            // of its stages ahead, into registers of their own, and hands them
+            // round through shared memory (a read of four tokens'
+            // scales costs what a shuffle of one does)
             const int mine = lo + ((lo & 1) != group);
             const float* pa = p.sa + min(lane, p.M - 1) * p.sa_rs + mine * p.sa_cs;
             const float* pb = p.sb + u * p.sb_cs + mine * p.sb_rs;
@@ -181,7 +185,8 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
                     if (s + 2 * j >= hi) break;
-                    const float f = a[j] * b[j];
+                    float* const f = my_scales + (j & 1) * NT;
+                    if (lane < NT) f[lane] = a[j] * b[j];
                     fetch(a[j], b[j]);
                     if (!wait_bar(ctl, acc_full + 8 * acc.slot, acc.phase, WAIT_ACC_FULL)) {
                         ok = false;
@@ -202,10 +207,10 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
                     if (s + 2 * j + 1 < hi) acc.next();
                     if (live) {
 #pragma unroll
-                        for (int i = 0; i < NT / 2; ++i) {
-                            const uint32_t f0 = __float_as_uint(__shfl_sync(0xFFFFFFFFu, f, 2 * i));
-                            const uint32_t f1 = __float_as_uint(__shfl_sync(0xFFFFFFFFu, f, 2 * i + 1));
-                            sum[i] = fma_f32x2(pack_f32x2(r[2 * i], r[2 * i + 1]), pack_f32x2(f0, f1), sum[i]);
+                        for (int i = 0; i < NT / 4; ++i) {
+                            const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(f + 4 * i);
+                            sum[2 * i] = fma_f32x2(pack_f32x2(r[4 * i], r[4 * i + 1]), f4.x, sum[2 * i]);
+                            sum[2 * i + 1] = fma_f32x2(pack_f32x2(r[4 * i + 2], r[4 * i + 3]), f4.y, sum[2 * i + 1]);
                         }
                     }
                 }

@@ -159,11 +159,12 @@ struct Geo {
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
     // a stage holds one A and one B box; KIND_WG: the converted A and B, and
     // the codes have a ring of their own (RAWS slots)
-    static constexpr int STAGES = KIND == KIND_MM && CG == 2 ? 5 : 4;
+    static constexpr int STAGES = KIND == KIND_WG ? 4 : CG == 2 ? 5 : 6;
     static constexpr int RAWS = KIND == KIND_MM ? 0 : 4;
     static constexpr int ISSUERS = KIND == KIND_MM && CG == 1 ? 2 : 1;  // warps that issue MMAs
     static constexpr int THREADS = KIND == KIND_MM ? 384 : 640;
-    static constexpr uint32_t OUT_BYTES = 2 * 32 * 128;  // staging per promotion warp: two boxes
+    static constexpr int BOXES = KIND == KIND_MM && CG == 1 ? 1 : 2;  // staging per promotion warp, 32 x 128 bytes each
+    static constexpr uint32_t OUT_BYTES = BOXES * 32 * 128;
     static constexpr int TMEM_COLS = 512;
     static constexpr int ACCS = TMEM_COLS / BN;        // accumulators under way
     // Two warps that take turns at a ring (issuers, converter groups) each own
@@ -476,7 +477,7 @@ struct Worker {
     const int w, lane, q, h;
     uint8_t* const stg;
     Ring<G::ACCS> from;  // the accumulator that the next chunk will be in
-    uint32_t tiles_done = 0, stores = 0;
+    uint32_t rounds = 0, stores = 0;
     unsigned long long acc[COLS / 2];  // pairs of fp32 sums
 
     __device__ __forceinline__ Worker(const GemmParams& p_, const Ctl& c_, Smem<KIND, CG>& s_, uint32_t t_, int w_, int lane_)
@@ -575,71 +576,77 @@ struct Worker {
     }
 
     // Split contraction over S CTAs: each warp lays its 32 x 64 sums into shared
-    // memory (rows of 16 units of 16 bytes, XORed with the row), tells the same
-    // warp of every part, and adds its part's share of the columns (units
-    // rank * 16 / S ...) over all parts in order.  Every S makes 16 loads from
-    // the other CTAs, all under way at once.
+    // memory, as many columns at a time as its staging holds (rows of units of
+    // 16 bytes, XORed with the row), tells the same warp of every part, and adds
+    // its part's share of them over all parts in order.  The loads from the
+    // other CTAs are all under way at once.
     template <int S>
     __device__ __forceinline__ bool join(const Place& pl, bool more) {
-        // the other parts have read what lay here before
-        if (tiles_done > 0 && !wait_bar_cluster(ctl, sm.parts_out + 8 * w, (tiles_done - 1) & 1, WAIT_PARTS)) return false;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            float v[4];
-            unpack_f32x2(acc[2 * j], v[0], v[1]);
-            unpack_f32x2(acc[2 * j + 1], v[2], v[3]);
-            *reinterpret_cast<float4*>(stg + lane * 256 + ((j ^ (lane & 15)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
-        }
-        __syncwarp();
-        if (lane < S) mbar_arrive_cluster(map_to(sm.parts_in + 8 * w, lane));
-        if (!wait_bar_cluster(ctl, sm.parts_in + 8 * w, tiles_done & 1, WAIT_PARTS)) return false;
-        ++tiles_done;
-        constexpr int UNITS = 16 / S;
-        const uint32_t mine = smem_u32(stg) + lane * 256;
-        float4 t[UNITS][S];
-#pragma unroll
-        for (int k = 0; k < S; ++k) {
-            const uint32_t from_k = map_to(mine, k);
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i)
-                t[i][k] = ld_shared_cluster_f4(from_k + (((ctl.rank * UNITS + i) ^ (lane & 15)) << 4));
-        }
+        constexpr int UNITS = G::OUT_BYTES / 512, ROUNDS = 16 / UNITS, SHARE = UNITS / S;
+        const uint32_t row_at = lane * UNITS * 16;
         const int row = pl.row0 + lane;
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            float4 sum = t[i][0];
+        for (int r = 0; r < ROUNDS; ++r) {
+            // the other parts have read what lay here before
+            if (rounds > 0 && !wait_bar_cluster(ctl, sm.parts_out + 8 * w, (rounds - 1) & 1, WAIT_PARTS)) return false;
+            __syncwarp();
 #pragma unroll
-            for (int k = 1; k < S; ++k) {
-                sum.x += t[i][k].x;
-                sum.y += t[i][k].y;
-                sum.z += t[i][k].z;
-                sum.w += t[i][k].w;
+            for (int j = 0; j < UNITS; ++j) {
+                float v[4];
+                unpack_f32x2(acc[2 * (r * UNITS + j)], v[0], v[1]);
+                unpack_f32x2(acc[2 * (r * UNITS + j) + 1], v[2], v[3]);
+                *reinterpret_cast<float4*>(stg + row_at + ((j ^ (lane & (UNITS - 1))) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
             }
-            const int c = col_of(pl, 0) + (ctl.rank * UNITS + i) * 4;
-            float v[4] = {sum.x, sum.y, sum.z, sum.w};
-            if (KIND == KIND_MM && p.bias) {
+            __syncwarp();
+            if (lane < S) mbar_arrive_cluster(map_to(sm.parts_in + 8 * w, lane));
+            if (!wait_bar_cluster(ctl, sm.parts_in + 8 * w, rounds & 1, WAIT_PARTS)) return false;
+            __syncwarp();
+            ++rounds;
+            const uint32_t mine = smem_u32(stg) + row_at;
+            float4 t[SHARE][S];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += load_bias(p, c + e);
+            for (int k = 0; k < S; ++k) {
+                const uint32_t from_k = map_to(mine, k);
+#pragma unroll
+                for (int i = 0; i < SHARE; ++i)
+                    t[i][k] = ld_shared_cluster_f4(from_k + (((ctl.rank * SHARE + i) ^ (lane & (UNITS - 1))) << 4));
             }
-            if (row < p.M) {
-                if (p.tma_out && c + 4 <= p.N) {  // unit stride, rows on 16 bytes
-                    const long long o = row * p.out_rs + c;
-                    if (p.out_type == T_F32)
-                        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
-                    else
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
-                            make_uint2(pack16(v[0], v[1], p.out_type == T_BF16), pack16(v[2], v[3], p.out_type == T_BF16));
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < p.N) store_out(p, row, c + e, v[e]);
+            for (int i = 0; i < SHARE; ++i) {
+                float4 sum = t[i][0];
+#pragma unroll
+                for (int k = 1; k < S; ++k) {
+                    sum.x += t[i][k].x;
+                    sum.y += t[i][k].y;
+                    sum.z += t[i][k].z;
+                    sum.w += t[i][k].w;
+                }
+                const int c = col_of(pl, 0) + (r * UNITS + ctl.rank * SHARE + i) * 4;
+                float v[4] = {sum.x, sum.y, sum.z, sum.w};
+                if (KIND == KIND_MM && p.bias) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += load_bias(p, c + e);
+                }
+                if (row < p.M) {
+                    if (p.tma_out && c + 4 <= p.N) {  // unit stride, rows on 16 bytes
+                        const long long o = row * p.out_rs + c;
+                        if (p.out_type == T_F32)
+                            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+                        else
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
+                                make_uint2(pack16(v[0], v[1], p.out_type == T_BF16), pack16(v[2], v[3], p.out_type == T_BF16));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (c + e < p.N) store_out(p, row, c + e, v[e]);
+                    }
                 }
             }
+            // the values above are in registers: the parts may lay their next
+            // sums, if there are any: a CTA on its way out gets no more arrivals
+            __syncwarp();
+            if ((more || r + 1 < ROUNDS) && lane < S) mbar_arrive_cluster(map_to(sm.parts_out + 8 * w, lane));
         }
-        // the values above are in registers: the parts may lay their next sums,
-        // if there are any: a CTA on its way out gets no more arrivals
-        __syncwarp();
-        if (more && lane < S) mbar_arrive_cluster(map_to(sm.parts_out + 8 * w, lane));
         return true;
     }
 
@@ -650,8 +657,8 @@ struct Worker {
             clear();
             return true;
         }
-        // 32 rows x 128 bytes at a time through swizzled staging, two boxes in
-        // turn; the sums are rounded here, once
+        // 32 rows x 128 bytes at a time through swizzled staging; the sums are
+        // rounded here, once
         if (pl.live) {
             const bool wide = p.out_type == T_F32;
             const bool add_bias = KIND == KIND_MM && p.bias != nullptr;
@@ -666,10 +673,10 @@ struct Worker {
                     for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
                 }
                 if (wide || (c & 1) == 0) {  // a staging box is used anew
-                    if (lane == 0) bulk_wait_read<1>();
+                    if (lane == 0) bulk_wait_read<G::BOXES - 1>();
                     __syncwarp();
                 }
-                uint8_t* box = stg + (stores & 1) * 4096;
+                uint8_t* box = stg + (stores % G::BOXES) * 4096;
                 if (wide) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
