@@ -203,13 +203,13 @@ int launch_repack(const iris_b200_mat* m, Operand& o, void* dst, int sms, cudaSt
     return IRIS_OK;
 }
 
-int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand& o, uint32_t b0, uint32_t b1, bool swizzle) {
+int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand& o, uint32_t b0, uint32_t b1) {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.pitch) * elem};
     cuuint32_t box[2] = {b0, b1}, es[2] = {1, 1};
     const CUresult r = g_encode(m, dt, 2, const_cast<void*>(o.data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit operand)", static_cast<int>(r));
 }
 // 16-bit rows as groups of 64 columns, {64, row, column / 64}: a box of 64 rows
@@ -383,12 +383,12 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (wg) {
         const CUtensorMapDataType t16 = b_type == IRIS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-        if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, 64, false))) return rc;
+        if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, 64))) return rc;
         // one box of all of a CTA's columns where no 64-column group runs past
         // the end of a row, else a box per group
         p.b_chunked = cols % 64 == 0;
         if ((rc = p.b_chunked ? make_map_groups(&p.tmB, t16, b, 2)
-                              : make_map_2d(&p.tmB, t16, 2, b, 64, 64, true)))
+                              : make_map_2d(&p.tmB, t16, 2, b, 64, 64)))
             return rc;
         const int t = b_type == IRIS_BF16;
         p.idesc = idesc_of(t, t, 1, 1, 128 * pl.cg, 128 * pl.cg);
@@ -398,8 +398,8 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
         p.b_mn = !b.transposed;
         const bool few = pl.variant >= FEW16;
         p.a_box = pl.variant == FEW16 ? 16 : pl.variant == FEW32 ? 32 : 128;
-        if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, p.a_box, true))) return rc;
-        if ((rc = make_map_2d(&p.tmB, u8, 1, b, 128, 128, true))) return rc;
+        if ((rc = make_map_2d(&p.tmA, u8, 1, a, 128, p.a_box))) return rc;
+        if ((rc = make_map_2d(&p.tmB, u8, 1, b, 128, 128))) return rc;
         // few rows: the weights are the MMA's first operand
         p.idesc = few ? idesc_of(b_type, a_type, p.b_mn, 0, 128, p.a_box)
                       : idesc_of(a_type, b_type, 0, p.b_mn, 128 * pl.cg, 128 * pl.cg);

@@ -79,7 +79,7 @@ struct WsHeader {
 static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 
 struct GemmParams {
-    CUtensorMap tmA;  // MM: codes {k, row}, box {128, a_box}; WG: codes {k, m}, box {128, 64}, no swizzle
+    CUtensorMap tmA;  // MM: codes {k, row}, box {128, a_box}; WG: codes {k, m}, box {128, 64}
     CUtensorMap tmB;  // MM: codes {k, n} or {n, k}, box {128, 128}; WG: dY {n, m}, box {64, 64}
     CUtensorMap tmC;  // out {n, row}, box {128 bytes, 32}
     int M, N;         // output rows and columns
@@ -443,7 +443,7 @@ __device__ __forceinline__ void convert16(const uint4& c, float scale, uint32_t 
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t h = cvt_f8x2_f16x2(w[j / 2] >> (16 * (j & 1)), E5M2);
+        const uint32_t h = cvt_f8x2_f16x2<E5M2>(w[j / 2], j & 1);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
         o[j] = pack16(f.x * scale, f.y * scale, BF16);
     }
@@ -777,47 +777,55 @@ __device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG
 
 // Conversion: 64 x 128 codes -> 16-bit values times their row's scale, in the
 // MN-major swizzled layout (two columns of 64 k, rows of 128 bytes, 16-byte
-// units XORed with the row).  Two groups of four warps take the stages in
-// turn, so one stage's latencies (barrier, shared memory, fence) pass under the
-// other's arithmetic.  A thread takes 16 codes of four rows; threads of the
-// second column write their two units in the other order, so eight threads of
-// a row touch all banks once.
+// units XORed with the row; the codes lie swizzled alike).  Two groups of four
+// warps take the stages in turn, so one stage's latencies (barrier, shared
+// memory, fence) pass under the other's arithmetic.  A thread takes 16 codes
+// of four rows, 16 apart.  Eight neighbouring threads take half of two rows
+// whose numbers differ in bits 0 and 2: their codes' units and their results'
+// units then are eight different ones, so no bank is asked twice.
 template <int CG, bool BF16, bool E5M2>
 __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, int t, int first, int step) {
     using G = Geo<KIND_WG, CG>;
     Ring<G::RAWS> rs;
     Ring<G::STAGES> st;
     const int group = t >> 7, tt = t & 127;
-    const int seg = tt & 7, r0 = tt >> 3, col = seg >> 2, j0 = (seg & 3) * 2;
-    // offsets of the two units of row r0 in a slot; rows r0 + 16 i have the same XOR
-    const uint32_t u0 = col * 8192 + r0 * 128 + ((j0 ^ (r0 & 7)) << 4);
-    const uint32_t u1 = col * 8192 + r0 * 128 + (((j0 + 1) ^ (r0 & 7)) << 4);
+    const int col = tt >> 3 & 1, j = tt & 3;                 // column of 64 k, quarter of it
+    const int r0 = (tt >> 4) * 2 ^ ((tt & 4) ? 5 : 0);        // first row
+    // offsets in a slot; rows r0 + 16 i have the same XOR
+    const uint32_t from = r0 * 128 + (((col * 4 + j) ^ (r0 & 7)) << 4);
+    const uint32_t to0 = col * 8192 + r0 * 128 + (((2 * j) ^ (r0 & 7)) << 4);
+    const uint32_t to1 = col * 8192 + r0 * 128 + (((2 * j + 1) ^ (r0 & 7)) << 4);
+    const long long apart = 16 * p.sa_rs;
     int turn = 0;  // stages so far, over all units
     for (int u = first; u < p.n_tiles; u += step) {
         const Unit x = unit_of<CG>(p, ctl, u);
-        // this CTA's 128 output rows are one block of scales
+        // this CTA's 128 output rows are one block of scales; a stage's are
+        // fetched one turn (two stages) ahead.  Rows past the last count as 0.
         const int kblk = x.mb * CG + half<CG>(ctl);
-        const bool live = kblk * BM < p.M;
-        const float* sx = p.sa + kblk * p.sa_cs;
-        // a stage's scales are fetched one turn (two stages) ahead
+        const int s0 = x.lo + ((turn & 1) != group);
+        const float* at = p.sa + kblk * p.sa_cs + (static_cast<long long>(s0) * G::DEPTH + r0) * p.sa_rs;
+        int left = kblk * BM < p.M ? min(p.D, x.hi * G::DEPTH) - s0 * G::DEPTH - r0 : 0;  // rows from `at` on
         float next[4];
-        auto fetch = [&](int s) {
+        auto fetch = [&]() {
+            const float* q = at;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int m = s * G::DEPTH + r0 + 16 * i;
-                next[i] = (live && s < x.hi && m < p.D) ? __ldg(sx + m * p.sa_rs) : 0.f;
+                next[i] = 16 * i < left ? __ldg(q) : 0.f;
+                q += apart;
             }
+            at += 8 * apart;
+            left -= 2 * G::DEPTH;
         };
-        fetch(x.lo + ((turn & 1) != group));
+        fetch();
         for (int s = x.lo; s < x.hi; ++s, ++turn, rs.next(), st.next()) {
             if ((turn & 1) != group) continue;
             float sc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[i] = next[i];
-            fetch(s + 2);
+            fetch();
             if (!wait_bar(ctl, sm.raw_full + 8 * rs.slot, rs.phase, WAIT_RAW)) return;
             if (!wait_bar(ctl, sm.done + 8 * st.slot, st.phase ^ 1, WAIT_A_EMPTY)) return;
-            const uint8_t* src = sm.at(sm.raw(rs.slot)) + r0 * 128 + seg * 16;
+            const uint8_t* src = sm.at(sm.raw(rs.slot)) + from;
             uint8_t* dst = sm.at(sm.a(st.slot));
             uint4 c4 = *reinterpret_cast<const uint4*>(src);
 #pragma unroll
@@ -826,9 +834,8 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
                 if (i < 3) c4 = *reinterpret_cast<const uint4*>(src + (i + 1) * 2048);
                 uint32_t o[8];
                 convert16<BF16, E5M2>(c, sc[i], o);
-                const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
-                *reinterpret_cast<uint4*>(dst + (col ? u1 : u0) + i * 2048) = col ? v1 : v0;
-                *reinterpret_cast<uint4*>(dst + (col ? u0 : u1) + i * 2048) = col ? v0 : v1;
+                *reinterpret_cast<uint4*>(dst + to0 + i * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(dst + to1 + i * 2048) = make_uint4(o[4], o[5], o[6], o[7]);
             }
             fence_proxy_async_shared();
             __syncwarp();

@@ -264,14 +264,17 @@ __device__ __forceinline__ uint32_t cvt_f8x2(float lo, float hi, int e5m2) {
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
     return v;
 }
-// two 8-bit codes -> f16x2 (exact: both types' values are f16 values)
-__device__ __forceinline__ uint32_t cvt_f8x2_f16x2(uint32_t codes, int e5m2) {
+// the low or high two of four 8-bit codes -> f16x2 (exact: both types' values
+// are f16 values)
+template <bool E5M2>
+__device__ __forceinline__ uint32_t cvt_f8x2_f16x2(uint32_t codes, int high) {
+    uint16_t lo, hi;
     uint32_t v;
-    const uint16_t c = static_cast<uint16_t>(codes);
-    if (e5m2)
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(v) : "h"(c));
+    asm("mov.b32 {%0, %1}, %2;" : "=h"(lo), "=h"(hi) : "r"(codes));
+    if (E5M2)
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(v) : "h"(high ? hi : lo));
     else
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"(c));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"(high ? hi : lo));
     return v;
 }
 
