@@ -177,8 +177,8 @@ struct Geo {
     static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
     // registers: the launch's total (168 or 96 a thread) is shared out anew
     static constexpr int REGS_CTL = KIND == KIND_MM ? 56 : 48;
-    static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 224 : 160;
-    static constexpr int REGS_CONVERT = KIND == KIND_MM ? 0 : 56;
+    static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 224 : 152;
+    static constexpr int REGS_CONVERT = KIND == KIND_MM ? 0 : 64;
     static constexpr int REGS_TOTAL = 128 * REGS_CTL + 256 * (REGS_PROMOTE + REGS_CONVERT);
 };
 static_assert(Geo<KIND_MM, 2>::REGS_TOTAL <= 384 * 168 && Geo<KIND_WG, 2>::REGS_TOTAL <= 640 * 96, "register split");
