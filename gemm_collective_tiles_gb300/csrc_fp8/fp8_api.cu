@@ -241,8 +241,13 @@ int make_store_map(CUtensorMap* m, int t, const void* data, int64_t N, int64_t M
 struct Plan {
     Variant variant;
     int cg, split, part_stages, stages, m_blocks, n_blocks, group_m, grid;
-    size_t copy_a, copy_b, total;  // workspace offsets
+    int tail_tiles;  // pairs: tiles of the last round that are cut in two
+    size_t copy_a, copy_b, tail, total;  // workspace offsets
 };
+
+// Tail tiles: 2 CTAs x 8 promotion warps each hand over 32 x 128 fp32 sums.
+constexpr size_t TAIL_SUMS = 32 * 128 * 4;
+size_t tail_flag_bytes(int tiles) { return round_up(size_t(tiles) * 16 * 8, 256); }
 
 // Estimated time in us of a variant: `slots` clusters run at once and take the
 // tiles in turn; a tile costs `part` stages, its epilogue and, where its
@@ -251,13 +256,14 @@ struct Plan {
 // over 8; 100 x 1000 x 3000: 7.8 us whole, 11.4 split over 2; 8192 x 512 x 512
 // weight gradient: 57 us whole, 26 split over 4).  Element stores, for outputs
 // that no tensor store can reach, cost a tile about 2 us and a meeting 6.
-double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, bool direct) {
+double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, bool direct, bool tail) {
     const double stage = wg ? (v == PAIR ? 0.47 : 0.40) : (v == PAIR ? 0.45 : v == CTA ? 0.32 : v == FEW16 ? 0.27 : 0.42);
     double tile = part * stage + (v == PAIR ? 2.0 : 1.0);
     if (split > 1)
         tile += v >= FEW16 ? 2.0 : 4.5 + (direct ? 0.0 : 6.0);
     else if (!direct && v <= CTA)
         tile += 2.0;
+    if (tail) return 4.5 + tiles / slots * tile + part * stage / 2 + 8.0;
     return 4.5 + cdiv(tiles, slots) * tile;
 }
 
@@ -289,7 +295,13 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
             if (slots < 1) continue;
             // every part has stages (an empty one, where the config asks for it, adds zeros)
             if (cfg->k_split ? split != cfg->k_split : part * (split - 1) >= stages) continue;
-            const double t = estimate(wg, v, slots, tiles, part, split, direct);
+            // A last round with at most half of the pairs at work: cut its
+            // tiles in two, where half a tile's time outweighs handing over
+            // the sums (weight gradient over 16384 tokens, 4096 x 4096: 3.4 rounds
+            // in 401 us, whole in 448)
+            const int64_t last = tiles % slots;
+            const bool tail = v == PAIR && last > 0 && 2 * last <= slots && part >= 32;
+            const double t = estimate(wg, v, slots, tiles, part, split, direct, tail);
             if (pl.cg == 0 || t < best) {
                 best = t;
                 pl.cg = cg;
@@ -298,7 +310,8 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
                 pl.part_stages = static_cast<int>(part);
                 pl.m_blocks = static_cast<int>(mb);
                 pl.n_blocks = static_cast<int>(nb);
-                pl.grid = static_cast<int>(std::min<int64_t>(tiles, slots)) * cg * split;
+                pl.tail_tiles = tail ? static_cast<int>(last) : 0;
+                pl.grid = static_cast<int>(std::min<int64_t>(tiles + pl.tail_tiles, slots)) * cg * split;
             }
         }
     }
@@ -307,7 +320,8 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
     pl.group_m = cfg->group_m ? std::max(1, cfg->group_m / pl.cg) : 16 / pl.cg;
     pl.copy_a = WS_HEADER;
     pl.copy_b = pl.copy_a + a.copy_bytes;
-    pl.total = pl.copy_b + b.copy_bytes;
+    pl.tail = pl.copy_b + b.copy_bytes;
+    pl.total = pl.tail + (pl.tail_tiles ? tail_flag_bytes(pl.tail_tiles) + size_t(pl.tail_tiles) * 16 * TAIL_SUMS : 0);
     return IRIS_OK;
 }
 
@@ -416,7 +430,11 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
     p.m_blocks = pl.m_blocks;
     p.n_blocks = pl.n_blocks;
     p.group_m = pl.group_m;
-    p.n_tiles = pl.m_blocks * pl.n_blocks;
+    p.tail_tiles = pl.tail_tiles;
+    p.tail_first = pl.m_blocks * pl.n_blocks - pl.tail_tiles;
+    p.n_units = p.tail_first + 2 * pl.tail_tiles;
+    p.tail_flag = reinterpret_cast<unsigned long long*>(w + pl.tail);
+    p.tail_sums = reinterpret_cast<unsigned long long*>(w + pl.tail + tail_flag_bytes(pl.tail_tiles));
     p.ws = reinterpret_cast<WsHeader*>(w);
     p.tma_out = direct;
     p.wait_ns = cfg && cfg->wait_ns ? cfg->wait_ns : DEFAULT_WAIT_NS;

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
             Ring<G::STAGES> st;
             Fills fills;
             bool ok = true;
-            for (int u = first; u < p.n_tiles && ok; u += step)
+            for (int u = first; u < p.n_units && ok; u += step)
                 for (int s = lo; s < hi; ++s) {
                     if (!wait_bar(ctl, done + 8 * st.slot, st.phase ^ 1, WAIT_EMPTY)) {
                         ok = false;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
         Ring<G::STAGES> st;
         Ring<G::ACCS> acc;
         bool ok = true;
-        for (int u = first; u < p.n_tiles && ok; u += step) {
+        for (int u = first; u < p.n_units && ok; u += step) {
             const bool report = p.debug_skip != static_cast<uint32_t>(u) + 1;
             for (int s = lo; s < hi; ++s, st.next(), acc.next()) {
                 if ((acc.slot & 1) != issuer) continue;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
         constexpr int AHEAD = NT == 16 ? 4 : 2;
         float* const my_scales = scales + w * 2 * NT;
         bool ok = true;
-        for (int u = first; u < p.n_tiles && ok; u += step) {
+        for (int u = first; u < p.n_units && ok; u += step) {
             const int col0 = u * 128;
             const bool live = col0 + q * 32 < p.N;
             unsigned long long sum[NT / 2];
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
             // tell the parts that their sums have been read, unless none will
             // write again: a CTA on its way out gets no more arrivals
             __syncwarp();
-            if (u + step < p.n_tiles) {
+            if (u + step < p.n_units) {
                 if (S == 1) {
                     if (lane == 0) bar_arrive(parts_out);
                 } else if (lane < S) {

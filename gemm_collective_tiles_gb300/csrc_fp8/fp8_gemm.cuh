@@ -61,6 +61,7 @@ enum : int {
     WAIT_RAW = 106,
     WAIT_A_EMPTY = 107,
     WAIT_PARTS = 108,
+    WAIT_TAIL = 109,
     WAIT_DRAIN_TMA = 120,  // from here on: teardown
     WAIT_DRAIN_MMA = 121,
 };
@@ -85,7 +86,9 @@ struct GemmParams {
     int M, N;         // output rows and columns
     int D;            // contraction length
     int stages_total, part_stages, split;  // contraction in stages; stages per part; parts
-    int m_blocks, n_blocks, group_m, n_tiles;
+    int m_blocks, n_blocks, group_m;
+    int n_units;      // work units: tiles, and two halves of each tail tile (pairs)
+    int tail_first, tail_tiles;
     int b_mn;         // MM: B has its columns contiguous
     int b_chunked;    // WG: tmB is {64, m, n / 64}, one box per stage
     int a_box;        // MM: rows of A that a stage loads
@@ -102,6 +105,8 @@ struct GemmParams {
     long long out_rs, out_cs;
     WsHeader* ws;
     int tma_out;                  // tensor stores can write the output
+    unsigned long long* tail_flag;  // per (tail tile, CTA, promotion warp): a first half's sums are in tail_sums
+    unsigned long long* tail_sums;  // 32 x 128 fp32 each, in pairs of columns, a lane per row
     unsigned long long wait_ns;
     uint32_t debug_skip;          // test hook: k > 0: tile k - 1 never reports its accumulator
 };
@@ -253,12 +258,21 @@ __device__ __forceinline__ int half(const Ctl& ctl) {
 
 struct Unit {
     int mb, nb, lo, hi;  // tile and this CTA's stages of it
+    int tail;            // pairs: half * tail_tiles + index of a tail tile, or -1
 };
 // Tiles in groups of group_m rows of tiles, so the tiles running at once share
-// their operands in L2.
+// their operands in L2.  The tiles of a last round that would keep at most half
+// of the pairs busy are cut into two halves of the contraction, all first
+// halves before all second ones.
 template <int CG>
-__device__ __forceinline__ Unit unit_of(const GemmParams& p, const Ctl& ctl, int t) {
+__device__ __forceinline__ Unit unit_of(const GemmParams& p, const Ctl& ctl, int u) {
     Unit x;
+    int t = u;
+    x.tail = -1;
+    if (CG == 2 && u >= p.tail_first) {
+        x.tail = u - p.tail_first;
+        t = p.tail_first + x.tail % p.tail_tiles;
+    }
     const int per = p.group_m * p.n_blocks;
     const int g = t / per, first = g * p.group_m;
     const int rows = min(p.group_m, p.m_blocks - first), in = t - g * per;
@@ -266,6 +280,12 @@ __device__ __forceinline__ Unit unit_of(const GemmParams& p, const Ctl& ctl, int
     x.nb = in / rows;
     x.lo = CG == 1 ? ctl.rank * p.part_stages : 0;
     x.hi = min(p.stages_total, x.lo + p.part_stages);
+    if (CG == 2 && x.tail >= 0) {
+        if (x.tail < p.tail_tiles)
+            x.hi = p.stages_total / 2;
+        else
+            x.lo = p.stages_total / 2;
+    }
     return x;
 }
 
@@ -280,7 +300,7 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         Fills fills;
         const uint32_t bytes = p.a_box * 128 + G::B_BYTES;
         bool ok = true;
-        for (int u = first; u < p.n_tiles && ok; u += step) {
+        for (int u = first; u < p.n_units && ok; u += step) {
             const Unit x = unit_of<CG>(p, ctl, u);
             const int row = (x.mb * CG + half<CG>(ctl)) * BM;
             const int col = x.nb * G::BN + half<CG>(ctl) * (G::BN / CG);
@@ -310,7 +330,7 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         Ring<G::RAWS> st;
         Fills fills;
         bool ok = true;
-        for (int u = first; u < p.n_tiles && ok; u += step) {
+        for (int u = first; u < p.n_units && ok; u += step) {
             const Unit x = unit_of<CG>(p, ctl, u);
             const int row = (x.mb * CG + half<CG>(ctl)) * BM;
             for (int s = x.lo; s < x.hi; ++s) {
@@ -329,7 +349,7 @@ __device__ void run_tma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
         Ring<G::STAGES> st;
         Fills fills;
         bool ok = true;
-        for (int u = first; u < p.n_tiles && ok; u += step) {
+        for (int u = first; u < p.n_units && ok; u += step) {
             const Unit x = unit_of<CG>(p, ctl, u);
             const int col = x.nb * G::BN + half<CG>(ctl) * (G::BN / CG);
             for (int s = x.lo; s < x.hi; ++s) {
@@ -383,7 +403,7 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
     Ring<G::STAGES> st;
     Ring<G::ACCS> acc;
     bool ok = true;
-    for (int u = first; u < p.n_tiles && ok; u += step) {
+    for (int u = first; u < p.n_units && ok; u += step) {
         const Unit x = unit_of<CG>(p, ctl, u);
         const bool report = p.debug_skip != static_cast<uint32_t>(u) + 1;
         for (int s0 = x.lo; s0 < x.hi && ok; s0 += CH, acc.next()) {
@@ -650,7 +670,47 @@ struct Worker {
         return true;
     }
 
+    // Tail tiles: the first half's warps leave their sums in global memory, the
+    // same warps of the second half take them up, first half first.  Both halves
+    // run in the launch's last round, the first ones on the pairs that start
+    // first.  A flag holds the launch's epoch.
+    __device__ __forceinline__ bool tail(const Place& pl) {
+        const int i = ((pl.x.tail % p.tail_tiles) * CG + ctl.rank) * 8 + w;
+        unsigned long long* at = p.tail_sums + static_cast<size_t>(i) * (COLS / 2 * 32) + lane;
+        const unsigned long long ready = static_cast<unsigned long long>(ctl.epoch) << 32 | 0x5A17F1A6u;
+        if (pl.x.tail < p.tail_tiles) {
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) at[j * 32] = acc[j];
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) st_release_gpu_u64(p.tail_flag + i, ready);
+            return true;
+        }
+        bool there = ld_acquire_gpu_u64(p.tail_flag + i) == ready;
+        const uint64_t t0 = global_timer_ns();
+        while (!there) {
+            __nanosleep(100);
+            there = ld_acquire_gpu_u64(p.tail_flag + i) == ready;
+            if (!there && (launch_aborted(ctl) || global_timer_ns() - t0 > ctl.limit)) {
+                if (!launch_aborted(ctl)) raise_timeout(ctl, WAIT_TAIL, i);
+                return false;
+            }
+        }
+        __syncwarp();
+        const unsigned long long one = pack_f32x2(0x3F800000u, 0x3F800000u);
+#pragma unroll
+        for (int j = 0; j < COLS / 2; ++j) acc[j] = fma_f32x2(acc[j], one, __ldcg(at + j * 32));
+        return true;
+    }
+
     __device__ __forceinline__ bool epilogue(const Place& pl, bool more) {
+        if (CG == 2 && pl.x.tail >= 0) {
+            if (pl.live && !tail(pl)) return false;
+            if (pl.x.tail < p.tail_tiles) {  // the second half writes the output
+                clear();
+                return true;
+            }
+        }
         if (CG == 1 && p.split > 1) {
             // not live in one part: not live in any
             if (pl.live && !(p.split == 2 ? join<2>(pl, more) : p.split == 4 ? join<4>(pl, more) : join<8>(pl, more))) return false;
@@ -721,7 +781,7 @@ template <int CG>
 __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM, CG>& sm, uint32_t tmem, int w, int lane,
                             int first, int step) {
     Worker<KIND_MM, CG> wk(p, ctl, sm, tmem, w, lane);
-    for (int u = first; u < p.n_tiles; u += step) {
+    for (int u = first; u < p.n_units; u += step) {
         const auto pl = wk.place(u);
         // A stage's two scales are fetched AHEAD stages ahead, into registers
         // of their own (the loop is unrolled by as many), so that no load is
@@ -757,7 +817,7 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
                 if (!wk.template promote<64>(pl.live, scale)) return false;
             }
         }
-        if (!wk.epilogue(pl, u + step < p.n_tiles)) return false;
+        if (!wk.epilogue(pl, u + step < p.n_units)) return false;
     }
     return true;
 }
@@ -766,11 +826,11 @@ template <int CG>
 __device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, uint32_t tmem, int w, int lane,
                                int first, int step) {
     Worker<KIND_WG, CG> wk(p, ctl, sm, tmem, w, lane);
-    for (int u = first; u < p.n_tiles; u += step) {
+    for (int u = first; u < p.n_units; u += step) {
         const auto pl = wk.place(u);
         for (int s = pl.x.lo; s < pl.x.hi; s += WG_CHUNK)
             if (!wk.template promote<16>(pl.live, 1.f)) return false;
-        if (!wk.epilogue(pl, u + step < p.n_tiles)) return false;
+        if (!wk.epilogue(pl, u + step < p.n_units)) return false;
     }
     return true;
 }
@@ -797,7 +857,7 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
     const uint32_t to1 = col * 8192 + r0 * 128 + (((2 * j + 1) ^ (r0 & 7)) << 4);
     const long long apart = 16 * p.sa_rs;
     int turn = 0;  // stages so far, over all units
-    for (int u = first; u < p.n_tiles; u += step) {
+    for (int u = first; u < p.n_units; u += step) {
         const Unit x = unit_of<CG>(p, ctl, u);
         // this CTA's 128 output rows are one block of scales; a stage's are
         // fetched one turn (two stages) ahead.  Rows past the last count as 0.

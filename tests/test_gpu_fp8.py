@@ -507,6 +507,28 @@ def test_a_wait_that_runs_out_is_reported(op, config):
     assert np.array_equal(f64(out), want)
 
 
+@pytest.mark.parametrize("op", ["matmul", "weight_grad"])
+@pytest.mark.parametrize("grid,rows,cols", [(152, 300, 700), (6, 500, 500), (10, 900, 700), (4, 250, 1030)])
+def test_halved_tail_tiles(op, grid, rows, cols):
+    """Pairs cut the tiles of a half empty last round in two along a long
+    contraction: one round and several, edges inside the tail tiles, twice on
+    one workspace, and with an odd number of stages."""
+    config = dict(tile_m=256, grid=grid)
+    if op == "matmul":
+        args = mm_ints(rows, 4300, cols, True, seed=23)
+        want, fn, out = mm_want(*args)[0], gct.matmul_fp8, torch.empty(rows, cols, device="cuda")
+    else:
+        args = wg_ints(2150, rows, cols, "bf16", seed=23)
+        want, fn, out = wg_want(*args)[0], gct.weight_grad_fp8, torch.empty(rows, cols, device="cuda")
+    ws = None
+    for _ in range(3):
+        out.fill_(float("nan"))
+        ws = fn(*args, out, config=config, workspace=ws)
+        done(ws)
+        assert np.array_equal(f64(out), want)
+    assert ws.nbytes > 4096, "no tail tile was cut"
+
+
 def test_refusals_on_the_device():
     a, sa, b, sb = mm_ints(4, 256, 64, False)
     out = torch.empty(4, 64, device="cuda")
