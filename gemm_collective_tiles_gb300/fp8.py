@@ -31,28 +31,39 @@ def _blocks(n: int) -> int:
     return (n + _BLOCK - 1) // _BLOCK
 
 
-def _refuse(name: str, t, shape, dtypes, device) -> None:
-    """Say what is wrong with an argument that _mat did not take."""
+def _refuse(name: str, t, shape, dtypes, dims: int, index: int) -> None:
+    """Say what is wrong with an argument that _mat or _vec did not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} is not a tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has type {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} has {t.dim()} dimensions, not 2")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, not {dims}")
     if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     if not t.is_cuda:
         raise ValueError(f"{name} is not on a CUDA device")
-    raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.get_device() != index >= 0:
+        raise ValueError(f"{name} is on {t.device}, not cuda:{index}")
+    raise ValueError(f"{name} is not contiguous")
 
 
-def _mat(name: str, t: torch.Tensor, shape, dtypes, device):
-    """(data, row stride, column stride) of a 2-D device tensor of this shape and one of these types."""
+def _mat(name: str, t: torch.Tensor, shape, dtypes, index: int):
+    """(data, row stride, column stride) of a 2-D tensor of this shape and one
+    of these types on CUDA device `index` (-1: on any)."""
     if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2 and (shape is None or t.shape == shape)
-            and t.is_cuda and (device is None or t.device == device)):
-        _refuse(name, t, shape, dtypes, device)
+            and (t.get_device() == index if index >= 0 else t.is_cuda)):
+        _refuse(name, t, shape, dtypes, 2, index)
     r, c = t.stride()
     return t.data_ptr(), r, c
+
+
+def _vec(name: str, t: torch.Tensor, n: int, dtypes, index: int) -> int:
+    """Address of a contiguous 1-D tensor of n elements."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 1 and t.shape[0] == n
+            and t.get_device() == index and (n <= 1 or t.stride(0) == 1)):
+        _refuse(name, t, (n,), dtypes, 1, index)
+    return t.data_ptr()
 
 
 def _cfgp(config):
@@ -62,9 +73,10 @@ def _cfgp(config):
     return ctypes.byref(make_config(**config) if isinstance(config, dict) else config)
 
 
-def _stream(stream, device) -> int:
+def _stream(stream, index: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        # the raw handle; building a torch.cuda.Stream would cost as much as the launch
+        return torch._C._cuda_getCurrentRawStream(index)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -99,34 +111,34 @@ def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
     block's other elements; zero blocks get the smallest scale."""
     if block not in _ROWS:
         raise ValueError(f"unknown block {block!r}")
-    mx = _mat("x", x, None, _DT, None)
+    mx = _mat("x", x, None, _DT, -1)
     M, K = x.shape
-    dev = x.device
-    mc = _mat("codes", codes, (M, K), _FP8, dev)
-    ms = _mat("scales", scales, (M if block == "rows" else _blocks(M), _blocks(K)), _F32, dev)
+    index = x.get_device()
+    mc = _mat("codes", codes, (M, K), _FP8, index)
+    ms = _mat("scales", scales, (M if block == "rows" else _blocks(M), _blocks(K)), _F32, index)
     args = _native.pack_quantize_fp8(*mx, *mc, *ms, M, K, _DT[x.dtype], _FP8[codes.dtype], _ROWS[block], bool(pow2))
-    lib, st = _native.load(), _stream(stream, dev)
-    if dev.index == torch.cuda.current_device():
+    lib, st = _native.load(), _stream(stream, index)
+    if index == torch._C._cuda_getDevice():
         rc = lib.iris_b200_quantize_fp8(args, st)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = lib.iris_b200_quantize_fp8(args, st)
     if rc:
         _native.check("iris_b200_quantize_fp8", rc)
 
 
-def _product(name: str, fn, args, config, ws, dev, stream):
+def _product(name: str, fn, args, config, ws, index: int, stream):
     """One product with the given workspace, or a new one where it is missing or too small."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _product(name, fn, args, config, ws, dev, stream)
-    cfg, st = _cfgp(config), _stream(stream, dev)
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _product(name, fn, args, config, ws, index, stream)
+    cfg, st = _cfgp(config), _stream(stream, index)
     rc = _native.IRIS_ENOWS if ws is None else fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc == _native.IRIS_ENOWS:
         from . import Workspace
         need, size = ctypes.c_size_t(0), "iris_b200_" + name + "_workspace_size"
         _native.check(size, getattr(_native.load(), size)(args, cfg, ctypes.byref(need)))
-        ws = Workspace(int(need.value), dev)
+        ws = Workspace(int(need.value), torch.device("cuda", index))
         rc = fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc:
         _native.check("iris_b200_" + name, rc)
@@ -142,26 +154,23 @@ def matmul_fp8(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale:
     of a quantised matrix is ``codes.t(), scales.t()``.  bias (N,) and out
     (M, N) are f16, bf16 or f32.  The 128-deep blocks are summed in fp32 and
     rounded once.  Returns the workspace."""
-    ma = _mat("A", A, None, _FP8, None)
+    ma = _mat("A", A, None, _FP8, -1)
     M, K = A.shape
-    dev = A.device
-    mb = _mat("B", B, None, _FP8, dev)
+    index = A.get_device()
+    mb = _mat("B", B, None, _FP8, index)
     N = B.shape[1]
     if B.shape[0] != K:
         raise ValueError(f"A has {K} columns and B has {B.shape[0]} rows")
     kb = _blocks(K)
-    msa = _mat("A_scale", A_scale, (M, kb), _F32, dev)
-    msb = _mat("B_scale", B_scale, (kb, _blocks(N)), _F32, dev)
-    mo = _mat("out", out, (M, N), _DT, dev)
+    msa = _mat("A_scale", A_scale, (M, kb), _F32, index)
+    msb = _mat("B_scale", B_scale, (kb, _blocks(N)), _F32, index)
+    mo = _mat("out", out, (M, N), _DT, index)
     bias_ptr, bias_dt = 0, _native.IRIS_F32
     if bias is not None:
-        if bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
-            raise ValueError(f"bias is not a contiguous tensor of shape ({N},)")
-        _mat("bias", bias.unsqueeze(0), None, _DT, dev)
-        bias_ptr, bias_dt = bias.data_ptr(), _DT[bias.dtype]
+        bias_ptr, bias_dt = _vec("bias", bias, N, _DT, index), _DT[bias.dtype]
     args = _native.pack_matmul_fp8(*ma, *msa, *mb, *msb, *mo, bias_ptr, M, N, K, _FP8[A.dtype], _FP8[B.dtype], bias_dt,
                                    _DT[out.dtype])
-    return _product("matmul_fp8", _native.load().iris_b200_matmul_fp8, args, config, workspace, dev, stream)
+    return _product("matmul_fp8", _native.load().iris_b200_matmul_fp8, args, config, workspace, index, stream)
 
 
 def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, out: torch.Tensor, config=None,
@@ -172,17 +181,17 @@ def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, ou
     X (M, K) codes with "rows" scales (M, ceil(K/128)); dY (M, N) f16 or bf16;
     out f16, bf16 or f32.  X's values enter in dY's type, exactly where the
     scales are powers of two.  Returns the workspace."""
-    mx = _mat("X", X, None, _FP8, None)
+    mx = _mat("X", X, None, _FP8, -1)
     M, K = X.shape
-    dev = X.device
-    md = _mat("dY", dY, None, _DT16, dev)
+    index = X.get_device()
+    md = _mat("dY", dY, None, _DT16, index)
     if dY.shape[0] != M:
         raise ValueError(f"X has {M} rows and dY has {dY.shape[0]}")
     N = dY.shape[1]
-    ms = _mat("X_scale", X_scale, (M, _blocks(K)), _F32, dev)
-    mo = _mat("out", out, (K, N), _DT, dev)
+    ms = _mat("X_scale", X_scale, (M, _blocks(K)), _F32, index)
+    mo = _mat("out", out, (K, N), _DT, index)
     args = _native.pack_weight_grad_fp8(*mx, *ms, *md, *mo, M, N, K, _FP8[X.dtype], _DT[dY.dtype], _DT[out.dtype], 0)
-    return _product("weight_grad_fp8", _native.load().iris_b200_weight_grad_fp8, args, config, workspace, dev, stream)
+    return _product("weight_grad_fp8", _native.load().iris_b200_weight_grad_fp8, args, config, workspace, index, stream)
 
 
 class _Fp8Linear(torch.autograd.Function):
