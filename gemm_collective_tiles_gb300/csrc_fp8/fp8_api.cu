@@ -93,8 +93,12 @@ int setup_kernel(Kernel kernel, int* clusters, int lg_lo, int lg_hi, int threads
 template <int KIND, int CG>
 int setup_tiles(DeviceInfo& d) {
     using G = Geo<KIND, CG>;
-    return setup_kernel(block_gemm_kernel<KIND, CG>, d.clusters[KIND][CG == 2 ? PAIR : CTA], CG == 2, CG == 2 ? 1 : 3,
-                        G::THREADS, G::BYTES, G::REGS_TOTAL, d.sms);
+    int* const clusters = d.clusters[KIND][CG == 2 ? PAIR : CTA];  // both forms hold the same registers and memory
+    const int rc = setup_kernel(block_gemm_kernel<KIND, CG, false>, clusters, CG == 2, CG == 2 ? 1 : 3, G::THREADS, G::BYTES,
+                                G::REGS_TOTAL, d.sms);
+    return rc ? rc
+              : setup_kernel(block_gemm_kernel<KIND, CG, true>, clusters, CG == 2, CG == 2 ? 1 : 3, G::THREADS, G::BYTES,
+                             G::REGS_TOTAL, d.sms);
 }
 template <int NT>
 int setup_few(DeviceInfo& d) {
@@ -187,16 +191,27 @@ Operand resolve_operand(const iris_b200_mat* m, int64_t rows, int64_t cols, int 
         if (cols == 1) o.pitch = packed_pitch(rows, elem);
         return o;
     }
+    // columns of unit stride are copied as the rows that they are
+    if (may_transpose && rows > 1 && m->row_stride == 1 && m->col_stride != 1) o = Operand{m->data, cols, rows, 0, true, false, 0};
     o.copy = true;
-    o.pitch = packed_pitch(cols, elem);
-    o.copy_bytes = round_up(static_cast<size_t>(rows) * o.pitch * elem, 256);
+    o.pitch = packed_pitch(o.cols, elem);
+    o.copy_bytes = round_up(static_cast<size_t>(o.rows) * o.pitch * elem, 256);
     return o;
 }
 template <typename E>
 int launch_repack(const iris_b200_mat* m, Operand& o, void* dst, int sms, cudaStream_t stream) {
-    const int64_t tiles = cdiv(o.rows, 32) * cdiv(o.cols, 32);
-    repack_kernel<E><<<static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(sms) * 8)), 256, 0, stream>>>(
-        static_cast<const E*>(m->data), m->row_stride, m->col_stride, static_cast<E*>(dst), o.pitch, o.rows, o.cols);
+    const int64_t rs = o.transposed ? m->col_stride : m->row_stride, cs = o.transposed ? m->row_stride : m->col_stride;
+    constexpr int64_t elem = sizeof(E);
+    if (cs == 1 || o.cols == 1) {
+        const int64_t tiles = cdiv(o.rows, COPY_ROWS) * cdiv(o.pitch * elem, 512);
+        repack_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(sms) * 8)), 256, 0, stream>>>(
+            static_cast<const uint8_t*>(m->data), rs * elem, static_cast<uint8_t*>(dst), o.pitch * elem, o.rows,
+            o.cols * elem);
+    } else {
+        const int64_t tiles = cdiv(o.rows, 32) * cdiv(o.cols, 32);
+        repack_kernel<E><<<static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(sms) * 8)), 256, 0, stream>>>(
+            static_cast<const E*>(m->data), rs, cs, static_cast<E*>(dst), o.pitch, o.rows, o.cols);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("repack launch", static_cast<int>(e));
     o.data = dst;
@@ -333,9 +348,9 @@ int launch_kernel(Kernel kernel, const GemmParams& p, int grid, int threads, siz
     return e == cudaSuccess ? IRIS_OK : cuda_fail("kernel launch (8-bit product)", static_cast<int>(e));
 }
 template <int KIND, int CG>
-int launch_tiles(const GemmParams& p, int grid, cudaStream_t stream) {
+int launch_tiles(const GemmParams& p, bool direct, int grid, cudaStream_t stream) {
     using G = Geo<KIND, CG>;
-    return launch_kernel(block_gemm_kernel<KIND, CG>, p, grid, G::THREADS, G::BYTES, CG * p.split, stream);
+    return launch_kernel(direct ? block_gemm_kernel<KIND, CG, true> : block_gemm_kernel<KIND, CG, false>, p, grid, G::THREADS, G::BYTES, CG * p.split, stream);
 }
 template <int NT>
 int launch_few(const GemmParams& p, int grid, cudaStream_t stream) {
@@ -436,16 +451,15 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
     p.tail_flag = reinterpret_cast<unsigned long long*>(w + pl.tail);
     p.tail_sums = reinterpret_cast<unsigned long long*>(w + pl.tail + tail_flag_bytes(pl.tail_tiles));
     p.ws = reinterpret_cast<WsHeader*>(w);
-    p.tma_out = direct;
     p.wait_ns = cfg && cfg->wait_ns ? cfg->wait_ns : DEFAULT_WAIT_NS;
     p.debug_skip = cfg ? static_cast<uint32_t>(cfg->debug_skip_flag) : 0u;
     if (direct && pl.variant <= CTA && (rc = make_store_map(&p.tmC, out_dtype, out->data, cols, rows,
                                        rows == 1 ? packed_pitch(cols, dtype_size(out_dtype)) : out->row_stride)))
         return rc;
-    if (wg) return pl.variant == PAIR ? launch_tiles<KIND_WG, 2>(p, pl.grid, stream) : launch_tiles<KIND_WG, 1>(p, pl.grid, stream);
+    if (wg) return pl.variant == PAIR ? launch_tiles<KIND_WG, 2>(p, direct, pl.grid, stream) : launch_tiles<KIND_WG, 1>(p, direct, pl.grid, stream);
     switch (pl.variant) {
-        case PAIR: return launch_tiles<KIND_MM, 2>(p, pl.grid, stream);
-        case CTA: return launch_tiles<KIND_MM, 1>(p, pl.grid, stream);
+        case PAIR: return launch_tiles<KIND_MM, 2>(p, direct, pl.grid, stream);
+        case CTA: return launch_tiles<KIND_MM, 1>(p, direct, pl.grid, stream);
         case FEW16: return launch_few<16>(p, pl.grid, stream);
         default: return launch_few<32>(p, pl.grid, stream);
     }
@@ -487,9 +501,11 @@ int product(const iris_b200_weight_grad_fp8_args* g, const iris_b200_config* cfg
 }
 
 template <int T>
-void launch_quant(const QuantParams& q, bool vec, bool tile, unsigned grid, cudaStream_t stream) {
-    if (vec && tile) quantize_vec_kernel<T, true><<<grid, Q_THREADS, 0, stream>>>(q);
-    else if (vec) quantize_vec_kernel<T, false><<<grid, Q_THREADS, 0, stream>>>(q);
+void launch_quant(const QuantParams& q, bool vec, bool shift, bool tile, unsigned grid, cudaStream_t stream) {
+    if (vec && shift && tile) quantize_vec_kernel<T, true, true><<<grid, Q_THREADS, 0, stream>>>(q);
+    else if (vec && shift) quantize_vec_kernel<T, false, true><<<grid, Q_THREADS, 0, stream>>>(q);
+    else if (vec && tile) quantize_vec_kernel<T, true, false><<<grid, Q_THREADS, 0, stream>>>(q);
+    else if (vec) quantize_vec_kernel<T, false, false><<<grid, Q_THREADS, 0, stream>>>(q);
     else if (tile) quantize_any_kernel<T, true><<<grid, Q_THREADS, 0, stream>>>(q);
     else quantize_any_kernel<T, false><<<grid, Q_THREADS, 0, stream>>>(q);
 }
@@ -533,15 +549,16 @@ int iris_b200_quantize_fp8(const iris_b200_quantize_fp8_args* g, cudaStream_t st
     // nothing that f16 can hold is lost to the bound
     q.pmin = g->x_dtype == IRIS_F16 ? (q.e5m2 ? -8 : -15) : -100;
     const int e = dtype_size(g->x_dtype);
-    // 16-byte reads and writes where every row starts on them (16384 x 4096
-    // bf16: 31 us; the same rows one element off: 60 us)
-    const bool vec = (x->col_stride == 1 || K == 1) && (codes->col_stride == 1 || K == 1) && aligned16(x->data) &&
-                     (M == 1 || x->row_stride * e % 16 == 0) && aligned16(codes->data) &&
+    // 16-byte reads and writes where rows are of unit stride and code rows start
+    // on 16 bytes.  Rows of x that do not are shifted into place: 16384 x 4096
+    // bf16 one element off 37 us, against 33 aligned and 90 element by element.
+    const bool vec = (x->col_stride == 1 || K == 1) && (codes->col_stride == 1 || K == 1) && aligned16(codes->data) &&
                      (M == 1 || codes->row_stride % 16 == 0);
+    const bool shift = !aligned16(x->data) || (M > 1 && x->row_stride * e % 16 != 0);
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (g->x_dtype == IRIS_F32) launch_quant<T_F32>(q, vec, tile, grid, stream);
-    else if (g->x_dtype == IRIS_F16) launch_quant<T_F16>(q, vec, tile, grid, stream);
-    else launch_quant<T_BF16>(q, vec, tile, grid, stream);
+    if (g->x_dtype == IRIS_F32) launch_quant<T_F32>(q, vec, shift, tile, grid, stream);
+    else if (g->x_dtype == IRIS_F16) launch_quant<T_F16>(q, vec, shift, tile, grid, stream);
+    else launch_quant<T_BF16>(q, vec, shift, tile, grid, stream);
     const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? IRIS_OK : cuda_fail("quantize launch", static_cast<int>(err));
 }

@@ -104,7 +104,6 @@ struct GemmParams {
     int out_type;
     long long out_rs, out_cs;
     WsHeader* ws;
-    int tma_out;                  // tensor stores can write the output
     unsigned long long* tail_flag;  // per (tail tile, CTA, promotion warp): a first half's sums are in tail_sums
     unsigned long long* tail_sums;  // 32 x 128 fp32 each, in pairs of columns, a lane per row
     unsigned long long wait_ns;
@@ -485,8 +484,8 @@ __device__ __forceinline__ void store_out(const GemmParams& p, long long row, lo
 }
 
 // A promotion warp: sums and epilogue of its 32 rows x COLS columns of each
-// tile, kept in fp32 registers.
-template <int KIND, int CG>
+// tile, kept in fp32 registers.  DIRECT: tensor stores can write the output.
+template <int KIND, int CG, bool DIRECT>
 struct Worker {
     using G = Geo<KIND, CG>;
     static constexpr int COLS = G::COLS;
@@ -570,41 +569,65 @@ struct Worker {
         return true;
     }
 
-    // a staged box to an output that no tensor store can reach: a lane per
-    // column, eight rows at a time
+    // A staged box to an output that no tensor store can reach.  Rows of unit
+    // stride that start anywhere: eight lanes to a row, each shifts a granule of
+    // 16 bytes that lies whole in the row's part of the output into place; the
+    // elements before the first and after the last granule go one to a lane.
     template <typename E>
-    __device__ __forceinline__ void store_box(const uint8_t* box, int row0, int c0) const {
+    __device__ __forceinline__ void store_rows(const uint8_t* box, int row0, int c0) const {
+        constexpr int SIZE = sizeof(E), EDGE = 16 / SIZE;
+        const int g = lane & 7, rows = min(32, p.M - row0), bytes = min(128, (p.N - c0) * SIZE);
+        uint8_t* to = static_cast<uint8_t*>(p.out) + ((row0 + (lane >> 3)) * p.out_rs + c0) * SIZE;
+#pragma unroll 1
+        for (int r = lane >> 3; r < rows; r += 4, to += 4 * SIZE * p.out_rs) {
+            const uint8_t* const from_row = box + r * 128;
+            auto element = [&](int b) {  // at byte b of the row
+                *reinterpret_cast<E*>(to + b) = *reinterpret_cast<const E*>(from_row + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
+            };
+            const uint32_t skip = -static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)) & 15u;  // bytes before the first
+            const uint4 lo = *reinterpret_cast<const uint4*>(from_row + ((g ^ (r & 7)) << 4));
+            const uint4 hi = *reinterpret_cast<const uint4*>(from_row + (((g + 1) ^ (r & 7)) & 7) * 16);
+            const uint32_t two[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t v[4];
+            shift_granules<1>(two, skip, v);
+            const int at = skip + 16 * g, last = skip + ((bytes - static_cast<int>(skip)) & ~15);  // end of the last granule
+            if (at < last) *reinterpret_cast<uint4*>(to + at) = make_uint4(v[0], v[1], v[2], v[3]);
+            if (g < EDGE) {
+                const int b = g * SIZE;
+                if (b < min(static_cast<int>(skip), bytes)) element(b);
+                if (last + b < bytes && last + b >= static_cast<int>(skip)) element(last + b);
+            }
+        }
+    }
+    // any strides: a lane per column
+    template <typename E>
+    __device__ __forceinline__ void store_elements(const uint8_t* box, int row0, int c0) const {
         constexpr int PER = 128 / (32 * sizeof(E));  // columns per lane
         const int rows = min(32, p.M - row0);
-        E* const to = static_cast<E*>(p.out) + row0 * p.out_rs + (c0 + lane) * p.out_cs;
-#pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-            E v[8][PER];
+        E* to = static_cast<E*>(p.out) + row0 * p.out_rs + (c0 + lane) * p.out_cs;
+#pragma unroll 2
+        for (int r = 0; r < rows; ++r, to += p.out_rs) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    const int b = (lane + 32 * e) * static_cast<int>(sizeof(E));  // byte in the row
-                    v[i][e] = *reinterpret_cast<const E*>(box + (r0 + i) * 128 + (((b >> 4) ^ i) << 4) + (b & 15));
-                }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < PER; ++e)
-                    if (r0 + i < rows && c0 + lane + 32 * e < p.N) to[(r0 + i) * p.out_rs + 32 * e * p.out_cs] = v[i][e];
+            for (int e = 0; e < PER; ++e) {
+                const int b = (lane + 32 * e) * static_cast<int>(sizeof(E));  // byte in the row
+                if (c0 + lane + 32 * e < p.N)
+                    to[32 * e * p.out_cs] = *reinterpret_cast<const E*>(box + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
+            }
         }
     }
 
     // Split contraction over S CTAs: each warp lays its 32 x 64 sums into shared
     // memory, as many columns at a time as its staging holds (rows of units of
     // 16 bytes, XORed with the row), tells the same warp of every part, and adds
-    // its part's share of them over all parts in order.  The loads from the
-    // other CTAs are all under way at once.
+    // its part's rows of them over all parts in order.  The loads from the
+    // other CTAs are all under way at once; neighbouring lanes hold neighbouring
+    // columns of a row, so stores reach few rows each.
     template <int S>
     __device__ __forceinline__ bool join(const Place& pl, bool more) {
         constexpr int UNITS = G::OUT_BYTES / 512, ROUNDS = 16 / UNITS, SHARE = UNITS / S;
         const uint32_t row_at = lane * UNITS * 16;
-        const int row = pl.row0 + lane;
+        const int unit = lane % UNITS;
+        auto share_row = [&](int i) { return ctl.rank * (32 / S) + i * (32 / UNITS) + lane / UNITS; };  // of the warp's 32
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) {
             // the other parts have read what lay here before
@@ -622,14 +645,16 @@ struct Worker {
             if (!wait_bar_cluster(ctl, sm.parts_in + 8 * w, rounds & 1, WAIT_PARTS)) return false;
             __syncwarp();
             ++rounds;
-            const uint32_t mine = smem_u32(stg) + row_at;
+            const uint32_t all = smem_u32(stg);
             float4 t[SHARE][S];
 #pragma unroll
             for (int k = 0; k < S; ++k) {
-                const uint32_t from_k = map_to(mine, k);
+                const uint32_t from_k = map_to(all, k);
 #pragma unroll
-                for (int i = 0; i < SHARE; ++i)
-                    t[i][k] = ld_shared_cluster_f4(from_k + (((ctl.rank * SHARE + i) ^ (lane & (UNITS - 1))) << 4));
+                for (int i = 0; i < SHARE; ++i) {
+                    const int at = share_row(i);
+                    t[i][k] = ld_shared_cluster_f4(from_k + at * UNITS * 16 + ((unit ^ (at & (UNITS - 1))) << 4));
+                }
             }
 #pragma unroll
             for (int i = 0; i < SHARE; ++i) {
@@ -641,14 +666,14 @@ struct Worker {
                     sum.z += t[i][k].z;
                     sum.w += t[i][k].w;
                 }
-                const int c = col_of(pl, 0) + (r * UNITS + ctl.rank * SHARE + i) * 4;
+                const int row = pl.row0 + share_row(i), c = col_of(pl, 0) + (r * UNITS + unit) * 4;
                 float v[4] = {sum.x, sum.y, sum.z, sum.w};
                 if (KIND == KIND_MM && p.bias) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] += load_bias(p, c + e);
                 }
                 if (row < p.M) {
-                    if (p.tma_out && c + 4 <= p.N) {  // unit stride, rows on 16 bytes
+                    if (DIRECT && c + 4 <= p.N) {  // unit stride, rows on 16 bytes
                         const long long o = row * p.out_rs + c;
                         if (p.out_type == T_F32)
                             *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
@@ -752,7 +777,7 @@ struct Worker {
                 }
                 if (wide || (c & 1) == 1) {
                     const int cc = col_of(pl, wide ? c : c - 1);
-                    if (p.tma_out) {  // a tensor store, which clips the ragged edges
+                    if constexpr (DIRECT) {  // a tensor store, which clips the ragged edges
                         fence_proxy_async_shared();
                         __syncwarp();
                         if (lane == 0) {
@@ -762,10 +787,17 @@ struct Worker {
                         ++stores;
                     } else {
                         __syncwarp();
-                        if (wide)
-                            store_box<float>(box, pl.row0, cc);
-                        else
-                            store_box<uint16_t>(box, pl.row0, cc);
+                        const bool rows = p.out_cs == 1;
+                        if (cc >= p.N) {
+                        } else if (rows && wide) {
+                            store_rows<float>(box, pl.row0, cc);
+                        } else if (rows) {
+                            store_rows<uint16_t>(box, pl.row0, cc);
+                        } else if (wide) {
+                            store_elements<float>(box, pl.row0, cc);
+                        } else {
+                            store_elements<uint16_t>(box, pl.row0, cc);
+                        }
                         __syncwarp();
                     }
                 }
@@ -777,10 +809,10 @@ struct Worker {
 };
 
 // Promotion warps; false = a wait gave up.
-template <int CG>
+template <int CG, bool DIRECT>
 __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM, CG>& sm, uint32_t tmem, int w, int lane,
                             int first, int step) {
-    Worker<KIND_MM, CG> wk(p, ctl, sm, tmem, w, lane);
+    Worker<KIND_MM, CG, DIRECT> wk(p, ctl, sm, tmem, w, lane);
     for (int u = first; u < p.n_units; u += step) {
         const auto pl = wk.place(u);
         // A stage's two scales are fetched AHEAD stages ahead, into registers
@@ -822,10 +854,10 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
     return true;
 }
 
-template <int CG>
+template <int CG, bool DIRECT>
 __device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, uint32_t tmem, int w, int lane,
                                int first, int step) {
-    Worker<KIND_WG, CG> wk(p, ctl, sm, tmem, w, lane);
+    Worker<KIND_WG, CG, DIRECT> wk(p, ctl, sm, tmem, w, lane);
     for (int u = first; u < p.n_units; u += step) {
         const auto pl = wk.place(u);
         for (int s = pl.x.lo; s < pl.x.hi; s += WG_CHUNK)
@@ -910,7 +942,9 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
     }
 }
 
-template <int KIND, int CG>
+// DIRECT is a form of its own because the code of the other kind of stores,
+// beside the pairs' promotion loop, costs that loop registers.
+template <int KIND, int CG, bool DIRECT>
 __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(const __grid_constant__ GemmParams p) {
     using G = Geo<KIND, CG>;
     extern __shared__ uint8_t smem_raw[];
@@ -945,7 +979,7 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
         *sm.epoch_slot = e == 0u ? 1u : e;
         tma_prefetch_desc(&p.tmA);
         tma_prefetch_desc(&p.tmB);
-        if (p.split == 1 && p.tma_out) tma_prefetch_desc(&p.tmC);
+        if (DIRECT && p.split == 1) tma_prefetch_desc(&p.tmC);
     }
     if (warp == 1) tmem_alloc<G::TMEM_COLS, CG>(sm.tmem_slot);
     tc_fence_before();
@@ -970,9 +1004,9 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
     } else if (warp < 12) {
         reg_inc<G::REGS_PROMOTE>();
         if constexpr (KIND == KIND_MM)
-            run_promote_mm<CG>(p, ctl, sm, tmem, warp - 4, lane, first, step);
+            run_promote_mm<CG, DIRECT>(p, ctl, sm, tmem, warp - 4, lane, first, step);
         else
-            run_promote_wg<CG>(p, ctl, sm, tmem, warp - 4, lane, first, step);
+            run_promote_wg<CG, DIRECT>(p, ctl, sm, tmem, warp - 4, lane, first, step);
         if (lane == 0) bulk_wait_all();  // its stores have left shared memory, stopped or not
         __syncwarp();
     } else if constexpr (KIND == KIND_WG) {

@@ -7,6 +7,19 @@
 namespace gct {
 namespace fp8 {
 
+// The 4 * N words that start `off` (0 .. 15) bytes into the N + 1 granules of 16
+// bytes in w: whole words by two selections, bytes by a funnel shift.
+template <int N>
+__device__ __forceinline__ void shift_granules(const uint32_t (&w)[4 * N + 4], uint32_t off, uint32_t (&out)[4 * N]) {
+    uint32_t two[4 * N + 2], one[4 * N + 1];
+#pragma unroll
+    for (int j = 0; j < 4 * N + 2; ++j) two[j] = (off & 8) ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 4 * N + 1; ++j) one[j] = (off & 4) ? two[j + 1] : two[j];
+#pragma unroll
+    for (int j = 0; j < 4 * N; ++j) out[j] = __funnelshift_r(one[j], one[j + 1], 8 * (off & 3));
+}
+
 // one lane of a converged warp (the same every time)
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;

@@ -96,11 +96,14 @@ __device__ __forceinline__ float cta_max(float v) {
 // integers (magnitudes order like their bits), which keeps them to about six
 // per element.
 // TILE: one scale for the whole 128 x 128 block, else one per row.
-// Needs rows of x and codes on 16 bytes, both with unit stride.
-template <int T, bool TILE>
-__global__ void __launch_bounds__(Q_THREADS, TILE ? 3 : 4) quantize_vec_kernel(const __grid_constant__ QuantParams p) {
+// Needs x and codes of unit stride, with code rows on 16 bytes.
+// SHIFT: rows of x start anywhere; a lane reads the 16-byte granules around its
+// elements, as far as they lie within x, and shifts them into place.
+template <int T, bool TILE, bool SHIFT>
+__global__ void __launch_bounds__(Q_THREADS, !TILE ? 4 : SHIFT && T == T_F32 ? 2 : 3)
+    quantize_vec_kernel(const __grid_constant__ QuantParams p) {
     constexpr int GROUPS = Q_THREADS / 8, R = TILE ? Q_TILE : Q_ROWS, PER = R / GROUPS;
-    constexpr int E = T == T_F32 ? 4 : 2, W = E;  // bytes per element; 16-byte words per 16 elements
+    constexpr int E = T == T_F32 ? 4 : 2, W = E;  // bytes per element; granules of 16 bytes per 16 elements
     const int lane8 = threadIdx.x & 7, grp = threadIdx.x >> 3;
     const unsigned kb = blockIdx.x % p.kblocks, rb = blockIdx.x / p.kblocks;
     const long long col = static_cast<long long>(kb) * 128 + lane8 * 16;
@@ -110,30 +113,64 @@ __global__ void __launch_bounds__(Q_THREADS, TILE ? 3 : 4) quantize_vec_kernel(c
     const char* src = static_cast<const char*>(p.x) + (row * p.x_rs + col) * E;
     const long long step = GROUPS * p.x_rs * E;
     uint32_t raw[PER][4 * W];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    auto by_element = [&](int i) {
 #pragma unroll
         for (int w = 0; w < 4 * W; ++w) raw[i][w] = 0u;
-        if (i < rows && left > 0) {
+        const char* at = src + i * step;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (e < left) {
+                if constexpr (T == T_F32)
+                    raw[i][e] = reinterpret_cast<const uint32_t*>(at)[e];
+                else
+                    raw[i][e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[e]) << (16 * (e & 1));
+            }
+    };
+    if constexpr (SHIFT) {
+        uint32_t g[PER][4 * W + 4];
+        uint32_t off[PER];
+        bool whole[PER];
+        const char* const x = static_cast<const char*>(p.x);
+        const char* const end = x + ((p.M - 1) * p.x_rs + p.K) * E;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
             const char* at = src + i * step;
-            if (left == 16) {
+            off[i] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+            at -= off[i];
+            whole[i] = i < rows && left == 16 && at >= x && at + 16 * W + (off[i] ? 16 : 0) <= end;
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const uint4 q = __ldg(reinterpret_cast<const uint4*>(at) + w);
-                    raw[i][4 * w] = q.x;
-                    raw[i][4 * w + 1] = q.y;
-                    raw[i][4 * w + 2] = q.z;
-                    raw[i][4 * w + 3] = q.w;
-                }
-            } else {  // ragged last block: element by element
+            for (int w = 0; w <= W; ++w) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (whole[i] && (w < W || off[i])) q = __ldg(reinterpret_cast<const uint4*>(at) + w);
+                g[i][4 * w] = q.x;
+                g[i][4 * w + 1] = q.y;
+                g[i][4 * w + 2] = q.z;
+                g[i][4 * w + 3] = q.w;
+            }
+        }
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (e < left) {
-                        if constexpr (T == T_F32)
-                            raw[i][e] = reinterpret_cast<const uint32_t*>(at)[e];
-                        else
-                            raw[i][e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[e]) << (16 * (e & 1));
+        for (int i = 0; i < PER; ++i) {
+            shift_granules<W>(g[i], off[i], raw[i]);
+            if (!whole[i] && i < rows) by_element(i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+#pragma unroll
+            for (int w = 0; w < 4 * W; ++w) raw[i][w] = 0u;
+            if (i < rows && left > 0) {
+                if (left == 16) {
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + i * step) + w);
+                        raw[i][4 * w] = q.x;
+                        raw[i][4 * w + 1] = q.y;
+                        raw[i][4 * w + 2] = q.z;
+                        raw[i][4 * w + 3] = q.w;
                     }
+                } else {  // ragged last block
+                    by_element(i);
+                }
             }
         }
     }
@@ -309,8 +346,57 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_any_kernel(const __grid_co
     }
 }
 
-// Copy of a rows x cols matrix of E-byte elements with any strides into rows
-// of `pitch` elements (a multiple of 16 bytes) on a 16-byte base.
+// Copy of `rows` rows of unit-stride bytes, any distance apart, into rows of
+// `pitch` bytes (a multiple of 16) on a 16-byte base; the last granule's bytes
+// past a row's end are whatever follows there.  Bound by memory: a lane reads
+// the two granules of 16 bytes around its source (the second is a neighbour's
+// first, so it comes from the L1 cache), shifts and writes one; four rows are
+// under way per thread.  Near the matrix's ends, byte by byte.
+constexpr int COPY_ROWS = 32;  // rows of a CTA's tile: 8 warps x 4; columns: 32 granules
+__global__ void __launch_bounds__(256) repack_rows_kernel(const uint8_t* __restrict__ src, long long rs,
+                                                          uint8_t* __restrict__ dst, long long pitch, long long rows,
+                                                          long long bytes) {
+    constexpr int PER = COPY_ROWS / 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long tiles_c = (pitch + 511) / 512, tiles = tiles_c * ((rows + COPY_ROWS - 1) / COPY_ROWS);
+    const uint8_t* const end = src + (rows - 1) * rs + bytes;
+    for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const long long r0 = t / tiles_c * COPY_ROWS + warp, c = t % tiles_c * 512 + lane * 16;
+        if (c >= pitch) continue;
+        uint32_t g[PER][8], off[PER];
+        bool whole[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const long long r = r0 + 8 * i;
+            const uint8_t* at = src + r * rs + c;
+            off[i] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+            at -= off[i];
+            whole[i] = r < rows && at >= src && at + (off[i] ? 32 : 16) <= end;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (whole[i] && (w == 0 || off[i])) q = __ldg(reinterpret_cast<const uint4*>(at) + w);
+                g[i][4 * w] = q.x;
+                g[i][4 * w + 1] = q.y;
+                g[i][4 * w + 2] = q.z;
+                g[i][4 * w + 3] = q.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const long long r = r0 + 8 * i;
+            if (whole[i]) {
+                uint32_t o[4];
+                shift_granules<1>(g[i], off[i], o);
+                *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else if (r < rows) {
+                for (int e = 0; e < 16 && c + e < bytes; ++e) dst[r * pitch + c + e] = src[r * rs + c + e];
+            }
+        }
+    }
+}
+
+// The same from any strides, in elements E.
 template <typename E>
 __global__ void __launch_bounds__(256) repack_kernel(const E* __restrict__ src, long long rs, long long cs,
                                                      E* __restrict__ dst, long long pitch, long long rows,
