@@ -52,22 +52,35 @@ struct DeviceInfo {
 };
 DeviceInfo g_dev[64];
 
-cudaLaunchConfig_t launch_config(int grid, int threads, size_t smem, int cluster, cudaStream_t stream,
-                                 cudaLaunchAttribute* attr) {
+// Every kernel here may start while the one before it in the stream still runs
+// (it waits for that one's end before it touches memory), which hides its launch
+// and set-up behind its forerunner's last CTAs: one token's quantisation 1.5 ->
+// 1.1 us, 333 x 1000 x 1111 9.9 -> 9.2, 8192^3 388 -> 380.
+cudaLaunchConfig_t launch_config(unsigned grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                                 cudaLaunchAttribute (&attr)[2]) {
     cudaLaunchConfig_t lc;
     std::memset(&lc, 0, sizeof(lc));
     lc.gridDim = dim3(grid);
     lc.blockDim = dim3(threads);
     lc.dynamicSmemBytes = smem;
     lc.stream = stream;
+    std::memset(attr, 0, sizeof(attr));
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
     if (cluster > 1) {
-        attr->id = cudaLaunchAttributeClusterDimension;
-        attr->val.clusterDim.x = cluster;
-        attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-        lc.attrs = attr;
-        lc.numAttrs = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        lc.numAttrs = 2;
     }
     return lc;
+}
+template <typename... Params, typename... Args>
+int launch(const char* what, void (*kernel)(Params...), const cudaLaunchConfig_t& lc, Args... args) {
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, static_cast<Params>(args)...);
+    return e == cudaSuccess ? IRIS_OK : cuda_fail(what, static_cast<int>(e));
 }
 
 template <typename Kernel>
@@ -83,8 +96,8 @@ int setup_kernel(Kernel kernel, int* clusters, int lg_lo, int lg_hi, int threads
     for (int lg = lg_lo; lg <= lg_hi; ++lg) {
         clusters[lg] = sms;
         if (lg == 0) continue;
-        cudaLaunchAttribute attr;
-        const cudaLaunchConfig_t lc = launch_config(sms >> lg << lg, threads, smem, 1 << lg, nullptr, &attr);
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t lc = launch_config(sms >> lg << lg, threads, smem, 1 << lg, nullptr, attr);
         e = cudaOccupancyMaxActiveClusters(&clusters[lg], kernel, &lc);
         if (e != cudaSuccess || clusters[lg] < 1) return cuda_fail("cudaOccupancyMaxActiveClusters", static_cast<int>(e));
     }
@@ -202,18 +215,15 @@ template <typename E>
 int launch_repack(const iris_b200_mat* m, Operand& o, void* dst, int sms, cudaStream_t stream) {
     const int64_t rs = o.transposed ? m->col_stride : m->row_stride, cs = o.transposed ? m->row_stride : m->col_stride;
     constexpr int64_t elem = sizeof(E);
-    if (cs == 1 || o.cols == 1) {
-        const int64_t tiles = cdiv(o.rows, COPY_ROWS) * cdiv(o.pitch * elem, 512);
-        repack_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(sms) * 8)), 256, 0, stream>>>(
-            static_cast<const uint8_t*>(m->data), rs * elem, static_cast<uint8_t*>(dst), o.pitch * elem, o.rows,
-            o.cols * elem);
-    } else {
-        const int64_t tiles = cdiv(o.rows, 32) * cdiv(o.cols, 32);
-        repack_kernel<E><<<static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(sms) * 8)), 256, 0, stream>>>(
-            static_cast<const E*>(m->data), rs, cs, static_cast<E*>(dst), o.pitch, o.rows, o.cols);
-    }
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail("repack launch", static_cast<int>(e));
+    const bool by_rows = cs == 1 || o.cols == 1;
+    const int64_t tiles = by_rows ? cdiv(o.rows, COPY_ROWS) * cdiv(o.pitch * elem, 512) : cdiv(o.rows, 32) * cdiv(o.cols, 32);
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(std::min<int64_t>(tiles, int64_t(sms) * 8)), 256, 0, 1, stream, attr);
+    const int rc = by_rows ? launch("repack launch", repack_rows_kernel, lc, static_cast<const uint8_t*>(m->data), rs * elem,
+                                    static_cast<uint8_t*>(dst), o.pitch * elem, o.rows, o.cols * elem)
+                           : launch("repack launch", repack_kernel<E>, lc, static_cast<const E*>(m->data), rs, cs,
+                                    static_cast<E*>(dst), o.pitch, o.rows, o.cols);
+    if (rc) return rc;
     o.data = dst;
     return IRIS_OK;
 }
@@ -268,22 +278,24 @@ size_t tail_flag_bytes(int tiles) { return round_up(size_t(tiles) * 16 * 8, 256)
 // tiles in turn; a tile costs `part` stages, its epilogue and, where its
 // contraction is split, the meeting of the parts.  Constants measured on GB300
 // (launch 4.5; e.g. 1 x 4096 x 1024: 12.3 us as 8 CTAs of 32 stages, 9.1 split
-// over 8; 100 x 1000 x 3000: 7.8 us whole, 11.4 split over 2; 8192 x 512 x 512
-// weight gradient: 57 us whole, 26 split over 4).  Element stores, for outputs
-// that no tensor store can reach, cost a tile about 2 us and a meeting 6.
-double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, bool direct, bool tail) {
+// over 8; 333 x 1000 x 1112: 8.6 us whole, 10.3 split over 2; 8192 x 512 x 512
+// weight gradient: 57 us whole, 26 split over 4).  Outputs that no tensor store
+// can reach cost a pair's tile 1.2 us per byte of an element (3000 x 512 x 4097
+// bf16: 22.9 us, with 4096 columns 16.2, in three rounds), a CTA's half of
+// that, a meeting 1.
+double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, bool direct, int out_elem, bool tail) {
     const double stage = wg ? (v == PAIR ? 0.47 : 0.40) : (v == PAIR ? 0.45 : v == CTA ? 0.32 : v == FEW16 ? 0.27 : 0.42);
     double tile = part * stage + (v == PAIR ? 2.0 : 1.0);
     if (split > 1)
-        tile += v >= FEW16 ? 2.0 : 4.5 + (direct ? 0.0 : 6.0);
+        tile += v >= FEW16 ? 2.0 : direct ? 4.5 : 5.5;
     else if (!direct && v <= CTA)
-        tile += 2.0;
+        tile += (v == PAIR ? 1.2 : 0.6) * out_elem;
     if (tail) return 4.5 + tiles / slots * tile + part * stage / 2 + 8.0;
     return 4.5 + cdiv(tiles, slots) * tile;
 }
 
 int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& d, const Operand& a, const Operand& b,
-              bool direct, int64_t rows, int64_t cols, int64_t depth) {
+              bool direct, int out_elem, int64_t rows, int64_t cols, int64_t depth) {
     iris_b200_config z;
     std::memset(&z, 0, sizeof(z));
     if (!cfg) cfg = &z;
@@ -316,7 +328,7 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
             // in 401 us, whole in 448)
             const int64_t last = tiles % slots;
             const bool tail = v == PAIR && last > 0 && 2 * last <= slots && part >= 32;
-            const double t = estimate(wg, v, slots, tiles, part, split, direct, tail);
+            const double t = estimate(wg, v, slots, tiles, part, split, direct, out_elem, tail);
             if (pl.cg == 0 || t < best) {
                 best = t;
                 pl.cg = cg;
@@ -340,21 +352,18 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
     return IRIS_OK;
 }
 
-template <typename Kernel>
-int launch_kernel(Kernel kernel, const GemmParams& p, int grid, int threads, size_t smem, int cluster, cudaStream_t stream) {
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t lc = launch_config(grid, threads, smem, cluster, stream, &attr);
-    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p);
-    return e == cudaSuccess ? IRIS_OK : cuda_fail("kernel launch (8-bit product)", static_cast<int>(e));
-}
 template <int KIND, int CG>
 int launch_tiles(const GemmParams& p, bool direct, int grid, cudaStream_t stream) {
     using G = Geo<KIND, CG>;
-    return launch_kernel(direct ? block_gemm_kernel<KIND, CG, true> : block_gemm_kernel<KIND, CG, false>, p, grid, G::THREADS, G::BYTES, CG * p.split, stream);
+    cudaLaunchAttribute attr[2];
+    return launch("kernel launch (8-bit product)", direct ? block_gemm_kernel<KIND, CG, true> : block_gemm_kernel<KIND, CG, false>,
+                  launch_config(grid, G::THREADS, G::BYTES, CG * p.split, stream, attr), p);
 }
 template <int NT>
 int launch_few(const GemmParams& p, int grid, cudaStream_t stream) {
-    return launch_kernel(few_rows_kernel<NT>, p, grid, FewGeo<NT>::THREADS, FewGeo<NT>::BYTES, p.split, stream);
+    cudaLaunchAttribute attr[2];
+    return launch("kernel launch (8-bit product)", few_rows_kernel<NT>,
+                  launch_config(grid, FewGeo<NT>::THREADS, FewGeo<NT>::BYTES, p.split, stream, attr), p);
 }
 
 // out (rows x cols) of one product: everything that both kinds share.
@@ -377,7 +386,7 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
     DeviceInfo d;
     if ((rc = device_info(&d))) return rc;
     Plan pl;
-    if ((rc = make_plan(pl, wg, cfg, d, a, b, direct, rows, cols, std::max<int64_t>(depth, 1)))) return rc;
+    if ((rc = make_plan(pl, wg, cfg, d, a, b, direct, dtype_size(out_dtype), rows, cols, std::max<int64_t>(depth, 1)))) return rc;
     if (need) {
         *need = pl.total;
         return IRIS_OK;
@@ -398,9 +407,9 @@ int run_product(bool wg, const iris_b200_mat* ma, int a_type, const iris_b200_ma
     p.out_cs = out->col_stride;
     if (depth == 0) {
         const int64_t n = cdiv(rows * cols, 256);
-        fill_kernel<<<static_cast<unsigned>(std::min<int64_t>(n, int64_t(d.sms) * 8)), 256, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
-        return e == cudaSuccess ? IRIS_OK : cuda_fail("fill launch", static_cast<int>(e));
+        cudaLaunchAttribute attr[2];
+        return launch("fill launch", fill_kernel,
+                      launch_config(static_cast<unsigned>(std::min<int64_t>(n, int64_t(d.sms) * 8)), 256, 0, 1, stream, attr), p);
     }
     char* w = static_cast<char*>(ws);
     if (a.copy && (rc = launch_repack<uint8_t>(ma, a, w + pl.copy_a, d.sms, stream))) return rc;
@@ -501,13 +510,13 @@ int product(const iris_b200_weight_grad_fp8_args* g, const iris_b200_config* cfg
 }
 
 template <int T>
-void launch_quant(const QuantParams& q, bool vec, bool shift, bool tile, unsigned grid, cudaStream_t stream) {
-    if (vec && shift && tile) quantize_vec_kernel<T, true, true><<<grid, Q_THREADS, 0, stream>>>(q);
-    else if (vec && shift) quantize_vec_kernel<T, false, true><<<grid, Q_THREADS, 0, stream>>>(q);
-    else if (vec && tile) quantize_vec_kernel<T, true, false><<<grid, Q_THREADS, 0, stream>>>(q);
-    else if (vec) quantize_vec_kernel<T, false, false><<<grid, Q_THREADS, 0, stream>>>(q);
-    else if (tile) quantize_any_kernel<T, true><<<grid, Q_THREADS, 0, stream>>>(q);
-    else quantize_any_kernel<T, false><<<grid, Q_THREADS, 0, stream>>>(q);
+int launch_quant(const QuantParams& q, bool vec, bool shift, bool tile, unsigned grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    return launch("quantize launch",
+                  vec && shift ? (tile ? quantize_vec_kernel<T, true, true> : quantize_vec_kernel<T, false, true>)
+                  : vec        ? (tile ? quantize_vec_kernel<T, true, false> : quantize_vec_kernel<T, false, false>)
+                               : (tile ? quantize_any_kernel<T, true> : quantize_any_kernel<T, false>),
+                  launch_config(grid, Q_THREADS, 0, 1, stream, attr), q);
 }
 
 }  // namespace
@@ -556,11 +565,9 @@ int iris_b200_quantize_fp8(const iris_b200_quantize_fp8_args* g, cudaStream_t st
                      (M == 1 || codes->row_stride % 16 == 0);
     const bool shift = !aligned16(x->data) || (M > 1 && x->row_stride * e % 16 != 0);
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (g->x_dtype == IRIS_F32) launch_quant<T_F32>(q, vec, shift, tile, grid, stream);
-    else if (g->x_dtype == IRIS_F16) launch_quant<T_F16>(q, vec, shift, tile, grid, stream);
-    else launch_quant<T_BF16>(q, vec, shift, tile, grid, stream);
-    const cudaError_t err = cudaGetLastError();
-    return err == cudaSuccess ? IRIS_OK : cuda_fail("quantize launch", static_cast<int>(err));
+    if (g->x_dtype == IRIS_F32) return launch_quant<T_F32>(q, vec, shift, tile, grid, stream);
+    if (g->x_dtype == IRIS_F16) return launch_quant<T_F16>(q, vec, shift, tile, grid, stream);
+    return launch_quant<T_BF16>(q, vec, shift, tile, grid, stream);
 }
 
 int iris_b200_matmul_fp8_workspace_size(const iris_b200_matmul_fp8_args* args, const iris_b200_config* cfg, size_t* bytes) {

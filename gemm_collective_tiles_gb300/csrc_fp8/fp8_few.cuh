@@ -76,10 +76,13 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
         bar_init(final_bar, 1);
         bar_init(final_bar + 8, 1);
         fence_mbar_init();
-        const uint32_t e = *reinterpret_cast<volatile uint32_t*>(&p.ws->epoch) + 1u;
-        tmem_slot[1] = e == 0u ? 1u : e;
         tma_prefetch_desc(&p.tmA);
         tma_prefetch_desc(&p.tmB);
+        // for the whole CTA, which waits for this thread below
+        grid_wait();
+        grid_release();
+        const uint32_t e = *reinterpret_cast<volatile uint32_t*>(&p.ws->epoch) + 1u;
+        tmem_slot[1] = e == 0u ? 1u : e;
     }
     if (warp == 1) tmem_alloc<G::TMEM_COLS, 1>(tmem_slot);
     tc_fence_before();

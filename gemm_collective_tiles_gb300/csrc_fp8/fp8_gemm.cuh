@@ -975,11 +975,14 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
         bar_init(sm.final_bar, 1);
         bar_init(sm.final_bar + 8, 1);
         fence_mbar_init();
-        uint32_t e = *reinterpret_cast<volatile uint32_t*>(&p.ws->epoch) + 1u;
-        *sm.epoch_slot = e == 0u ? 1u : e;
         tma_prefetch_desc(&p.tmA);
         tma_prefetch_desc(&p.tmB);
         if (DIRECT && p.split == 1) tma_prefetch_desc(&p.tmC);
+        // for the whole CTA, which waits for this thread below
+        grid_wait();
+        grid_release();
+        uint32_t e = *reinterpret_cast<volatile uint32_t*>(&p.ws->epoch) + 1u;
+        *sm.epoch_slot = e == 0u ? 1u : e;
     }
     if (warp == 1) tmem_alloc<G::TMEM_COLS, CG>(sm.tmem_slot);
     tc_fence_before();
@@ -1039,6 +1042,8 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
 
 // Empty contraction: out = bias, or zero.
 __global__ void __launch_bounds__(256) fill_kernel(const __grid_constant__ GemmParams p) {
+    grid_wait();
+    grid_release();
     const long long n = static_cast<long long>(p.M) * p.N;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll)
         store_out(p, i / p.N, i % p.N, load_bias(p, static_cast<int>(i % p.N)));

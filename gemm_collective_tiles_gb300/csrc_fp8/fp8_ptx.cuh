@@ -20,6 +20,13 @@ __device__ __forceinline__ void shift_granules(const uint32_t (&w)[4 * N + 4], u
     for (int j = 0; j < 4 * N; ++j) out[j] = __funnelshift_r(one[j], one[j + 1], 8 * (off & 3));
 }
 
+// A kernel of these may start while the one before it in the stream still runs:
+// grid_wait waits until that one has ended and its writes are seen by the whole
+// grid, and no global memory is touched before; grid_release, after it, lets the
+// next kernel start once every CTA has come there.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // one lane of a converged warp (the same every time)
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;

@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(Q_THREADS, !TILE ? 4 : SHIFT && T == T_F32 ? 2
     const int rows = static_cast<int>(max(0ll, min(static_cast<long long>(PER), (p.M - row + GROUPS - 1) / GROUPS)));
     const char* src = static_cast<const char*>(p.x) + (row * p.x_rs + col) * E;
     const long long step = GROUPS * p.x_rs * E;
+    grid_wait();
+    grid_release();
     uint32_t raw[PER][4 * W];
     auto by_element = [&](int i) {
 #pragma unroll
@@ -280,6 +282,8 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_any_kernel(const __grid_co
     uint8_t* const c0 = p.codes + row * p.c_rs + col * p.c_cs;
     const long long x_row = p.x_rs * WARPS * E, x_col = p.x_cs * 32 * E, c_row = p.c_rs * WARPS, c_col = p.c_cs * 32;
     const int rows = static_cast<int>(max(0ll, min(static_cast<long long>(PER), (p.M - row + WARPS - 1) / WARPS)));
+    grid_wait();
+    grid_release();
     bool there[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) there[e] = col + 32 * e < p.K;
@@ -360,6 +364,8 @@ __global__ void __launch_bounds__(256) repack_rows_kernel(const uint8_t* __restr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long tiles_c = (pitch + 511) / 512, tiles = tiles_c * ((rows + COPY_ROWS - 1) / COPY_ROWS);
     const uint8_t* const end = src + (rows - 1) * rs + bytes;
+    grid_wait();
+    grid_release();
     for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
         const long long r0 = t / tiles_c * COPY_ROWS + warp, c = t % tiles_c * 512 + lane * 16;
         if (c >= pitch) continue;
@@ -407,6 +413,8 @@ __global__ void __launch_bounds__(256) repack_kernel(const E* __restrict__ src, 
     const long long tiles_c = (cols + 31) / 32, tiles = tiles_c * ((rows + 31) / 32);
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const bool by_col = rs == 1 && cs != 1;  // the source's rows are its unit-stride dimension
+    grid_wait();
+    grid_release();
     for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
         const long long r0 = t / tiles_c * 32, c0 = t % tiles_c * 32;
         for (int i = ty; i < 32; i += 8) {
