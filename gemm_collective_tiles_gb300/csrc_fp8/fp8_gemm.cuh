@@ -180,8 +180,8 @@ struct Geo {
     static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES + RAWS * RAW_BYTES;
     static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
     // registers: the launch's total (168 or 96 a thread) is shared out anew
-    static constexpr int REGS_CTL = KIND == KIND_MM ? 56 : 48;
-    static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 224 : 152;
+    static constexpr int REGS_CTL = KIND == KIND_MM ? 40 : 48;
+    static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 232 : 152;
     static constexpr int REGS_CONVERT = KIND == KIND_MM ? 0 : 64;
     static constexpr int REGS_TOTAL = 128 * REGS_CTL + 256 * (REGS_PROMOTE + REGS_CONVERT);
 };
@@ -529,9 +529,20 @@ struct Worker {
         return pl.x.nb * G::BN + h * COLS + c * 32;
     }
 
-    // acc += the next chunk's product * scale.  Wide loads make few round
-    // trips to tensor memory; the buffer is handed back as soon as the last
-    // one has arrived.
+    // 32 columns' products times the scale, from the warp's column AT on
+    template <int AT>
+    __device__ __forceinline__ void add(const uint32_t (&r)[32], unsigned long long f2) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc[AT / 2 + i] = fma_f32x2(pack_f32x2(r[2 * i], r[2 * i + 1]), f2, acc[AT / 2 + i]);
+    }
+    // acc += the next chunk's product * scale; the buffer is handed back as soon
+    // as its last load has arrived.  Pairs read 32 columns while they add the
+    // 32 before, and read rows and columns that do not exist as well: the loop
+    // runs once per stage on the way from one MMA to the next but one, and fewer
+    // instructions in it are worth more than idle warps (8192^3: 373 us; with 64
+    // columns at a time, added in between, and a test of `live` 385).
+    // Otherwise wide loads make few round trips to tensor memory.
     template <int LD>
     __device__ __forceinline__ bool promote(bool live, float scale) {
         const uint32_t buf = from.slot;
@@ -549,19 +560,37 @@ struct Worker {
                     bar_arrive(sm.acc_empty + 8 * buf);
             }
         };
-        if (live) {
+        constexpr bool PAIRS = KIND == KIND_MM && CG == 2;
+        if (PAIRS || live) {
             const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::BN + h * COLS;
             const uint32_t f = __float_as_uint(scale);
             const unsigned long long f2 = pack_f32x2(f, f);
-            uint32_t r[LD];
+            if constexpr (PAIRS) {
+                uint32_t r0[32], r1[32];
+                tmem_ld_cols(base, r0);
+                tmem_wait_regs(r0);
+                tmem_ld_cols(base + 32, r1);
+                add<0>(r0, f2);
+                tmem_wait_regs(r1);
+                tmem_ld_cols(base + 64, r0);
+                add<32>(r1, f2);
+                tmem_wait_regs(r0);
+                tmem_ld_cols(base + 96, r1);
+                add<64>(r0, f2);
+                tmem_wait_regs(r1);
+                release();
+                add<96>(r1, f2);
+            } else {
+                uint32_t r[LD];
 #pragma unroll
-            for (int c = 0; c < COLS / LD; ++c) {
-                tmem_ld_cols(base + c * LD, r);
-                tmem_wait_regs(r);
-                if (c == COLS / LD - 1) release();
+                for (int c = 0; c < COLS / LD; ++c) {
+                    tmem_ld_cols(base + c * LD, r);
+                    tmem_wait_regs(r);
+                    if (c == COLS / LD - 1) release();
 #pragma unroll
-                for (int i = 0; i < LD / 2; ++i)
-                    acc[c * (LD / 2) + i] = fma_f32x2(pack_f32x2(r[2 * i], r[2 * i + 1]), f2, acc[c * (LD / 2) + i]);
+                    for (int i = 0; i < LD / 2; ++i)
+                        acc[c * (LD / 2) + i] = fma_f32x2(pack_f32x2(r[2 * i], r[2 * i + 1]), f2, acc[c * (LD / 2) + i]);
+                }
             }
         } else {
             release();
@@ -818,12 +847,11 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
         // A stage's two scales are fetched AHEAD stages ahead, into registers
         // of their own (the loop is unrolled by as many), so that no load is
         // waited for: passing them from register to register would wait for
-        // each within its stage.  Pairs unroll by two only, because three
-        // copies of their longer loop no longer run from the instruction
-        // cache (8192^3: 411 us passed on, 394 with two, 444 with three).
+        // each within its stage.  Pairs do not unroll: two copies of their
+        // longer loop do not run from the nearest instruction cache.
         // Rows below the last read its scales; past the last stage the last
         // one's are read.
-        constexpr int AHEAD = CG == 2 ? 2 : 4;
+        constexpr int AHEAD = CG == 2 ? 1 : 4;
         const float* pa = p.sa + min(pl.row0 + lane, p.M - 1) * p.sa_rs + pl.x.lo * p.sa_cs;
         const float* pb = p.sb + min(wk.col_of(pl, 0), p.N - 1) / 128 * p.sb_cs + pl.x.lo * p.sb_rs;
         int left = pl.x.hi - pl.x.lo;
