@@ -599,32 +599,54 @@ struct Worker {
     }
 
     // A staged box to an output that no tensor store can reach.  Rows of unit
-    // stride that start anywhere: eight lanes to a row, each shifts a granule of
-    // 16 bytes that lies whole in the row's part of the output into place; the
-    // elements before the first and after the last granule go one to a lane.
+    // stride that start anywhere: box k of a warp's part of a row fills the 128
+    // aligned bytes from its first byte's granule on, with what the box before
+    // left over, eight lanes to a row, each shifting 16 bytes into place; only
+    // what lies before the row's first granule and after its last goes by
+    // elements.  Bound by the latency of its instructions (8 warps), hence one
+    // aligned pointer, fixed shared addresses and edges in loops of their own
+    // (weight gradient of 4 tokens, 6840 x 3567 f32: TODO).
     template <typename E>
-    __device__ __forceinline__ void store_rows(const uint8_t* box, int row0, int c0) const {
-        constexpr int SIZE = sizeof(E), EDGE = 16 / SIZE;
-        const int g = lane & 7, rows = min(32, p.M - row0), bytes = min(128, (p.N - c0) * SIZE);
-        uint8_t* to = static_cast<uint8_t*>(p.out) + ((row0 + (lane >> 3)) * p.out_rs + c0) * SIZE;
-#pragma unroll 1
-        for (int r = lane >> 3; r < rows; r += 4, to += 4 * SIZE * p.out_rs) {
-            const uint8_t* const from_row = box + r * 128;
-            auto element = [&](int b) {  // at byte b of the row
-                *reinterpret_cast<E*>(to + b) = *reinterpret_cast<const E*>(from_row + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
-            };
-            const uint32_t skip = -static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)) & 15u;  // bytes before the first
-            const uint4 lo = *reinterpret_cast<const uint4*>(from_row + ((g ^ (r & 7)) << 4));
-            const uint4 hi = *reinterpret_cast<const uint4*>(from_row + (((g + 1) ^ (r & 7)) & 7) * 16);
+    __device__ __forceinline__ void store_rows(int k, int row0, int c0) const {
+        constexpr int SIZE = sizeof(E), ROW = G::BOXES == 1 ? 128 : COLS * SIZE;
+        const int g = lane & 7, r0 = lane >> 3, rows = min(32, p.M - row0), bytes = min(ROW, (p.N - c0) * SIZE);
+        const long long step = 4 * SIZE * p.out_rs;
+        uint8_t* const to0 = static_cast<uint8_t*>(p.out) + ((row0 + r0) * p.out_rs + c0) * SIZE;
+        // unit n of row r, units XORed with the row
+        auto unit = [&](int n, int r) { return stg + (n >> 3) % G::BOXES * 4096 + r * 128 + (((n ^ r) & 7) << 4); };
+        const uint8_t *const here = unit(8 * k + g, r0), *const before = unit(8 * k + g + 8 * G::BOXES - 1, r0);
+        uint8_t* to = to0;
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i, to += step) {
+            if (r0 + 4 * i >= rows) break;
+            const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(to)) & 15, o = 128 * k + 16 * g - mis;
+            // row r0 + 4 i: 512 bytes per i, and every other i flips bit 2 of the unit
+            const uint8_t* const a = (mis ? before : here) + i * 512;
+            const uint8_t* const b = here + i * 512;
+            const uint4 lo = *reinterpret_cast<const uint4*>(stg + (static_cast<int>(a - stg) ^ (i & 1) << 6));
+            const uint4 hi = *reinterpret_cast<const uint4*>(stg + (static_cast<int>(b - stg) ^ (i & 1) << 6));
             const uint32_t two[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t v[4];
-            shift_granules<1>(two, skip, v);
-            const int at = skip + 16 * g, last = skip + ((bytes - static_cast<int>(skip)) & ~15);  // end of the last granule
-            if (at < last) *reinterpret_cast<uint4*>(to + at) = make_uint4(v[0], v[1], v[2], v[3]);
-            if (g < EDGE) {
-                const int b = g * SIZE;
-                if (b < min(static_cast<int>(skip), bytes)) element(b);
-                if (last + b < bytes && last + b >= static_cast<int>(skip)) element(last + b);
+            shift_granules<1>(two, (16 - mis) & 15, v);
+            if (o >= 0 && o + 16 <= bytes) *reinterpret_cast<uint4*>(to + o) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        auto element = [&](uint8_t* row, int r, int b) {
+            *reinterpret_cast<E*>(row + b) = *reinterpret_cast<const E*>(unit(b >> 4, r) + (b & 15));
+        };
+        if (k == 0) {
+            to = to0;
+#pragma unroll 1
+            for (int r = r0; r < rows; r += 4, to += step)
+                if (g * SIZE < min(-static_cast<int>(reinterpret_cast<uintptr_t>(to)) & 15, bytes)) element(to, r, g * SIZE);
+        }
+        if (128 * (k + 1) >= bytes) {
+            to = to0;
+#pragma unroll 1
+            for (int r = r0; r < rows; r += 4, to += step) {
+                const int head = -static_cast<int>(reinterpret_cast<uintptr_t>(to)) & 15;
+                const int end = bytes - (static_cast<int>(reinterpret_cast<uintptr_t>(to + bytes)) & 15);
+                const int b = max(head, end) + g * SIZE;
+                if (g * SIZE < 16 && b < bytes) element(to, r, b);
             }
         }
     }
@@ -800,7 +822,7 @@ struct Worker {
                     if (lane == 0) bulk_wait_read<G::BOXES - 1>();
                     __syncwarp();
                 }
-                uint8_t* box = stg + (stores % G::BOXES) * 4096;
+                uint8_t* box = stg + (DIRECT ? stores : wide ? c : c / 2) % G::BOXES * 4096;
                 if (wide) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -826,12 +848,14 @@ struct Worker {
                         ++stores;
                     } else {
                         __syncwarp();
+                        // box k of the warp's part of a row, or of its own
+                        const int k = G::BOXES == 1 ? 0 : wide ? c : c / 2, row_c = G::BOXES == 1 ? cc : col_of(pl, 0);
                         const bool rows = p.out_cs == 1;
                         if (cc >= p.N) {
                         } else if (rows && wide) {
-                            store_rows<float>(box, pl.row0, cc);
+                            store_rows<float>(k, pl.row0, row_c);
                         } else if (rows) {
-                            store_rows<uint16_t>(box, pl.row0, cc);
+                            store_rows<uint16_t>(k, pl.row0, row_c);
                         } else if (wide) {
                             store_elements<float>(box, pl.row0, cc);
                         } else {
