@@ -29,7 +29,7 @@
 //
 // CG = 1 can split the contraction: a cluster of 2, 4 or 8 CTAs takes a tile,
 // each a part of its stages; the fp32 sums meet in shared memory, where each
-// CTA adds a slice of every warp's columns over all parts in part order, so
+// CTA adds a slice of every warp's rows over all parts in part order, so
 // results do not depend on timing and nothing goes through global memory.
 //
 // Tiles are dealt out in a fixed order.  Every wait is bounded: one that gives
@@ -603,9 +603,10 @@ struct Worker {
     // aligned bytes from its first byte's granule on, with what the box before
     // left over, eight lanes to a row, each shifting 16 bytes into place; only
     // what lies before the row's first granule and after its last goes by
-    // elements.  Bound by the latency of its instructions (8 warps), hence one
-    // aligned pointer, fixed shared addresses and edges in loops of their own
-    // (weight gradient of 4 tokens, 6840 x 3567 f32: TODO).
+    // elements.  Bound by the latency of its instructions (8 warps), hence fixed
+    // shared addresses and edges in loops of their own (weight gradient of 4
+    // tokens, 6840 x 3567 f32: 49 us; a box at a time, edges and all, 66; with
+    // 3568 columns and tensor stores 20).
     template <typename E>
     __device__ __forceinline__ void store_rows(int k, int row0, int c0) const {
         constexpr int SIZE = sizeof(E), ROW = G::BOXES == 1 ? 128 : COLS * SIZE;
