@@ -279,15 +279,16 @@ size_t tail_flag_bytes(int tiles) { return round_up(size_t(tiles) * 16 * 8, 256)
 // contraction is split, the meeting of the parts.  Constants measured on GB300
 // (launch 4.5; e.g. 1 x 4096 x 1024: 12.3 us as 8 CTAs of 32 stages, 9.1 split
 // over 8; 333 x 1000 x 1112: 8.0 us whole, 9.9 split over 2; 100 x 4096 x 4096:
-// 12.7 us whole, 10.4 split over 4; 8192 x 512 x 512 weight gradient: 57 us
+// 12.7 us whole, 10.4 split over 4; weight gradients of 2000 tokens, 500 x 504:
+// 16.2 us whole, 11.1 split over 4, and of 8192 tokens, 512 x 512: 57 us
 // whole, 26 split over 4).  Outputs that no tensor store can reach cost a pair's
 // tile 1.2 us per byte of an element (3000 x 512 x 4097 bf16: 22.9 us, with 4096
 // columns 16.2, in three rounds), a CTA's half of that, a meeting 0.8.
 double estimate(bool wg, Variant v, int slots, int64_t tiles, int64_t part, int split, bool direct, int out_elem, bool tail) {
-    const double stage = wg ? (v == PAIR ? 0.47 : 0.40) : (v == PAIR ? 0.45 : v == CTA ? 0.32 : v == FEW16 ? 0.27 : 0.42);
+    const double stage = wg ? (v == PAIR ? 0.47 : 0.35) : (v == PAIR ? 0.45 : v == CTA ? 0.32 : v == FEW16 ? 0.27 : 0.42);
     double tile = part * stage + (v == PAIR ? 2.0 : 1.0);
     if (split > 1)
-        tile += v >= FEW16 ? 2.0 : direct ? 2.7 : 3.5;
+        tile += v >= FEW16 ? 2.0 : (wg ? 3.3 : 2.7) + (direct ? 0.0 : 0.8);
     else if (!direct && v <= CTA)
         tile += (v == PAIR ? 1.2 : 0.6) * out_elem;
     if (tail) return 4.5 + tiles / slots * tile + part * stage / 2 + 8.0;

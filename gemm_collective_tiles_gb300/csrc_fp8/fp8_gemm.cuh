@@ -604,8 +604,9 @@ struct Worker {
     // left over, eight lanes to a row, each shifting 16 bytes into place; only
     // what lies before the row's first granule and after its last goes by
     // elements.  Bound by the latency of its instructions (8 warps), hence fixed
-    // shared addresses and edges in loops of their own (weight gradient of 4
-    // tokens, 6840 x 3567 f32: 49 us; a box at a time, edges and all, 66; with
+    // shared addresses and, beside several boxes, edges in loops of their own
+    // (333 x 1000 x 1111: 9.4 us, with such loops 9.7; weight gradient of 4
+    // tokens, 6840 x 3567 f32: 48 us; a box at a time, edges and all, 66; with
     // 3568 columns and tensor stores 20).
     template <typename E>
     __device__ __forceinline__ void store_rows(int k, int row0, int c0) const {
@@ -616,6 +617,18 @@ struct Worker {
         // unit n of row r, units XORed with the row
         auto unit = [&](int n, int r) { return stg + (n >> 3) % G::BOXES * 4096 + r * 128 + (((n ^ r) & 7) << 4); };
         const uint8_t *const here = unit(8 * k + g, r0), *const before = unit(8 * k + g + 8 * G::BOXES - 1, r0);
+        auto element = [&](uint8_t* row, int r, int b) {
+            *reinterpret_cast<E*>(row + b) = *reinterpret_cast<const E*>(unit(b >> 4, r) + (b & 15));
+        };
+        auto head = [&](uint8_t* row, int r) {
+            if (g * SIZE < min(-static_cast<int>(reinterpret_cast<uintptr_t>(row)) & 15, bytes)) element(row, r, g * SIZE);
+        };
+        auto tail = [&](uint8_t* row, int r) {
+            const int first = -static_cast<int>(reinterpret_cast<uintptr_t>(row)) & 15;
+            const int end = bytes - (static_cast<int>(reinterpret_cast<uintptr_t>(row + bytes)) & 15);
+            const int b = max(first, end) + g * SIZE;
+            if (g * SIZE < 16 && b < bytes) element(row, r, b);
+        };
         uint8_t* to = to0;
 #pragma unroll 2
         for (int i = 0; i < 8; ++i, to += step) {
@@ -630,25 +643,20 @@ struct Worker {
             uint32_t v[4];
             shift_granules<1>(two, (16 - mis) & 15, v);
             if (o >= 0 && o + 16 <= bytes) *reinterpret_cast<uint4*>(to + o) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-        auto element = [&](uint8_t* row, int r, int b) {
-            *reinterpret_cast<E*>(row + b) = *reinterpret_cast<const E*>(unit(b >> 4, r) + (b & 15));
-        };
-        if (k == 0) {
-            to = to0;
-#pragma unroll 1
-            for (int r = r0; r < rows; r += 4, to += step)
-                if (g * SIZE < min(-static_cast<int>(reinterpret_cast<uintptr_t>(to)) & 15, bytes)) element(to, r, g * SIZE);
-        }
-        if (128 * (k + 1) >= bytes) {
-            to = to0;
-#pragma unroll 1
-            for (int r = r0; r < rows; r += 4, to += step) {
-                const int head = -static_cast<int>(reinterpret_cast<uintptr_t>(to)) & 15;
-                const int end = bytes - (static_cast<int>(reinterpret_cast<uintptr_t>(to + bytes)) & 15);
-                const int b = max(head, end) + g * SIZE;
-                if (g * SIZE < 16 && b < bytes) element(to, r, b);
+            if (G::BOXES == 1) {
+                head(to, r0 + 4 * i);
+                tail(to, r0 + 4 * i);
             }
+        }
+        if (G::BOXES > 1 && k == 0) {
+            to = to0;
+#pragma unroll 2
+            for (int r = r0; r < rows; r += 4, to += step) head(to, r);
+        }
+        if (G::BOXES > 1 && 128 * (k + 1) >= bytes) {
+            to = to0;
+#pragma unroll 2
+            for (int r = r0; r < rows; r += 4, to += step) tail(to, r);
         }
     }
     // any strides: a lane per column
