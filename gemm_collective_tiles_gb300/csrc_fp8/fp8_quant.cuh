@@ -99,6 +99,8 @@ __device__ __forceinline__ float cta_max(float v) {
 // Needs x and codes of unit stride, with code rows on 16 bytes.
 // SHIFT: rows of x start anywhere; a lane reads the 16-byte granules around its
 // elements, as far as they lie within x, and shifts them into place.
+// Shifted f32 tiles hold 144 words of x for a moment: two CTAs per SM (three
+// spill: 16384 x 4096 70 us against 73, 1537 x 5003 13.2 against 10.9).
 template <int T, bool TILE, bool SHIFT>
 __global__ void __launch_bounds__(Q_THREADS, !TILE ? 4 : SHIFT && T == T_F32 ? 2 : 3)
     quantize_vec_kernel(const __grid_constant__ QuantParams p) {
