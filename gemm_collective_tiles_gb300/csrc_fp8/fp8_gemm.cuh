@@ -611,7 +611,8 @@ struct Worker {
     template <typename E>
     __device__ __forceinline__ void store_rows(int k, int row0, int c0) const {
         constexpr int SIZE = sizeof(E), ROW = G::BOXES == 1 ? 128 : COLS * SIZE;
-        const int g = lane & 7, r0 = lane >> 3, rows = min(32, p.M - row0), bytes = min(ROW, (p.N - c0) * SIZE);
+        // columns are clipped before they become bytes, which may pass 2^31
+        const int g = lane & 7, r0 = lane >> 3, rows = min(32, p.M - row0), bytes = min(ROW / SIZE, p.N - c0) * SIZE;
         const long long step = 4 * SIZE * p.out_rs;
         uint8_t* const to0 = static_cast<uint8_t*>(p.out) + ((row0 + r0) * p.out_rs + c0) * SIZE;
         // unit n of row r, units XORed with the row
