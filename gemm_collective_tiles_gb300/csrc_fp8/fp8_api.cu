@@ -345,7 +345,9 @@ int make_plan(Plan& pl, bool wg, const iris_b200_config* cfg, const DeviceInfo& 
     }
     if (pl.cg == 0) return IRIS_EINVAL;
     pl.stages = static_cast<int>(stages);
-    pl.group_m = cfg->group_m ? std::max(1, cfg->group_m / pl.cg) : 16 / pl.cg;
+    // one group holds all rows of tiles at most: the same order, and its size times
+    // the columns of tiles is no larger than their number
+    pl.group_m = std::min(cfg->group_m ? std::max(1, cfg->group_m / pl.cg) : 16 / pl.cg, pl.m_blocks);
     pl.copy_a = WS_HEADER;
     pl.copy_b = pl.copy_a + a.copy_bytes;
     pl.tail = pl.copy_b + b.copy_bytes;
