@@ -13,13 +13,15 @@
 // 16-bit operands on their way from shared memory to the MMA (exact for
 // power-of-two scales: a code has at most 4 significant bits), and a chunk is
 // WG_CHUNK stages long, which bounds the length of the sums that the tensor
-// cores keep by themselves.
+// cores keep by themselves.  f16 operands of a chunk whose values would leave
+// f16's range are held times a power of two (run_factors).
 //
 // CTA layout, one CTA per SM:
 //   warp 0       TMA producer (lane 0); KIND_WG: of the codes
 //   warp 1       MMA issuer; owns tensor memory
 //   warp 2       KIND_WG: TMA producer of dY (lane 0)
-//   warp 3       KIND_MM, CG = 1: second MMA issuer
+//   warp 3       KIND_MM, CG = 1: second MMA issuer; KIND_WG, f16: the chunks'
+//                powers of two
 //   warps 4-11   promotion and epilogue: quadrant warp % 4 of the accumulator's
 //                rows, column half (warp - 4) / 4
 //   warps 12-19  KIND_WG: converters
@@ -62,6 +64,8 @@ enum : int {
     WAIT_A_EMPTY = 107,
     WAIT_PARTS = 108,
     WAIT_TAIL = 109,
+    WAIT_FACTOR = 110,
+    WAIT_FACTOR_EMPTY = 111,
     WAIT_DRAIN_TMA = 120,  // from here on: teardown
     WAIT_DRAIN_MMA = 121,
 };
@@ -165,6 +169,7 @@ struct Geo {
     // the codes have a ring of their own (RAWS slots)
     static constexpr int STAGES = KIND == KIND_WG ? 4 : CG == 2 ? 5 : 6;
     static constexpr int RAWS = KIND == KIND_MM ? 0 : 4;
+    static constexpr int FACTORS = KIND == KIND_MM ? 0 : 4;  // chunks whose powers of two are known ahead
     static constexpr int ISSUERS = KIND == KIND_MM && CG == 1 ? 2 : 1;  // warps that issue MMAs
     static constexpr int THREADS = KIND == KIND_MM ? 384 : 640;
     static constexpr int BOXES = KIND == KIND_MM && CG == 1 ? 1 : 2;  // staging per promotion warp, 32 x 128 bytes each
@@ -176,9 +181,9 @@ struct Geo {
     // phase of the barrier, and with an odd ring each would see every other.
     static_assert(ISSUERS == 1 || (STAGES % 2 == 0 && ACCS % 2 == 0), "issuers by parity of the slot");
     static_assert(KIND == KIND_MM || (STAGES % 2 == 0 && RAWS % 2 == 0), "converter groups by parity of the slot");
-    static constexpr int NUM_BARS = 3 * STAGES + 2 * RAWS + 2 * ACCS + 2 * 8 + 2;
+    static constexpr int NUM_BARS = 3 * STAGES + 2 * RAWS + 2 * FACTORS + 2 * ACCS + 2 * 8 + 2;
     static constexpr uint32_t TILES_BYTES = STAGES * STAGE_BYTES + RAWS * RAW_BYTES;
-    static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 32;
+    static constexpr uint32_t BYTES = 1024 + TILES_BYTES + 8 * OUT_BYTES + NUM_BARS * 8 + 16 + FACTORS * 8 + 16;
     // registers: the launch's total (168 or 96 a thread) is shared out anew
     static constexpr int REGS_CTL = KIND == KIND_MM ? 40 : 48;
     static constexpr int REGS_PROMOTE = KIND == KIND_MM ? 232 : 152;
@@ -194,11 +199,12 @@ struct Smem {
     // shared-memory addresses.  Barriers per stage: full (KIND_MM: A and B have
     // landed; KIND_WG: A is converted), b_full (KIND_WG: B has landed), done
     // (its MMAs have run: the stage may be filled again); per slot of codes:
-    // raw_full, raw_empty; per accumulator: acc_full, acc_empty; per promotion
-    // warp: parts_in (every part's sums lie in shared memory), parts_out (every
+    // raw_full, raw_empty; per slot of factors: fac_full, fac_empty; per
+    // accumulator: acc_full, acc_empty; per promotion warp: parts_in (every part's sums lie in shared memory), parts_out (every
     // part has read this CTA's)
-    uint32_t tiles, raw_tiles, full, done, raw_full, raw_empty, b_full, acc_full, acc_empty, parts_in, parts_out, final_bar;
+    uint32_t tiles, raw_tiles, full, done, raw_full, raw_empty, fac_full, fac_empty, b_full, acc_full, acc_empty, parts_in, parts_out, final_bar;
     uint32_t *tmem_slot, *epoch_slot;
+    float2* factors;  // per slot: what a chunk's scales are multiplied by, and what its sums are
     __device__ void carve(uint8_t* p) {
         base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
         tiles = smem_u32(base);
@@ -208,13 +214,16 @@ struct Smem {
         b_full = done + 8 * G::STAGES;
         raw_full = b_full + 8 * G::STAGES;
         raw_empty = raw_full + 8 * G::RAWS;
-        acc_full = raw_empty + 8 * G::RAWS;
+        fac_full = raw_empty + 8 * G::RAWS;
+        fac_empty = fac_full + 8 * G::FACTORS;
+        acc_full = fac_empty + 8 * G::FACTORS;
         acc_empty = acc_full + 8 * G::ACCS;
         parts_in = acc_empty + 8 * G::ACCS;
         parts_out = parts_in + 64;
         final_bar = parts_out + 64;
         tmem_slot = reinterpret_cast<uint32_t*>(base + (final_bar + 16 - tiles));
         epoch_slot = tmem_slot + 1;
+        factors = reinterpret_cast<float2*>(tmem_slot + 4);
     }
     __device__ __forceinline__ uint32_t a(uint32_t s) const { return tiles + s * G::STAGE_BYTES; }
     __device__ __forceinline__ uint32_t b(uint32_t s) const { return tiles + s * G::STAGE_BYTES + G::A_BYTES; }
@@ -926,14 +935,90 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
     return true;
 }
 
-template <int CG, bool DIRECT>
+// f16 weight gradients: code * scale can be as large as fp32 holds, and f16 ends
+// at 65504 (an f16 input close to that becomes 2^16 by its codes already).  So
+// each chunk of WG_CHUNK stages has a power of two 2^-f, by which its scales are
+// multiplied on their way into f16 and its sums divided again in fp32.  f is 0
+// where the chunk's largest finite scale keeps every code within f16's range and
+// the finest code step at f16's own, 2^-24, or above it: there a code times a
+// power-of-two scale is exact.  Otherwise the largest scale is taken to the
+// largest power of two that fits, and values are exact down to 2^(f - 24), 2^-39
+// of the largest value that the chunk could hold.
+// Warp 3, which has nothing else to do, is up to FACTORS chunks ahead: 16
+// scales a lane, all loads in flight, beside some 3 us of MMAs per chunk.  What
+// it costs is the converters' wait, once a chunk, and the first chunk's scales:
+// 4096 x 4096 x 14336 f16 into f32 340 -> 350 us, 777 x 1000 x 1112 9.8 -> 10.4
+// (with the power left out of the scales where it is 1; 355, 10.5 always in).
+template <int CG>
+__device__ void run_factors(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, int lane, int first, int step) {
+    using G = Geo<KIND_WG, CG>;
+    constexpr int PER = WG_CHUNK * G::DEPTH / 32;
+    Ring<G::FACTORS> fac;
+    const float fmax = p.codes_e5m2 ? 57344.f : 448.f;
+    const int top = p.codes_e5m2 ? 0 : 7;        // largest 2^top with fmax * 2^top <= 65504
+    const int bottom = p.codes_e5m2 ? -8 : -15;  // 2^bottom times the codes' finest step is 2^-24
+    for (int u = first; u < p.n_units; u += step) {
+        const Unit x = unit_of<CG>(p, ctl, u);
+        const int kblk = x.mb * CG + half<CG>(ctl);
+        const bool live = kblk * BM < p.M;
+        for (int s = x.lo; s < x.hi; s += WG_CHUNK, fac.next()) {
+            const long long m0 = static_cast<long long>(s) * G::DEPTH + lane;
+            const int left = live ? min(p.D, min(x.hi, s + WG_CHUNK) * G::DEPTH) - s * G::DEPTH - lane : 0;
+            const float* at = p.sa + kblk * p.sa_cs + m0 * p.sa_rs;
+            const long long apart = 32 * p.sa_rs;
+            float v[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                v[i] = 32 * i < left ? *at : 0.f;
+                at += apart;
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) v[i] = amax_finite(0.f, v[i]);
+#pragma unroll
+            for (int w = PER / 2; w > 0; w /= 2)
+#pragma unroll
+                for (int i = 0; i < w; ++i) v[i] = fmaxf(v[i], v[i + w]);
+            // magnitudes order like their bits
+            const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[0]));
+            const float m = __uint_as_float(bits);
+            // m <= 2^e (subnormal scales: 2^-126)
+            const int e = max(static_cast<int>(bits >> 23), 1) - 127 + ((bits & 0x7FFFFFu) && bits >> 23 ? 1 : 0);
+            int f = 0;
+            if (bits != 0u && (m * fmax >= 65520.f || e < bottom)) f = max(-126, min(126, e - top));
+            if (!wait_bar(ctl, sm.fac_empty + 8 * fac.slot, fac.phase ^ 1, WAIT_FACTOR_EMPTY)) return;
+            if (lane == 0) {
+                sm.factors[fac.slot] = make_float2(__int_as_float((127 - f) << 23), __int_as_float((127 + f) << 23));
+                bar_arrive(sm.fac_full + 8 * fac.slot);
+            }
+            __syncwarp();
+        }
+    }
+}
+// The next chunk's factors, for a warp; each of the sixteen that use them tells
+// warp 3 that it has them.
+template <int CG>
+__device__ __forceinline__ bool take_factor(const Ctl& ctl, Smem<KIND_WG, CG>& sm, Ring<Geo<KIND_WG, CG>::FACTORS>& fac, int lane,
+                                            float2& f) {
+    if (!wait_bar(ctl, sm.fac_full + 8 * fac.slot, fac.phase, WAIT_FACTOR)) return false;
+    f = sm.factors[fac.slot];
+    __syncwarp();
+    if (lane == 0) bar_arrive(sm.fac_empty + 8 * fac.slot);
+    fac.next();
+    return true;
+}
+
+template <int CG, bool DIRECT, bool BF16>
 __device__ bool run_promote_wg(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, CG>& sm, uint32_t tmem, int w, int lane,
                                int first, int step) {
     Worker<KIND_WG, CG, DIRECT> wk(p, ctl, sm, tmem, w, lane);
+    Ring<Geo<KIND_WG, CG>::FACTORS> fac;
     for (int u = first; u < p.n_units; u += step) {
         const auto pl = wk.place(u);
-        for (int s = pl.x.lo; s < pl.x.hi; s += WG_CHUNK)
-            if (!wk.template promote<16>(pl.live, 1.f)) return false;
+        for (int s = pl.x.lo; s < pl.x.hi; s += WG_CHUNK) {
+            float2 f = make_float2(1.f, 1.f);
+            if (!BF16 && !take_factor(ctl, sm, fac, lane, f)) return false;
+            if (!wk.template promote<16>(pl.live, f.y)) return false;
+        }
         if (!wk.epilogue(pl, u + step < p.n_units)) return false;
     }
     return true;
@@ -952,6 +1037,8 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
     using G = Geo<KIND_WG, CG>;
     Ring<G::RAWS> rs;
     Ring<G::STAGES> st;
+    Ring<G::FACTORS> fac;
+    float2 factor = make_float2(1.f, 1.f);
     const int group = t >> 7, tt = t & 127;
     const int col = tt >> 3 & 1, j = tt & 3;                 // column of 64 k, quarter of it
     const int r0 = (tt >> 4) * 2 ^ ((tt & 4) ? 5 : 0);        // first row
@@ -982,10 +1069,16 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
         };
         fetch();
         for (int s = x.lo; s < x.hi; ++s, ++turn, rs.next(), st.next()) {
+            // both groups take every chunk's factors, whether or not it has a stage of theirs
+            if (!BF16 && (s - x.lo) % WG_CHUNK == 0 && !take_factor(ctl, sm, fac, t & 31, factor)) return;
             if ((turn & 1) != group) continue;
             float sc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[i] = next[i];
+            if (!BF16 && factor.x != 1.f) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[i] *= factor.x;
+            }
             fetch();
             if (!wait_bar(ctl, sm.raw_full + 8 * rs.slot, rs.phase, WAIT_RAW)) return;
             if (!wait_bar(ctl, sm.done + 8 * st.slot, st.phase ^ 1, WAIT_A_EMPTY)) return;
@@ -1056,6 +1149,11 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
         uint32_t e = *reinterpret_cast<volatile uint32_t*>(&p.ws->epoch) + 1u;
         *sm.epoch_slot = e == 0u ? 1u : e;
     }
+    if (KIND == KIND_WG && threadIdx.x == 96 && !p.x_bf16)
+        for (int s = 0; s < G::FACTORS; ++s) {
+            bar_init(sm.fac_full + 8 * s, 1);
+            bar_init(sm.fac_empty + 8 * s, 16);
+        }
     if (warp == 1) tmem_alloc<G::TMEM_COLS, CG>(sm.tmem_slot);
     tc_fence_before();
     __syncthreads();
@@ -1075,13 +1173,16 @@ __global__ void __launch_bounds__(Geo<KIND, CG>::THREADS, 1) block_gemm_kernel(c
             if (CG == 1 || rank == 0) run_mma<KIND, CG>(p, ctl, sm, tmem, 0, first, step);
         }
         if (G::ISSUERS == 2 && warp == 3) run_mma<KIND, CG>(p, ctl, sm, tmem, 1, first, step);
+        if constexpr (KIND == KIND_WG)
+            if (warp == 3 && !p.x_bf16) run_factors<CG>(p, ctl, sm, lane, first, step);
         __syncwarp();
     } else if (warp < 12) {
         reg_inc<G::REGS_PROMOTE>();
         if constexpr (KIND == KIND_MM)
             run_promote_mm<CG, DIRECT>(p, ctl, sm, tmem, warp - 4, lane, first, step);
         else
-            run_promote_wg<CG, DIRECT>(p, ctl, sm, tmem, warp - 4, lane, first, step);
+            p.x_bf16 ? run_promote_wg<CG, DIRECT, true>(p, ctl, sm, tmem, warp - 4, lane, first, step)
+                     : run_promote_wg<CG, DIRECT, false>(p, ctl, sm, tmem, warp - 4, lane, first, step);
         if (lane == 0) bulk_wait_all();  // its stores have left shared memory, stopped or not
         __syncwarp();
     } else if constexpr (KIND == KIND_WG) {

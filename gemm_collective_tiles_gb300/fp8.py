@@ -106,8 +106,9 @@ def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
 
     With ``pow2`` a block's scale is the smallest power of two that takes its
     largest finite magnitude into the codes' range, and scaled codes are exact
-    16-bit floats; without it the scale maps that magnitude to the largest
-    code.  NaN and infinities become the NaN code and leave the scale to the
+    bf16 numbers (f16 numbers too for f16 input, but for 65536, to which codes
+    round what is close to f16's largest); without it the scale maps that
+    magnitude to the largest code.  NaN and infinities become the NaN code and leave the scale to the
     block's other elements; zero blocks get the smallest scale."""
     if block not in _ROWS:
         raise ValueError(f"unknown block {block!r}")
@@ -180,7 +181,10 @@ def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, ou
 
     X (M, K) codes with "rows" scales (M, ceil(K/128)); dY (M, N) f16 or bf16;
     out f16, bf16 or f32.  X's values enter in dY's type, exactly where the
-    scales are powers of two.  Returns the workspace."""
+    scales are powers of two; for f16, values past its range or below its
+    finest step are held times a power of two for each run of 512 tokens, and
+    lose at most what lies under 2^-39 of the largest value that the run's
+    scales allow.  Returns the workspace."""
     mx = _mat("X", X, None, _FP8, -1)
     M, K = X.shape
     index = X.get_device()

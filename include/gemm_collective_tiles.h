@@ -541,8 +541,14 @@ IRIS_API int iris_b200_matmul_fp8(const iris_b200_matmul_fp8_args* args, const i
  *   X, x_scales  M x K codes, M x ceil(K/128) scales (1 x 128 blocks).
  *   dY           M x N, f16 or bf16.
  *   out          f16, bf16 or f32.
- * X's values enter the product in dY's type: exact for power-of-two scales
- * (in f16's range), rounded once to 16 bits otherwise.  Sums are fp32.
+ * X's values enter the product in dY's type: exact for power-of-two scales,
+ * rounded once to 16 bits otherwise.  Sums are fp32.  f16: where a run of 512
+ * tokens (counted from the start of a CTA's part of the contraction) has a
+ * scale whose codes may pass 65504, or only scales whose finest code step is
+ * below 2^-24, the run's values are held times a power of two that takes its
+ * largest scale's codes to the top of f16's range, and its sums divided by it:
+ * any finite scales serve, and what a value loses lies under 2^-39 of the
+ * largest value that the run's scales allow.
  */
 typedef struct {
     iris_b200_mat X, x_scales, dY, out;
