@@ -228,13 +228,26 @@ int launch_repack(const iris_b200_mat* m, Operand& o, void* dst, int sms, cudaSt
     return IRIS_OK;
 }
 
+// A tensor map.  The driver's call wants the calling thread to have a context,
+// which runtime calls give it; a thread that has made none that does (autograd's,
+// whose first work may be a product) is given the current device's here.
+CUresult encode(CUtensorMap* m, CUtensorMapDataType dt, cuuint32_t rank, const void* data, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapL2promotion l2) {
+    const cuuint32_t es[3] = {1, 1, 1};
+    auto call = [&] {
+        return g_encode(m, dt, rank, const_cast<void*>(data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    const CUresult r = call();
+    int dev = 0;
+    if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+    return call();
+}
 int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand& o, uint32_t b0, uint32_t b1) {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.pitch) * elem};
-    cuuint32_t box[2] = {b0, b1}, es[2] = {1, 1};
-    const CUresult r = g_encode(m, dt, 2, const_cast<void*>(o.data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    cuuint32_t box[2] = {b0, b1};
+    const CUresult r = encode(m, dt, 2, o.data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit operand)", static_cast<int>(r));
 }
 // 16-bit rows as groups of 64 columns, {64, row, column / 64}: a box of 64 rows
@@ -242,10 +255,8 @@ int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand&
 int make_map_groups(CUtensorMap* m, CUtensorMapDataType dt, const Operand& o, uint32_t groups) {
     cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(o.rows), static_cast<cuuint64_t>(o.cols / 64)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.pitch) * 2, 128};
-    cuuint32_t box[3] = {64, 64, groups}, es[3] = {1, 1, 1};
-    const CUresult r = g_encode(m, dt, 3, const_cast<void*>(o.data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    cuuint32_t box[3] = {64, 64, groups};
+    const CUresult r = encode(m, dt, 3, o.data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (groups of columns)", static_cast<int>(r));
 }
 // out {n, row} with a box of 128 bytes x 32 rows
@@ -253,12 +264,11 @@ int make_store_map(CUtensorMap* m, int t, const void* data, int64_t N, int64_t M
     const int elem = dtype_size(t);
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * elem};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), 32}, es[2] = {1, 1};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), 32};
     const CUtensorMapDataType dt = t == IRIS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : t == IRIS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const CUresult r = g_encode(m, dt, 2, const_cast<void*>(data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode(m, dt, 2, data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_NONE);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit output)", static_cast<int>(r));
 }
 
