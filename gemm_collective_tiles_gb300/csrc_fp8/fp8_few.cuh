@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) few_rows_kernel(const 
             int left = (hi - mine + 1) / 2;
             float a[AHEAD], b[AHEAD];
             auto fetch = [&](float& fa, float& fb) {
-                fa = __ldg(pa);
-                fb = __ldg(pb);
+                fa = *pa;
+                fb = *pb;
                 if (--left > 0) {
                     pa += 2 * p.sa_cs;
                     pb += 2 * p.sb_rs;

@@ -910,8 +910,8 @@ __device__ bool run_promote_mm(const GemmParams& p, const Ctl& ctl, Smem<KIND_MM
         int left = pl.x.hi - pl.x.lo;
         float a[AHEAD], b[AHEAD];
         auto fetch = [&](float& fa, float& fb) {
-            fa = __ldg(pa);
-            fb = __ldg(pb);
+            fa = *pa;
+            fb = *pb;
             if (--left > 0) {
                 pa += p.sa_cs;
                 pb += p.sb_rs;
@@ -1061,7 +1061,7 @@ __device__ void run_convert(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
             const float* q = at;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                next[i] = 16 * i < left ? __ldg(q) : 0.f;
+                next[i] = 16 * i < left ? *q : 0.f;
                 q += apart;
             }
             at += 8 * apart;

@@ -144,8 +144,7 @@ __global__ void __launch_bounds__(Q_THREADS, !TILE ? 4 : SHIFT && T == T_F32 ? 2
             whole[i] = i < rows && left == 16 && at >= x && at + 16 * W + (off[i] ? 16 : 0) <= end;
 #pragma unroll
             for (int w = 0; w <= W; ++w) {
-                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                if (whole[i] && (w < W || off[i])) q = __ldg(reinterpret_cast<const uint4*>(at) + w);
+                const uint4 q = load16_if(at + 16 * w, whole[i] && (w < W || off[i]));
                 g[i][4 * w] = q.x;
                 g[i][4 * w + 1] = q.y;
                 g[i][4 * w + 2] = q.z;
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(Q_THREADS, !TILE ? 4 : SHIFT && T == T_F32 ? 2
                 if (left == 16) {
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
-                        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + i * step) + w);
+                        const uint4 q = reinterpret_cast<const uint4*>(src + i * step)[w];
                         raw[i][4 * w] = q.x;
                         raw[i][4 * w + 1] = q.y;
                         raw[i][4 * w + 2] = q.z;
@@ -359,9 +358,8 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_any_kernel(const __grid_co
 // first, so it comes from the L1 cache), shifts and writes one; four rows are
 // under way per thread.  Near the matrix's ends, byte by byte.
 constexpr int COPY_ROWS = 32;  // rows of a CTA's tile: 8 warps x 4; columns: 32 granules
-__global__ void __launch_bounds__(256) repack_rows_kernel(const uint8_t* __restrict__ src, long long rs,
-                                                          uint8_t* __restrict__ dst, long long pitch, long long rows,
-                                                          long long bytes) {
+__global__ void __launch_bounds__(256) repack_rows_kernel(const uint8_t* src, long long rs, uint8_t* dst, long long pitch,
+                                                          long long rows, long long bytes) {
     constexpr int PER = COPY_ROWS / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long tiles_c = (pitch + 511) / 512, tiles = tiles_c * ((rows + COPY_ROWS - 1) / COPY_ROWS);
@@ -382,8 +380,7 @@ __global__ void __launch_bounds__(256) repack_rows_kernel(const uint8_t* __restr
             whole[i] = r < rows && at >= src && at + (off[i] ? 32 : 16) <= end;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                if (whole[i] && (w == 0 || off[i])) q = __ldg(reinterpret_cast<const uint4*>(at) + w);
+                const uint4 q = load16_if(at + 16 * w, whole[i] && (w == 0 || off[i]));
                 g[i][4 * w] = q.x;
                 g[i][4 * w + 1] = q.y;
                 g[i][4 * w + 2] = q.z;
@@ -406,9 +403,8 @@ __global__ void __launch_bounds__(256) repack_rows_kernel(const uint8_t* __restr
 
 // The same from any strides, in elements E.
 template <typename E>
-__global__ void __launch_bounds__(256) repack_kernel(const E* __restrict__ src, long long rs, long long cs,
-                                                     E* __restrict__ dst, long long pitch, long long rows,
-                                                     long long cols) {
+__global__ void __launch_bounds__(256) repack_kernel(const E* src, long long rs, long long cs, E* dst, long long pitch,
+                                                     long long rows, long long cols) {
     // 32 x 32 tiles through shared memory: reads run along the source's
     // unit-stride dimension, writes along the destination's rows
     __shared__ E tile[32][33];
