@@ -27,6 +27,7 @@ a ``HeapTensor`` names the same byte offset in every region.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import math
@@ -173,12 +174,14 @@ class Workspace:
     """Zero-initialised device workspace, reusable across calls on one stream.
 
     The zero-fill is finished before the constructor returns, so the first
-    call may run on any stream (a workspace is created once and reused)."""
+    call may run on any stream (a workspace is created once and reused).  With
+    ``wait=False`` it is only enqueued on the current stream, and the memory
+    belongs to that stream: the ops make theirs so, on the stream they run on."""
 
-    def __init__(self, nbytes: int, device="cuda"):
+    def __init__(self, nbytes: int, device="cuda", wait: bool = True):
         self.nbytes = max(256, _round_up(int(nbytes), 256))
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
-        if self.buf.is_cuda:
+        if wait and self.buf.is_cuda:
             torch.cuda.current_stream(self.buf.device).synchronize()
 
     @property
@@ -186,9 +189,22 @@ class Workspace:
         return self.buf.data_ptr()
 
 
-def _ws(ws: Optional[Workspace], need: int, device) -> Workspace:
+def _on(stream, index: int):
+    """Context in which memory is allocated on `stream` (None: the current one;
+    a torch stream or a raw handle) of device `index`."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else torch.cuda.default_stream(index)
+    return torch.cuda.stream(stream)
+
+
+def _ws(ws: Optional[Workspace], need: int, device, stream=None) -> Workspace:
     if ws is None or ws.nbytes < need:
-        ws = Workspace(need, device)
+        # on the stream that will use it: a workspace that the caller drops goes
+        # back to that stream, behind the work that still uses it
+        with _on(stream, torch.device(device).index or 0):
+            ws = Workspace(need, device, wait=False)
     return ws
 
 
@@ -213,7 +229,7 @@ def all_gather_matmul(heap: SymmetricHeap, A: HeapTensor, B: HeapTensor, out: He
     K, N = B.shape
     config = _resolve(config, "all_gather_matmul", heap.world, M, N, K, B.dtype)
     ws = _ws(workspace, workspace_size("all_gather_matmul", M, N, K, heap.world, B.dtype, config),
-             heap.buf.device)
+             heap.buf.device, stream)
     _native.check("iris_b200_all_gather_matmul", _native.load().iris_b200_all_gather_matmul(
         ctypes.byref(heap.c_heap()), A.offset, B.offset, _bias_off(bias), out.offset,
         gathered.offset, M, N, K, _DT[B.dtype], _cfgp(config), ws.ptr, ws.nbytes, _stream(stream)))
@@ -222,7 +238,7 @@ def all_gather_matmul(heap: SymmetricHeap, A: HeapTensor, B: HeapTensor, out: He
 
 def _mm_coll(name, heap, A, B, out, bias, config, workspace, stream, M, N, K):
     config = _resolve(config, name, heap.world, M, N, K, B.dtype)
-    ws = _ws(workspace, workspace_size(name, M, N, K, heap.world, B.dtype, config), heap.buf.device)
+    ws = _ws(workspace, workspace_size(name, M, N, K, heap.world, B.dtype, config), heap.buf.device, stream)
     fn = getattr(_native.load(), "iris_b200_" + name)
     _native.check("iris_b200_" + name, fn(
         ctypes.byref(heap.c_heap()), A.offset, B.offset, _bias_off(bias), out.offset, M, N, K,
@@ -278,7 +294,7 @@ def concurrent_gemm_collective(A: Optional[torch.Tensor], B: Optional[torch.Tens
     count = x_in.nbytes // torch.empty((), dtype=x_in.dtype).element_size() if x_in is not None else 0
     config = _resolve(config, "concurrent", W, M, N, K, gdt, coll if count else None, count,
                       x_in.dtype if x_in is not None else None)
-    ws = _ws(workspace, workspace_size("concurrent", M, N, K, W, gdt, config), dev)
+    ws = _ws(workspace, workspace_size("concurrent", M, N, K, W, gdt, config), dev, stream)
     hp = ctypes.byref(heap.c_heap()) if heap is not None else None
     _native.check("iris_b200_concurrent_gemm_collective",
                   _native.load().iris_b200_concurrent_gemm_collective(

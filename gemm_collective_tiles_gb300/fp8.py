@@ -136,10 +136,10 @@ def _product(name: str, fn, args, config, ws, index: int, stream):
     cfg, st = _cfgp(config), _stream(stream, index)
     rc = _native.IRIS_ENOWS if ws is None else fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc == _native.IRIS_ENOWS:
-        from . import Workspace
+        from . import _ws
         need, size = ctypes.c_size_t(0), "iris_b200_" + name + "_workspace_size"
         _native.check(size, getattr(_native.load(), size)(args, cfg, ctypes.byref(need)))
-        ws = Workspace(int(need.value), torch.device("cuda", index))
+        ws = _ws(None, int(need.value), torch.device("cuda", index), stream)
         rc = fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc:
         _native.check("iris_b200_" + name, rc)
