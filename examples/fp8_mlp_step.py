@@ -39,7 +39,7 @@ def train(steps=20, tokens=4096, width=1024, hidden=4096, rate=None, seed=0):
     g = torch.Generator(device="cuda").manual_seed(seed)
     up, down = Layer(width, hidden, g), Layer(hidden, width, g)
     target = torch.randn(width, width, generator=g, device="cuda") / width ** 0.5
-    workspace = gct.Workspace(256)  # enough where no operand has to be copied; the ops replace one that is not
+    workspace = gct.Workspace(256)  # grows to what the layers need
     optimizer = torch.optim.Adam([up.weight, up.bias, down.weight, down.bias], lr=rate or 0.75 / width)
     losses = []
     for _ in range(steps):
@@ -53,6 +53,8 @@ def train(steps=20, tokens=4096, width=1024, hidden=4096, rate=None, seed=0):
         loss.backward()
         optimizer.step()
         losses.append(loss.item())
+        if gct.query_status(workspace)[0]:
+            raise RuntimeError("a product gave up waiting on the device")
     return losses, (up, down)
 
 

@@ -55,7 +55,7 @@ __all__ = [
     "SymmetricHeap", "HeapTensor", "Workspace", "make_config", "workspace_size",
     "all_gather_matmul", "matmul_reduce_scatter", "matmul_all_gather", "matmul_all_reduce",
     "concurrent_gemm_collective", "concurrent_two_stream", "query_status", "num_sms", "IrisError",
-    "empty_fp8", "quantize_fp8", "matmul_fp8", "weight_grad_fp8", "fp8_linear",
+    "empty_fp8", "quantize_fp8", "matmul_fp8", "weight_grad_fp8", "fp8_linear", "fp8_workspace",
 ]
 
 _DT = {torch.float16: _native.IRIS_F16, torch.bfloat16: _native.IRIS_BF16,
@@ -181,8 +181,19 @@ class Workspace:
     def __init__(self, nbytes: int, device="cuda", wait: bool = True):
         self.nbytes = max(256, _round_up(int(nbytes), 256))
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        self._outgrown = []
         if wait and self.buf.is_cuda:
             torch.cuda.current_stream(self.buf.device).synchronize()
+
+    def _grow(self, nbytes: int) -> None:
+        """At least nbytes, in new memory of the current stream.  The header
+        moves along, with whatever error it holds; the memory before is kept,
+        for graphs that were captured with it."""
+        more = Workspace(nbytes, self.buf.device, wait=False)
+        more.buf[:256].copy_(self.buf[:256])
+        self.buf[16:32].zero_()  # the error is the new header's
+        self._outgrown.append(self.buf)
+        self.buf, self.nbytes = more.buf, more.nbytes
 
     @property
     def ptr(self) -> int:
@@ -353,8 +364,12 @@ def sm_partition_release():
 def query_status(workspace: Workspace, stream=None):
     """Synchronise the stream and return (code, raw_status, where, index)."""
     st, wh, ix = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
-    rc = _native.load().iris_b200_query_status(ctypes.c_void_p(workspace.ptr), _stream(stream),
-                                               ctypes.byref(st), ctypes.byref(wh), ctypes.byref(ix))
+    # graphs that were captured before the workspace grew report to what it was
+    for buf in (workspace.buf, *workspace._outgrown):
+        rc = _native.load().iris_b200_query_status(ctypes.c_void_p(buf.data_ptr()), _stream(stream),
+                                                   ctypes.byref(st), ctypes.byref(wh), ctypes.byref(ix))
+        if rc:
+            break
     return rc, st.value, wh.value, ix.value
 
 
@@ -364,4 +379,4 @@ def num_sms() -> int:
     return n.value
 
 
-from .fp8 import empty_fp8, fp8_linear, matmul_fp8, quantize_fp8, weight_grad_fp8  # noqa: E402
+from .fp8 import empty_fp8, fp8_linear, fp8_workspace, matmul_fp8, quantize_fp8, weight_grad_fp8  # noqa: E402

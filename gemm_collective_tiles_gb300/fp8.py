@@ -8,8 +8,8 @@ forward product and as the 8-bit checkpoint that the backward pass reads.
 
 Like the library's other ops, every op here writes into tensors that the
 caller owns, enqueues its kernels on one stream and returns (the products:
-the workspace, to be passed to the next call on that stream).  Tensors may
-have any non-negative strides.
+the workspace, to be passed to the next call on that stream; one that is passed
+and too small grows).  Tensors may have any non-negative strides.
 """
 from __future__ import annotations
 
@@ -129,17 +129,21 @@ def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
 
 
 def _product(name: str, fn, args, config, ws, index: int, stream):
-    """One product with the given workspace, or a new one where it is missing or too small."""
+    """One product with the given workspace, grown where it is too small, or with a new one."""
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _product(name, fn, args, config, ws, index, stream)
     cfg, st = _cfgp(config), _stream(stream, index)
     rc = _native.IRIS_ENOWS if ws is None else fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc == _native.IRIS_ENOWS:
-        from . import _ws
+        from . import _on, _ws
         need, size = ctypes.c_size_t(0), "iris_b200_" + name + "_workspace_size"
         _native.check(size, getattr(_native.load(), size)(args, cfg, ctypes.byref(need)))
-        ws = _ws(None, int(need.value), torch.device("cuda", index), stream)
+        if ws is None:
+            ws = _ws(None, int(need.value), torch.device("cuda", index), stream)
+        else:
+            with _on(stream, index):
+                ws._grow(int(need.value))
         rc = fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc:
         _native.check("iris_b200_" + name, rc)
@@ -198,6 +202,35 @@ def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, ou
     return _product("weight_grad_fp8", _native.load().iris_b200_weight_grad_fp8, args, config, workspace, index, stream)
 
 
+_layer_workspaces = {}  # by device and stream
+
+
+def fp8_workspace(device="cuda"):
+    """The workspace of ``fp8_linear`` calls on the device's current stream that
+    are given none: one per stream, kept and grown as needed.  Errors on the
+    device in such calls are found by ``query_status(fp8_workspace())``."""
+    from . import Workspace
+    index = torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    key = index, _stream(None, index)
+    ws = _layer_workspaces.get(key)
+    if ws is None:
+        ws = _layer_workspaces.setdefault(key, Workspace(256, torch.device("cuda", index), wait=False))
+    return ws
+
+
+def _layer_workspace(workspace, device):
+    """The caller's; else the stream's; else, in a capture, whose graph may run
+    beside that stream's work, a new one."""
+    if workspace is not None:
+        return workspace
+    if torch.cuda.is_current_stream_capturing():
+        from . import Workspace
+        return Workspace(256, device, wait=False)
+    return fp8_workspace(device)
+
+
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, W_scale, weight, bias, grad_dtype, workspace):
@@ -206,10 +239,10 @@ class _Fp8Linear(torch.autograd.Function):
         codes, scales = empty_fp8(M, K, "rows", device=x.device)
         quantize_fp8(x2, codes, scales)
         y = torch.empty(M, W.shape[1], dtype=x.dtype, device=x.device)
-        ctx.ws = matmul_fp8(codes, scales, W, W_scale, y, bias=bias, workspace=workspace)
+        matmul_fp8(codes, scales, W, W_scale, y, bias=bias, workspace=_layer_workspace(workspace, x.device))
         # the 8-bit checkpoint is all that is kept of x
         ctx.save_for_backward(codes, scales, W, W_scale)
-        ctx.x_shape, ctx.grad_dtype, ctx.has_bias = x.shape, grad_dtype, bias is not None
+        ctx.x_shape, ctx.grad_dtype, ctx.has_bias, ctx.workspace = x.shape, grad_dtype, bias is not None, workspace
         return y.reshape(*x.shape[:-1], W.shape[1])
 
     @staticmethod
@@ -219,12 +252,12 @@ class _Fp8Linear(torch.autograd.Function):
         N = W.shape[1]
         dy2 = dy.reshape(M, N)
         dx = dw = db = None
-        ws = ctx.ws
+        ws = _layer_workspace(ctx.workspace, dy.device)
         if ctx.needs_input_grad[0]:
             dcodes, dscales = empty_fp8(M, N, "rows", ctx.grad_dtype, dy.device)
             quantize_fp8(dy2, dcodes, dscales)
             dx = torch.empty(M, K, dtype=dy.dtype, device=dy.device)
-            ws = matmul_fp8(dcodes, dscales, W.t(), W_scale.t(), dx, workspace=ws)
+            matmul_fp8(dcodes, dscales, W.t(), W_scale.t(), dx, workspace=ws)
             dx = dx.reshape(ctx.x_shape)
         if ctx.needs_input_grad[3]:
             dw = torch.empty(K, N, dtype=torch.float32, device=dy.device)
@@ -242,7 +275,12 @@ def fp8_linear(x: torch.Tensor, W: torch.Tensor, W_scale: torch.Tensor, weight: 
     (K, N) that W was quantised from and that receives the gradient (None: no
     weight gradient).  The forward pass quantises x once; codes and scales are
     the product's operand and, in place of x, what is kept for the backward
-    pass: dx = quantised(dy) @ W^T, dweight = checkpoint^T @ dy."""
+    pass: dx = quantised(dy) @ W^T, dweight = checkpoint^T @ dy.
+
+    All products use ``workspace``, which grows to what they need and reports
+    their device errors to ``query_status``; without one they use the stream's,
+    ``fp8_workspace()``.  In a graph capture, where that belongs to work beside
+    the graph, calls without one make their own: pass one to be told of errors."""
     if x.dim() < 1 or x.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("x is a f16 or bf16 tensor (..., K)")
     if weight is not None and (weight.dtype != torch.float32 or weight.shape != W.shape):
