@@ -245,7 +245,10 @@ class _Fp8Linear(torch.autograd.Function):
         ctx.x_shape, ctx.grad_dtype, ctx.has_bias, ctx.workspace = x.shape, grad_dtype, bias is not None, workspace
         return y.reshape(*x.shape[:-1], W.shape[1])
 
+    # the kernels' gradients have no derivatives of their own: asking for second
+    # ones is an error, not a sum without some of its terms
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         codes, scales, W, W_scale = ctx.saved_tensors
         M, K = codes.shape
