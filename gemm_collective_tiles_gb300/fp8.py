@@ -66,6 +66,11 @@ def _vec(name: str, t: torch.Tensor, n: int, dtypes, index: int) -> int:
     return t.data_ptr()
 
 
+# Tells autograd that tensors were written by address: a backward pass that kept
+# what was there before is an error then.
+_written = torch._C._increment_version
+
+
 def _cfgp(config):
     if config is None:
         return None
@@ -126,13 +131,14 @@ def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
             rc = lib.iris_b200_quantize_fp8(args, st)
     if rc:
         _native.check("iris_b200_quantize_fp8", rc)
+    _written((codes, scales))
 
 
-def _product(name: str, fn, args, config, ws, index: int, stream):
+def _product(name: str, fn, args, out, config, ws, index: int, stream):
     """One product with the given workspace, grown where it is too small, or with a new one."""
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
-            return _product(name, fn, args, config, ws, index, stream)
+            return _product(name, fn, args, out, config, ws, index, stream)
     cfg, st = _cfgp(config), _stream(stream, index)
     rc = _native.IRIS_ENOWS if ws is None else fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc == _native.IRIS_ENOWS:
@@ -147,6 +153,7 @@ def _product(name: str, fn, args, config, ws, index: int, stream):
         rc = fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc:
         _native.check("iris_b200_" + name, rc)
+    _written((out,))
     return ws
 
 
@@ -175,7 +182,7 @@ def matmul_fp8(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale:
         bias_ptr, bias_dt = _vec("bias", bias, N, _DT, index), _DT[bias.dtype]
     args = _native.pack_matmul_fp8(*ma, *msa, *mb, *msb, *mo, bias_ptr, M, N, K, _FP8[A.dtype], _FP8[B.dtype], bias_dt,
                                    _DT[out.dtype])
-    return _product("matmul_fp8", _native.load().iris_b200_matmul_fp8, args, config, workspace, index, stream)
+    return _product("matmul_fp8", _native.load().iris_b200_matmul_fp8, args, out, config, workspace, index, stream)
 
 
 def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, out: torch.Tensor, config=None,
@@ -199,7 +206,7 @@ def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, ou
     ms = _mat("X_scale", X_scale, (M, _blocks(K)), _F32, index)
     mo = _mat("out", out, (K, N), _DT, index)
     args = _native.pack_weight_grad_fp8(*mx, *ms, *md, *mo, M, N, K, _FP8[X.dtype], _DT[dY.dtype], _DT[out.dtype], 0)
-    return _product("weight_grad_fp8", _native.load().iris_b200_weight_grad_fp8, args, config, workspace, index, stream)
+    return _product("weight_grad_fp8", _native.load().iris_b200_weight_grad_fp8, args, out, config, workspace, index, stream)
 
 
 _layer_workspaces = {}  # by device and stream

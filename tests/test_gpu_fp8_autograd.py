@@ -26,3 +26,47 @@ def test_second_derivatives_are_refused():
     for g in grads:  # a penalty on a gradient beside the loss itself
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (loss + g.float().sum()).backward(retain_graph=True)
+
+
+@pytest.mark.parametrize("what", ["codes and scales", "the scales alone"])
+def test_weights_quantised_again_before_the_backward_pass_are_an_error(what):
+    x, W, W_scale, weight, bias = layer(40, 256, 128)
+    y = gct.fp8_linear(x, W, W_scale, weight, bias)
+    other = gct.empty_fp8(256, 128, "tiles")[0]
+    gct.quantize_fp8(weight.detach() * 2, other if "alone" in what else W, W_scale, block="tiles")
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward(torch.ones_like(y))
+    gct.fp8_linear(x, W, W_scale, weight, bias).sum().backward()  # the next forward pass has the new ones
+
+
+def test_what_the_ops_write_counts_as_written():
+    x, W, W_scale, _, _ = layer(40, 256, 128)
+    codes, scales = gct.empty_fp8(40, 256)
+    out, dw = torch.empty(40, 128, device="cuda"), torch.empty(256, 128, device="cuda")
+    before = [t._version for t in (codes, scales, out, dw)]
+    gct.quantize_fp8(x.detach(), codes, scales)
+    gct.matmul_fp8(codes, scales, W, W_scale, out)
+    gct.weight_grad_fp8(codes, scales, torch.ones(40, 128, dtype=torch.bfloat16, device="cuda"), dw)
+    assert all(t._version > v for t, v in zip((codes, scales, out, dw), before))
+    with torch.inference_mode():  # whose tensors have no count
+        again = gct.empty_fp8(40, 256)
+        gct.quantize_fp8(x.detach(), *again)
+        y = torch.empty(40, 128, device="cuda")
+        gct.matmul_fp8(*again, W, W_scale, y)
+    assert torch.equal(y, out)
+
+
+@pytest.mark.parametrize("op", ["matmul", "weight_grad"])
+def test_an_output_that_a_graph_has_kept_is_not_overwritten_unnoticed(op):
+    x, W, W_scale, _, _ = layer(40, 256, 128)
+    codes, scales = gct.empty_fp8(40, 256)
+    gct.quantize_fp8(x.detach(), codes, scales)
+    out = torch.ones((40, 128) if op == "matmul" else (256, 128), device="cuda")
+    factor = torch.ones_like(out, requires_grad=True)
+    loss = (factor * out).sum()  # keeps out
+    if op == "matmul":
+        gct.matmul_fp8(codes, scales, W, W_scale, out)
+    else:
+        gct.weight_grad_fp8(codes, scales, torch.ones(40, 128, dtype=torch.bfloat16, device="cuda"), out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
