@@ -249,7 +249,8 @@ class _Fp8Linear(torch.autograd.Function):
         matmul_fp8(codes, scales, W, W_scale, y, bias=bias, workspace=_layer_workspace(workspace, x.device))
         # the 8-bit checkpoint is all that is kept of x
         ctx.save_for_backward(codes, scales, W, W_scale)
-        ctx.x_shape, ctx.grad_dtype, ctx.has_bias, ctx.workspace = x.shape, grad_dtype, bias is not None, workspace
+        ctx.x_shape, ctx.grad_dtype, ctx.workspace = x.shape, grad_dtype, workspace
+        ctx.bias_dtype = None if bias is None else bias.dtype
         return y.reshape(*x.shape[:-1], W.shape[1])
 
     # the kernels' gradients have no derivatives of their own: asking for second
@@ -272,8 +273,8 @@ class _Fp8Linear(torch.autograd.Function):
         if ctx.needs_input_grad[3]:
             dw = torch.empty(K, N, dtype=torch.float32, device=dy.device)
             weight_grad_fp8(codes, scales, dy2, dw, workspace=ws)
-        if ctx.has_bias and ctx.needs_input_grad[4]:
-            db = dy2.float().sum(0).to(dy.dtype)
+        if ctx.bias_dtype is not None and ctx.needs_input_grad[4]:
+            db = dy2.sum(0, dtype=torch.float32).to(ctx.bias_dtype)
         return dx, None, None, dw, db, None, None
 
 

@@ -70,3 +70,28 @@ def test_an_output_that_a_graph_has_kept_is_not_overwritten_unnoticed(op):
         gct.weight_grad_fp8(codes, scales, torch.ones(40, 128, dtype=torch.bfloat16, device="cuda"), out)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+@pytest.mark.parametrize("tokens", [1, 70, 5000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_the_gradient_of_a_32_bit_bias_has_32_bits(dtype, tokens):
+    """Sums of `tokens` fp32 additions: at most tokens * 2^-23 of the terms' sizes off, and no 16-bit rounding."""
+    x, W, W_scale, weight, bias = layer(tokens, 128, 96, dtype=dtype, bias=torch.float32)
+    g = torch.Generator(device="cuda").manual_seed(72)
+    y = gct.fp8_linear(x.detach(), W, W_scale, None, bias)
+    dy = torch.randn(y.shape, generator=g, device="cuda").to(dtype)
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    db, = torch.autograd.grad(y, bias, dy)
+    assert torch.cuda.max_memory_allocated() - held < dy.numel() * 2 + 65536  # no 32-bit copy of dy
+    assert db.dtype == torch.float32
+    want, S = dy.double().sum(0), dy.double().abs().sum(0)
+    assert ((db.double() - want).abs() <= tokens * 2.0 ** -23 * S).all()
+
+
+@pytest.mark.parametrize("bias", [torch.bfloat16, torch.float16, torch.float32])
+def test_bias_gradients_have_the_biass_type(bias):
+    x, W, W_scale, weight, b = layer(33, 128, 96, bias=bias)
+    gct.fp8_linear(x, W, W_scale, weight, b).backward(torch.ones(33, 96, dtype=torch.bfloat16, device="cuda"))
+    assert b.grad.dtype == bias and (b.grad == 33).all()
