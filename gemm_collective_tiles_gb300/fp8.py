@@ -14,6 +14,7 @@ and too small grows).  Tensors may have any non-negative strides.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional
 
 import torch
@@ -241,7 +242,7 @@ def _layer_workspace(workspace, device):
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, W_scale, weight, bias, grad_dtype, workspace):
-        x2 = x.reshape(-1, x.shape[-1])
+        x2 = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])  # sizes of zero among them
         M, K = x2.shape
         codes, scales = empty_fp8(M, K, "rows", device=x.device)
         quantize_fp8(x2, codes, scales)

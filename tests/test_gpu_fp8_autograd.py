@@ -95,3 +95,24 @@ def test_bias_gradients_have_the_biass_type(bias):
     x, W, W_scale, weight, b = layer(33, 128, 96, bias=bias)
     gct.fp8_linear(x, W, W_scale, weight, b).backward(torch.ones(33, 96, dtype=torch.bfloat16, device="cuda"))
     assert b.grad.dtype == bias and (b.grad == 33).all()
+
+
+@pytest.mark.parametrize("shape,N", [((3, 0), 40), ((2, 5, 0), 40), ((0, 256), 40), ((2, 0, 256), 40), ((0, 0), 40), ((7, 256), 0),
+                                     ((256,), 40), ((0,), 40)])
+def test_layers_of_no_size(shape, N):
+    """No tokens, no inputs, no outputs: bias or nothing forward, zeros or nothing backward."""
+    K = shape[-1]
+    _, W, W_scale, weight, bias = layer(1, K, N)
+    x = torch.ones(shape, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    y = gct.fp8_linear(x, W, W_scale, weight, bias)
+    assert y.shape == (*shape[:-1], N)
+    if K == 0:
+        assert torch.equal(y, bias.expand(y.shape))
+    y.backward(torch.ones_like(y))
+    assert x.grad.shape == x.shape and weight.grad.shape == weight.shape and bias.grad.shape == bias.shape
+    tokens = y.numel() // N if N else 7
+    assert (bias.grad == tokens).all()
+    if N == 0:
+        assert (x.grad == 0).all()
+    if tokens == 0:
+        assert (weight.grad == 0).all()
