@@ -140,6 +140,8 @@ def _product(name: str, fn, args, out, config, ws, index: int, stream):
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _product(name, fn, args, out, config, ws, index, stream)
+    if ws is not None and ws.buf.get_device() != index:
+        raise ValueError(f"the workspace is on {ws.buf.device}, not cuda:{index}")
     cfg, st = _cfgp(config), _stream(stream, index)
     rc = _native.IRIS_ENOWS if ws is None else fn(args, cfg, ws.ptr, ws.nbytes, st)
     if rc == _native.IRIS_ENOWS:

@@ -239,3 +239,16 @@ def test_errors_of_a_graph_captured_before_the_workspace_grew_are_found():
     graph.replay()
     assert gct.query_status(ws)[0] == gct._native.IRIS_ETIMEOUT
     done(ws)
+
+
+def test_a_workspace_elsewhere_is_refused():
+    """Before anything is launched: the device would write to the host's address."""
+    args, out = mm_ints(30, 256, 64, False, seed=66), torch.full((30, 64), 7.0, device="cuda")
+    ws = gct.Workspace(1 << 20, "cpu")
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        gct.matmul_fp8(*args, out, workspace=ws)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        gct.weight_grad_fp8(*wg_ints(30, 30, 64, "bf16"), out, workspace=ws)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        gct.fp8_linear(*layer(30, 256, 64), workspace=ws)
+    assert (out == 7).all() and not ws.buf.any()
