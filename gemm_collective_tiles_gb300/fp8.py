@@ -52,7 +52,7 @@ def _refuse(name: str, t, shape, dtypes, dims: int, index: int) -> None:
 def _mat(name: str, t: torch.Tensor, shape, dtypes, index: int):
     """(data, row stride, column stride) of a 2-D tensor of this shape and one
     of these types on CUDA device `index` (-1: on any)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2 and (shape is None or t.shape == shape)
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and (t.dim() == 2 if shape is None else t.shape == shape)
             and (t.get_device() == index if index >= 0 else t.is_cuda)):
         _refuse(name, t, shape, dtypes, 2, index)
     r, c = t.stride()
@@ -140,10 +140,13 @@ def _product(name: str, fn, args, out, config, ws, index: int, stream):
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _product(name, fn, args, out, config, ws, index, stream)
-    if ws is not None and ws.buf.get_device() != index:
-        raise ValueError(f"the workspace is on {ws.buf.device}, not cuda:{index}")
     cfg, st = _cfgp(config), _stream(stream, index)
-    rc = _native.IRIS_ENOWS if ws is None else fn(args, cfg, ws.ptr, ws.nbytes, st)
+    if ws is None:
+        rc = _native.IRIS_ENOWS
+    elif ws.buf.get_device() == index:
+        rc = fn(args, cfg, ws.buf.data_ptr(), ws.nbytes, st)
+    else:
+        raise ValueError(f"the workspace is on {ws.buf.device}, not cuda:{index}")
     if rc == _native.IRIS_ENOWS:
         from . import _on, _ws
         need, size = ctypes.c_size_t(0), "iris_b200_" + name + "_workspace_size"
