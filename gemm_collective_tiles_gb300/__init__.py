@@ -21,6 +21,7 @@ Block-scaled 8-bit floats (``fp8.py``), on plain device tensors:
 * ``matmul_fp8``       out = (A * scales) @ (B * scales) + bias
 * ``weight_grad_fp8``  out = (X * scales)^T @ dY from an 8-bit checkpoint of X
 * ``fp8_linear``       the three as one differentiable linear layer
+* ``fp8_workspace``    the workspace of a stream's layers that are given none
 
 The W ranks live in W regions of one device allocation (``SymmetricHeap``);
 a ``HeapTensor`` names the same byte offset in every region.

@@ -55,7 +55,7 @@ DeviceInfo g_dev[64];
 // Every kernel here may start while the one before it in the stream still runs
 // (it waits for that one's end before it touches memory), which hides its launch
 // and set-up behind its forerunner's last CTAs: one token's quantisation 1.5 ->
-// 1.1 us, 333 x 1000 x 1111 9.9 -> 9.2, 8192^3 388 -> 380.
+// 1.3 us, 333 x 1000 x 1111 9.9 -> 9.2, 8192^3 388 -> 380.
 cudaLaunchConfig_t launch_config(unsigned grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                                  cudaLaunchAttribute (&attr)[2]) {
     cudaLaunchConfig_t lc;

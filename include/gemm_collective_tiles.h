@@ -542,7 +542,8 @@ IRIS_API int iris_b200_matmul_fp8(const iris_b200_matmul_fp8_args* args, const i
  *   dY           M x N, f16 or bf16.
  *   out          f16, bf16 or f32.
  * X's values enter the product in dY's type: exact for power-of-two scales,
- * rounded once to 16 bits otherwise.  Sums are fp32.  f16: where a run of 512
+ * rounded once to 16 bits otherwise.  Sums are fp32.  A code times its scale
+ * has to be a finite fp32 number.  f16: where a run of 512
  * tokens (counted from the start of a CTA's part of the contraction) has a
  * scale whose codes may pass 65504, or only scales whose finest code step is
  * below 2^-24, the run's values are held times a power of two that takes its
