@@ -985,7 +985,8 @@ __device__ void run_factors(const GemmParams& p, const Ctl& ctl, Smem<KIND_WG, C
             const int e = max(static_cast<int>(bits >> 23), 1) - 127 + ((bits & 0x7FFFFFu) && bits >> 23 ? 1 : 0);
             int f = 0;
             if (bits != 0u && (m * fmax >= 65520.f || e < bottom)) f = max(-126, min(126, e - top));
-            if (!wait_bar(ctl, sm.fac_empty + 8 * fac.slot, fac.phase ^ 1, WAIT_FACTOR_EMPTY)) return;
+            // all lanes leave or none: the reduction above is the whole warp's
+            if (!__all_sync(0xFFFFFFFFu, wait_bar(ctl, sm.fac_empty + 8 * fac.slot, fac.phase ^ 1, WAIT_FACTOR_EMPTY))) return;
             if (lane == 0) {
                 sm.factors[fac.slot] = make_float2(__int_as_float((127 - f) << 23), __int_as_float((127 + f) << 23));
                 bar_arrive(sm.fac_full + 8 * fac.slot);
