@@ -32,6 +32,7 @@ import contextlib
 import ctypes
 import dataclasses
 import math
+import threading
 from typing import Optional, Sequence
 
 import torch
@@ -183,6 +184,7 @@ class Workspace:
         self.nbytes = max(256, _round_up(int(nbytes), 256))
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
         self._outgrown = []
+        self._lock = threading.Lock()  # held while a product that may share it is enqueued
         if wait and self.buf.is_cuda:
             torch.cuda.current_stream(self.buf.device).synchronize()
 

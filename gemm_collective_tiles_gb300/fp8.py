@@ -135,6 +135,13 @@ def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
     _written((codes, scales))
 
 
+def _need(name: str, args, cfg) -> int:
+    """Bytes of workspace of a product."""
+    size, n = "iris_b200_" + name + "_workspace_size", ctypes.c_size_t(0)
+    _native.check(size, getattr(_native.load(), size)(args, cfg, ctypes.byref(n)))
+    return int(n.value)
+
+
 def _product(name: str, fn, args, out, config, ws, index: int, stream):
     """One product with the given workspace, grown where it is too small, or with a new one."""
     if index != torch._C._cuda_getDevice():
@@ -142,21 +149,18 @@ def _product(name: str, fn, args, out, config, ws, index: int, stream):
             return _product(name, fn, args, out, config, ws, index, stream)
     cfg, st = _cfgp(config), _stream(stream, index)
     if ws is None:
-        rc = _native.IRIS_ENOWS
-    elif ws.buf.get_device() == index:
-        rc = fn(args, cfg, ws.buf.data_ptr(), ws.nbytes, st)
-    else:
+        from . import _ws
+        ws = _ws(None, _need(name, args, cfg), torch.device("cuda", index), stream)
+    elif ws.buf.get_device() != index:
         raise ValueError(f"the workspace is on {ws.buf.device}, not cuda:{index}")
-    if rc == _native.IRIS_ENOWS:
-        from . import _on, _ws
-        need, size = ctypes.c_size_t(0), "iris_b200_" + name + "_workspace_size"
-        _native.check(size, getattr(_native.load(), size)(args, cfg, ctypes.byref(need)))
-        if ws is None:
-            ws = _ws(None, int(need.value), torch.device("cuda", index), stream)
-        else:
+    # a product may be several launches: those of two threads must not mix
+    with ws._lock:
+        rc = fn(args, cfg, ws.buf.data_ptr(), ws.nbytes, st)
+        if rc == _native.IRIS_ENOWS:
+            from . import _on
             with _on(stream, index):
-                ws._grow(int(need.value))
-        rc = fn(args, cfg, ws.ptr, ws.nbytes, st)
+                ws._grow(_need(name, args, cfg))
+            rc = fn(args, cfg, ws.buf.data_ptr(), ws.nbytes, st)
     if rc:
         _native.check("iris_b200_" + name, rc)
     _written((out,))

@@ -56,3 +56,40 @@ def test_a_backward_pass_that_starts_with_the_weight_gradient():
     y = gct.fp8_linear(x, W, W_scale, weight)
     in_a_new_thread(lambda: y.backward(torch.ones_like(y)))
     assert (weight.grad == 64).all()
+
+
+def test_threads_that_share_a_stream_and_its_workspace():
+    """Layers whose weights are copied into the workspace before each product
+    (rows of 255 bytes), from several threads on one stream, without one of their own."""
+    def layer(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        K, N = 256 + 128 * (seed % 3), 255
+        weight = torch.randn(K, N, generator=g, device="cuda").requires_grad_()
+        W, W_scale = torch.empty(K, N, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn), torch.empty(K // 128, 2, device="cuda")
+        gct.quantize_fp8(weight.detach(), W, W_scale, block="tiles")
+        x = torch.randn(64 + seed, K, generator=g, device="cuda").bfloat16().requires_grad_()
+        return x, W, W_scale, weight
+
+    def step(x, W, W_scale, weight):
+        y = gct.fp8_linear(x, W, W_scale, weight)
+        return (y, *torch.autograd.grad(y, (x, weight), torch.ones_like(y)))
+
+    layers = [layer(s) for s in range(6)]
+    wants = [step(*a) for a in layers]
+    wrong = []
+
+    def run(a, want):
+        try:
+            for _ in range(60):
+                if not all(torch.equal(p, q) for p, q in zip(step(*a), want)):
+                    wrong.append(a[0].shape)
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=p) for p in zip(layers, wants)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert gct.query_status(gct.fp8_workspace())[0] == 0
