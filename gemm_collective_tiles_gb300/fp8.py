@@ -33,7 +33,7 @@ def _blocks(n: int) -> int:
 
 
 def _refuse(name: str, t, shape, dtypes, dims: int, index: int) -> None:
-    """Say what is wrong with an argument that _mat or _vec did not take."""
+    """Say what is wrong with an argument that _lead, _mat or _vec did not take."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} is not a tensor")
     if t.dtype not in dtypes:
@@ -49,22 +49,36 @@ def _refuse(name: str, t, shape, dtypes, dims: int, index: int) -> None:
     raise ValueError(f"{name} is not contiguous")
 
 
-def _mat(name: str, t: torch.Tensor, shape, dtypes, index: int):
-    """(data, row stride, column stride) of a 2-D tensor of this shape and one
-    of these types on CUDA device `index` (-1: on any)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and (t.dim() == 2 if shape is None else t.shape == shape)
-            and (t.get_device() == index if index >= 0 else t.is_cuda)):
-        _refuse(name, t, shape, dtypes, 2, index)
+def _lead(name: str, t: torch.Tensor, dtypes):
+    """(data, row stride, column stride), rows, columns and CUDA device of a
+    call's first matrix, of one of these types."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2 and t.is_cuda):
+        _refuse(name, t, None, dtypes, 2, -1)
+    rows, cols = t.shape
     r, c = t.stride()
-    return t.data_ptr(), r, c
+    return (t.data_ptr(), r, c), rows, cols, t.get_device()
+
+
+def _mat(name: str, t: torch.Tensor, shape, dtypes, index: int):
+    """(data, row stride, column stride) of a matrix of this shape and one of
+    these types on CUDA device `index`."""
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.get_device() == index:
+            r, c = t.stride()
+            return t.data_ptr(), r, c
+    except AttributeError:
+        pass
+    _refuse(name, t, shape, dtypes, 2, index)
 
 
 def _vec(name: str, t: torch.Tensor, n: int, dtypes, index: int) -> int:
     """Address of a contiguous 1-D tensor of n elements."""
-    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 1 and t.shape[0] == n
-            and t.get_device() == index and (n <= 1 or t.stride(0) == 1)):
-        _refuse(name, t, (n,), dtypes, 1, index)
-    return t.data_ptr()
+    try:
+        if t.dtype in dtypes and t.shape == (n,) and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(name, t, (n,), dtypes, 1, index)
 
 
 # Tells autograd that tensors were written by address: a backward pass that kept
@@ -118,9 +132,7 @@ def quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
     block's other elements; zero blocks get the smallest scale."""
     if block not in _ROWS:
         raise ValueError(f"unknown block {block!r}")
-    mx = _mat("x", x, None, _DT, -1)
-    M, K = x.shape
-    index = x.get_device()
+    mx, M, K, index = _lead("x", x, _DT)
     mc = _mat("codes", codes, (M, K), _FP8, index)
     ms = _mat("scales", scales, (M if block == "rows" else _blocks(M), _blocks(K)), _F32, index)
     args = _native.pack_quantize_fp8(*mx, *mc, *ms, M, K, _DT[x.dtype], _FP8[codes.dtype], _ROWS[block], bool(pow2))
@@ -176,13 +188,12 @@ def matmul_fp8(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale:
     of a quantised matrix is ``codes.t(), scales.t()``.  bias (N,) and out
     (M, N) are f16, bf16 or f32.  The 128-deep blocks are summed in fp32 and
     rounded once.  Returns the workspace."""
-    ma = _mat("A", A, None, _FP8, -1)
-    M, K = A.shape
-    index = A.get_device()
-    mb = _mat("B", B, None, _FP8, index)
-    N = B.shape[1]
-    if B.shape[0] != K:
-        raise ValueError(f"A has {K} columns and B has {B.shape[0]} rows")
+    ma, M, K, index = _lead("A", A, _FP8)
+    mb, rows, N, b_index = _lead("B", B, _FP8)
+    if b_index != index:
+        _refuse("B", B, None, _FP8, 2, index)
+    if rows != K:
+        raise ValueError(f"A has {K} columns and B has {rows} rows")
     kb = _blocks(K)
     msa = _mat("A_scale", A_scale, (M, kb), _F32, index)
     msb = _mat("B_scale", B_scale, (kb, _blocks(N)), _F32, index)
@@ -206,13 +217,12 @@ def weight_grad_fp8(X: torch.Tensor, X_scale: torch.Tensor, dY: torch.Tensor, ou
     finest step are held times a power of two for each run of 512 tokens, and
     lose at most what lies under 2^-39 of the largest value that the run's
     scales allow.  Returns the workspace."""
-    mx = _mat("X", X, None, _FP8, -1)
-    M, K = X.shape
-    index = X.get_device()
-    md = _mat("dY", dY, None, _DT16, index)
-    if dY.shape[0] != M:
-        raise ValueError(f"X has {M} rows and dY has {dY.shape[0]}")
-    N = dY.shape[1]
+    mx, M, K, index = _lead("X", X, _FP8)
+    md, rows, N, dy_index = _lead("dY", dY, _DT16)
+    if dy_index != index:
+        _refuse("dY", dY, None, _DT16, 2, index)
+    if rows != M:
+        raise ValueError(f"X has {M} rows and dY has {rows}")
     ms = _mat("X_scale", X_scale, (M, _blocks(K)), _F32, index)
     mo = _mat("out", out, (K, N), _DT, index)
     args = _native.pack_weight_grad_fp8(*mx, *ms, *md, *mo, M, N, K, _FP8[X.dtype], _DT[dY.dtype], _DT[out.dtype], 0)
