@@ -27,6 +27,8 @@ IRIS_NOALLOC_SCRATCH_BYTES = 256 + 8 * IRIS_NOALLOC_MAX_FLAGS
 
 IRIS_F16, IRIS_BF16, IRIS_F32 = 0, 1, 2
 IRIS_E4M3, IRIS_E5M2 = 0, 1
+IRIS_ACT_NONE, IRIS_ACT_RELU, IRIS_ACT_GELU, IRIS_ACT_GELU_TANH, IRIS_ACT_SILU = range(5)
+IRIS_NORM_NONE, IRIS_NORM_RMS, IRIS_NORM_LAYER = range(3)
 IRIS_COLL_ALL_GATHER, IRIS_COLL_ALL_REDUCE, IRIS_COLL_REDUCE_SCATTER = 0, 1, 2
 IRIS_COLL_ALL_TO_ALL, IRIS_COLL_BROADCAST = 3, 4
 (IRIS_OP_ALL_GATHER_MATMUL, IRIS_OP_MATMUL_REDUCE_SCATTER, IRIS_OP_MATMUL_ALL_GATHER,
@@ -49,6 +51,14 @@ EXPORTS = (
     "iris_b200_matmul_fp8",
     "iris_b200_weight_grad_fp8_workspace_size",
     "iris_b200_weight_grad_fp8",
+    "iris_b200_matmul_act_workspace_size",
+    "iris_b200_matmul_act",
+    "iris_b200_act_grad_workspace_size",
+    "iris_b200_act_grad",
+    "iris_b200_dropout",
+    "iris_b200_norm_join",
+    "iris_b200_norm_join_grad_workspace_size",
+    "iris_b200_norm_join_grad",
     "iris_b200_query_status",
     "iris_b200_strerror",
     "iris_b200_num_sms",
@@ -102,6 +112,15 @@ pack_quantize_fp8 = struct.Struct("@11q4i").pack     # x, codes, scales; M, K; x
 pack_matmul_fp8 = struct.Struct("@19q4i").pack       # A, a_scales, B, b_scales, out; bias; M, N, K; 4 types
 pack_weight_grad_fp8 = struct.Struct("@15q4i").pack  # X, x_scales, dY, out; M, N, K; 3 types, 0
 
+# Those of the operators around linear layers; an absent matrix or vector is 0.
+pack_matmul_act = struct.Struct("@20qd4i").pack  # A, B, out, residual, z; bias, rng; M, N, K; p; 3 types, act
+pack_act_grad = struct.Struct("@13qd4i").pack    # dy, z, dz; dbias, rng; M, N; p; 3 types, act
+pack_dropout = struct.Struct("@12qd2i").pack     # x, residual, out; rng; M, N; p; type, 0
+# y, x, gate, h, n; 4 vectors; stats; M, D, gate rows; scale, eps; 7 types, post, pre, 0
+pack_norm_join = struct.Struct("@23q2d10i").pack
+# the forward call's; dh, dn, dy, dx, dgate; the gradients of the 4 vectors
+pack_norm_join_grad = struct.Struct("@23q2d10i19q").pack
+
 
 _lib = None
 
@@ -128,6 +147,14 @@ def _declare(lib):
         "iris_b200_matmul_fp8": (ci, [args, cfgp, vp, sz, vp]),
         "iris_b200_weight_grad_fp8_workspace_size": (ci, [args, cfgp, P(sz)]),
         "iris_b200_weight_grad_fp8": (ci, [args, cfgp, vp, sz, vp]),
+        "iris_b200_matmul_act_workspace_size": (ci, [args, cfgp, P(sz)]),
+        "iris_b200_matmul_act": (ci, [args, cfgp, vp, sz, vp]),
+        "iris_b200_act_grad_workspace_size": (ci, [args, cfgp, P(sz)]),
+        "iris_b200_act_grad": (ci, [args, cfgp, vp, sz, vp]),
+        "iris_b200_dropout": (ci, [args, vp]),
+        "iris_b200_norm_join": (ci, [args, vp]),
+        "iris_b200_norm_join_grad_workspace_size": (ci, [args, cfgp, P(sz)]),
+        "iris_b200_norm_join_grad": (ci, [args, cfgp, vp, sz, vp]),
         "iris_b200_query_status": (ci, [vp, vp, P(ci), P(ci), P(ci)]),
         "iris_b200_strerror": (ctypes.c_char_p, [ci]),
         "iris_b200_num_sms": (ci, [P(ci)]),

@@ -1,0 +1,406 @@
+"""The sides of a block's linear layers: a product with its epilogue, dropout,
+the norms around a block's end.
+
+As the library's other ops, ``matmul_act``, ``act_grad``, ``dropout_add``,
+``norm_join`` and ``norm_join_grad`` write into tensors that the caller owns,
+enqueue their kernels on one stream and return (those with a workspace: the
+workspace, to be passed to the next call on that stream; one that is passed and
+too small grows).  Tensors may have any non-negative strides; rows that start on
+16 bytes are read and written fastest.  ``linear_act``, ``dropout`` and
+``block_norm`` are the differentiable forms, which make their outputs; their
+products and sums use the stream's workspace (``fp8_workspace``) where they are
+given none.
+
+Dropout takes its random bits from ``rng``, an int64 tensor (seed, offset) on
+the device, and from an element's row and column (Philox4x32-10, 16 bits an
+element: p is rounded to a multiple of 2^-16).  The same rng gives the same mask
+in every op, forward and backward, so no mask is stored; a program adds 1 to the
+offset, or to the seed, for each layer and step, by a kernel where it replays a
+graph.
+"""
+from __future__ import annotations
+
+import math
+from typing import Optional
+
+import torch
+
+from . import _native
+from .fp8 import (_DT, _DT16, _lead, _layer_workspace, _mat, _product, _refuse, _stream, _vec, _written)
+
+_ACTS = {None: _native.IRIS_ACT_NONE, "relu": _native.IRIS_ACT_RELU, "gelu": _native.IRIS_ACT_GELU,
+         "gelu_tanh": _native.IRIS_ACT_GELU_TANH, "silu": _native.IRIS_ACT_SILU}
+_NORMS = {None: _native.IRIS_NORM_NONE, "rms": _native.IRIS_NORM_RMS, "layer": _native.IRIS_NORM_LAYER}
+_NO_MAT = (0, 0, 0)
+_I64 = (torch.int64,)
+
+
+def _choice(name: str, value, table):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown {name} {value!r}") from None
+
+
+def _rng(p: float, rng, index: int) -> int:
+    """Address of the random state that a dropout of p needs, or 0."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p is {p}, not between 0 and 1")
+    if rng is None:
+        if round(p * 65536) > 0:
+            raise ValueError("dropout needs rng, an int64 tensor (seed, offset)")
+        return 0
+    return _vec("rng", rng, 2, _I64, index)
+
+
+def _like(name: str, t, shape, dtype, index: int):
+    """An optional matrix of this shape and type."""
+    return _NO_MAT if t is None else _mat(name, t, shape, (dtype,), index)
+
+
+def _run(name: str, args, index: int, stream) -> None:
+    """A call without a workspace."""
+    fn, st = getattr(_native.load(), "iris_b200_" + name), _stream(stream, index)
+    if index == torch._C._cuda_getDevice():
+        rc = fn(args, st)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(args, st)
+    if rc:
+        _native.check("iris_b200_" + name, rc)
+
+
+def matmul_act(A: torch.Tensor, B: torch.Tensor, out: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               act: Optional[str] = None, residual: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+               p: float = 0.0, rng: Optional[torch.Tensor] = None, config=None, workspace=None, stream=None):
+    """z = A @ B + bias, out = residual + dropout(act(z)).
+
+    A (M, K) and B (K, N) f16 or bf16, either order of each (a transposed view
+    is read as it is); out (M, N) f16, bf16 or f32; bias (N,) any of the three;
+    act None, "relu", "gelu" (by the normal distribution), "gelu_tanh" or
+    "silu"; residual as out, out itself among them (which adds to out: a
+    gradient buffer); z as out, None: not wanted.  Everything after the product
+    is fp32, rounded once.  Returns the workspace."""
+    a = _choice("activation", act, _ACTS)
+    ma, M, K, index = _lead("A", A, _DT16)
+    mb, rows, N, b_index = _lead("B", B, (A.dtype,))
+    if b_index != index:
+        _refuse("B", B, None, (A.dtype,), 2, index)
+    if rows != K:
+        raise ValueError(f"A has {K} columns and B has {rows} rows")
+    mo = _mat("out", out, (M, N), _DT, index)
+    mr = _like("residual", residual, (M, N), out.dtype, index)
+    mz = _like("z", z, (M, N), out.dtype, index)
+    bias_ptr, bias_dt = 0, 0
+    if bias is not None:
+        bias_ptr, bias_dt = _vec("bias", bias, N, _DT, index), _DT[bias.dtype]
+    args = _native.pack_matmul_act(*ma, *mb, *mo, *mr, *mz, bias_ptr, _rng(p, rng, index), M, N, K, p, _DT[A.dtype],
+                                   _DT[out.dtype], bias_dt, a)
+    ws = _product("matmul_act", _native.load().iris_b200_matmul_act, args, out, config, workspace, index, stream)
+    if z is not None:
+        _written((z,))
+    return ws
+
+
+def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], dz: Optional[torch.Tensor], dbias: Optional[torch.Tensor] = None,
+             act: Optional[str] = None, p: float = 0.0, rng: Optional[torch.Tensor] = None, workspace=None, stream=None):
+    """dz = dropout(dy) act'(z), dbias = the column sums of dz.
+
+    dy (M, N) f16, bf16 or f32; z as dy (None without an activation); dz (M, N)
+    and dbias (N,) of any of the three types, either None.  dz may be dy or z.
+    Sums are fp32, of values before their rounding, in a fixed order.  Returns
+    the workspace."""
+    a = _choice("activation", act, _ACTS)
+    md, M, N, index = _lead("dy", dy, _DT)
+    if a and z is None:
+        raise ValueError("the gradient of an activation needs z")
+    mz = _like("z", z, (M, N), dy.dtype, index) if a else _NO_MAT
+    mo, dz_dt = _NO_MAT, 0
+    if dz is not None:
+        mo, dz_dt = _mat("dz", dz, (M, N), _DT, index), _DT[dz.dtype]
+    bias_ptr, bias_dt = 0, 0
+    if dbias is not None:
+        bias_ptr, bias_dt = _vec("dbias", dbias, N, _DT, index), _DT[dbias.dtype]
+    args = _native.pack_act_grad(*md, *mz, *mo, bias_ptr, _rng(p, rng, index), M, N, p, _DT[dy.dtype], dz_dt, bias_dt, a)
+    return _sums("act_grad", args, [t for t in (dz, dbias) if t is not None], workspace, index, stream)
+
+
+def _sums(name: str, args, outs, workspace, index: int, stream):
+    """A call whose workspace holds sums over rows."""
+    ws = _product(name, getattr(_native.load(), "iris_b200_" + name), args, outs[0], None, workspace, index, stream) \
+        if outs else workspace
+    if len(outs) > 1:
+        _written(tuple(outs[1:]))
+    return ws
+
+
+def dropout_add(x: torch.Tensor, out: torch.Tensor, p: float, rng: Optional[torch.Tensor],
+                residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out = residual + dropout(x), (M, N) of one type, f16, bf16 or f32; out may
+    be x or residual itself.  The gradient of x is the same call on out's."""
+    mx, M, N, index = _lead("x", x, _DT)
+    mo = _mat("out", out, (M, N), (x.dtype,), index)
+    mr = _like("residual", residual, (M, N), x.dtype, index)
+    _run("dropout", _native.pack_dropout(*mx, *mr, *mo, _rng(p, rng, index), M, N, p, _DT[x.dtype], 0), index, stream)
+    _written((out,))
+
+
+def _norm_args(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps, stats):
+    """The packed arguments of norm_join, as a tuple, and the device."""
+    kinds = _choice("norm", post, _NORMS), _choice("norm", pre, _NORMS)
+    my, M, D, index = _lead("y", y, _DT)
+    mx = mh = _NO_MAT
+    x_type = y.dtype
+    for name, t in (("x", x), ("h", h)):
+        if t is not None:
+            types = (y.dtype, torch.float32) if x is None or name == "x" else (x.dtype,)
+            m = _mat(name, t, (M, D), types, index)
+            x_type = t.dtype
+            mx, mh = (m, mh) if name == "x" else (mx, m)
+    mg, gate_rows, gate_dt = _NO_MAT, 0, 0
+    if gate is not None:
+        mg, gate_rows, cols, g_index = _lead("gate", gate, _DT)
+        if g_index != index or cols != D:
+            _refuse("gate", gate, (gate_rows, D), _DT, 2, index)
+        if gate_rows < 1 or M % gate_rows or gate_rows > max(M, 1):
+            raise ValueError(f"gate has {gate_rows} rows, which do not divide y's {M}")
+        gate_dt = _DT[gate.dtype]
+    mn = _like("n", n, (M, D), y.dtype, index)
+    vectors, types = [], []
+    for name, t, kind in (("post_weight", post_weight, kinds[0]), ("post_bias", post_bias, kinds[0]),
+                          ("weight", weight, kinds[1]), ("bias", bias, kinds[1])):
+        if t is not None and not kind:
+            raise ValueError(f"{name} without its norm")
+        vectors.append(0 if t is None else _vec(name, t, D, _DT, index))
+        types.append(0 if t is None else _DT[t.dtype])
+    st = 0
+    if stats is not None:
+        st = _mat("stats", stats, (M, 4), (torch.float32,), index)[0]
+        if not stats.is_contiguous():
+            raise ValueError("stats is not contiguous")
+    return (*my, *mx, *mg, *mh, *mn, *vectors, st, M, D, gate_rows, scale, eps, _DT[y.dtype], _DT[x_type], gate_dt, *types,
+            *kinds, 0), M, D, index, x_type
+
+
+def norm_join(y: torch.Tensor, h: Optional[torch.Tensor], n: Optional[torch.Tensor], x: Optional[torch.Tensor] = None,
+              gate: Optional[torch.Tensor] = None, scale: float = 1.0, post: Optional[str] = None,
+              post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None, pre: Optional[str] = None,
+              weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-6,
+              stats: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The end of a block and the start of the next: u = post-norm of y (or y),
+    h = x + scale * gate * u, n = pre-norm of h.
+
+    y (M, D) f16, bf16 or f32, n as y; x and h (M, D) of y's type or f32 (the
+    residual stream), x None: not added; gate (G, D), each row for M / G rows of y:
+    a learned scale (1, D), one per sequence, one per token (M, D); post, pre: None,
+    "rms" or "layer", with optional weights and biases (D,); any of the three types
+    for gate and vectors.  h None: not wanted; n None just where pre is.  stats
+    (M, 4) f32, where given, takes what ``norm_join_grad`` needs.  h may be x
+    itself, n may be y."""
+    if (pre is None) != (n is None):
+        raise ValueError("n is written by the pre-norm: both or neither")
+    args, _, _, index, _ = _norm_args(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps, stats)
+    _run("norm_join", _native.pack_norm_join(*args), index, stream)
+    _written(tuple(t for t in (h, n, stats) if t is not None))
+
+
+def norm_join_grad(y: torch.Tensor, stats: torch.Tensor, dh: Optional[torch.Tensor], dn: Optional[torch.Tensor],
+                   x: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                   post: Optional[str] = None, post_weight: Optional[torch.Tensor] = None,
+                   post_bias: Optional[torch.Tensor] = None, pre: Optional[str] = None, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, eps: float = 1e-6, dy: Optional[torch.Tensor] = None,
+                   dx: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                   dpost_weight: Optional[torch.Tensor] = None, dpost_bias: Optional[torch.Tensor] = None,
+                   dweight: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None, workspace=None, stream=None):
+    """The gradients of ``norm_join`` from those of h and n (either None): dy, dx,
+    dgate and those of the vectors, each None or as its tensor (dx without an x:
+    the gradient of h, which has h's type).  The other arguments are the forward
+    call's; h and n are not needed.  dx may be dh itself, dy may be dn.  Returns
+    the workspace."""
+    args, M, D, index, x_type = _norm_args(y, None, None, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps,
+                                           stats)
+    if stats is None:
+        raise ValueError("the gradient needs the forward call's stats")
+    if dh is None and dn is None:
+        raise ValueError("neither dh nor dn is given")
+    if dn is not None and pre is None:
+        raise ValueError("dn without a pre-norm")
+    if x is None and (dh is not None or dx is not None):
+        x_type = (dh if dh is not None else dx).dtype
+        if x_type not in (y.dtype, torch.float32):
+            raise TypeError(f"dh has type {x_type}")
+        args = (*args[:26], _DT[x_type], *args[27:])
+    grads = [_like("dh", dh, (M, D), x_type, index), _like("dn", dn, (M, D), y.dtype, index),
+             _like("dy", dy, (M, D), y.dtype, index), _like("dx", dx, (M, D), x_type, index)]
+    if dgate is not None and gate is None:
+        raise ValueError("dgate without a gate")
+    grads.append(_NO_MAT if dgate is None else _like("dgate", dgate, tuple(gate.shape), gate.dtype, index))
+    vectors = []
+    for name, t, of in (("dpost_weight", dpost_weight, post_weight), ("dpost_bias", dpost_bias, post_bias),
+                        ("dweight", dweight, weight), ("dbias", dbias, bias)):
+        if t is not None and of is None:
+            raise ValueError(f"{name} without its vector")
+        vectors.append(0 if t is None else _vec(name, t, D, (of.dtype,), index))
+    packed = _native.pack_norm_join_grad(*args, *(v for m in grads for v in m), *vectors)
+    outs = [t for t in (dy, dx, dgate, dpost_weight, dpost_bias, dweight, dbias) if t is not None]
+    return _sums("norm_join_grad", packed, outs, workspace, index, stream)
+
+
+# ------------------------------------------------------------------ differentiable forms
+
+def _rows(t: Optional[torch.Tensor], cols: int):
+    """(..., cols) as a matrix; sizes of zero among them."""
+    return None if t is None else t.reshape(math.prod(t.shape[:-1]), cols)
+
+
+class _LinearAct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, act, residual, p, rng, workspace):
+        K, N = weight.shape
+        x2 = _rows(x, K)
+        M = x2.shape[0]
+        y = torch.empty(M, N, dtype=x.dtype, device=x.device)
+        z = None
+        if act is not None and any(ctx.needs_input_grad[:3]):
+            z = torch.empty(M, N, dtype=x.dtype, device=x.device)
+        matmul_act(x2, weight, y, bias=bias, act=act, residual=_rows(residual, N), z=z, p=p, rng=rng,
+                   workspace=_layer_workspace(workspace, x.device))
+        ctx.save_for_backward(x, weight, z, rng)
+        ctx.act, ctx.p, ctx.workspace = act, p, workspace
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y.reshape(*x.shape[:-1], N)
+
+    # the kernels' gradients have no derivatives of their own: asking for second
+    # ones is an error, not a sum without some of its terms
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, weight, z, rng = ctx.saved_tensors
+        K, N = weight.shape
+        x2, dy2 = _rows(x, K), _rows(dy, N)
+        ws = _layer_workspace(ctx.workspace, dy.device)
+        dx = dw = db = None
+        want_db = ctx.bias_dtype is not None and ctx.needs_input_grad[2]
+        if ctx.needs_input_grad[0] or ctx.needs_input_grad[1] or want_db:
+            dz = dy2
+            # z of a layer without an activation is not kept: its derivative is 1
+            if z is not None or ctx.p > 0:
+                dz = torch.empty_like(dy2, memory_format=torch.contiguous_format)
+            if want_db:
+                db = torch.empty(N, dtype=ctx.bias_dtype, device=dy.device)
+            if want_db or dz is not dy2:
+                act_grad(dy2, z, None if dz is dy2 else dz, db, act=ctx.act, p=ctx.p, rng=rng, workspace=ws)
+        if ctx.needs_input_grad[0]:
+            dx = torch.empty(x2.shape, dtype=x.dtype, device=dy.device)
+            matmul_act(dz, weight.t(), dx, workspace=ws)
+            dx = dx.reshape(x.shape)
+        if ctx.needs_input_grad[1]:
+            dw = torch.empty(K, N, dtype=weight.dtype, device=dy.device)
+            matmul_act(x2.t(), dz, dw, workspace=ws)
+        return dx, dw, db, None, dy if ctx.needs_input_grad[4] else None, None, None, None
+
+
+def linear_act(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, act: Optional[str] = None,
+               residual: Optional[torch.Tensor] = None, p: float = 0.0, rng: Optional[torch.Tensor] = None, workspace=None):
+    """Differentiable y = residual + dropout(act(x @ weight + bias)), x (..., K) and
+    weight (K, N) f16 or bf16, residual (..., N) and y of the same type.
+
+    Kept for the backward pass: x, weight, and with an activation its argument in
+    16 bits; the gradient between the products is rounded to 16 bits, their
+    operands' type.  A workspace that is given serves forward and backward."""
+    if x.dim() < 1 or x.dtype not in _DT16:
+        raise TypeError("x is a f16 or bf16 tensor (..., K)")
+    if weight.dim() != 2 or weight.dtype != x.dtype or weight.shape[0] != x.shape[-1]:
+        raise ValueError(f"weight is a {x.dtype} matrix of {x.shape[-1]} rows")
+    if residual is not None and (residual.dtype != x.dtype or residual.shape != (*x.shape[:-1], weight.shape[1])):
+        raise ValueError(f"residual is a {x.dtype} tensor of shape {(*x.shape[:-1], weight.shape[1])}")
+    return _LinearAct.apply(x, weight, bias, act, residual, p, rng, workspace)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, rng, residual):
+        N = x.shape[-1]
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dropout_add(_rows(x, N), _rows(out, N), p, rng, residual=_rows(residual, N))
+        ctx.save_for_backward(rng)
+        ctx.p = p
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        rng, = ctx.saved_tensors
+        dx = None
+        if ctx.needs_input_grad[0]:
+            N = dy.shape[-1]
+            dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+            dropout_add(_rows(dy, N), _rows(dx, N), ctx.p, rng)
+        return dx, None, None, dy if ctx.needs_input_grad[3] else None
+
+
+def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Optional[torch.Tensor] = None):
+    """Differentiable residual + dropout(x) of tensors (..., N).  Nothing is kept
+    but rng, which must not change before the backward pass (autograd tells)."""
+    if x.dim() < 1 or x.dtype not in _DT:
+        raise TypeError("x is a f16, bf16 or f32 tensor (..., N)")
+    if residual is not None and (residual.dtype != x.dtype or residual.shape != x.shape):
+        raise ValueError(f"residual is a {x.dtype} tensor of shape {tuple(x.shape)}")
+    return _Dropout.apply(x, p, rng, residual)
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, workspace):
+        D = y.shape[-1]
+        y2, x2, joins = _rows(y, D), _rows(x, D), x is not None or gate is not None or post is not None or scale != 1.0
+        h = torch.empty(y.shape, dtype=(y if x is None else x).dtype, device=y.device) if joins else None
+        n = torch.empty(y.shape, dtype=y.dtype, device=y.device) if pre is not None else None
+        stats = torch.empty(y2.shape[0], 4, dtype=torch.float32, device=y.device) if any(ctx.needs_input_grad) else None
+        norm_join(y2, _rows(h, D), _rows(n, D), x=x2, gate=gate, scale=scale, post=post, post_weight=post_weight,
+                  post_bias=post_bias, pre=pre, weight=weight, bias=bias, eps=eps, stats=stats)
+        ctx.save_for_backward(y, x, gate, post_weight, post_bias, weight, bias, stats)
+        ctx.args = scale, post, pre, eps, workspace
+        ctx.set_materialize_grads(False)
+        return h, n
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh, dn):
+        y, x, gate, post_weight, post_bias, weight, bias, stats = ctx.saved_tensors
+        scale, post, pre, eps, workspace = ctx.args
+        if dh is None and dn is None:
+            return (None,) * 12
+        D, wants = y.shape[-1], ctx.needs_input_grad
+        inputs = (y, x, gate, post_weight, post_bias, weight, bias)
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=y.device) if t is not None and w else None
+                 for t, w in zip(inputs, wants)]
+        # n has had no part in the loss: its norm's vectors get no gradient
+        idle = dn is None
+        dpost_weight, dpost_bias, dweight, dbias = grads[3:]
+        norm_join_grad(_rows(y, D), stats, _rows(dh, D), _rows(dn, D), x=_rows(x, D), gate=gate, scale=scale, post=post,
+                       post_weight=post_weight, post_bias=post_bias, pre=None if idle else pre, weight=None if idle else weight,
+                       bias=None if idle else bias, eps=eps, dy=_rows(grads[0], D), dx=_rows(grads[1], D), dgate=grads[2],
+                       dpost_weight=dpost_weight, dpost_bias=dpost_bias, dweight=None if idle else dweight,
+                       dbias=None if idle else dbias, workspace=_layer_workspace(workspace, y.device))
+        if idle:
+            grads[5] = grads[6] = None
+        return (*grads, None, None, None, None, None)
+
+
+def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+               post: Optional[str] = None, post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None,
+               pre: Optional[str] = None, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-6, workspace=None):
+    """Differentiable ``norm_join`` of tensors (..., D): returns (h, n), n None
+    without a pre-norm, h y itself where nothing joins it.  gate (G, D) counts y's
+    rows with the leading dimensions flattened.  Kept for the backward pass: the
+    inputs and 4 numbers a row."""
+    if y.dim() < 1 or y.dtype not in _DT:
+        raise TypeError("y is a f16, bf16 or f32 tensor (..., D)")
+    if x is not None and (x.dtype not in (y.dtype, torch.float32) or x.shape != y.shape):
+        raise ValueError(f"x is a {y.dtype} or float32 tensor of shape {tuple(y.shape)}")
+    if post is None and pre is None and x is None and gate is None and scale == 1.0:
+        raise ValueError("nothing to do: no norm, residual, gate or scale")
+    h, n = _BlockNorm.apply(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, workspace)
+    return (y if h is None else h), n

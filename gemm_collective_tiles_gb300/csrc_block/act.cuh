@@ -1,0 +1,165 @@
+// Activations, their derivatives, and dropout's random numbers.
+#pragma once
+#include "../csrc_fp8/fp8_elem.cuh"
+
+namespace gct {
+namespace block {
+
+enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float LOG2E = 1.44269504088896f;
+constexpr float GELU_ROOT = 1.59576912160573f;  // 2 sqrt(2 / pi)
+constexpr float GELU_CUBE = 0.044715f;
+
+__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + exp2_approx(-LOG2E * x)); }
+
+// The upper tail of the normal distribution at |z|: half of erfc(x), x = |z| /
+// sqrt(2), as exp(-x^2) times a polynomial in t = 1 / (1 + 0.37 x) (the form of
+// Hastings' approximations; these coefficients are a least-maximum fit to
+// exp(x^2) erfc(x), relative error 7e-7).  `e` is exp(-z^2 / 2).  Small tails keep
+// their relative precision, which 1 + erf(x) of a negative x loses.
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+    const float t = rcp_approx(fmaf(0.37f * 0.70710678118655f, fabsf(z), 1.f));
+    e = exp2_approx(-0.5f * LOG2E * z * z);
+    float g = -0.14294943f;
+    g = fmaf(g, t, 0.43710686f);
+    g = fmaf(g, t, -0.18854363f);
+    g = fmaf(g, t, 0.31898374f);
+    g = fmaf(g, t, 0.15202124f);
+    g = fmaf(g, t, 0.21501255f);
+    g = fmaf(g, t, 0.20836934f);
+    return 0.5f * t * g * e;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+    if (ACT == ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
+    if (ACT == ACT_GELU) {
+        float e;
+        const float tail = normal_tail(z, e);
+        return z * (z < 0.f ? tail : 1.f - tail);
+    }
+    if (ACT == ACT_GELU_TANH) return z * sigmoid(GELU_ROOT * fmaf(GELU_CUBE * z * z, z, z));  // 0.5 (1 + tanh(u)) = sigmoid(2 u)
+    if (ACT == ACT_SILU) return z * sigmoid(z);
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ float act_grad_of(float z) {
+    if (ACT == ACT_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
+    if (ACT == ACT_GELU) {
+        float e;
+        const float tail = normal_tail(z, e);
+        return fmaf(0.398942280401433f * z, e, z < 0.f ? tail : 1.f - tail);
+    }
+    if (ACT == ACT_GELU_TANH) {
+        const float s = sigmoid(GELU_ROOT * fmaf(GELU_CUBE * z * z, z, z));
+        // past 16 the second term is 0; its factor must not overflow there
+        const float q = fminf(z * z, 256.f);
+        return fmaf(z * s * (1.f - s), GELU_ROOT * fmaf(3.f * GELU_CUBE, q, 1.f), s);
+    }
+    if (ACT == ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    return 1.f;
+}
+// one of them for N values, chosen once
+template <int N>
+__device__ __forceinline__ void apply_act(float (&v)[N], int act) {
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = f(v[i]);
+    };
+    switch (act) {
+        case ACT_RELU: all([](float z) { return act_of<ACT_RELU>(z); }); break;
+        case ACT_GELU: all([](float z) { return act_of<ACT_GELU>(z); }); break;
+        case ACT_GELU_TANH: all([](float z) { return act_of<ACT_GELU_TANH>(z); }); break;
+        case ACT_SILU: all([](float z) { return act_of<ACT_SILU>(z); }); break;
+        default: break;
+    }
+}
+
+// Dropout.  Element (i, j) has 16 random bits: lane j % 8 of Philox4x32-10
+// (Salmon, Moraes, Dror and Shaw, 2011) under the seed as key, with counter
+// (j / 8, i, offset).  It is kept where they are at least `least` =
+// rint(65536 p), so the mask is a function of the element's place and never
+// stored.  16 bits an element halve the rounds that 32 would need: ten rounds
+// are 20 wide multiplications for 8 elements.
+struct Drop {
+    const long long* rng;  // seed, offset
+    uint32_t least;        // 0: nothing is dropped
+    float scale;           // 1 / (1 - least / 65536), or 0
+};
+struct DropKey {
+    uint32_t k0, k1, o0, o1;
+};
+__device__ __forceinline__ DropKey drop_key(const Drop& d) {
+    DropKey k{0u, 0u, 0u, 0u};
+    if (d.least) {
+        const unsigned long long s = static_cast<unsigned long long>(d.rng[0]), o = static_cast<unsigned long long>(d.rng[1]);
+        k = DropKey{static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32), static_cast<uint32_t>(o), static_cast<uint32_t>(o >> 32)};
+    }
+    return k;
+}
+// the random bits of elements (row, 8 group .. 8 group + 7), two to a word
+__device__ __forceinline__ void philox8(const DropKey& key, uint32_t group, uint32_t row, uint32_t (&w)[4]) {
+    uint32_t c0 = group, c1 = row, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const unsigned long long a = static_cast<unsigned long long>(c0) * 0xD2511F53u;
+        const unsigned long long b = static_cast<unsigned long long>(c2) * 0xCD9E8D57u;
+        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+        c1 = static_cast<uint32_t>(b);
+        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+        c3 = static_cast<uint32_t>(a);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    w[0] = c0;
+    w[1] = c1;
+    w[2] = c2;
+    w[3] = c3;
+}
+__device__ __forceinline__ bool kept(const uint32_t (&w)[4], int lane, uint32_t least) {
+    return ((lane & 1) ? w[lane >> 1] >> 16 : w[lane >> 1] & 0xFFFFu) >= least;
+}
+// v[0..7] are the elements of one group; dropped ones become 0 whatever they were
+__device__ __forceinline__ void drop8(float* v, const Drop& d, const DropKey& key, uint32_t group, uint32_t row) {
+    uint32_t w[4];
+    philox8(key, group, row, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = kept(w, e, d.least) ? v[e] * d.scale : 0.f;
+}
+__device__ __forceinline__ float drop1(float v, const Drop& d, const DropKey& key, long long row, long long col) {
+    uint32_t w[4];
+    philox8(key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row), w);
+    const int lane = static_cast<int>(col & 7);
+    const uint32_t pair = lane < 4 ? (lane < 2 ? w[0] : w[1]) : (lane < 6 ? w[2] : w[3]);
+    return ((lane & 1) ? pair >> 16 : pair & 0xFFFFu) >= d.least ? v * d.scale : 0.f;
+}
+
+__device__ __forceinline__ float load_any(const void* p, int type, long long i) {
+    if (type == fp8::T_F32) return fp8::load_elem<fp8::T_F32>(p, i);
+    return type == fp8::T_F16 ? fp8::load_elem<fp8::T_F16>(p, i) : fp8::load_elem<fp8::T_BF16>(p, i);
+}
+__device__ __forceinline__ void store_any(void* p, int type, long long i, float v) {
+    if (type == fp8::T_F32)
+        static_cast<float*>(p)[i] = v;
+    else if (type == fp8::T_F16)
+        static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+}  // namespace block
+}  // namespace gct

@@ -1,0 +1,611 @@
+// Host side of matmul_act, act_grad, dropout, norm_join and norm_join_grad, as
+// declared in include/gemm_collective_tiles.h: argument checks, the choice of
+// kernels, tensor maps and launches.
+#include <cmath>
+
+#include "../csrc_fp8/fp8_host.cuh"
+#include "block_few.cuh"
+#include "block_norm.cuh"
+
+using namespace gct::block;
+
+namespace {
+
+// The kernels: a pair's 256 x 256 or 256 x 128 tile, a CTA's 128 x 128, and the
+// ones for at most 16, 32 or 64 rows.
+enum Variant { PAIR = 0, HALF = 1, CTA = 2, FEW16 = 3, FEW32 = 4, FEW64 = 5, VARIANTS = 6 };
+bool is_pair(int v) { return v <= HALF; }
+int few_rows(int v) { return v == FEW16 ? 16 : v == FEW32 ? 32 : 64; }
+
+struct DeviceInfo {
+    int sms;
+    int clusters[VARIANTS][4];  // that run at once, by log2 of the cluster's CTAs
+    bool done;
+};
+DeviceInfo g_dev[64];
+
+template <int CG, int BN>
+int setup_tiles(DeviceInfo& d, int v) {
+    using G = Geo<CG, BN>;
+    return setup_kernel(act_gemm_kernel<CG, BN>, d.clusters[v], CG == 2, CG == 2 ? 1 : 3, G::THREADS, G::BYTES, G::REGS_TOTAL, d.sms);
+}
+template <int NT>
+int setup_few(DeviceInfo& d, int v) {
+    return setup_kernel(act_few_kernel<NT>, d.clusters[v], 0, 3, FewGeo<NT>::THREADS, FewGeo<NT>::BYTES, 0, d.sms);
+}
+int device_info(DeviceInfo* out) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IRIS_ECUDA;
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceInfo& d = g_dev[dev];
+    if (!d.done) {
+        if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return IRIS_ECUDA;
+        int rc;
+        if ((rc = setup_tiles<2, 256>(d, PAIR)) || (rc = setup_tiles<2, 128>(d, HALF)) || (rc = setup_tiles<1, 128>(d, CTA)) ||
+            (rc = setup_few<16>(d, FEW16)) || (rc = setup_few<32>(d, FEW32)) || (rc = setup_few<64>(d, FEW64)) ||
+            (rc = find_encode()))
+            return rc;
+        d.done = true;
+    }
+    *out = d;
+    return IRIS_OK;
+}
+
+bool act_ok(int a) { return a >= IRIS_ACT_NONE && a <= IRIS_ACT_SILU; }
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int set_drop(Drop& d, double p, const int64_t* rng) {
+    if (!(p >= 0.0 && p <= 1.0)) return IRIS_EINVAL;
+    d.least = static_cast<uint32_t>(std::nearbyint(p * 65536.0));
+    d.scale = d.least == 65536u ? 0.f : static_cast<float>(65536.0 / (65536.0 - d.least));
+    d.rng = reinterpret_cast<const long long*>(rng);
+    if (d.least && !rng) return IRIS_EINVAL;
+    return d.least && !aligned(rng, 8) ? IRIS_EALIGN : IRIS_OK;
+}
+// an optional vector
+int check_vec(const void* data, int type) {
+    if (!data) return IRIS_OK;
+    if (!dtype_ok(type)) return IRIS_EINVAL;
+    return aligned(data, dtype_size(type)) ? IRIS_OK : IRIS_EALIGN;
+}
+Mat mat_of(const iris_b200_mat& m) { return Mat{m.data, m.row_stride, m.col_stride}; }
+// rows of unit stride on 16 bytes
+bool rows16(const iris_b200_mat& m, int64_t rows, int64_t cols, int elem) {
+    return !m.data || (aligned16(m.data) && (m.col_stride == 1 || cols == 1) && (rows <= 1 || m.row_stride * elem % 16 == 0));
+}
+
+// ---------------------------------------------------------------- matmul_act
+struct Plan {
+    int variant, split, stages, m_blocks, n_blocks, group_m, grid;
+};
+
+// Estimated time in us of a variant: `slots` clusters run at once and take the
+// tiles in turn; a tile costs its stages, and what it adds at its end.
+double estimate(int v, int slots, int64_t tiles, int64_t part, int split) {
+    const double stage = v == PAIR ? 0.30 : v == HALF ? 0.20 : v == CTA ? 0.18 : v == FEW16 ? 0.20 : v == FEW32 ? 0.21 : 0.24;
+    double tile = part * stage + (is_pair(v) ? 0.6 : v == CTA ? 1.0 : 0.5);
+    if (split > 1) tile += v >= FEW16 ? 1.5 : 2.5;
+    const double rounds = static_cast<double>(cdiv(tiles, slots));
+    return 4.5 + rounds * tile + (v == PAIR ? 3.0 : v == HALF ? 1.8 : 0.0);
+}
+
+int make_plan(Plan& pl, const iris_b200_config* cfg, const DeviceInfo& d, int64_t rows, int64_t cols, int64_t depth) {
+    iris_b200_config z;
+    std::memset(&z, 0, sizeof(z));
+    if (!cfg) cfg = &z;
+    if (cfg->tile_m != 0 && cfg->tile_m != 128 && cfg->tile_m != 256) return IRIS_EINVAL;
+    if (cfg->tile_n != 0 && cfg->tile_n != 128 && cfg->tile_n != 256) return IRIS_EINVAL;
+    if (cfg->k_split != 0 && cfg->k_split != 1 && cfg->k_split != 2 && cfg->k_split != 4 && cfg->k_split != 8) return IRIS_EINVAL;
+    if (cfg->group_m < 0 || cfg->debug_skip_flag < 0 || cfg->grid < 0 || cfg->grid > d.sms) return IRIS_EINVAL;
+    const int64_t stages = cdiv(depth, DEPTH);
+    const int grid = cfg->grid ? cfg->grid : d.sms;
+    double best = 0;
+    pl.variant = -1;
+    for (int v = PAIR; v < VARIANTS; ++v) {
+        const int cg = is_pair(v) ? 2 : 1, bn = v == PAIR ? 256 : 128;
+        if (cfg->tile_m && cfg->tile_m != 128 * cg) continue;
+        if (cfg->tile_n && cfg->tile_n != bn) continue;
+        if (v >= FEW16 && rows > few_rows(v)) continue;
+        const int64_t mb = cdiv(rows, 128 * cg), nb = cdiv(cols, bn), tiles = mb * nb;
+        if (tiles > 0x7FFFFFFF) continue;
+        for (int lg = 0; lg < (cg == 2 ? 1 : 4); ++lg) {
+            const int split = 1 << lg;
+            const int64_t part = cdiv(stages, split);
+            const int slots = std::min(d.clusters[v][cg == 2 ? 1 : lg], grid / (cg * split));
+            // every part has stages, unless the config asks for it (an empty one adds zeros)
+            if (slots < 1 || (cfg->k_split ? split != cfg->k_split : split > stages)) continue;
+            const double t = estimate(v, slots, tiles, part, split);
+            if (pl.variant < 0 || t < best) {
+                best = t;
+                pl.variant = v;
+                pl.split = split;
+                pl.m_blocks = static_cast<int>(mb);
+                pl.n_blocks = static_cast<int>(nb);
+                pl.grid = static_cast<int>(std::min<int64_t>(tiles, slots)) * cg * split;
+                // one group holds all rows of tiles at most
+                pl.group_m = std::min(cfg->group_m ? std::max(1, cfg->group_m / cg) : 16 / cg, pl.m_blocks);
+            }
+        }
+    }
+    pl.stages = static_cast<int>(stages);
+    return pl.variant < 0 ? IRIS_EINVAL : IRIS_OK;
+}
+
+template <int CG, int BN>
+int launch_tiles(const ActParams& p, int grid, cudaStream_t stream) {
+    using G = Geo<CG, BN>;
+    cudaLaunchAttribute attr[2];
+    return launch("kernel launch (matmul_act)", act_gemm_kernel<CG, BN>,
+                  launch_config(grid, G::THREADS, G::BYTES, CG * p.split, stream, attr), p);
+}
+template <int NT>
+int launch_few(const ActParams& p, int grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    return launch("kernel launch (matmul_act)", act_few_kernel<NT>,
+                  launch_config(grid, FewGeo<NT>::THREADS, FewGeo<NT>::BYTES, p.split, stream, attr), p);
+}
+
+int check_matmul_act(const iris_b200_matmul_act_args* g, Drop& drop) {
+    int rc;
+    if (!g || !dims_ok(g->M, g->N, g->K) || !dtype16(g->ab_dtype) || !dtype_ok(g->out_dtype) || !act_ok(g->act)) return IRIS_EINVAL;
+    if ((rc = set_drop(drop, g->p, g->rng)) || (rc = check_vec(g->bias, g->bias_dtype))) return rc;
+    const int e = dtype_size(g->out_dtype);
+    if ((rc = check_in(&g->A, g->M, g->K, 2)) || (rc = check_in(&g->B, g->K, g->N, 2)) || (rc = check_out(&g->out, g->M, g->N, e)))
+        return rc;
+    if (g->residual.data && (rc = check_in(&g->residual, g->M, g->N, e))) return rc;
+    return g->z.data ? check_out(&g->z, g->M, g->N, e) : IRIS_OK;
+}
+
+int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, void* ws, size_t ws_bytes, cudaStream_t stream,
+               size_t* need) {
+    ActParams p;
+    std::memset(&p, 0, sizeof(p));
+    int rc = check_matmul_act(g, p.drop);
+    if (rc) return rc;
+    const int64_t M = g->M, N = g->N, K = g->K;
+    if (M == 0 || N == 0) {
+        if (need) *need = WS_HEADER;
+        return IRIS_OK;
+    }
+    DeviceInfo d;
+    if ((rc = device_info(&d))) return rc;
+    Plan pl;
+    if ((rc = make_plan(pl, cfg, d, M, N, std::max<int64_t>(K, 1)))) return rc;
+    const bool few = pl.variant >= FEW16;
+    const Operand none{nullptr, 0, 0, 0, false, false, 0};
+    // few rows: the tokens are read K-major, of which there is little to copy
+    Operand a = K == 0 ? none : resolve_operand(&g->A, M, K, 2, !few);
+    Operand b = K == 0 ? none : resolve_operand(&g->B, K, N, 2, true);
+    const size_t total = WS_HEADER + a.copy_bytes + b.copy_bytes;
+    if (need) {
+        *need = total;
+        return IRIS_OK;
+    }
+    if (!ws || ws_bytes < total) return IRIS_ENOWS;
+    if (!aligned16(ws)) return IRIS_EALIGN;
+
+    const int e = dtype_size(g->out_dtype);
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.D = static_cast<int>(K);
+    p.bias = g->bias;
+    p.bias_type = g->bias_dtype;
+    p.type = g->out_dtype;
+    p.act = g->act;
+    p.out = g->out.data;
+    p.out_rs = g->out.row_stride;
+    p.out_cs = g->out.col_stride;
+    p.residual = g->residual.data;
+    p.res_rs = g->residual.row_stride;
+    p.res_cs = g->residual.col_stride;
+    p.z = g->z.data;
+    p.z_rs = g->z.row_stride;
+    p.z_cs = g->z.col_stride;
+    auto by_tma = [&](const iris_b200_mat& m) { return m.data && tma_rows(m.data, m.row_stride, m.col_stride, M, N, e); };
+    p.out_tma = by_tma(g->out);
+    p.res_tma = by_tma(g->residual);
+    p.z_tma = by_tma(g->z);
+    if (K == 0) {
+        const int64_t n = cdiv(M * cdiv(N, 4), 256);
+        cudaLaunchAttribute attr[2];
+        return launch("fill launch", act_fill_kernel<0>,
+                      launch_config(static_cast<unsigned>(std::min<int64_t>(n, int64_t(d.sms) * 8)), 256, 0, 1, stream, attr), p);
+    }
+    char* w = static_cast<char*>(ws);
+    if (a.copy && (rc = launch_repack<uint16_t>(&g->A, a, w + WS_HEADER, d.sms, stream))) return rc;
+    if (b.copy && (rc = launch_repack<uint16_t>(&g->B, b, w + WS_HEADER + a.copy_bytes, d.sms, stream))) return rc;
+    const int t = g->ab_dtype == IRIS_BF16;
+    const CUtensorMapDataType t16 = t ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    p.a_mn = a.transposed;
+    p.b_mn = !b.transposed;
+    const int a_rows = few ? few_rows(pl.variant) : 128, b_rows = pl.variant == HALF ? 64 : 128;
+    if ((rc = make_map_2d(&p.tmA, t16, 2, a, 64, p.a_mn ? 64 : a_rows)) ||
+        (rc = make_map_2d(&p.tmB, t16, 2, b, 64, p.b_mn ? 64 : b_rows)))
+        return rc;
+    // few rows: the weights are the MMA's first operand
+    p.idesc = few ? idesc_of(t, t, p.b_mn, 0, 128, a_rows)
+                  : idesc_of(t, t, p.a_mn, p.b_mn, is_pair(pl.variant) ? 256 : 128, pl.variant == PAIR ? 256 : 128);
+    auto store_map = [&](CUtensorMap* m, const iris_b200_mat& x) {
+        return make_store_map(m, p.type, x.data, N, M, M == 1 ? packed_pitch(N, e) : x.row_stride);
+    };
+    if (!few && pl.split == 1 &&
+        ((p.out_tma && (rc = store_map(&p.tmC, g->out))) || (p.res_tma && (rc = store_map(&p.tmR, g->residual))) ||
+         (p.z_tma && (rc = store_map(&p.tmZ, g->z)))))
+        return rc;
+    p.stages_total = pl.stages;
+    p.split = pl.split;
+    p.m_blocks = pl.m_blocks;
+    p.n_blocks = pl.n_blocks;
+    p.group_m = pl.group_m;
+    p.n_units = pl.m_blocks * pl.n_blocks;
+    p.ws = reinterpret_cast<WsHeader*>(w);
+    p.wait_ns = cfg && cfg->wait_ns ? cfg->wait_ns : DEFAULT_WAIT_NS;
+    p.debug_skip = cfg ? static_cast<uint32_t>(cfg->debug_skip_flag) : 0u;
+    switch (pl.variant) {
+        case PAIR: return launch_tiles<2, 256>(p, pl.grid, stream);
+        case HALF: return launch_tiles<2, 128>(p, pl.grid, stream);
+        case CTA: return launch_tiles<1, 128>(p, pl.grid, stream);
+        case FEW16: return launch_few<16>(p, pl.grid, stream);
+        case FEW32: return launch_few<32>(p, pl.grid, stream);
+        default: return launch_few<64>(p, pl.grid, stream);
+    }
+}
+
+// ---------------------------------------------------------------- elements
+int sm_count(int* sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return IRIS_ECUDA;
+    return IRIS_OK;
+}
+
+template <int T>
+int launch_dropout(const DropParams& p, bool vec, unsigned grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    return launch("dropout launch", vec ? dropout_kernel<T, true> : dropout_kernel<T, false>,
+                  launch_config(grid, 256, 0, 1, stream, attr), p);
+}
+template <int T>
+int launch_act_grad(const ActGradParams& p, bool vec, unsigned grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    return launch("act_grad launch", vec ? act_grad_kernel<T, true> : act_grad_kernel<T, false>,
+                  launch_config(grid, 256, 0, 1, stream, attr), p);
+}
+
+int act_grad(const iris_b200_act_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
+    int rc;
+    ActGradParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!g || !dims_ok(g->M, g->N, 0) || !dtype_ok(g->dtype) || !act_ok(g->act)) return IRIS_EINVAL;
+    if ((rc = set_drop(p.drop, g->p, g->rng)) || (rc = check_vec(g->dbias, g->dbias_dtype))) return rc;
+    const int64_t M = g->M, N = g->N;
+    const int e = dtype_size(g->dtype);
+    if ((rc = check_in(&g->dy, M, N, e)) || (g->act != IRIS_ACT_NONE && (rc = check_in(&g->z, M, N, e)))) return rc;
+    if (g->dz.data && (!dtype_ok(g->dz_dtype) || (rc = check_out(&g->dz, M, N, dtype_size(g->dz_dtype))))) return rc ? rc : IRIS_EINVAL;
+    p.segs = static_cast<unsigned>(cdiv(N, SEG));
+    // Rows of a CTA: enough CTAs to fill the GPU several times, and few partial
+    // sums beside the tensors.
+    p.rows = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(16, round_up(cdiv(M * p.segs, 2048), 8))));
+    const int64_t blocks = cdiv(M, p.rows);
+    const size_t total = WS_HEADER + (g->dbias ? static_cast<size_t>(blocks) * N * 4 : 0);
+    if (need) {
+        *need = total;
+        return IRIS_OK;
+    }
+    if (N == 0 || (!g->dz.data && !g->dbias)) return IRIS_OK;
+    if (g->dbias) {
+        if (!ws || ws_bytes < total) return IRIS_ENOWS;
+        if (!aligned16(ws)) return IRIS_EALIGN;
+        p.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER);
+    }
+    if (M > 0) {
+        if (blocks * p.segs > 0x7FFFFFFF) return IRIS_EINVAL;
+        p.dy = mat_of(g->dy);
+        if (g->act != IRIS_ACT_NONE) p.z = mat_of(g->z);
+        p.dz = mat_of(g->dz);
+        p.M = M;
+        p.N = static_cast<int>(N);
+        p.type = g->dtype;
+        p.dz_type = g->dz_dtype;
+        p.act = g->act;
+        const bool vec = N % 8 == 0 && rows16(g->dy, M, N, e) && (g->act == IRIS_ACT_NONE || rows16(g->z, M, N, e)) &&
+                         (!g->dz.data || rows16(g->dz, M, N, dtype_size(g->dz_dtype)));
+        const unsigned grid = static_cast<unsigned>(blocks * p.segs);
+        rc = g->dtype == IRIS_F32   ? launch_act_grad<T_F32>(p, vec, grid, stream)
+             : g->dtype == IRIS_F16 ? launch_act_grad<T_F16>(p, vec, grid, stream)
+                                    : launch_act_grad<T_BF16>(p, vec, grid, stream);
+        if (rc) return rc;
+    }
+    if (!g->dbias) return IRIS_OK;
+    const ColumnSumParams c{p.sums, static_cast<int>(blocks), static_cast<int>(N), g->dbias, g->dbias_dtype};
+    cudaLaunchAttribute attr[2];
+    return launch("column sum launch", column_sum_kernel<0>,
+                  launch_config(static_cast<unsigned>(cdiv(N, 32)), 256, 0, 1, stream, attr), c);
+}
+
+// ---------------------------------------------------------------- norms
+bool norm_ok(int k) { return k >= IRIS_NORM_NONE && k <= IRIS_NORM_LAYER; }
+
+// checks and parameters of a forward call; `vec`: every tensor so far has rows on 16 bytes
+int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec) {
+    int rc;
+    std::memset(&p, 0, sizeof(p));
+    if (!dims_ok(g->M, 0, g->D) || !dtype_ok(g->y_dtype) || !dtype_ok(g->x_dtype) || !norm_ok(g->post) || !norm_ok(g->pre) ||
+        g->reserved || !(g->eps >= 0.0) || (g->x_dtype != g->y_dtype && g->x_dtype != IRIS_F32))
+        return IRIS_EINVAL;
+    const int64_t M = g->M, D = g->D;
+    const int ye = dtype_size(g->y_dtype), xe = dtype_size(g->x_dtype);
+    if ((rc = check_in(&g->y, M, D, ye)) || (g->x.data && (rc = check_in(&g->x, M, D, xe))) ||
+        (g->h.data && (rc = check_out(&g->h, M, D, xe))) || (g->n.data && (rc = check_out(&g->n, M, D, ye))))
+        return rc;
+    p.group_rows = M;
+    if (g->gate.data) {
+        if (g->gate_rows < 1 || g->gate_rows > std::max<int64_t>(M, 1) || M % g->gate_rows || !dtype_ok(g->gate_dtype)) return IRIS_EINVAL;
+        if ((rc = check_in(&g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)))) return rc;
+        p.group_rows = M / g->gate_rows;
+    }
+    if (!g->post && (g->post_weight || g->post_bias)) return IRIS_EINVAL;
+    if (!g->pre && (g->weight || g->bias)) return IRIS_EINVAL;
+    if ((rc = check_vec(g->post_weight, g->post_weight_dtype)) || (rc = check_vec(g->post_bias, g->post_bias_dtype)) ||
+        (rc = check_vec(g->weight, g->weight_dtype)) || (rc = check_vec(g->bias, g->bias_dtype)))
+        return rc;
+    if (!aligned(g->stats, 16)) return IRIS_EALIGN;
+    p.y = mat_of(g->y);
+    p.x = mat_of(g->x);
+    p.gate = mat_of(g->gate);
+    p.h = mat_of(g->h);
+    p.n = mat_of(g->n);
+    p.post_w = Vec{g->post_weight, g->post_weight_dtype};
+    p.post_b = Vec{g->post_bias, g->post_bias_dtype};
+    p.pre_w = Vec{g->weight, g->weight_dtype};
+    p.pre_b = Vec{g->bias, g->bias_dtype};
+    p.gate_type = g->gate_dtype;
+    p.M = M;
+    p.D = static_cast<int>(D);
+    p.post = g->post;
+    p.pre = g->pre;
+    p.scale = static_cast<float>(g->scale);
+    p.eps = static_cast<float>(g->eps);
+    p.stats = reinterpret_cast<float4*>(g->stats);
+    vec = D % 8 == 0 && rows16(g->y, M, D, ye) && rows16(g->x, M, D, xe) && rows16(g->h, M, D, xe) && rows16(g->n, M, D, ye) &&
+          rows16(g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)) && aligned16(g->post_weight) && aligned16(g->post_bias) &&
+          aligned16(g->weight) && aligned16(g->bias);
+    return IRIS_OK;
+}
+
+// dynamic shared memory of a kernel is allowed once per device
+int allow_smem(const void* kernel, size_t bytes) {
+    struct Entry {
+        const void* kernel;
+        uint64_t devices;
+    };
+    static Entry known[128];
+    if (bytes <= 32768) return IRIS_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IRIS_ECUDA;
+    std::lock_guard<std::mutex> lk(g_mu);
+    for (Entry& e : known) {
+        if (e.kernel == kernel && (e.devices >> dev & 1)) return IRIS_OK;
+        if (e.kernel && e.kernel != kernel) continue;
+        const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+        if (rc != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (norm_join_grad)", static_cast<int>(rc));
+        e.kernel = kernel;
+        e.devices |= uint64_t(1) << dev;
+        return IRIS_OK;
+    }
+    return IRIS_ECUDA;
+}
+
+// Threads T of a row at C chunks of 8 elements each.
+struct RowShape {
+    int T, C;
+};
+RowShape row_shape(int64_t D, int C) {
+    const int64_t chunks = cdiv(D, 8);
+    while (C < NORM_MAX_C && cdiv(chunks, C) > NORM_MAX_T) C *= 2;
+    return RowShape{static_cast<int>(std::min<int64_t>(NORM_MAX_T, round_up(cdiv(chunks, C), 32))), C};
+}
+
+template <int TY, int TX, bool VEC>
+int launch_norm_c(const NormParams& p, RowShape r, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    const int per = r.T == 32 ? 4 : 1;
+    cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(cdiv(p.M, per)), r.T, 0, 1, stream, attr);
+    lc.blockDim = dim3(r.T, per);
+    return launch("norm launch", r.C == 1 ? norm_kernel<TY, TX, VEC, 1> : r.C == 2 ? norm_kernel<TY, TX, VEC, 2> : norm_kernel<TY, TX, VEC, 4>, lc, p);
+}
+template <int TY, int TX>
+int launch_norm(const NormParams& p, bool vec, cudaStream_t stream) {
+    if (p.D > NORM_LONGEST) {
+        cudaLaunchAttribute attr[2];
+        return launch("norm launch", norm_long_kernel<TY, TX>, launch_config(static_cast<unsigned>(p.M), NORM_MAX_T, 0, 1, stream, attr), p);
+    }
+    // few rows: more threads each, for the shortest way through; else more work a thread
+    const RowShape r = row_shape(p.D, p.M < 256 ? 1 : 4);
+    return vec ? launch_norm_c<TY, TX, true>(p, r, stream) : launch_norm_c<TY, TX, false>(p, r, stream);
+}
+template <typename F>
+int by_types(int y, int x, F f) {
+    if (y == IRIS_F32) return f(std::integral_constant<int, T_F32>(), std::integral_constant<int, T_F32>());
+    if (y == IRIS_F16)
+        return x == IRIS_F32 ? f(std::integral_constant<int, T_F16>(), std::integral_constant<int, T_F32>())
+                             : f(std::integral_constant<int, T_F16>(), std::integral_constant<int, T_F16>());
+    return x == IRIS_F32 ? f(std::integral_constant<int, T_BF16>(), std::integral_constant<int, T_F32>())
+                         : f(std::integral_constant<int, T_BF16>(), std::integral_constant<int, T_BF16>());
+}
+
+struct GradPlan {
+    RowShape r;
+    bool in_registers;
+    int64_t ctas;
+    size_t smem, part, total;
+};
+
+template <int TY, int TX, bool VEC>
+int launch_norm_grad_c(const NormGradParams& p, const GradPlan& pl, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    const auto kernel = pl.r.C == 1 ? norm_grad_kernel<TY, TX, VEC, 1> : pl.r.C == 2 ? norm_grad_kernel<TY, TX, VEC, 2> : norm_grad_kernel<TY, TX, VEC, 4>;
+    const int rc = allow_smem(reinterpret_cast<const void*>(kernel), pl.smem);
+    return rc ? rc : launch("norm gradient launch", kernel, launch_config(static_cast<unsigned>(pl.ctas), pl.r.T, pl.smem, 1, stream, attr), p);
+}
+
+int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
+    int rc;
+    NormGradParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!g) return IRIS_EINVAL;
+    const iris_b200_norm_join_args& f = g->f;
+    bool vec;
+    iris_b200_norm_join_args ff = f;
+    ff.h.data = ff.n.data = nullptr;
+    if ((rc = set_norm(&ff, p.f, vec))) return rc;
+    const int64_t M = f.M, D = f.D, G = f.gate.data ? f.gate_rows : 0;
+    const int ye = dtype_size(f.y_dtype), xe = dtype_size(f.x_dtype), ge = dtype_size(f.gate_dtype);
+    if ((g->dn.data && !f.pre) || (g->dgate.data && !f.gate.data) || (M > 0 && D > 0 && !f.stats)) return IRIS_EINVAL;
+    if (M > 0 && D > 0 && !g->dh.data && !g->dn.data) return IRIS_EINVAL;
+    if ((g->dh.data && (rc = check_in(&g->dh, M, D, xe))) || (g->dn.data && (rc = check_in(&g->dn, M, D, ye))) ||
+        (g->dy.data && (rc = check_out(&g->dy, M, D, ye))) || (g->dx.data && (rc = check_out(&g->dx, M, D, xe))) ||
+        (g->dgate.data && (rc = check_out(&g->dgate, G, D, ge))))
+        return rc;
+    void* const vectors[4] = {g->dweight, g->dbias, g->dpost_weight, g->dpost_bias};
+    const int types[4] = {f.weight_dtype, f.bias_dtype, f.post_weight_dtype, f.post_bias_dtype};
+    const int kinds[4] = {f.pre, f.pre, f.post, f.post};
+    NormFinishParams fin;
+    std::memset(&fin, 0, sizeof(fin));
+    for (int i = 0; i < 4; ++i) {
+        p.slot[i] = -1;
+        if (!vectors[i]) continue;
+        if (!kinds[i]) return IRIS_EINVAL;
+        if ((rc = check_vec(vectors[i], types[i]))) return rc;
+        fin.out[p.slots] = vectors[i];
+        fin.type[p.slots] = types[i];
+        p.slot[i] = p.slots++;
+    }
+    p.gate_sums = g->dgate.data && p.f.group_rows != 1;
+    vec = vec && rows16(g->dh, M, D, xe) && rows16(g->dn, M, D, ye) && rows16(g->dy, M, D, ye) && rows16(g->dx, M, D, xe) &&
+          rows16(g->dgate, G, D, ge);
+    int sms;
+    if ((rc = sm_count(&sms))) return rc;
+    GradPlan pl;
+    pl.r = row_shape(D, 1);
+    pl.smem = static_cast<size_t>(p.slots + p.gate_sums) * 8 * pl.r.C * pl.r.T * 4;
+    pl.in_registers = D <= NORM_LONGEST && pl.smem <= 225 * 1024;
+    const int per_sm = static_cast<int>(std::max<size_t>(1, std::min<size_t>(std::min(8, 1024 / pl.r.T), 225 * 1024 / (pl.smem + 2048))));
+    pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1));
+    pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
+    pl.total = WS_HEADER + pl.part + (p.gate_sums ? static_cast<size_t>(pl.ctas) * 2 * D * 4 : 0);
+    if (need) {
+        *need = pl.total;
+        return IRIS_OK;
+    }
+    if (D == 0) return IRIS_OK;
+    if (p.slots || p.gate_sums) {
+        if (!ws || ws_bytes < pl.total) return IRIS_ENOWS;
+        if (!aligned16(ws)) return IRIS_EALIGN;
+        p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER);
+        p.gate_part = reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER + pl.part);
+    }
+    p.dh = mat_of(g->dh);
+    p.dn = mat_of(g->dn);
+    p.dy = mat_of(g->dy);
+    p.dx = mat_of(g->dx);
+    p.dgate = mat_of(g->dgate);
+    p.ctas = pl.ctas;
+    if (M > 0) {
+        rc = by_types(f.y_dtype, f.x_dtype, [&](auto ty, auto tx) {
+            constexpr int TY = decltype(ty)::value, TX = decltype(tx)::value;
+            if (pl.in_registers)
+                return vec ? launch_norm_grad_c<TY, TX, true>(p, pl, stream) : launch_norm_grad_c<TY, TX, false>(p, pl, stream);
+            cudaLaunchAttribute attr[2];
+            return launch("norm gradient launch", norm_grad_long_kernel<TY, TX>,
+                          launch_config(static_cast<unsigned>(pl.ctas), NORM_MAX_T, 0, 1, stream, attr), p);
+        });
+        if (rc) return rc;
+    }
+    if (!p.slots && !p.gate_sums) return IRIS_OK;
+    fin.part = p.part;
+    fin.gate_part = p.gate_part;
+    fin.ctas = static_cast<int>(pl.ctas);
+    fin.slots = p.slots;
+    fin.D = static_cast<int>(D);
+    fin.dgate = p.dgate;
+    fin.gate_type = f.gate_dtype;
+    fin.M = M;
+    fin.group_rows = p.f.group_rows;
+    fin.groups = p.gate_sums ? G : 0;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(cdiv(D, 32)), 256, 0, 1, stream, attr);
+    lc.gridDim.y = static_cast<unsigned>(std::min<int64_t>(fin.slots + fin.groups, 1024));
+    return launch("norm sums launch", norm_finish_kernel<0>, lc, fin);
+}
+
+}  // namespace
+
+extern "C" {
+
+int iris_b200_matmul_act_workspace_size(const iris_b200_matmul_act_args* args, const iris_b200_config* cfg, size_t* bytes) {
+    return bytes ? matmul_act(args, cfg, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;
+}
+int iris_b200_matmul_act(const iris_b200_matmul_act_args* args, const iris_b200_config* cfg, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream) {
+    return matmul_act(args, cfg, workspace, workspace_bytes, stream, nullptr);
+}
+int iris_b200_act_grad_workspace_size(const iris_b200_act_grad_args* args, const iris_b200_config*, size_t* bytes) {
+    return bytes ? act_grad(args, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;
+}
+int iris_b200_act_grad(const iris_b200_act_grad_args* args, const iris_b200_config*, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+    return act_grad(args, workspace, workspace_bytes, stream, nullptr);
+}
+
+int iris_b200_dropout(const iris_b200_dropout_args* g, cudaStream_t stream) {
+    int rc;
+    DropParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!g || !dims_ok(g->M, g->N, 0) || !dtype_ok(g->dtype) || g->reserved) return IRIS_EINVAL;
+    if ((rc = set_drop(p.drop, g->p, g->rng))) return rc;
+    const int64_t M = g->M, N = g->N;
+    const int e = dtype_size(g->dtype);
+    if ((rc = check_in(&g->x, M, N, e)) || (rc = check_out(&g->out, M, N, e)) ||
+        (g->residual.data && (rc = check_in(&g->residual, M, N, e))))
+        return rc;
+    if (M == 0 || N == 0) return IRIS_OK;
+    const int64_t segs = cdiv(N, SEG), items = M * segs;
+    if (items > 0x7FFFFFFF) return IRIS_EINVAL;
+    int sms;
+    if ((rc = sm_count(&sms))) return rc;
+    p.x = mat_of(g->x);
+    p.residual = mat_of(g->residual);
+    p.out = mat_of(g->out);
+    p.M = M;
+    p.N = static_cast<int>(N);
+    p.type = g->dtype;
+    p.segs = static_cast<unsigned>(segs);
+    p.items = static_cast<unsigned>(items);
+    const bool vec = N % 8 == 0 && rows16(g->x, M, N, e) && rows16(g->out, M, N, e) && rows16(g->residual, M, N, e);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cdiv(items, 16), int64_t(sms) * 8));
+    if (g->dtype == IRIS_F32) return launch_dropout<T_F32>(p, vec, grid, stream);
+    if (g->dtype == IRIS_F16) return launch_dropout<T_F16>(p, vec, grid, stream);
+    return launch_dropout<T_BF16>(p, vec, grid, stream);
+}
+
+int iris_b200_norm_join(const iris_b200_norm_join_args* g, cudaStream_t stream) {
+    NormParams p;
+    bool vec;
+    if (!g) return IRIS_EINVAL;
+    const int rc = set_norm(g, p, vec);
+    if (rc) return rc;
+    if ((g->pre != 0) != (g->n.data != nullptr) && g->M > 0 && g->D > 0) return IRIS_EINVAL;
+    if (g->M == 0 || g->D == 0) return IRIS_OK;
+    return by_types(g->y_dtype, g->x_dtype,
+                    [&](auto ty, auto tx) { return launch_norm<decltype(ty)::value, decltype(tx)::value>(p, vec, stream); });
+}
+int iris_b200_norm_join_grad_workspace_size(const iris_b200_norm_join_grad_args* args, const iris_b200_config*, size_t* bytes) {
+    return bytes ? norm_grad(args, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;
+}
+int iris_b200_norm_join_grad(const iris_b200_norm_join_grad_args* args, const iris_b200_config*, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream) {
+    return norm_grad(args, workspace, workspace_bytes, stream, nullptr);
+}
+
+}  // extern "C"

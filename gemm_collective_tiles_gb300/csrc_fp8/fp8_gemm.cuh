@@ -43,6 +43,7 @@
 
 #include "fp8_ptx.cuh"
 #include "fp8_quant.cuh"
+#include "fp8_wait.cuh"
 
 namespace gct {
 namespace fp8 {
@@ -51,37 +52,6 @@ enum : int { KIND_MM = 0, KIND_WG = 1 };
 constexpr int BM = 128;         // rows per CTA (tensor-memory lanes)
 constexpr int WG_CHUNK = 8;     // KIND_WG: 64-deep stages per chunk
 constexpr int MAX_SPLIT = 8;    // CTAs of a cluster that share a tile
-constexpr int DEV_TIMEOUT = 1;
-
-// where-codes recorded when a bounded wait gives up
-enum : int {
-    WAIT_EMPTY = 101,
-    WAIT_FULL = 102,
-    WAIT_FULL_B = 103,
-    WAIT_ACC_EMPTY = 104,
-    WAIT_ACC_FULL = 105,
-    WAIT_RAW = 106,
-    WAIT_A_EMPTY = 107,
-    WAIT_PARTS = 108,
-    WAIT_TAIL = 109,
-    WAIT_FACTOR = 110,
-    WAIT_FACTOR_EMPTY = 111,
-    WAIT_DRAIN_TMA = 120,  // from here on: teardown
-    WAIT_DRAIN_MMA = 121,
-};
-
-// The library's workspace header (same layout for every op).
-struct WsHeader {
-    uint32_t epoch;        // epoch of the last completed launch
-    uint32_t ctr[2];       // queue heads of other ops; zero between launches
-    uint32_t done_ctr;     // CTAs finished in this launch
-    int status;            // sticky first device error (0 = none)
-    uint32_t abort_epoch;  // == current epoch while the launch is stopping
-    int err_where;
-    int err_index;
-    uint32_t pad[56];
-};
-static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 
 struct GemmParams {
     CUtensorMap tmA;  // MM: codes {k, row}, box {128, a_box}; WG: codes {k, m}, box {128, 64}
@@ -113,47 +83,6 @@ struct GemmParams {
     unsigned long long wait_ns;
     uint32_t debug_skip;          // test hook: k > 0: tile k - 1 never reports its accumulator
 };
-
-struct Ctl {
-    WsHeader* ws;
-    uint32_t epoch;
-    unsigned long long limit;
-    int rank;  // in the cluster: the half of a pair's tile, or the part of the contraction
-};
-
-__device__ __forceinline__ bool launch_aborted(const Ctl& c) {
-    return *reinterpret_cast<volatile uint32_t*>(&c.ws->abort_epoch) == c.epoch;
-}
-__device__ __forceinline__ void raise_timeout(const Ctl& c, int where, int index) {
-    if (atomicCAS(&c.ws->status, 0, DEV_TIMEOUT) == 0) {
-        c.ws->err_where = where;
-        c.ws->err_index = index;
-    }
-    __threadfence();
-    atomicExch(&c.ws->abort_epoch, c.epoch);
-}
-// Bounded wait for a phase of a barrier; false = gave up, here or elsewhere.
-__device__ __forceinline__ bool wait_bar(const Ctl& c, uint32_t bar, uint32_t parity, int where) {
-    if (bar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1;; ++i) {
-        if (bar_try_wait(bar, parity)) return true;
-        if ((i & 15) == 0) {
-            // teardown waits are for work already issued: they go on while the launch stops
-            if (where < WAIT_DRAIN_TMA && launch_aborted(c)) return false;
-            if (global_timer_ns() - t0 > c.limit) {
-                raise_timeout(c, where, -1);
-                return false;
-            }
-        }
-    }
-}
-// for barriers that other CTAs' promotion warps arrive on after writing shared
-// memory that this one reads
-__device__ __forceinline__ bool wait_bar_cluster(const Ctl& c, uint32_t bar, uint32_t parity, int where) {
-    if (!wait_bar(c, bar, parity, where)) return false;
-    return bar_try_wait_cluster(bar, parity);  // the phase is over: this only acquires at cluster scope
-}
 
 template <int KIND, int CG>
 struct Geo {
@@ -230,32 +159,6 @@ struct Smem {
     __device__ __forceinline__ uint32_t raw(uint32_t s) const { return raw_tiles + s * G::RAW_BYTES; }
     __device__ __forceinline__ uint8_t* at(uint32_t addr) const { return base + (addr - tiles); }
     __device__ __forceinline__ uint8_t* out(int w) const { return base + G::TILES_BYTES + w * G::OUT_BYTES; }
-};
-
-// Position in a ring of N slots.
-template <int N>
-struct Ring {
-    uint32_t slot = 0, phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == N) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-};
-// A producer's record of its fills: bit s of `filled` is the phase of slot s's
-// last one.
-struct Fills {
-    uint32_t used = 0, filled = 0;
-    __device__ __forceinline__ void add(uint32_t slot, uint32_t phase) {
-        filled = (filled & ~(1u << slot)) | phase << slot;
-        used |= 1u << slot;
-    }
-    // every load has landed before the CTA leaves
-    __device__ __forceinline__ void drain(const Ctl& ctl, uint32_t bars, int n) const {
-        for (int s = 0; s < n; ++s)
-            if ((used & (1u << s)) && !wait_bar(ctl, bars + 8 * s, filled >> s & 1u, WAIT_DRAIN_TMA)) return;
-    }
 };
 
 // which half of a pair's tile this CTA works on
@@ -454,14 +357,6 @@ __device__ void run_mma(const GemmParams& p, const Ctl& ctl, Smem<KIND, CG>& sm,
     wait_bar(ctl, sm.final_bar + 8 * issuer, 0, WAIT_DRAIN_MMA);
 }
 
-__device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
-    if (bf16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 // 16 codes -> 16 scaled 16-bit values.  Codes go to f16 pairs (exact) and
 // through fp32, times the scale, to the 16-bit type: one rounding, none for a
 // power-of-two scale.  (Setting a code's bits into a bf16 number and scaling

@@ -564,6 +564,142 @@ IRIS_API int iris_b200_weight_grad_fp8_workspace_size(const iris_b200_weight_gra
 IRIS_API int iris_b200_weight_grad_fp8(const iris_b200_weight_grad_fp8_args* args, const iris_b200_config* cfg,
                                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * The sides of a block's linear layers, on plain device tensors: a 16-bit
+ * product with bias, activation, dropout and residual in its epilogue and the
+ * gradient of that epilogue; dropout; the norms around a block's end.
+ *
+ * Matrices have any non-negative strides, vectors are contiguous.  An optional
+ * matrix or vector is absent where its data is NULL.  Outputs do not overlap
+ * other tensors of the call, but for those named below that may be an input
+ * itself (same address, strides and type).
+ *
+ * Dropout: element (i, j) has 16 random bits r, lane j % 8 of Philox4x32-10
+ * with rng[0]'s two words (low, high) as key and (j / 8, i, rng[1]'s two words)
+ * as counter; lane 2 w + 1 is the upper half of output word w.  With T =
+ * rint(65536 p) it is divided by 1 - T / 65536 where r >= T, and 0 elsewhere,
+ * whatever it was.  rng is device memory, read when the kernel runs, and not
+ * needed where T is 0.  0 <= p <= 1.
+ */
+typedef enum {
+    IRIS_ACT_NONE = 0,
+    IRIS_ACT_RELU = 1,
+    IRIS_ACT_GELU = 2,      /* z Phi(z) */
+    IRIS_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    IRIS_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} iris_act;
+
+/*
+ * matmul_act -- z = A (M x K) @ B (K x N) + bias; out = residual + dropout(act(z)).
+ * A and B are f16 or bf16, the same type; out, residual and z share a type
+ * (f16, bf16 or f32); bias is any of the three.  Sums, bias, activation and
+ * residual are fp32, rounded once to out (and once to z, where it is wanted).
+ * residual may be out itself.
+ *
+ * Workspace: as the 8-bit products'.  Of the config, tile_m (128: 128 x 128
+ * tiles, or the kernel of few rows; 256: pairs), tile_n (128 or 256: columns of a
+ * pair's tile), k_split (1, 2, 4 or 8 CTAs of a cluster share a 128 x 128 tile's
+ * contraction), group_m, grid, wait_ns and
+ * debug_skip_flag apply.
+ */
+typedef struct {
+    iris_b200_mat A, B, out, residual, z;
+    const void* bias;
+    const int64_t* rng;
+    int64_t M, N, K;
+    double p;
+    int32_t ab_dtype, out_dtype, bias_dtype; /* iris_dtype */
+    int32_t act;                             /* iris_act */
+} iris_b200_matmul_act_args;
+
+IRIS_API int iris_b200_matmul_act_workspace_size(const iris_b200_matmul_act_args* args, const iris_b200_config* cfg,
+                                                 size_t* bytes);
+IRIS_API int iris_b200_matmul_act(const iris_b200_matmul_act_args* args, const iris_b200_config* cfg, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * act_grad -- dz = dropout(dy) act'(z) (M x N) and dbias = the column sums of dz
+ * (before its rounding); either may be absent.  dy and z share a type; z is not
+ * read for IRIS_ACT_NONE.  dz may be dy or z itself.  No config.
+ */
+typedef struct {
+    iris_b200_mat dy, z, dz;
+    void* dbias;
+    const int64_t* rng;
+    int64_t M, N;
+    double p;
+    int32_t dtype, dz_dtype, dbias_dtype; /* iris_dtype; dtype: of dy and z */
+    int32_t act;
+} iris_b200_act_grad_args;
+
+IRIS_API int iris_b200_act_grad_workspace_size(const iris_b200_act_grad_args* args, const iris_b200_config* cfg,
+                                               size_t* bytes);
+IRIS_API int iris_b200_act_grad(const iris_b200_act_grad_args* args, const iris_b200_config* cfg, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * dropout -- out = residual + dropout(x), all M x N of one type; out may be x or
+ * residual itself.  The gradient of x is the same call on out's.
+ */
+typedef struct {
+    iris_b200_mat x, residual, out;
+    const int64_t* rng;
+    int64_t M, N;
+    double p;
+    int32_t dtype;
+    int32_t reserved; /* 0 */
+} iris_b200_dropout_args;
+
+IRIS_API int iris_b200_dropout(const iris_b200_dropout_args* args, cudaStream_t stream);
+
+/*
+ * norm_join -- u = N_post(y) (or y), h = x + scale * gate * u (x, gate absent:
+ * left out), n = N_pre(h).
+ *   N(v) = (v - m) / sqrt(mean((v - m)^2) + eps) * weight + bias over a row;
+ *   m is the row's mean (IRIS_NORM_LAYER) or 0 (IRIS_NORM_RMS).
+ * y, n: M x D of y_dtype; x, h: M x D of x_dtype; gate: gate_rows x D, each row
+ * for M / gate_rows rows of y.  Vectors of D.  Everything is fp32 between the
+ * loads and the stores, and h enters the second norm unrounded.  h is written
+ * where given, n where pre is not NONE.  stats, where given: 4 floats a row,
+ * mean and 1 / sqrt of y's norm and of h's, for the gradient.
+ * (y_dtype, x_dtype): equal, or x_dtype f32.  h may be x (or y, where the types
+ * agree) itself, n may be y.
+ */
+typedef enum { IRIS_NORM_NONE = 0, IRIS_NORM_RMS = 1, IRIS_NORM_LAYER = 2 } iris_norm;
+
+typedef struct {
+    iris_b200_mat y, x, gate, h, n;
+    const void *post_weight, *post_bias, *weight, *bias;
+    float* stats;
+    int64_t M, D, gate_rows;
+    double scale, eps;
+    int32_t y_dtype, x_dtype, gate_dtype;
+    int32_t post_weight_dtype, post_bias_dtype, weight_dtype, bias_dtype;
+    int32_t post, pre; /* iris_norm */
+    int32_t reserved;  /* 0 */
+} iris_b200_norm_join_args;
+
+IRIS_API int iris_b200_norm_join(const iris_b200_norm_join_args* args, cudaStream_t stream);
+
+/*
+ * norm_join_grad -- the gradients of norm_join, from those of h and n (one may be
+ * absent; dn is absent where pre is NONE).  f: the forward call's, whose h and n
+ * are not used and whose stats are read.  dy as y, dx as x and dh (x_dtype
+ * without an x too), dgate as gate, the vectors' as the vectors; each may be
+ * absent.  dx may be dh itself, dy may be dn or y.  Sums over rows are fp32, in a
+ * fixed order.  No config.
+ */
+typedef struct {
+    iris_b200_norm_join_args f;
+    iris_b200_mat dh, dn, dy, dx, dgate;
+    void *dpost_weight, *dpost_bias, *dweight, *dbias;
+} iris_b200_norm_join_grad_args;
+
+IRIS_API int iris_b200_norm_join_grad_workspace_size(const iris_b200_norm_join_grad_args* args,
+                                                     const iris_b200_config* cfg, size_t* bytes);
+IRIS_API int iris_b200_norm_join_grad(const iris_b200_norm_join_grad_args* args, const iris_b200_config* cfg,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
