@@ -93,17 +93,17 @@ int make_plan(Plan& pl, const iris_b200_config* cfg, const DeviceInfo& d, int64_
     iris_b200_config z;
     std::memset(&z, 0, sizeof(z));
     if (!cfg) cfg = &z;
-    if (cfg->tile_m != 0 && cfg->tile_m != 128 && cfg->tile_m != 256) return IRIS_EINVAL;
+    const int tm = cfg->tile_m;
+    if (tm != 0 && tm != 16 && tm != 32 && tm != 64 && tm != 128 && tm != 256) return IRIS_EINVAL;
     if (cfg->tile_n != 0 && cfg->tile_n != 128 && cfg->tile_n != 256) return IRIS_EINVAL;
     if (cfg->k_split != 0 && cfg->k_split != 1 && cfg->k_split != 2 && cfg->k_split != 4 && cfg->k_split != 8) return IRIS_EINVAL;
     if (cfg->group_m < 0 || cfg->debug_skip_flag < 0 || cfg->grid < 0 || cfg->grid > d.sms) return IRIS_EINVAL;
     const int64_t stages = cdiv(depth, DEPTH);
-    const int grid = cfg->grid ? cfg->grid : d.sms;
     double best = 0;
     pl.variant = -1;
     for (int v = PAIR; v < VARIANTS; ++v) {
         const int cg = is_pair(v) ? 2 : 1, bn = v == PAIR ? 256 : 128;
-        if (cfg->tile_m && cfg->tile_m != 128 * cg) continue;
+        if (tm && tm != (v >= FEW16 ? few_rows(v) : 128 * cg)) continue;
         if (cfg->tile_n && cfg->tile_n != bn) continue;
         if (v >= FEW16 && rows > few_rows(v)) continue;
         const int64_t mb = cdiv(rows, 128 * cg), nb = cdiv(cols, bn), tiles = mb * nb;
@@ -111,7 +111,7 @@ int make_plan(Plan& pl, const iris_b200_config* cfg, const DeviceInfo& d, int64_
         for (int lg = 0; lg < (cg == 2 ? 1 : 4); ++lg) {
             const int split = 1 << lg;
             const int64_t part = cdiv(stages, split);
-            const int slots = std::min(d.clusters[v][cg == 2 ? 1 : lg], grid / (cg * split));
+            const int slots = std::min(d.clusters[v][cg == 2 ? 1 : lg], cfg->grid ? cfg->grid / (cg * split) : INT32_MAX);
             // every part has stages, unless the config asks for it (an empty one adds zeros)
             if (slots < 1 || (cfg->k_split ? split != cfg->k_split : split > stages)) continue;
             const double t = estimate(v, slots, tiles, part, split);
@@ -218,12 +218,16 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
     const CUtensorMapDataType t16 = t ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     p.a_mn = a.transposed;
     p.b_mn = !b.transposed;
-    const int a_rows = few ? few_rows(pl.variant) : 128, b_rows = pl.variant == HALF ? 64 : 128;
+    // few rows: no more of a box than there are tokens (rows past a tensor's end cost
+    // the tensor memory accelerator more than rows that exist: one token 4096 x
+    // 14336 42 us with boxes of 16); what lies in the others' place reaches only
+    // sums that nobody reads
+    const int a_rows = few ? static_cast<int>(M) : 128, b_rows = pl.variant == HALF ? 64 : 128;
     if ((rc = make_map_2d(&p.tmA, t16, 2, a, 64, p.a_mn ? 64 : a_rows)) ||
         (rc = make_map_2d(&p.tmB, t16, 2, b, 64, p.b_mn ? 64 : b_rows)))
         return rc;
     // few rows: the weights are the MMA's first operand
-    p.idesc = few ? idesc_of(t, t, p.b_mn, 0, 128, a_rows)
+    p.idesc = few ? idesc_of(t, t, p.b_mn, 0, 128, few_rows(pl.variant))
                   : idesc_of(t, t, p.a_mn, p.b_mn, is_pair(pl.variant) ? 256 : 128, pl.variant == PAIR ? 256 : 128);
     auto store_map = [&](CUtensorMap* m, const iris_b200_mat& x) {
         return make_store_map(m, p.type, x.data, N, M, M == 1 ? packed_pitch(N, e) : x.row_stride);
@@ -387,7 +391,7 @@ int allow_smem(const void* kernel, size_t bytes) {
     for (Entry& e : known) {
         if (e.kernel == kernel && (e.devices >> dev & 1)) return IRIS_OK;
         if (e.kernel && e.kernel != kernel) continue;
-        const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+        const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
         if (rc != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (norm_join_grad)", static_cast<int>(rc));
         e.kernel = kernel;
         e.devices |= uint64_t(1) << dev;
@@ -440,13 +444,15 @@ struct GradPlan {
     int64_t ctas;
     size_t smem, part, total;
 };
+constexpr int64_t NORM_GRAD_PART = NORM_MAX_T * NORM_GRAD_C * 8;  // elements of a row that a CTA takes
+constexpr size_t SM_SMEM = 226 * 1024;
 
 template <int TY, int TX, bool VEC>
 int launch_norm_grad_c(const NormGradParams& p, const GradPlan& pl, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
-    const auto kernel = pl.r.C == 1 ? norm_grad_kernel<TY, TX, VEC, 1> : pl.r.C == 2 ? norm_grad_kernel<TY, TX, VEC, 2> : norm_grad_kernel<TY, TX, VEC, 4>;
+    const auto kernel = pl.r.C == 1 ? norm_grad_kernel<TY, TX, VEC, 1> : norm_grad_kernel<TY, TX, VEC, 2>;
     const int rc = allow_smem(reinterpret_cast<const void*>(kernel), pl.smem);
-    return rc ? rc : launch("norm gradient launch", kernel, launch_config(static_cast<unsigned>(pl.ctas), pl.r.T, pl.smem, 1, stream, attr), p);
+    return rc ? rc : launch("norm gradient launch", kernel, launch_config(static_cast<unsigned>(pl.ctas * p.parts), pl.r.T, pl.smem, p.parts, stream, attr), p);
 }
 
 int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
@@ -487,11 +493,22 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     int sms;
     if ((rc = sm_count(&sms))) return rc;
     GradPlan pl;
-    pl.r = row_shape(D, 1);
-    pl.smem = static_cast<size_t>(p.slots + p.gate_sums) * 8 * pl.r.C * pl.r.T * 4;
-    pl.in_registers = D <= NORM_LONGEST && pl.smem <= 225 * 1024;
-    const int per_sm = static_cast<int>(std::max<size_t>(1, std::min<size_t>(std::min(8, 1024 / pl.r.T), 225 * 1024 / (pl.smem + 2048))));
-    pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1));
+    // A row to a CTA, or, where it is too long for one's registers, to a cluster.
+    pl.in_registers = D <= 8 * NORM_GRAD_PART;
+    p.parts = 1;
+    while (pl.in_registers && p.parts * NORM_GRAD_PART < D) p.parts *= 2;
+    pl.r = row_shape(cdiv(D, p.parts), 1);
+    // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
+    const int per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
+    const size_t pieces = static_cast<size_t>(pl.r.C) * pl.r.T * 16;
+    const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pieces;
+    const size_t y_bytes = pieces * (ye / 2), x_bytes = pieces * (xe / 2);
+    p.row_bytes = static_cast<unsigned>(y_bytes + (f.x.data ? x_bytes : 0) + (g->dh.data ? x_bytes : 0) + (g->dn.data ? y_bytes : 0));
+    const size_t room = SM_SMEM / per_sm - 2048;
+    p.depth = vec && sums < room ? static_cast<int>(std::min<size_t>(4, (room - sums) / p.row_bytes)) : 0;
+    pl.smem = sums + p.depth * p.row_bytes;
+    if (pl.smem > SM_SMEM - 2048) return IRIS_EUNSUPPORTED;
+    pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
     pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
     pl.total = WS_HEADER + pl.part + (p.gate_sums ? static_cast<size_t>(pl.ctas) * 2 * D * 4 : 0);
     if (need) {

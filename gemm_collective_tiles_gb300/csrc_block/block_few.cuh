@@ -9,8 +9,8 @@
 // CTA layout (256 threads, one CTA per SM): warp 0 loads, warp 1 issues the
 // MMAs, warps 4-7 are the epilogue: 32 columns of the output each.  A cluster of
 // up to 8 CTAs shares a tile's contraction.  At the end every part's sums lie in
-// shared memory as [token][column]; each CTA adds a share of the tile's outputs
-// over them, in the order of the parts, and finishes four columns a thread.
+// shared memory as [token][column]; each CTA adds its share of the rows over them,
+// in the order of the parts, and finishes them, four columns a lane.
 #pragma once
 #include "block_gemm.cuh"
 
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) act_few_kernel(const _
                         break;
                     }
                     const uint32_t w = tiles + st.slot * G::STAGE_BYTES, bar = full + 8 * st.slot;
-                    bar_expect_tx(bar, G::STAGE_BYTES);
+                    bar_expect_tx(bar, G::W_BYTES + p.M * 128);
                     load_operand<1>(w, &p.tmB, p.b_mn, u * 128, 128, s * DEPTH, bar);
                     tma_load_2d(w + G::W_BYTES, &p.tmA, s * DEPTH, 0, bar);
                     fills.add(st.slot, st.phase);
@@ -137,9 +137,14 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) act_few_kernel(const _
     } else if (warp >= 4) {
         const int q = warp - 4;
         const DropKey key = drop_key(p.drop);
+        const int row_lo = p.M * rank / S, row_hi = p.M * (rank + 1) / S;  // this part's share of the outputs
         Ring<G::ACCS> acc;
         uint32_t tiles_done = 0;
         for (int u = first; u < p.n_units; u += step, ++tiles_done) {
+            const Four four(p, u * 128 + lane * 4);
+            float4 res[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) res[j] = four.residual(p, min(row_lo + q + 4 * j, p.M - 1));
             uint32_t r[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) r[i] = 0u;
@@ -169,25 +174,35 @@ __global__ void __launch_bounds__(FewGeo<NT>::THREADS, 1) act_few_kernel(const _
                        : !wait_bar_cluster(ctl, parts_in, tiles_done & 1, WAIT_PARTS))
                 break;
             __syncwarp();
-            // this part's share of the tile's M x 32 groups of four columns
-            const int all = p.M * 32, share = ((all + S - 1) / S + 31) / 32 * 32;
-            const int end = min(all, (rank + 1) * share);
-            const uint32_t mine = smem_u32(sums);
-            for (int i = rank * share + q * 32 + lane; i < end; i += 128) {
-                float4 t[MOST_PARTS];
+            // this part's rows of the tile: four columns a lane, every 16th of them a warp
+            // at once with the loads of four rows under way
+            const uint32_t mine = smem_u32(sums) + lane * 16;
+            for (int i = row_lo + q; i < row_hi; i += 16) {
+                float4 part[4][MOST_PARTS];
 #pragma unroll
-                for (int k = 0; k < MOST_PARTS; ++k)
-                    if (k < S) t[k] = ld_shared_cluster_f4((S == 1 ? mine : map_to(mine, k)) + i * 16);
-                float v[4] = {t[0].x, t[0].y, t[0].z, t[0].w};
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int k = 1; k < MOST_PARTS; ++k)
-                    if (k < S) {
-                        v[0] += t[k].x;
-                        v[1] += t[k].y;
-                        v[2] += t[k].z;
-                        v[3] += t[k].w;
-                    }
-                finish4(p, key, i >> 5, u * 128 + (i & 31) * 4, v);
+                    for (int k = 0; k < MOST_PARTS; ++k)
+                        if (k < S && i + 4 * j < row_hi)
+                            part[j][k] = ld_shared_cluster_f4((S == 1 ? mine : map_to(mine, k)) + (i + 4 * j) * 512);
+                if (i > row_lo + q) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) res[j] = four.residual(p, min(i + 4 * j, p.M - 1));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (i + 4 * j >= row_hi) break;
+                    float v[4] = {part[j][0].x, part[j][0].y, part[j][0].z, part[j][0].w};
+#pragma unroll
+                    for (int k = 1; k < MOST_PARTS; ++k)
+                        if (k < S) {
+                            v[0] += part[j][k].x;
+                            v[1] += part[j][k].y;
+                            v[2] += part[j][k].z;
+                            v[3] += part[j][k].w;
+                        }
+                    four.finish(p, key, i + 4 * j, v, res[j]);
+                }
             }
             // tell the parts that their sums have been read, unless none will write
             // again: a CTA on its way out gets no more arrivals

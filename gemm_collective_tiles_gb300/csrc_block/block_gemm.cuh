@@ -64,13 +64,38 @@ __device__ __forceinline__ float bias_at(const ActParams& p, int col) {
     return p.bias && col < p.N ? load_any(p.bias, p.bias_type, col) : 0.f;
 }
 
-// The rest of the formula for up to four neighbouring columns of a row, from
-// their sums.  Columns are a multiple of 4.
-__device__ __forceinline__ void finish4(const ActParams& p, const DropKey& key, long long row, int col, float (&v)[4]) {
-    if (row >= p.M || col >= p.N) return;
-    const bool four = col + 4 <= p.N;
-    auto put = [&](void* to, bool tma, long long rs, long long cs) {
-        if (tma && four) {  // unit stride, rows on 16 bytes
+// A lane's four neighbouring columns (from a multiple of 4 on), for rows whose
+// sums come through shared memory: the rest of the formula.  Their bias is
+// fetched before the sums are there.
+struct Four {
+    int col;
+    bool live, whole;  // some of them exist, all do
+    float bias[4];
+    __device__ __forceinline__ Four(const ActParams& p, int c) : col(c), live(c < p.N), whole(c + 4 <= p.N) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[e] = bias_at(p, c + e);
+    }
+    __device__ __forceinline__ float4 residual(const ActParams& p, long long row) const {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!p.residual || !live || row >= p.M) return f;
+        if (p.res_tma && whole) {  // unit stride, rows on 16 bytes
+            if (p.type == T_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + row * p.res_rs + col);
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) + row * p.res_rs + col);
+            if (p.type == T_F16) {
+                unpack16<T_F16>(u.x, f.x, f.y);
+                unpack16<T_F16>(u.y, f.z, f.w);
+            } else {
+                unpack16<T_BF16>(u.x, f.x, f.y);
+                unpack16<T_BF16>(u.y, f.z, f.w);
+            }
+            return f;
+        }
+        auto at = [&](int e) { return col + e < p.N ? load_any(p.residual, p.type, row * p.res_rs + (col + e) * p.res_cs) : 0.f; };
+        return make_float4(at(0), at(1), at(2), at(3));
+    }
+    __device__ __forceinline__ void put(const ActParams& p, void* to, bool tma, long long rs, long long cs, long long row,
+                                        const float (&v)[4]) const {
+        if (tma && whole) {
             if (p.type == T_F32)
                 *reinterpret_cast<float4*>(static_cast<float*>(to) + row * rs + col) = make_float4(v[0], v[1], v[2], v[3]);
             else
@@ -81,29 +106,29 @@ __device__ __forceinline__ void finish4(const ActParams& p, const DropKey& key, 
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (col + e < p.N) store_any(to, p.type, row * rs + (col + e) * cs, v[e]);
-    };
-    if (p.bias) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += bias_at(p, col + e);
     }
-    if (p.z) put(p.z, p.z_tma, p.z_rs, p.z_cs);
-    apply_act(v, p.act);
-    if (p.drop.least) {
-        uint32_t w[4];
-        philox8(key, static_cast<uint32_t>(col) >> 3, static_cast<uint32_t>(row), w);
+    __device__ __forceinline__ void finish(const ActParams& p, const DropKey& key, long long row, float (&v)[4], const float4& res) const {
+        if (!live || row >= p.M) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t pair = (col & 4) ? w[2 + e / 2] : w[e / 2];
-            v[e] = ((e & 1) ? pair >> 16 : pair & 0xFFFFu) >= p.drop.least ? v[e] * p.drop.scale : 0.f;
+        for (int e = 0; e < 4; ++e) v[e] += bias[e];
+        if (p.z) put(p, p.z, p.z_tma, p.z_rs, p.z_cs, row, v);
+        apply_act(v, p.act);
+        if (p.drop.least) {
+            uint32_t w[4];
+            philox8(key, static_cast<uint32_t>(col) >> 3, static_cast<uint32_t>(row), w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t pair = (col & 4) ? w[2 + e / 2] : w[e / 2];
+                v[e] = ((e & 1) ? pair >> 16 : pair & 0xFFFFu) >= p.drop.least ? v[e] * p.drop.scale : 0.f;
+            }
         }
+        v[0] += res.x;
+        v[1] += res.y;
+        v[2] += res.z;
+        v[3] += res.w;
+        put(p, p.out, p.out_tma, p.out_rs, p.out_cs, row, v);
     }
-    if (p.residual) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (col + e < p.N) v[e] += load_any(p.residual, p.type, row * p.res_rs + (col + e) * p.res_cs);
-    }
-    put(p.out, p.out_tma, p.out_rs, p.out_cs);
-}
+};
 
 template <int CG, int BN>
 struct Geo {
@@ -506,6 +531,12 @@ struct Epilogue {
         constexpr int UNITS = 16, SHARE = UNITS / S;
         static_assert(UNITS * 512 <= G::OUT_BYTES || CG == 2, "a warp's sums fit its boxes");
         const bool empty = part_start(p, ctl.rank) == part_start(p, ctl.rank + 1);  // adds zeros
+        const int unit = lane % UNITS;
+        auto share_row = [&](int i) { return ctl.rank * (32 / S) + i * (32 / UNITS) + lane / UNITS; };
+        const Four four(p, col0 + unit * 4);
+        float4 res[SHARE];
+#pragma unroll
+        for (int i = 0; i < SHARE; ++i) res[i] = four.residual(p, row0 + share_row(i));
         if (!empty && !acc_ready()) return false;
         // the other parts have read what lay here before
         if (joins > 0 && !wait_bar_cluster(ctl, sm.parts_out + 8 * w, (joins - 1) & 1, WAIT_PARTS)) return false;
@@ -530,10 +561,8 @@ struct Epilogue {
         if (!wait_bar_cluster(ctl, sm.parts_in + 8 * w, joins & 1, WAIT_PARTS)) return false;
         __syncwarp();
         ++joins;
-        const int unit = lane % UNITS;
         const uint32_t all = smem_u32(stg);
         float4 t[SHARE][S];
-        auto share_row = [&](int i) { return ctl.rank * (32 / S) + i * (32 / UNITS) + lane / UNITS; };
 #pragma unroll
         for (int k = 0; k < S; ++k) {
             const uint32_t from_k = map_to(all, k);
@@ -553,7 +582,7 @@ struct Epilogue {
                 v[2] += t[i][k].z;
                 v[3] += t[i][k].w;
             }
-            finish4(p, key, row0 + share_row(i), col0 + unit * 4, v);
+            four.finish(p, key, row0 + share_row(i), v, res[i]);
         }
         // the values above are in registers: the parts may lay their next sums, if
         // there are any: a CTA on its way out gets no more arrivals
@@ -669,7 +698,8 @@ __global__ void __launch_bounds__(256) act_fill_kernel(const __grid_constant__ A
     const long long groups = (p.N + 3) / 4, n = p.M * groups;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        finish4(p, key, i / groups, static_cast<int>(i % groups) * 4, v);
+        const Four four(p, static_cast<int>(i % groups) * 4);
+        four.finish(p, key, i / groups, v, four.residual(p, i / groups));
     }
 }
 

@@ -26,6 +26,7 @@ namespace block {
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
 constexpr int NORM_MAX_T = 512, NORM_MAX_C = 4;
 constexpr int NORM_LONGEST = NORM_MAX_T * NORM_MAX_C * 8;  // elements of a row in registers
+constexpr int NORM_GRAD_C = 2;                             // of the gradient, whose long rows are shared by a cluster
 
 struct Vec {
     const void* data;
@@ -47,6 +48,9 @@ struct NormGradParams {
     // dpost_w, dpost_b are wanted, by slot (-1: not)
     int slot[4], slots;
     int gate_sums;            // dgate is a sum over rows
+    int parts;                // CTAs of a cluster that share a row
+    int depth;                // rows ahead in shared memory
+    unsigned row_bytes;       // of them each
     float* part;              // (CTA, slot, D)
     float* gate_part;         // (CTA, 2, D): a group begun before, a group that goes on
     long long ctas;
@@ -65,26 +69,23 @@ struct NormFinishParams {
 // first row of CTA c
 __host__ __device__ __forceinline__ long long norm_row(long long M, long long ctas, long long c) { return M * c / ctas; }
 
-template <int C>
-struct Piece {
-    float v[8 * C];
-};
+// column of a thread's element i, in the CTA's part of the row
 template <bool VEC>
 __device__ __forceinline__ int norm_column(int T, int t, int i) {
     return VEC ? ((i >> 3) * T + t) * 8 + (i & 7) : i * T + t;
 }
 template <int TYPE, bool VEC, int C>
-__device__ __forceinline__ void load_row(const Mat& m, long long row, int T, int t, int D, float (&v)[8 * C]) {
+__device__ __forceinline__ void load_row(const Mat& m, long long row, int T, int t, int base, int D, float (&v)[8 * C]) {
     const long long o = row * m.rs;
     if constexpr (VEC) {
         Raw<TYPE> raw[C];
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (norm_column<true>(T, t, 8 * c) < D) raw[c] = load8<TYPE>(m.data, o + norm_column<true>(T, t, 8 * c));
+            if (base + norm_column<true>(T, t, 8 * c) < D) raw[c] = load8<TYPE>(m.data, o + base + norm_column<true>(T, t, 8 * c));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float w[8];
-            if (norm_column<true>(T, t, 8 * c) < D) {
+            if (base + norm_column<true>(T, t, 8 * c) < D) {
                 spread8<TYPE>(raw[c], w);
             } else {
 #pragma unroll
@@ -96,19 +97,20 @@ __device__ __forceinline__ void load_row(const Mat& m, long long row, int T, int
     } else {
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) {
-            const int c = norm_column<false>(T, t, i);
+            const int c = base + norm_column<false>(T, t, i);
             v[i] = c < D ? load_elem<TYPE>(m.data, o + c * m.cs) : 0.f;
         }
     }
 }
 template <bool VEC, int C>
-__device__ __forceinline__ void store_row(const Mat& m, int type, long long row, int T, int t, int D, const float (&v)[8 * C]) {
+__device__ __forceinline__ void store_row(const Mat& m, int type, long long row, int T, int t, int base, int D,
+                                          const float (&v)[8 * C]) {
     void* const to = const_cast<void*>(m.data);
     const long long o = row * m.rs;
     if constexpr (VEC) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int at = norm_column<true>(T, t, 8 * c);
+            const int at = base + norm_column<true>(T, t, 8 * c);
             float w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = v[8 * c + e];
@@ -117,19 +119,19 @@ __device__ __forceinline__ void store_row(const Mat& m, int type, long long row,
     } else {
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) {
-            const int c = norm_column<false>(T, t, i);
+            const int c = base + norm_column<false>(T, t, i);
             if (c < D) store_any(to, type, o + c * m.cs, v[i]);
         }
     }
 }
 // f(i, value) for this thread's elements of a vector or of a row of gate
 template <bool VEC, int C, typename F>
-__device__ __forceinline__ void with_vector(const void* data, int type, long long o, long long cs, int T, int t, int D, F f) {
+__device__ __forceinline__ void with_vector(const void* data, int type, long long o, long long cs, int T, int t, int base, int D, F f) {
     if (!data) return;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         if (VEC) {
-            const int at = norm_column<true>(T, t, 8 * c);
+            const int at = base + norm_column<true>(T, t, 8 * c);
             if (at >= D) continue;
             float w[8];
             if (type == T_F32)
@@ -143,7 +145,7 @@ __device__ __forceinline__ void with_vector(const void* data, int type, long lon
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int at = norm_column<false>(T, t, 8 * c + e);
+                const int at = base + norm_column<false>(T, t, 8 * c + e);
                 if (at < D) f(8 * c + e, load_any(data, type, o + at * cs));
             }
         }
@@ -200,8 +202,8 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_kernel(const __grid_constant_
     const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= p.M) return;
     float v[8 * C], x[8 * C];
-    load_row<TY, VEC, C>(p.y, row, T, t, D, v);
-    if (p.x.data) load_row<TX, VEC, C>(p.x, row, T, t, D, x);
+    load_row<TY, VEC, C>(p.y, row, T, t, 0, D, v);
+    if (p.x.data) load_row<TX, VEC, C>(p.x, row, T, t, 0, D, x);
     float4 stats = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.post) {
         const float2 s = row_stats<VEC, C>(v, p.post, p.eps, T, t, D, buffer, turn);
@@ -209,23 +211,23 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_kernel(const __grid_constant_
         stats.y = s.y;
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) v[i] = norm_column<VEC>(T, t, i) < D ? (v[i] - s.x) * s.y : 0.f;
-        with_vector<VEC, C>(p.post_w.data, p.post_w.type, 0, 1, T, t, D, [&](int i, float w) { v[i] *= w; });
-        with_vector<VEC, C>(p.post_b.data, p.post_b.type, 0, 1, T, t, D, [&](int i, float w) { v[i] += w; });
+        with_vector<VEC, C>(p.post_w.data, p.post_w.type, 0, 1, T, t, 0, D, [&](int i, float w) { v[i] *= w; });
+        with_vector<VEC, C>(p.post_b.data, p.post_b.type, 0, 1, T, t, 0, D, [&](int i, float w) { v[i] += w; });
     }
-    with_vector<VEC, C>(p.gate.data, p.gate_type, p.gate.data ? row / p.group_rows * p.gate.rs : 0, p.gate.cs, T, t, D,
+    with_vector<VEC, C>(p.gate.data, p.gate_type, p.gate.data ? row / p.group_rows * p.gate.rs : 0, p.gate.cs, T, t, 0, D,
                         [&](int i, float w) { v[i] *= w; });
 #pragma unroll
     for (int i = 0; i < 8 * C; ++i) v[i] = p.x.data ? fmaf(p.scale, v[i], x[i]) : p.scale * v[i];
-    if (p.h.data) store_row<VEC, C>(p.h, TX, row, T, t, D, v);
+    if (p.h.data) store_row<VEC, C>(p.h, TX, row, T, t, 0, D, v);
     if (p.pre) {
         const float2 s = row_stats<VEC, C>(v, p.pre, p.eps, T, t, D, buffer, turn);
         stats.z = s.x;
         stats.w = s.y;
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) v[i] = (v[i] - s.x) * s.y;
-        with_vector<VEC, C>(p.pre_w.data, p.pre_w.type, 0, 1, T, t, D, [&](int i, float w) { v[i] *= w; });
-        with_vector<VEC, C>(p.pre_b.data, p.pre_b.type, 0, 1, T, t, D, [&](int i, float w) { v[i] += w; });
-        store_row<VEC, C>(p.n, TY, row, T, t, D, v);
+        with_vector<VEC, C>(p.pre_w.data, p.pre_w.type, 0, 1, T, t, 0, D, [&](int i, float w) { v[i] *= w; });
+        with_vector<VEC, C>(p.pre_b.data, p.pre_b.type, 0, 1, T, t, 0, D, [&](int i, float w) { v[i] += w; });
+        store_row<VEC, C>(p.n, TY, row, T, t, 0, D, v);
     }
     if (p.stats && t == 0) p.stats[row] = stats;
 }
@@ -286,69 +288,255 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_long_kernel(const __grid_cons
     if (p.stats && t == 0) p.stats[row] = stats;
 }
 
-// A CTA's rows are consecutive; it keeps its sums over them in shared memory
-// (each thread its own columns) and leaves them in `part`.  A gate row's sum is
-// done where all of its rows are the CTA's, else its share goes to gate_part.
+__device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest `left` groups of this thread have landed
+__device__ __forceinline__ void copies_wait(int left) {
+    if (left <= 0)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (left == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (left == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// Rows come to a thread through shared memory that only it uses: it copies its
+// own pieces of the next `depth` rows asynchronously, so that no barrier stands
+// between a copy and its use, and the copies of rows ahead run under the
+// reductions of this one.
+template <int TY, int TX, bool VEC, int C>
+struct RowQueue {
+    static constexpr int GY = TY == T_F32 ? 2 : 1, GX = TX == T_F32 ? 2 : 1;  // 16-byte pieces of 8 elements
+    const NormGradParams& g;
+    int T, t, base, depth, slot = 0;
+    uint32_t ring, unit;  // address of this thread's first piece; a row's bytes
+    long long next, end;
+
+    __device__ __forceinline__ void issue() {
+        uint32_t to = ring + slot * unit;
+        if (next < end) {
+            auto copy = [&](const Mat& m, int elem, int pieces) {
+                if (!m.data) return;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int col = base + norm_column<true>(T, t, 8 * c);
+                    if (col < g.f.D) {
+                        const char* from = static_cast<const char*>(m.data) + (next * m.rs + col) * elem;
+                        for (int k = 0; k < pieces; ++k) copy16_async(to + (c * pieces + k) * T * 16, from + 16 * k);
+                    }
+                }
+                to += C * pieces * T * 16;
+            };
+            copy(g.f.y, TY == T_F32 ? 4 : 2, GY);
+            copy(g.f.x, TX == T_F32 ? 4 : 2, GX);
+            copy(g.dh, TX == T_F32 ? 4 : 2, GX);
+            copy(g.dn, TY == T_F32 ? 4 : 2, GY);
+        }
+        ++next;
+        copies_commit();
+        slot = slot + 1 == depth ? 0 : slot + 1;
+    }
+    template <int TYPE>
+    __device__ __forceinline__ void take(const Mat& m, uint32_t& from, float (&v)[8 * C]) const {
+        constexpr int G = TYPE == T_F32 ? 2 : 1;
+        if (!m.data) return;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            Raw<TYPE> raw;
+#pragma unroll
+            for (int k = 0; k < G; ++k)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(raw.q[k].x), "=r"(raw.q[k].y), "=r"(raw.q[k].z), "=r"(raw.q[k].w)
+                             : "r"(from + (c * G + k) * T * 16)
+                             : "memory");
+            float w[8];
+            spread8<TYPE>(raw, w);
+            const bool there = base + norm_column<true>(T, t, 8 * c) < g.f.D;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[8 * c + e] = there ? w[e] : 0.f;
+        }
+        from += C * G * T * 16;
+    }
+    // the row's pieces into registers, and the copies of a row ahead on their way
+    __device__ __forceinline__ void row(long long r, float (&y)[8 * C], float (&x)[8 * C], float (&dh)[8 * C], float (&dn)[8 * C]) {
+        if (VEC && depth > 0) {
+            copies_wait(depth - 1);
+            uint32_t from = ring + slot * unit;
+            take<TY>(g.f.y, from, y);
+            take<TX>(g.f.x, from, x);
+            take<TX>(g.dh, from, dh);
+            take<TY>(g.dn, from, dn);
+            issue();
+            return;
+        }
+        load_row<TY, VEC, C>(g.f.y, r, T, t, base, g.f.D, y);
+        if (g.f.x.data) load_row<TX, VEC, C>(g.f.x, r, T, t, base, g.f.D, x);
+        if (g.dh.data) load_row<TX, VEC, C>(g.dh, r, T, t, base, g.f.D, dh);
+        if (g.dn.data) load_row<TY, VEC, C>(g.dn, r, T, t, base, g.f.D, dn);
+    }
+};
+
+// A row's sums over the CTAs of a cluster that share it, in their order.
+struct Shared {
+    float2 (*buffer)[32];
+    float2 (*meet)[8];
+    int T, t, parts, rank, turn;
+    __device__ __forceinline__ float2 sum(float a, float b) {
+        const int now = turn;
+        float2 s = row_sum(a, b, T, t, buffer, turn);
+        if (parts == 1) {
+            return s;
+        }
+        if (T == 32) turn ^= 1;
+        if (t < parts) {
+            const uint32_t to = map_to(smem_u32(&meet[now][rank]), t);
+            st_shared_cluster_u32(to, __float_as_uint(s.x));
+            st_shared_cluster_u32(to + 4, __float_as_uint(s.y));
+        }
+        cluster_sync();
+        s = make_float2(0.f, 0.f);
+        for (int k = 0; k < parts; ++k) {
+            s.x += meet[now][k].x;
+            s.y += meet[now][k].y;
+        }
+        return s;
+    }
+};
+
+// Sums over rows: element i of a thread, in registers (8 elements a thread: 40
+// numbers) or, two float4 per 8 elements, in shared memory that only it uses.
+template <int C>
+struct RowSums {
+    float v[C == 1 ? 5 : 1][C == 1 ? 8 : 1];
+    float4* at;
+    int T;
+    __device__ __forceinline__ void clear(int slots) {
+        if constexpr (C == 1) {
+#pragma unroll
+            for (int s = 0; s < 5; ++s)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
+        } else {
+            for (int s = 0; s < slots; ++s) zero(s, s);
+        }
+    }
+    __device__ __forceinline__ void zero(int which, int slot) {
+        if constexpr (C == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[which][i] = 0.f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2 * C; ++j) at[(slot * 2 * C + j) * T] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    // `which` names the sum (a constant), `slot` its place
+    __device__ __forceinline__ void add(int which, int slot, const float (&x)[8 * C]) {
+        if constexpr (C == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[which][i] += x[i];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2 * C; ++j) {
+                float4 f = at[(slot * 2 * C + j) * T];
+                f.x += x[4 * j];
+                f.y += x[4 * j + 1];
+                f.z += x[4 * j + 2];
+                f.w += x[4 * j + 3];
+                at[(slot * 2 * C + j) * T] = f;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int which, int slot, float (&x)[8 * C]) const {
+        if constexpr (C == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = v[which][i];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2 * C; ++j) {
+                const float4 f = at[(slot * 2 * C + j) * T];
+                x[4 * j] = f.x;
+                x[4 * j + 1] = f.y;
+                x[4 * j + 2] = f.z;
+                x[4 * j + 3] = f.w;
+            }
+        }
+    }
+};
+
+// The rows of a CTA, or of a cluster of `parts` CTAs that each take a part of a
+// row, are consecutive; the sums over them are left in `part`.  A gate row's sum
+// is done where all of its rows are the CTA's, else its share goes to gate_part.
 template <int TY, int TX, bool VEC, int C>
 __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_constant__ NormGradParams g) {
-    extern __shared__ float sums[];  // (slots [+ gate], elements of T threads), element i of thread t at i * T + t
-    __shared__ float2 buffer[2][32];
+    extern __shared__ float4 dynamic[];  // sums (C > 1), then the rows ahead
+    __shared__ float2 buffer[2][32], meet[2][8];
     const NormParams& p = g.f;
-    const int T = blockDim.x, t = threadIdx.x, D = p.D, all = 8 * C * T;
-    int turn = 0;
-    for (int i = t; i < (g.slots + g.gate_sums) * all; i += T) sums[i] = 0.f;
+    const int T = blockDim.x, t = threadIdx.x, D = p.D;
+    const int rank = g.parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int base = rank * T * 8 * C;
+    const long long cta = blockIdx.x / g.parts;
+    const long long begin = norm_row(p.M, g.ctas, cta), end = norm_row(p.M, g.ctas, cta + 1);
+    Shared shared{buffer, meet, T, t, g.parts, rank, 0};
+    const int all = g.slots + g.gate_sums;
+    RowSums<C> sums;
+    sums.at = dynamic + t;
+    sums.T = T;
+    sums.clear(all);
+    RowQueue<TY, TX, VEC, C> queue{g, T, t, base, g.depth, 0, 0u, g.row_bytes, begin, end};
+    queue.ring = smem_u32(dynamic + (C == 1 ? 0 : all * 2 * C * T) + t);
+    // every CTA of the cluster is there before another writes its shared memory
+    if (g.parts > 1) cluster_sync();
     grid_wait();
     grid_release();
-    float* const gate_sum = sums + g.slots * all;
+    if (VEC)
+        for (int i = 0; i < g.depth; ++i) queue.issue();
     auto add = [&](int which, const float (&v)[8 * C]) {
-        if (g.slot[which] < 0) return;
-        float* const to = sums + g.slot[which] * all + t;
-#pragma unroll
-        for (int i = 0; i < 8 * C; ++i) to[i * T] += v[i];
+        if (g.slot[which] >= 0) sums.add(which, g.slot[which], v);
     };
+    auto there = [&](int i) { return base + norm_column<VEC>(T, t, i) < D; };
     const float over_d = 1.f / D;
-    const long long begin = norm_row(p.M, g.ctas, blockIdx.x), end = norm_row(p.M, g.ctas, blockIdx.x + 1);
     for (long long row = begin; row < end; ++row) {
         float y[8 * C], h[8 * C], d[8 * C], e[8 * C];
-        load_row<TY, VEC, C>(p.y, row, T, t, D, y);
-        if (p.x.data) load_row<TX, VEC, C>(p.x, row, T, t, D, h);
-        if (g.dh.data) load_row<TX, VEC, C>(g.dh, row, T, t, D, d);
-        if (g.dn.data) load_row<TY, VEC, C>(g.dn, row, T, t, D, e);
         const float4 stats = p.stats[row];
+        queue.row(row, y, h, d, e);
         const long long gate_row = p.gate.data ? row / p.group_rows : 0;
         // y becomes yhat, u what the gate multiplies, h the sum
         float u[8 * C];
         if (p.post) {
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) y[i] = norm_column<VEC>(T, t, i) < D ? (y[i] - stats.x) * stats.y : 0.f;
+            for (int i = 0; i < 8 * C; ++i) y[i] = there(i) ? (y[i] - stats.x) * stats.y : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) u[i] = y[i];
         if (p.post) {
-            with_vector<VEC, C>(p.post_w.data, p.post_w.type, 0, 1, T, t, D, [&](int i, float w) { u[i] *= w; });
-            with_vector<VEC, C>(p.post_b.data, p.post_b.type, 0, 1, T, t, D, [&](int i, float w) { u[i] += w; });
+            with_vector<VEC, C>(p.post_w.data, p.post_w.type, 0, 1, T, t, base, D, [&](int i, float w) { u[i] *= w; });
+            with_vector<VEC, C>(p.post_b.data, p.post_b.type, 0, 1, T, t, base, D, [&](int i, float w) { u[i] += w; });
         }
         if (g.dn.data) {
             float v[8 * C];
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) v[i] = u[i];
-            with_vector<VEC, C>(p.gate.data, p.gate_type, gate_row * p.gate.rs, p.gate.cs, T, t, D, [&](int i, float w) { v[i] *= w; });
+            with_vector<VEC, C>(p.gate.data, p.gate_type, gate_row * p.gate.rs, p.gate.cs, T, t, base, D, [&](int i, float w) { v[i] *= w; });
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) {
                 h[i] = p.x.data ? fmaf(p.scale, v[i], h[i]) : p.scale * v[i];
-                h[i] = norm_column<VEC>(T, t, i) < D ? (h[i] - stats.z) * stats.w : 0.f;  // hhat
+                h[i] = there(i) ? (h[i] - stats.z) * stats.w : 0.f;  // hhat
                 v[i] = e[i] * h[i];
             }
             add(0, v);
             add(1, e);
-            with_vector<VEC, C>(p.pre_w.data, p.pre_w.type, 0, 1, T, t, D, [&](int i, float w) { e[i] *= w; });
+            with_vector<VEC, C>(p.pre_w.data, p.pre_w.type, 0, 1, T, t, base, D, [&](int i, float w) { e[i] *= w; });
             float a = 0.f, b = 0.f;
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) {
                 a = fmaf(e[i], h[i], a);
                 b += e[i];
             }
-            const float2 s = row_sum(a, b, T, t, buffer, turn);
+            const float2 s = shared.sum(a, b);
             const float m1 = s.x * over_d, m0 = p.pre == NORM_LAYER ? s.y * over_d : 0.f;
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) {
@@ -356,66 +544,71 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
                 d[i] = g.dh.data ? d[i] + v : v;
             }
         }
-        if (g.dx.data) store_row<VEC, C>(g.dx, TX, row, T, t, D, d);
+        if (g.dx.data) store_row<VEC, C>(g.dx, TX, row, T, t, base, D, d);
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) d[i] *= p.scale;
         if (p.gate.data) {
-            if (g.gate_sums) {
 #pragma unroll
-                for (int i = 0; i < 8 * C; ++i) gate_sum[i * T + t] += d[i] * u[i];
-            } else if (g.dgate.data) {
-#pragma unroll
-                for (int i = 0; i < 8 * C; ++i) u[i] *= d[i];
-                store_row<VEC, C>(g.dgate, p.gate_type, gate_row, T, t, D, u);
-            }
-            with_vector<VEC, C>(p.gate.data, p.gate_type, gate_row * p.gate.rs, p.gate.cs, T, t, D, [&](int i, float w) { d[i] *= w; });
+            for (int i = 0; i < 8 * C; ++i) u[i] *= d[i];
+            if (g.gate_sums)
+                sums.add(4, g.slots, u);
+            else if (g.dgate.data)
+                store_row<VEC, C>(g.dgate, p.gate_type, gate_row, T, t, base, D, u);
+            with_vector<VEC, C>(p.gate.data, p.gate_type, gate_row * p.gate.rs, p.gate.cs, T, t, base, D, [&](int i, float w) { d[i] *= w; });
         }
         if (p.post) {
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) {
-                d[i] = norm_column<VEC>(T, t, i) < D ? d[i] : 0.f;
+                d[i] = there(i) ? d[i] : 0.f;
                 u[i] = d[i] * y[i];
             }
             add(2, u);
             add(3, d);
-            with_vector<VEC, C>(p.post_w.data, p.post_w.type, 0, 1, T, t, D, [&](int i, float w) { d[i] *= w; });
+            with_vector<VEC, C>(p.post_w.data, p.post_w.type, 0, 1, T, t, base, D, [&](int i, float w) { d[i] *= w; });
             float a = 0.f, b = 0.f;
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) {
                 a = fmaf(d[i], y[i], a);
                 b += d[i];
             }
-            const float2 s = row_sum(a, b, T, t, buffer, turn);
+            const float2 s = shared.sum(a, b);
             const float m1 = s.x * over_d, m0 = p.post == NORM_LAYER ? s.y * over_d : 0.f;
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) d[i] = stats.y * (d[i] - y[i] * m1 - m0);
         }
-        if (g.dy.data) store_row<VEC, C>(g.dy, TY, row, T, t, D, d);
+        if (g.dy.data) store_row<VEC, C>(g.dy, TY, row, T, t, base, D, d);
         // the last row of a gate row, or of this CTA
         if (g.gate_sums && (row + 1 == end || (row + 1) % p.group_rows == 0)) {
             const bool begins = gate_row * p.group_rows >= begin, ends = (gate_row + 1) * p.group_rows <= end;
-            float* const to = g.gate_part + (static_cast<long long>(blockIdx.x) * 2 + begins) * D;
+            float* const to = g.gate_part + (cta * 2 + begins) * D;
+            sums.get(4, g.slots, u);
+            sums.zero(4, g.slots);
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) {
-                const int c = norm_column<VEC>(T, t, i);
-                if (c < D) {
-                    if (begins && ends)
-                        store_any(const_cast<void*>(g.dgate.data), p.gate_type, gate_row * g.dgate.rs + c * g.dgate.cs, gate_sum[i * T + t]);
-                    else
-                        to[c] = gate_sum[i * T + t];
-                }
-                gate_sum[i * T + t] = 0.f;
+                const int c = base + norm_column<VEC>(T, t, i);
+                if (c >= D) continue;
+                if (begins && ends)
+                    store_any(const_cast<void*>(g.dgate.data), p.gate_type, gate_row * g.dgate.rs + c * g.dgate.cs, u[i]);
+                else
+                    to[c] = u[i];
             }
         }
     }
-    for (int s = 0; s < g.slots; ++s) {
-        float* const to = g.part + (static_cast<long long>(blockIdx.x) * g.slots + s) * D;
+    if (VEC) copies_wait(0);
+#pragma unroll
+    for (int which = 0; which < 4; ++which) {
+        if (g.slot[which] < 0) continue;
+        float* const to = g.part + (cta * g.slots + g.slot[which]) * D;
+        float u[8 * C];
+        sums.get(which, g.slot[which], u);
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) {
-            const int c = norm_column<VEC>(T, t, i);
-            if (c < D) to[c] = sums[s * all + i * T + t];
+            const int c = base + norm_column<VEC>(T, t, i);
+            if (c < D) to[c] = u[i];
         }
     }
+    // no CTA leaves while another may write its shared memory
+    if (g.parts > 1) cluster_sync();
 }
 
 // Rows of any length; the sums are kept in `part` and gate_part themselves.

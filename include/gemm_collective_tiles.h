@@ -597,9 +597,9 @@ typedef enum {
  * residual may be out itself.
  *
  * Workspace: as the 8-bit products'.  Of the config, tile_m (128: 128 x 128
- * tiles, or the kernel of few rows; 256: pairs), tile_n (128 or 256: columns of a
- * pair's tile), k_split (1, 2, 4 or 8 CTAs of a cluster share a 128 x 128 tile's
- * contraction), group_m, grid, wait_ns and
+ * tiles; 256: pairs; 16, 32 or 64: the kernel for at most as many rows), tile_n
+ * (128 or 256: columns of a tile), k_split (1, 2, 4 or 8 CTAs of a cluster share
+ * a tile's contraction; not for pairs), group_m, grid, wait_ns and
  * debug_skip_flag apply.
  */
 typedef struct {

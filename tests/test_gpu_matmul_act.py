@@ -79,8 +79,18 @@ def test_integers_by_size(M, N, K, config):
 @pytest.mark.parametrize("M", [1, 2, 7, 15, 16, 17, 31, 32, 33, 48, 63, 64])
 @pytest.mark.parametrize("split", [1, 2, 4, 8])
 def test_few_rows(M, split):
-    check_ints(M, 392, 1024, config=dict(tile_m=128, k_split=split), z=True, p=0.5, seed=M)
-    check_ints(M, 136, 520, out_dtype=BF, config=dict(tile_m=128, k_split=split), layouts=("cols", "cols", "rows"), act="relu")
+    for tile_m in (16, 32, 64, 128):
+        if M <= tile_m:
+            config = dict(tile_m=tile_m, k_split=split)
+            check_ints(M, 392, 1024, config=config, z=True, p=0.5, seed=M)
+            check_ints(M, 136, 520, out_dtype=BF, config=config, layouts=("cols", "cols", "rows"), act="relu")
+            check_ints(M, 129, 300, dtype=HF, out_dtype=HF, config=config, layouts=("every other", "odd rows", "odd rows"))
+
+
+def test_few_rows_many_tiles():
+    """More tiles than CTAs run at once, whole and in parts."""
+    for tile_m, split in ((16, 1), (32, 2), (64, 1), (64, 4), (16, 8)):
+        check_ints(tile_m - 3, 42000, 256, config=dict(tile_m=tile_m, k_split=split), act="relu", z=True)
 
 
 @pytest.mark.parametrize("split", [2, 4, 8])
@@ -357,7 +367,8 @@ def test_layer_shapes_leaves_and_refusals():
 def test_waits_are_bounded():
     """A tile that never reports its accumulator: the call ends with an error that the host reads, and the next one runs."""
     A, B = torch.ones(300, 256, device="cuda").bfloat16(), torch.ones(256, 520, device="cuda").bfloat16()
-    for M, config in ((300, PAIR), (300, HALF), (300, CTA), (300, dict(tile_m=128, k_split=2)), (16, dict(tile_m=128))):
+    for M, config in ((300, PAIR), (300, HALF), (300, CTA), (300, dict(tile_m=128, k_split=2)), (16, dict(tile_m=16)),
+                      (16, dict(tile_m=32, k_split=2))):
         out, res = torch.empty(M, 520, device="cuda"), torch.ones(M, 520, device="cuda")
         ws = gct.matmul_act(A[:M], B, out, residual=res, config=config)
         assert gct.query_status(ws)[0] == 0
