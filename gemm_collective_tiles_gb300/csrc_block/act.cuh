@@ -98,6 +98,7 @@ __device__ __forceinline__ void apply_act(float (&v)[N], int act) {
 struct Drop {
     const long long* rng;  // seed, offset
     uint32_t least;        // 0: nothing is dropped
+    uint32_t limit;        // (least << 16) - 1: upper 16 bits are at least `least` where a word is above it
     float scale;           // 1 / (1 - least / 65536), or 0
 };
 struct DropKey {
@@ -130,24 +131,17 @@ __device__ __forceinline__ void philox8(const DropKey& key, uint32_t group, uint
     w[2] = c2;
     w[3] = c3;
 }
-__device__ __forceinline__ bool kept(const uint32_t (&w)[4], int lane, uint32_t least) {
-    return ((lane & 1) ? w[lane >> 1] >> 16 : w[lane >> 1] & 0xFFFFu) >= least;
+// by element 0 .. 7 of a group: even ones have the lower half of a word
+__device__ __forceinline__ bool kept(const uint32_t (&w)[4], int e, const Drop& d) {
+    return ((e & 1) ? w[e >> 1] : w[e >> 1] << 16) > d.limit;
 }
 // v[0..7] are the elements of one group; dropped ones become 0 whatever they were
 __device__ __forceinline__ void drop8(float* v, const Drop& d, const DropKey& key, uint32_t group, uint32_t row) {
     uint32_t w[4];
     philox8(key, group, row, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = kept(w, e, d.least) ? v[e] * d.scale : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = kept(w, e, d) ? v[e] * d.scale : 0.f;
 }
-__device__ __forceinline__ float drop1(float v, const Drop& d, const DropKey& key, long long row, long long col) {
-    uint32_t w[4];
-    philox8(key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row), w);
-    const int lane = static_cast<int>(col & 7);
-    const uint32_t pair = lane < 4 ? (lane < 2 ? w[0] : w[1]) : (lane < 6 ? w[2] : w[3]);
-    return ((lane & 1) ? pair >> 16 : pair & 0xFFFFu) >= d.least ? v * d.scale : 0.f;
-}
-
 __device__ __forceinline__ float load_any(const void* p, int type, long long i) {
     if (type == fp8::T_F32) return fp8::load_elem<fp8::T_F32>(p, i);
     return type == fp8::T_F16 ? fp8::load_elem<fp8::T_F16>(p, i) : fp8::load_elem<fp8::T_BF16>(p, i);

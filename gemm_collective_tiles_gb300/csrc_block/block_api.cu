@@ -57,6 +57,7 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 int set_drop(Drop& d, double p, const int64_t* rng) {
     if (!(p >= 0.0 && p <= 1.0)) return IRIS_EINVAL;
     d.least = static_cast<uint32_t>(std::nearbyint(p * 65536.0));
+    d.limit = static_cast<uint32_t>((static_cast<uint64_t>(d.least) << 16) - 1);
     d.scale = d.least == 65536u ? 0.f : static_cast<float>(65536.0 / (65536.0 - d.least));
     d.rng = reinterpret_cast<const long long*>(rng);
     if (d.least && !rng) return IRIS_EINVAL;
@@ -371,6 +372,7 @@ int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec) {
     p.scale = static_cast<float>(g->scale);
     p.eps = static_cast<float>(g->eps);
     p.stats = reinterpret_cast<float4*>(g->stats);
+    for (int& at : p.vec_at) at = -1;
     vec = D % 8 == 0 && rows16(g->y, M, D, ye) && rows16(g->x, M, D, xe) && rows16(g->h, M, D, xe) && rows16(g->n, M, D, ye) &&
           rows16(g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)) && aligned16(g->post_weight) && aligned16(g->post_bias) &&
           aligned16(g->weight) && aligned16(g->bias);
@@ -410,23 +412,53 @@ RowShape row_shape(int64_t D, int C) {
     return RowShape{static_cast<int>(std::min<int64_t>(NORM_MAX_T, round_up(cdiv(chunks, C), 32))), C};
 }
 
+constexpr size_t SM_SMEM = 226 * 1024;
+
+// What of `room` bytes the vectors (in fp32) and the rows ahead of a row's threads
+// take: vectors first, then up to 4 rows, where they lie on 16 bytes.
+size_t row_memory(NormParams& p, RowShape r, bool bias, size_t row_pieces, bool vec, size_t room) {
+    const size_t piece = static_cast<size_t>(r.C) * r.T * 16;
+    const void* all[5] = {p.post_w.data, p.post_b.data, p.pre_w.data, bias ? p.pre_b.data : nullptr, p.group_rows > 1 ? p.gate.data : nullptr};
+    int n = 0;
+    for (int i = 0; i < 5; ++i) p.vec_at[i] = all[i] ? n++ : -1;
+    p.vec_bytes = static_cast<unsigned>(n * 2 * piece);
+    if (p.vec_bytes > room) {
+        p.vec_bytes = 0;
+        for (int& at : p.vec_at) at = -1;
+    }
+    if (vec && p.gate.data && p.group_rows == 1) row_pieces += p.gate_type == T_F32 ? 2 : 1;
+    p.row_bytes = static_cast<unsigned>(row_pieces * piece);
+    p.depth = vec ? static_cast<int>(std::min<size_t>(4, (room - p.vec_bytes) / p.row_bytes)) : 0;
+    return p.vec_bytes + static_cast<size_t>(p.depth) * p.row_bytes;
+}
+
 template <int TY, int TX, bool VEC>
-int launch_norm_c(const NormParams& p, RowShape r, cudaStream_t stream) {
+int launch_norm_c(NormParams p, RowShape r, int sms, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     const int per = r.T == 32 ? 4 : 1;
-    cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(cdiv(p.M, per)), r.T, 0, 1, stream, attr);
+    // 1024 threads an SM, with up to 64 registers each
+    const int per_sm = std::max(1, 1024 / (r.T * per));
+    const int64_t ctas = std::min<int64_t>(cdiv(p.M, per), int64_t(sms) * per_sm);
+    size_t smem = 0;
+    if (ctas * per < p.M) {  // units of several rows
+        const int ys = TY == T_F32 ? 2 : 1, xs = TX == T_F32 ? 2 : 1;
+        smem = per * row_memory(p, r, true, ys + (p.x.data ? xs : 0), VEC, (SM_SMEM / per_sm - 2048) / per);
+    }
+    const auto kernel = r.C == 1 ? norm_kernel<TY, TX, VEC, 1> : r.C == 2 ? norm_kernel<TY, TX, VEC, 2> : norm_kernel<TY, TX, VEC, 4>;
+    const int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (rc) return rc;
+    cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(ctas), r.T, smem, 1, stream, attr);
     lc.blockDim = dim3(r.T, per);
-    return launch("norm launch", r.C == 1 ? norm_kernel<TY, TX, VEC, 1> : r.C == 2 ? norm_kernel<TY, TX, VEC, 2> : norm_kernel<TY, TX, VEC, 4>, lc, p);
+    return launch("norm launch", kernel, lc, p);
 }
 template <int TY, int TX>
-int launch_norm(const NormParams& p, bool vec, cudaStream_t stream) {
+int launch_norm(const NormParams& p, bool vec, int sms, cudaStream_t stream) {
     if (p.D > NORM_LONGEST) {
         cudaLaunchAttribute attr[2];
         return launch("norm launch", norm_long_kernel<TY, TX>, launch_config(static_cast<unsigned>(p.M), NORM_MAX_T, 0, 1, stream, attr), p);
     }
-    // few rows: more threads each, for the shortest way through; else more work a thread
-    const RowShape r = row_shape(p.D, p.M < 256 ? 1 : 4);
-    return vec ? launch_norm_c<TY, TX, true>(p, r, stream) : launch_norm_c<TY, TX, false>(p, r, stream);
+    const RowShape r = row_shape(p.D, 1);
+    return vec ? launch_norm_c<TY, TX, true>(p, r, sms, stream) : launch_norm_c<TY, TX, false>(p, r, sms, stream);
 }
 template <typename F>
 int by_types(int y, int x, F f) {
@@ -445,7 +477,6 @@ struct GradPlan {
     size_t smem, part, total;
 };
 constexpr int64_t NORM_GRAD_PART = NORM_MAX_T * NORM_GRAD_C * 8;  // elements of a row that a CTA takes
-constexpr size_t SM_SMEM = 226 * 1024;
 
 template <int TY, int TX, bool VEC>
 int launch_norm_grad_c(const NormGradParams& p, const GradPlan& pl, cudaStream_t stream) {
@@ -502,11 +533,10 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     const int per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
     const size_t pieces = static_cast<size_t>(pl.r.C) * pl.r.T * 16;
     const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pieces;
-    const size_t y_bytes = pieces * (ye / 2), x_bytes = pieces * (xe / 2);
-    p.row_bytes = static_cast<unsigned>(y_bytes + (f.x.data ? x_bytes : 0) + (g->dh.data ? x_bytes : 0) + (g->dn.data ? y_bytes : 0));
-    const size_t room = SM_SMEM / per_sm - 2048;
-    p.depth = vec && sums < room ? static_cast<int>(std::min<size_t>(4, (room - sums) / p.row_bytes)) : 0;
-    pl.smem = sums + p.depth * p.row_bytes;
+    const size_t room = SM_SMEM / per_sm - 2048, ys = ye / 2, xs = xe / 2;
+    pl.smem = sums;
+    if (sums < room)
+        pl.smem += row_memory(p.f, pl.r, false, ys + (f.x.data ? xs : 0) + (g->dh.data ? xs : 0) + (g->dn.data ? ys : 0), vec, room - sums);
     if (pl.smem > SM_SMEM - 2048) return IRIS_EUNSUPPORTED;
     pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
     pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
@@ -587,8 +617,7 @@ int iris_b200_dropout(const iris_b200_dropout_args* g, cudaStream_t stream) {
         (g->residual.data && (rc = check_in(&g->residual, M, N, e))))
         return rc;
     if (M == 0 || N == 0) return IRIS_OK;
-    const int64_t segs = cdiv(N, SEG), items = M * segs;
-    if (items > 0x7FFFFFFF) return IRIS_EINVAL;
+    const int64_t segs = cdiv(N, SEG);
     int sms;
     if ((rc = sm_count(&sms))) return rc;
     p.x = mat_of(g->x);
@@ -598,9 +627,11 @@ int iris_b200_dropout(const iris_b200_dropout_args* g, cudaStream_t stream) {
     p.N = static_cast<int>(N);
     p.type = g->dtype;
     p.segs = static_cast<unsigned>(segs);
-    p.items = static_cast<unsigned>(items);
+    // a CTA takes 8 rows' pieces, or, of more than 64 CTAs an SM, every row_step-th 8
+    const int64_t down = std::min<int64_t>(cdiv(M, 8), std::max<int64_t>(1, int64_t(sms) * 64 / segs));
+    p.row_step = down * 8;
     const bool vec = N % 8 == 0 && rows16(g->x, M, N, e) && rows16(g->out, M, N, e) && rows16(g->residual, M, N, e);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cdiv(items, 16), int64_t(sms) * 8));
+    const unsigned grid = static_cast<unsigned>(down * segs);
     if (g->dtype == IRIS_F32) return launch_dropout<T_F32>(p, vec, grid, stream);
     if (g->dtype == IRIS_F16) return launch_dropout<T_F16>(p, vec, grid, stream);
     return launch_dropout<T_BF16>(p, vec, grid, stream);
@@ -614,8 +645,10 @@ int iris_b200_norm_join(const iris_b200_norm_join_args* g, cudaStream_t stream) 
     if (rc) return rc;
     if ((g->pre != 0) != (g->n.data != nullptr) && g->M > 0 && g->D > 0) return IRIS_EINVAL;
     if (g->M == 0 || g->D == 0) return IRIS_OK;
+    int sms;
+    if (sm_count(&sms)) return IRIS_ECUDA;
     return by_types(g->y_dtype, g->x_dtype,
-                    [&](auto ty, auto tx) { return launch_norm<decltype(ty)::value, decltype(tx)::value>(p, vec, stream); });
+                    [&](auto ty, auto tx) { return launch_norm<decltype(ty)::value, decltype(tx)::value>(p, vec, sms, stream); });
 }
 int iris_b200_norm_join_grad_workspace_size(const iris_b200_norm_join_grad_args* args, const iris_b200_config*, size_t* bytes) {
     return bytes ? norm_grad(args, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;

@@ -25,7 +25,8 @@ struct DropParams {
     Mat x, residual, out;
     long long M;
     int N, type;
-    unsigned segs, items;  // pieces of a row, of all rows
+    unsigned segs;         // pieces of a row
+    long long row_step;    // rows that the grid takes at once
     Drop drop;
 };
 struct ActGradParams {
@@ -133,7 +134,7 @@ __device__ __forceinline__ void drop_piece(float (&v)[8], const Drop& d, const D
         uint32_t w[4], keep = 0;
         philox8(key, group, static_cast<uint32_t>(row), w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) keep |= static_cast<uint32_t>(kept(w, e, d.least)) << e;
+        for (int e = 0; e < 8; ++e) keep |= static_cast<uint32_t>(kept(w, e, d)) << e;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t bits = __shfl_sync(0xFFFFFFFFu, keep, e * 4 + (lane >> 3));
@@ -148,28 +149,17 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
     grid_wait();
     grid_release();
     const DropKey key = drop_key(p.drop);
-    constexpr int U = 2;  // pieces under way
-    const unsigned warps = gridDim.x * 8;
-    for (unsigned i = (blockIdx.x * 8 + (threadIdx.x >> 5)) * U; i < p.items; i += warps * U) {
-        float v[U][8], r[U][8];
+    const unsigned seg = blockIdx.x % p.segs;
+    for (long long row = blockIdx.x / p.segs * 8 + (threadIdx.x >> 5); row < p.M; row += p.row_step) {
+        float v[8], r[8];
+        load_piece<T, VEC>(p.x, row, seg, lane, p.N, v);
+        if (p.residual.data) load_piece<T, VEC>(p.residual, row, seg, lane, p.N, r);
+        if (p.drop.least) drop_piece<VEC>(v, p.drop, key, row, seg, lane);
+        if (p.residual.data) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i + k >= p.items) break;
-            const unsigned row = (i + k) / p.segs, seg = (i + k) % p.segs;
-            load_piece<T, VEC>(p.x, row, seg, lane, p.N, v[k]);
-            if (p.residual.data) load_piece<T, VEC>(p.residual, row, seg, lane, p.N, r[k]);
+            for (int e = 0; e < 8; ++e) v[e] += r[e];
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i + k >= p.items) break;
-            const unsigned row = (i + k) / p.segs, seg = (i + k) % p.segs;
-            if (p.drop.least) drop_piece<VEC>(v[k], p.drop, key, row, seg, lane);
-            if (p.residual.data) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[k][e] += r[k][e];
-            }
-            store_piece<VEC>(p.out, T, row, seg, lane, p.N, v[k]);
-        }
+        store_piece<VEC>(p.out, T, row, seg, lane, p.N, v);
     }
 }
 

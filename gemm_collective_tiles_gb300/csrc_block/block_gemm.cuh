@@ -119,7 +119,7 @@ struct Four {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t pair = (col & 4) ? w[2 + e / 2] : w[e / 2];
-                v[e] = ((e & 1) ? pair >> 16 : pair & 0xFFFFu) >= p.drop.least ? v[e] * p.drop.scale : 0.f;
+                v[e] = ((e & 1) ? pair : pair << 16) > p.drop.limit ? v[e] * p.drop.scale : 0.f;
             }
         }
         v[0] += res.x;
