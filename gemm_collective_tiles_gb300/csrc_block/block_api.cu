@@ -343,11 +343,13 @@ int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec) {
     if ((rc = check_in(&g->y, M, D, ye)) || (g->x.data && (rc = check_in(&g->x, M, D, xe))) ||
         (g->h.data && (rc = check_out(&g->h, M, D, xe))) || (g->n.data && (rc = check_out(&g->n, M, D, ye))))
         return rc;
-    p.group_rows = M;
+    p.group_rows = std::max<int64_t>(M, 1);
+    p.gate_rows = 1;
     if (g->gate.data) {
         if (g->gate_rows < 1 || g->gate_rows > std::max<int64_t>(M, 1) || M % g->gate_rows || !dtype_ok(g->gate_dtype)) return IRIS_EINVAL;
         if ((rc = check_in(&g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)))) return rc;
-        p.group_rows = M / g->gate_rows;
+        p.group_rows = std::max<int64_t>(M / g->gate_rows, 1);
+        p.gate_rows = g->gate_rows;
     }
     if (!g->post && (g->post_weight || g->post_bias)) return IRIS_EINVAL;
     if (!g->pre && (g->weight || g->bias)) return IRIS_EINVAL;
@@ -402,23 +404,23 @@ int allow_smem(const void* kernel, size_t bytes) {
     return IRIS_ECUDA;
 }
 
-// Threads T of a row at C chunks of 8 elements each.
+// Threads T of a row at 8 C elements each.
 struct RowShape {
     int T, C;
 };
-RowShape row_shape(int64_t D, int C) {
+RowShape row_shape(int64_t D, int C, int most) {
     const int64_t chunks = cdiv(D, 8);
-    while (C < NORM_MAX_C && cdiv(chunks, C) > NORM_MAX_T) C *= 2;
-    return RowShape{static_cast<int>(std::min<int64_t>(NORM_MAX_T, round_up(cdiv(chunks, C), 32))), C};
+    while (C < 2 && cdiv(chunks, C) > most) C *= 2;
+    return RowShape{static_cast<int>(std::min<int64_t>(most, round_up(cdiv(chunks, C), 32))), C};
 }
+constexpr size_t SM_SMEM = 222 * 1024;  // dynamic shared memory of an SM, beside the kernels' own
 
-constexpr size_t SM_SMEM = 226 * 1024;
-
-// What of `room` bytes the vectors (in fp32) and the rows ahead of a row's threads
-// take: vectors first, then up to 4 rows, where they lie on 16 bytes.
-size_t row_memory(NormParams& p, RowShape r, bool bias, size_t row_pieces, bool vec, size_t room) {
+// What of `room` bytes the vectors (in fp32) and the rows ahead of `groups` rows'
+// threads take: vectors first, then up to 4 rows each, where they lie on 16
+// bytes.  `pieces`: 16 bytes a thread and row, at C = 1.
+size_t row_memory(NormParams& p, RowShape r, int groups, bool bias, bool vec, int w, size_t pieces, size_t room) {
     const size_t piece = static_cast<size_t>(r.C) * r.T * 16;
-    const void* all[5] = {p.post_w.data, p.post_b.data, p.pre_w.data, bias ? p.pre_b.data : nullptr, p.group_rows > 1 ? p.gate.data : nullptr};
+    const void* all[5] = {p.post_w.data, p.post_b.data, p.pre_w.data, bias ? p.pre_b.data : nullptr, p.gate_rows == 1 ? p.gate.data : nullptr};
     int n = 0;
     for (int i = 0; i < 5; ++i) p.vec_at[i] = all[i] ? n++ : -1;
     p.vec_bytes = static_cast<unsigned>(n * 2 * piece);
@@ -426,29 +428,36 @@ size_t row_memory(NormParams& p, RowShape r, bool bias, size_t row_pieces, bool 
         p.vec_bytes = 0;
         for (int& at : p.vec_at) at = -1;
     }
-    if (vec && p.gate.data && p.group_rows == 1) row_pieces += p.gate_type == T_F32 ? 2 : 1;
-    p.row_bytes = static_cast<unsigned>(row_pieces * piece);
-    p.depth = vec ? static_cast<int>(std::min<size_t>(4, (room - p.vec_bytes) / p.row_bytes)) : 0;
-    return p.vec_bytes + static_cast<size_t>(p.depth) * p.row_bytes;
+    if (p.gate.data && p.gate_rows > 1) pieces += w == 4 || p.gate_type == T_F32 ? 2 : 1;
+    p.row_bytes = static_cast<unsigned>(pieces * piece);
+    p.depth = vec ? static_cast<int>(std::min<size_t>(4, (room - p.vec_bytes) / (groups * static_cast<size_t>(p.row_bytes)))) : 0;
+    return p.vec_bytes + static_cast<size_t>(groups) * p.depth * p.row_bytes;
 }
+// pieces of 16 bytes that 8 elements take
+constexpr int pieces_of(int type, int w) { return w == 4 || type == T_F32 ? 2 : 1; }
 
-template <int TY, int TX, bool VEC>
-int launch_norm_c(NormParams p, RowShape r, int sms, cudaStream_t stream) {
+template <int TY, int TX, int W>
+int launch_norm_w(NormParams p, bool vec, int sms, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
-    const int per = r.T == 32 ? 4 : 1;
-    // 1024 threads an SM, with up to 64 registers each
-    const int per_sm = std::max(1, 1024 / (r.T * per));
-    const int64_t ctas = std::min<int64_t>(cdiv(p.M, per), int64_t(sms) * per_sm);
+    constexpr int w = TX == T_F32 ? 4 : 8;
+    // Few rows: the more threads a row the shorter its way; many: work for a thread
+    // between two reductions
+    const RowShape r = row_shape(p.D, p.M < 2 * sms ? 1 : 2, NORM_CTA);
+    // 512 threads an SM have registers enough for rows that come through shared
+    // memory (16384 x 4096, 32-bit residual: 129 us, with 1024 threads 186); loads that
+    // threads wait for want more of them (1537 x 5003: 55 us, 94 with 512)
+    const int threads = W && r.T <= NORM_MAX_T ? NORM_MAX_T : NORM_CTA;
+    const int groups = static_cast<int>(std::min<int64_t>(std::min(16, threads / r.T), cdiv(p.M, sms)));
+    const int64_t ctas = std::min<int64_t>(cdiv(p.M, groups), sms);
     size_t smem = 0;
-    if (ctas * per < p.M) {  // units of several rows
-        const int ys = TY == T_F32 ? 2 : 1, xs = TX == T_F32 ? 2 : 1;
-        smem = per * row_memory(p, r, true, ys + (p.x.data ? xs : 0), VEC, (SM_SMEM / per_sm - 2048) / per);
-    }
-    const auto kernel = r.C == 1 ? norm_kernel<TY, TX, VEC, 1> : r.C == 2 ? norm_kernel<TY, TX, VEC, 2> : norm_kernel<TY, TX, VEC, 4>;
+    if (ctas * groups < p.M)  // several rows for a group
+        smem = row_memory(p, r, groups, true, vec, w, pieces_of(TY, w) + (p.x.data ? pieces_of(TX, w) : 0), SM_SMEM);
+    auto kernel = r.C == 1 ? norm_kernel<TY, TX, W, 1, NORM_CTA> : norm_kernel<TY, TX, W, 2, NORM_CTA>;
+    if (W && threads == NORM_MAX_T) kernel = r.C == 1 ? norm_kernel<TY, TX, W, 1, W ? NORM_MAX_T : NORM_CTA> : norm_kernel<TY, TX, W, 2, W ? NORM_MAX_T : NORM_CTA>;
     const int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem);
     if (rc) return rc;
     cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(ctas), r.T, smem, 1, stream, attr);
-    lc.blockDim = dim3(r.T, per);
+    lc.blockDim = dim3(r.T, groups);
     return launch("norm launch", kernel, lc, p);
 }
 template <int TY, int TX>
@@ -457,8 +466,7 @@ int launch_norm(const NormParams& p, bool vec, int sms, cudaStream_t stream) {
         cudaLaunchAttribute attr[2];
         return launch("norm launch", norm_long_kernel<TY, TX>, launch_config(static_cast<unsigned>(p.M), NORM_MAX_T, 0, 1, stream, attr), p);
     }
-    const RowShape r = row_shape(p.D, 1);
-    return vec ? launch_norm_c<TY, TX, true>(p, r, sms, stream) : launch_norm_c<TY, TX, false>(p, r, sms, stream);
+    return vec ? launch_norm_w<TY, TX, TX == T_F32 ? 4 : 8>(p, true, sms, stream) : launch_norm_w<TY, TX, 0>(p, false, sms, stream);
 }
 template <typename F>
 int by_types(int y, int x, F f) {
@@ -476,12 +484,10 @@ struct GradPlan {
     int64_t ctas;
     size_t smem, part, total;
 };
-constexpr int64_t NORM_GRAD_PART = NORM_MAX_T * NORM_GRAD_C * 8;  // elements of a row that a CTA takes
-
-template <int TY, int TX, bool VEC>
-int launch_norm_grad_c(const NormGradParams& p, const GradPlan& pl, cudaStream_t stream) {
+template <int TY, int TX, int W>
+int launch_norm_grad_w(const NormGradParams& p, const GradPlan& pl, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
-    const auto kernel = pl.r.C == 1 ? norm_grad_kernel<TY, TX, VEC, 1> : norm_grad_kernel<TY, TX, VEC, 2>;
+    const auto kernel = pl.r.C == 1 ? norm_grad_kernel<TY, TX, W, 1> : norm_grad_kernel<TY, TX, W, 2>;
     const int rc = allow_smem(reinterpret_cast<const void*>(kernel), pl.smem);
     return rc ? rc : launch("norm gradient launch", kernel, launch_config(static_cast<unsigned>(pl.ctas * p.parts), pl.r.T, pl.smem, p.parts, stream, attr), p);
 }
@@ -525,19 +531,20 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     if ((rc = sm_count(&sms))) return rc;
     GradPlan pl;
     // A row to a CTA, or, where it is too long for one's registers, to a cluster.
-    pl.in_registers = D <= 8 * NORM_GRAD_PART;
+    pl.in_registers = D <= 8 * NORM_GRAD_LONGEST;
     p.parts = 1;
-    while (pl.in_registers && p.parts * NORM_GRAD_PART < D) p.parts *= 2;
-    pl.r = row_shape(cdiv(D, p.parts), 1);
+    while (pl.in_registers && p.parts * NORM_GRAD_LONGEST < D) p.parts *= 2;
+    pl.r = row_shape(cdiv(D, p.parts), 1, NORM_MAX_T);
     // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
     const int per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
     const size_t pieces = static_cast<size_t>(pl.r.C) * pl.r.T * 16;
     const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pieces;
-    const size_t room = SM_SMEM / per_sm - 2048, ys = ye / 2, xs = xe / 2;
+    const int w = f.x_dtype == IRIS_F32 ? 4 : 8, ys = pieces_of(f.y_dtype, w), xs = pieces_of(f.x_dtype, w);
+    const size_t room = SM_SMEM / per_sm - 1024;
     pl.smem = sums;
     if (sums < room)
-        pl.smem += row_memory(p.f, pl.r, false, ys + (f.x.data ? xs : 0) + (g->dh.data ? xs : 0) + (g->dn.data ? ys : 0), vec, room - sums);
-    if (pl.smem > SM_SMEM - 2048) return IRIS_EUNSUPPORTED;
+        pl.smem += row_memory(p.f, pl.r, 1, false, vec, w, ys + (f.x.data ? xs : 0) + (g->dh.data ? xs : 0) + (g->dn.data ? ys : 0), room - sums);
+    if (pl.smem > SM_SMEM) return IRIS_EUNSUPPORTED;
     pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
     pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
     pl.total = WS_HEADER + pl.part + (p.gate_sums ? static_cast<size_t>(pl.ctas) * 2 * D * 4 : 0);
@@ -562,7 +569,7 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
         rc = by_types(f.y_dtype, f.x_dtype, [&](auto ty, auto tx) {
             constexpr int TY = decltype(ty)::value, TX = decltype(tx)::value;
             if (pl.in_registers)
-                return vec ? launch_norm_grad_c<TY, TX, true>(p, pl, stream) : launch_norm_grad_c<TY, TX, false>(p, pl, stream);
+                return vec ? launch_norm_grad_w<TY, TX, TX == T_F32 ? 4 : 8>(p, pl, stream) : launch_norm_grad_w<TY, TX, 0>(p, pl, stream);
             cudaLaunchAttribute attr[2];
             return launch("norm gradient launch", norm_grad_long_kernel<TY, TX>,
                           launch_config(static_cast<unsigned>(pl.ctas), NORM_MAX_T, 0, 1, stream, attr), p);

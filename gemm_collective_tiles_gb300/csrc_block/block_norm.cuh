@@ -24,9 +24,9 @@ namespace gct {
 namespace block {
 
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
-constexpr int NORM_MAX_T = 512, NORM_MAX_C = 4;
-constexpr int NORM_LONGEST = NORM_MAX_T * NORM_MAX_C * 8;  // elements of a row in registers
-constexpr int NORM_GRAD_C = 2;                             // of the gradient, whose long rows are shared by a cluster
+constexpr int NORM_MAX_T = 512;                          // threads of a row, in the gradient
+constexpr int NORM_CTA = 1024;                           // of a CTA, and of a row
+constexpr int NORM_LONGEST = NORM_CTA * 2 * 8, NORM_GRAD_LONGEST = NORM_MAX_T * 2 * 8;  // elements of a row in registers
 
 struct Vec {
     const void* data;
@@ -36,7 +36,7 @@ struct NormParams {
     Mat y, x, gate, h, n;
     Vec post_w, post_b, pre_w, pre_b;
     int gate_type;
-    long long M, group_rows;  // rows of y per row of gate
+    long long M, group_rows, gate_rows;  // rows of y per row of gate
     int D, post, pre;
     float scale, eps;
     float4* stats;            // per row: mean and r of y, mean and r of h; may be absent
@@ -72,136 +72,199 @@ struct NormFinishParams {
 // first row of CTA c
 __host__ __device__ __forceinline__ long long norm_row(long long M, long long ctas, long long c) { return M * c / ctas; }
 
-// column of a thread's element i, in the CTA's part of the row
-template <bool VEC>
+// The layout of a row over its T threads, 8 C elements each: W > 0: pieces of W
+// neighbouring elements, one piece of every thread after another (8 where all
+// tensors are of 16 bits, 4 beside f32: 16 bytes of the wider type, so that a
+// warp's access is one run of memory); W = 0: one element in T, any strides.
+template <int W>
 __device__ __forceinline__ int norm_column(int T, int t, int i) {
-    return VEC ? ((i >> 3) * T + t) * 8 + (i & 7) : i * T + t;
+    return W ? (i / (W ? W : 1) * T + t) * W + i % (W ? W : 1) : i * T + t;
 }
-template <int TYPE, bool VEC, int C>
-__device__ __forceinline__ void load_row(const Mat& m, long long row, int T, int t, int base, int D, float (&v)[8 * C]) {
-    const long long o = row * m.rs;
-    if constexpr (VEC) {
-        Raw<TYPE> raw[C];
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+    return q;
+}
+__device__ __forceinline__ uint2 shared_8(uint32_t at) {
+    uint2 q;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "r"(at) : "memory");
+    return q;
+}
+__device__ __forceinline__ void shared16(uint32_t at, const uint4& q) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
+}
+// W elements of a type, as they lie in memory
+template <int TYPE, int W>
+struct Bits {
+    static constexpr int WORDS = W * (TYPE == T_F32 ? 4 : 2) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const void* p) {
+        if constexpr (WORDS == 2) {
+            const uint2 q = *static_cast<const uint2*>(p);
+            w[0] = q.x;
+            w[1] = q.y;
+        } else {
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (base + norm_column<true>(T, t, 8 * c) < D) raw[c] = load8<TYPE>(m.data, o + base + norm_column<true>(T, t, 8 * c));
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            float w[8];
-            if (base + norm_column<true>(T, t, 8 * c) < D) {
-                spread8<TYPE>(raw[c], w);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * c + e] = w[e];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8 * C; ++i) {
-            const int c = base + norm_column<false>(T, t, i);
-            v[i] = c < D ? load_elem<TYPE>(m.data, o + c * m.cs) : 0.f;
+            for (int k = 0; k < WORDS / 4; ++k) put(k, static_cast<const uint4*>(p)[k]);
         }
     }
-}
-template <bool VEC, int C>
-__device__ __forceinline__ void store_row(const Mat& m, int type, long long row, int T, int t, int base, int D,
-                                          const float (&v)[8 * C]) {
-    void* const to = const_cast<void*>(m.data);
-    const long long o = row * m.rs;
-    if constexpr (VEC) {
+    // from shared memory, 16 bytes `apart`
+    __device__ __forceinline__ void load_shared(uint32_t at, uint32_t apart) {
+        if constexpr (WORDS == 2) {
+            const uint2 q = shared_8(at);
+            w[0] = q.x;
+            w[1] = q.y;
+        } else {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int at = base + norm_column<true>(T, t, 8 * c);
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = v[8 * c + e];
-            if (at < D) store8(to, type, o + at, w);
+            for (int k = 0; k < WORDS / 4; ++k) put(k, shared16(at + k * apart));
         }
+    }
+    __device__ __forceinline__ void put(int k, const uint4& q) {
+        w[4 * k] = q.x;
+        w[4 * k + 1] = q.y;
+        w[4 * k + 2] = q.z;
+        w[4 * k + 3] = q.w;
+    }
+    __device__ __forceinline__ void spread(float* v) const {
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) {
+            if (TYPE == T_F32)
+                v[k] = __uint_as_float(w[k]);
+            else
+                unpack16<TYPE>(w[k], v[2 * k], v[2 * k + 1]);
+        }
+    }
+};
+template <int TYPE, int W>
+__device__ __forceinline__ void store_bits(char* to, const float* v) {
+    if constexpr (TYPE == T_F32) {
+#pragma unroll
+        for (int k = 0; k < W / 4; ++k) reinterpret_cast<float4*>(to)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    } else if constexpr (W == 4) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack16(v[0], v[1], TYPE == T_BF16), pack16(v[2], v[3], TYPE == T_BF16));
     } else {
+        constexpr int bf = TYPE == T_BF16;
+        *reinterpret_cast<uint4*>(to) = make_uint4(pack16(v[0], v[1], bf), pack16(v[2], v[3], bf), pack16(v[4], v[5], bf), pack16(v[6], v[7], bf));
+    }
+}
+template <int TYPE, int W, int C>
+__device__ __forceinline__ void load_row(const Mat& m, long long row, int T, int t, int base, int D, float (&v)[8 * C]) {
+    const long long o = row * m.rs;
+    if constexpr (W > 0) {
+        constexpr int P = 8 * C / W, E = TYPE == T_F32 ? 4 : 2;
+        Bits<TYPE, W> raw[P];
 #pragma unroll
-        for (int i = 0; i < 8 * C; ++i) {
-            const int c = base + norm_column<false>(T, t, i);
-            if (c < D) store_any(to, type, o + c * m.cs, v[i]);
+        for (int k = 0; k < P; ++k) {
+            const int c = base + norm_column<W>(T, t, W * k);
+            if (c < D) {
+                raw[k].load(static_cast<const char*>(m.data) + (o + c) * E);
+            } else {
+#pragma unroll
+                for (int j = 0; j < Bits<TYPE, W>::WORDS; ++j) raw[k].w[j] = 0u;
+            }
         }
+#pragma unroll
+        for (int k = 0; k < P; ++k) raw[k].spread(v + W * k);
+    } else {
+        constexpr int E = TYPE == T_F32 ? 4 : 2;
+        const char* at = static_cast<const char*>(m.data) + (o + (base + t) * m.cs) * E;
+        const long long step = T * m.cs * E;
+        int left = D - base - t;
+#pragma unroll
+        for (int i = 0; i < 8 * C; ++i, at += step, left -= T) v[i] = left > 0 ? load_elem<TYPE>(at, 0) : 0.f;
     }
 }
 // f(i, value) for this thread's elements of a vector or of a row of gate
-template <bool VEC, int C, typename F>
+template <int W, int C, typename F>
 __device__ __forceinline__ void with_vector(const void* data, int type, long long o, long long cs, int T, int t, int base, int D, F f) {
     if (!data) return;
+    auto typed = [&](auto tag) {
+        constexpr int TYPE = decltype(tag)::value, E = TYPE == T_F32 ? 4 : 2;
+        if constexpr (W > 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        if (VEC) {
-            const int at = base + norm_column<true>(T, t, 8 * c);
-            if (at >= D) continue;
-            float w[8];
-            if (type == T_F32)
-                spread8<T_F32>(load8<T_F32>(data, o + at), w);
-            else if (type == T_F16)
-                spread8<T_F16>(load8<T_F16>(data, o + at), w);
-            else
-                spread8<T_BF16>(load8<T_BF16>(data, o + at), w);
+            for (int k = 0; k < 8 * C / W; ++k) {
+                const int at = base + norm_column<W>(T, t, W * k);
+                if (at >= D) continue;
+                Bits<TYPE, W> raw;
+                raw.load(static_cast<const char*>(data) + (o + at) * E);
+                float w[W];
+                raw.spread(w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f(8 * c + e, w[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int at = base + norm_column<false>(T, t, 8 * c + e);
-                if (at < D) f(8 * c + e, load_any(data, type, o + at * cs));
+                for (int e = 0; e < W; ++e) f(W * k + e, w[e]);
             }
+        } else {
+            const char* at = static_cast<const char*>(data) + (o + (base + t) * cs) * E;
+            const long long step = T * cs * E;
+            int left = D - base - t;
+#pragma unroll
+            for (int i = 0; i < 8 * C; ++i, at += step, left -= T)
+                if (left > 0) f(i, load_elem<TYPE>(at, 0));
         }
-    }
+    };
+    if (type == T_F32)
+        typed(std::integral_constant<int, T_F32>());
+    else if (type == T_F16)
+        typed(std::integral_constant<int, T_F16>());
+    else
+        typed(std::integral_constant<int, T_BF16>());
 }
-// Sums of one or two values over a row's T threads (a whole number of warps, 16
-// at most).  `turn` alternates between two buffers, so that one barrier a
-// reduction is enough; every warp adds the warps' sums up for itself.
-template <bool TWO>
-__device__ __forceinline__ float2 row_sum(float a, float b, int T, int t, float2 (*buffer)[16], int& turn) {
+// Sums of one or two values over a row's T threads (a whole number of warps, 32
+// at most), which are group `id` of the CTA.  `turn` alternates between two
+// buffers, so that one barrier a reduction is enough; every warp adds the warps'
+// sums up for itself.
+struct RowGroup {
+    int T, t, id, turn;
+    float2 (*buffer)[32];  // by warp of the CTA
+    template <bool TWO>
+    __device__ __forceinline__ float2 sum(float a, float b) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        if (TWO) b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    }
-    if (T == 32) return make_float2(a, b);
-    if ((t & 31) == 0) buffer[turn][t >> 5] = make_float2(a, b);
-    __syncthreads();
-    const int w = t & 15;
-    float2 s = buffer[turn][w];
-    if (w * 32 >= T) s = make_float2(0.f, 0.f);
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            if (TWO) b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        }
+        if (T == 32) return make_float2(a, b);
+        float2* const mine = buffer[turn] + id * (T >> 5);
+        if ((t & 31) == 0) mine[t >> 5] = make_float2(a, b);
+        asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(T) : "memory");
+        const int w = t & 31;
+        float2 s = make_float2(0.f, 0.f);
+        if (w * 32 < T) s = mine[w];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
-        if (TWO) s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+            if (TWO) s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+        }
+        turn ^= 1;
+        return s;
     }
-    turn ^= 1;
-    return s;
-}
+};
 // Mean and r of the values; those past the row's end are 0 and left out.
-template <bool VEC, int C>
-__device__ __forceinline__ float2 row_stats(const float (&v)[8 * C], int kind, float eps, float over_d, int T, int t, int D,
-                                            float2 (*buffer)[16], int& turn) {
+template <int W, int C>
+__device__ __forceinline__ float2 row_stats(const float (&v)[8 * C], int kind, float eps, float over_d, int D, RowGroup& group) {
     float s = 0.f;
     if (kind == NORM_RMS) {
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) s = fmaf(v[i], v[i], s);
-        return make_float2(0.f, rsqrtf(fmaf(row_sum<false>(s, 0.f, T, t, buffer, turn).x, over_d, eps)));
+        return make_float2(0.f, rsqrtf(fmaf(group.sum<false>(s, 0.f).x, over_d, eps)));
     }
 #pragma unroll
     for (int i = 0; i < 8 * C; ++i) s += v[i];
-    const float mean = row_sum<false>(s, 0.f, T, t, buffer, turn).x * over_d;
+    const float mean = group.sum<false>(s, 0.f).x * over_d;
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8 * C; ++i) {
-        const float d = norm_column<VEC>(T, t, VEC ? i & ~7 : i) < D ? v[i] - mean : 0.f;
+        const float d = norm_column<W>(group.T, group.t, W ? i / (W ? W : 1) * W : i) < D ? v[i] - mean : 0.f;
         s = fmaf(d, d, s);
     }
-    return make_float2(mean, rsqrtf(fmaf(row_sum<false>(s, 0.f, T, t, buffer, turn).x, over_d, eps)));
+    return make_float2(mean, rsqrtf(fmaf(group.sum<false>(s, 0.f).x, over_d, eps)));
 }
 
-__device__ __forceinline__ void copy16_async(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the newest `left` groups of this thread have landed
@@ -215,78 +278,61 @@ __device__ __forceinline__ void copies_wait(int left) {
     else
         asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
-__device__ __forceinline__ uint4 shared16(uint32_t at) {
-    uint4 q;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
-    return q;
-}
-__device__ __forceinline__ void shared16(uint32_t at, const uint4& q) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
-}
-// 8 elements of a piece in shared memory, whose second 16 bytes (f32) lie `apart` further on
-template <int TYPE>
-__device__ __forceinline__ void shared8(uint32_t at, uint32_t apart, float (&w)[8]) {
-    Raw<TYPE> raw;
-    raw.q[0] = shared16(at);
-    if (TYPE == T_F32) raw.q[TYPE == T_F32 ? 1 : 0] = shared16(at + apart);
-    spread8<TYPE>(raw, w);
-}
 
-// One of the tensors whose rows come ahead: where this thread's next piece lies,
-// and the bytes to the row after.  `type` decides the pieces' size.
-struct Ahead {
-    const char* at;
-    long long step;
-    int pieces;  // of 16 bytes per 8 elements; 0: not there
-    __device__ __forceinline__ void start(const Mat& m, int type, long long row, int col) {
-        const int elem = type == T_F32 ? 4 : 2;
-        pieces = m.data ? elem / 2 : 0;
-        at = static_cast<const char*>(m.data) + (row * m.rs + col) * elem;
-        step = m.rs * elem;
+// The gate's row for a row of y, kept up row by row.
+struct GateRow {
+    long long row, left, rows;
+    __device__ __forceinline__ GateRow(long long first, long long group_rows) : row(first / group_rows), rows(group_rows) {
+        left = (row + 1) * group_rows - first;
+    }
+    __device__ __forceinline__ bool next() {  // whether the gate's row is another one now
+        if (--left) return false;
+        ++row;
+        left = rows;
+        return true;
     }
 };
 
-// The threads of a row, and the shared memory that each of them has to itself:
-// its elements of the vectors, in fp32, and its pieces of the next rows, which it
-// copies asynchronously.  No barrier stands between a copy and its use, and the
-// copies run under the reductions of the rows before.
-template <bool VEC, int C>
-struct RowThreads {
+// What a row's threads have of shared memory.  The vectors (post_w, post_b,
+// pre_w, pre_b, and a gate of one row) lie there in fp32, for all of a CTA's rows.
+// Each thread has its pieces of the next rows to itself, which it copies
+// asynchronously: no barrier stands between a copy and its use, and the copies
+// run under the reductions of the rows before.  A gate of several rows comes
+// with the rows.
+template <int W, int C>
+struct RowMemory {
     int T, t, base, D;     // base: first column of the CTA's part of the row
     uint32_t cache, ring;  // this thread's
     uint32_t bytes;        // of a row ahead
     int depth, slot, left; // rows ahead (0: none), the next one's place, rows not yet copied
+    uint32_t to;           // where the row under copy goes on
 
     __device__ __forceinline__ uint32_t apart() const { return T * 16; }
-    __device__ __forceinline__ bool chunk_there(int c) const { return base + norm_column<true>(T, t, 8 * c) < D; }
-    __device__ __forceinline__ bool there(int i) const { return base + norm_column<VEC>(T, t, VEC ? i & ~7 : i) < D; }
-    // a vector, or a gate's row, into shared memory; zeros past its end
-    __device__ __forceinline__ void keep(int slot, const void* data, int type, long long o, long long cs) const {
-        if (!data || slot < 0) return;
-        const uint32_t to = cache + slot * (2 * C) * apart();
+    __device__ __forceinline__ int column(int i) const { return base + norm_column<W>(T, t, i); }
+    __device__ __forceinline__ bool there(int i) const { return column(W ? i / (W ? W : 1) * W : i) < D; }
+    // a vector into shared memory; zeros past its end
+    __device__ __forceinline__ void keep(int at, const Vec& v, long long cs) const {
+        if (!v.data || at < 0) return;
+        float w[8 * C];
 #pragma unroll
-        for (int j = 0; j < 2 * C; ++j) {
-            float w[4];
+        for (int i = 0; i < 8 * C; ++i) w[i] = 0.f;
+        with_vector<W, C>(v.data, v.type, 0, cs, T, t, base, D, [&](int i, float x) { w[i] = x; });
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int at = base + norm_column<VEC>(T, t, 4 * j + e);
-                w[e] = at < D ? load_any(data, type, o + at * cs) : 0.f;
-            }
-            shared16(to + j * apart(), make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]), __float_as_uint(w[3])));
-        }
+        for (int j = 0; j < 2 * C; ++j)
+            shared16(cache + (at * 2 * C + j) * apart(), make_uint4(__float_as_uint(w[4 * j]), __float_as_uint(w[4 * j + 1]),
+                                                                    __float_as_uint(w[4 * j + 2]), __float_as_uint(w[4 * j + 3])));
     }
-    // f(i, value) for this thread's elements of a vector or a gate's row
+    // f(i, value) for this thread's elements of a vector
     template <typename F>
-    __device__ __forceinline__ void each(int slot, const void* data, int type, long long o, long long cs, F f) const {
-        if (!data) return;
-        if (slot < 0) {
-            with_vector<VEC, C>(data, type, o, cs, T, t, base, D, f);
+    __device__ __forceinline__ void each(int at, const Vec& v, F f, long long cs = 1) const {
+        if (!v.data) return;
+        if (at < 0) {
+            with_vector<W, C>(v.data, v.type, 0, cs, T, t, base, D, f);
             return;
         }
-        const uint32_t from = cache + slot * (2 * C) * apart();
 #pragma unroll
         for (int j = 0; j < 2 * C; ++j) {
-            const uint4 q = shared16(from + j * apart());
+            const uint4 q = shared16(cache + (at * 2 * C + j) * apart());
             f(4 * j, __uint_as_float(q.x));
             f(4 * j + 1, __uint_as_float(q.y));
             f(4 * j + 2, __uint_as_float(q.z));
@@ -295,200 +341,228 @@ struct RowThreads {
     }
     // threads past a row's end find zeros
     __device__ __forceinline__ void clear() const {
-        if constexpr (VEC) {
-            bool all = true;
-#pragma unroll
-            for (int c = 0; c < C; ++c) all = all && chunk_there(c);
-            if (!all)
+        if constexpr (W > 0) {
+            if (!there(8 * C - 1))
                 for (uint32_t at = 0; at < depth * bytes; at += apart()) shared16(ring + at, make_uint4(0u, 0u, 0u, 0u));
         }
     }
-    // a row of N tensors on its way
-    template <int N>
-    __device__ __forceinline__ void issue(Ahead (&a)[N]) {
-        if (left > 0) {
-            uint32_t to = ring + slot * bytes;
+    // Pieces lie T * 16 bytes apart, whatever their size.
+    template <int TYPE>
+    __device__ __forceinline__ void copy(const char* from) {
+        constexpr int B = W * (TYPE == T_F32 ? 4 : 2);
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                if (a[k].pieces) {
+        for (int k = 0; k < 8 * C / (W ? W : 1); ++k) {
+            if (there(W * k)) {
+                const char* at = from + static_cast<long long>(k) * T * B;
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        if (chunk_there(c)) {
-                            const char* from = a[k].at + static_cast<long long>(c) * T * 16 * a[k].pieces;
-                            copy16_async(to, from);
-                            if (a[k].pieces == 2) copy16_async(to + apart(), from + 16);
-                        }
-                        to += a[k].pieces * apart();
-                    }
-                    a[k].at += a[k].step;
-                }
+                for (int j = 0; j < (B + 15) / 16; ++j) copy_async<(B < 16 ? 8 : 16)>(to + j * apart(), at + 16 * j);
             }
+            to += (B + 15) / 16 * apart();
         }
+    }
+    __device__ __forceinline__ void copy_typed(int type, const char* from) {
+        if (type == T_F32)
+            copy<T_F32>(from);
+        else
+            copy<T_F16>(from);
+    }
+    __device__ __forceinline__ bool begin_copy() {
+        to = ring + slot * bytes;
+        return left > 0;
+    }
+    __device__ __forceinline__ void end_copy() {
         --left;
         copies_commit();
         slot = slot + 1 == depth ? 0 : slot + 1;
     }
-    template <int TYPE>
-    __device__ __forceinline__ void take(uint32_t& from, const Mat& m, float (&v)[8 * C]) const {
-        if (!m.data) return;
+    template <int TYPE, typename F>
+    __device__ __forceinline__ void take(uint32_t& from, F f) const {
+        constexpr int N = (W * (TYPE == T_F32 ? 4 : 2) + 15) / 16;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            float w[8];
-            shared8<TYPE>(from, apart(), w);
-            from += (TYPE == T_F32 ? 2 : 1) * apart();
+        for (int k = 0; k < 8 * C / (W ? W : 1); ++k) {
+            Bits<TYPE, W ? W : 8> raw;
+            raw.load_shared(from, apart());
+            from += N * apart();
+            float w[W ? W : 8];
+            raw.spread(w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * c + e] = w[e];
+            for (int e = 0; e < W; ++e) f(W * k + e, w[e]);
         }
     }
-};
-// the gate's row for a row of y, kept up row by row
-struct GateRow {
-    long long row, left, rows;
-    __device__ __forceinline__ GateRow(long long first, long long group_rows) : row(first / group_rows), rows(group_rows) {
-        left = (row + 1) * group_rows - first;
-    }
-    __device__ __forceinline__ void next() {
-        if (--left == 0) {
-            ++row;
-            left = rows;
-        }
+    template <typename F>
+    __device__ __forceinline__ void take_typed(int type, uint32_t& from, F f) const {
+        if (type == T_F32)
+            take<T_F32>(from, f);
+        else if (type == T_F16)
+            take<T_F16>(from, f);
+        else
+            take<T_BF16>(from, f);
     }
 };
-// this thread's pieces of a row: a pointer that moves on by rows, or any strides
-template <bool VEC, int C>
+// One of the tensors whose rows come ahead: where this thread's first piece of the
+// next one lies.
+struct Ahead {
+    const char* at;
+    long long step;
+    __device__ __forceinline__ Ahead(const Mat& m, int type, long long row, int col) {
+        const int elem = type == T_F32 ? 4 : 2;
+        at = m.data ? static_cast<const char*>(m.data) + (row * m.rs + col) * elem : nullptr;
+        step = m.rs * elem;
+    }
+};
+// this thread's part of an output, a row after the other
+template <int TYPE, int W, int C>
 struct Output {
     char* at;
     long long step;
-    __device__ __forceinline__ Output(const Mat& m, int type, long long row, int col) {
-        const int elem = type == T_F32 ? 4 : 2;
-        at = const_cast<char*>(static_cast<const char*>(m.data)) + (row * m.rs + col) * elem;
-        step = m.rs * elem;
+    __device__ __forceinline__ Output(const Mat& m, long long row, int col) {
+        constexpr int E = TYPE == T_F32 ? 4 : 2;
+        at = m.data ? const_cast<char*>(static_cast<const char*>(m.data)) + (row * m.rs + col * (W ? 1 : m.cs)) * E : nullptr;
+        step = m.rs * E;
     }
-    template <int TYPE>
-    __device__ __forceinline__ void store(const RowThreads<VEC, C>& rt, const Mat& m, long long row, const float (&v)[8 * C]) {
-        if constexpr (VEC) {
+    __device__ __forceinline__ void store(const RowMemory<W, C>& rm, const Mat& m, const float (&v)[8 * C]) {
+        if (!at) return;
+        if constexpr (W > 0) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = v[8 * c + e];
-                if (rt.chunk_there(c)) store8(at, TYPE, static_cast<long long>(c) * rt.T * 8, w);
-            }
-            at += step;
+            for (int k = 0; k < 8 * C / W; ++k)
+                if (rm.there(W * k)) store_bits<TYPE, W>(at + static_cast<long long>(k) * rm.T * W * (TYPE == T_F32 ? 4 : 2), v + W * k);
         } else {
-            store_row<false, C>(m, TYPE, row, rt.T, rt.t, rt.base, rt.D, v);
+            const long long apart = rm.T * m.cs * (TYPE == T_F32 ? 4 : 2);
+            char* to = at;
+            int left = rm.D - rm.column(0);
+#pragma unroll
+            for (int i = 0; i < 8 * C; ++i, to += apart, left -= rm.T)
+                if (left > 0) store_any(to, TYPE, 0, v[i]);
         }
+        at += step;
     }
 };
 
-// A unit of T threads (blockDim.y of them in a CTA where T is a warp) takes
-// consecutive rows.
-template <int TY, int TX, bool VEC, int C>
-__global__ void __launch_bounds__(NORM_MAX_T) norm_kernel(const __grid_constant__ NormParams p) {
+// blockDim.y groups of T threads, each with rows of its own one after another, so
+// that one group's reductions pass under the others' work.
+template <int TY, int TX, int W, int C, int CTA>
+__global__ void __launch_bounds__(CTA) norm_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ float4 dynamic[];
-    __shared__ float2 buffer[2][16];
+    __shared__ float2 buffer[2][32];
     const int T = blockDim.x, t = threadIdx.x, D = p.D;
     const long long units = static_cast<long long>(gridDim.x) * blockDim.y, unit = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const long long begin = norm_row(p.M, units, unit), end = norm_row(p.M, units, unit + 1);
-    if (begin == end) return;
-    int turn = 0;
-    RowThreads<VEC, C> rt{T, t, 0, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin)};
-    rt.cache = smem_u32(dynamic) + threadIdx.y * (p.vec_bytes + p.depth * p.row_bytes) + t * 16;
-    rt.ring = rt.cache + p.vec_bytes;
-    rt.clear();
-    const bool row_gate = p.gate.data && p.group_rows == 1;
-    const int col = norm_column<VEC>(T, t, 0);
-    Ahead ahead[3];
-    ahead[0].start(p.y, TY, begin, col);
-    ahead[1].start(p.x, TX, begin, col);
-    ahead[2].start(row_gate ? p.gate : Mat{nullptr, 0, 0}, p.gate_type, begin, col);
-    Output<VEC, C> out_h(p.h, TX, begin, col), out_n(p.n, TY, begin, col);
-    GateRow gate(begin, p.group_rows);
-    float4* to_stats = p.stats + begin;
+    RowGroup group{T, t, static_cast<int>(threadIdx.y), 0, buffer};
+    RowMemory<W, C> rm{T, t, 0, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin), 0u};
+    rm.cache = smem_u32(dynamic) + t * 16;
+    rm.ring = rm.cache + p.vec_bytes + threadIdx.y * p.depth * p.row_bytes;
+    rm.clear();
+    const bool row_gate = p.gate.data && p.gate_rows > 1;
+    const int col = norm_column<W>(T, t, 0);
+    Ahead ahead_y(p.y, TY, begin, col), ahead_x(p.x, TX, begin, col);
+    Output<TX, W, C> out_h(p.h, begin, col);
+    Output<TY, W, C> out_n(p.n, begin, col);
+    GateRow gate(begin, p.group_rows), gate_ahead(gate);
+    Ahead ahead_gate(row_gate ? p.gate : Mat{nullptr, 0, 0}, p.gate_type, gate.row, col);
+    float4* to_stats = p.stats ? p.stats + begin : nullptr;
+    auto issue = [&]() {
+        if (rm.begin_copy()) {
+            rm.template copy<TY>(ahead_y.at);
+            ahead_y.at += ahead_y.step;
+            if (ahead_x.at) {
+                rm.template copy<TX>(ahead_x.at);
+                ahead_x.at += ahead_x.step;
+            }
+            if (row_gate) {
+                rm.copy_typed(p.gate_type, ahead_gate.at);
+                if (gate_ahead.next()) ahead_gate.at += ahead_gate.step;
+            }
+        }
+        rm.end_copy();
+    };
     grid_wait();
     grid_release();
-    if (VEC)
-        for (int i = 0; i < p.depth; ++i) rt.issue(ahead);
-    rt.keep(p.vec_at[0], p.post_w.data, p.post_w.type, 0, 1);
-    rt.keep(p.vec_at[1], p.post_b.data, p.post_b.type, 0, 1);
-    rt.keep(p.vec_at[2], p.pre_w.data, p.pre_w.type, 0, 1);
-    rt.keep(p.vec_at[3], p.pre_b.data, p.pre_b.type, 0, 1);
-    long long kept_gate = -1;
+    if constexpr (W > 0)
+        for (int i = 0; i < p.depth; ++i) issue();
+    const Vec one_gate{row_gate ? nullptr : p.gate.data, p.gate_type};
+    if (p.vec_bytes) {
+        if (threadIdx.y == 0) {
+            rm.keep(p.vec_at[0], p.post_w, 1);
+            rm.keep(p.vec_at[1], p.post_b, 1);
+            rm.keep(p.vec_at[2], p.pre_w, 1);
+            rm.keep(p.vec_at[3], p.pre_b, 1);
+            rm.keep(p.vec_at[4], one_gate, p.gate.cs);
+        }
+        __syncthreads();
+    }
     const float over_d = 1.f / D;
     for (long long row = begin; row < end; ++row) {
-        float v[8 * C], x[8 * C], gv[8 * C];
-        if (p.gate.data && !row_gate && gate.row != kept_gate) {
-            rt.keep(p.vec_at[4], p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs);
-            kept_gate = gate.row;
-        }
-        auto get = [&](int i, float w) { gv[i] = w; };
-        if (VEC && p.depth > 0) {
+        float v[8 * C], x[8 * C];
+        const bool queued = W > 0 && p.depth > 0;
+        uint32_t from = rm.ring + rm.slot * rm.bytes;
+        auto get = [&](int i, float w) { v[i] = w; };
+        auto times = [&](int i, float w) { v[i] *= w; };
+        auto plus = [&](int i, float w) { v[i] += w; };
+        if (queued) {
             copies_wait(p.depth - 1);
-            uint32_t from = rt.ring + rt.slot * rt.bytes;
-            rt.template take<TY>(from, p.y, v);
-            rt.template take<TX>(from, p.x, x);
-            if (row_gate) {
-                if (p.gate_type == T_F32)
-                    rt.template take<T_F32>(from, p.gate, gv);
-                else if (p.gate_type == T_F16)
-                    rt.template take<T_F16>(from, p.gate, gv);
-                else
-                    rt.template take<T_BF16>(from, p.gate, gv);
-            }
-            rt.issue(ahead);
+            rm.template take<TY>(from, get);
         } else {
-            load_row<TY, VEC, C>(p.y, row, T, t, 0, D, v);
-            if (p.x.data) load_row<TX, VEC, C>(p.x, row, T, t, 0, D, x);
-            if (row_gate) with_vector<VEC, C>(p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, T, t, 0, D, get);
+            load_row<TY, W, C>(p.y, row, T, t, 0, D, v);
+            if (p.x.data) load_row<TX, W, C>(p.x, row, T, t, 0, D, x);
         }
         float4 stats = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.post) {
-            const float2 s = row_stats<VEC, C>(v, p.post, p.eps, over_d, T, t, D, buffer, turn);
+            const float2 s = row_stats<W, C>(v, p.post, p.eps, over_d, D, group);
             stats.x = s.x;
             stats.y = s.y;
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) v[i] = (v[i] - s.x) * (rt.there(i) ? s.y : 0.f);
-            rt.each(p.vec_at[0], p.post_w.data, p.post_w.type, 0, 1, [&](int i, float w) { v[i] *= w; });
-            rt.each(p.vec_at[1], p.post_b.data, p.post_b.type, 0, 1, [&](int i, float w) { v[i] += w; });
+            for (int i = 0; i < 8 * C; ++i) v[i] = (v[i] - s.x) * (rm.there(i) ? s.y : 0.f);
+            rm.each(p.vec_at[0], p.post_w, times);
+            rm.each(p.vec_at[1], p.post_b, plus);
         }
-        if (p.gate.data) {
-            if (!row_gate) rt.each(p.vec_at[4], p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, get);
-#pragma unroll
-            for (int i = 0; i < 8 * C; ++i) v[i] = rt.there(i) ? v[i] * gv[i] : 0.f;
+        // what lies past a row's end of x and of the gate in shared memory is 0
+        auto add_x = [&](int i, float w) { v[i] = fmaf(p.scale, v[i], w); };
+        if (queued) {
+            if (row_gate) {
+                uint32_t gate_from = from + (p.x.data ? 8 * C / (W ? W : 1) * rm.apart() : 0u);
+                rm.take_typed(p.gate_type, gate_from, times);
+            }
+        } else if (row_gate) {
+            with_vector<W, C>(p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, T, t, 0, D, times);
         }
-        if (p.x.data) {
-#pragma unroll
-            for (int i = 0; i < 8 * C; ++i) v[i] = fmaf(p.scale, v[i], x[i]);
-        } else {
+        rm.each(p.vec_at[4], one_gate, times, p.gate.cs);
+        if (!p.x.data) {
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) v[i] *= p.scale;
+        } else if (queued) {
+            rm.template take<TX>(from, add_x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8 * C; ++i) add_x(i, x[i]);
         }
-        if (p.h.data) out_h.template store<TX>(rt, p.h, row, v);
+        if constexpr (W > 0)
+            if (p.depth > 0) issue();
+        out_h.store(rm, p.h, v);
         if (p.pre) {
-            const float2 s = row_stats<VEC, C>(v, p.pre, p.eps, over_d, T, t, D, buffer, turn);
+            const float2 s = row_stats<W, C>(v, p.pre, p.eps, over_d, D, group);
             stats.z = s.x;
             stats.w = s.y;
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) v[i] = (v[i] - s.x) * s.y;
-            rt.each(p.vec_at[2], p.pre_w.data, p.pre_w.type, 0, 1, [&](int i, float w) { v[i] *= w; });
-            rt.each(p.vec_at[3], p.pre_b.data, p.pre_b.type, 0, 1, [&](int i, float w) { v[i] += w; });
-            out_n.template store<TY>(rt, p.n, row, v);
+            rm.each(p.vec_at[2], p.pre_w, times);
+            rm.each(p.vec_at[3], p.pre_b, plus);
+            out_n.store(rm, p.n, v);
         }
-        if (p.stats) {
+        if (to_stats) {
             if (t == 0) *to_stats = stats;
             ++to_stats;
         }
         gate.next();
     }
-    if (VEC) copies_wait(0);
+    if constexpr (W > 0) copies_wait(0);
 }
 
 // Rows of any length, read anew for each reduction: one CTA per row.
 template <int TY, int TX>
 __global__ void __launch_bounds__(NORM_MAX_T) norm_long_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float2 buffer[2][16];
+    __shared__ float2 buffer[2][32];
     const int T = blockDim.x, t = threadIdx.x, D = p.D;
-    int turn = 0;
+    RowGroup group{T, t, 0, 0, buffer};
     grid_wait();
     grid_release();
     const long long row = blockIdx.x;
@@ -509,14 +583,14 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_long_kernel(const __grid_cons
         float m = 0.f, s = 0.f;
         if (kind == NORM_LAYER) {
             for (int c = t; c < D; c += T) s += value(c);
-            m = row_sum<false>(s, 0.f, T, t, buffer, turn).x / D;
+            m = group.sum<false>(s, 0.f).x / D;
         }
         s = 0.f;
         for (int c = t; c < D; c += T) {
             const float d = value(c) - m;
             s = fmaf(d, d, s);
         }
-        r = rsqrtf(row_sum<false>(s, 0.f, T, t, buffer, turn).x / D + p.eps);
+        r = rsqrtf(group.sum<false>(s, 0.f).x / D + p.eps);
         mean = m;
     };
     if (p.post) {
@@ -541,26 +615,25 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_long_kernel(const __grid_cons
 
 // A row's sums over the CTAs of a cluster that share it, in their order.
 struct Shared {
-    float2 (*buffer)[16];
+    RowGroup group;
     float2 (*meet)[8];
-    int T, t, parts, rank, turn;
+    int parts, rank, turn;
     template <bool TWO>
     __device__ __forceinline__ float2 sum(float a, float b) {
-        const int now = turn;
-        float2 s = row_sum<TWO>(a, b, T, t, buffer, turn);
+        float2 s = group.sum<TWO>(a, b);
         if (parts == 1) return s;
-        if (T == 32) turn ^= 1;
-        if (t < parts) {
-            const uint32_t to = map_to(smem_u32(&meet[now][rank]), t);
+        if (group.t < parts) {
+            const uint32_t to = map_to(smem_u32(&meet[turn][rank]), group.t);
             st_shared_cluster_u32(to, __float_as_uint(s.x));
             st_shared_cluster_u32(to + 4, __float_as_uint(s.y));
         }
         cluster_sync();
         s = make_float2(0.f, 0.f);
         for (int k = 0; k < parts; ++k) {
-            s.x += meet[now][k].x;
-            s.y += meet[now][k].y;
+            s.x += meet[turn][k].x;
+            s.y += meet[turn][k].y;
         }
+        turn ^= 1;
         return s;
     }
 };
@@ -645,93 +718,112 @@ struct RowSums {
 // The rows of a CTA, or of a cluster of `parts` CTAs that each take a part of a
 // row, are consecutive; the sums over them are left in `part`.  A gate row's sum
 // is done where all of its rows are the CTA's, else its share goes to gate_part.
-template <int TY, int TX, bool VEC, int C>
+template <int TY, int TX, int W, int C>
 __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_constant__ NormGradParams g) {
     extern __shared__ float4 dynamic[];  // sums (C > 1), vectors, the rows ahead
-    __shared__ float2 buffer[2][16], meet[2][8];
+    __shared__ float2 buffer[2][32], meet[2][8];
     const NormParams& p = g.f;
     const int T = blockDim.x, t = threadIdx.x, D = p.D;
     const int rank = g.parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int base = rank * T * 8 * C;
     const long long cta = blockIdx.x / g.parts;
     const long long begin = norm_row(p.M, g.ctas, cta), end = norm_row(p.M, g.ctas, cta + 1);
-    Shared shared{buffer, meet, T, t, g.parts, rank, 0};
+    Shared shared{RowGroup{T, t, 0, 0, buffer}, meet, g.parts, rank, 0};
     const int all = g.slots + g.gate_sums;
     RowSums<C> sums;
     sums.at = dynamic + t;
     sums.T = T;
     sums.clear(all);
-    RowThreads<VEC, C> rt{T, t, base, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin)};
-    rt.cache = smem_u32(dynamic + (C == 1 ? 0 : all * 2 * C * T) + t);
-    rt.ring = rt.cache + p.vec_bytes;
-    rt.clear();
-    const bool row_gate = p.gate.data && p.group_rows == 1;
-    const Mat none{nullptr, 0, 0};
-    const int col = base + norm_column<VEC>(T, t, 0);
-    Ahead ahead[5];
-    ahead[0].start(p.y, TY, begin, col);
-    ahead[1].start(p.x, TX, begin, col);
-    ahead[2].start(g.dh, TX, begin, col);
-    ahead[3].start(g.dn, TY, begin, col);
-    ahead[4].start(row_gate ? p.gate : none, p.gate_type, begin, col);
-    Output<VEC, C> out_x(g.dx, TX, begin, col), out_y(g.dy, TY, begin, col);
-    GateRow gate(begin, p.group_rows);
+    RowMemory<W, C> rm{T, t, base, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin), 0u};
+    rm.cache = smem_u32(dynamic + (C == 1 ? 0 : all * 2 * C * T) + t);
+    rm.ring = rm.cache + p.vec_bytes;
+    rm.clear();
+    const bool row_gate = p.gate.data && p.gate_rows > 1;
+    const Vec one_gate{row_gate ? nullptr : p.gate.data, p.gate_type};
+    const int col = base + norm_column<W>(T, t, 0);
+    Ahead ahead_y(p.y, TY, begin, col), ahead_x(p.x, TX, begin, col), ahead_h(g.dh, TX, begin, col), ahead_n(g.dn, TY, begin, col);
+    Output<TX, W, C> out_x(g.dx, begin, col);
+    Output<TY, W, C> out_y(g.dy, begin, col);
+    GateRow gate(begin, p.group_rows), gate_ahead(gate);
+    Ahead ahead_gate(row_gate ? p.gate : Mat{nullptr, 0, 0}, p.gate_type, gate.row, col);
     const float4* stats_at = p.stats + begin;
+    auto issue = [&]() {
+        if (rm.begin_copy()) {
+            rm.template copy<TY>(ahead_y.at);
+            ahead_y.at += ahead_y.step;
+            if (ahead_x.at) {
+                rm.template copy<TX>(ahead_x.at);
+                ahead_x.at += ahead_x.step;
+            }
+            if (ahead_h.at) {
+                rm.template copy<TX>(ahead_h.at);
+                ahead_h.at += ahead_h.step;
+            }
+            if (ahead_n.at) {
+                rm.template copy<TY>(ahead_n.at);
+                ahead_n.at += ahead_n.step;
+            }
+            if (row_gate) {
+                rm.copy_typed(p.gate_type, ahead_gate.at);
+                if (gate_ahead.next()) ahead_gate.at += ahead_gate.step;
+            }
+        }
+        rm.end_copy();
+    };
     // every CTA of the cluster is there before another writes its shared memory
     if (g.parts > 1) cluster_sync();
     grid_wait();
     grid_release();
-    if (VEC)
-        for (int i = 0; i < p.depth; ++i) rt.issue(ahead);
-    rt.keep(p.vec_at[0], p.post_w.data, p.post_w.type, 0, 1);
-    rt.keep(p.vec_at[1], p.post_b.data, p.post_b.type, 0, 1);
-    rt.keep(p.vec_at[2], p.pre_w.data, p.pre_w.type, 0, 1);
-    long long kept_gate = -1;
+    if constexpr (W > 0)
+        for (int i = 0; i < p.depth; ++i) issue();
+    rm.keep(p.vec_at[0], p.post_w, 1);
+    rm.keep(p.vec_at[1], p.post_b, 1);
+    rm.keep(p.vec_at[2], p.pre_w, 1);
+    rm.keep(p.vec_at[4], one_gate, p.gate.cs);
+    // a gate row per row of y: its gradient
+    auto store_gate = [&](const float (&u)[8 * C]) {
+#pragma unroll
+        for (int i = 0; i < 8 * C; ++i)
+            if (rm.column(i) < D) store_any(const_cast<void*>(g.dgate.data), p.gate_type, gate.row * g.dgate.rs + rm.column(i) * g.dgate.cs, u[i]);
+    };
     float4 next = *stats_at;
     const float over_d = 1.f / D;
     for (long long row = begin; row < end; ++row) {
         float y[8 * C], h[8 * C], d[8 * C], e[8 * C], u[8 * C], gv[8 * C];
         const float4 stats = next;
         if (row + 1 < end) next = *++stats_at;
-        if (p.gate.data && !row_gate && gate.row != kept_gate) {
-            rt.keep(p.vec_at[4], p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs);
-            kept_gate = gate.row;
-        }
         auto get = [&](int i, float w) { gv[i] = w; };
-        if (VEC && p.depth > 0) {
-            copies_wait(p.depth - 1);
-            uint32_t from = rt.ring + rt.slot * rt.bytes;
-            rt.template take<TY>(from, p.y, y);
-            rt.template take<TX>(from, p.x, h);
-            rt.template take<TX>(from, g.dh, d);
-            rt.template take<TY>(from, g.dn, e);
-            if (row_gate) {
-                if (p.gate_type == T_F32)
-                    rt.template take<T_F32>(from, p.gate, gv);
-                else if (p.gate_type == T_F16)
-                    rt.template take<T_F16>(from, p.gate, gv);
-                else
-                    rt.template take<T_BF16>(from, p.gate, gv);
-            }
-            rt.issue(ahead);
-        } else {
-            load_row<TY, VEC, C>(p.y, row, T, t, base, D, y);
-            if (p.x.data) load_row<TX, VEC, C>(p.x, row, T, t, base, D, h);
-            if (g.dh.data) load_row<TX, VEC, C>(g.dh, row, T, t, base, D, d);
-            if (g.dn.data) load_row<TY, VEC, C>(g.dn, row, T, t, base, D, e);
-            if (row_gate) with_vector<VEC, C>(p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, T, t, base, D, get);
+        if (p.gate.data && (W == 0 || p.depth == 0 || p.vec_bytes == 0)) {  // read where it lies, which leaves out what is past the end
+#pragma unroll
+            for (int i = 0; i < 8 * C; ++i) gv[i] = 0.f;
         }
-        if (p.gate.data && !row_gate) rt.each(p.vec_at[4], p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, get);
+        if (W > 0 && p.depth > 0) {
+            copies_wait(p.depth - 1);
+            uint32_t from = rm.ring + rm.slot * rm.bytes;
+            rm.template take<TY>(from, [&](int i, float w) { y[i] = w; });
+            if (p.x.data) rm.template take<TX>(from, [&](int i, float w) { h[i] = w; });
+            if (g.dh.data) rm.template take<TX>(from, [&](int i, float w) { d[i] = w; });
+            if (g.dn.data) rm.template take<TY>(from, [&](int i, float w) { e[i] = w; });
+            if (row_gate) rm.take_typed(p.gate_type, from, get);
+            if constexpr (W > 0) issue();
+        } else {
+            load_row<TY, W, C>(p.y, row, T, t, base, D, y);
+            if (p.x.data) load_row<TX, W, C>(p.x, row, T, t, base, D, h);
+            if (g.dh.data) load_row<TX, W, C>(g.dh, row, T, t, base, D, d);
+            if (g.dn.data) load_row<TY, W, C>(g.dn, row, T, t, base, D, e);
+            if (row_gate) with_vector<W, C>(p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, T, t, base, D, get);
+        }
+        rm.each(p.vec_at[4], one_gate, get, p.gate.cs);
         // y becomes yhat, u what the gate multiplies, h the sum and then hhat
         if (p.post) {
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) y[i] = (y[i] - stats.x) * (rt.there(i) ? stats.y : 0.f);
+            for (int i = 0; i < 8 * C; ++i) y[i] = (y[i] - stats.x) * (rm.there(i) ? stats.y : 0.f);
         }
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) u[i] = y[i];
         if (p.post) {
-            rt.each(p.vec_at[0], p.post_w.data, p.post_w.type, 0, 1, [&](int i, float w) { u[i] *= w; });
-            rt.each(p.vec_at[1], p.post_b.data, p.post_b.type, 0, 1, [&](int i, float w) { u[i] += w; });
+            rm.each(p.vec_at[0], p.post_w, [&](int i, float w) { u[i] *= w; });
+            rm.each(p.vec_at[1], p.post_b, [&](int i, float w) { u[i] += w; });
         }
         if (g.dn.data) {
             if (p.gate.data) {
@@ -742,10 +834,10 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
                 for (int i = 0; i < 8 * C; ++i) h[i] = fmaf(p.scale, u[i], p.x.data ? h[i] : 0.f);
             }
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) h[i] = rt.there(i) ? (h[i] - stats.z) * stats.w : 0.f;
+            for (int i = 0; i < 8 * C; ++i) h[i] = (h[i] - stats.z) * (rm.there(i) ? stats.w : 0.f);
             if (g.slot[0] >= 0) sums.add(0, g.slot[0], e, h);
             if (g.slot[1] >= 0) sums.add(1, g.slot[1], e);
-            rt.each(p.vec_at[2], p.pre_w.data, p.pre_w.type, 0, 1, [&](int i, float w) { e[i] *= w; });
+            rm.each(p.vec_at[2], p.pre_w, [&](int i, float w) { e[i] *= w; });
             float a = 0.f, b = 0.f;
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) a = fmaf(e[i], h[i], a);
@@ -769,7 +861,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
                 for (int i = 0; i < 8 * C; ++i) d[i] = stats.w * e[i];
             }
         }
-        if (g.dx.data) out_x.template store<TX>(rt, g.dx, row, d);
+        out_x.store(rm, g.dx, d);
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) d[i] *= p.scale;
         if (p.gate.data) {
@@ -778,7 +870,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
             } else if (g.dgate.data) {
 #pragma unroll
                 for (int i = 0; i < 8 * C; ++i) u[i] *= d[i];
-                store_row<VEC, C>(g.dgate, p.gate_type, gate.row, T, t, base, D, u);
+                store_gate(u);
             }
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) d[i] *= gv[i];
@@ -786,14 +878,14 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
         if (p.post) {
             if (g.slot[2] >= 0) sums.add(2, g.slot[2], d, y);
             if (g.slot[3] >= 0) sums.add(3, g.slot[3], d);
-            rt.each(p.vec_at[0], p.post_w.data, p.post_w.type, 0, 1, [&](int i, float w) { d[i] *= w; });
+            rm.each(p.vec_at[0], p.post_w, [&](int i, float w) { d[i] *= w; });
             float a = 0.f, b = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) a = fmaf(rt.there(i) ? d[i] : 0.f, y[i], a);
+            for (int i = 0; i < 8 * C; ++i) a = fmaf(rm.there(i) ? d[i] : 0.f, y[i], a);
             float m0 = 0.f, m1;
             if (p.post == NORM_LAYER) {
 #pragma unroll
-                for (int i = 0; i < 8 * C; ++i) b += rt.there(i) ? d[i] : 0.f;
+                for (int i = 0; i < 8 * C; ++i) b += rm.there(i) ? d[i] : 0.f;
                 const float2 s = shared.template sum<true>(a, b);
                 m1 = s.x * over_d;
                 m0 = s.y * over_d;
@@ -803,7 +895,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) d[i] = stats.y * fmaf(-m1, y[i], d[i] - m0);
         }
-        if (g.dy.data) out_y.template store<TY>(rt, g.dy, row, d);
+        out_y.store(rm, g.dy, d);
         // the last row of a gate row, or of this CTA
         if (g.gate_sums && (row + 1 == end || gate.left == 1)) {
             const bool begins = gate.row * p.group_rows >= begin, ends = (gate.row + 1) * p.group_rows <= end;
@@ -812,7 +904,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
             sums.zero(4, g.slots);
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) {
-                const int c = base + norm_column<VEC>(T, t, i);
+                const int c = rm.column(i);
                 if (c >= D) continue;
                 if (begins && ends)
                     store_any(const_cast<void*>(g.dgate.data), p.gate_type, gate.row * g.dgate.rs + c * g.dgate.cs, u[i]);
@@ -822,7 +914,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
         }
         gate.next();
     }
-    if (VEC) copies_wait(0);
+    if constexpr (W > 0) copies_wait(0);
 #pragma unroll
     for (int which = 0; which < 4; ++which) {
         if (g.slot[which] < 0) continue;
@@ -831,7 +923,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
         sums.get(which, g.slot[which], u);
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) {
-            const int c = base + norm_column<VEC>(T, t, i);
+            const int c = rm.column(i);
             if (c < D) to[c] = u[i];
         }
     }
@@ -842,10 +934,10 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
 // Rows of any length; the sums are kept in `part` and gate_part themselves.
 template <int TY, int TX>
 __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_long_kernel(const __grid_constant__ NormGradParams g) {
-    __shared__ float2 buffer[2][16];
+    __shared__ float2 buffer[2][32];
     const NormParams& p = g.f;
     const int T = blockDim.x, t = threadIdx.x, D = p.D;
-    int turn = 0;
+    RowGroup group{T, t, 0, 0, buffer};
     grid_wait();
     grid_release();
     const float over_d = 1.f / D;
@@ -883,7 +975,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_long_kernel(const __grid
                 a = fmaf(e, load_hhat(c), a);
                 b += e;
             }
-            const float2 s = row_sum<true>(a, b, T, t, buffer, turn);
+            const float2 s = group.sum<true>(a, b);
             h1 = s.x * over_d;
             h0 = p.pre == NORM_LAYER ? s.y * over_d : 0.f;
         }
@@ -900,7 +992,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_long_kernel(const __grid
                 a = fmaf(d, load_yhat(c), a);
                 b += d;
             }
-            const float2 s = row_sum<true>(a, b, T, t, buffer, turn);
+            const float2 s = group.sum<true>(a, b);
             y1 = s.x * over_d;
             y0 = p.post == NORM_LAYER ? s.y * over_d : 0.f;
         }
