@@ -2,6 +2,7 @@
 // declared in include/gemm_collective_tiles.h: argument checks, the choice of
 // kernels, tensor maps and launches.
 #include <cmath>
+#include <initializer_list>
 
 #include "../csrc_fp8/fp8_host.cuh"
 #include "block_few.cuh"
@@ -331,8 +332,12 @@ int act_grad(const iris_b200_act_grad_args* g, void* ws, size_t ws_bytes, cudaSt
 // ---------------------------------------------------------------- norms
 bool norm_ok(int k) { return k >= IRIS_NORM_NONE && k <= IRIS_NORM_LAYER; }
 
-// checks and parameters of a forward call; `vec`: every tensor so far has rows on 16 bytes
-int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec) {
+// rows of unit stride, or not there
+bool unit(const iris_b200_mat& m) { return !m.data || m.col_stride == 1; }
+
+// checks and parameters of a forward call; `vec`: every tensor so far has rows on 16
+// bytes; `shared`: those that are read have rows of unit stride
+int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec, bool& words) {
     int rc;
     std::memset(&p, 0, sizeof(p));
     if (!dims_ok(g->M, 0, g->D) || !dtype_ok(g->y_dtype) || !dtype_ok(g->x_dtype) || !norm_ok(g->post) || !norm_ok(g->pre) ||
@@ -378,6 +383,7 @@ int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec) {
     vec = D % 8 == 0 && rows16(g->y, M, D, ye) && rows16(g->x, M, D, xe) && rows16(g->h, M, D, xe) && rows16(g->n, M, D, ye) &&
           rows16(g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)) && aligned16(g->post_weight) && aligned16(g->post_bias) &&
           aligned16(g->weight) && aligned16(g->bias);
+    words = unit(g->y) && unit(g->x) && unit(g->gate);
     return IRIS_OK;
 }
 
@@ -415,10 +421,17 @@ RowShape row_shape(int64_t D, int C, int most) {
 }
 constexpr size_t SM_SMEM = 222 * 1024;  // dynamic shared memory of an SM, beside the kernels' own
 
+// How rows reach their threads: pieces of W elements (8 or 4) where all of them
+// lie on 16 bytes; single elements, which rows of unit stride bring through shared
+// memory too (`shared`), or which are read where they lie.
+struct RowKind {
+    int w;
+    bool shared;
+};
 // What of `room` bytes the vectors (in fp32) and the rows ahead of `groups` rows'
-// threads take: vectors first, then up to 4 rows each, where they lie on 16
-// bytes.  `pieces`: 16 bytes a thread and row, at C = 1.
-size_t row_memory(NormParams& p, RowShape r, int groups, bool bias, bool vec, int w, size_t pieces, size_t room) {
+// threads take: vectors first, then up to 4 rows each.  `types`: of the tensors
+// whose rows come, -1: not there.
+size_t row_memory(NormParams& p, RowShape r, int groups, bool bias, RowKind kind, std::initializer_list<int> types, size_t room) {
     const size_t piece = static_cast<size_t>(r.C) * r.T * 16;
     const void* all[5] = {p.post_w.data, p.post_b.data, p.pre_w.data, bias ? p.pre_b.data : nullptr, p.gate_rows == 1 ? p.gate.data : nullptr};
     int n = 0;
@@ -428,18 +441,25 @@ size_t row_memory(NormParams& p, RowShape r, int groups, bool bias, bool vec, in
         p.vec_bytes = 0;
         for (int& at : p.vec_at) at = -1;
     }
-    if (p.gate.data && p.gate_rows > 1) pieces += w == 4 || p.gate_type == T_F32 ? 2 : 1;
-    p.row_bytes = static_cast<unsigned>(pieces * piece);
-    p.depth = vec ? static_cast<int>(std::min<size_t>(4, (room - p.vec_bytes) / (groups * static_cast<size_t>(p.row_bytes)))) : 0;
+    size_t bytes = 0;
+    auto add = [&](int type) {
+        if (kind.w)
+            bytes += piece * (kind.w == 4 || type == T_F32 ? 2 : 1);
+        else
+            bytes += 8 * r.C * r.T * dtype_size(type) + 32;
+    };
+    for (int type : types)
+        if (type >= 0) add(type);
+    if (p.gate.data && p.gate_rows > 1) add(p.gate_type);
+    p.row_bytes = static_cast<unsigned>(bytes);
+    p.depth = 0;
+    if (kind.w || kind.shared) p.depth = static_cast<int>(std::min<size_t>(4, (room - p.vec_bytes) / (groups * bytes)));
+    if (!kind.w && p.depth < 2) p.depth = 0;
     return p.vec_bytes + static_cast<size_t>(groups) * p.depth * p.row_bytes;
 }
-// pieces of 16 bytes that 8 elements take
-constexpr int pieces_of(int type, int w) { return w == 4 || type == T_F32 ? 2 : 1; }
-
 template <int TY, int TX, int W>
-int launch_norm_w(NormParams p, bool vec, int sms, cudaStream_t stream) {
+int launch_norm_w(NormParams p, bool words, int sms, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
-    constexpr int w = TX == T_F32 ? 4 : 8;
     // Few rows: the more threads a row the shorter its way; many: work for a thread
     // between two reductions
     const RowShape r = row_shape(p.D, p.M < 2 * sms ? 1 : 2, NORM_CTA);
@@ -451,7 +471,7 @@ int launch_norm_w(NormParams p, bool vec, int sms, cudaStream_t stream) {
     const int64_t ctas = std::min<int64_t>(cdiv(p.M, groups), sms);
     size_t smem = 0;
     if (ctas * groups < p.M)  // several rows for a group
-        smem = row_memory(p, r, groups, true, vec, w, pieces_of(TY, w) + (p.x.data ? pieces_of(TX, w) : 0), SM_SMEM);
+        smem = row_memory(p, r, groups, true, RowKind{W, words}, {TY, p.x.data ? TX : -1}, SM_SMEM);
     auto kernel = r.C == 1 ? norm_kernel<TY, TX, W, 1, NORM_CTA> : norm_kernel<TY, TX, W, 2, NORM_CTA>;
     if (W && threads == NORM_MAX_T) kernel = r.C == 1 ? norm_kernel<TY, TX, W, 1, W ? NORM_MAX_T : NORM_CTA> : norm_kernel<TY, TX, W, 2, W ? NORM_MAX_T : NORM_CTA>;
     const int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem);
@@ -461,12 +481,12 @@ int launch_norm_w(NormParams p, bool vec, int sms, cudaStream_t stream) {
     return launch("norm launch", kernel, lc, p);
 }
 template <int TY, int TX>
-int launch_norm(const NormParams& p, bool vec, int sms, cudaStream_t stream) {
+int launch_norm(const NormParams& p, bool vec, bool words, int sms, cudaStream_t stream) {
     if (p.D > NORM_LONGEST) {
         cudaLaunchAttribute attr[2];
         return launch("norm launch", norm_long_kernel<TY, TX>, launch_config(static_cast<unsigned>(p.M), NORM_MAX_T, 0, 1, stream, attr), p);
     }
-    return vec ? launch_norm_w<TY, TX, TX == T_F32 ? 4 : 8>(p, true, sms, stream) : launch_norm_w<TY, TX, 0>(p, false, sms, stream);
+    return vec ? launch_norm_w<TY, TX, TX == T_F32 ? 4 : 8>(p, false, sms, stream) : launch_norm_w<TY, TX, 0>(p, words, sms, stream);
 }
 template <typename F>
 int by_types(int y, int x, F f) {
@@ -498,10 +518,10 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     std::memset(&p, 0, sizeof(p));
     if (!g) return IRIS_EINVAL;
     const iris_b200_norm_join_args& f = g->f;
-    bool vec;
+    bool vec, words;
     iris_b200_norm_join_args ff = f;
     ff.h.data = ff.n.data = nullptr;
-    if ((rc = set_norm(&ff, p.f, vec))) return rc;
+    if ((rc = set_norm(&ff, p.f, vec, words))) return rc;
     const int64_t M = f.M, D = f.D, G = f.gate.data ? f.gate_rows : 0;
     const int ye = dtype_size(f.y_dtype), xe = dtype_size(f.x_dtype), ge = dtype_size(f.gate_dtype);
     if ((g->dn.data && !f.pre) || (g->dgate.data && !f.gate.data) || (M > 0 && D > 0 && !f.stats)) return IRIS_EINVAL;
@@ -539,11 +559,12 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     const int per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
     const size_t pieces = static_cast<size_t>(pl.r.C) * pl.r.T * 16;
     const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pieces;
-    const int w = f.x_dtype == IRIS_F32 ? 4 : 8, ys = pieces_of(f.y_dtype, w), xs = pieces_of(f.x_dtype, w);
     const size_t room = SM_SMEM / per_sm - 1024;
+    words = words && unit(g->dh) && unit(g->dn);
     pl.smem = sums;
     if (sums < room)
-        pl.smem += row_memory(p.f, pl.r, 1, false, vec, w, ys + (f.x.data ? xs : 0) + (g->dh.data ? xs : 0) + (g->dn.data ? ys : 0), room - sums);
+        pl.smem += row_memory(p.f, pl.r, 1, false, RowKind{!vec ? 0 : f.x_dtype == IRIS_F32 ? 4 : 8, words},
+                              {f.y_dtype, f.x.data ? f.x_dtype : -1, g->dh.data ? f.x_dtype : -1, g->dn.data ? f.y_dtype : -1}, room - sums);
     if (pl.smem > SM_SMEM) return IRIS_EUNSUPPORTED;
     pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
     pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
@@ -646,16 +667,16 @@ int iris_b200_dropout(const iris_b200_dropout_args* g, cudaStream_t stream) {
 
 int iris_b200_norm_join(const iris_b200_norm_join_args* g, cudaStream_t stream) {
     NormParams p;
-    bool vec;
+    bool vec, words;
     if (!g) return IRIS_EINVAL;
-    const int rc = set_norm(g, p, vec);
+    const int rc = set_norm(g, p, vec, words);
     if (rc) return rc;
     if ((g->pre != 0) != (g->n.data != nullptr) && g->M > 0 && g->D > 0) return IRIS_EINVAL;
     if (g->M == 0 || g->D == 0) return IRIS_OK;
     int sms;
     if (sm_count(&sms)) return IRIS_ECUDA;
     return by_types(g->y_dtype, g->x_dtype,
-                    [&](auto ty, auto tx) { return launch_norm<decltype(ty)::value, decltype(tx)::value>(p, vec, sms, stream); });
+                    [&](auto ty, auto tx) { return launch_norm<decltype(ty)::value, decltype(tx)::value>(p, vec, words, sms, stream); });
 }
 int iris_b200_norm_join_grad_workspace_size(const iris_b200_norm_join_grad_args* args, const iris_b200_config*, size_t* bytes) {
     return bytes ? norm_grad(args, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;

@@ -215,6 +215,12 @@ __device__ __forceinline__ void with_vector(const void* data, int type, long lon
 struct RowGroup {
     int T, t, id, turn;
     float2 (*buffer)[32];  // by warp of the CTA
+    __device__ __forceinline__ void sync() const {
+        if (T == 32)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(T) : "memory");
+    }
     template <bool TWO>
     __device__ __forceinline__ float2 sum(float a, float b) {
 #pragma unroll
@@ -225,7 +231,7 @@ struct RowGroup {
         if (T == 32) return make_float2(a, b);
         float2* const mine = buffer[turn] + id * (T >> 5);
         if ((t & 31) == 0) mine[t >> 5] = make_float2(a, b);
-        asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(T) : "memory");
+        sync();
         const int w = t & 31;
         float2 s = make_float2(0.f, 0.f);
         if (w * 32 < T) s = mine[w];
@@ -306,6 +312,18 @@ struct RowMemory {
     uint32_t bytes;        // of a row ahead
     int depth, slot, left; // rows ahead (0: none), the next one's place, rows not yet copied
     uint32_t to;           // where the row under copy goes on
+    int used;              // the place of the row that is used next
+    __device__ __forceinline__ uint32_t here() const { return ring + used * bytes; }
+    // the row that is used next is there
+    __device__ __forceinline__ void arrived(const RowGroup& group) {
+        if (W > 0) {
+            copies_wait(depth - 1);
+        } else {
+            copies_wait(depth - 2);
+            group.sync();  // all of its threads' copies
+        }
+        used = used + 1 == depth ? 0 : used + 1;
+    }
 
     __device__ __forceinline__ uint32_t apart() const { return T * 16; }
     __device__ __forceinline__ int column(int i) const { return base + norm_column<W>(T, t, i); }
@@ -360,6 +378,59 @@ struct RowMemory {
             to += (B + 15) / 16 * apart();
         }
     }
+    // W = 0, elements of unit stride: a row's threads copy it together, in the pieces
+    // of 16 bytes that it lies in, and its elements begin `shift` bytes into the
+    // first.  Pieces that reach past the tensor's ends are filled by elements.
+    static __device__ __forceinline__ uint32_t shift(const char* row) {
+        return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u;
+    }
+    __device__ __forceinline__ uint32_t room(int elem) const { return 8 * C * T * elem + 32; }
+    template <int TYPE>
+    __device__ __forceinline__ void copy_pieces(const char* row, const char* lo, const char* hi) {
+        constexpr int E = TYPE == T_F32 ? 4 : 2;
+        const uint32_t s = shift(row);
+        const int bytes_here = min(D - base, 8 * C * T) * E + static_cast<int>(s);  // from the first piece on
+        const char* const first = row - s;
+        const int from_lo = static_cast<int>(min(static_cast<long long>(s), max(0ll, static_cast<long long>(lo - first))));
+        const long long to_hi = hi - first;
+#pragma unroll
+        for (int k = 0; k < C * E / 2 + 1; ++k) {
+            const int at = (t + k * T) * 16;
+            if (at >= bytes_here) break;
+            if (at >= from_lo && at + 16 <= to_hi) {
+                copy_async<16>(to + at, first + at);
+            } else {
+                for (int b = 0; b < 16; b += E) {
+                    if (at + b < from_lo || at + b >= bytes_here) continue;
+                    if (TYPE == T_F32)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + at + b), "f"(*reinterpret_cast<const float*>(first + at + b)) : "memory");
+                    else
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + at + b), "h"(*reinterpret_cast<const uint16_t*>(first + at + b)) : "memory");
+                }
+            }
+        }
+        to += room(E);
+    }
+    // an element past the row's end is read as well, and left out
+    template <int TYPE, typename F>
+    __device__ __forceinline__ void take_pieces(uint32_t& from, const char* row, F f) const {
+        constexpr int E = TYPE == T_F32 ? 4 : 2;
+        uint32_t at = from + shift(row) + t * E;
+        const int n = D - base - t;
+#pragma unroll
+        for (int i = 0; i < 8 * C; ++i, at += T * E) {
+            float v;
+            if (TYPE == T_F32) {
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+            } else {
+                uint32_t h;
+                asm volatile("{\n\t.reg .b16 x;\n\tld.shared.b16 x, [%1];\n\tmov.b32 %0, {x, x};\n\t}" : "=r"(h) : "r"(at) : "memory");
+                v = TYPE == T_BF16 ? __uint_as_float(h & 0xFFFF0000u) : __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+            }
+            f(i, i * T < n ? v : 0.f);
+        }
+        from += room(E);
+    }
     __device__ __forceinline__ void copy_typed(int type, const char* from) {
         if (type == T_F32)
             copy<T_F32>(from);
@@ -402,12 +473,79 @@ struct RowMemory {
 // One of the tensors whose rows come ahead: where this thread's first piece of the
 // next one lies.
 struct Ahead {
-    const char* at;
+    const char *at, *hi;  // hi: the tensor's end
     long long step;
-    __device__ __forceinline__ Ahead(const Mat& m, int type, long long row, int col) {
+    __device__ __forceinline__ Ahead(const Mat& m, int type, long long row, int col, long long rows, int D) {
         const int elem = type == T_F32 ? 4 : 2;
         at = m.data ? static_cast<const char*>(m.data) + (row * m.rs + col) * elem : nullptr;
+        hi = static_cast<const char*>(m.data) + ((rows - 1) * m.rs + D) * elem;
         step = m.rs * elem;
+    }
+};
+// A tensor's rows under way, and where the one that is used now lies (W = 0: its
+// address says how its pieces hold it).
+template <int TYPE, int W, int C>
+struct Stream {
+    Ahead a;
+    const char *lo, *now;
+    __device__ __forceinline__ Stream(const Mat& m, long long row, int base, int col, long long rows, int D)
+        : a(m, TYPE, row, W ? col : base, rows, D), lo(static_cast<const char*>(m.data)), now(a.at) {}
+    __device__ __forceinline__ void copy(RowMemory<W, C>& rm) {
+        if (!a.at) return;
+        if constexpr (W > 0)
+            rm.template copy<TYPE>(a.at);
+        else
+            rm.template copy_pieces<TYPE>(a.at, lo, a.hi);
+        a.at += a.step;
+    }
+    template <typename F>
+    __device__ __forceinline__ void take(const RowMemory<W, C>& rm, uint32_t& from, F f) {
+        if (!a.at) return;
+        if constexpr (W > 0) {
+            rm.template take<TYPE>(from, f);
+        } else {
+            rm.template take_pieces<TYPE>(from, now, f);
+            now += a.step;
+        }
+    }
+};
+// The same of a gate of several rows, whose type is one of three.
+template <int W, int C>
+struct GateStream {
+    Ahead a;
+    const char *lo, *now;
+    GateRow under_way, used;
+    int type;
+    __device__ __forceinline__ GateStream(const NormParams& p, bool there, long long row, int base, int col)
+        : a(there ? p.gate : Mat{nullptr, 0, 0}, p.gate_type, row / p.group_rows, W ? col : base, p.gate_rows, p.D),
+          lo(static_cast<const char*>(p.gate.data)), now(a.at), under_way(row, p.group_rows), used(under_way), type(p.gate_type) {}
+    __device__ __forceinline__ void copy(RowMemory<W, C>& rm) {
+        if (!a.at) return;
+        if constexpr (W > 0) {
+            rm.copy_typed(type, a.at);
+        } else if (type == T_F32) {
+            rm.template copy_pieces<T_F32>(a.at, lo, a.hi);
+        } else {
+            rm.template copy_pieces<T_F16>(a.at, lo, a.hi);
+        }
+        if (under_way.next()) a.at += a.step;
+    }
+    template <typename F>
+    __device__ __forceinline__ void take(const RowMemory<W, C>& rm, uint32_t& from, F f) {
+        if (!a.at) return;
+        if constexpr (W > 0) {
+            rm.take_typed(type, from, f);
+        } else {
+            if (type == T_F32)
+                rm.template take_pieces<T_F32>(from, now, f);
+            else if (type == T_F16)
+                rm.template take_pieces<T_F16>(from, now, f);
+            else
+                rm.template take_pieces<T_BF16>(from, now, f);
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (used.next()) now += a.step;
     }
 };
 // this thread's part of an output, a row after the other
@@ -448,37 +586,31 @@ __global__ void __launch_bounds__(CTA) norm_kernel(const __grid_constant__ NormP
     const long long units = static_cast<long long>(gridDim.x) * blockDim.y, unit = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const long long begin = norm_row(p.M, units, unit), end = norm_row(p.M, units, unit + 1);
     RowGroup group{T, t, static_cast<int>(threadIdx.y), 0, buffer};
-    RowMemory<W, C> rm{T, t, 0, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin), 0u};
+    RowMemory<W, C> rm{T, t, 0, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin), 0u, 0};
     rm.cache = smem_u32(dynamic) + t * 16;
-    rm.ring = rm.cache + p.vec_bytes + threadIdx.y * p.depth * p.row_bytes;
+    rm.ring = rm.cache + p.vec_bytes + threadIdx.y * p.depth * p.row_bytes - (W ? 0 : t * 16);
     rm.clear();
     const bool row_gate = p.gate.data && p.gate_rows > 1;
     const int col = norm_column<W>(T, t, 0);
-    Ahead ahead_y(p.y, TY, begin, col), ahead_x(p.x, TX, begin, col);
+    Stream<TY, W, C> in_y(p.y, begin, 0, col, p.M, D);
+    Stream<TX, W, C> in_x(p.x, begin, 0, col, p.M, D);
+    GateStream<W, C> in_gate(p, row_gate, begin, 0, col);
     Output<TX, W, C> out_h(p.h, begin, col);
     Output<TY, W, C> out_n(p.n, begin, col);
-    GateRow gate(begin, p.group_rows), gate_ahead(gate);
-    Ahead ahead_gate(row_gate ? p.gate : Mat{nullptr, 0, 0}, p.gate_type, gate.row, col);
     float4* to_stats = p.stats ? p.stats + begin : nullptr;
     auto issue = [&]() {
         if (rm.begin_copy()) {
-            rm.template copy<TY>(ahead_y.at);
-            ahead_y.at += ahead_y.step;
-            if (ahead_x.at) {
-                rm.template copy<TX>(ahead_x.at);
-                ahead_x.at += ahead_x.step;
-            }
-            if (row_gate) {
-                rm.copy_typed(p.gate_type, ahead_gate.at);
-                if (gate_ahead.next()) ahead_gate.at += ahead_gate.step;
-            }
+            in_y.copy(rm);
+            in_gate.copy(rm);
+            in_x.copy(rm);
         }
         rm.end_copy();
     };
     grid_wait();
     grid_release();
-    if constexpr (W > 0)
-        for (int i = 0; i < p.depth; ++i) issue();
+    // W = 0: a row's place is free again once all its threads have passed the next
+    // row's barrier, so one row less is under way
+    for (int i = 0; i < (W ? p.depth : p.depth - 1); ++i) issue();
     const Vec one_gate{row_gate ? nullptr : p.gate.data, p.gate_type};
     if (p.vec_bytes) {
         if (threadIdx.y == 0) {
@@ -493,14 +625,15 @@ __global__ void __launch_bounds__(CTA) norm_kernel(const __grid_constant__ NormP
     const float over_d = 1.f / D;
     for (long long row = begin; row < end; ++row) {
         float v[8 * C], x[8 * C];
-        const bool queued = W > 0 && p.depth > 0;
-        uint32_t from = rm.ring + rm.slot * rm.bytes;
+        const bool queued = p.depth > 0;
+        uint32_t from = rm.here();
         auto get = [&](int i, float w) { v[i] = w; };
         auto times = [&](int i, float w) { v[i] *= w; };
         auto plus = [&](int i, float w) { v[i] += w; };
         if (queued) {
-            copies_wait(p.depth - 1);
-            rm.template take<TY>(from, get);
+            rm.arrived(group);
+            if constexpr (W == 0) issue();
+            in_y.take(rm, from, get);
         } else {
             load_row<TY, W, C>(p.y, row, T, t, 0, D, v);
             if (p.x.data) load_row<TX, W, C>(p.x, row, T, t, 0, D, x);
@@ -517,26 +650,23 @@ __global__ void __launch_bounds__(CTA) norm_kernel(const __grid_constant__ NormP
         }
         // what lies past a row's end of x and of the gate in shared memory is 0
         auto add_x = [&](int i, float w) { v[i] = fmaf(p.scale, v[i], w); };
-        if (queued) {
-            if (row_gate) {
-                uint32_t gate_from = from + (p.x.data ? 8 * C / (W ? W : 1) * rm.apart() : 0u);
-                rm.take_typed(p.gate_type, gate_from, times);
-            }
-        } else if (row_gate) {
-            with_vector<W, C>(p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, T, t, 0, D, times);
-        }
+        if (queued)
+            in_gate.take(rm, from, times);
+        else if (row_gate)
+            with_vector<W, C>(p.gate.data, p.gate_type, in_gate.used.row * p.gate.rs, p.gate.cs, T, t, 0, D, times);
         rm.each(p.vec_at[4], one_gate, times, p.gate.cs);
         if (!p.x.data) {
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) v[i] *= p.scale;
         } else if (queued) {
-            rm.template take<TX>(from, add_x);
+            in_x.take(rm, from, add_x);
         } else {
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) add_x(i, x[i]);
         }
-        if constexpr (W > 0)
-            if (p.depth > 0) issue();
+        if constexpr (W > 0) {
+            if (queued) issue();
+        }
         out_h.store(rm, p.h, v);
         if (p.pre) {
             const float2 s = row_stats<W, C>(v, p.pre, p.eps, over_d, D, group);
@@ -552,9 +682,9 @@ __global__ void __launch_bounds__(CTA) norm_kernel(const __grid_constant__ NormP
             if (t == 0) *to_stats = stats;
             ++to_stats;
         }
-        gate.next();
+        in_gate.next();
     }
-    if constexpr (W > 0) copies_wait(0);
+    copies_wait(0);
 }
 
 // Rows of any length, read anew for each reduction: one CTA per row.
@@ -734,39 +864,27 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
     sums.at = dynamic + t;
     sums.T = T;
     sums.clear(all);
-    RowMemory<W, C> rm{T, t, base, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin), 0u};
+    RowMemory<W, C> rm{T, t, base, D, 0u, 0u, p.row_bytes, p.depth, 0, static_cast<int>(end - begin), 0u, 0};
     rm.cache = smem_u32(dynamic + (C == 1 ? 0 : all * 2 * C * T) + t);
-    rm.ring = rm.cache + p.vec_bytes;
+    rm.ring = rm.cache + p.vec_bytes - (W ? 0 : t * 16);
     rm.clear();
     const bool row_gate = p.gate.data && p.gate_rows > 1;
     const Vec one_gate{row_gate ? nullptr : p.gate.data, p.gate_type};
     const int col = base + norm_column<W>(T, t, 0);
-    Ahead ahead_y(p.y, TY, begin, col), ahead_x(p.x, TX, begin, col), ahead_h(g.dh, TX, begin, col), ahead_n(g.dn, TY, begin, col);
+    Stream<TY, W, C> in_y(p.y, begin, base, col, p.M, D), in_n(g.dn, begin, base, col, p.M, D);
+    Stream<TX, W, C> in_x(p.x, begin, base, col, p.M, D), in_h(g.dh, begin, base, col, p.M, D);
+    GateStream<W, C> in_gate(p, row_gate, begin, base, col);
     Output<TX, W, C> out_x(g.dx, begin, col);
     Output<TY, W, C> out_y(g.dy, begin, col);
-    GateRow gate(begin, p.group_rows), gate_ahead(gate);
-    Ahead ahead_gate(row_gate ? p.gate : Mat{nullptr, 0, 0}, p.gate_type, gate.row, col);
+    GateRow gate(begin, p.group_rows);
     const float4* stats_at = p.stats + begin;
     auto issue = [&]() {
         if (rm.begin_copy()) {
-            rm.template copy<TY>(ahead_y.at);
-            ahead_y.at += ahead_y.step;
-            if (ahead_x.at) {
-                rm.template copy<TX>(ahead_x.at);
-                ahead_x.at += ahead_x.step;
-            }
-            if (ahead_h.at) {
-                rm.template copy<TX>(ahead_h.at);
-                ahead_h.at += ahead_h.step;
-            }
-            if (ahead_n.at) {
-                rm.template copy<TY>(ahead_n.at);
-                ahead_n.at += ahead_n.step;
-            }
-            if (row_gate) {
-                rm.copy_typed(p.gate_type, ahead_gate.at);
-                if (gate_ahead.next()) ahead_gate.at += ahead_gate.step;
-            }
+            in_y.copy(rm);
+            in_x.copy(rm);
+            in_h.copy(rm);
+            in_n.copy(rm);
+            in_gate.copy(rm);
         }
         rm.end_copy();
     };
@@ -774,8 +892,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
     if (g.parts > 1) cluster_sync();
     grid_wait();
     grid_release();
-    if constexpr (W > 0)
-        for (int i = 0; i < p.depth; ++i) issue();
+    for (int i = 0; i < (W ? p.depth : p.depth - 1); ++i) issue();  // as in norm_kernel
     rm.keep(p.vec_at[0], p.post_w, 1);
     rm.keep(p.vec_at[1], p.post_b, 1);
     rm.keep(p.vec_at[2], p.pre_w, 1);
@@ -793,18 +910,19 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
         const float4 stats = next;
         if (row + 1 < end) next = *++stats_at;
         auto get = [&](int i, float w) { gv[i] = w; };
-        if (p.gate.data && (W == 0 || p.depth == 0 || p.vec_bytes == 0)) {  // read where it lies, which leaves out what is past the end
+        if (p.gate.data && (p.depth == 0 || p.vec_bytes == 0)) {  // read where it lies, which leaves out what is past the end
 #pragma unroll
             for (int i = 0; i < 8 * C; ++i) gv[i] = 0.f;
         }
-        if (W > 0 && p.depth > 0) {
-            copies_wait(p.depth - 1);
-            uint32_t from = rm.ring + rm.slot * rm.bytes;
-            rm.template take<TY>(from, [&](int i, float w) { y[i] = w; });
-            if (p.x.data) rm.template take<TX>(from, [&](int i, float w) { h[i] = w; });
-            if (g.dh.data) rm.template take<TX>(from, [&](int i, float w) { d[i] = w; });
-            if (g.dn.data) rm.template take<TY>(from, [&](int i, float w) { e[i] = w; });
-            if (row_gate) rm.take_typed(p.gate_type, from, get);
+        if (p.depth > 0) {
+            uint32_t from = rm.here();
+            rm.arrived(shared.group);
+            if constexpr (W == 0) issue();
+            in_y.take(rm, from, [&](int i, float w) { y[i] = w; });
+            in_x.take(rm, from, [&](int i, float w) { h[i] = w; });
+            in_h.take(rm, from, [&](int i, float w) { d[i] = w; });
+            in_n.take(rm, from, [&](int i, float w) { e[i] = w; });
+            in_gate.take(rm, from, get);
             if constexpr (W > 0) issue();
         } else {
             load_row<TY, W, C>(p.y, row, T, t, base, D, y);
@@ -814,10 +932,11 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
             if (row_gate) with_vector<W, C>(p.gate.data, p.gate_type, gate.row * p.gate.rs, p.gate.cs, T, t, base, D, get);
         }
         rm.each(p.vec_at[4], one_gate, get, p.gate.cs);
-        // y becomes yhat, u what the gate multiplies, h the sum and then hhat
+        // y becomes yhat, u what the gate multiplies, h the sum and then hhat.  What
+        // they are past the row's end meets zeros of dn, or of d below.
         if (p.post) {
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) y[i] = (y[i] - stats.x) * (rm.there(i) ? stats.y : 0.f);
+            for (int i = 0; i < 8 * C; ++i) y[i] = (y[i] - stats.x) * stats.y;
         }
 #pragma unroll
         for (int i = 0; i < 8 * C; ++i) u[i] = y[i];
@@ -834,7 +953,7 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
                 for (int i = 0; i < 8 * C; ++i) h[i] = fmaf(p.scale, u[i], p.x.data ? h[i] : 0.f);
             }
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) h[i] = (h[i] - stats.z) * (rm.there(i) ? stats.w : 0.f);
+            for (int i = 0; i < 8 * C; ++i) h[i] = (h[i] - stats.z) * stats.w;
             if (g.slot[0] >= 0) sums.add(0, g.slot[0], e, h);
             if (g.slot[1] >= 0) sums.add(1, g.slot[1], e);
             rm.each(p.vec_at[2], p.pre_w, [&](int i, float w) { e[i] *= w; });
@@ -876,16 +995,18 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
             for (int i = 0; i < 8 * C; ++i) d[i] *= gv[i];
         }
         if (p.post) {
+#pragma unroll
+            for (int i = 0; i < 8 * C; ++i) d[i] = rm.there(i) ? d[i] : 0.f;
             if (g.slot[2] >= 0) sums.add(2, g.slot[2], d, y);
             if (g.slot[3] >= 0) sums.add(3, g.slot[3], d);
             rm.each(p.vec_at[0], p.post_w, [&](int i, float w) { d[i] *= w; });
             float a = 0.f, b = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8 * C; ++i) a = fmaf(rm.there(i) ? d[i] : 0.f, y[i], a);
+            for (int i = 0; i < 8 * C; ++i) a = fmaf(d[i], y[i], a);
             float m0 = 0.f, m1;
             if (p.post == NORM_LAYER) {
 #pragma unroll
-                for (int i = 0; i < 8 * C; ++i) b += rm.there(i) ? d[i] : 0.f;
+                for (int i = 0; i < 8 * C; ++i) b += d[i];
                 const float2 s = shared.template sum<true>(a, b);
                 m1 = s.x * over_d;
                 m0 = s.y * over_d;
@@ -913,8 +1034,9 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
             }
         }
         gate.next();
+        in_gate.next();
     }
-    if constexpr (W > 0) copies_wait(0);
+    copies_wait(0);
 #pragma unroll
     for (int which = 0; which < 4; ++which) {
         if (g.slot[which] < 0) continue;
@@ -1029,32 +1151,40 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_long_kernel(const __grid
 }
 
 // The CTAs' sums, in the order of the CTAs: blockIdx.y names a sum over all rows,
-// or a gate row past those; 32 columns a CTA, 8 warps take every 8th part.
+// or a gate row past those; 32 columns a CTA, 8 warps take every 8th part, with
+// 20 loads of a thread under way.
 template <int DUMMY>
 __global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant__ NormFinishParams p) {
     __shared__ float part[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     grid_wait();
     grid_release();
-    for (long long what = blockIdx.y; what < p.slots + p.groups; what += gridDim.y) {
+    for (int what = blockIdx.y; what < p.slots + p.groups; what += gridDim.y) {
         const bool gate = what >= p.slots;
-        const long long group = what - p.slots;
-        long long first = 0, last = p.ctas - 1;
-        if (gate) {
+        const int group = what - p.slots;
+        int first = 0, last = p.ctas - 1;
+        if (gate && p.M > 0) {
             // the CTAs that hold the group's first and last row
             const long long r0 = group * p.group_rows, r1 = r0 + p.group_rows - 1;
-            first = r0 * p.ctas / p.M;
+            first = static_cast<int>(r0 * p.ctas / p.M);
             while (norm_row(p.M, p.ctas, first + 1) <= r0) ++first;
-            last = r1 * p.ctas / p.M;
+            last = static_cast<int>(r1 * p.ctas / p.M);
             while (norm_row(p.M, p.ctas, last + 1) <= r1) ++last;
             if (first == last) continue;  // that CTA has written it
         }
         float s = 0.f;
         if (c < p.D) {
-#pragma unroll 4
-            for (long long k = first + warp; k <= last; k += 8) {
-                const long long at = gate ? k * 2 + (k == first) : k * p.slots + what;
-                s += (gate ? p.gate_part : p.part)[at * p.D + c];
+            // a gate row begins in its first CTA, whose share lies in the second half
+            const float* at = (gate ? p.gate_part : p.part + static_cast<long long>(what) * p.D) + c;
+            const long long step = static_cast<long long>(gate ? 2 : p.slots) * p.D;
+            if (gate && warp == 0) s = at[first * step + p.D];
+            at += (first + warp) * step;
+            for (int k = first + warp; k <= last; k += 160) {
+                float v[20];
+#pragma unroll
+                for (int j = 0; j < 20; ++j, at += 8 * step) v[j] = k + 8 * j <= last && !(gate && k + 8 * j == first) ? *at : 0.f;
+#pragma unroll
+                for (int j = 0; j < 20; ++j) s += v[j];
             }
         }
         __syncthreads();
