@@ -79,16 +79,31 @@ bool rows16(const iris_b200_mat& m, int64_t rows, int64_t cols, int elem) {
 // ---------------------------------------------------------------- matmul_act
 struct Plan {
     int variant, split, stages, m_blocks, n_blocks, group_m, grid;
+    int tail_tiles, tail_parts;
 };
 
 // Estimated time in us of a variant: `slots` clusters run at once and take the
-// tiles in turn; a tile costs its stages, and what it adds at its end.
-double estimate(int v, int slots, int64_t tiles, int64_t part, int split) {
-    const double stage = v == PAIR ? 0.30 : v == HALF ? 0.20 : v == CTA ? 0.18 : v == FEW16 ? 0.20 : v == FEW32 ? 0.21 : 0.24;
-    double tile = part * stage + (is_pair(v) ? 0.6 : v == CTA ? 1.0 : 0.5);
-    if (split > 1) tile += v >= FEW16 ? 1.5 : 2.5;
-    const double rounds = static_cast<double>(cdiv(tiles, slots));
-    return 4.5 + rounds * tile + (v == PAIR ? 3.0 : v == HALF ? 1.8 : 0.0);
+// tiles in turn; a tile costs its stages, what it adds at its end and, where a
+// cluster shares it, the meeting of the parts; and no product is faster than its
+// bytes at 5.6 TB/s.  Constants fitted to 70 shapes from 512 x 512 x 512 to 4096 x
+// 4096 x 14336 in every variant and split (rms 6 to 12 %); the choice that they
+// make is on average 2 % slower than the fastest one measured.  A tail costs a
+// part's stages, an end, and 4 us for the sums' way through global memory.
+double estimate(int v, int slots, int64_t tiles, int64_t part, int split, int64_t stages, int tail_parts, double bytes) {
+    static const double start[] = {5.4, 5.2, 4.7, 3.3, 3.7, 4.1}, stage[] = {0.292, 0.256, 0.259, 0.25, 0.253, 0.254},
+                        end[] = {3.0, 1.4, 1.9, 1.8, 3.1, 4.3}, meet[] = {0, 0, 2.5, 0.9, 0, 0};
+    const double tile = part * stage[v] + end[v] + (split > 1 ? meet[v] : 0.0);
+    const double rounds = tail_parts ? static_cast<double>(tiles / slots) : static_cast<double>(cdiv(tiles, slots));
+    const double tail = tail_parts ? stages * stage[v] / tail_parts + end[v] + 4.0 : 0.0;
+    return start[v] + std::max(rounds * tile + tail, bytes / 5.6e6);
+}
+
+constexpr size_t TAIL_SUMS = 32 * 4;  // bytes per column of an epilogue warp
+size_t tail_flag_bytes(const Plan& pl) { return round_up(size_t(pl.tail_tiles) * (pl.tail_parts - 1) * 16 * 8, 256); }
+size_t tail_bytes(const Plan& pl) {
+    if (!pl.tail_tiles) return 0;
+    const size_t columns = pl.variant == PAIR ? 128 : 64;
+    return tail_flag_bytes(pl) + size_t(pl.tail_tiles) * (pl.tail_parts - 1) * 16 * columns * TAIL_SUMS;
 }
 
 int make_plan(Plan& pl, const iris_b200_config* cfg, const DeviceInfo& d, int64_t rows, int64_t cols, int64_t depth) {
@@ -101,6 +116,7 @@ int make_plan(Plan& pl, const iris_b200_config* cfg, const DeviceInfo& d, int64_
     if (cfg->k_split != 0 && cfg->k_split != 1 && cfg->k_split != 2 && cfg->k_split != 4 && cfg->k_split != 8) return IRIS_EINVAL;
     if (cfg->group_m < 0 || cfg->debug_skip_flag < 0 || cfg->grid < 0 || cfg->grid > d.sms) return IRIS_EINVAL;
     const int64_t stages = cdiv(depth, DEPTH);
+    const double bytes = 2.0 * (double(rows) * depth + double(depth) * cols + double(rows) * cols);
     double best = 0;
     pl.variant = -1;
     for (int v = PAIR; v < VARIANTS; ++v) {
@@ -116,16 +132,23 @@ int make_plan(Plan& pl, const iris_b200_config* cfg, const DeviceInfo& d, int64_
             const int slots = std::min(d.clusters[v][cg == 2 ? 1 : lg], cfg->grid ? cfg->grid / (cg * split) : INT32_MAX);
             // every part has stages, unless the config asks for it (an empty one adds zeros)
             if (slots < 1 || (cfg->k_split ? split != cfg->k_split : split > stages)) continue;
-            const double t = estimate(v, slots, tiles, part, split);
-            if (pl.variant < 0 || t < best) {
+            // Pairs: a last round with at most half of them at work is cut into 2, 3 or
+            // 4 parts of at least 16 stages (4096 x 14336 x 4096: 3.4 rounds, TAILFIG)
+            const int64_t last = tiles % slots;
+            for (int parts = 0; parts <= 4; parts = parts ? parts + 1 : 2) {
+                if (parts && (cg != 2 || last == 0 || parts * last > slots || stages < 16 * parts)) continue;
+                const double t = estimate(v, slots, tiles, part, split, stages, parts, bytes);
+                if (pl.variant >= 0 && t >= best) continue;
                 best = t;
                 pl.variant = v;
                 pl.split = split;
                 pl.m_blocks = static_cast<int>(mb);
                 pl.n_blocks = static_cast<int>(nb);
-                pl.grid = static_cast<int>(std::min<int64_t>(tiles, slots)) * cg * split;
+                pl.tail_parts = parts;
+                pl.tail_tiles = parts ? static_cast<int>(last) : 0;
+                pl.grid = static_cast<int>(std::min<int64_t>(tiles + (parts ? (parts - 1) * last : 0), slots)) * cg * split;
                 // one group holds all rows of tiles at most
-                pl.group_m = std::min(cfg->group_m ? std::max(1, cfg->group_m / cg) : 16 / cg, pl.m_blocks);
+                pl.group_m = std::min(cfg->group_m ? std::max(1, cfg->group_m / cg) : 32 / cg, pl.m_blocks);
             }
         }
     }
@@ -178,7 +201,7 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
     // few rows: the tokens are read K-major, of which there is little to copy
     Operand a = K == 0 ? none : resolve_operand(&g->A, M, K, 2, !few);
     Operand b = K == 0 ? none : resolve_operand(&g->B, K, N, 2, true);
-    const size_t total = WS_HEADER + a.copy_bytes + b.copy_bytes;
+    const size_t total = WS_HEADER + a.copy_bytes + b.copy_bytes + tail_bytes(pl);
     if (need) {
         *need = total;
         return IRIS_OK;
@@ -218,19 +241,19 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
     if (b.copy && (rc = launch_repack<uint16_t>(&g->B, b, w + WS_HEADER + a.copy_bytes, d.sms, stream))) return rc;
     const int t = g->ab_dtype == IRIS_BF16;
     const CUtensorMapDataType t16 = t ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    p.a_mn = a.transposed;
-    p.b_mn = !b.transposed;
-    // few rows: no more of a box than there are tokens (rows past a tensor's end cost
-    // the tensor memory accelerator more than rows that exist: one token 4096 x
-    // 14336 42 us with boxes of 16); what lies in the others' place reaches only
-    // sums that nobody reads
+    // MN-major: whole groups of 64 rows or columns come in one box a stage
+    p.a_mn = !a.transposed ? 0 : a.cols % 64 == 0 ? 2 : 1;
+    p.b_mn = b.transposed ? 0 : b.cols % 64 == 0 ? 2 : 1;
+    // few rows: no more of a box than there are tokens; what lies in the others'
+    // place reaches only sums that nobody reads
     const int a_rows = few ? static_cast<int>(M) : 128, b_rows = pl.variant == HALF ? 64 : 128;
-    if ((rc = make_map_2d(&p.tmA, t16, 2, a, 64, p.a_mn ? 64 : a_rows)) ||
-        (rc = make_map_2d(&p.tmB, t16, 2, b, 64, p.b_mn ? 64 : b_rows)))
-        return rc;
+    auto map_operand = [&](CUtensorMap* m, const Operand& o, int mn, int rows) {
+        return mn == 2 ? make_map_groups(m, t16, o, rows / 64) : make_map_2d(m, t16, 2, o, 64, mn ? 64 : rows);
+    };
+    if ((rc = map_operand(&p.tmA, a, p.a_mn, a_rows)) || (rc = map_operand(&p.tmB, b, p.b_mn, b_rows))) return rc;
     // few rows: the weights are the MMA's first operand
-    p.idesc = few ? idesc_of(t, t, p.b_mn, 0, 128, few_rows(pl.variant))
-                  : idesc_of(t, t, p.a_mn, p.b_mn, is_pair(pl.variant) ? 256 : 128, pl.variant == PAIR ? 256 : 128);
+    p.idesc = few ? idesc_of(t, t, p.b_mn != 0, 0, 128, few_rows(pl.variant))
+                  : idesc_of(t, t, p.a_mn != 0, p.b_mn != 0, is_pair(pl.variant) ? 256 : 128, pl.variant == PAIR ? 256 : 128);
     auto store_map = [&](CUtensorMap* m, const iris_b200_mat& x) {
         return make_store_map(m, p.type, x.data, N, M, M == 1 ? packed_pitch(N, e) : x.row_stride);
     };
@@ -243,7 +266,13 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
     p.m_blocks = pl.m_blocks;
     p.n_blocks = pl.n_blocks;
     p.group_m = pl.group_m;
-    p.n_units = pl.m_blocks * pl.n_blocks;
+    p.tail_tiles = pl.tail_tiles;
+    p.tail_parts = pl.tail_parts;
+    p.tail_first = pl.m_blocks * pl.n_blocks - pl.tail_tiles;
+    p.n_units = p.tail_first + pl.tail_tiles * pl.tail_parts;
+    char* const tail = w + WS_HEADER + a.copy_bytes + b.copy_bytes;
+    p.tail_flags = reinterpret_cast<unsigned long long*>(tail);
+    p.tail_sums = reinterpret_cast<float*>(tail + (pl.tail_tiles ? tail_flag_bytes(pl) : 0));
     p.ws = reinterpret_cast<WsHeader*>(w);
     p.wait_ns = cfg && cfg->wait_ns ? cfg->wait_ns : DEFAULT_WAIT_NS;
     p.debug_skip = cfg ? static_cast<uint32_t>(cfg->debug_skip_flag) : 0u;
@@ -462,18 +491,19 @@ int launch_norm_w(NormParams p, bool words, int sms, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     // Few rows: the more threads a row the shorter its way; many: work for a thread
     // between two reductions
-    const RowShape r = row_shape(p.D, p.M < 2 * sms ? 1 : 2, NORM_CTA);
-    // 512 threads an SM have registers enough for rows that come through shared
-    // memory (16384 x 4096, 32-bit residual: 129 us, with 1024 threads 186); loads that
-    // threads wait for want more of them (1537 x 5003: 55 us, 94 with 512)
-    const int threads = W && r.T <= NORM_MAX_T ? NORM_MAX_T : NORM_CTA;
+    RowShape r = row_shape(p.D, p.M < 2 * sms ? 1 : 2, NORM_MAX_T);
+    if (p.D > 16 * NORM_MAX_T) r = RowShape{static_cast<int>(round_up(cdiv(p.D, 16), 32)), 2};
+    // 512 threads an SM, for registers enough (16384 x 4096, 32-bit residual: 129 us,
+    // with 1024 threads 186; 1537 x 5003 f16: 40 and 59), unless a row needs more
+    const int threads = r.T <= NORM_MAX_T ? NORM_MAX_T : NORM_CTA;
     const int groups = static_cast<int>(std::min<int64_t>(std::min(16, threads / r.T), cdiv(p.M, sms)));
     const int64_t ctas = std::min<int64_t>(cdiv(p.M, groups), sms);
     size_t smem = 0;
     if (ctas * groups < p.M)  // several rows for a group
         smem = row_memory(p, r, groups, true, RowKind{W, words}, {TY, p.x.data ? TX : -1}, SM_SMEM);
-    auto kernel = r.C == 1 ? norm_kernel<TY, TX, W, 1, NORM_CTA> : norm_kernel<TY, TX, W, 2, NORM_CTA>;
-    if (W && threads == NORM_MAX_T) kernel = r.C == 1 ? norm_kernel<TY, TX, W, 1, W ? NORM_MAX_T : NORM_CTA> : norm_kernel<TY, TX, W, 2, W ? NORM_MAX_T : NORM_CTA>;
+    const auto kernel = threads == NORM_CTA ? norm_kernel<TY, TX, W, 2, NORM_CTA>
+                        : r.C == 1          ? norm_kernel<TY, TX, W, 1, NORM_MAX_T>
+                                            : norm_kernel<TY, TX, W, 2, NORM_MAX_T>;
     const int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem);
     if (rc) return rc;
     cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(ctas), r.T, smem, 1, stream, attr);

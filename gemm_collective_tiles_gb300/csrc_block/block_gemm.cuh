@@ -44,7 +44,10 @@ struct ActParams {
     int M, N, D;           // output rows and columns, contraction
     int stages_total, split;  // contraction in stages; CTAs that share a tile's
     int m_blocks, n_blocks, group_m, n_units;
-    int a_mn, b_mn;        // MN-major operands
+    int a_mn, b_mn;        // MN-major operands; 2: their maps are {64, k, row / 64}, one box a stage
+    int tail_first, tail_tiles, tail_parts;  // pairs: the last tiles are cut into parts of the contraction
+    unsigned long long* tail_flags;  // per (part but the last, tail tile, CTA, epilogue warp): its sums are there
+    float* tail_sums;                // 32 x COLS each, a column's 32 rows next to each other
     uint32_t idesc;
     const void* bias;
     int bias_type;
@@ -178,16 +181,24 @@ struct Smem {
 
 struct Unit {
     int mb, nb, lo, hi;  // tile and this CTA's stages of it
+    int tail, part;      // pairs: index of a tail tile and the part of it, or -1
 };
 // first stage of a part of the contraction; parts differ by one stage at most
 __device__ __forceinline__ int part_start(const ActParams& p, int part) {
     return static_cast<int>(static_cast<long long>(p.stages_total) * part / p.split);
 }
-// tiles in groups of group_m rows of tiles, so that the tiles running at once
-// share their operands in L2
+// Tiles in groups of group_m rows of tiles, so that the tiles running at once
+// share their operands in L2.  The tiles of a last round that would leave half of
+// the pairs idle or more are cut into parts of the contraction.
 template <int CG>
 __device__ __forceinline__ Unit unit_of(const ActParams& p, const Ctl& ctl, int u) {
     Unit x;
+    x.tail = x.part = -1;
+    if (CG == 2 && u >= p.tail_first) {  // all first parts before all second ones
+        x.part = (u - p.tail_first) / p.tail_tiles;
+        x.tail = u - p.tail_first - x.part * p.tail_tiles;
+        u = p.tail_first + x.tail;
+    }
     const int per = p.group_m * p.n_blocks;
     const int g = u / per, first = g * p.group_m;
     const int rows = min(p.group_m, p.m_blocks - first), in = u - g * per;
@@ -195,6 +206,10 @@ __device__ __forceinline__ Unit unit_of(const ActParams& p, const Ctl& ctl, int 
     x.nb = in / rows;
     x.lo = CG == 1 ? part_start(p, ctl.rank) : 0;
     x.hi = CG == 1 ? part_start(p, ctl.rank + 1) : p.stages_total;
+    if (CG == 2 && x.tail >= 0) {
+        x.lo = p.stages_total * x.part / p.tail_parts;
+        x.hi = p.stages_total * (x.part + 1) / p.tail_parts;
+    }
     return x;
 }
 template <int CG>
@@ -204,7 +219,11 @@ __device__ __forceinline__ int half(const Ctl& ctl) {
 
 // One operand's box or boxes of a stage: `n` of its rows from `row` on.
 template <int CG>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, bool mn, int row, int n, int d, uint32_t bar) {
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, int mn, int row, int n, int d, uint32_t bar) {
+    if (mn == 2) {
+        CG == 1 ? tma_load_3d(dst, m, 0, d, row / 64, bar) : tma_load_3d_pair(dst, m, 0, d, row / 64, bar);
+        return;
+    }
     if (!mn) {
         CG == 1 ? tma_load_2d(dst, m, d, row, bar) : tma_load_2d_pair(dst, m, d, row, bar);
         return;
@@ -454,7 +473,51 @@ struct Epilogue {
         return true;
     }
 
-    __device__ __forceinline__ bool whole() {
+    // where the sums of a part of a tail tile lie, of this warp
+    __device__ __forceinline__ int tail_slot(int tail, int part) const {
+        return ((part * p.tail_tiles + tail) * 2 + ctl.rank) * 8 + w;
+    }
+    __device__ __forceinline__ unsigned long long tail_ready() const {
+        return static_cast<unsigned long long>(ctl.epoch) << 32 | 0x7A115C0Du;
+    }
+    // All parts but the last leave their sums in global memory, for the same warp of
+    // the last one's pair, which runs them in the order of the parts.
+    __device__ __forceinline__ bool leave(const Unit& x) {
+        if (!acc_ready()) return false;
+        const int slot = tail_slot(x.tail, x.part);
+        float* at = p.tail_sums + static_cast<size_t>(slot) * (G::COLS * 32) + lane;
+#pragma unroll 1
+        for (int c = 0; c < G::COLS / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(acc_at(c), r);
+            tmem_wait_regs(r);
+            if (c == G::COLS / 32 - 1) hand_back();
+#pragma unroll
+            for (int i = 0; i < 32; ++i, at += 32) *at = __uint_as_float(r[i]);
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) st_release_gpu_u64(p.tail_flags + slot, tail_ready());
+        return true;
+    }
+    __device__ __forceinline__ bool tail_there(int tail) {
+        for (int part = 0; part < p.tail_parts - 1; ++part) {
+            const unsigned long long* flag = p.tail_flags + tail_slot(tail, part);
+            const uint64_t t0 = global_timer_ns();
+            while (ld_acquire_gpu_u64(flag) != tail_ready()) {
+                __nanosleep(100);
+                if (launch_aborted(ctl)) return false;
+                if (global_timer_ns() - t0 > ctl.limit) {
+                    raise_timeout(ctl, WAIT_TAIL, tail);
+                    return false;
+                }
+            }
+        }
+        __syncwarp();
+        return true;
+    }
+
+    __device__ __forceinline__ bool whole(int tail) {
         const bool wide = p.type == T_F32;
         const int per = wide ? 1 : 2;  // 32-column groups of a box
         const int boxes = min(G::COLS / 32 / per, (p.N - col0 + 32 * per - 1) / (32 * per));
@@ -468,6 +531,7 @@ struct Epilogue {
             }
         }
         if (!acc_ready()) return false;
+        if (CG == 2 && tail >= 0 && !tail_there(tail)) return false;
         const int groups = boxes * per;
 #pragma unroll 1
         for (int c = 0; c < groups; ++c) {
@@ -480,6 +544,19 @@ struct Epilogue {
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            if (CG == 2 && tail >= 0) {
+                float sum[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+#pragma unroll 1
+                for (int part = 0; part < p.tail_parts - 1; ++part) {
+                    const float* at = p.tail_sums + static_cast<size_t>(tail_slot(tail, part)) * (G::COLS * 32) + c * 1024 + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[i] += __ldcg(at + i * 32);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += sum[i];
+            }
             if (p.bias) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
@@ -609,7 +686,7 @@ struct Epilogue {
                     continue;
                 }
             }
-            if (!whole()) break;
+            if (CG == 2 && x.tail >= 0 && x.part < p.tail_parts - 1 ? !leave(x) : !whole(x.tail)) break;
         }
         for (uint32_t s = 0; s < 2; ++s) landed(s, WAIT_DRAIN_TMA);  // where the launch stopped
         if (lane == 0) bulk_wait_all();  // its stores have left shared memory

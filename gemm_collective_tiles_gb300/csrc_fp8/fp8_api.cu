@@ -57,15 +57,6 @@ int device_info(DeviceInfo* out) {
     return IRIS_OK;
 }
 
-// 16-bit rows as groups of 64 columns, {64, row, column / 64}: a box of 64 rows
-// of `groups` groups, 8192 bytes each
-int make_map_groups(CUtensorMap* m, CUtensorMapDataType dt, const Operand& o, uint32_t groups) {
-    cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(o.rows), static_cast<cuuint64_t>(o.cols / 64)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.pitch) * 2, 128};
-    cuuint32_t box[3] = {64, 64, groups};
-    const CUresult r = encode(m, dt, 3, o.data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (groups of columns)", static_cast<int>(r));
-}
 // Tile, split and workspace of one product (rows x cols over depth).
 struct Plan {
     Variant variant;

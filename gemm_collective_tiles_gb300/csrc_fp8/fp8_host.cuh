@@ -206,6 +206,15 @@ int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand&
     const CUresult r = encode(m, dt, 2, o.data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit operand)", static_cast<int>(r));
 }
+// 16-bit rows as groups of 64 columns, {64, row, column / 64}: a box of 64 rows
+// of `groups` groups, 8192 bytes each
+int make_map_groups(CUtensorMap* m, CUtensorMapDataType dt, const Operand& o, uint32_t groups) {
+    cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(o.rows), static_cast<cuuint64_t>(o.cols / 64)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.pitch) * 2, 128};
+    cuuint32_t box[3] = {64, 64, groups};
+    const CUresult r = encode(m, dt, 3, o.data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (groups of columns)", static_cast<int>(r));
+}
 // out {n, row} with a box of 128 bytes x 32 rows
 int make_store_map(CUtensorMap* m, int t, const void* data, int64_t N, int64_t M, int64_t pitch) {
     const int elem = dtype_size(t);

@@ -110,6 +110,35 @@ def test_operand_layouts(la, lb, config):
     check_ints(200, 328, 200, layouts=(la, lb, "rows"), config=config)
 
 
+@pytest.mark.parametrize("config", [PAIR, HALF, CTA, dict(tile_m=128, k_split=4)], ids=["pair", "half", "cta", "split"])
+def test_operands_of_whole_groups(config):
+    """Rows and columns in multiples of 64: other boxes, which may lie partly past the end."""
+    for M, N in ((64, 64), (320, 448), (576, 704)):
+        for layouts in (("cols", "rows", "rows"), ("cols", "cols", "rows"), ("rows", "rows", "rows")):
+            check_ints(M, N, 264, layouts=layouts, config=config)
+
+
+@pytest.mark.parametrize("config", [PAIR, HALF], ids=["pair", "half"])
+@pytest.mark.parametrize("M,N,K", [(512, 2000, 8192), (250, 250, 4096), (2100, 4300, 4096), (1000, 1300, 6200)])
+def test_tail_tiles(M, N, K, config):
+    """Last rounds that are cut along the contraction: their sums take memory, and meet in the order of the parts."""
+    A, out = torch.ones(M, K, device="cuda").bfloat16(), torch.empty(M, N, device="cuda")
+    ws = gct.matmul_act(A, torch.ones(K, N, device="cuda").bfloat16(), out, config=config)
+    assert (out == K).all() and ws.nbytes > 256 + 16 * 32 * 64 * 4
+    check_ints(M, N, K, layouts=("cols", "rows", "rows"), config=config, z=True, act="relu", p=0.5)
+    g = generator(2)
+    A, B = torch.randn(M, K, generator=g, device="cuda").half(), torch.randn(K, N, generator=g, device="cuda").half()
+    gct.matmul_act(A, B, out, config=config, workspace=ws)
+    for _ in range(3):
+        again = torch.empty_like(out)
+        gct.matmul_act(A, B, again, config=config, workspace=ws)
+        assert torch.equal(again, out)
+    gct.matmul_act(A, B, again, config=dict(config, debug_skip_flag=1, wait_ns=20_000_000), workspace=ws)
+    assert gct.query_status(ws)[0] == gct._native.IRIS_ETIMEOUT
+    gct.matmul_act(A, B, again, config=config, workspace=ws)
+    assert torch.equal(again, out)
+
+
 @pytest.mark.parametrize("config", [PAIR, HALF, CTA, dict(tile_m=128, k_split=2)], ids=["pair", "half", "cta", "split"])
 @pytest.mark.parametrize("lo", LAYOUTS)
 @pytest.mark.parametrize("out_dtype", [BF, F32])
