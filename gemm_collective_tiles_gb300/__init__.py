@@ -26,8 +26,9 @@ Block-scaled 8-bit floats (``fp8.py``), on plain device tensors:
 The sides of a block's linear layers (``block.py``), on plain device tensors:
 
 * ``matmul_act``       out = residual + dropout(act(A @ B + bias))
-* ``act_grad``         the gradient of that epilogue
-* ``linear_act``       the two and their products as one differentiable layer
+* ``act_grad``         the gradient of that epilogue; ``linear_act_grad`` with the
+  products of its result
+* ``linear_act``       the differentiable layer
 * ``dropout_add``      out = residual + dropout(x); ``dropout`` is differentiable
 * ``norm_join``        norm, gate, scale and residual at a block's end and the
   next block's norm; ``norm_join_grad``, and ``block_norm`` as a layer
@@ -67,7 +68,7 @@ __all__ = [
     "all_gather_matmul", "matmul_reduce_scatter", "matmul_all_gather", "matmul_all_reduce",
     "concurrent_gemm_collective", "concurrent_two_stream", "query_status", "num_sms", "IrisError",
     "empty_fp8", "quantize_fp8", "matmul_fp8", "weight_grad_fp8", "fp8_linear", "fp8_workspace",
-    "matmul_act", "act_grad", "linear_act", "dropout_add", "dropout", "norm_join", "norm_join_grad", "block_norm",
+    "matmul_act", "act_grad", "linear_act_grad", "linear_act", "dropout_add", "dropout", "norm_join", "norm_join_grad", "block_norm",
 ]
 
 _DT = {torch.float16: _native.IRIS_F16, torch.bfloat16: _native.IRIS_BF16,
@@ -394,4 +395,4 @@ def num_sms() -> int:
 
 from .fp8 import empty_fp8, fp8_linear, fp8_workspace, matmul_fp8, quantize_fp8, weight_grad_fp8  # noqa: E402
 from .block import (  # noqa: E402
-    act_grad, block_norm, dropout, dropout_add, linear_act, matmul_act, norm_join, norm_join_grad)
+    act_grad, block_norm, dropout, dropout_add, linear_act, linear_act_grad, matmul_act, norm_join, norm_join_grad)

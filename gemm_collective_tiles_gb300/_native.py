@@ -55,6 +55,8 @@ EXPORTS = (
     "iris_b200_matmul_act",
     "iris_b200_act_grad_workspace_size",
     "iris_b200_act_grad",
+    "iris_b200_linear_act_grad_workspace_size",
+    "iris_b200_linear_act_grad",
     "iris_b200_dropout",
     "iris_b200_norm_join",
     "iris_b200_norm_join_grad_workspace_size",
@@ -115,6 +117,8 @@ pack_weight_grad_fp8 = struct.Struct("@15q4i").pack  # X, x_scales, dY, out; M, 
 # Those of the operators around linear layers; an absent matrix or vector is 0.
 pack_matmul_act = struct.Struct("@20qd4i").pack  # A, B, out, residual, z; bias, rng; M, N, K; p; 3 types, act
 pack_act_grad = struct.Struct("@13qd4i").pack    # dy, z, dz; dbias, rng; M, N; p; 3 types, act
+# dy, x, weight, z, dx, dweight; dbias, rng; M, N, K; p; 2 types, act, 0
+pack_linear_act_grad = struct.Struct("@23qd4i").pack
 pack_dropout = struct.Struct("@12qd2i").pack     # x, residual, out; rng; M, N; p; type, 0
 # y, x, gate, h, n; 4 vectors; stats; M, D, gate rows; scale, eps; 7 types, post, pre, 0
 pack_norm_join = struct.Struct("@23q2d10i").pack
@@ -151,6 +155,8 @@ def _declare(lib):
         "iris_b200_matmul_act": (ci, [args, cfgp, vp, sz, vp]),
         "iris_b200_act_grad_workspace_size": (ci, [args, cfgp, P(sz)]),
         "iris_b200_act_grad": (ci, [args, cfgp, vp, sz, vp]),
+        "iris_b200_linear_act_grad_workspace_size": (ci, [args, cfgp, P(sz)]),
+        "iris_b200_linear_act_grad": (ci, [args, cfgp, vp, sz, vp]),
         "iris_b200_dropout": (ci, [args, vp]),
         "iris_b200_norm_join": (ci, [args, vp]),
         "iris_b200_norm_join_grad_workspace_size": (ci, [args, cfgp, P(sz)]),

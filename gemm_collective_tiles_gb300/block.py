@@ -125,6 +125,46 @@ def act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], dz: Optional[torch.Ten
     return _sums("act_grad", args, [t for t in (dz, dbias) if t is not None], workspace, index, stream)
 
 
+def linear_act_grad(dy: torch.Tensor, x: Optional[torch.Tensor], weight: Optional[torch.Tensor], z: Optional[torch.Tensor],
+                    dx: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                    dbias: Optional[torch.Tensor] = None, act: Optional[str] = None, p: float = 0.0,
+                    rng: Optional[torch.Tensor] = None, workspace=None, stream=None):
+    """The gradients of residual + dropout(act(x @ weight + bias)) in one call:
+    dz = dropout(dy) act'(z), dx = dz @ weight^T, dweight = x^T @ dz, dbias = the
+    column sums of dz.
+
+    dy (M, N), x (M, K), weight (K, N), z (M, N) (None without an activation), dx
+    and dweight f16 or bf16, the same type; dbias (N,) f16, bf16 or f32.  Each of
+    the three gradients may be None, and x or weight with the one that reads it.
+    dz is rounded to that type, for the products, and lies in the workspace, which
+    is returned."""
+    a = _choice("activation", act, _ACTS)
+    md, M, N, index = _lead("dy", dy, _DT16)
+    types = (dy.dtype,)
+    if a and z is None:
+        raise ValueError("the gradient of an activation needs z")
+    mz = _mat("z", z, (M, N), types, index) if a else _NO_MAT
+    K = 0
+    mx = mw = mdx = mdw = _NO_MAT
+    if dx is not None:
+        mw, K, _, _ = _lead("weight", weight, types)
+        mw = _mat("weight", weight, (K, N), types, index)
+        mdx = _mat("dx", dx, (M, K), types, index)
+    if dweight is not None:
+        mx, _, k, _ = _lead("x", x, types)
+        if dx is not None and k != K:
+            raise ValueError(f"x has {k} columns and weight has {K} rows")
+        K = k
+        mx = _mat("x", x, (M, K), types, index)
+        mdw = _mat("dweight", dweight, (K, N), types, index)
+    bias_ptr, bias_dt = 0, 0
+    if dbias is not None:
+        bias_ptr, bias_dt = _vec("dbias", dbias, N, _DT, index), _DT[dbias.dtype]
+    args = _native.pack_linear_act_grad(*md, *mx, *mw, *mz, *mdx, *mdw, bias_ptr, _rng(p, rng, index), M, N, K, p,
+                                        _DT[dy.dtype], bias_dt, a, 0)
+    return _sums("linear_act_grad", args, [t for t in (dx, dweight, dbias) if t is not None], workspace, index, stream)
+
+
 def _sums(name: str, args, outs, workspace, index: int, stream):
     """A call whose workspace holds sums over rows."""
     ws = _product(name, getattr(_native.load(), "iris_b200_" + name), args, outs[0], None, workspace, index, stream) \
@@ -250,25 +290,24 @@ def norm_join_grad(y: torch.Tensor, stats: torch.Tensor, dh: Optional[torch.Tens
 
 def _rows(t: Optional[torch.Tensor], cols: int):
     """(..., cols) as a matrix; sizes of zero among them."""
-    return None if t is None else t.reshape(math.prod(t.shape[:-1]), cols)
+    return t if t is None or t.dim() == 2 else t.reshape(math.prod(t.shape[:-1]), cols)
 
 
 class _LinearAct(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, act, residual, p, rng, workspace):
         K, N = weight.shape
-        x2 = _rows(x, K)
-        M = x2.shape[0]
-        y = torch.empty(M, N, dtype=x.dtype, device=x.device)
+        x2, dev = _rows(x, K), x.device
+        y = torch.empty(x2.shape[0], N, dtype=x.dtype, device=dev)
         z = None
         if act is not None and any(ctx.needs_input_grad[:3]):
-            z = torch.empty(M, N, dtype=x.dtype, device=x.device)
+            z = torch.empty(x2.shape[0], N, dtype=x.dtype, device=dev)
         matmul_act(x2, weight, y, bias=bias, act=act, residual=_rows(residual, N), z=z, p=p, rng=rng,
-                   workspace=_layer_workspace(workspace, x.device))
+                   workspace=_layer_workspace(workspace, dev))
         ctx.save_for_backward(x, weight, z, rng)
         ctx.act, ctx.p, ctx.workspace = act, p, workspace
         ctx.bias_dtype = None if bias is None else bias.dtype
-        return y.reshape(*x.shape[:-1], N)
+        return y if x.dim() == 2 else y.reshape(*x.shape[:-1], N)
 
     # the kernels' gradients have no derivatives of their own: asking for second
     # ones is an error, not a sum without some of its terms
@@ -277,26 +316,19 @@ class _LinearAct(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, z, rng = ctx.saved_tensors
         K, N = weight.shape
-        x2, dy2 = _rows(x, K), _rows(dy, N)
-        ws = _layer_workspace(ctx.workspace, dy.device)
+        want_x, want_w, want_b = ctx.needs_input_grad[:3]
         dx = dw = db = None
-        want_db = ctx.bias_dtype is not None and ctx.needs_input_grad[2]
-        if ctx.needs_input_grad[0] or ctx.needs_input_grad[1] or want_db:
-            dz = dy2
-            # z of a layer without an activation is not kept: its derivative is 1
-            if z is not None or ctx.p > 0:
-                dz = torch.empty_like(dy2, memory_format=torch.contiguous_format)
-            if want_db:
-                db = torch.empty(N, dtype=ctx.bias_dtype, device=dy.device)
-            if want_db or dz is not dy2:
-                act_grad(dy2, z, None if dz is dy2 else dz, db, act=ctx.act, p=ctx.p, rng=rng, workspace=ws)
-        if ctx.needs_input_grad[0]:
-            dx = torch.empty(x2.shape, dtype=x.dtype, device=dy.device)
-            matmul_act(dz, weight.t(), dx, workspace=ws)
-            dx = dx.reshape(x.shape)
-        if ctx.needs_input_grad[1]:
-            dw = torch.empty(K, N, dtype=weight.dtype, device=dy.device)
-            matmul_act(x2.t(), dz, dw, workspace=ws)
+        if want_x or want_w or want_b:
+            x2, dy2 = _rows(x, K), _rows(dy, N)
+            dev = dy.device
+            if want_x:
+                dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            if want_w:
+                dw = torch.empty(K, N, dtype=weight.dtype, device=dev)
+            if want_b:
+                db = torch.empty(N, dtype=ctx.bias_dtype, device=dev)
+            linear_act_grad(dy2, x2, weight, z, _rows(dx, K), dw, db, act=ctx.act, p=ctx.p, rng=rng,
+                            workspace=_layer_workspace(ctx.workspace, dev))
         return dx, dw, db, None, dy if ctx.needs_input_grad[4] else None, None, None, None
 
 

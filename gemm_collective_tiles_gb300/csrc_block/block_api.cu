@@ -87,14 +87,15 @@ struct Plan {
 // cluster shares it, the meeting of the parts; and no product is faster than its
 // bytes at 5.6 TB/s.  Constants fitted to 70 shapes from 512 x 512 x 512 to 4096 x
 // 4096 x 14336 in every variant and split (rms 6 to 12 %); the choice that they
-// make is on average 2 % slower than the fastest one measured.  A tail costs a
-// part's stages, an end, and 4 us for the sums' way through global memory.
+// make is on average 2 % slower than the fastest one measured.   A tail costs a
+// part's stages, an end, and the sums' way through global memory (5 to 11 us of 256
+// columns, by the parts).
 double estimate(int v, int slots, int64_t tiles, int64_t part, int split, int64_t stages, int tail_parts, double bytes) {
     static const double start[] = {5.4, 5.2, 4.7, 3.3, 3.7, 4.1}, stage[] = {0.292, 0.256, 0.259, 0.25, 0.253, 0.254},
                         end[] = {3.0, 1.4, 1.9, 1.8, 3.1, 4.3}, meet[] = {0, 0, 2.5, 0.9, 0, 0};
     const double tile = part * stage[v] + end[v] + (split > 1 ? meet[v] : 0.0);
     const double rounds = tail_parts ? static_cast<double>(tiles / slots) : static_cast<double>(cdiv(tiles, slots));
-    const double tail = tail_parts ? stages * stage[v] / tail_parts + end[v] + 4.0 : 0.0;
+    const double tail = tail_parts ? stages * stage[v] / tail_parts + end[v] + (v == PAIR ? 3.0 * tail_parts - 1.0 : 3.5) : 0.0;
     return start[v] + std::max(rounds * tile + tail, bytes / 5.6e6);
 }
 
@@ -133,7 +134,8 @@ int make_plan(Plan& pl, const iris_b200_config* cfg, const DeviceInfo& d, int64_
             // every part has stages, unless the config asks for it (an empty one adds zeros)
             if (slots < 1 || (cfg->k_split ? split != cfg->k_split : split > stages)) continue;
             // Pairs: a last round with at most half of them at work is cut into 2, 3 or
-            // 4 parts of at least 16 stages (4096 x 14336 x 4096: 3.4 rounds, TAILFIG)
+            // 4 parts of at least 16 stages (4096 x 14336 x 4096, 3.4 rounds: 278 us whole, 254 in 2;
+            // 1024 x 16384 x 1024, 16 tiles: 76, 48 in 2, 37 in 4)
             const int64_t last = tiles % slots;
             for (int parts = 0; parts <= 4; parts = parts ? parts + 1 : 2) {
                 if (parts && (cg != 2 || last == 0 || parts * last > slots || stages < 16 * parts)) continue;
@@ -181,15 +183,16 @@ int check_matmul_act(const iris_b200_matmul_act_args* g, Drop& drop) {
     return g->z.data ? check_out(&g->z, g->M, g->N, e) : IRIS_OK;
 }
 
+// `reserve`: bytes behind the workspace's header that are the caller's
 int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, void* ws, size_t ws_bytes, cudaStream_t stream,
-               size_t* need) {
+               size_t* need, size_t reserve = 0) {
     ActParams p;
     std::memset(&p, 0, sizeof(p));
     int rc = check_matmul_act(g, p.drop);
     if (rc) return rc;
     const int64_t M = g->M, N = g->N, K = g->K;
     if (M == 0 || N == 0) {
-        if (need) *need = WS_HEADER;
+        if (need) *need = WS_HEADER + reserve;
         return IRIS_OK;
     }
     DeviceInfo d;
@@ -201,7 +204,7 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
     // few rows: the tokens are read K-major, of which there is little to copy
     Operand a = K == 0 ? none : resolve_operand(&g->A, M, K, 2, !few);
     Operand b = K == 0 ? none : resolve_operand(&g->B, K, N, 2, true);
-    const size_t total = WS_HEADER + a.copy_bytes + b.copy_bytes + tail_bytes(pl);
+    const size_t copies = WS_HEADER + reserve, total = copies + a.copy_bytes + b.copy_bytes + tail_bytes(pl);
     if (need) {
         *need = total;
         return IRIS_OK;
@@ -237,8 +240,8 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
                       launch_config(static_cast<unsigned>(std::min<int64_t>(n, int64_t(d.sms) * 8)), 256, 0, 1, stream, attr), p);
     }
     char* w = static_cast<char*>(ws);
-    if (a.copy && (rc = launch_repack<uint16_t>(&g->A, a, w + WS_HEADER, d.sms, stream))) return rc;
-    if (b.copy && (rc = launch_repack<uint16_t>(&g->B, b, w + WS_HEADER + a.copy_bytes, d.sms, stream))) return rc;
+    if (a.copy && (rc = launch_repack<uint16_t>(&g->A, a, w + copies, d.sms, stream))) return rc;
+    if (b.copy && (rc = launch_repack<uint16_t>(&g->B, b, w + copies + a.copy_bytes, d.sms, stream))) return rc;
     const int t = g->ab_dtype == IRIS_BF16;
     const CUtensorMapDataType t16 = t ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     // MN-major: whole groups of 64 rows or columns come in one box a stage
@@ -270,7 +273,7 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
     p.tail_parts = pl.tail_parts;
     p.tail_first = pl.m_blocks * pl.n_blocks - pl.tail_tiles;
     p.n_units = p.tail_first + pl.tail_tiles * pl.tail_parts;
-    char* const tail = w + WS_HEADER + a.copy_bytes + b.copy_bytes;
+    char* const tail = w + copies + a.copy_bytes + b.copy_bytes;
     p.tail_flags = reinterpret_cast<unsigned long long*>(tail);
     p.tail_sums = reinterpret_cast<float*>(tail + (pl.tail_tiles ? tail_flag_bytes(pl) : 0));
     p.ws = reinterpret_cast<WsHeader*>(w);
@@ -307,7 +310,7 @@ int launch_act_grad(const ActGradParams& p, bool vec, unsigned grid, cudaStream_
                   launch_config(grid, 256, 0, 1, stream, attr), p);
 }
 
-int act_grad(const iris_b200_act_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
+int act_grad(const iris_b200_act_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need, size_t reserve = 0) {
     int rc;
     ActGradParams p;
     std::memset(&p, 0, sizeof(p));
@@ -322,7 +325,7 @@ int act_grad(const iris_b200_act_grad_args* g, void* ws, size_t ws_bytes, cudaSt
     // sums beside the tensors.
     p.rows = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(16, round_up(cdiv(M * p.segs, 2048), 8))));
     const int64_t blocks = cdiv(M, p.rows);
-    const size_t total = WS_HEADER + (g->dbias ? static_cast<size_t>(blocks) * N * 4 : 0);
+    const size_t total = WS_HEADER + reserve + (g->dbias ? static_cast<size_t>(blocks) * N * 4 : 0);
     if (need) {
         *need = total;
         return IRIS_OK;
@@ -331,7 +334,7 @@ int act_grad(const iris_b200_act_grad_args* g, void* ws, size_t ws_bytes, cudaSt
     if (g->dbias) {
         if (!ws || ws_bytes < total) return IRIS_ENOWS;
         if (!aligned16(ws)) return IRIS_EALIGN;
-        p.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER);
+        p.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER + reserve);
     }
     if (M > 0) {
         if (blocks * p.segs > 0x7FFFFFFF) return IRIS_EINVAL;
@@ -356,6 +359,80 @@ int act_grad(const iris_b200_act_grad_args* g, void* ws, size_t ws_bytes, cudaSt
     cudaLaunchAttribute attr[2];
     return launch("column sum launch", column_sum_kernel<0>,
                   launch_config(static_cast<unsigned>(cdiv(N, 32)), 256, 0, 1, stream, attr), c);
+}
+
+// ---------------------------------------------------------------- linear_act_grad
+// act_grad, then the two products of its result, which lies in the workspace in
+// rows of whole 16 bytes where it is anything but dy.
+int linear_act_grad(const iris_b200_linear_act_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
+    int rc;
+    Drop drop;
+    if (!g || !dims_ok(g->M, g->N, g->K) || !dtype16(g->dtype) || !act_ok(g->act) || g->reserved) return IRIS_EINVAL;
+    if ((rc = set_drop(drop, g->p, g->rng))) return rc;
+    const int64_t M = g->M, N = g->N, K = g->K;
+    if ((rc = check_in(&g->dy, M, N, 2)) || (g->dx.data && ((rc = check_in(&g->weight, K, N, 2)) || (rc = check_out(&g->dx, M, K, 2)))) ||
+        (g->dweight.data && ((rc = check_in(&g->x, M, K, 2)) || (rc = check_out(&g->dweight, K, N, 2)))))
+        return rc;
+    const bool products = g->dx.data || g->dweight.data, own = products && (g->act != IRIS_ACT_NONE || drop.least);
+    iris_b200_mat dz = g->dy;
+    size_t reserve = 0;
+    iris_b200_act_grad_args a;
+    std::memset(&a, 0, sizeof(a));
+    if (own) {
+        const int64_t pitch = packed_pitch(N, 2);
+        reserve = round_up(static_cast<size_t>(M) * pitch * 2, 256);
+        dz = iris_b200_mat{ws ? static_cast<char*>(ws) + WS_HEADER : reinterpret_cast<void*>(16), pitch, 1};
+        a.dz = dz;
+    }
+    a.dy = g->dy;
+    a.z = g->z;
+    a.dbias = g->dbias;
+    a.rng = g->rng;
+    a.M = M;
+    a.N = N;
+    a.p = g->p;
+    a.dtype = a.dz_dtype = g->dtype;
+    a.dbias_dtype = g->dbias_dtype;
+    a.act = g->act;
+    iris_b200_matmul_act_args m[2];
+    std::memset(m, 0, sizeof(m));
+    auto transposed = [](const iris_b200_mat& x) { return iris_b200_mat{x.data, x.col_stride, x.row_stride}; };
+    m[0].A = dz;  // dx = dz weight^T
+    m[0].B = transposed(g->weight);
+    m[0].out = g->dx;
+    m[0].M = M;
+    m[0].N = K;
+    m[0].K = N;
+    m[1].A = transposed(g->x);  // dweight = x^T dz
+    m[1].B = dz;
+    m[1].out = g->dweight;
+    m[1].M = K;
+    m[1].N = N;
+    m[1].K = M;
+    size_t total = WS_HEADER + reserve;
+    for (int run = 0; run < 2; ++run) {  // sizes first: nothing is launched where one of the three would be refused
+        size_t n = 0;
+        size_t* const size = run ? nullptr : &n;
+        if (run) {
+            if (need) {
+                *need = total;
+                return IRIS_OK;
+            }
+            if (!ws || ws_bytes < total) return IRIS_ENOWS;
+            if (!aligned16(ws)) return IRIS_EALIGN;
+        }
+        if (own || g->dbias) {
+            if ((rc = act_grad(&a, ws, ws_bytes, stream, size, reserve))) return rc;
+            total = std::max(total, n);
+        }
+        for (iris_b200_matmul_act_args& x : m) {
+            if (!x.out.data) continue;
+            x.ab_dtype = x.out_dtype = g->dtype;
+            if ((rc = matmul_act(&x, nullptr, ws, ws_bytes, stream, size, reserve))) return rc;
+            total = std::max(total, n);
+        }
+    }
+    return IRIS_OK;
 }
 
 // ---------------------------------------------------------------- norms
@@ -661,6 +738,13 @@ int iris_b200_act_grad_workspace_size(const iris_b200_act_grad_args* args, const
 int iris_b200_act_grad(const iris_b200_act_grad_args* args, const iris_b200_config*, void* workspace, size_t workspace_bytes,
                        cudaStream_t stream) {
     return act_grad(args, workspace, workspace_bytes, stream, nullptr);
+}
+int iris_b200_linear_act_grad_workspace_size(const iris_b200_linear_act_grad_args* args, const iris_b200_config*, size_t* bytes) {
+    return bytes ? linear_act_grad(args, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;
+}
+int iris_b200_linear_act_grad(const iris_b200_linear_act_grad_args* args, const iris_b200_config*, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+    return linear_act_grad(args, workspace, workspace_bytes, stream, nullptr);
 }
 
 int iris_b200_dropout(const iris_b200_dropout_args* g, cudaStream_t stream) {

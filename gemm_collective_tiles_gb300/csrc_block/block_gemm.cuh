@@ -47,7 +47,7 @@ struct ActParams {
     int a_mn, b_mn;        // MN-major operands; 2: their maps are {64, k, row / 64}, one box a stage
     int tail_first, tail_tiles, tail_parts;  // pairs: the last tiles are cut into parts of the contraction
     unsigned long long* tail_flags;  // per (part but the last, tail tile, CTA, epilogue warp): its sums are there
-    float* tail_sums;                // 32 x COLS each, a column's 32 rows next to each other
+    float* tail_sums;                // 32 x COLS each, in fours of columns, 32 rows next to each other
     uint32_t idesc;
     const void* bias;
     int bias_type;
@@ -485,7 +485,7 @@ struct Epilogue {
     __device__ __forceinline__ bool leave(const Unit& x) {
         if (!acc_ready()) return false;
         const int slot = tail_slot(x.tail, x.part);
-        float* at = p.tail_sums + static_cast<size_t>(slot) * (G::COLS * 32) + lane;
+        float4* at = reinterpret_cast<float4*>(p.tail_sums + static_cast<size_t>(slot) * (G::COLS * 32)) + lane;
 #pragma unroll 1
         for (int c = 0; c < G::COLS / 32; ++c) {
             uint32_t r[32];
@@ -493,7 +493,8 @@ struct Epilogue {
             tmem_wait_regs(r);
             if (c == G::COLS / 32 - 1) hand_back();
 #pragma unroll
-            for (int i = 0; i < 32; ++i, at += 32) *at = __uint_as_float(r[i]);
+            for (int j = 0; j < 8; ++j, at += 32)
+                *at = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
         }
         __threadfence();
         __syncwarp();
@@ -550,9 +551,15 @@ struct Epilogue {
                 for (int i = 0; i < 32; ++i) sum[i] = 0.f;
 #pragma unroll 1
                 for (int part = 0; part < p.tail_parts - 1; ++part) {
-                    const float* at = p.tail_sums + static_cast<size_t>(tail_slot(tail, part)) * (G::COLS * 32) + c * 1024 + lane;
+                    const float4* at = reinterpret_cast<const float4*>(p.tail_sums + static_cast<size_t>(tail_slot(tail, part)) * (G::COLS * 32)) + c * 256 + lane;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[i] += __ldcg(at + i * 32);
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 f = __ldcg(at + j * 32);
+                        sum[4 * j] += f.x;
+                        sum[4 * j + 1] += f.y;
+                        sum[4 * j + 2] += f.z;
+                        sum[4 * j + 3] += f.w;
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += sum[i];

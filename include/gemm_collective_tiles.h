@@ -638,6 +638,29 @@ IRIS_API int iris_b200_act_grad(const iris_b200_act_grad_args* args, const iris_
                                 size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * linear_act_grad -- the gradients of out = residual + dropout(act(x @ weight +
+ * bias)) from dy in one call: dz = dropout(dy) act'(z) in dtype (dy itself without
+ * either), dx = dz @ weight^T, dweight = x^T @ dz, dbias = the column sums of dz
+ * before its rounding.  dx, dweight (of dtype) and dbias may be absent, and with
+ * them what only they read.  dz lies in the workspace.  No config.
+ */
+typedef struct {
+    iris_b200_mat dy, x, weight, z, dx, dweight; /* M x N, M x K, K x N, M x N, M x K, K x N */
+    void* dbias;
+    const int64_t* rng;
+    int64_t M, N, K;
+    double p;
+    int32_t dtype, dbias_dtype; /* iris_dtype; dtype: f16 or bf16 */
+    int32_t act;
+    int32_t reserved;           /* 0 */
+} iris_b200_linear_act_grad_args;
+
+IRIS_API int iris_b200_linear_act_grad_workspace_size(const iris_b200_linear_act_grad_args* args,
+                                                      const iris_b200_config* cfg, size_t* bytes);
+IRIS_API int iris_b200_linear_act_grad(const iris_b200_linear_act_grad_args* args, const iris_b200_config* cfg,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * dropout -- out = residual + dropout(x), all M x N of one type; out may be x or
  * residual itself.  The gradient of x is the same call on out's.
  */
