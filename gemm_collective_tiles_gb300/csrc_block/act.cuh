@@ -17,75 +17,133 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two values at once: packed fp32 arithmetic issues once for both, each rounded to
+// nearest as by itself; the special functions take one after the other.
+struct Two {
+    unsigned long long v;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
+    __device__ __forceinline__ void get(float& a, float& b) const { fp8::unpack_f32x2(v, a, b); }
+    template <typename F>
+    __device__ __forceinline__ Two map(F f) const {
+        float a, b;
+        get(a, b);
+        return Two(f(a), f(b));
+    }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+    Two d;
+    d.v = fp8::fma_f32x2(a.v, b.v, c.v);
+    return d;
+}
+
 constexpr float LOG2E = 1.44269504088896f;
 constexpr float GELU_ROOT = 1.59576912160573f;  // 2 sqrt(2 / pi)
 constexpr float GELU_CUBE = 0.044715f;
 
-__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + exp2_approx(-LOG2E * x)); }
+// 1 / (1 + 2^t)
+__device__ __forceinline__ Two falling(Two t) {
+    return (t.map([](float x) { return exp2_approx(x); }) + Two(1.f)).map([](float x) { return rcp_approx(x); });
+}
+// Half of 1 + tanh of gelu's argument is a sigmoid of twice that
+__device__ __forceinline__ Two gelu_tanh_sigmoid(Two z, Two z2) {
+    return falling(z * fma(z2, Two(-LOG2E * GELU_ROOT * GELU_CUBE), Two(-LOG2E * GELU_ROOT)));
+}
 
 // The upper tail of the normal distribution at |z|: half of erfc(x), x = |z| /
 // sqrt(2), as exp(-x^2) times a polynomial in t = 1 / (1 + 0.37 x) (the form of
 // Hastings' approximations; these coefficients are a least-maximum fit to
-// exp(x^2) erfc(x), relative error 7e-7).  `e` is exp(-z^2 / 2).  Small tails keep
-// their relative precision, which 1 + erf(x) of a negative x loses.
-__device__ __forceinline__ float normal_tail(float z, float& e) {
-    const float t = rcp_approx(fmaf(0.37f * 0.70710678118655f, fabsf(z), 1.f));
-    e = exp2_approx(-0.5f * LOG2E * z * z);
-    float g = -0.14294943f;
-    g = fmaf(g, t, 0.43710686f);
-    g = fmaf(g, t, -0.18854363f);
-    g = fmaf(g, t, 0.31898374f);
-    g = fmaf(g, t, 0.15202124f);
-    g = fmaf(g, t, 0.21501255f);
-    g = fmaf(g, t, 0.20836934f);
-    return 0.5f * t * g * e;
+// exp(x^2) erfc(x) / 2, relative error 7e-7).  `e` is exp(-z^2 / 2).  Small tails
+// keep their relative precision, which 1 + erf(x) of a negative x loses.
+__device__ __forceinline__ Two normal_tail(Two z, Two& e) {
+    const Two size = z.map([](float x) { return fabsf(x); });
+    const Two t = fma(Two(0.37f * 0.70710678118655f), size, Two(1.f)).map([](float x) { return rcp_approx(x); });
+    e = (z * z * Two(-0.5f * LOG2E)).map([](float x) { return exp2_approx(x); });
+    Two g = fma(Two(0.5f * -0.14294943f), t, Two(0.5f * 0.43710686f));
+    g = fma(g, t, Two(0.5f * -0.18854363f));
+    g = fma(g, t, Two(0.5f * 0.31898374f));
+    g = fma(g, t, Two(0.5f * 0.15202124f));
+    g = fma(g, t, Two(0.5f * 0.21501255f));
+    g = fma(g, t, Two(0.5f * 0.20836934f));
+    return g * t * e;
+}
+// Phi(z) from the tail at |z|
+__device__ __forceinline__ Two normal_below(Two z, Two tail) {
+    float z0, z1, t0, t1;
+    z.get(z0, z1);
+    tail.get(t0, t1);
+    return Two(z0 < 0.f ? t0 : 1.f - t0, z1 < 0.f ? t1 : 1.f - t1);
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-    if (ACT == ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
+__device__ __forceinline__ Two act_of(Two z) {
+    if (ACT == ACT_RELU) return z.map([](float x) { return x < 0.f ? 0.f : x; });  // NaN stays
     if (ACT == ACT_GELU) {
-        float e;
-        const float tail = normal_tail(z, e);
-        return z * (z < 0.f ? tail : 1.f - tail);
+        Two e;
+        return z * normal_below(z, normal_tail(z, e));
     }
-    if (ACT == ACT_GELU_TANH) return z * sigmoid(GELU_ROOT * fmaf(GELU_CUBE * z * z, z, z));  // 0.5 (1 + tanh(u)) = sigmoid(2 u)
-    if (ACT == ACT_SILU) return z * sigmoid(z);
+    if (ACT == ACT_GELU_TANH) return z * gelu_tanh_sigmoid(z, z * z);
+    if (ACT == ACT_SILU) return z * falling(z * Two(-LOG2E));
     return z;
 }
 template <int ACT>
-__device__ __forceinline__ float act_grad_of(float z) {
-    if (ACT == ACT_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
+__device__ __forceinline__ Two act_grad_of(Two z) {
+    if (ACT == ACT_RELU) return z.map([](float x) { return x > 0.f ? 1.f : x == x ? 0.f : x; });
     if (ACT == ACT_GELU) {
-        float e;
-        const float tail = normal_tail(z, e);
-        return fmaf(0.398942280401433f * z, e, z < 0.f ? tail : 1.f - tail);
+        Two e;
+        const Two below = normal_below(z, normal_tail(z, e));
+        return fma(Two(0.398942280401433f) * z, e, below);
     }
     if (ACT == ACT_GELU_TANH) {
-        const float s = sigmoid(GELU_ROOT * fmaf(GELU_CUBE * z * z, z, z));
-        // past 16 the second term is 0; its factor must not overflow there
-        const float q = fminf(z * z, 256.f);
-        return fmaf(z * s * (1.f - s), GELU_ROOT * fmaf(3.f * GELU_CUBE, q, 1.f), s);
+        const Two z2 = z * z, s = gelu_tanh_sigmoid(z, z2);
+        const Two rest = fma(s * Two(-1.f), s, s);  // s (1 - s): 0 past 16, where its factor must not overflow
+        const Two q = z2.map([](float x) { return fminf(x, 256.f); });
+        return fma(z * rest, fma(q, Two(3.f * GELU_CUBE * GELU_ROOT), Two(GELU_ROOT)), s);
     }
     if (ACT == ACT_SILU) {
-        const float s = sigmoid(z);
-        return s * fmaf(z, 1.f - s, 1.f);
+        const Two s = falling(z * Two(-LOG2E));
+        return fma(z, fma(s * Two(-1.f), s, s), s);
     }
-    return 1.f;
+    return Two(1.f);
 }
 // one of them for N values, chosen once
 template <int N>
 __device__ __forceinline__ void apply_act(float (&v)[N], int act) {
     auto all = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = f(v[i]);
+        for (int i = 0; i < N; i += 2) f(Two(v[i], v[i + 1])).get(v[i], v[i + 1]);
     };
     switch (act) {
-        case ACT_RELU: all([](float z) { return act_of<ACT_RELU>(z); }); break;
-        case ACT_GELU: all([](float z) { return act_of<ACT_GELU>(z); }); break;
-        case ACT_GELU_TANH: all([](float z) { return act_of<ACT_GELU_TANH>(z); }); break;
-        case ACT_SILU: all([](float z) { return act_of<ACT_SILU>(z); }); break;
+        case ACT_RELU: all([](Two z) { return act_of<ACT_RELU>(z); }); break;
+        case ACT_GELU: all([](Two z) { return act_of<ACT_GELU>(z); }); break;
+        case ACT_GELU_TANH: all([](Two z) { return act_of<ACT_GELU_TANH>(z); }); break;
+        case ACT_SILU: all([](Two z) { return act_of<ACT_SILU>(z); }); break;
         default: break;
+    }
+}
+// g times the derivative at z
+template <int N>
+__device__ __forceinline__ void apply_act_grad(float (&g)[N], const float (&z)[N], int act) {
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) (Two(g[i], g[i + 1]) * f(Two(z[i], z[i + 1]))).get(g[i], g[i + 1]);
+    };
+    switch (act) {
+        case ACT_RELU: all([](Two v) { return act_grad_of<ACT_RELU>(v); }); break;
+        case ACT_GELU: all([](Two v) { return act_grad_of<ACT_GELU>(v); }); break;
+        case ACT_GELU_TANH: all([](Two v) { return act_grad_of<ACT_GELU_TANH>(v); }); break;
+        default: all([](Two v) { return act_grad_of<ACT_SILU>(v); }); break;
     }
 }
 

@@ -218,6 +218,7 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
     p.D = static_cast<int>(K);
     p.bias = g->bias;
     p.bias_type = g->bias_dtype;
+    p.bias_near = g->bias && dtype16(g->bias_dtype) && aligned16(g->bias);
     p.type = g->out_dtype;
     p.act = g->act;
     p.out = g->out.data;

@@ -183,16 +183,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
         if (p.act != ACT_NONE) {
             float z[8];
             load_piece<T, VEC>(p.z, row, seg, lane, p.N, z);
-            auto all = [&](auto f) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] *= f(z[e]);
-            };
-            switch (p.act) {
-                case ACT_RELU: all([](float v) { return act_grad_of<ACT_RELU>(v); }); break;
-                case ACT_GELU: all([](float v) { return act_grad_of<ACT_GELU>(v); }); break;
-                case ACT_GELU_TANH: all([](float v) { return act_grad_of<ACT_GELU_TANH>(v); }); break;
-                default: all([](float v) { return act_grad_of<ACT_SILU>(v); }); break;
-            }
+            apply_act_grad(g, z, p.act);
         }
         if (p.dz.data) store_piece<VEC>(p.dz, p.dz_type, row, seg, lane, p.N, g);
 #pragma unroll

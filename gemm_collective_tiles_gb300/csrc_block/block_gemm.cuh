@@ -51,6 +51,7 @@ struct ActParams {
     uint32_t idesc;
     const void* bias;
     int bias_type;
+    int bias_near;         // of 16 bits, on 16 bytes
     void *out, *z;         // z may be absent
     const void* residual;  // may be absent
     int type;              // of out, z and residual
@@ -539,7 +540,13 @@ struct Epilogue {
             uint32_t r[32];
             tmem_ld_32x32b_x32(acc_at(c), r);
             const int col = col0 + c * 32;
-            const float b = bias_at(p, col + lane);
+            const bool near = p.bias_near && col + 32 <= p.N;
+            const float b = near ? 0.f : bias_at(p, col + lane);
+            uint4 near_bias[4];  // the same for all lanes; 16-bit
+            if (near) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) near_bias[j] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + col)[j];
+            }
             tmem_wait_regs(r);
             if (c == groups - 1) hand_back();
             float v[32];
@@ -564,7 +571,23 @@ struct Epilogue {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += sum[i];
             }
-            if (p.bias) {
+            if (near) {
+                const bool bf = p.bias_type == T_BF16;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t words[4] = {near_bias[j].x, near_bias[j].y, near_bias[j].z, near_bias[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lo, hi;
+                        if (bf)
+                            unpack16<T_BF16>(words[e], lo, hi);
+                        else
+                            unpack16<T_F16>(words[e], lo, hi);
+                        v[8 * j + 2 * e] += lo;
+                        v[8 * j + 2 * e + 1] += hi;
+                    }
+                }
+            } else if (p.bias) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
             }
