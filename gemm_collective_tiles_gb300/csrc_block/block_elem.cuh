@@ -92,25 +92,38 @@ template <bool VEC>
 __device__ __forceinline__ int column(unsigned seg, int lane, int e) {
     return seg * SEG + (VEC ? lane * 8 + e : e * 32 + lane);
 }
-// 8 elements of a row's piece, zeros past its end
+// 8 elements of a row's piece as they were loaded, zeros past its end
 template <int T, bool VEC>
-__device__ __forceinline__ void load_piece(const Mat& m, long long row, unsigned seg, int lane, int N, float (&v)[8]) {
-    if constexpr (VEC) {
-        const int c = column<true>(seg, lane, 0);
-        if (c < N) {
-            spread8<T>(load8<T>(m.data, row * m.rs + c), v);
+struct Piece {
+    Raw<T> raw;
+    float v[VEC ? 1 : 8];
+    __device__ __forceinline__ void load(const Mat& m, long long row, unsigned seg, int lane, int N) {
+        if constexpr (VEC) {
+            const int c = column<true>(seg, lane, 0);
+            if (c < N) {
+                raw = load8<T>(m.data, row * m.rs + c);
+            } else {
+#pragma unroll
+                for (uint4& q : raw.q) q = make_uint4(0u, 0u, 0u, 0u);
+            }
         } else {
+            const long long o = row * m.rs;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = column<false>(seg, lane, e);
-            v[e] = c < N ? load_elem<T>(m.data, row * m.rs + c * m.cs) : 0.f;
+            for (int e = 0; e < 8; ++e) {
+                const int c = column<false>(seg, lane, e);
+                v[e] = c < N ? load_elem<T>(m.data, o + c * m.cs) : 0.f;
+            }
         }
     }
-}
+    __device__ __forceinline__ void spread(float (&x)[8]) const {
+        if constexpr (VEC) {
+            spread8<T>(raw, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = v[e];
+        }
+    }
+};
 template <bool VEC>
 __device__ __forceinline__ void store_piece(const Mat& m, int type, long long row, unsigned seg, int lane, int N, const float (&v)[8]) {
     void* const to = const_cast<void*>(m.data);
@@ -151,11 +164,15 @@ __global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ Dr
     const DropKey key = drop_key(p.drop);
     const unsigned seg = blockIdx.x % p.segs;
     for (long long row = blockIdx.x / p.segs * 8 + (threadIdx.x >> 5); row < p.M; row += p.row_step) {
-        float v[8], r[8];
-        load_piece<T, VEC>(p.x, row, seg, lane, p.N, v);
-        if (p.residual.data) load_piece<T, VEC>(p.residual, row, seg, lane, p.N, r);
+        Piece<T, VEC> x, res;
+        x.load(p.x, row, seg, lane, p.N);
+        if (p.residual.data) res.load(p.residual, row, seg, lane, p.N);
+        float v[8];
+        x.spread(v);
         if (p.drop.least) drop_piece<VEC>(v, p.drop, key, row, seg, lane);
         if (p.residual.data) {
+            float r[8];
+            res.spread(r);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += r[e];
         }
@@ -175,19 +192,32 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const __grid_constant__ A
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-#pragma unroll 2
-    for (long long row = first + warp; row < end; row += 8) {
-        float g[8];
-        load_piece<T, VEC>(p.dy, row, seg, lane, p.N, g);
-        if (p.drop.least) drop_piece<VEC>(g, p.drop, key, row, seg, lane);
-        if (p.act != ACT_NONE) {
-            float z[8];
-            load_piece<T, VEC>(p.z, row, seg, lane, p.N, z);
-            apply_act_grad(g, z, p.act);
-        }
-        if (p.dz.data) store_piece<VEC>(p.dz, p.dz_type, row, seg, lane, p.N, g);
+    // the loads of U rows are under way at once
+    constexpr int U = 2;
+    const bool act = p.act != ACT_NONE;
+    for (long long row = first + warp; row < end; row += 8 * U) {
+        Piece<T, VEC> g[U], z[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += g[e];
+        for (int k = 0; k < U; ++k)
+            if (row + 8 * k < end) {
+                g[k].load(p.dy, row + 8 * k, seg, lane, p.N);
+                if (act) z[k].load(p.z, row + 8 * k, seg, lane, p.N);
+            }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (row + 8 * k >= end) break;
+            float v[8];
+            g[k].spread(v);
+            if (p.drop.least) drop_piece<VEC>(v, p.drop, key, row + 8 * k, seg, lane);
+            if (act) {
+                float w[8];
+                z[k].spread(w);
+                apply_act_grad(v, w, p.act);
+            }
+            if (p.dz.data) store_piece<VEC>(p.dz, p.dz_type, row + 8 * k, seg, lane, p.N, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        }
     }
     if (!p.sums) return;
 #pragma unroll

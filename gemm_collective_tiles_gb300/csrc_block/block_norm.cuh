@@ -981,8 +981,10 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
             }
         }
         out_x.store(rm, g.dx, d);
+        if (p.scale != 1.f) {
 #pragma unroll
-        for (int i = 0; i < 8 * C; ++i) d[i] *= p.scale;
+            for (int i = 0; i < 8 * C; ++i) d[i] *= p.scale;
+        }
         if (p.gate.data) {
             if (g.gate_sums) {
                 sums.add(4, g.slots, d, u);
