@@ -293,21 +293,30 @@ def _rows(t: Optional[torch.Tensor], cols: int):
     return t if t is None or t.dim() == 2 else t.reshape(math.prod(t.shape[:-1]), cols)
 
 
+def _graph_of(*tensors) -> bool:
+    """Whether autograd wants a node for an op on these."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _linear(x, weight, bias, act, residual, p, rng, workspace, keep_z):
+    """(y, z): the layer's output, and the activation's argument where it is to be kept."""
+    K, N = weight.shape
+    x2, dev = _rows(x, K), x.device
+    y = torch.empty(x2.shape[0], N, dtype=x.dtype, device=dev)
+    z = torch.empty(x2.shape[0], N, dtype=x.dtype, device=dev) if keep_z and act is not None else None
+    matmul_act(x2, weight, y, bias=bias, act=act, residual=_rows(residual, N), z=z, p=p, rng=rng,
+               workspace=_layer_workspace(workspace, dev))
+    return (y if x.dim() == 2 else y.reshape(*x.shape[:-1], N)), z
+
+
 class _LinearAct(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, act, residual, p, rng, workspace):
-        K, N = weight.shape
-        x2, dev = _rows(x, K), x.device
-        y = torch.empty(x2.shape[0], N, dtype=x.dtype, device=dev)
-        z = None
-        if act is not None and any(ctx.needs_input_grad[:3]):
-            z = torch.empty(x2.shape[0], N, dtype=x.dtype, device=dev)
-        matmul_act(x2, weight, y, bias=bias, act=act, residual=_rows(residual, N), z=z, p=p, rng=rng,
-                   workspace=_layer_workspace(workspace, dev))
+        y, z = _linear(x, weight, bias, act, residual, p, rng, workspace, any(ctx.needs_input_grad[:3]))
         ctx.save_for_backward(x, weight, z, rng)
         ctx.act, ctx.p, ctx.workspace = act, p, workspace
         ctx.bias_dtype = None if bias is None else bias.dtype
-        return y if x.dim() == 2 else y.reshape(*x.shape[:-1], N)
+        return y
 
     # the kernels' gradients have no derivatives of their own: asking for second
     # ones is an error, not a sum without some of its terms
@@ -346,29 +355,31 @@ def linear_act(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
         raise ValueError(f"weight is a {x.dtype} matrix of {x.shape[-1]} rows")
     if residual is not None and (residual.dtype != x.dtype or residual.shape != (*x.shape[:-1], weight.shape[1])):
         raise ValueError(f"residual is a {x.dtype} tensor of shape {(*x.shape[:-1], weight.shape[1])}")
+    if not _graph_of(x, weight, bias, residual):
+        return _linear(x, weight, bias, act, residual, p, rng, workspace, False)[0]
     return _LinearAct.apply(x, weight, bias, act, residual, p, rng, workspace)
+
+
+def _dropped(x, p, rng, residual=None):
+    N = x.shape[-1]
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dropout_add(_rows(x, N), _rows(out, N), p, rng, residual=_rows(residual, N))
+    return out
 
 
 class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, p, rng, residual):
-        N = x.shape[-1]
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dropout_add(_rows(x, N), _rows(out, N), p, rng, residual=_rows(residual, N))
         ctx.save_for_backward(rng)
         ctx.p = p
-        return out
+        return _dropped(x, p, rng, residual)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         rng, = ctx.saved_tensors
-        dx = None
-        if ctx.needs_input_grad[0]:
-            N = dy.shape[-1]
-            dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-            dropout_add(_rows(dy, N), _rows(dx, N), ctx.p, rng)
-        return dx, None, None, dy if ctx.needs_input_grad[3] else None
+        wants = ctx.needs_input_grad
+        return _dropped(dy, ctx.p, rng) if wants[0] else None, None, None, dy if wants[3] else None
 
 
 def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Optional[torch.Tensor] = None):
@@ -378,19 +389,27 @@ def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Op
         raise TypeError("x is a f16, bf16 or f32 tensor (..., N)")
     if residual is not None and (residual.dtype != x.dtype or residual.shape != x.shape):
         raise ValueError(f"residual is a {x.dtype} tensor of shape {tuple(x.shape)}")
+    if not _graph_of(x, residual):
+        return _dropped(x, p, rng, residual)
     return _Dropout.apply(x, p, rng, residual)
+
+
+def _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, keep_stats):
+    """(h, n, stats); h None where nothing joins y, n without a pre-norm, stats where they are not to be kept."""
+    D, dev = y.shape[-1], y.device
+    y2, joins = _rows(y, D), x is not None or gate is not None or post is not None or scale != 1.0
+    h = torch.empty(y.shape, dtype=(y if x is None else x).dtype, device=dev) if joins else None
+    n = torch.empty(y.shape, dtype=y.dtype, device=dev) if pre is not None else None
+    stats = torch.empty(y2.shape[0], 4, dtype=torch.float32, device=dev) if keep_stats else None
+    norm_join(y2, _rows(h, D), _rows(n, D), x=_rows(x, D), gate=gate, scale=scale, post=post, post_weight=post_weight,
+              post_bias=post_bias, pre=pre, weight=weight, bias=bias, eps=eps, stats=stats)
+    return h, n, stats
 
 
 class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, workspace):
-        D = y.shape[-1]
-        y2, x2, joins = _rows(y, D), _rows(x, D), x is not None or gate is not None or post is not None or scale != 1.0
-        h = torch.empty(y.shape, dtype=(y if x is None else x).dtype, device=y.device) if joins else None
-        n = torch.empty(y.shape, dtype=y.dtype, device=y.device) if pre is not None else None
-        stats = torch.empty(y2.shape[0], 4, dtype=torch.float32, device=y.device) if any(ctx.needs_input_grad) else None
-        norm_join(y2, _rows(h, D), _rows(n, D), x=x2, gate=gate, scale=scale, post=post, post_weight=post_weight,
-                  post_bias=post_bias, pre=pre, weight=weight, bias=bias, eps=eps, stats=stats)
+        h, n, stats = _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, True)
         ctx.save_for_backward(y, x, gate, post_weight, post_bias, weight, bias, stats)
         ctx.args = scale, post, pre, eps, workspace
         ctx.set_materialize_grads(False)
@@ -434,5 +453,8 @@ def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None, gate: Optional
         raise ValueError(f"x is a {y.dtype} or float32 tensor of shape {tuple(y.shape)}")
     if post is None and pre is None and x is None and gate is None and scale == 1.0:
         raise ValueError("nothing to do: no norm, residual, gate or scale")
-    h, n = _BlockNorm.apply(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, workspace)
+    if _graph_of(y, x, gate, post_weight, post_bias, weight, bias):
+        h, n = _BlockNorm.apply(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, workspace)
+    else:
+        h, n, _ = _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, False)
     return (y if h is None else h), n
