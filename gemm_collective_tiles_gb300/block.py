@@ -351,6 +351,8 @@ def linear_act(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     operands' type.  A workspace that is given serves forward and backward."""
     if x.dim() < 1 or x.dtype not in _DT16:
         raise TypeError("x is a f16 or bf16 tensor (..., K)")
+    if not x.is_cuda:
+        raise ValueError("x is not on a CUDA device")
     if weight.dim() != 2 or weight.dtype != x.dtype or weight.shape[0] != x.shape[-1]:
         raise ValueError(f"weight is a {x.dtype} matrix of {x.shape[-1]} rows")
     if residual is not None and (residual.dtype != x.dtype or residual.shape != (*x.shape[:-1], weight.shape[1])):
