@@ -239,9 +239,15 @@ def norm_join(y: torch.Tensor, h: Optional[torch.Tensor], n: Optional[torch.Tens
     itself, n may be y."""
     if (pre is None) != (n is None):
         raise ValueError("n is written by the pre-norm: both or neither")
+    _norm_join(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps, stats, stream)
+    _written(tuple(t for t in (h, n, stats) if t is not None))
+
+
+def _norm_join(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps, stats, stream=None):
+    """The call, and its arguments."""
     args, _, _, index, _ = _norm_args(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps, stats)
     _run("norm_join", _native.pack_norm_join(*args), index, stream)
-    _written(tuple(t for t in (h, n, stats) if t is not None))
+    return args
 
 
 def norm_join_grad(y: torch.Tensor, stats: torch.Tensor, dh: Optional[torch.Tensor], dn: Optional[torch.Tensor],
@@ -287,15 +293,33 @@ def norm_join_grad(y: torch.Tensor, stats: torch.Tensor, dh: Optional[torch.Tens
 
 
 # ------------------------------------------------------------------ differentiable forms
+# Their forward passes go through the ops above, with all of their checks; the
+# backward passes' tensors are those, or made here, and are handed on as they are:
+# autograd's threads run on cold caches, where each step costs three times as much.
 
 def _rows(t: Optional[torch.Tensor], cols: int):
     """(..., cols) as a matrix; sizes of zero among them."""
     return t if t is None or t.dim() == 2 else t.reshape(math.prod(t.shape[:-1]), cols)
 
 
+def _m(t: Optional[torch.Tensor]):
+    """(data, row stride, column stride) of a matrix that needs no check."""
+    return _NO_MAT if t is None else (t.data_ptr(), *t.stride())
+
+
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
 def _graph_of(*tensors) -> bool:
     """Whether autograd wants a node for an op on these."""
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _call(name: str, args, workspace, index: int) -> None:
+    """A gradient's call with the caller's workspace, or the stream's."""
+    ws = _layer_workspace(workspace, torch.device("cuda", index))
+    _product(name, getattr(_native.load(), "iris_b200_" + name), args, None, None, ws, index, None)
 
 
 def _linear(x, weight, bias, act, residual, p, rng, workspace, keep_z):
@@ -314,8 +338,7 @@ class _LinearAct(torch.autograd.Function):
     def forward(ctx, x, weight, bias, act, residual, p, rng, workspace):
         y, z = _linear(x, weight, bias, act, residual, p, rng, workspace, any(ctx.needs_input_grad[:3]))
         ctx.save_for_backward(x, weight, z, rng)
-        ctx.act, ctx.p, ctx.workspace = act, p, workspace
-        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.args = _ACTS[act], p, workspace, None if bias is None else bias.dtype
         return y
 
     # the kernels' gradients have no derivatives of their own: asking for second
@@ -324,21 +347,26 @@ class _LinearAct(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, weight, z, rng = ctx.saved_tensors
-        K, N = weight.shape
-        want_x, want_w, want_b = ctx.needs_input_grad[:3]
+        act, p, workspace, bias_dtype = ctx.args
+        want_x, want_w, want_b, _, want_r = ctx.needs_input_grad[:5]
         dx = dw = db = None
         if want_x or want_w or want_b:
-            x2, dy2 = _rows(x, K), _rows(dy, N)
-            dev = dy.device
+            K, N = weight.shape
+            x2, dy2, dev, dtype = _rows(x, K), _rows(dy, N), dy.device, x.dtype
+            M = x2.shape[0]
+            mdx = mdw = _NO_MAT
             if want_x:
-                dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+                dx = torch.empty(x.shape, dtype=dtype, device=dev)
+                mdx = dx.data_ptr(), K, 1
             if want_w:
-                dw = torch.empty(K, N, dtype=weight.dtype, device=dev)
+                dw = torch.empty(K, N, dtype=dtype, device=dev)
+                mdw = dw.data_ptr(), N, 1
             if want_b:
-                db = torch.empty(N, dtype=ctx.bias_dtype, device=dev)
-            linear_act_grad(dy2, x2, weight, z, _rows(dx, K), dw, db, act=ctx.act, p=ctx.p, rng=rng,
-                            workspace=_layer_workspace(ctx.workspace, dev))
-        return dx, dw, db, None, dy if ctx.needs_input_grad[4] else None, None, None, None
+                db = torch.empty(N, dtype=bias_dtype, device=dev)
+            args = _native.pack_linear_act_grad(*_m(dy2), *_m(x2), *_m(weight), *_m(z), *mdx, *mdw, _ptr(db), _ptr(rng), M, N, K, p,
+                                                _DT[dtype], _DT[bias_dtype] if want_b else 0, act, 0)
+            _call("linear_act_grad", args, workspace, dev.index)
+        return dx, dw, db, None, dy if want_r else None, None, None, None
 
 
 def linear_act(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, act: Optional[str] = None,
@@ -397,47 +425,53 @@ def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Op
 
 
 def _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, keep_stats):
-    """(h, n, stats); h None where nothing joins y, n without a pre-norm, stats where they are not to be kept."""
+    """(h, n, stats, the call's arguments); h None where nothing joins y, n without a pre-norm, stats where they are not to
+    be kept."""
     D, dev = y.shape[-1], y.device
     y2, joins = _rows(y, D), x is not None or gate is not None or post is not None or scale != 1.0
     h = torch.empty(y.shape, dtype=(y if x is None else x).dtype, device=dev) if joins else None
     n = torch.empty(y.shape, dtype=y.dtype, device=dev) if pre is not None else None
     stats = torch.empty(y2.shape[0], 4, dtype=torch.float32, device=dev) if keep_stats else None
-    norm_join(y2, _rows(h, D), _rows(n, D), x=_rows(x, D), gate=gate, scale=scale, post=post, post_weight=post_weight,
-              post_bias=post_bias, pre=pre, weight=weight, bias=bias, eps=eps, stats=stats)
-    return h, n, stats
+    args = _norm_join(y2, _rows(h, D), _rows(n, D), _rows(x, D), gate, scale, post, post_weight, post_bias, pre, weight, bias, eps,
+                      stats)
+    return h, n, stats, args
 
 
 class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, workspace):
-        h, n, stats = _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, True)
+        h, n, stats, args = _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, True)
         ctx.save_for_backward(y, x, gate, post_weight, post_bias, weight, bias, stats)
-        ctx.args = scale, post, pre, eps, workspace
+        ctx.args = args, scale, post, pre, eps, workspace
         ctx.set_materialize_grads(False)
         return h, n
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dn):
-        y, x, gate, post_weight, post_bias, weight, bias, stats = ctx.saved_tensors
-        scale, post, pre, eps, workspace = ctx.args
+        y, x, gate, post_weight, post_bias, weight, bias, stats = saved = ctx.saved_tensors
+        args, scale, post, pre, eps, workspace = ctx.args
         if dh is None and dn is None:
             return (None,) * 12
-        D, wants = y.shape[-1], ctx.needs_input_grad
-        inputs = (y, x, gate, post_weight, post_bias, weight, bias)
-        grads = [torch.empty(t.shape, dtype=t.dtype, device=y.device) if t is not None and w else None
-                 for t, w in zip(inputs, wants)]
-        # n has had no part in the loss: its norm's vectors get no gradient
-        idle = dn is None
+        D, dev = y.shape[-1], y.device
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=dev) if w and t is not None else None
+                 for t, w in zip(saved[:7], ctx.needs_input_grad)]
+        if pre is not None and dn is None:
+            # n has had no part in the loss: its norm's vectors get no gradient
+            grads[5] = grads[6] = None
+            weight = bias = pre = None
+        elif all(_ptr(t) == args[i] for t, i in zip(saved, (0, 3, 6, 15, 16, 17, 18, 19))):
+            # the tensors are where the forward call found them
+            mats = [_NO_MAT if t is None else (t.data_ptr(), D, 1) for t in grads[:3]]
+            packed = _native.pack_norm_join_grad(*args, *_m(_rows(dh, D)), *_m(_rows(dn, D)), *mats[0], *mats[1], *mats[2],
+                                                 *map(_ptr, grads[3:]))
+            _call("norm_join_grad", packed, workspace, dev.index)
+            return (*grads, None, None, None, None, None)
         dpost_weight, dpost_bias, dweight, dbias = grads[3:]
         norm_join_grad(_rows(y, D), stats, _rows(dh, D), _rows(dn, D), x=_rows(x, D), gate=gate, scale=scale, post=post,
-                       post_weight=post_weight, post_bias=post_bias, pre=None if idle else pre, weight=None if idle else weight,
-                       bias=None if idle else bias, eps=eps, dy=_rows(grads[0], D), dx=_rows(grads[1], D), dgate=grads[2],
-                       dpost_weight=dpost_weight, dpost_bias=dpost_bias, dweight=None if idle else dweight,
-                       dbias=None if idle else dbias, workspace=_layer_workspace(workspace, y.device))
-        if idle:
-            grads[5] = grads[6] = None
+                       post_weight=post_weight, post_bias=post_bias, pre=pre, weight=weight, bias=bias, eps=eps,
+                       dy=_rows(grads[0], D), dx=_rows(grads[1], D), dgate=grads[2], dpost_weight=dpost_weight,
+                       dpost_bias=dpost_bias, dweight=dweight, dbias=dbias, workspace=_layer_workspace(workspace, dev))
         return (*grads, None, None, None, None, None)
 
 
@@ -458,5 +492,5 @@ def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None, gate: Optional
     if _graph_of(y, x, gate, post_weight, post_bias, weight, bias):
         h, n = _BlockNorm.apply(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, workspace)
     else:
-        h, n, _ = _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, False)
+        h, n, _, _ = _joined(y, x, gate, post_weight, post_bias, weight, bias, scale, post, pre, eps, False)
     return (y if h is None else h), n

@@ -155,7 +155,7 @@ def _need(name: str, args, cfg) -> int:
 
 
 def _product(name: str, fn, args, out, config, ws, index: int, stream):
-    """One product with the given workspace, grown where it is too small, or with a new one."""
+    """One product with the given workspace, grown where it is too small, or with a new one; `out` is marked as written."""
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _product(name, fn, args, out, config, ws, index, stream)
@@ -175,7 +175,8 @@ def _product(name: str, fn, args, out, config, ws, index: int, stream):
             rc = fn(args, cfg, ws.buf.data_ptr(), ws.nbytes, st)
     if rc:
         _native.check("iris_b200_" + name, rc)
-    _written((out,))
+    if out is not None:
+        _written((out,))
     return ws
 
 
