@@ -662,7 +662,11 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     pl.in_registers = D <= 8 * NORM_GRAD_LONGEST;
     p.parts = 1;
     while (pl.in_registers && p.parts * NORM_GRAD_LONGEST < D) p.parts *= 2;
-    pl.r = row_shape(cdiv(D, p.parts), 1, NORM_MAX_T);
+    // 16 elements a thread hide more of a reduction than 8 and leave two CTAs an SM
+    // (16384 x 4096 bf16, rms: 158 us, with 8 199), but where a post-norm's values and
+    // sums need registers too, where they come singly or beside 32-bit ones, 8 do
+    // (16384 x 2048, both norms: 150 and 184; 16384 x 1003 f16: 119 and 205)
+    pl.r = row_shape(cdiv(D, p.parts), vec && f.x_dtype != IRIS_F32 && !f.post && D >= 512 ? 2 : 1, NORM_MAX_T);
     // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
     const int per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
     const size_t pieces = static_cast<size_t>(pl.r.C) * pl.r.T * 16;
