@@ -658,25 +658,31 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     int sms;
     if ((rc = sm_count(&sms))) return rc;
     GradPlan pl;
-    // A row to a CTA, or, where it is too long for one's registers, to a cluster.
+    // A row to a CTA, or, where it is too long for one's registers, to a cluster; also
+    // where no rows that start anywhere fit beside the sums (4000 x 8001 bf16: 411 us
+    // read where they lie, 279 shared by two)
     pl.in_registers = D <= 8 * NORM_GRAD_LONGEST;
     p.parts = 1;
     while (pl.in_registers && p.parts * NORM_GRAD_LONGEST < D) p.parts *= 2;
-    // 16 elements a thread hide more of a reduction than 8 and leave two CTAs an SM
-    // (16384 x 4096 bf16, rms: 158 us, with 8 199), but where a post-norm's values and
-    // sums need registers too, where they come singly or beside 32-bit ones, 8 do
-    // (16384 x 2048, both norms: 150 and 184; 16384 x 1003 f16: 119 and 205)
-    pl.r = row_shape(cdiv(D, p.parts), vec && f.x_dtype != IRIS_F32 && !f.post && D >= 512 ? 2 : 1, NORM_MAX_T);
-    // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
-    const int per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
-    const size_t pieces = static_cast<size_t>(pl.r.C) * pl.r.T * 16;
-    const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pieces;
-    const size_t room = SM_SMEM / per_sm - 1024;
     words = words && unit(g->dh) && unit(g->dn);
-    pl.smem = sums;
-    if (sums < room)
-        pl.smem += row_memory(p.f, pl.r, 1, false, RowKind{!vec ? 0 : f.x_dtype == IRIS_F32 ? 4 : 8, words},
-                              {f.y_dtype, f.x.data ? f.x_dtype : -1, g->dh.data ? f.x_dtype : -1, g->dn.data ? f.y_dtype : -1}, room - sums);
+    int per_sm;
+    for (;; p.parts *= 2) {
+        // 16 elements a thread hide more of a reduction than 8 and leave two CTAs an SM
+        // (16384 x 4096 bf16, rms: 158 us, with 8 199), but where a post-norm's values and
+        // sums need registers too, where they come singly or beside 32-bit ones, 8 do
+        // (16384 x 2048, both norms: 150 and 184; 16384 x 1003 f16: 119 and 205)
+        pl.r = row_shape(cdiv(D, p.parts), vec && f.x_dtype != IRIS_F32 && !f.post && D >= 512 ? 2 : 1, NORM_MAX_T);
+        // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
+        per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
+        const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pl.r.C * pl.r.T * 16;
+        const size_t room = SM_SMEM / per_sm - 1024;
+        pl.smem = sums;
+        p.f.depth = 0;
+        if (sums < room)
+            pl.smem += row_memory(p.f, pl.r, 1, false, RowKind{!vec ? 0 : f.x_dtype == IRIS_F32 ? 4 : 8, words},
+                                  {f.y_dtype, f.x.data ? f.x_dtype : -1, g->dh.data ? f.x_dtype : -1, g->dn.data ? f.y_dtype : -1}, room - sums);
+        if (vec || !words || !pl.in_registers || p.f.depth || p.parts == 8) break;
+    }
     if (pl.smem > SM_SMEM) return IRIS_EUNSUPPORTED;
     pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
     pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
