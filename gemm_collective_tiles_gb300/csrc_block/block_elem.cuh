@@ -6,7 +6,10 @@
 // 16-byte accesses), else column lane + 32 e, so that any strides serve and
 // elements of unit stride still make whole sectors.  Either way a lane computes
 // the random bits of its own 8 columns once; in the second layout the warp hands
-// them round as bytes of keep bits.
+// them round as bytes of keep bits.  Measured: dropout of 16384 x 4096 bf16 with its
+// residual 57.6 us (7.0 TB/s, with what stays in L2), without 45; 1537 x 5003 f32
+// (second layout) 17; act_grad of 4096 x 14336 bf16 with gelu and bias 72 us (4.9
+// TB/s: loads of two rows under way a warp, 78 registers).
 #pragma once
 #include "act.cuh"
 

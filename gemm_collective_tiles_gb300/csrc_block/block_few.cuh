@@ -6,6 +6,10 @@
 // than its tokens, a stage is 16 KB of weights and its tokens' 64 columns, and
 // ten of them are under way per SM.
 //
+// Measured: one token 4096 x 14336 in 21.7 us (5.4 TB/s; as 128 x 128 tiles 42),
+// 48 x 14336 x 4096 with its residual in 25.9 us.  Two CTAs an SM of five stages
+// each instead of one of eleven: 24.4 us for the token.
+//
 // CTA layout (256 threads, one CTA per SM): warp 0 loads, warp 1 issues the
 // MMAs, warps 4-7 are the epilogue: 32 columns of the output each.  A cluster of
 // up to 8 CTAs shares a tile's contraction.  At the end every part's sums lie in

@@ -11,6 +11,12 @@
 // are.  Sums stay in tensor memory until a tile is done; with two or four
 // accumulators the next tile's MMAs run under this one's epilogue.
 //
+// Bound by the tensor cores, and before them by what the L2 delivers: a stage of a
+// pair's 256 x 256 tile is 32 KB per SM for 512 cycles of MMA, one of a 128 x 128
+// tile 32 KB for 256.  Measured, 4096 x 4096 x 14336: 247 us (1.95 PFLOP/s), with
+// bias 249, gelu 254, gelu_tanh 250, z beside out 261, dropout 256; on 256 x 128
+// tiles 405, on 128 x 128 455.
+//
 // CTA layout, one CTA per SM:
 //   warp 0       TMA producer (lane 0)
 //   warp 1       MMA issuer; owns tensor memory
