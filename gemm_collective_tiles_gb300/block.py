@@ -26,7 +26,7 @@ from typing import Optional
 import torch
 
 from . import _native
-from .fp8 import (_DT, _DT16, _lead, _layer_workspace, _mat, _product, _refuse, _stream, _vec, _written)
+from .fp8 import (_DT, _DT16, _F32, _lead, _layer_workspace, _mat, _product, _refuse, _stream, _vec, _written)
 
 _ACTS = {None: _native.IRIS_ACT_NONE, "relu": _native.IRIS_ACT_RELU, "gelu": _native.IRIS_ACT_GELU,
          "gelu_tanh": _native.IRIS_ACT_GELU_TANH, "silu": _native.IRIS_ACT_SILU}
@@ -185,19 +185,28 @@ def dropout_add(x: torch.Tensor, out: torch.Tensor, p: float, rng: Optional[torc
     _written((out,))
 
 
+def _norm_vec(name: str, t, kind: int, D: int, index: int):
+    """(address, type) of an optional vector of a norm."""
+    if t is None:
+        return 0, 0
+    if not kind:
+        raise ValueError(f"{name} without its norm")
+    return _vec(name, t, D, _DT, index), _DT[t.dtype]
+
+
 def _norm_args(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps, stats):
     """The packed arguments of norm_join, as a tuple, and the device."""
-    kinds = _choice("norm", post, _NORMS), _choice("norm", pre, _NORMS)
+    kind_post, kind_pre = _choice("norm", post, _NORMS), _choice("norm", pre, _NORMS)
     my, M, D, index = _lead("y", y, _DT)
-    mx = mh = _NO_MAT
-    x_type = y.dtype
-    for name, t in (("x", x), ("h", h)):
-        if t is not None:
-            types = (y.dtype, torch.float32) if x is None or name == "x" else (x.dtype,)
-            m = _mat(name, t, (M, D), types, index)
-            x_type = t.dtype
-            mx, mh = (m, mh) if name == "x" else (mx, m)
-    mg, gate_rows, gate_dt = _NO_MAT, 0, 0
+    mx = mh = mg = _NO_MAT
+    x_type, y_type = y.dtype, (y.dtype,)
+    if x is not None:
+        mx = _mat("x", x, (M, D), (x_type, torch.float32), index)
+        x_type = x.dtype
+    if h is not None:
+        mh = _mat("h", h, (M, D), (x_type, torch.float32) if x is None else (x_type,), index)
+        x_type = h.dtype
+    gate_rows = gate_dt = 0
     if gate is not None:
         mg, gate_rows, cols, g_index = _lead("gate", gate, _DT)
         if g_index != index or cols != D:
@@ -205,21 +214,18 @@ def _norm_args(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weigh
         if gate_rows < 1 or M % gate_rows or gate_rows > max(M, 1):
             raise ValueError(f"gate has {gate_rows} rows, which do not divide y's {M}")
         gate_dt = _DT[gate.dtype]
-    mn = _like("n", n, (M, D), y.dtype, index)
-    vectors, types = [], []
-    for name, t, kind in (("post_weight", post_weight, kinds[0]), ("post_bias", post_bias, kinds[0]),
-                          ("weight", weight, kinds[1]), ("bias", bias, kinds[1])):
-        if t is not None and not kind:
-            raise ValueError(f"{name} without its norm")
-        vectors.append(0 if t is None else _vec(name, t, D, _DT, index))
-        types.append(0 if t is None else _DT[t.dtype])
+    mn = _NO_MAT if n is None else _mat("n", n, (M, D), y_type, index)
+    pw, pw_dt = _norm_vec("post_weight", post_weight, kind_post, D, index)
+    pb, pb_dt = _norm_vec("post_bias", post_bias, kind_post, D, index)
+    w, w_dt = _norm_vec("weight", weight, kind_pre, D, index)
+    b, b_dt = _norm_vec("bias", bias, kind_pre, D, index)
     st = 0
     if stats is not None:
-        st = _mat("stats", stats, (M, 4), (torch.float32,), index)[0]
+        st = _mat("stats", stats, (M, 4), _F32, index)[0]
         if not stats.is_contiguous():
             raise ValueError("stats is not contiguous")
-    return (*my, *mx, *mg, *mh, *mn, *vectors, st, M, D, gate_rows, scale, eps, _DT[y.dtype], _DT[x_type], gate_dt, *types,
-            *kinds, 0), M, D, index, x_type
+    return (*my, *mx, *mg, *mh, *mn, pw, pb, w, b, st, M, D, gate_rows, scale, eps, _DT[y.dtype], _DT[x_type], gate_dt, pw_dt, pb_dt,
+            w_dt, b_dt, kind_post, kind_pre, 0), M, D, index, x_type
 
 
 def norm_join(y: torch.Tensor, h: Optional[torch.Tensor], n: Optional[torch.Tensor], x: Optional[torch.Tensor] = None,
@@ -313,7 +319,11 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
 
 def _graph_of(*tensors) -> bool:
     """Whether autograd wants a node for an op on these."""
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def _call(name: str, args, workspace, index: int) -> None:

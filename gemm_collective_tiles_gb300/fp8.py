@@ -256,7 +256,8 @@ def _layer_workspace(workspace, device):
     if torch.cuda.is_current_stream_capturing():
         from . import Workspace
         return Workspace(256, device, wait=False)
-    return fp8_workspace(device)
+    index = device.index
+    return _layer_workspaces.get((index, torch._C._cuda_getCurrentRawStream(index))) or fp8_workspace(device)
 
 
 class _Fp8Linear(torch.autograd.Function):

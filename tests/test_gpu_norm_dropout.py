@@ -192,6 +192,15 @@ def test_norm_sums_over_rows(M, gate_rows):
     check_norm(norm_case(M, 40, HF, F32, gate_rows, False, "layer", "layer", vec_dtype=F32), HF, F32)
 
 
+@pytest.mark.parametrize("D", [264, 1032, 4096])
+@pytest.mark.parametrize("gate_rows", [1, 4, 100, 700])
+def test_norm_gates_of_another_type(D, gate_rows):
+    """32-bit gates and vectors beside 16-bit rows, and 16-bit ones beside a 32-bit stream, several rows a CTA."""
+    check_norm(norm_case(700, D, BF, BF, gate_rows, True, "rms", "layer", vec_dtype=F32), BF, BF)
+    check_norm(norm_case(700, D, HF, F32, gate_rows, True, None, "rms", vec_dtype=HF), HF, F32)
+    check_norm(norm_case(1400, D, HF, HF, gate_rows, False, "layer", "rms", layout="odd rows", vec_dtype=F32), HF, HF, "odd rows")
+
+
 @pytest.mark.parametrize("M,D,gate_rows", [(40, 17000, 1), (40, 17000, 8), (300, 16500, 3)])
 def test_long_rows(M, D, gate_rows):
     check_norm(norm_case(M, D, BF, F32, gate_rows, True, "layer", "rms"), BF, F32)
