@@ -1,12 +1,11 @@
-// Host side of matmul_act, act_grad, dropout, norm_join and norm_join_grad, as
-// declared in include/gemm_collective_tiles.h: argument checks, the choice of
-// kernels, tensor maps and launches.
+// Host side of matmul_act, act_grad, linear_act_grad and dropout, as declared in
+// include/gemm_collective_tiles.h: argument checks, the choice of kernels, tensor
+// maps and launches.
 #include <cmath>
-#include <initializer_list>
 
-#include "../csrc_fp8/fp8_host.cuh"
+#include "block_elem.cuh"
 #include "block_few.cuh"
-#include "block_norm.cuh"
+#include "block_host.cuh"
 
 using namespace gct::block;
 
@@ -53,8 +52,6 @@ int device_info(DeviceInfo* out) {
 }
 
 bool act_ok(int a) { return a >= IRIS_ACT_NONE && a <= IRIS_ACT_SILU; }
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 int set_drop(Drop& d, double p, const int64_t* rng) {
     if (!(p >= 0.0 && p <= 1.0)) return IRIS_EINVAL;
     d.least = static_cast<uint32_t>(std::nearbyint(p * 65536.0));
@@ -64,18 +61,6 @@ int set_drop(Drop& d, double p, const int64_t* rng) {
     if (d.least && !rng) return IRIS_EINVAL;
     return d.least && !aligned(rng, 8) ? IRIS_EALIGN : IRIS_OK;
 }
-// an optional vector
-int check_vec(const void* data, int type) {
-    if (!data) return IRIS_OK;
-    if (!dtype_ok(type)) return IRIS_EINVAL;
-    return aligned(data, dtype_size(type)) ? IRIS_OK : IRIS_EALIGN;
-}
-Mat mat_of(const iris_b200_mat& m) { return Mat{m.data, m.row_stride, m.col_stride}; }
-// rows of unit stride on 16 bytes
-bool rows16(const iris_b200_mat& m, int64_t rows, int64_t cols, int elem) {
-    return !m.data || (aligned16(m.data) && (m.col_stride == 1 || cols == 1) && (rows <= 1 || m.row_stride * elem % 16 == 0));
-}
-
 // ---------------------------------------------------------------- matmul_act
 struct Plan {
     int variant, split, stages, m_blocks, n_blocks, group_m, grid;
@@ -291,13 +276,6 @@ int matmul_act(const iris_b200_matmul_act_args* g, const iris_b200_config* cfg, 
 }
 
 // ---------------------------------------------------------------- elements
-int sm_count(int* sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return IRIS_ECUDA;
-    return IRIS_OK;
-}
-
 template <int T>
 int launch_dropout(const DropParams& p, bool vec, unsigned grid, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
@@ -436,302 +414,6 @@ int linear_act_grad(const iris_b200_linear_act_grad_args* g, void* ws, size_t ws
     return IRIS_OK;
 }
 
-// ---------------------------------------------------------------- norms
-bool norm_ok(int k) { return k >= IRIS_NORM_NONE && k <= IRIS_NORM_LAYER; }
-
-// rows of unit stride, or not there
-bool unit(const iris_b200_mat& m) { return !m.data || m.col_stride == 1; }
-
-// checks and parameters of a forward call; `vec`: every tensor so far has rows on 16
-// bytes; `shared`: those that are read have rows of unit stride
-int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec, bool& words) {
-    int rc;
-    std::memset(&p, 0, sizeof(p));
-    if (!dims_ok(g->M, 0, g->D) || !dtype_ok(g->y_dtype) || !dtype_ok(g->x_dtype) || !norm_ok(g->post) || !norm_ok(g->pre) ||
-        g->reserved || !(g->eps >= 0.0) || (g->x_dtype != g->y_dtype && g->x_dtype != IRIS_F32))
-        return IRIS_EINVAL;
-    const int64_t M = g->M, D = g->D;
-    const int ye = dtype_size(g->y_dtype), xe = dtype_size(g->x_dtype);
-    if ((rc = check_in(&g->y, M, D, ye)) || (g->x.data && (rc = check_in(&g->x, M, D, xe))) ||
-        (g->h.data && (rc = check_out(&g->h, M, D, xe))) || (g->n.data && (rc = check_out(&g->n, M, D, ye))))
-        return rc;
-    p.group_rows = std::max<int64_t>(M, 1);
-    p.gate_rows = 1;
-    if (g->gate.data) {
-        if (g->gate_rows < 1 || g->gate_rows > std::max<int64_t>(M, 1) || M % g->gate_rows || !dtype_ok(g->gate_dtype)) return IRIS_EINVAL;
-        if ((rc = check_in(&g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)))) return rc;
-        p.group_rows = std::max<int64_t>(M / g->gate_rows, 1);
-        p.gate_rows = g->gate_rows;
-    }
-    if (!g->post && (g->post_weight || g->post_bias)) return IRIS_EINVAL;
-    if (!g->pre && (g->weight || g->bias)) return IRIS_EINVAL;
-    if ((rc = check_vec(g->post_weight, g->post_weight_dtype)) || (rc = check_vec(g->post_bias, g->post_bias_dtype)) ||
-        (rc = check_vec(g->weight, g->weight_dtype)) || (rc = check_vec(g->bias, g->bias_dtype)))
-        return rc;
-    if (!aligned(g->stats, 16)) return IRIS_EALIGN;
-    p.y = mat_of(g->y);
-    p.x = mat_of(g->x);
-    p.gate = mat_of(g->gate);
-    p.h = mat_of(g->h);
-    p.n = mat_of(g->n);
-    p.post_w = Vec{g->post_weight, g->post_weight_dtype};
-    p.post_b = Vec{g->post_bias, g->post_bias_dtype};
-    p.pre_w = Vec{g->weight, g->weight_dtype};
-    p.pre_b = Vec{g->bias, g->bias_dtype};
-    p.gate_type = g->gate_dtype;
-    p.M = M;
-    p.D = static_cast<int>(D);
-    p.post = g->post;
-    p.pre = g->pre;
-    p.scale = static_cast<float>(g->scale);
-    p.eps = static_cast<float>(g->eps);
-    p.stats = reinterpret_cast<float4*>(g->stats);
-    for (int& at : p.vec_at) at = -1;
-    vec = D % 8 == 0 && rows16(g->y, M, D, ye) && rows16(g->x, M, D, xe) && rows16(g->h, M, D, xe) && rows16(g->n, M, D, ye) &&
-          rows16(g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)) && aligned16(g->post_weight) && aligned16(g->post_bias) &&
-          aligned16(g->weight) && aligned16(g->bias);
-    words = unit(g->y) && unit(g->x) && unit(g->gate);
-    return IRIS_OK;
-}
-
-// dynamic shared memory of a kernel is allowed once per device
-int allow_smem(const void* kernel, size_t bytes) {
-    struct Entry {
-        const void* kernel;
-        uint64_t devices;
-    };
-    static Entry known[128];
-    if (bytes <= 32768) return IRIS_OK;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IRIS_ECUDA;
-    std::lock_guard<std::mutex> lk(g_mu);
-    for (Entry& e : known) {
-        if (e.kernel == kernel && (e.devices >> dev & 1)) return IRIS_OK;
-        if (e.kernel && e.kernel != kernel) continue;
-        const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
-        if (rc != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (norm_join_grad)", static_cast<int>(rc));
-        e.kernel = kernel;
-        e.devices |= uint64_t(1) << dev;
-        return IRIS_OK;
-    }
-    return IRIS_ECUDA;
-}
-
-// Threads T of a row at 8 C elements each.
-struct RowShape {
-    int T, C;
-};
-RowShape row_shape(int64_t D, int C, int most) {
-    const int64_t chunks = cdiv(D, 8);
-    while (C < 2 && cdiv(chunks, C) > most) C *= 2;
-    return RowShape{static_cast<int>(std::min<int64_t>(most, round_up(cdiv(chunks, C), 32))), C};
-}
-constexpr size_t SM_SMEM = 222 * 1024;  // dynamic shared memory of an SM, beside the kernels' own
-
-// How rows reach their threads: pieces of W elements (8 or 4) where all of them
-// lie on 16 bytes; single elements, which rows of unit stride bring through shared
-// memory too (`shared`), or which are read where they lie.
-struct RowKind {
-    int w;
-    bool shared;
-};
-// What of `room` bytes the vectors (in fp32) and the rows ahead of `groups` rows'
-// threads take: vectors first, then up to 4 rows each.  `types`: of the tensors
-// whose rows come, -1: not there.
-size_t row_memory(NormParams& p, RowShape r, int groups, bool bias, RowKind kind, std::initializer_list<int> types, size_t room) {
-    const size_t piece = static_cast<size_t>(r.C) * r.T * 16;
-    const void* all[5] = {p.post_w.data, p.post_b.data, p.pre_w.data, bias ? p.pre_b.data : nullptr, p.gate_rows == 1 ? p.gate.data : nullptr};
-    int n = 0;
-    for (int i = 0; i < 5; ++i) p.vec_at[i] = all[i] ? n++ : -1;
-    p.vec_bytes = static_cast<unsigned>(n * 2 * piece);
-    if (p.vec_bytes > room) {
-        p.vec_bytes = 0;
-        for (int& at : p.vec_at) at = -1;
-    }
-    size_t bytes = 0;
-    auto add = [&](int type) {
-        if (kind.w)
-            bytes += piece * (kind.w == 4 || type == T_F32 ? 2 : 1);
-        else
-            bytes += 8 * r.C * r.T * dtype_size(type) + 32;
-    };
-    for (int type : types)
-        if (type >= 0) add(type);
-    if (p.gate.data && p.gate_rows > 1) add(p.gate_type);
-    p.row_bytes = static_cast<unsigned>(bytes);
-    p.depth = 0;
-    if (kind.w || kind.shared) p.depth = static_cast<int>(std::min<size_t>(4, (room - p.vec_bytes) / (groups * bytes)));
-    if (!kind.w && p.depth < 2) p.depth = 0;
-    return p.vec_bytes + static_cast<size_t>(groups) * p.depth * p.row_bytes;
-}
-template <int TY, int TX, int W>
-int launch_norm_w(NormParams p, bool words, int sms, cudaStream_t stream) {
-    cudaLaunchAttribute attr[2];
-    // Few rows: the more threads a row the shorter its way; many: work for a thread
-    // between two reductions
-    RowShape r = row_shape(p.D, p.M < 2 * sms ? 1 : 2, NORM_MAX_T);
-    if (p.D > 16 * NORM_MAX_T) r = RowShape{static_cast<int>(round_up(cdiv(p.D, 16), 32)), 2};
-    // 512 threads an SM, for registers enough (16384 x 4096, 32-bit residual: 129 us,
-    // with 1024 threads 186; 1537 x 5003 f16: 40 and 59), unless a row needs more
-    const int threads = r.T <= NORM_MAX_T ? NORM_MAX_T : NORM_CTA;
-    const int groups = static_cast<int>(std::min<int64_t>(std::min(16, threads / r.T), cdiv(p.M, sms)));
-    const int64_t ctas = std::min<int64_t>(cdiv(p.M, groups), sms);
-    size_t smem = 0;
-    if (ctas * groups < p.M)  // several rows for a group
-        smem = row_memory(p, r, groups, true, RowKind{W, words}, {TY, p.x.data ? TX : -1}, SM_SMEM);
-    const auto kernel = threads == NORM_CTA ? norm_kernel<TY, TX, W, 2, NORM_CTA>
-                        : r.C == 1          ? norm_kernel<TY, TX, W, 1, NORM_MAX_T>
-                                            : norm_kernel<TY, TX, W, 2, NORM_MAX_T>;
-    const int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem);
-    if (rc) return rc;
-    cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(ctas), r.T, smem, 1, stream, attr);
-    lc.blockDim = dim3(r.T, groups);
-    return launch("norm launch", kernel, lc, p);
-}
-template <int TY, int TX>
-int launch_norm(const NormParams& p, bool vec, bool words, int sms, cudaStream_t stream) {
-    if (p.D > NORM_LONGEST) {
-        cudaLaunchAttribute attr[2];
-        return launch("norm launch", norm_long_kernel<TY, TX>, launch_config(static_cast<unsigned>(p.M), NORM_MAX_T, 0, 1, stream, attr), p);
-    }
-    return vec ? launch_norm_w<TY, TX, TX == T_F32 ? 4 : 8>(p, false, sms, stream) : launch_norm_w<TY, TX, 0>(p, words, sms, stream);
-}
-template <typename F>
-int by_types(int y, int x, F f) {
-    if (y == IRIS_F32) return f(std::integral_constant<int, T_F32>(), std::integral_constant<int, T_F32>());
-    if (y == IRIS_F16)
-        return x == IRIS_F32 ? f(std::integral_constant<int, T_F16>(), std::integral_constant<int, T_F32>())
-                             : f(std::integral_constant<int, T_F16>(), std::integral_constant<int, T_F16>());
-    return x == IRIS_F32 ? f(std::integral_constant<int, T_BF16>(), std::integral_constant<int, T_F32>())
-                         : f(std::integral_constant<int, T_BF16>(), std::integral_constant<int, T_BF16>());
-}
-
-struct GradPlan {
-    RowShape r;
-    bool in_registers;
-    int64_t ctas;
-    size_t smem, part, total;
-};
-template <int TY, int TX, int W>
-int launch_norm_grad_w(const NormGradParams& p, const GradPlan& pl, cudaStream_t stream) {
-    cudaLaunchAttribute attr[2];
-    const auto kernel = pl.r.C == 1 ? norm_grad_kernel<TY, TX, W, 1> : norm_grad_kernel<TY, TX, W, 2>;
-    const int rc = allow_smem(reinterpret_cast<const void*>(kernel), pl.smem);
-    return rc ? rc : launch("norm gradient launch", kernel, launch_config(static_cast<unsigned>(pl.ctas * p.parts), pl.r.T, pl.smem, p.parts, stream, attr), p);
-}
-
-int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
-    int rc;
-    NormGradParams p;
-    std::memset(&p, 0, sizeof(p));
-    if (!g) return IRIS_EINVAL;
-    const iris_b200_norm_join_args& f = g->f;
-    bool vec, words;
-    iris_b200_norm_join_args ff = f;
-    ff.h.data = ff.n.data = nullptr;
-    if ((rc = set_norm(&ff, p.f, vec, words))) return rc;
-    const int64_t M = f.M, D = f.D, G = f.gate.data ? f.gate_rows : 0;
-    const int ye = dtype_size(f.y_dtype), xe = dtype_size(f.x_dtype), ge = dtype_size(f.gate_dtype);
-    if ((g->dn.data && !f.pre) || (g->dgate.data && !f.gate.data) || (M > 0 && D > 0 && !f.stats)) return IRIS_EINVAL;
-    if (M > 0 && D > 0 && !g->dh.data && !g->dn.data) return IRIS_EINVAL;
-    if ((g->dh.data && (rc = check_in(&g->dh, M, D, xe))) || (g->dn.data && (rc = check_in(&g->dn, M, D, ye))) ||
-        (g->dy.data && (rc = check_out(&g->dy, M, D, ye))) || (g->dx.data && (rc = check_out(&g->dx, M, D, xe))) ||
-        (g->dgate.data && (rc = check_out(&g->dgate, G, D, ge))))
-        return rc;
-    void* const vectors[4] = {g->dweight, g->dbias, g->dpost_weight, g->dpost_bias};
-    const int types[4] = {f.weight_dtype, f.bias_dtype, f.post_weight_dtype, f.post_bias_dtype};
-    const int kinds[4] = {f.pre, f.pre, f.post, f.post};
-    NormFinishParams fin;
-    std::memset(&fin, 0, sizeof(fin));
-    for (int i = 0; i < 4; ++i) {
-        p.slot[i] = -1;
-        if (!vectors[i]) continue;
-        if (!kinds[i]) return IRIS_EINVAL;
-        if ((rc = check_vec(vectors[i], types[i]))) return rc;
-        fin.out[p.slots] = vectors[i];
-        fin.type[p.slots] = types[i];
-        p.slot[i] = p.slots++;
-    }
-    p.gate_sums = g->dgate.data && p.f.group_rows != 1;
-    vec = vec && rows16(g->dh, M, D, xe) && rows16(g->dn, M, D, ye) && rows16(g->dy, M, D, ye) && rows16(g->dx, M, D, xe) &&
-          rows16(g->dgate, G, D, ge);
-    int sms;
-    if ((rc = sm_count(&sms))) return rc;
-    GradPlan pl;
-    // A row to a CTA, or, where it is too long for one's registers, to a cluster; also
-    // where no rows that start anywhere fit beside the sums (4000 x 8001 bf16: 411 us
-    // read where they lie, 279 shared by two)
-    pl.in_registers = D <= 8 * NORM_GRAD_LONGEST;
-    p.parts = 1;
-    while (pl.in_registers && p.parts * NORM_GRAD_LONGEST < D) p.parts *= 2;
-    words = words && unit(g->dh) && unit(g->dn);
-    int per_sm;
-    for (;; p.parts *= 2) {
-        // 16 elements a thread hide more of a reduction than 8 and leave two CTAs an SM
-        // (16384 x 4096 bf16, rms: 158 us, with 8 199), but where a post-norm's values and
-        // sums need registers too, where they come singly or beside 32-bit ones, 8 do
-        // (16384 x 2048, both norms: 150 and 184; 16384 x 1003 f16: 119 and 205)
-        pl.r = row_shape(cdiv(D, p.parts), vec && f.x_dtype != IRIS_F32 && !f.post && D >= 512 ? 2 : 1, NORM_MAX_T);
-        // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
-        per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
-        const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pl.r.C * pl.r.T * 16;
-        const size_t room = SM_SMEM / per_sm - 1024;
-        pl.smem = sums;
-        p.f.depth = 0;
-        if (sums < room)
-            pl.smem += row_memory(p.f, pl.r, 1, false, RowKind{!vec ? 0 : f.x_dtype == IRIS_F32 ? 4 : 8, words},
-                                  {f.y_dtype, f.x.data ? f.x_dtype : -1, g->dh.data ? f.x_dtype : -1, g->dn.data ? f.y_dtype : -1}, room - sums);
-        if (vec || !words || !pl.in_registers || p.f.depth || p.parts == 8) break;
-    }
-    if (pl.smem > SM_SMEM) return IRIS_EUNSUPPORTED;
-    pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
-    pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
-    pl.total = WS_HEADER + pl.part + (p.gate_sums ? static_cast<size_t>(pl.ctas) * 2 * D * 4 : 0);
-    if (need) {
-        *need = pl.total;
-        return IRIS_OK;
-    }
-    if (D == 0) return IRIS_OK;
-    if (p.slots || p.gate_sums) {
-        if (!ws || ws_bytes < pl.total) return IRIS_ENOWS;
-        if (!aligned16(ws)) return IRIS_EALIGN;
-        p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER);
-        p.gate_part = reinterpret_cast<float*>(static_cast<char*>(ws) + WS_HEADER + pl.part);
-    }
-    p.dh = mat_of(g->dh);
-    p.dn = mat_of(g->dn);
-    p.dy = mat_of(g->dy);
-    p.dx = mat_of(g->dx);
-    p.dgate = mat_of(g->dgate);
-    p.ctas = pl.ctas;
-    if (M > 0) {
-        rc = by_types(f.y_dtype, f.x_dtype, [&](auto ty, auto tx) {
-            constexpr int TY = decltype(ty)::value, TX = decltype(tx)::value;
-            if (pl.in_registers)
-                return vec ? launch_norm_grad_w<TY, TX, TX == T_F32 ? 4 : 8>(p, pl, stream) : launch_norm_grad_w<TY, TX, 0>(p, pl, stream);
-            cudaLaunchAttribute attr[2];
-            return launch("norm gradient launch", norm_grad_long_kernel<TY, TX>,
-                          launch_config(static_cast<unsigned>(pl.ctas), NORM_MAX_T, 0, 1, stream, attr), p);
-        });
-        if (rc) return rc;
-    }
-    if (!p.slots && !p.gate_sums) return IRIS_OK;
-    fin.part = p.part;
-    fin.gate_part = p.gate_part;
-    fin.ctas = static_cast<int>(pl.ctas);
-    fin.slots = p.slots;
-    fin.D = static_cast<int>(D);
-    fin.dgate = p.dgate;
-    fin.gate_type = f.gate_dtype;
-    fin.M = M;
-    fin.group_rows = p.f.group_rows;
-    fin.groups = p.gate_sums ? G : 0;
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(cdiv(D, 32)), 256, 0, 1, stream, attr);
-    lc.gridDim.y = static_cast<unsigned>(std::min<int64_t>(fin.slots + fin.groups, 1024));
-    return launch("norm sums launch", norm_finish_kernel<0>, lc, fin);
-}
-
 }  // namespace
 
 extern "C" {
@@ -788,27 +470,6 @@ int iris_b200_dropout(const iris_b200_dropout_args* g, cudaStream_t stream) {
     if (g->dtype == IRIS_F32) return launch_dropout<T_F32>(p, vec, grid, stream);
     if (g->dtype == IRIS_F16) return launch_dropout<T_F16>(p, vec, grid, stream);
     return launch_dropout<T_BF16>(p, vec, grid, stream);
-}
-
-int iris_b200_norm_join(const iris_b200_norm_join_args* g, cudaStream_t stream) {
-    NormParams p;
-    bool vec, words;
-    if (!g) return IRIS_EINVAL;
-    const int rc = set_norm(g, p, vec, words);
-    if (rc) return rc;
-    if ((g->pre != 0) != (g->n.data != nullptr) && g->M > 0 && g->D > 0) return IRIS_EINVAL;
-    if (g->M == 0 || g->D == 0) return IRIS_OK;
-    int sms;
-    if (sm_count(&sms)) return IRIS_ECUDA;
-    return by_types(g->y_dtype, g->x_dtype,
-                    [&](auto ty, auto tx) { return launch_norm<decltype(ty)::value, decltype(tx)::value>(p, vec, words, sms, stream); });
-}
-int iris_b200_norm_join_grad_workspace_size(const iris_b200_norm_join_grad_args* args, const iris_b200_config*, size_t* bytes) {
-    return bytes ? norm_grad(args, nullptr, 0, nullptr, bytes) : IRIS_EINVAL;
-}
-int iris_b200_norm_join_grad(const iris_b200_norm_join_grad_args* args, const iris_b200_config*, void* workspace,
-                             size_t workspace_bytes, cudaStream_t stream) {
-    return norm_grad(args, workspace, workspace_bytes, stream, nullptr);
 }
 
 }  // extern "C"
