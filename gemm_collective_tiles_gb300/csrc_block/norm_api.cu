@@ -18,9 +18,13 @@ int launch_norm_w(NormParams p, bool words, int sms, cudaStream_t stream) {
     size_t smem = 0;
     if (ctas * groups < p.M)  // several rows for a group
         smem = row_memory(p, r, groups, true, RowKind{W, words}, {TY, p.x.data ? TX : -1}, SM_SMEM);
-    const auto kernel = threads == NORM_CTA ? norm_kernel<TY, TX, W, 2, NORM_CTA>
-                        : r.C == 1          ? norm_kernel<TY, TX, W, 1, NORM_MAX_T>
-                                            : norm_kernel<TY, TX, W, 2, NORM_MAX_T>;
+    auto of = [&](auto queued) {
+        constexpr bool Q = decltype(queued)::value;
+        return threads == NORM_CTA ? norm_kernel<TY, TX, W, 2, NORM_CTA, Q>
+               : r.C == 1          ? norm_kernel<TY, TX, W, 1, NORM_MAX_T, Q>
+                                   : norm_kernel<TY, TX, W, 2, NORM_MAX_T, Q>;
+    };
+    const auto kernel = W || p.depth > 0 ? of(std::true_type()) : of(std::integral_constant<bool, W != 0>());
     const int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem);
     if (rc) return rc;
     cudaLaunchConfig_t lc = launch_config(static_cast<unsigned>(ctas), r.T, smem, 1, stream, attr);
