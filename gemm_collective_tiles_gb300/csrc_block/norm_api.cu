@@ -11,7 +11,7 @@ int launch_norm_w(NormParams p, bool words, int sms, cudaStream_t stream) {
     RowShape r = row_shape(p.D, p.M < 2 * sms ? 1 : 2, NORM_MAX_T);
     if (p.D > 16 * NORM_MAX_T) r = RowShape{static_cast<int>(round_up(cdiv(p.D, 16), 32)), 2};
     // 512 threads an SM, for registers enough (16384 x 4096, 32-bit residual: 129 us,
-    // with 1024 threads 186; 1537 x 5003 f16: 40 and 59), unless a row needs more
+    // with 1024 threads 186; 1537 x 5003 f16: 38 and 59), unless a row needs more
     const int threads = r.T <= NORM_MAX_T ? NORM_MAX_T : NORM_CTA;
     const int groups = static_cast<int>(std::min<int64_t>(std::min(16, threads / r.T), cdiv(p.M, sms)));
     const int64_t ctas = std::min<int64_t>(cdiv(p.M, groups), sms);
