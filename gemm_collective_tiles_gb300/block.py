@@ -470,8 +470,10 @@ class _BlockNorm(torch.autograd.Function):
             # n has had no part in the loss: its norm's vectors get no gradient
             grads[5] = grads[6] = None
             weight = bias = pre = None
-        elif all(_ptr(t) == args[i] for t, i in zip(saved, (0, 3, 6, 15, 16, 17, 18, 19))):
-            # the tensors are where the forward call found them
+        elif all(_m(_rows(t, D)) == args[i:i + 3] for t, i in zip(saved, (0, 3, 6))) and \
+                all(_ptr(t) == args[i] for t, i in zip(saved[3:], range(15, 20))):
+            # the tensors lie as the forward call found them (those that a hook on saved
+            # ones has brought back may lie in the same place with other strides)
             mats = [_NO_MAT if t is None else (t.data_ptr(), D, 1) for t in grads[:3]]
             packed = _native.pack_norm_join_grad(*args, *_m(_rows(dh, D)), *_m(_rows(dn, D)), *mats[0], *mats[1], *mats[2],
                                                  *map(_ptr, grads[3:]))

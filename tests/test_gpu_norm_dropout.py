@@ -294,6 +294,38 @@ def test_block_norm_uses_of_less():
         d.sum().backward()
 
 
+def test_block_norm_saved_tensors_that_are_moved():
+    """A hook on saved tensors may bring one back with other strides, in the same place among others."""
+    M, D = 40, 264
+    g = generator(5)
+    base = torch.randn(M, 2 * D, generator=g, device="cuda").bfloat16()
+    w = torch.rand(D, generator=g, device="cuda").requires_grad_()
+    dh, dn = (torch.randn(M, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    for moved in (0, 1):
+        y, x = torch.randn(2, M, D, generator=g, device="cuda").bfloat16().unbind()
+        plain = [y.clone().requires_grad_(), x.clone().requires_grad_()]
+        want = torch.autograd.grad(gct.block_norm(*plain, post="rms", pre="rms", weight=w), [*plain, w], (dh, dn))
+        ins = [y.clone(), x.clone()]
+        base[:, :D].copy_(ins[moved])
+        ins[moved] = base[:, :D]
+        ins = [t.detach().requires_grad_() for t in ins]
+        at = base.data_ptr()
+
+        def pack(t):
+            there = t.data_ptr() == at
+            return there, t.clone(memory_format=torch.contiguous_format) if there else t.detach()
+
+        def unpack(kept):
+            there, t = kept
+            return base.view(-1)[:M * D].copy_(t.view(-1)).view(M, D) if there else t
+
+        with torch.autograd.graph.saved_tensors_hooks(pack, unpack):
+            outs = gct.block_norm(*ins, post="rms", pre="rms", weight=w)
+        got = torch.autograd.grad(outs, [*ins, w], (dh, dn))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_norm_refusals():
     y, x, w = torch.zeros(6, 64, device="cuda").bfloat16(), torch.zeros(6, 64, device="cuda").bfloat16(), torch.ones(64, device="cuda")
     n = torch.empty_like(y)
