@@ -19,12 +19,12 @@ CSRC_BLOCK = os.path.join(PKG, "csrc_block")
 LIBDIR = os.path.join(PKG, "_lib")
 LIBNAME = "libgemm_collective_tiles.so"
 SOURCES = [os.path.join(CSRC, "iris_api.cu"), os.path.join(CSRC_FP8, "fp8_api.cu"),
-           *(os.path.join(CSRC_BLOCK, f) for f in ("block_api.cu", "norm_api.cu", "norm_grad_api.cu"))]
+           *(os.path.join(CSRC_BLOCK, f) for f in ("block_api.cu", "norm_api.cu", "norm_grad_api.cu", "norm_grad_post.cu"))]
 HEADERS = [os.path.join(CSRC, f) for f in ("fused_kernel.cuh", "ptx.cuh")]
 HEADERS += [os.path.join(CSRC_FP8, f) for f in ("fp8_ptx.cuh", "fp8_elem.cuh", "fp8_wait.cuh", "fp8_repack.cuh", "fp8_quant.cuh",
                                                 "fp8_gemm.cuh", "fp8_few.cuh", "fp8_host.cuh")]
 HEADERS += [os.path.join(CSRC_BLOCK, f) for f in ("act.cuh", "block_gemm.cuh", "block_few.cuh", "block_elem.cuh",
-                                                  "block_norm.cuh", "block_host.cuh", "norm_host.cuh")]
+                                                  "block_norm.cuh", "block_host.cuh", "norm_host.cuh", "norm_grad.cuh")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,21 +1,8 @@
-// Host side of norm_join_grad, as declared in include/gemm_collective_tiles.h.
-#include "norm_host.cuh"
+// Host side of norm_join_grad, as declared in include/gemm_collective_tiles.h, and
+// its kernels without a post-norm.
+#include "norm_grad.cuh"
 
 namespace {
-
-struct GradPlan {
-    RowShape r;
-    bool in_registers;
-    int64_t ctas;
-    size_t smem, part, total;
-};
-template <int TY, int TX, int W>
-int launch_norm_grad_w(const NormGradParams& p, const GradPlan& pl, cudaStream_t stream) {
-    cudaLaunchAttribute attr[2];
-    const auto kernel = pl.r.C == 1 ? norm_grad_kernel<TY, TX, W, 1> : norm_grad_kernel<TY, TX, W, 2>;
-    const int rc = allow_smem(reinterpret_cast<const void*>(kernel), pl.smem);
-    return rc ? rc : launch("norm gradient launch", kernel, launch_config(static_cast<unsigned>(pl.ctas * p.parts), pl.r.T, pl.smem, p.parts, stream, attr), p);
-}
 
 int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes, cudaStream_t stream, size_t* need) {
     int rc;
@@ -54,7 +41,7 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
           rows16(g->dgate, G, D, ge);
     int sms;
     if ((rc = sm_count(&sms))) return rc;
-    GradPlan pl;
+    NormGradPlan pl;
     // A row to a CTA, or, where it is too long for one's registers, to a cluster; also
     // where no rows that start anywhere fit beside the sums (4000 x 8001 bf16: 411 us
     // read where they lie, 279 shared by two)
@@ -81,6 +68,9 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
         if (vec || !words || !pl.in_registers || p.f.depth || p.parts == 8) break;
     }
     if (pl.smem > SM_SMEM) return IRIS_EUNSUPPORTED;
+    const bool held = f.post_weight || f.post_bias || f.weight || (f.gate.data && f.gate_rows == 1);
+    pl.vec = vec;
+    pl.all = vec && f.x.data && g->dh.data && g->dn.data && p.f.depth > 0 && (p.f.vec_bytes || !held);
     pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
     pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
     pl.total = WS_HEADER + pl.part + (p.gate_sums ? static_cast<size_t>(pl.ctas) * 2 * D * 4 : 0);
@@ -102,14 +92,16 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     p.dgate = mat_of(g->dgate);
     p.ctas = pl.ctas;
     if (M > 0) {
-        rc = by_types(f.y_dtype, f.x_dtype, [&](auto ty, auto tx) {
-            constexpr int TY = decltype(ty)::value, TX = decltype(tx)::value;
-            if (pl.in_registers)
-                return vec ? launch_norm_grad_w<TY, TX, TX == T_F32 ? 4 : 8>(p, pl, stream) : launch_norm_grad_w<TY, TX, 0>(p, pl, stream);
-            cudaLaunchAttribute attr[2];
-            return launch("norm gradient launch", norm_grad_long_kernel<TY, TX>,
-                          launch_config(static_cast<unsigned>(pl.ctas), NORM_MAX_T, 0, 1, stream, attr), p);
-        });
+        if (pl.in_registers)
+            rc = f.post ? norm_grad_post(p, pl, f.y_dtype, f.x_dtype, stream)
+                        : launch_norm_grad<false>(p, pl, f.y_dtype, f.x_dtype, stream);
+        else
+            rc = by_types(f.y_dtype, f.x_dtype, [&](auto ty, auto tx) {
+                constexpr int TY = decltype(ty)::value, TX = decltype(tx)::value;
+                cudaLaunchAttribute attr[2];
+                return launch("norm gradient launch", norm_grad_long_kernel<TY, TX>,
+                              launch_config(static_cast<unsigned>(pl.ctas), NORM_MAX_T, 0, 1, stream, attr), p);
+            });
         if (rc) return rc;
     }
     if (!p.slots && !p.gate_sums) return IRIS_OK;

@@ -87,10 +87,6 @@ int allow_smem(const void* kernel, size_t bytes) {
     return IRIS_ECUDA;
 }
 
-// Threads T of a row at 8 C elements each.
-struct RowShape {
-    int T, C;
-};
 RowShape row_shape(int64_t D, int C, int most) {
     const int64_t chunks = cdiv(D, 8);
     while (C < 2 && cdiv(chunks, C) > most) C *= 2;
