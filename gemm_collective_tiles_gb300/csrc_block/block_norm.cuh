@@ -920,9 +920,26 @@ __global__ void __launch_bounds__(NORM_MAX_T) norm_grad_kernel(const __grid_cons
     rm.keep(p.vec_at[4], one_gate, p.gate.cs);
     // a gate row per row of y: its gradient
     auto store_gate = [&](const float (&u)[8 * C]) {
+        if constexpr (W > 0) {
+            auto typed = [&](auto tag) {
+                constexpr int TYPE = decltype(tag)::value, E = TYPE == T_F32 ? 4 : 2;
+                char* const to = const_cast<char*>(static_cast<const char*>(g.dgate.data)) + (gate.row * g.dgate.rs + col) * E;
 #pragma unroll
-        for (int i = 0; i < 8 * C; ++i)
-            if (rm.column(i) < D) store_any(const_cast<void*>(g.dgate.data), p.gate_type, gate.row * g.dgate.rs + rm.column(i) * g.dgate.cs, u[i]);
+                for (int k = 0; k < 8 * C / W; ++k)
+                    if (rm.there(W * k)) store_bits<TYPE, W>(to + k * T * W * E, u + W * k);
+            };
+            if (p.gate_type == T_F32)
+                typed(std::integral_constant<int, T_F32>());
+            else if (p.gate_type == T_F16)
+                typed(std::integral_constant<int, T_F16>());
+            else
+                typed(std::integral_constant<int, T_BF16>());
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8 * C; ++i)
+                if (rm.column(i) < D)
+                    store_any(const_cast<void*>(g.dgate.data), p.gate_type, gate.row * g.dgate.rs + rm.column(i) * g.dgate.cs, u[i]);
+        }
     };
     float4 next = *stats_at;
     const float over_d = 1.f / D;
