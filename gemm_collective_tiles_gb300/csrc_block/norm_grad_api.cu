@@ -39,6 +39,10 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     p.gate_sums = g->dgate.data && p.f.group_rows != 1;
     vec = vec && rows16(g->dh, M, D, xe) && rows16(g->dn, M, D, ye) && rows16(g->dy, M, D, ye) && rows16(g->dx, M, D, xe) &&
           rows16(g->dgate, G, D, ge);
+    if (D == 0) {
+        if (need) *need = WS_HEADER;
+        return IRIS_OK;
+    }
     int sms;
     if ((rc = sm_count(&sms))) return rc;
     NormGradPlan pl;
@@ -78,7 +82,6 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
         *need = pl.total;
         return IRIS_OK;
     }
-    if (D == 0) return IRIS_OK;
     if (p.slots || p.gate_sums) {
         if (!ws || ws_bytes < pl.total) return IRIS_ENOWS;
         if (!aligned16(ws)) return IRIS_EALIGN;

@@ -167,3 +167,13 @@ def test_reference_generator():
     import block_reference as ref
     words = lambda b: [int(b[2 * i + 1]) << 16 | int(b[2 * i]) for i in range(4)]
     assert words(ref.random_bits(0, 0, 1, 8)[0]) == [0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8]
+
+
+def test_norm_gradient_of_rows_without_elements():
+    """Rows of no elements have no threads to plan for: done before a GPU is asked for anything."""
+    none = dict(D=0, y=(P, 1, 1), n=(P, 1, 1), dh=(P, 1, 1), dn=(P, 1, 1), dy=(P, 1, 1))
+    assert ng(**none) == N.IRIS_OK
+    kw = {k: none[k] for k in ("D", "y", "n")}
+    a = N.pack_norm_join_grad(*packed(stats=P, **kw), *none["dh"], *none["dn"], *none["dy"], *NO, *NO, 0, 0, 0, 0)
+    n = ctypes.c_size_t()
+    assert N.load().iris_b200_norm_join_grad_workspace_size(a, None, ctypes.byref(n)) == N.IRIS_OK and n.value > 0
