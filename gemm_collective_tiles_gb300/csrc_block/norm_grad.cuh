@@ -8,7 +8,9 @@ namespace block {
 
 struct NormGradPlan {
     RowShape r;
-    bool in_registers, vec, all;
+    // kept: rows come ahead, and the vectors lie in shared memory; all: so do those of x, dh
+    // and dn, in pieces
+    bool in_registers, vec, kept, all;
     int64_t ctas;
     size_t smem, part, total;
 };

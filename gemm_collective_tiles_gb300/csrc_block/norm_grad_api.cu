@@ -53,13 +53,15 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
     p.parts = 1;
     while (pl.in_registers && p.parts * NORM_GRAD_LONGEST < D) p.parts *= 2;
     words = words && unit(g->dh) && unit(g->dn);
-    int per_sm;
-    for (;; p.parts *= 2) {
-        // 16 elements a thread hide more of a reduction than 8 and leave two CTAs an SM
-        // (16384 x 4096 bf16, rms: 158 us, with 8 199), but where a post-norm's values and
-        // sums need registers too, where they come singly or beside 32-bit ones, 8 do
-        // (16384 x 2048, both norms: 150 and 184; 16384 x 1003 f16: 119 and 205)
-        pl.r = row_shape(cdiv(D, p.parts), vec && f.x_dtype != IRIS_F32 && !f.post && D >= 512 ? 2 : 1, NORM_MAX_T);
+    const bool held = f.post_weight || f.post_bias || f.weight || (f.gate.data && f.gate_rows == 1);
+    // 16 elements a thread hide more of a reduction than 8 and leave two CTAs an SM
+    // (16384 x 4096 bf16, rms: 128 us, with 8 154; layer norm and gate 165 and 184), where
+    // their sums leave shared memory for the vectors and a row ahead (both norms and a gate
+    // of one row, 16384 x 2048: 182 and 121 us) and rows do not come singly (16384 x 1003
+    // f16: 205 and 119) or beside 32-bit ones (16384 x 4096 f32: 269 and 248)
+    int per_sm, most = vec && f.x_dtype != IRIS_F32 && D >= 512 ? 2 : 1;
+    for (;;) {
+        pl.r = row_shape(cdiv(D, p.parts), most, NORM_MAX_T);
         // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
         per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
         const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pl.r.C * pl.r.T * 16;
@@ -69,12 +71,17 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
         if (sums < room)
             pl.smem += row_memory(p.f, pl.r, 1, false, RowKind{!vec ? 0 : f.x_dtype == IRIS_F32 ? 4 : 8, words},
                                   {f.y_dtype, f.x.data ? f.x_dtype : -1, g->dh.data ? f.x_dtype : -1, g->dn.data ? f.y_dtype : -1}, room - sums);
-        if (vec || !words || !pl.in_registers || p.f.depth || p.parts == 8) break;
+        pl.kept = p.f.depth > 0 && (p.f.vec_bytes || !held);
+        if (most == 2 && !pl.kept)
+            most = 1;
+        else if (vec || !words || !pl.in_registers || p.f.depth || p.parts == 8)
+            break;
+        else
+            p.parts *= 2;
     }
     if (pl.smem > SM_SMEM) return IRIS_EUNSUPPORTED;
-    const bool held = f.post_weight || f.post_bias || f.weight || (f.gate.data && f.gate_rows == 1);
     pl.vec = vec;
-    pl.all = vec && f.x.data && g->dh.data && g->dn.data && p.f.depth > 0 && (p.f.vec_bytes || !held);
+    pl.all = vec && f.x.data && g->dh.data && g->dn.data && pl.kept;
     pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);
     pl.part = round_up(static_cast<size_t>(pl.ctas) * p.slots * D * 4, 256);
     pl.total = WS_HEADER + pl.part + (p.gate_sums ? static_cast<size_t>(pl.ctas) * 2 * D * 4 : 0);
