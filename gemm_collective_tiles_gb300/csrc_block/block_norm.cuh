@@ -17,9 +17,9 @@
 // come ahead of their use by asynchronous copies.  The forward pass is bound by
 // memory (16384 x 4096 bf16, f32 stream, both norms and a gate: 129 us, 6.2 TB/s),
 // the gradient by its reductions, whose latency 16 warps an SM (128 registers) hide
-// in part, and by instructions (16384 x 4096 bf16, layer norm and gate: 209 us, 3.9
-// TB/s; rms alone 158).  Rows that start anywhere come as single elements (1537 x 5003
-// f16, both norms: 38 and 120 us, 5000 columns 25 and 58).  Rows that are too long
+// in part, and by instructions (16384 x 4096 bf16, layer norm and gate: 165 us, 4.9
+// TB/s; rms alone 128, 6.3).  Rows that start anywhere come as single elements (1537 x 5003
+// f16, both norms: 38 and 117 us).  Rows that are too long
 // for a group's registers are shared by a cluster (gradient), or gone over once per
 // reduction.
 #pragma once
