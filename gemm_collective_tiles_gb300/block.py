@@ -464,6 +464,8 @@ class _BlockNorm(torch.autograd.Function):
         if dh is None and dn is None:
             return (None,) * 12
         D, dev = y.shape[-1], y.device
+        # what _rows copies has no other owner, so it is held here until the call has been made
+        dh2, dn2 = _rows(dh, D), _rows(dn, D)
         grads = [torch.empty(t.shape, dtype=t.dtype, device=dev) if w and t is not None else None
                  for t, w in zip(saved[:7], ctx.needs_input_grad)]
         if pre is not None and dn is None:
@@ -475,12 +477,12 @@ class _BlockNorm(torch.autograd.Function):
             # the tensors lie as the forward call found them (those that a hook on saved
             # ones has brought back may lie in the same place with other strides)
             mats = [_NO_MAT if t is None else (t.data_ptr(), D, 1) for t in grads[:3]]
-            packed = _native.pack_norm_join_grad(*args, *_m(_rows(dh, D)), *_m(_rows(dn, D)), *mats[0], *mats[1], *mats[2],
+            packed = _native.pack_norm_join_grad(*args, *_m(dh2), *_m(dn2), *mats[0], *mats[1], *mats[2],
                                                  *map(_ptr, grads[3:]))
             _call("norm_join_grad", packed, workspace, dev.index)
             return (*grads, None, None, None, None, None)
         dpost_weight, dpost_bias, dweight, dbias = grads[3:]
-        norm_join_grad(_rows(y, D), stats, _rows(dh, D), _rows(dn, D), x=_rows(x, D), gate=gate, scale=scale, post=post,
+        norm_join_grad(_rows(y, D), stats, dh2, dn2, x=_rows(x, D), gate=gate, scale=scale, post=post,
                        post_weight=post_weight, post_bias=post_bias, pre=pre, weight=weight, bias=bias, eps=eps,
                        dy=_rows(grads[0], D), dx=_rows(grads[1], D), dgate=grads[2], dpost_weight=dpost_weight,
                        dpost_bias=dpost_bias, dweight=dweight, dbias=dbias, workspace=_layer_workspace(workspace, dev))

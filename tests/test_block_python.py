@@ -1,0 +1,60 @@
+"""What the differentiable forms around linear layers do in Python, with the library's calls replaced.  CPU only."""
+import struct
+import weakref
+
+import pytest
+import torch
+
+from gemm_collective_tiles_gb300 import _native as N
+from gemm_collective_tiles_gb300 import block
+
+GRAD = "@23q2d10i19q"  # the packed arguments of norm_join_grad: dh's matrix is word 35, dn's word 38
+DH, DN = 35, 38
+
+
+class Library:
+    """Stands in for the calls of a forward and a backward pass: notes every matrix that _rows has to copy, and at the backward
+    call which of these are still held, and the packed arguments."""
+
+    def __init__(self, monkeypatch):
+        self.copies, self.packed = [], None
+        rows = block._rows
+
+        def noted(t, cols):
+            m = rows(t, cols)
+            if t is not None and m.data_ptr() != t.data_ptr():
+                self.copies.append((weakref.ref(m), m.data_ptr()))
+            return m
+
+        def forward(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weight, bias, eps, stats, stream=None):
+            for t in (h, n, stats):
+                if t is not None:
+                    t.zero_()
+            one = N.IRIS_F32
+            return (*block._m(y), *block._m(x), *block._m(gate), *block._m(h), *block._m(n), *map(block._ptr, (post_weight, post_bias)),
+                    *map(block._ptr, (weight, bias, stats)), y.shape[0], y.shape[1], 0, scale, eps, one, one, 0, 0, 0, 0, 0,
+                    block._NORMS[post], block._NORMS[pre], 0)
+
+        def backward(name, packed, workspace, index):
+            assert name == "norm_join_grad"
+            self.held = [(at, ref() is not None) for ref, at in self.copies]
+            self.packed = struct.unpack(GRAD, packed)
+
+        monkeypatch.setattr(block, "_rows", noted)
+        monkeypatch.setattr(block, "_norm_join", forward)
+        monkeypatch.setattr(block, "_call", backward)
+        monkeypatch.setattr(block, "_layer_workspace", lambda workspace, device: None)
+
+
+def test_gradients_that_are_copied_are_held(monkeypatch):
+    """Incoming gradients that are no matrix as they lie are copied, and each copy lives until the call has been made."""
+    lib = Library(monkeypatch)
+    y, x = (torch.randn(3, 4, 8, requires_grad=True) for _ in range(2))
+    h, n = block.block_norm(y, x=x, pre="rms")
+    lib.copies.clear()
+    dh, dn = (torch.randn(4, 3, 8).transpose(0, 1) for _ in range(2))
+    torch.autograd.grad([h, n], [y, x], [dh, dn])
+    assert len(lib.held) == 2 and all(alive for _, alive in lib.held)
+    at = [a for a, _ in lib.held]
+    assert [lib.packed[DH], lib.packed[DN]] == at and at[0] != at[1]
+    assert lib.packed[DH + 1:DH + 3] == (8, 1) == lib.packed[DN + 1:DN + 3]
