@@ -465,14 +465,14 @@ class _BlockNorm(torch.autograd.Function):
             return (None,) * 12
         D, dev = y.shape[-1], y.device
         # what _rows copies has no other owner, so it is held here until the call has been made
-        dh2, dn2 = _rows(dh, D), _rows(dn, D)
+        y2, x2, dh2, dn2 = _rows(y, D), _rows(x, D), _rows(dh, D), _rows(dn, D)
         grads = [torch.empty(t.shape, dtype=t.dtype, device=dev) if w and t is not None else None
                  for t, w in zip(saved[:7], ctx.needs_input_grad)]
         if pre is not None and dn is None:
             # n has had no part in the loss: its norm's vectors get no gradient
             grads[5] = grads[6] = None
             weight = bias = pre = None
-        elif all(_m(_rows(t, D)) == args[i:i + 3] for t, i in zip(saved, (0, 3, 6))) and \
+        elif all(_m(t) == args[i:i + 3] for t, i in ((y2, 0), (x2, 3), (gate, 6))) and \
                 all(_ptr(t) == args[i] for t, i in zip(saved[3:], range(15, 20))):
             # the tensors lie as the forward call found them (those that a hook on saved
             # ones has brought back may lie in the same place with other strides)
@@ -482,7 +482,7 @@ class _BlockNorm(torch.autograd.Function):
             _call("norm_join_grad", packed, workspace, dev.index)
             return (*grads, None, None, None, None, None)
         dpost_weight, dpost_bias, dweight, dbias = grads[3:]
-        norm_join_grad(_rows(y, D), stats, dh2, dn2, x=_rows(x, D), gate=gate, scale=scale, post=post,
+        norm_join_grad(y2, stats, dh2, dn2, x=x2, gate=gate, scale=scale, post=post,
                        post_weight=post_weight, post_bias=post_bias, pre=pre, weight=weight, bias=bias, eps=eps,
                        dy=_rows(grads[0], D), dx=_rows(grads[1], D), dgate=grads[2], dpost_weight=dpost_weight,
                        dpost_bias=dpost_bias, dweight=dweight, dbias=dbias, workspace=_layer_workspace(workspace, dev))

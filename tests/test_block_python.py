@@ -58,3 +58,43 @@ def test_gradients_that_are_copied_are_held(monkeypatch):
     at = [a for a, _ in lib.held]
     assert [lib.packed[DH], lib.packed[DN]] == at and at[0] != at[1]
     assert lib.packed[DH + 1:DH + 3] == (8, 1) == lib.packed[DN + 1:DN + 3]
+
+
+@pytest.mark.parametrize("which", ["y", "x", "both"])
+def test_inputs_that_are_copied_are_held(monkeypatch, which):
+    """The same of the saved inputs, with an allocator that gives released memory out again, so that the backward pass's
+    copies lie where the forward pass's lay."""
+    lib = Library(monkeypatch)
+    rows, memory, handed_on = block._rows, {}, []
+
+    def recycled(t, cols):
+        m = rows(t, cols)
+        if t is None or m.data_ptr() == t.data_ptr():
+            return m
+        for i in range(8):
+            buf, ref = memory.get((m.numel(), i), (None, None))
+            if buf is None or ref() is None:
+                buf = torch.empty_like(m) if buf is None else buf
+                v = buf.view(m.shape).copy_(m).view(m.shape)
+                memory[m.numel(), i] = buf, weakref.ref(v)
+                handed_on.append((v.data_ptr(), weakref.ref(v)))
+                return v
+
+    def gradient(y, stats, dh, dn, x=None, **kw):
+        lib.packed = (y.data_ptr(), 0, 0, x.data_ptr())
+        call("norm_join_grad", None, None, None)
+
+    def call(name, packed, workspace, index):
+        lib.alive = [at for at, ref in handed_on if ref() is not None]
+        if packed is not None:
+            lib.packed = struct.unpack(GRAD, packed)
+
+    monkeypatch.setattr(block, "_rows", recycled)
+    monkeypatch.setattr(block, "_call", call)
+    monkeypatch.setattr(block, "norm_join_grad", gradient)
+    lay = lambda swap: (torch.randn(4, 3, 8).transpose(0, 1) if swap else torch.randn(3, 4, 8)).requires_grad_()
+    y, x = lay(which != "x"), lay(which != "y")
+    h, n = block.block_norm(y, x=x, pre="rms")
+    torch.autograd.grad([h, n], [y, x], [torch.randn(3, 4, 8) for _ in range(2)])
+    for name, t, at in (("y", y, lib.packed[0]), ("x", x, lib.packed[3])):
+        assert at == t.data_ptr() if which not in (name, "both") else at in lib.alive
