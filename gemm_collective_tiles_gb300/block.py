@@ -24,6 +24,7 @@ import math
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native
 from .fp8 import (_DT, _DT16, _F32, _lead, _layer_workspace, _mat, _product, _refuse, _stream, _vec, _written)
@@ -318,10 +319,15 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
 
 
 def _graph_of(*tensors) -> bool:
-    """Whether autograd wants a node for an op on these."""
+    """Whether autograd has to see an op on these: it wants a node, or has tangents to refuse (these ops have no
+    forward-mode derivatives)."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
+                return True
+    if forward_ad._current_level >= 0:  # within a dual level
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
                 return True
     return False
 

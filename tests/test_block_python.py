@@ -98,3 +98,34 @@ def test_inputs_that_are_copied_are_held(monkeypatch, which):
     torch.autograd.grad([h, n], [y, x], [torch.randn(3, 4, 8) for _ in range(2)])
     for name, t, at in (("y", y, lib.packed[0]), ("x", x, lib.packed[3])):
         assert at == t.data_ptr() if which not in (name, "both") else at in lib.alive
+
+
+def test_tangents_are_refused(monkeypatch):
+    """There is no forward-mode derivative: an input with a tangent is an error, not an output without one.  Without a tangent
+    a dual level changes nothing."""
+    import torch.autograd.forward_ad as fw
+    monkeypatch.setattr(block, "_dropped", lambda x, p, rng, residual=None: x.detach().clone())
+    monkeypatch.setattr(block, "_joined", lambda y, *a: (y.detach().clone(), y.detach().clone(), torch.zeros(2, 4), ()))
+    monkeypatch.setattr(block, "_linear", lambda x, weight, *a: (x.detach() @ weight.detach(), None))
+    x, w = torch.randn(2, 4), torch.randn(4)
+    calls = [lambda t, v: block.dropout(t, 0.5, None), lambda t, v: block.dropout(x, 0.5, None, residual=t),
+             lambda t, v: block.block_norm(t, pre="rms"), lambda t, v: block.block_norm(x, x=t, pre="rms"),
+             lambda t, v: block.block_norm(x, gate=t, pre="rms"), lambda t, v: block.block_norm(x, pre="rms", weight=v),
+             lambda t, v: block.block_norm(x, pre="rms", bias=v), lambda t, v: block.block_norm(x, post="rms", post_weight=v),
+             lambda t, v: block.block_norm(x, post="layer", post_bias=v)]
+    with fw.dual_level():
+        dual = fw.make_dual(x, torch.ones_like(x)), fw.make_dual(w, torch.ones_like(w))
+        for call in calls:
+            for mode in (torch.enable_grad, torch.no_grad):
+                with mode():
+                    with pytest.raises(NotImplementedError):
+                        call(*dual)
+                    call(x, w)
+        for i in range(4):
+            with pytest.raises(NotImplementedError):
+                args = [x.clone(), torch.randn(4, 3), w[:3], torch.randn(2, 3)]
+                args[i] = fw.make_dual(args[i], torch.ones_like(args[i]))
+                block._LinearAct.apply(*args[:3], None, args[3], 0.0, None, None) if block._graph_of(*args) else None
+    for call in calls:
+        call(x, w)
+    assert not block._graph_of(x, w, None)
