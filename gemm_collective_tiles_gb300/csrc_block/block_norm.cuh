@@ -1221,7 +1221,7 @@ __global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant_
             // a gate row begins in its first CTA, whose share lies in the second half
             const float* at = (gate ? p.gate_part : p.part + static_cast<long long>(what) * p.D) + c;
             const long long step = static_cast<long long>(gate ? 2 : p.slots) * p.D;
-            if (gate && warp == 0) s = at[first * step + p.D];
+            if (gate && warp == 0 && p.M > 0) s = at[first * step + p.D];
             at += (first + warp) * step;
             for (int k = first + warp; k <= last; k += 160) {
                 float v[20];

@@ -27,3 +27,24 @@ def test_forward_mode_is_refused():
         inside = gct.linear_act(x, w), gct.dropout(x, 0.5, rng), gct.block_norm(x, pre="rms", weight=v)[1]
     outside = gct.linear_act(x, w), gct.dropout(x, 0.5, rng), gct.block_norm(x, pre="rms", weight=v)[1]
     assert all(torch.equal(a, b) for a, b in zip(inside, outside))
+
+
+@pytest.mark.parametrize("dtype", [F32, HF, BF])
+@pytest.mark.parametrize("D", [64, 131, 20000, 70000])
+def test_no_rows_give_a_gate_no_gradient(D, dtype):
+    """Zeros, whatever lay there, and beside other sums or alone."""
+    y, gate = torch.empty(0, D, dtype=dtype, device="cuda"), torch.ones(1, D, dtype=dtype, device="cuda")
+    stats, w = torch.empty(0, 4, device="cuda"), torch.ones(D, dtype=dtype, device="cuda")
+    for post, grads in ((None, False), ("rms", False), ("layer", True)):
+        dgate = torch.full_like(gate, 9)
+        of = dict(dweight=torch.full_like(w, 9), dpost_weight=torch.full_like(w, 9)) if grads else {}
+        ws = gct.norm_join_grad(y, stats, y, y, x=y, gate=gate, post=post, post_weight=w if post else None, pre="rms", weight=w, dy=y,
+                                dgate=dgate, **of)
+        assert (dgate == 0).all() and all((t == 0).all() for t in of.values())
+        assert gct.query_status(ws)[0] == 0
+    for x in (None, torch.empty(0, D, dtype=dtype, device="cuda")):
+        g = gate.detach().requires_grad_()
+        torch.full_like(g, 9)  # memory that is given out again
+        h, n = gct.block_norm(y.detach().requires_grad_(), x=x, gate=g, pre="layer")
+        (h.sum() + n.sum()).backward()
+        assert (g.grad == 0).all()
