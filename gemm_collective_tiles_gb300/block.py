@@ -212,7 +212,7 @@ def _norm_args(y, h, n, x, gate, scale, post, post_weight, post_bias, pre, weigh
         mg, gate_rows, cols, g_index = _lead("gate", gate, _DT)
         if g_index != index or cols != D:
             _refuse("gate", gate, (gate_rows, D), _DT, 2, index)
-        if gate_rows < 1 or M % gate_rows or gate_rows > max(M, 1):
+        if gate_rows < (M > 0) or gate_rows > max(M, 1) or gate_rows and M % gate_rows:
             raise ValueError(f"gate has {gate_rows} rows, which do not divide y's {M}")
         gate_dt = _DT[gate.dtype]
     mn = _NO_MAT if n is None else _mat("n", n, (M, D), y_type, index)
@@ -239,7 +239,8 @@ def norm_join(y: torch.Tensor, h: Optional[torch.Tensor], n: Optional[torch.Tens
 
     y (M, D) f16, bf16 or f32, n as y; x and h (M, D) of y's type or f32 (the
     residual stream), x None: not added; gate (G, D), each row for M / G rows of y:
-    a learned scale (1, D), one per sequence, one per token (M, D); post, pre: None,
+    a learned scale (1, D), one per sequence, one per token (M, D), which may be no
+    rows where M is 0; post, pre: None,
     "rms" or "layer", with optional weights and biases (D,); any of the three types
     for gate and vectors.  h None: not wanted; n None just where pre is.  stats
     (M, 4) f32, where given, takes what ``norm_join_grad`` needs.  h may be x

@@ -37,7 +37,7 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
         p.slot[i] = p.slots++;
     }
     // (no rows: a gate's gradient is a sum of nothing)
-    p.gate_sums = g->dgate.data && (M == 0 || p.f.group_rows != 1);
+    p.gate_sums = g->dgate.data && G && (M == 0 || p.f.group_rows != 1);
     vec = vec && rows16(g->dh, M, D, xe) && rows16(g->dn, M, D, ye) && rows16(g->dy, M, D, ye) && rows16(g->dx, M, D, xe) &&
           rows16(g->dgate, G, D, ge);
     if (D == 0) {

@@ -28,10 +28,11 @@ int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec, bool& 
     p.group_rows = std::max<int64_t>(M, 1);
     p.gate_rows = 1;
     if (g->gate.data) {
-        if (g->gate_rows < 1 || g->gate_rows > std::max<int64_t>(M, 1) || M % g->gate_rows || !dtype_ok(g->gate_dtype)) return IRIS_EINVAL;
-        if ((rc = check_in(&g->gate, g->gate_rows, D, dtype_size(g->gate_dtype)))) return rc;
-        p.group_rows = std::max<int64_t>(M / g->gate_rows, 1);
-        p.gate_rows = g->gate_rows;
+        const int64_t G = g->gate_rows;  // 0 where there are no rows of y either
+        if (G < (M > 0) || G > std::max<int64_t>(M, 1) || (G && M % G) || !dtype_ok(g->gate_dtype)) return IRIS_EINVAL;
+        if ((rc = check_in(&g->gate, G, D, dtype_size(g->gate_dtype)))) return rc;
+        if (M > 0) p.group_rows = M / G;
+        p.gate_rows = G;
     }
     if (!g->post && (g->post_weight || g->post_bias)) return IRIS_EINVAL;
     if (!g->pre && (g->weight || g->bias)) return IRIS_EINVAL;

@@ -681,7 +681,7 @@ IRIS_API int iris_b200_dropout(const iris_b200_dropout_args* args, cudaStream_t 
  *   N(v) = (v - m) / sqrt(mean((v - m)^2) + eps) * weight + bias over a row;
  *   m is the row's mean (IRIS_NORM_LAYER) or 0 (IRIS_NORM_RMS).
  * y, n: M x D of y_dtype; x, h: M x D of x_dtype; gate: gate_rows x D, each row
- * for M / gate_rows rows of y.  Vectors of D.  Everything is fp32 between the
+ * for M / gate_rows rows of y (1 or 0 rows where M is 0).  Vectors of D.  Everything is fp32 between the
  * loads and the stores, and h enters the second norm unrounded.  h is written
  * where given, n where pre is not NONE.  stats, where given: 4 floats a row,
  * mean and 1 / sqrt of y's norm and of h's, for the gradient.

@@ -129,3 +129,15 @@ def test_tangents_are_refused(monkeypatch):
     for call in calls:
         call(x, w)
     assert not block._graph_of(x, w, None)
+
+
+def test_gates_of_no_rows():
+    """A row per token, or per sequence, of a batch without any: no gate rows."""
+    from test_block_abi import NO, P, nj
+    none = (0, 1, 1)
+    for gate in (NO, none, (P, 64, 1)):
+        assert nj(M=0, y=none, n=none, gate=gate, gate_rows=0) == N.IRIS_OK
+    assert nj(M=0, y=none, n=none, gate=(P, 64, 1), gate_rows=1) == N.IRIS_OK
+    for rows in (-1, 2):
+        assert nj(M=0, y=none, n=none, gate=(P, 64, 1), gate_rows=rows) == N.IRIS_EINVAL
+    assert nj(gate=(P, 64, 1), gate_rows=0) == N.IRIS_EINVAL

@@ -48,3 +48,20 @@ def test_no_rows_give_a_gate_no_gradient(D, dtype):
         h, n = gct.block_norm(y.detach().requires_grad_(), x=x, gate=g, pre="layer")
         (h.sum() + n.sum()).backward()
         assert (g.grad == 0).all()
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (3, 0, 131)])
+def test_a_gate_row_per_token_of_none(shape):
+    """Rows of y, gate and all that is made of them: none; the vectors' gradients are sums of nothing."""
+    D = shape[-1]
+    leaves = [torch.empty(s, device="cuda", dtype=BF).requires_grad_() for s in (shape, shape, (0, D))] + [
+        torch.ones(D, device="cuda", dtype=BF).requires_grad_() for _ in range(2)]
+    y, x, gate, w, v = leaves
+    with torch.no_grad():
+        assert gct.block_norm(y, x=x, gate=gate, pre="rms", weight=w)[1].shape == shape
+    h, n = gct.block_norm(y, x=x, gate=gate, post="layer", post_weight=v, pre="rms", weight=w)
+    (h.sum() + n.sum()).backward()
+    assert all(t.grad.shape == t.shape for t in leaves) and (w.grad == 0).all() and (v.grad == 0).all()
+    rows = torch.zeros(6, D, device="cuda", dtype=BF)
+    with pytest.raises(ValueError):
+        gct.block_norm(rows, gate=gate.detach(), pre="rms")
