@@ -183,31 +183,55 @@ def workspace_size(op: str, M: int, N: int, K: int, world: int, dtype=torch.bflo
     return int(out.value)
 
 
+def _capture(stream: int) -> int:
+    """The graph capture that a stream (a raw handle) is in, or 0."""
+    n = ctypes.c_ulonglong(0)
+    return n.value if _native.load().iris_b200_capture_id(stream, ctypes.byref(n)) == _native.IRIS_OK else 0
+
+
+# The last word of a header whose zero-fill a capture has recorded, once it has run.
+_FILLED = 0x5EED
+
+
 class Workspace:
     """Zero-initialised device workspace, reusable across calls on one stream.
 
     The zero-fill is finished before the constructor returns, so the first
     call may run on any stream (a workspace is created once and reused).  With
     ``wait=False`` it is only enqueued on the current stream, and the memory
-    belongs to that stream: the ops make theirs so, on the stream they run on."""
+    belongs to that stream: the ops make theirs so, on the stream they run on.
+    In a graph capture that fill runs with the graph's launches, so the memory
+    serves the calls of that capture; others find new memory here."""
 
     def __init__(self, nbytes: int, device="cuda", wait: bool = True):
         self.nbytes = max(256, _round_up(int(nbytes), 256))
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
-        self._outgrown = []
+        self._outgrown = []  # (memory, its capture)
         self._lock = threading.Lock()  # held while a product that may share it is enqueued
-        if wait and self.buf.is_cuda:
-            torch.cuda.current_stream(self.buf.device).synchronize()
+        self._capture = 0
+        if self.buf.is_cuda:
+            if wait:
+                torch.cuda.current_stream(self.buf.device).synchronize()
+            else:
+                self._capture = _capture(torch.cuda.current_stream(self.buf.device).cuda_stream)
+                if self._capture:
+                    self.buf[252:256].view(torch.int32).fill_(_FILLED)
 
     def _grow(self, nbytes: int) -> None:
         """At least nbytes, in new memory of the current stream.  The header
-        moves along, with whatever error it holds; the memory before is kept,
-        for graphs that were captured with it."""
+        moves along, with whatever error it holds, unless a capture would only
+        record that; the memory before is kept, for graphs that were captured
+        with it."""
         more = Workspace(nbytes, self.buf.device, wait=False)
-        more.buf[:256].copy_(self.buf[:256])
-        self.buf[16:32].zero_()  # the error is the new header's
-        self._outgrown.append(self.buf)
-        self.buf, self.nbytes = more.buf, more.nbytes
+        if not (self._capture or more._capture):
+            more.buf[:256].copy_(self.buf[:256])
+            self.buf[16:32].zero_()  # the error is the new header's
+        self._outgrown.append((self.buf, self._capture))
+        self.buf, self.nbytes, self._capture = more.buf, more.nbytes, more._capture
+
+    def _elsewhere(self, stream: int) -> bool:
+        """Whether the memory is another capture's than the stream's."""
+        return self._capture != 0 and self._capture != _capture(stream)
 
     @property
     def ptr(self) -> int:
@@ -225,7 +249,7 @@ def _on(stream, index: int):
 
 
 def _ws(ws: Optional[Workspace], need: int, device, stream=None) -> Workspace:
-    if ws is None or ws.nbytes < need:
+    if ws is None or ws.nbytes < need or ws._capture and ws._elsewhere(_stream(stream)):
         # on the stream that will use it: a workspace that the caller drops goes
         # back to that stream, behind the work that still uses it
         with _on(stream, torch.device(device).index or 0):
@@ -379,9 +403,11 @@ def query_status(workspace: Workspace, stream=None):
     """Synchronise the stream and return (code, raw_status, where, index)."""
     st, wh, ix = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
     # graphs that were captured before the workspace grew report to what it was
-    for buf in (workspace.buf, *workspace._outgrown):
+    for buf, capture in ((workspace.buf, workspace._capture), *workspace._outgrown):
         rc = _native.load().iris_b200_query_status(ctypes.c_void_p(buf.data_ptr()), _stream(stream),
                                                    ctypes.byref(st), ctypes.byref(wh), ctypes.byref(ix))
+        if rc == _native.IRIS_ETIMEOUT and capture and int(buf[252:256].view(torch.int32)) != _FILLED:
+            rc = st.value = wh.value = ix.value = 0  # its graph has not run: not a header yet
         if rc:
             break
     return rc, st.value, wh.value, ix.value

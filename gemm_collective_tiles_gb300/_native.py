@@ -62,6 +62,7 @@ EXPORTS = (
     "iris_b200_norm_join_grad_workspace_size",
     "iris_b200_norm_join_grad",
     "iris_b200_query_status",
+    "iris_b200_capture_id",
     "iris_b200_strerror",
     "iris_b200_num_sms",
 )
@@ -162,6 +163,7 @@ def _declare(lib):
         "iris_b200_norm_join_grad_workspace_size": (ci, [args, cfgp, P(sz)]),
         "iris_b200_norm_join_grad": (ci, [args, cfgp, vp, sz, vp]),
         "iris_b200_query_status": (ci, [vp, vp, P(ci), P(ci), P(ci)]),
+        "iris_b200_capture_id": (ci, [vp, P(ctypes.c_ulonglong)]),
         "iris_b200_strerror": (ctypes.c_char_p, [ci]),
         "iris_b200_num_sms": (ci, [P(ci)]),
     }

@@ -1124,6 +1124,14 @@ int iris_b200_query_status(void* workspace, cudaStream_t stream, int* device_sta
     return IRIS_OK;
 }
 
+int iris_b200_capture_id(cudaStream_t stream, unsigned long long* id) {
+    if (!id) return IRIS_EINVAL;
+    cudaStreamCaptureStatus status;
+    if (cudaStreamGetCaptureInfo(stream, &status, id) != cudaSuccess) return IRIS_ECUDA;
+    if (status != cudaStreamCaptureStatusActive) *id = 0;
+    return IRIS_OK;
+}
+
 }  // extern "C"
 
 // ---------------------------------------------------------------------------

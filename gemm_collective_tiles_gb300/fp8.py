@@ -167,6 +167,10 @@ def _product(name: str, fn, args, out, config, ws, index: int, stream):
         raise ValueError(f"the workspace is on {ws.buf.device}, not cuda:{index}")
     # a product may be several launches: those of two threads must not mix
     with ws._lock:
+        if ws._capture and ws._elsewhere(st):
+            from . import _on
+            with _on(stream, index):
+                ws._grow(ws.nbytes)
         rc = fn(args, cfg, ws.buf.data_ptr(), ws.nbytes, st)
         if rc == _native.IRIS_ENOWS:
             from . import _on

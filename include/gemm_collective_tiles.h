@@ -445,6 +445,13 @@ IRIS_API int iris_b200_all_gather_matmul_noalloc(const iris_b200_heap* heap, siz
 IRIS_API int iris_b200_query_status(void* workspace, cudaStream_t stream, int* device_status,
                            int* where, int* index);
 
+/*
+ * The graph capture that `stream` is in, 0 for none: a fill that a capture
+ * records runs with the graph's launches, so memory whose zero-fill was
+ * recorded is a workspace within that graph only.
+ */
+IRIS_API int iris_b200_capture_id(cudaStream_t stream, unsigned long long* id);
+
 /* Human-readable text of an IRIS_* code (static storage). */
 IRIS_API const char* iris_b200_strerror(int code);
 
