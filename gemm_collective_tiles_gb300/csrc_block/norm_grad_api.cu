@@ -66,12 +66,9 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
         // 512 threads' registers fill an SM; what shared memory the sums leave holds rows ahead
         per_sm = std::min(NORM_MAX_T / pl.r.T, 16);
         const size_t sums = pl.r.C == 1 ? 0 : static_cast<size_t>(p.slots + p.gate_sums) * 2 * pl.r.C * pl.r.T * 16;
-        const size_t room = SM_SMEM / per_sm - 1024;
-        pl.smem = sums;
-        p.f.depth = 0;
-        if (sums < room)
-            pl.smem += row_memory(p.f, pl.r, 1, false, RowKind{!vec ? 0 : f.x_dtype == IRIS_F32 ? 4 : 8, words},
-                                  {f.y_dtype, f.x.data ? f.x_dtype : -1, g->dh.data ? f.x_dtype : -1, g->dn.data ? f.y_dtype : -1}, room - sums);
+        const size_t room = SM_SMEM / per_sm - 1024;  // five sums of 64 T bytes leave at least 2944 of it (T = 32)
+        pl.smem = sums + row_memory(p.f, pl.r, 1, false, RowKind{!vec ? 0 : f.x_dtype == IRIS_F32 ? 4 : 8, words},
+                                    {f.y_dtype, f.x.data ? f.x_dtype : -1, g->dh.data ? f.x_dtype : -1, g->dn.data ? f.y_dtype : -1}, room - sums);
         pl.kept = p.f.depth > 0 && (p.f.vec_bytes || !held);
         if (most == 2 && !pl.kept)
             most = 1;
@@ -80,7 +77,6 @@ int norm_grad(const iris_b200_norm_join_grad_args* g, void* ws, size_t ws_bytes,
         else
             p.parts *= 2;
     }
-    if (pl.smem > SM_SMEM) return IRIS_EUNSUPPORTED;
     pl.vec = vec;
     pl.all = vec && f.x.data && g->dh.data && g->dn.data && pl.kept;
     pl.ctas = std::min<int64_t>(M, int64_t(sms) * (pl.in_registers ? per_sm : 1) / p.parts);

@@ -13,7 +13,7 @@ bool norm_ok(int k) { return k >= IRIS_NORM_NONE && k <= IRIS_NORM_LAYER; }
 bool unit(const iris_b200_mat& m) { return !m.data || m.col_stride == 1; }
 
 // checks and parameters of a forward call; `vec`: every tensor so far has rows on 16
-// bytes; `shared`: those that are read have rows of unit stride
+// bytes; `words`: those that are read have rows of unit stride
 int set_norm(const iris_b200_norm_join_args* g, NormParams& p, bool& vec, bool& words) {
     int rc;
     std::memset(&p, 0, sizeof(p));
@@ -80,7 +80,7 @@ int allow_smem(const void* kernel, size_t bytes) {
         if (e.kernel == kernel && (e.devices >> dev & 1)) return IRIS_OK;
         if (e.kernel && e.kernel != kernel) continue;
         const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
-        if (rc != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (norm_join_grad)", static_cast<int>(rc));
+        if (rc != cudaSuccess) return cuda_fail("cudaFuncSetAttribute (norms)", static_cast<int>(rc));
         e.kernel = kernel;
         e.devices |= uint64_t(1) << dev;
         return IRIS_OK;

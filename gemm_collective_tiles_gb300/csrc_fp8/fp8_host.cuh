@@ -204,7 +204,7 @@ int make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem, const Operand&
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.pitch) * elem};
     cuuint32_t box[2] = {b0, b1};
     const CUresult r = encode(m, dt, 2, o.data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit operand)", static_cast<int>(r));
+    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (operand)", static_cast<int>(r));
 }
 // 16-bit rows as groups of 64 columns, {64, row, column / 64}: a box of 64 rows
 // of `groups` groups, 8192 bytes each
@@ -225,7 +225,7 @@ int make_store_map(CUtensorMap* m, int t, const void* data, int64_t N, int64_t M
                                    : t == IRIS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUresult r = encode(m, dt, 2, data, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_NONE);
-    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (8-bit output)", static_cast<int>(r));
+    return r == CUDA_SUCCESS ? IRIS_OK : cuda_fail("cuTensorMapEncodeTiled (output)", static_cast<int>(r));
 }
 
 }  // namespace
