@@ -89,6 +89,10 @@ _written = torch._C._increment_version
 def _cfgp(config):
     if config is None:
         return None
+    if isinstance(config, str):
+        if config != "auto":
+            raise ValueError(f"unknown config {config!r}")
+        return None  # the estimate from the sizes
     from . import make_config
     return ctypes.byref(make_config(**config) if isinstance(config, dict) else config)
 

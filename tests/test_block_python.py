@@ -141,3 +141,12 @@ def test_gates_of_no_rows():
     for rows in (-1, 2):
         assert nj(M=0, y=none, n=none, gate=(P, 64, 1), gate_rows=rows) == N.IRIS_EINVAL
     assert nj(gate=(P, 64, 1), gate_rows=0) == N.IRIS_EINVAL
+
+
+def test_config_of_the_products():
+    """As every op's: a dict of fields, "auto" (which for these is the default, an estimate from the sizes), nothing else."""
+    from gemm_collective_tiles_gb300 import fp8, make_config
+    assert fp8._cfgp(None) is None and fp8._cfgp("auto") is None
+    assert fp8._cfgp(dict(tile_m=128))._obj.tile_m == 128 == fp8._cfgp(make_config(tile_m=128))._obj.tile_m
+    with pytest.raises(ValueError, match="unknown config"):
+        fp8._cfgp("fast")
