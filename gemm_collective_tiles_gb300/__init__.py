@@ -221,7 +221,10 @@ class Workspace:
         """At least nbytes, in new memory of the current stream.  The header
         moves along, with whatever error it holds, unless a capture would only
         record that; the memory before is kept, for graphs that were captured
-        with it."""
+        with it.  A workspace that grows does so by half at least, so that all
+        that is kept stays below twice what it has come to."""
+        if nbytes > self.nbytes:
+            nbytes = max(nbytes, self.nbytes + self.nbytes // 2)
         more = Workspace(nbytes, self.buf.device, wait=False)
         if not (self._capture or more._capture):
             more.buf[:256].copy_(self.buf[:256])

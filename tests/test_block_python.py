@@ -150,3 +150,21 @@ def test_config_of_the_products():
     assert fp8._cfgp(dict(tile_m=128))._obj.tile_m == 128 == fp8._cfgp(make_config(tile_m=128))._obj.tile_m
     with pytest.raises(ValueError, match="unknown config"):
         fp8._cfgp("fast")
+
+
+def test_workspaces_that_grow_little_by_little():
+    """Batches that get longer step by step: what is held, with all that was outgrown, stays within a few times the need."""
+    import gemm_collective_tiles_gb300 as gct
+    ws, grown = gct.Workspace(256, "cpu"), 0
+    ws.buf[5] = 1  # the header moves along
+    for need in range(300, 1 << 20, 512):
+        if need > ws.nbytes:
+            ws._grow(need)
+            grown += 1
+        assert ws.nbytes >= need and sum(b.numel() for b, _ in ws._outgrown) + ws.nbytes <= 4.5 * need + 4096
+    assert grown < 25 and ws.buf[5] == 1 and ws.buf.sum() == 1
+    size = ws.nbytes
+    ws._grow(size)  # other memory of the same size
+    assert ws.nbytes == size
+    ws._grow(10 * size)  # one that is far too small: no more than is asked for
+    assert ws.nbytes == 10 * size
