@@ -393,7 +393,9 @@ def linear_act(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
 
     Kept for the backward pass: x, weight, and with an activation its argument in
     16 bits; the gradient between the products is rounded to 16 bits, their
-    operands' type.  A workspace that is given serves forward and backward."""
+    operands' type, and lies in the workspace, which stays as large as that
+    (2 bytes an element of the output) when the backward pass is done.  A
+    workspace that is given serves forward and backward; else it is the stream's."""
     if x.dim() < 1 or x.dtype not in _DT16:
         raise TypeError("x is a f16 or bf16 tensor (..., K)")
     if not x.is_cuda:
@@ -502,7 +504,8 @@ def block_norm(y: torch.Tensor, x: Optional[torch.Tensor] = None, gate: Optional
                eps: float = 1e-6, workspace=None):
     """Differentiable ``norm_join`` of tensors (..., D): returns (h, n), n None
     without a pre-norm, h y itself where nothing joins it.  gate (G, D) counts y's
-    rows with the leading dimensions flattened.  Kept for the backward pass: the
+    rows with the leading dimensions flattened; y, x and the gradients that come
+    back are copied where their strides do not allow that.  Kept for the backward pass: the
     inputs and 4 numbers a row."""
     if y.dim() < 1 or y.dtype not in _DT:
         raise TypeError("y is a f16, bf16 or f32 tensor (..., D)")
