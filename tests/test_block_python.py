@@ -168,3 +168,7 @@ def test_workspaces_that_grow_little_by_little():
     assert ws.nbytes == size
     ws._grow(10 * size)  # one that is far too small: no more than is asked for
     assert ws.nbytes == 10 * size
+
+
+def test_capture_id_refuses_nothing_to_write():
+    assert N.load().iris_b200_capture_id(None, None) == N.IRIS_EINVAL
