@@ -1124,17 +1124,6 @@ int iris_b200_query_status(void* workspace, cudaStream_t stream, int* device_sta
     return IRIS_OK;
 }
 
-int iris_b200_capture_id(cudaStream_t stream, unsigned long long* id) {
-    if (!id) return IRIS_EINVAL;
-    cudaStreamCaptureStatus status;
-    if (cudaStreamGetCaptureInfo(stream, &status, id) != cudaSuccess) {
-        cudaGetLastError();  // the legacy stream while another captures: not an error of a later call
-        return IRIS_ECUDA;
-    }
-    if (status != cudaStreamCaptureStatusActive) *id = 0;
-    return IRIS_OK;
-}
-
 }  // extern "C"
 
 // ---------------------------------------------------------------------------

@@ -384,4 +384,15 @@ int iris_b200_weight_grad_fp8(const iris_b200_weight_grad_fp8_args* args, const 
     return product(args, cfg, workspace, workspace_bytes, stream, nullptr);
 }
 
+int iris_b200_capture_id(cudaStream_t stream, unsigned long long* id) {
+    if (!id) return IRIS_EINVAL;
+    cudaStreamCaptureStatus status;
+    if (cudaStreamGetCaptureInfo(stream, &status, id) != cudaSuccess) {
+        cudaGetLastError();  // the legacy stream while another captures: not an error of a later call
+        return IRIS_ECUDA;
+    }
+    if (status != cudaStreamCaptureStatusActive) *id = 0;
+    return IRIS_OK;
+}
+
 }  // extern "C"
